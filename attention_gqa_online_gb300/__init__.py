@@ -12,5 +12,9 @@ from ._binding import (ATTN_BF16, ATTN_CAUSAL, ATTN_CROSS, ATTN_ERR_CUDA, ATTN_E
                        attn_get_status, attn_prefill, attn_prefill_paged, attn_prefill_window, attn_rope_table, attn_selftest_wait_timeout,
                        attn_status_string, load_library, attn_set_workspace, attn_forward_workspace_bytes,
                        attn_prefill_workspace_bytes, attn_backward_workspace_bytes, attn_scratch_reserved_bytes,
-                       attn_scratch_peak_bytes, attn_release_scratch)
-from .api import backward, decode, forward, prefill, rope_table, DecodeState  # noqa: F401
+                       attn_scratch_peak_bytes, attn_release_scratch, ATTN_DT_BF16, ATTN_DT_F16, ATTN_DT_F32,
+                       ATTN_ROPE_BY_PARTS, ATTN_ROPE_HALF, ATTN_ROPE_INTERLEAVED, ATTN_ROPE_LINEAR, ATTN_ROPE_NONE,
+                       ATTN_ROPE_NTK, attn_append_paged, attn_batch_paged, attn_batch_paged_workspace_bytes,
+                       attn_rope_apply, attn_rope_table_scaled)
+from .api import (append_paged, attend_paged, backward, decode, forward, prefill, rope, rope_backward,  # noqa: F401
+                  rope_table, DecodeState, PagedBatch)

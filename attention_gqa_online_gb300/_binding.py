@@ -11,6 +11,9 @@ import os
 
 ATTN_CAUSAL, ATTN_FULL, ATTN_CROSS = 0, 1, 2
 ATTN_FP32, ATTN_TF32, ATTN_BF16 = 0, 1, 2
+ATTN_DT_F32, ATTN_DT_BF16, ATTN_DT_F16 = 0, 1, 2
+ATTN_ROPE_HALF, ATTN_ROPE_INTERLEAVED = 0, 1
+ATTN_ROPE_NONE, ATTN_ROPE_LINEAR, ATTN_ROPE_NTK, ATTN_ROPE_BY_PARTS = 0, 1, 2, 3
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT = 0, 1, 2, 3, 4
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn_gqa.so")
@@ -18,6 +21,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn_gqa
 _lib = None
 _u32 = ctypes.c_uint32
 _vp = ctypes.c_void_p
+_f64 = ctypes.c_double
 
 
 class AttnError(RuntimeError):
@@ -70,6 +74,19 @@ def load_library(path=None):
     lib.attn_backward.argtypes = [_vp] * 9 + [_u32] * 5 + [ctypes.c_int, ctypes.c_int, _u32, _vp]
     lib.attn_backward_rope.restype = ctypes.c_int
     lib.attn_backward_rope.argtypes = [_vp] * 9 + [_u32] * 5 + [ctypes.c_int, ctypes.c_int, _u32, _vp, _u32, _vp]
+    lib.attn_rope_table_scaled.restype = ctypes.c_int
+    lib.attn_rope_table_scaled.argtypes = [_vp, _u32, _u32, _f64, ctypes.c_int, _f64, _u32, _f64, _f64, _f64, _vp]
+    lib.attn_rope_apply.restype = ctypes.c_int
+    lib.attn_rope_apply.argtypes = [_vp, _vp, ctypes.c_int] + [_u32] * 6 + [ctypes.c_int, _vp, _vp, _u32,
+                                                                           ctypes.c_int, _vp]
+    lib.attn_append_paged.restype = ctypes.c_int
+    lib.attn_append_paged.argtypes = [_vp] * 4 + [ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, _vp, _vp] + \
+        [_u32] * 14 + [ctypes.c_int, _vp, _u32, _vp]
+    lib.attn_batch_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_batch_paged_workspace_bytes.argtypes = [_u32] * 3
+    lib.attn_batch_paged.restype = ctypes.c_int
+    lib.attn_batch_paged.argtypes = [_vp] * 4 + [ctypes.c_int, _vp, _vp, _vp] + [_u32] * 11 + \
+        [ctypes.c_float, _u32, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.attn_get_status.restype = ctypes.c_int
     lib.attn_get_status.argtypes = [_vp]
     lib.attn_set_workspace.restype = ctypes.c_int
@@ -280,6 +297,91 @@ def attn_prefill_paged(q_batch, k_pages, v_pages, block_table, out_batch, n_quer
         _addr(block_table, "block_table"), _addr(out_batch, "out_batch", f), n_queries, n_heads, n_kv_heads,
         head_dim, kv_dim, page_rows, num_pages, max_blocks, float(scale), start_pos, q_stride, out_stride, q_base,
         prec, window, _stream(stream)), "attn_prefill_paged")
+
+
+def _dtype_code(x, name):
+    """ATTN_DT_* of a tensor's elements."""
+    import torch
+    code = {torch.float32: ATTN_DT_F32, torch.bfloat16: ATTN_DT_BF16, torch.float16: ATTN_DT_F16}.get(x.dtype)
+    if code is None:
+        raise ValueError("%s must be float32, bfloat16 or float16, got %s" % (name, x.dtype))
+    return code
+
+
+def _same_dtype(code, **tensors):
+    for name, x in tensors.items():
+        if x is not None and _dtype_code(x, name) != code:
+            raise ValueError("%s has type %s, unlike the tensors it goes with" % (name, x.dtype))
+
+
+def _u32_addr(x, name):
+    """Device address of a 32-bit integer tensor (int32 or uint32), an int, or None."""
+    if x is not None and not isinstance(x, int):
+        if x.element_size() != 4 or x.is_floating_point():
+            raise ValueError("%s must hold 32-bit integers, got %s" % (name, x.dtype))
+        if not x.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    return _addr(x, name)
+
+
+def attn_rope_table_scaled(table, max_pos, rot_dim, base=10000.0, scaling=ATTN_ROPE_NONE, factor=1.0, orig_max_pos=0,
+                           beta_fast=32.0, beta_slow=1.0, attn_factor=1.0, stream=None):
+    """Fill a device [max_pos, rot_dim] fp32 rotary table with scaled angles; see attn_gqa.h."""
+    _check(load_library().attn_rope_table_scaled(
+        _addr(table, "table", _f32()), max_pos, rot_dim, float(base), scaling, float(factor), orig_max_pos,
+        float(beta_fast), float(beta_slow), float(attn_factor), _stream(stream)), "attn_rope_table_scaled")
+
+
+def attn_rope_apply(x, y, rows, heads, head_dim, rot_dim, x_stride, y_stride, layout, positions, table,
+                    table_rows=None, inverse=False, stream=None):
+    """Turn the rows of x by their positions (fp32, bf16 or fp16) into y; see attn_gqa.h."""
+    code = _dtype_code(x, "x")
+    _same_dtype(code, y=y)
+    if table_rows is None:
+        table_rows = table.shape[0]
+    _check(load_library().attn_rope_apply(
+        _addr(x, "x"), _addr(y, "y"), code, rows, heads, head_dim, rot_dim, x_stride, y_stride, layout,
+        _u32_addr(positions, "positions"), _addr(table, "table", _f32()), table_rows, 1 if inverse else 0,
+        _stream(stream)), "attn_rope_apply")
+
+
+def attn_append_paged(q, q_out, k_new, v_new, k_pages, v_pages, block_table, q_start, kv_len, total_rows, n_seqs,
+                      num_heads, num_kv_heads, head_dim, kv_dim, q_stride, q_out_stride, k_stride, v_stride, page_rows,
+                      num_pages, max_blocks, rot_dim=0, layout=ATTN_ROPE_HALF, table=None, table_rows=None,
+                      stream=None):
+    """Write a ragged batch's new K (turned) and V rows into a paged cache, and turn Q; see attn_gqa.h."""
+    code, cache = _dtype_code(k_new, "k_new"), _dtype_code(k_pages, "k_pages")
+    _same_dtype(code, v_new=v_new, q=q)
+    _same_dtype(cache, v_pages=v_pages, q_out=q_out)
+    if table_rows is None:
+        table_rows = 0 if table is None else table.shape[0]
+    _check(load_library().attn_append_paged(
+        _addr(q, "q"), _addr(q_out, "q_out"), _addr(k_new, "k_new"), _addr(v_new, "v_new"), code,
+        _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"), cache, _u32_addr(block_table, "block_table"),
+        _u32_addr(q_start, "q_start"), _u32_addr(kv_len, "kv_len"), total_rows, n_seqs, num_heads, num_kv_heads,
+        head_dim, kv_dim, q_stride, q_out_stride, k_stride, v_stride, page_rows, num_pages, max_blocks, rot_dim,
+        layout, _addr(table, "table", _f32()), table_rows, _stream(stream)), "attn_append_paged")
+
+
+def attn_batch_paged_workspace_bytes(n_heads, n_kv_heads, head_dim):
+    return int(load_library().attn_batch_paged_workspace_bytes(n_heads, n_kv_heads, head_dim))
+
+
+def attn_batch_paged(q, k_pages, v_pages, out, block_table, q_start, kv_len, total_rows, n_seqs, n_heads, n_kv_heads,
+                     head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks, scale, window, softcap,
+                     alibi_slopes, prefix_len, workspace, workspace_bytes=None, stream=None):
+    """Attention of a ragged batch's new tokens over a paged 16-bit cache; see attn_gqa.h."""
+    code = _dtype_code(q, "q")
+    _same_dtype(code, k_pages=k_pages, v_pages=v_pages, out=out)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(load_library().attn_batch_paged(
+        _addr(q, "q"), _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"), _addr(out, "out"), code,
+        _u32_addr(block_table, "block_table"), _u32_addr(q_start, "q_start"), _u32_addr(kv_len, "kv_len"), total_rows,
+        n_seqs, n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks,
+        float(scale), window, float(softcap), _addr(alibi_slopes, "alibi_slopes", _f32()),
+        _u32_addr(prefix_len, "prefix_len"), _addr(workspace, "workspace"), workspace_bytes, _stream(stream)),
+        "attn_batch_paged")
 
 
 def attn_decode_cached_noalloc(q, k_cache, v_cache, kv_pos_dev, out, num_heads, num_kv_heads, head_dim, max_seq,

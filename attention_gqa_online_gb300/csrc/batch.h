@@ -1,0 +1,94 @@
+// batch.h -- launch arguments of the batched paged attention and the paged
+// append, and the rotary operator.  Not part of the public interface.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/attn_gqa.h"
+
+namespace attn {
+
+struct RopeArgs {
+  const void* x;
+  void* y;
+  const uint32_t* positions;  // nullptr: row t is at position t
+  const float* table;
+  unsigned* status;
+  long long x_stride, y_stride;  // elements between rows
+  uint32_t rows, table_rows;
+  int heads, D, R;
+  bool interleaved;
+  float sgn;  // 1: turn, -1: turn back
+  // Set by launch_rope_apply.
+  int units;
+  bool total_fits32;
+};
+int launch_rope_apply(RopeArgs a, int dtype, cudaStream_t s);
+
+struct RopeScale {
+  int kind;
+  double base, factor, orig_max_pos, beta_fast, beta_slow, attn_factor;
+};
+int launch_rope_table_scaled(float* table, uint32_t max_pos, int R, RopeScale sc, cudaStream_t s);
+
+struct AppendArgs {
+  const void* q;  // nullptr with H == 0
+  void* q_out;
+  const void* k;
+  const void* v;
+  void* k_pages;
+  void* v_pages;
+  const uint32_t* block_table;  // [n_seqs][max_blocks]
+  const uint32_t* q_start;      // [n_seqs + 1]
+  const uint32_t* kv_len;       // [n_seqs]
+  const float* table;
+  unsigned* status;
+  long long q_stride, q_out_stride, k_stride, v_stride, kv_dim;
+  uint32_t total_rows, table_rows;
+  int n_seqs, H, G, D, R;
+  int page_rows, num_pages, max_blocks;
+  bool interleaved;
+  int units;  // set by launch_append_paged
+};
+int launch_append_paged(AppendArgs a, int in_dtype, int cache_dtype, cudaStream_t s);
+
+// One record per thread block of the attention grid: the item whose first
+// keys the block computed and whose last keys a later block did.
+struct BatchSplit {
+  int valid;
+  int seq, blk, g;  // the item
+  int slot0;        // partial slot of this block's piece (the later pieces are in slot 0 of theirs)
+  int last;         // block holding the last piece
+  int pad[2];
+};
+
+struct BatchArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  void* out;
+  const uint32_t* block_table;  // [n_seqs][max_blocks]
+  const uint32_t* q_start;      // [n_seqs + 1]
+  const uint32_t* kv_len;       // [n_seqs]
+  const float* slopes;          // [H] or nullptr
+  const uint32_t* prefix_len;   // [n_seqs] or nullptr
+  unsigned* status;
+  float* partial;     // [2 * blocks][rows * (D + 2)]: unnormalised output, then (max, sum) of each row
+  BatchSplit* split;  // [blocks]
+  long long q_stride, out_stride, kv_dim;  // elements
+  uint32_t total_rows;
+  int n_seqs, H, G, D, gs;
+  int page_rows, num_pages, max_blocks, capacity;
+  int window;  // 0 = none
+  float scale, softcap;
+};
+// Sequences of a batch at most (the plan keeps one count each in shared memory).
+constexpr int kMaxBatchSeqs = 16384;
+size_t batch_workspace_bytes(int D, int sm_count);
+int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s);
+int launch_batch_mma(const BatchArgs& a, int dtype, int blocks, cudaStream_t s);
+int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, int rows, cudaStream_t s);
+
+}  // namespace attn

@@ -1,0 +1,267 @@
+// batch_plan.cuh -- how the batched paged attention divides a ragged batch
+// over a fixed grid, from lengths that only the device knows.
+//
+// The query rows of sequence s and kv head g are flattened as r = t * gs + j
+// (token t, head g * gs + j) and cut into blocks of ROWS; an item is one
+// (sequence, row block, kv head).  Its keys are the union of its rows'
+// windows, walked in tiles of KEYS.  Every item weighs its tiles plus kItemCost
+// (Q load, epilogue); the weights of all items, laid end to end in (sequence,
+// row block, kv head) order, are cut into equal ranges, one per thread block.  A
+// range boundary inside an item splits its keys: each part is a piece, whose
+// unnormalised output and (max, sum) go to a partial slot, and a second kernel
+// joins the pieces of an item in key order (so results do not depend on the
+// order in which blocks run).
+#pragma once
+
+#include <cstdint>
+
+#include "batch.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace attn {
+namespace plan {
+
+constexpr int kItemCost = 1;  // tiles
+
+struct SeqInfo {
+  int row0;   // first row of the token batch
+  int q_len;  // new tokens
+  int len;    // cached positions, the new ones included
+  int pfx;    // keys below it are visible to every row
+};
+
+__device__ __forceinline__ SeqInfo load_seq(const BatchArgs& a, int s) {
+  SeqInfo q;
+  const uint32_t b = a.q_start[s], e = a.q_start[s + 1], n = a.kv_len[s];
+  const bool ok = b <= e && e <= a.total_rows && n <= (uint32_t)a.capacity && n >= e - b;
+  if (!ok) record_status(a.status, ATTN_ERR_INVALID_ARG);
+  q.row0 = (int)b;
+  q.q_len = (b <= e && e <= a.total_rows) ? (int)(e - b) : 0;
+  q.len = (int)min(n, (uint32_t)a.capacity);
+  q.pfx = a.prefix_len != nullptr ? (int)min(a.prefix_len[s], (uint32_t)q.len) : 0;
+  return q;
+}
+
+// Keys [lo, hi) of the row of token t (empty when hi <= lo).
+__device__ __forceinline__ int row_hi(const SeqInfo& q, int t) { return max(q.len - q.q_len + t + 1, q.pfx); }
+__device__ __forceinline__ int row_lo(const BatchArgs& a, const SeqInfo& q, int t) {
+  const int n = q.len - q.q_len + t + 1;
+  return (a.window > 0 && n > a.window) ? n - a.window : 0;
+}
+
+struct BlockKeys {
+  int lo_min, lo_max, hi_min, hi_max;  // extremes over the block's rows
+  int kt0, nt;                         // key tiles kt0 .. kt0 + nt - 1
+};
+
+template <int ROWS>
+__device__ __forceinline__ int row_blocks(const BatchArgs& a, const SeqInfo& q) {
+  return (q.q_len * a.gs + ROWS - 1) / ROWS;
+}
+
+template <int ROWS, int KEYS>
+__device__ __forceinline__ BlockKeys block_keys(const BatchArgs& a, const SeqInfo& q, int b) {
+  const int t0 = (b * ROWS) / a.gs;
+  const int t1 = (min(q.q_len * a.gs, (b + 1) * ROWS) - 1) / a.gs;
+  BlockKeys k;
+  k.lo_min = row_lo(a, q, t0);
+  k.lo_max = row_lo(a, q, t1);
+  k.hi_min = row_hi(q, t0);
+  k.hi_max = row_hi(q, t1);
+  const bool any = k.hi_max > k.lo_min;
+  k.kt0 = k.lo_min / KEYS;
+  k.nt = any ? (k.hi_max + KEYS - 1) / KEYS - k.kt0 : 0;
+  return k;
+}
+
+struct Piece {
+  SeqInfo q;
+  BlockKeys k;
+  int s, b, g;
+  int t0, t1;     // tiles [t0, t1) of the item's nt
+  int slot;       // partial slot of a piece that is not the whole item
+  bool whole;
+};
+
+// What a block needs to walk its range; written by make_plan.
+struct Start {
+  long long left;  // units of this block
+  long long x;     // offset into the first item
+  long long u0;    // the range's first unit
+  long long per;   // units per block
+  int s, b, g;
+};
+
+// Inclusive scan of one value a thread over the whole block; *total gets the sum.
+template <int THREADS>
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long* total) {
+  static_assert(THREADS % 32 == 0 && THREADS <= 1024, "whole warps");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();  // warp_sums may still be read by an earlier scan
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const long long x = warp_sums[w];
+    if (w < warp) before += x;
+    all += x;
+  }
+  *total = all;
+  return v + before;
+}
+
+// The range of thread block `c` of `blocks`.  Every thread of the block calls it;
+// first_block holds n_seqs + 1 ints and warp_sums THREADS/32 values in shared
+// memory.  On return (after its final barrier) *start is valid.
+template <int ROWS, int KEYS, int THREADS>
+__device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_block, long long* warp_sums, Start* start) {
+  const int tid = threadIdx.x;
+  // Row blocks before each sequence.
+  long long carry = 0;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
+    const int s = s0 + tid;
+    const int nb = s < a.n_seqs ? row_blocks<ROWS>(a, load_seq(a, s)) : 0;
+    long long sum;
+    const long long incl = block_scan<THREADS>(nb, warp_sums, &sum);
+    if (s < a.n_seqs) first_block[s] = (int)(carry + incl - nb);
+    carry += sum;
+  }
+  const int n_blk = (int)carry;  // at most total_rows * gs / ROWS + n_seqs
+  if (tid == 0) {
+    first_block[a.n_seqs] = n_blk;
+    start->left = 0;
+    start->x = start->u0 = 0;
+    start->per = 1;
+    start->s = start->b = start->g = 0;
+  }
+  __syncthreads();
+  // Weights of this thread's share of the row blocks (all kv heads of each).
+  const int share = (n_blk + THREADS - 1) / THREADS;
+  const int i0 = min(n_blk, tid * share), i1 = min(n_blk, i0 + share);
+  int s = 0;
+  if (i0 < i1) {  // last sequence whose first block is at or before i0
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (first_block[mid] <= i0)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    s = lo;
+  }
+  long long mine = 0;
+  {
+    int ss = s;
+    SeqInfo q{};
+    int have = -1;
+    for (int i = i0; i < i1; ++i) {
+      while (first_block[ss + 1] <= i) ++ss;
+      if (have != ss) q = load_seq(a, have = ss);
+      mine += (long long)(block_keys<ROWS, KEYS>(a, q, i - first_block[ss]).nt + kItemCost) * a.G;
+    }
+  }
+  long long units;
+  const long long upto = block_scan<THREADS>(mine, warp_sums, &units);
+  const long long per = max((units + blocks - 1) / blocks, (long long)(kItemCost + 1));
+  const long long u0 = per * c;
+  long long at = upto - mine;
+  if (u0 >= at && u0 < upto) {  // this thread's share holds the range's start
+    int ss = s;
+    for (int i = i0; i < i1; ++i) {
+      while (first_block[ss + 1] <= i) ++ss;
+      const int w = block_keys<ROWS, KEYS>(a, load_seq(a, ss), i - first_block[ss]).nt + kItemCost;
+      if (u0 < at + (long long)w * a.G) {
+        start->g = (int)((u0 - at) / w);
+        start->x = (u0 - at) % w;
+        start->s = ss;
+        start->b = i - first_block[ss];
+        start->u0 = u0;
+        start->per = per;
+        start->left = min(per, units - u0);
+        break;
+      }
+      at += (long long)w * a.G;
+    }
+  }
+  __syncthreads();
+}
+
+// Walks the pieces of a block's range, in order.  Warps of different roles
+// walk it independently and see the same pieces.
+template <int ROWS, int KEYS>
+struct Walker {
+  const BatchArgs& a;
+  SeqInfo q;
+  long long left, x, u, per;
+  int s, b, g, nb, index;
+
+  __device__ __forceinline__ Walker(const BatchArgs& args, const Start& st)
+      : a(args), q{}, left(st.left), x(st.x), u(st.u0), per(st.per), s(st.s), b(st.b), g(st.g), nb(0), index(0) {
+    if (left > 0) {
+      q = load_seq(a, s);
+      nb = row_blocks<ROWS>(a, q);
+    }
+  }
+
+  // The next piece, or false.  `split` (may be nullptr) receives the record of
+  // an item that starts here and ends in a later block.
+  __device__ __forceinline__ bool next(Piece& p, BatchSplit* split = nullptr) {
+    while (left > 0) {
+      const BlockKeys k = block_keys<ROWS, KEYS>(a, q, b);
+      const long long w = k.nt + kItemCost;
+      const long long take = min(left, w - x);
+      p.q = q;
+      p.k = k;
+      p.s = s;
+      p.b = b;
+      p.g = g;
+      p.t0 = (int)max(0ll, x - kItemCost);
+      p.t1 = (int)max(0ll, x + take - kItemCost);
+      p.slot = index == 0 ? 0 : 1;
+      p.whole = p.t0 == 0 && p.t1 == k.nt;
+      const bool have = p.t1 > p.t0 || (k.nt == 0 && x == 0);
+      if (split != nullptr && p.t0 == 0 && p.t1 > 0 && p.t1 < k.nt) {
+        split->valid = 1;
+        split->seq = s;
+        split->blk = b;
+        split->g = g;
+        split->slot0 = p.slot;
+        split->last = (int)((u + w - x - 1) / per);
+      }
+      ++index;
+      x += take;
+      u += take;
+      left -= take;
+      if (x == w) {
+        x = 0;
+        if (++g == a.G) {
+          g = 0;
+          if (++b == nb) {
+            b = 0;
+            do {
+              if (++s >= a.n_seqs) {
+                left = 0;
+                break;
+              }
+              q = load_seq(a, s);
+              nb = row_blocks<ROWS>(a, q);
+            } while (nb == 0);
+          }
+        }
+      }
+      if (have) return true;
+    }
+    return false;
+  }
+};
+
+}  // namespace plan
+}  // namespace attn

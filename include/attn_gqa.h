@@ -20,7 +20,8 @@
  *   Scale      scores are scale * (q . k); forward and decode use
  *              scale = 1 / sqrt(D) (the meganeura shaders' inverseSqrt), prefill
  *              takes scale as an argument (the cera shader's params[5]).
- *   Data       fp32 in, fp32 out, row-major, all pointers are DEVICE memory
+ *   Data       fp32 in, fp32 out (the calls with an attn_dtype_t argument say
+ *              otherwise), row-major, all pointers are DEVICE memory
  *              owned by the caller.  The library keeps no pointer after a call
  *              returns.  Some calls need temporary scratch (the 16-bit K/V
  *              operand copies of the tensor-core paths, K turned for RoPE,
@@ -111,6 +112,20 @@ typedef enum {
 } attn_mask_t;
 
 typedef enum { ATTN_FP32 = 0, ATTN_TF32 = 1, ATTN_BF16 = 2 } attn_prec_t;
+
+/* Element types of the calls that take more than fp32 (attn_rope_apply,
+ * attn_append_paged, attn_batch_paged). */
+typedef enum { ATTN_DT_F32 = 0, ATTN_DT_BF16 = 1, ATTN_DT_F16 = 2 } attn_dtype_t;
+
+/* Which columns of a head make a rotary pair, and how its angles are scaled
+ * for contexts longer than the model's own (see attn_rope_table_scaled). */
+typedef enum { ATTN_ROPE_HALF = 0, ATTN_ROPE_INTERLEAVED = 1 } attn_rope_layout_t;
+typedef enum {
+    ATTN_ROPE_NONE = 0,
+    ATTN_ROPE_LINEAR = 1,
+    ATTN_ROPE_NTK = 2,
+    ATTN_ROPE_BY_PARTS = 3
+} attn_rope_scaling_t;
 
 enum {
     ATTN_OK = 0,
@@ -326,6 +341,151 @@ ATTN_API int attn_prefill_paged(const float *q_batch, const float *k_pages, cons
                                 uint32_t num_pages, uint32_t max_blocks, float scale, uint32_t start_pos,
                                 uint32_t q_stride, uint32_t out_stride, uint32_t q_base, attn_prec_t prec, uint32_t window,
                                 attn_stream_t stream);
+
+/*
+ * Rotary positions as an operator of its own, for fp32, bf16 or fp16 rows:
+ *   y = m R(p) x
+ * Of every head, the pairs (i, i + R/2) (ATTN_ROPE_HALF) or (2i, 2i + 1)
+ * (ATTN_ROPE_INTERLEAVED), i < R/2 with R = rot_dim, turn by the angle
+ * p theta_i of the row's position p; columns >= R are copied:
+ *   y[a] = m (x[a] cos - x[b] sin),  y[b] = m (x[b] cos + x[a] sin)
+ *
+ *   x, y        [rows, heads*D]; rows x_stride / y_stride elements apart, so
+ *               the Q and K heads of a packed projection are one call.  y may
+ *               be x (same stride); otherwise they must not overlap.
+ *   dtype       of x and y; the arithmetic is fp32, rounded once
+ *   positions   [rows] uint32 in device memory, or NULL: row t is at position t
+ *   table       [table_rows, R] fp32: m cos of the R/2 pairs, then m sin
+ *               (attn_rope_table_scaled, or attn_rope_table with head_dim = R)
+ *   inverse     != 0 turns by -p theta_i and still multiplies by m: the
+ *               gradient with respect to x of the call without it, for dy
+ * A position >= table_rows writes zeros to the row's turned columns and
+ * records ATTN_ERR_INVALID_ARG in the status word.  Sizes, strides or
+ * addresses that do not allow 16-byte groups (D, strides % 8; R % 16, or % 8
+ * interleaved) run one pair a thread.  rows == 0 is a no-op.  Errors:
+ * INVALID_ARG for NULL pointers, addresses not aligned to their element, an
+ * unknown type or layout, heads == 0, D == 0 or D > 1024, an odd, zero or too
+ * large rot_dim, strides < heads*D, y == x with different strides, or (with
+ * positions NULL) table_rows < rows.
+ *
+ * attn_rope_table_scaled fills such a table, angles in fp64.  theta_i =
+ * base^(-2i/R) (base > 1, rot_dim even and <= 1024), changed by `scaling`
+ * with factor f > 0:
+ *   ATTN_ROPE_NONE      as it is (factor is not read)
+ *   ATTN_ROPE_LINEAR    theta_i / f
+ *   ATTN_ROPE_NTK       the base becomes base f^(R/(R-2)) (rot_dim >= 4)
+ *   ATTN_ROPE_BY_PARTS  theta_i (g + (1 - g)/f) with g = clamp((orig_max_pos
+ *                       theta_i / 2 pi - beta_slow) / (beta_fast - beta_slow),
+ *                       0, 1): pairs that turn more than beta_fast times over
+ *                       the original context keep their angle, those below
+ *                       beta_slow are interpolated
+ * and m = attn_factor on every entry.  Errors: INVALID_ARG for values outside
+ * these rules or max_pos * rot_dim >= 2^31; max_pos == 0 is a no-op.
+ */
+ATTN_API int attn_rope_table_scaled(float *table, uint32_t max_pos, uint32_t rot_dim, double base,
+                                    attn_rope_scaling_t scaling, double factor, uint32_t orig_max_pos,
+                                    double beta_fast, double beta_slow, double attn_factor, attn_stream_t stream);
+ATTN_API int attn_rope_apply(const void *x, void *y, attn_dtype_t dtype, uint32_t rows, uint32_t heads,
+                             uint32_t head_dim, uint32_t rot_dim, uint32_t x_stride, uint32_t y_stride,
+                             attn_rope_layout_t layout, const uint32_t *positions, const float *table,
+                             uint32_t table_rows, int inverse, attn_stream_t stream);
+
+/*
+ * Batches of ragged sequences over one paged cache: append, then attention.
+ * Both calls take the same description of the batch, in DEVICE memory, so that
+ * a captured step replays as the sequences grow:
+ *   q_start      [n_seqs + 1]: the new tokens of sequence s are rows
+ *                [q_start[s], q_start[s+1]) of the token batch (ascending; a
+ *                sequence may have none).  Rows at or past q_start[n_seqs], up
+ *                to total_rows, belong to no sequence and are left untouched.
+ *   kv_len       [n_seqs]: positions of sequence s after the append, its new
+ *                tokens included; they are the last ones, so row i is at
+ *                position kv_len[s] - q_start[s+1] + i
+ *   block_table  [n_seqs, max_blocks]: position t of sequence s is row
+ *                t % page_rows of pool page block_table[s][t / page_rows].
+ *                Only entries of positions that are written or attended are
+ *                read.  Sequences may share pages they only read.
+ *   k_pages,
+ *   v_pages      pools of num_pages * page_rows rows of kv_dim elements; kv
+ *                head g at column g*D
+ * The limits on sizes are those of attn_prefill_paged.
+ *
+ * attn_append_paged writes the new rows' K, turned by their positions, and V
+ * into the pages, and (num_heads > 0) the turned Q into q_out; q and q_out
+ * NULL with num_heads == 0 leave Q out.
+ *   k_new, v_new, q   [total_rows, ...] of type dtype, rows *_stride elements
+ *                     apart; q_out of type cache_dtype
+ *   cache_dtype       dtype itself, or any type when dtype is ATTN_DT_F32
+ *                     (else ATTN_ERR_UNSUPPORTED); values are rounded once,
+ *                     after the turn.  fp32 pools serve attn_decode_paged and
+ *                     attn_prefill_paged, 16-bit ones attn_batch_paged.
+ *   rot_dim, layout,
+ *   table             as attn_rope_apply; rot_dim == 0 (table NULL) turns nothing
+ * A row whose position is negative, past the capacity page_rows * max_blocks
+ * or past the table, or whose page is >= num_pages, is skipped (nothing of it
+ * is written) and ATTN_ERR_INVALID_ARG recorded in the status word.  Two rows
+ * that name the same pool row leave one of the two there.  total_rows == 0 or
+ * n_seqs == 0 is a no-op.  q_out may be q when the types are the same.
+ * Errors: INVALID_ARG for NULL pointers, addresses not
+ * aligned to their element, bad heads, sizes, types, layout or strides.
+ */
+ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, const void *v_new, attn_dtype_t dtype,
+                               void *k_pages, void *v_pages, attn_dtype_t cache_dtype, const uint32_t *block_table,
+                               const uint32_t *q_start, const uint32_t *kv_len, uint32_t total_rows, uint32_t n_seqs,
+                               uint32_t num_heads, uint32_t num_kv_heads, uint32_t head_dim, uint32_t kv_dim,
+                               uint32_t q_stride, uint32_t q_out_stride, uint32_t k_stride, uint32_t v_stride,
+                               uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks, uint32_t rot_dim,
+                               attn_rope_layout_t layout, const float *table, uint32_t table_rows,
+                               attn_stream_t stream);
+
+/*
+ * attn_batch_paged: attention of every new token over its sequence's pages, in
+ * bf16 or fp16.  One call takes whole prompts, chunks behind a long cache,
+ * single tokens and any mixture.  The row at position p of sequence s, head h,
+ * attends the keys [lo, hi) with
+ *   lo = max(0, p + 1 - window)                          (window 0: lo = 0)
+ *   hi = max(p + 1, min(prefix_len[s], kv_len[s]))       (prefix_len NULL: p + 1)
+ * on the scores
+ *   s_j = scale (q . k_j)
+ *   s_j = softcap tanh(s_j / softcap)                    (softcap > 0)
+ *   s_j = s_j - alibi_slopes[h] |p - j|                  (alibi_slopes != NULL)
+ * and writes sum_j softmax(s)_j v_j, rounded to dtype; a row without keys
+ * writes zeros.
+ *
+ *   q, out          [total_rows, ...], rows q_stride / out_stride elements apart
+ *   dtype           of q, the pools and out
+ *   alibi_slopes    [n_heads] fp32; prefix_len [n_seqs] uint32 (device), or NULL
+ *   workspace       device buffer of attn_batch_paged_workspace_bytes(...)
+ *                   bytes, 16-byte aligned; needs no initialisation and holds
+ *                   nothing between calls.  Calls that share it must not overlap on the GPU.
+ * Scores, softmax and sums are fp32; P is rounded to dtype for the second
+ * product.  The work is divided over the GPU by each row block's number of key
+ * tiles, splitting keys where rows are few; splits are joined in key order by
+ * a second kernel, so repeated calls give identical bits.
+ * What the pages hold at positions that none of a sequence's rows attends, or
+ * past its end, never reaches a result.  K and V at positions that some row of
+ * the sequence attends must be finite (a NaN or infinity there may also reach
+ * rows of the same sequence that do not attend it).
+ * A block-table entry >= num_pages reads as zeros; it, a kv_len[s] past the
+ * capacity (the sequence is cut there) or below its number of new rows (rows
+ * before position 0 attend no keys of their own), and a q_start that
+ * descends or passes total_rows (the sequence is left out) record
+ * ATTN_ERR_INVALID_ARG in the status word.  total_rows == 0 or n_seqs == 0 is
+ * a no-op.  Errors: INVALID_ARG for NULL pointers, bad heads, sizes or
+ * strides, a non-finite scale, a negative or non-finite softcap, or a
+ * workspace that is too small or misaligned; UNSUPPORTED for
+ * ATTN_DT_F32 (attn_decode_paged and attn_prefill_paged serve fp32 pools),
+ * head_dim % 8 != 0, kv_dim or strides % 8 != 0, addresses of q, out or the pools that are not 16-byte
+ * aligned, more than 16384 sequences, or total_rows * n_heads > 2^30.
+ */
+ATTN_API size_t attn_batch_paged_workspace_bytes(uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim);
+ATTN_API int attn_batch_paged(const void *q, const void *k_pages, const void *v_pages, void *out, attn_dtype_t dtype,
+                              const uint32_t *block_table, const uint32_t *q_start, const uint32_t *kv_len,
+                              uint32_t total_rows, uint32_t n_seqs, uint32_t n_heads, uint32_t n_kv_heads,
+                              uint32_t head_dim, uint32_t kv_dim, uint32_t q_stride, uint32_t out_stride,
+                              uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks, float scale,
+                              uint32_t window, float softcap, const float *alibi_slopes, const uint32_t *prefix_len,
+                              void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /*
  * Backward of attn_forward / attn_forward_window: the gradients of `out` with

@@ -1,0 +1,250 @@
+"""attn_batch_paged (attention of a ragged batch's new tokens over a paged
+16-bit cache) against a plain 64-bit form.
+
+Pools are shuffled pages; every pool row that no sequence owns holds NaN, so
+reading past a sequence or through a wrong page shows."""
+import pytest
+import torch
+
+from batch_ref import Batch, attend_tolerance
+
+pytestmark = pytest.mark.gpu
+BF16, F16 = torch.bfloat16, torch.float16
+CUT = float("nan")
+
+
+def check(A, b, where="", q=None, **kw):
+    rows = b.starts[-1]
+    keep = torch.full((b.rows, b.H * b.D), 7.0, dtype=b.dtype, device="cuda")
+    call = dict(kw)
+    if "prefix" in call:
+        call["prefix_len"] = b.dev(call.pop("prefix"))
+    if "slopes" in call:
+        call["alibi_slopes"] = call.pop("slopes")
+    got = A.attend_paged(b.object(A), b.q if q is None else q, b.k, b.v, out=keep, **call)
+    torch.cuda.synchronize()
+    assert A.attn_get_status() == 0
+    ref, mag = b.attend(q=q, **kw)
+    err = (got[:rows].double() - ref[:rows]).abs()
+    assert torch.isfinite(got[:rows].float()).all(), where + ": non-finite output"
+    tol = attend_tolerance(ref, mag, b.dtype, max(b.kv + [1]))[:rows]
+    bad = err > tol
+    assert not bad.any(), "%s: %d of %d off, worst err/tol %.3g" % (where, int(bad.sum()), bad.numel(),
+                                                                    float((err / tol).max()))
+    assert (got[rows:] == 7.0).all(), where + ": rows of no sequence were written"
+    return got
+
+
+HEADS = [(1, 1, 64), (8, 2, 64), (32, 8, 128), (7, 1, 128), (16, 16, 64), (20, 4, 128), (16, 1, 64), (6, 2, 80),
+         (5, 5, 8), (10, 2, 120), (4, 2, 96), (130, 1, 64)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H,G,D", HEADS)
+def test_single_tokens(cuda_lib, H, G, D, dtype):
+    """One new token a sequence; lengths around tile, page and split borders."""
+    kv = [1, 2, 63, 64, 65, 127, 128, 129, 257, 1000]
+    check(cuda_lib, Batch([1] * len(kv), kv, H, G, D, 32, dtype, seed=H), "decode H%d G%d D%d" % (H, G, D))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H,G,D", HEADS)
+def test_chunks(cuda_lib, H, G, D, dtype):
+    """Prompts, chunks behind a cache and single tokens in one batch, an empty sequence among them."""
+    new = [5, 0, 1, 64, 130, 33, 1]
+    kv = [5, 40, 300, 64, 511, 129, 1]
+    check(cuda_lib, Batch(new, kv, H, G, D, 16, dtype, seed=H + 1, pad=3), "chunks H%d G%d D%d" % (H, G, D))
+
+
+@pytest.mark.parametrize("page_rows", [1, 7, 8, 16, 24, 48, 64, 100, 128, 256, 512])
+@pytest.mark.parametrize("D", [64, 128])
+def test_page_sizes(cuda_lib, page_rows, D):
+    b = Batch([1, 70, 200], [333, 70, 700], 8, 2, D, page_rows, BF16, seed=page_rows)
+    check(cuda_lib, b, "page_rows %d" % page_rows)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("window", [1, 2, 31, 64, 100, 128, 1000, 2 ** 32 - 1])
+def test_window(cuda_lib, window, dtype):
+    """Pages before a window hold NaN: they must not be read into a result."""
+    b = Batch([1, 1, 90, 150], [50, 700, 90, 900], 8, 2, 64, 16, dtype, seed=window % 97)
+    if window < 2 ** 31:
+        for i, (n, length) in enumerate(zip(b.new, b.kv)):
+            gone = max(0, length - n + 1 - window)
+            if gone:
+                sl = b.slots(i, 0, gone)
+                b.k[sl] = CUT
+                b.v[sl] = CUT
+    check(cuda_lib, b, "window %d" % window, window=window if window < 2 ** 31 else 0)
+    if window >= 2 ** 31:
+        got = cuda_lib.attend_paged(b.object(cuda_lib), b.q, b.k, b.v, window=window)
+        assert torch.equal(got, cuda_lib.attend_paged(b.object(cuda_lib), b.q, b.k, b.v))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("softcap", [1.0, 30.0, 50.0, 1e4])
+def test_softcap(cuda_lib, softcap, D, dtype):
+    b = Batch([1, 1, 77, 140], [600, 17, 77, 400], 14, 2, D, 32, dtype, seed=3)
+    check(cuda_lib, b, "cap %g" % softcap, softcap=softcap)
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_distance_bias(cuda_lib, softcap, prefix):
+    b = Batch([1, 1, 77, 140], [600, 17, 77, 400], 16, 4, 128, 64, BF16, seed=4)
+    slopes = 2.0 ** (-0.5 * torch.arange(1, 17, device="cuda", dtype=torch.float32))
+    kw = dict(prefix=[100, 17, 30, 399]) if prefix else {}
+    check(cuda_lib, b, "alibi", slopes=slopes, softcap=softcap, **kw)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("prefix", [[0, 0, 0, 0], [1, 5, 64, 128], [600, 17, 77, 400], [300, 2, 40, 261]])
+def test_prefix(cuda_lib, prefix, window):
+    """Keys below the prefix are visible to every row (a prefix longer than the sequence is cut)."""
+    b = Batch([1, 3, 77, 140], [600, 17, 77, 400], 8, 2, 64, 16, F16, seed=5)
+    check(cuda_lib, b, "prefix", prefix=prefix, window=window)
+
+
+def test_prefix_past_the_sequence_is_cut(cuda_lib):
+    b = Batch([3, 9], [30, 9], 4, 2, 64, 16, BF16, seed=6)
+    A, obj = cuda_lib, b.object(cuda_lib)
+    got = A.attend_paged(obj, b.q, b.k, b.v, prefix_len=b.dev([2 ** 31 - 1, 10]))
+    want = A.attend_paged(obj, b.q, b.k, b.v, prefix_len=b.dev([30, 9]))
+    torch.cuda.synchronize()
+    assert A.attn_get_status() == 0
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("H,G,D,new,kv", [
+    (32, 8, 128, [1], [20000]),            # few rows, many keys: split over the GPU
+    (8, 8, 64, [1] * 3, [30000, 1, 5]),
+    (32, 8, 128, [200], [9000]),
+    (8, 1, 128, [1] * 150, list(range(1, 3000, 20))),
+    (4, 4, 128, [900, 1, 300], [900, 4000, 2300]),
+])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_split_items(cuda_lib, H, G, D, new, kv, dtype):
+    check(cuda_lib, Batch(new, kv, H, G, D, 64, dtype, seed=7), "split")
+
+
+def test_large_scores(cuda_lib):
+    """Scores of standard deviation 30 (near one-hot rows), exact ties and a constant cache.  The score error
+    allowed for in the tolerance grows with the scores: 128 * 2^-24 * (16 * 30) < 2^-8, twice that in a weight."""
+    b = Batch([1, 40], [500, 300], 8, 2, 128, 32, BF16, seed=8)
+    q = (b.q.float() * 30).to(BF16)
+    got = cuda_lib.attend_paged(b.object(cuda_lib), q, b.k, b.v)
+    ref, mag = b.attend(q=q)
+    tol = attend_tolerance(ref, mag, BF16, 500) + 2.0 ** -7 * mag
+    assert ((got.double() - ref).abs() <= tol).all()
+    for i, n in enumerate(b.kv):
+        b.k[b.slots(i, 0, n)] = 0.5
+    check(cuda_lib, b, "ties")
+
+
+def test_repeated_calls_give_identical_bits_and_graph_replays_as_lengths_grow(cuda_lib):
+    A = cuda_lib
+    kv = [9, 700, 64, 2000]
+    b = Batch([1] * 4, kv, 32, 8, 128, 16, BF16, seed=9)
+    obj = b.object(A)
+    out = torch.zeros_like(b.q)
+    first = A.attend_paged(obj, b.q, b.k, b.v).clone()
+    for _ in range(3):
+        assert torch.equal(first, A.attend_paged(obj, b.q, b.k, b.v, out=out))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        A.attend_paged(obj, b.q, b.k, b.v, out=out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        A.attend_paged(obj, b.q, b.k, b.v, out=out)
+    for lens in ([1, 1, 1, 1], kv, [5, 300, 1, 1999]):
+        b.kv_len.copy_(b.dev(lens))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        b.kv = lens
+        ref, mag = b.attend()
+        assert ((out.double() - ref).abs() <= attend_tolerance(ref, mag, BF16, 2000)).all()
+    assert A.attn_get_status() == 0
+
+
+def test_strided_rows_wide_pools_and_another_stream(cuda_lib):
+    A = cuda_lib
+    b = Batch([1, 100], [400, 250], 8, 2, 64, 32, BF16, seed=10, kv_dim=192)
+    ref, mag = b.attend()
+    wide_q = torch.full((b.rows, 8 * 64 + 40), float("nan"), dtype=BF16, device="cuda")
+    wide_q[:, :512] = b.q
+    wide_o = torch.full((b.rows, 8 * 64 + 8), 3.0, dtype=BF16, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    A.attend_paged(b.object(A), wide_q[:, :512], b.k, b.v, out=wide_o[:, :512], stream=stream)
+    torch.cuda.synchronize()
+    assert ((wide_o[:, :512].double() - ref).abs() <= attend_tolerance(ref, mag, BF16, 400)).all()
+    assert (wide_o[:, 512:] == 3.0).all()
+
+
+def test_bad_device_values_are_reported_and_stay_in_bounds(cuda_lib):
+    """Values only the device sees: a page outside the pool reads as zeros, a length past the capacity is cut, a
+    length below the new rows leaves rows empty, a descending q_start leaves the sequence out."""
+    A = cuda_lib
+    b = Batch([1, 4, 2], [40, 60, 33], 4, 2, 64, 16, BF16, seed=11, extra_blocks=0)
+    table = b.table.clone()
+    bad = torch.tensor([[0, 1, -1, 2], [0, 1, 2, 3], [1, 2, 3, 4]], dtype=torch.int32)
+    table[:, :4] = torch.where(bad == -1, torch.full_like(bad, 2 ** 31 - 1), bad)
+    b.k.zero_()
+    b.v.fill_(1.0)
+    out = A.attend_paged(b.object(A, block_table=table.cuda()), b.q, b.k, b.v)
+    assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG
+    # Equal scores: sequence 0 averages 32 ones and the 8 zeros of positions 32..39.
+    assert torch.allclose(out[0].float(), torch.full((256,), 32 / 40, device="cuda"), atol=2 ** -8)
+    assert torch.allclose(out[1:].float(), torch.ones(6, 256, device="cuda"))
+    good = b.block_table
+    out = A.attend_paged(b.object(A, kv_len=b.dev([40, 2, 10 ** 6])), b.q, b.k, b.v)
+    assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG
+    assert (out[1:3] == 0).all() and torch.isfinite(out.float()).all()
+    assert good.shape[1] == 4
+    out = A.attend_paged(b.object(A, q_start=b.dev([0, 1, 0, 7])), b.q, b.k, b.v)
+    assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG
+    out = A.attend_paged(b.object(A, q_start=b.dev([0, 1, 5, 2 ** 31 - 1])), b.q, b.k, b.v)
+    assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG
+    assert (out[5:] == 0).all()
+
+
+def test_rows_without_keys_write_zeros(cuda_lib):
+    A = cuda_lib
+    b = Batch([2, 3], [64, 64], 8, 2, 128, 32, F16, seed=12)
+    out = torch.full_like(b.q, 5.0)
+    A.attend_paged(b.object(A, kv_len=b.dev([64, 0])), b.q, b.k, b.v, out=out)
+    assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG
+    assert (out[2:] == 0).all() and torch.isfinite(out.float()).all()
+
+
+def test_many_short_sequences(cuda_lib):
+    n = 3000
+    kv = [1 + (i * 7) % 40 for i in range(n)]
+    check(cuda_lib, Batch([1] * n, kv, 4, 2, 64, 16, BF16, seed=13), "3000 sequences")
+
+
+def test_refused_workspace_and_types(cuda_lib):
+    A = cuda_lib
+    b = Batch([1], [20], 4, 2, 64, 16, BF16, seed=14)
+    obj = b.object(A)
+    obj.workspace = obj.workspace[:-1]
+    out = torch.full_like(b.q, 9.0)
+    with pytest.raises(A.AttnError):
+        A.attend_paged(obj, b.q, b.k, b.v, out=out)
+    obj = b.object(A)
+    with pytest.raises(ValueError):
+        A.attend_paged(obj, b.q, b.k.half(), b.v, out=out)
+    with pytest.raises(A.AttnError):
+        A.attend_paged(obj, b.q.float(), b.k.float(), b.v.float())
+    with pytest.raises(ValueError):
+        A.attend_paged(obj, b.q, b.k[:-1], b.v[:-1], out=out)
+    with pytest.raises(ValueError):
+        A.attend_paged(obj, b.q, b.k, b.v, out=out, prefix_len=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        A.attend_paged(obj, b.q, b.k.cpu(), b.v.cpu(), out=out)
+    torch.cuda.synchronize()
+    assert (out == 9.0).all()
