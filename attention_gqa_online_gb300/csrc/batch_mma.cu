@@ -342,9 +342,17 @@ size_t batch_workspace_bytes(int D, int sm_count) {
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s) {
   a.split = static_cast<BatchSplit*>(workspace);
   a.partial = reinterpret_cast<float*>(a.split + 2 * sm_count);
-  const int blocks = 2 * sm_count;
-  const int rc = launch_batch_mma(a, dtype, blocks, s);
-  return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, blocks, kRows, s);
+  // The tensor-core kernel moves pages by TMA boxes of the largest power of
+  // two of rows that divides a page, whole 8-row groups of the swizzle.
+  int box = a.page_rows & -a.page_rows;
+  if (box > 128) box = 128;
+  if ((a.D == 64 || a.D == 128) && box >= 8) {
+    const int rc = a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s)
+                             : launch_batch_tc_d128(a, dtype, sm_count, box, s);
+    return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, sm_count, 128, s);
+  }
+  const int rc = launch_batch_mma(a, dtype, 2 * sm_count, s);
+  return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, 2 * sm_count, kRows, s);
 }
 
 }  // namespace attn

@@ -30,13 +30,14 @@ inline ScoreMap score_map(const BatchArgs& a) {
 // whose cancellation is harmless there (absolute error about 2^-23 against
 // values above 0.55).
 constexpr float kTanhPolyMax = 0.625f;
+constexpr float kTanhQ0 = -0.333333283662796f, kTanhQ1 = 0.1333276927471161f, kTanhQ2 = -0.05385090783238411f,
+                kTanhQ3 = 0.020997179672122f, kTanhQ4 = -0.006096714176237583f;
 __device__ __forceinline__ float tanh_poly(float x) {
   const float u = x * x;
-  float q = -0.006096714176237583f;
-  q = fmaf(q, u, 0.020997179672122f);
-  q = fmaf(q, u, -0.05385090783238411f);
-  q = fmaf(q, u, 0.1333276927471161f);
-  q = fmaf(q, u, -0.333333283662796f);
+  float q = fmaf(kTanhQ4, u, kTanhQ3);
+  q = fmaf(q, u, kTanhQ2);
+  q = fmaf(q, u, kTanhQ1);
+  q = fmaf(q, u, kTanhQ0);
   return fmaf(x, u * q, x);
 }
 __device__ __forceinline__ float tanh_exp(float x) {
