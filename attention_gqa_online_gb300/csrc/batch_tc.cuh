@@ -418,13 +418,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto epilogue = [&](int x, int jl) {
       const PieceDesc& d = sm.desc[x % kDescs];
       const bool busy = 32 * qd < d.rows;
-      uint32_t o[kHalfD / 32][32];
       float inv = 0.f, m_fin = -INFINITY, l_row = 0.f;
       // A parity wait needs the phase before it to be over: for the other group's tile jl that follows from P V
       // of this group's tile jl - 1 (products complete in order).
       if (jl > 0 && (jl & 1) != grp) wait(&sm.pv_done[(jl - 1) & 1], (jl - 1) >> 1);
       wait(&sm.pv_done[jl & 1], jl >> 1);
       tc::fence_after_sync();
+      T* dst = nullptr;
+      float* part = nullptr;
       if (busy) {
         wait(&sm.stat_bar[qd][x & 1][grp ^ 1], x >> 1);
         const float2 s0 = sm.stat[x & 1][0][r], s1 = sm.stat[x & 1][1][r];
@@ -432,40 +433,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (s0.y != 0.f) l_row += s0.y * ex2(s0.x - m_fin);
         if (s1.y != 0.f) l_row += s1.y * ex2(s1.x - m_fin);
         inv = l_row == 0.f ? 0.f : 1.f / l_row;
-#pragma unroll
-        for (int c = 0; c < kHalfD / 32; ++c) tc::tmem_ld32(o_col + grp * kHalfD + 32 * c, o[c]);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < kHalfD / 32; ++c) tc::reg_fence(o[c]);
-      }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.o_free);
-      if (r < d.rows) {
         if (d.whole) {
           const int f = d.blk * kTcRows + r, t = f / a.gs, h = d.g * a.gs + f % a.gs;
-          T* dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D + grp * kHalfD;
-#pragma unroll
-          for (int c = 0; c < kHalfD / 32; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = l_row == 0.f ? 0u
-                                    : pack_pair<T>(__uint_as_float(o[c][e + 2 * k]) * inv,
-                                                   __uint_as_float(o[c][e + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+          dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D + grp * kHalfD;
         } else {
-          float* part = a.partial + (long long)(2 * blockIdx.x + d.slot) * kTcRows * (D + 2);
-          float* dst = part + r * D + grp * kHalfD;
+          part = a.partial + (long long)(2 * blockIdx.x + d.slot) * kTcRows * (D + 2);
+          if (grp == 0 && r < d.rows) *reinterpret_cast<float2*>(part + kTcRows * D + 2 * r) = make_float2(m_fin, l_row);
+          part += r * D + grp * kHalfD;
+        }
+      }
+      const bool store = r < d.rows;
 #pragma unroll
-          for (int c = 0; c < kHalfD / 32; ++c)
+      for (int c = 0; c < kHalfD / 32; ++c) {  // 32 columns at a time; O is free after the last read
+        uint32_t o[32];
+        if (busy) {
+          tc::tmem_ld32(o_col + grp * kHalfD + 32 * c, o);
+          tc::tmem_ld_wait();
+          tc::reg_fence(o);
+        }
+        if (c == kHalfD / 32 - 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.o_free);
+        }
+        if (store && dst != nullptr) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(o[c][e], o[c][e + 1], o[c][e + 2], o[c][e + 3]);
-          if (grp == 0) *reinterpret_cast<float2*>(part + kTcRows * D + 2 * r) = make_float2(m_fin, l_row);
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = l_row == 0.f
+                         ? 0u
+                         : pack_pair<T>(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (store) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(part + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       __syncwarp();
