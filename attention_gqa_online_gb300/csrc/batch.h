@@ -91,6 +91,7 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
 int launch_batch_mma(const BatchArgs& a, int dtype, int blocks, cudaStream_t s);
 int launch_batch_tc_d64(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_d128(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
+int launch_batch_tc_pair(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, int rows, cudaStream_t s);
 
 }  // namespace attn

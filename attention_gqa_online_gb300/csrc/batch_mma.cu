@@ -315,9 +315,10 @@ template <typename T>
 int launch_combine_t(const BatchArgs& a, int blocks, int rows, cudaStream_t s) {
   BatchArgs b = a;
   void* args[] = {&b};
-  const void* kern = rows == 64 ? reinterpret_cast<const void*>(batch_combine_kernel<T, 64>)
-                                : reinterpret_cast<const void*>(batch_combine_kernel<T, 128>);
-  return launch_pdl(kern, dim3(blocks, 4), dim3(kJoinThreads), 0, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const void* kern = rows == 64    ? reinterpret_cast<const void*>(batch_combine_kernel<T, 64>)
+                     : rows == 128 ? reinterpret_cast<const void*>(batch_combine_kernel<T, 128>)
+                                   : reinterpret_cast<const void*>(batch_combine_kernel<T, 256>);
+  return launch_pdl(kern, dim3(blocks, rows / 16), dim3(kJoinThreads), 0, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -346,6 +347,12 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   // two of rows that divides a page, whole 8-row groups of the swizzle.
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
+  const bool pair = a.D == 128 && box >= 8 && 128 % a.gs == 0 && sm_count % 2 == 0 &&
+                    (long long)a.total_rows * a.gs >= 256ll * a.n_seqs;
+  if (pair) {
+    const int rc = launch_batch_tc_pair(a, dtype, sm_count, box, s);
+    return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, sm_count / 2, 256, s);
+  }
   if ((a.D == 64 || a.D == 128) && box >= 8) {
     const int rc = a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s)
                              : launch_batch_tc_d128(a, dtype, sm_count, box, s);

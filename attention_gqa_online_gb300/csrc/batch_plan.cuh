@@ -22,7 +22,7 @@
 namespace attn {
 namespace plan {
 
-constexpr int kItemCost = 1;  // tiles
+constexpr int kItemCost = 3;  // tiles
 
 struct SeqInfo {
   int row0;   // first row of the token batch

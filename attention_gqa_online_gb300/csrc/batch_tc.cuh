@@ -9,13 +9,14 @@
 // scores are already being made.
 //
 // Warp roles (384 threads; three warpgroups, so registers can be split):
-//   warp 0      K producer: one TMA box per page part and 64-column chunk
-//               (lane l takes the l-th part; a part no row of the block sees is
-//               fetched from outside the pool, which arrives as zeros)
-//   warp 1      issues both products of every tile, S_(J+2) = Q K^T before O += P_J V
-//   warp 2      V producer
-//   warp 3      planner: walks the pieces, writes their descriptors into a
-//               four-deep ring, and loads each piece's Q block (two buffers)
+//   warp 0      planner and K producer: walks the pieces, writes their descriptors
+//               into a four-deep ring, loads each piece's Q block (two buffers) and
+//               its K tiles, one TMA box per page part and 64-column chunk (lane l takes
+//               the l-th part; a part no row of the block sees is fetched from outside
+//               the pool, which arrives as zeros)
+//   warp 1      issues S_J = Q K^T, up to two tiles ahead of
+//   warp 2      which issues O += P_J V
+//   warp 3      V producer
 //   warps 4-7,
 //   warps 8-11  softmax groups 0 and 1: tile J (counted over all pieces of
 //               the block) belongs to group J & 1; a thread owns a whole row
@@ -36,8 +37,9 @@
 // one goes to its partial slot in fp32.
 //
 // Rows of V that lie in a fetched page part but outside the block's windows
-// hold whatever the page holds; the issuing warp zeroes them in shared memory
-// (0 * NaN would reach every row).  The same rows of K only make scores that are masked.
+// hold whatever the page holds (0 * NaN would reach every row): such parts are
+// fetched row by row, those rows from outside the pool, as zeros. The same
+// rows of K only make scores that are masked.
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
 // MMAs, frees its tensor memory and leaves the status word set.
@@ -71,26 +73,37 @@ struct PieceDesc {
   int end;         // no more pieces
   int whole;       // the item's only piece
   int seq, g, slot;
-  int row0, q_len, len, pfx, blk;
-  int rows;        // valid rows of the block
+  int row0, q_len, len, pfx;
+  int first_row;   // first flattened row of this block
+  int rows;        // valid rows from there on, at most 128
   int lo_min, lo_max, hi_min, hi_max;
-  int tile0, n;    // key tiles tile0 .. tile0 + n - 1 of the sequence
+  int tile_last, n;  // key tiles tile_last, tile_last - 1, ... (n of them) of the sequence
+  int pos_min;       // position of the block's first row
 };
 
-template <int D>
+// Shared memory of one block.  A pair splits the keys of a K tile and the
+// columns of a V tile, so each block holds half of both.
+template <int D, bool PAIR>
 struct TcLayout {
+  static constexpr int rows = PAIR ? 256 : 128;       // flattened rows of an item
   static constexpr int chunks = D / 64;               // 128-byte column chunks of a row
-  static constexpr int chunk_bytes = 128 * 128;       // 128 rows of one chunk
-  static constexpr int tile_bytes = chunks * chunk_bytes;
-  static constexpr int slots = D == 128 ? 2 : 4;      // K tiles (and V tiles) in flight
-  static constexpr int operand_bytes = (2 + 2 * slots) * tile_bytes;
+  static constexpr int q_chunk = 128 * 128;           // bytes of one chunk of the Q block
+  static constexpr int q_bytes = chunks * q_chunk;
+  static constexpr int k_rows = PAIR ? 64 : 128;      // keys of a tile held here
+  static constexpr int k_chunk = k_rows * 128;
+  static constexpr int k_bytes = chunks * k_chunk;
+  static constexpr int v_chunks = PAIR ? chunks / 2 : chunks;
+  static constexpr int v_chunk = kTcKeys * 128;
+  static constexpr int v_bytes = v_chunks * v_chunk;
+  static constexpr int slots = k_bytes == 32768 ? 2 : 4;  // K tiles (and V tiles) in flight: 128 KB or 64 KB in all
 };
 
-template <int D>
+template <int D, bool PAIR>
 struct __align__(1024) TcSmem {
-  unsigned char q[2][TcLayout<D>::tile_bytes];
-  unsigned char k[TcLayout<D>::slots][TcLayout<D>::tile_bytes];
-  unsigned char v[TcLayout<D>::slots][TcLayout<D>::tile_bytes];
+  using L = TcLayout<D, PAIR>;
+  unsigned char q[2][L::q_bytes];
+  unsigned char k[L::slots][L::k_bytes];
+  unsigned char v[L::slots][L::v_bytes];
   uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
   uint64_t q_ready[2], q_free[2];
   uint64_t desc_full[kDescs], desc_free[kDescs];
@@ -98,7 +111,7 @@ struct __align__(1024) TcSmem {
   uint64_t chain_bar[4][kChain];  // [row quarter][J & 3]
   uint64_t stat_bar[4][2][2];     // [row quarter][piece & 1][group]
   uint64_t o_free;                // both groups have read O
-  uint64_t drain;
+  uint64_t drain[2];
   float chain[kChain][kTcRows];
   float2 stat[2][2][kTcRows];  // [piece & 1][group][row]: reference, sum
   PieceDesc desc[kDescs];
@@ -123,20 +136,178 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
   return std::is_same<T, __half>::value ? tc::pack_f16(lo, hi) : tc::pack_bf16(lo, hi);
 }
 
+// ---------------------------------------------------------------- block pairs
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Address, in the cluster's shared window, of the same object in the pair's first block.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Arrives on a barrier of the first block.  These barriers hand over tensor
+// memory only, which tcgen05's own fences order, so the arrival needs no
+// cluster-scope release (which would wait for every store of the thread).
+template <bool PAIR>
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+  if (PAIR)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_leader(smem_u32(bar)))
+                 : "memory");
+  else
+    mbar_arrive(bar);
+}
+// Waits for phase `parity` of `bar`, within kWaitLimitNs (as mbar_wait_bounded).
+// The thread suspends in try_wait itself: the form with a time hint becomes a
+// polling loop with sleeps, whose wake-ups come late (SYNCS and NANOSLEEP were
+// a tenth of all instructions).  REMOTE: the other block's threads arrive.
+template <bool REMOTE>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag) {
+  unsigned long long t0 = 0;
+  for (unsigned n = 0;; ++n) {
+    unsigned ok;
+    if (REMOTE)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+    else
+      ok = mbar_try_wait(bar, parity);
+    if (ok) return true;
+    if (n % 16 == 15) {
+      if (*abort_flag != 0) return false;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        record_status(status, ATTN_ERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+// Tensor copies into this block's shared memory that complete on `bar` (a
+// barrier of the first block, by its cluster address, when PAIR).
+template <bool PAIR>
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// Tensor-memory allocation and commits of a pair: both blocks allocate, the
+// first one issues, and a commit arrives in both.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc_all(uint32_t* dst) {
+  if (PAIR)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+  else
+    tc::tmem_alloc(dst, 512);
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free_all(uint32_t tmem) {
+  if (PAIR) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit_all(uint64_t* bar) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+  else
+    tc::commit_elect(bar);
+}
+// Four MMAs into one accumulator, issued by one lane of the converged warp
+// (mma4_f16_* of tc.cuh for a pair).
+#define ATTN_PAIR_MMA4(AFORM)                                                          \
+  asm volatile(                                                                        \
+      "{\n\t.reg .pred p, t, e;\n\telect.sync _|e, 0xffffffff;\n\t"                    \
+      "setp.ne.b32 p, %10, 0;\n\tsetp.eq.b32 t, %10, %10;\n\t"                         \
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], " AFORM(1) ", %5, %9, p;\n\t"       \
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], " AFORM(2) ", %6, %9, t;\n\t"       \
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], " AFORM(3) ", %7, %9, t;\n\t"       \
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], " AFORM(4) ", %8, %9, t;\n\t}"
+#define ATTN_A_DESC(i) "%" #i
+#define ATTN_A_TMEM(i) "[%" #i "]"
+template <bool PAIR>
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a0, uint64_t b0, uint32_t idesc, uint32_t accumulate) {
+  if (PAIR)
+    ATTN_PAIR_MMA4(ATTN_A_DESC)::"r"(d), "l"(a0), "l"(a0 + 2), "l"(a0 + 4), "l"(a0 + 6), "l"(b0), "l"(b0 + 2),
+        "l"(b0 + 4), "l"(b0 + 6), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    tc::mma4_f16_ss(d, a0, a0 + 2, a0 + 4, a0 + 6, b0, b0 + 2, b0 + 4, b0 + 6, idesc, accumulate);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uint64_t st, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if (PAIR)
+    ATTN_PAIR_MMA4(ATTN_A_TMEM)::"r"(d), "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b0), "l"(b0 + st),
+        "l"(b0 + 2 * st), "l"(b0 + 3 * st), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    tc::mma4_f16_ts(d, a, a + 8, a + 16, a + 24, b0, b0 + st, b0 + 2 * st, b0 + 3 * st, idesc, accumulate);
+}
+#undef ATTN_A_TMEM
+#undef ATTN_A_DESC
+#undef ATTN_PAIR_MMA4
+
 // MODE 0: scores are scale2 * S with scale2 > 0 (folded into the exponent's
 // fma); 1: scaled, with an optional distance bias; 2: capped, with an optional
 // distance bias.
-template <typename T, int D, int MODE>
+template <typename T, int D, int MODE, bool PAIR>
 __global__ void __launch_bounds__(kTcThreads, 1)
     batch_tc_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_q,
-                    const int box_rows, const int q_box) {
-  using L = TcLayout<D>;
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1,
+                    const __grid_constant__ CUtensorMap tm_q, const int box_rows, const int q_box) {
+  using L = TcLayout<D, PAIR>;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr float kRescale = kHalf ? 8.f : 24.f;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  TcSmem<D>& sm = *reinterpret_cast<TcSmem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  TcSmem<D, PAIR>& sm = *reinterpret_cast<TcSmem<D, PAIR>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The block (or pair) of the plan, and this block's place in its pair.
+  const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, units = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+  const int rank = PAIR ? (int)pair_rank() : 0;
 
   allow_dependent_launch();
   if (warp == 0) {
@@ -150,37 +321,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sm.q_ready[lane], 1);
       mbar_init(&sm.q_free[lane], 1);
       mbar_init(&sm.s_full[lane], 1);
-      mbar_init(&sm.s_free[lane], 4);
-      mbar_init(&sm.p_ready[lane], 4);
+      mbar_init(&sm.s_free[lane], PAIR ? 8 : 4);  // the group's warps, of both blocks
+      mbar_init(&sm.p_ready[lane], PAIR ? 8 : 4);
       mbar_init(&sm.pv_done[lane], 1);
     }
     if (lane < kDescs) {
       mbar_init(&sm.desc_full[lane], 1);
-      mbar_init(&sm.desc_free[lane], 11);  // K, MMA, V warps and eight softmax warps
+      mbar_init(&sm.desc_free[lane], rank == 0 ? 10 : 9);  // producer, (first block) P V and eight softmax warps
     }
     if (lane < 16) {
       mbar_init(&sm.chain_bar[lane >> 2][lane & 3], 1);
       mbar_init(&sm.stat_bar[lane >> 2][(lane >> 1) & 1][lane & 1], 1);
     }
     if (lane == 31) {
-      mbar_init(&sm.o_free, 8);
-      mbar_init(&sm.drain, 1);
+      mbar_init(&sm.o_free, PAIR ? 16 : 8);
+      mbar_init(&sm.drain[0], 1);
+      mbar_init(&sm.drain[1], 1);
       sm.abort = 0;
     }
     fence_mbar_init();
   }
-  if (warp == 1) tc::tmem_alloc(&sm.tmem_base, 512);
+  if (warp == 1) tmem_alloc_all<PAIR>(&sm.tmem_base);
   // Lengths, tables and pages may be the previous kernel's output.
   grid_dependency_wait();
-  plan::make_plan<kTcRows, kTcKeys, kTcThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums,
-                                                &sm.start);
+  plan::make_plan<L::rows, kTcKeys, kTcThreads>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
   // The plan's scratch is where Q and the K/V tiles land.
   fence_async_smem();
   tc::fence_before_sync();
-  __syncthreads();
+  if (PAIR)
+    pair_sync();  // the other block's barriers are initialised, too
+  else
+    __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
-  auto wait = [&](uint64_t* bar, int phase) { return mbar_wait_bounded(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  auto wait = [&](uint64_t* bar, int phase) { return wait_phase<false>(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
   // Descriptor of piece x (its slot stays valid until every role has released it).
   auto piece = [&](int x) -> const PieceDesc& {
     wait(&sm.desc_full[x % kDescs], x / kDescs);
@@ -189,157 +363,69 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < 4) {
     regs_dec<kCtrlRegs>();
-    if (warp == 0 || warp == 2) {
-      // ---------------------------------------------------------- K and V producers
-      const bool is_v = warp == 2;
-      const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-      unsigned char* ring = is_v ? &sm.v[0][0] : &sm.k[0][0];
-      uint64_t* full = is_v ? sm.v_full : sm.k_full;
-      uint64_t* empty = is_v ? sm.v_empty : sm.k_empty;
-      if (lane == 0) prefetch_tmap(tm);
-      const int parts = kTcKeys / box_rows;
-      const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
-      int J = 0;
-      for (int x = 0; !*(volatile int*)&sm.abort; ++x) {
-        const PieceDesc& d = piece(x);
-        if (d.end || *(volatile int*)&sm.abort) break;
-        const uint32_t* table = a.block_table + (long long)d.seq * a.max_blocks;
-        const int lo = d.lo_min, hi = d.hi_max, col = d.g * D, n = d.n, tile0 = d.tile0;
-        for (int i = 0; i < n; ++i, ++J) {
-          int row = outside;
-          const int key = (tile0 + i) * kTcKeys + lane * box_rows;
-          if (lane < parts && key < hi && key + box_rows > lo) {
-            const uint32_t pg = table[key / a.page_rows];
-            if (pg < (uint32_t)a.num_pages)
-              row = (int)pg * a.page_rows + key % a.page_rows;
-            else
-              record_status(a.status, ATTN_ERR_INVALID_ARG);
-          }
-          const int slot = J % L::slots, use = J / L::slots;
-          if (use >= 1) wait(&empty[slot], use - 1);
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], (unsigned)L::tile_bytes);
-          __syncwarp();
-          if (lane < parts) {
-            unsigned char* dst = ring + slot * L::tile_bytes + lane * box_rows * 128;
-#pragma unroll
-            for (int c = 0; c < L::chunks; ++c)
-              tma_load_2d(dst + c * L::chunk_bytes, tm, col + 64 * c, row, &full[slot]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+    // The producers (warps 0 and 3) walk a piece's page parts.  Pool rows are read from the block table 32 parts at a
+    // time (one a lane), at least 32 parts ahead: a table read is a trip to L2, longer than a tile's products.
+    const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
+    struct Parts {
+      int parts;             // page parts of a tile held here
+      int n, lo, hi, key0;   // tiles; the windows' ends; first key held here of tile 0
+      const uint32_t* table;
+      int now, next;         // pool rows of 32 parts, and of the 32 after
+    };
+    auto rows_of = [&](const Parts& w, int q0) {
+      const int q = q0 + lane, key = w.key0 - (q / w.parts) * kTcKeys + (q % w.parts) * box_rows;
+      if (q >= w.n * w.parts || key >= w.hi || key + box_rows <= w.lo) return outside;
+      const uint32_t pg = w.table[key / a.page_rows];
+      return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key % a.page_rows : -1;
+    };
+    auto open_parts = [&](int keys, int n, int lo, int hi, int key0, int seq) {
+      Parts w{keys / box_rows, n, lo, hi, key0, a.block_table + (long long)seq * a.max_blocks, 0, 0};
+      w.now = rows_of(w, 0);
+      w.next = rows_of(w, 32);
+      return w;
+    };
+    // Pool row of this lane's part of tile i (tiles in order).
+    auto part_row = [&](Parts& w, int i) {
+      const int q0 = i * w.parts;
+      if (i > 0 && q0 % 32 == 0) {
+        w.now = w.next;
+        w.next = rows_of(w, q0 + 32);
       }
-      // No copy may still be landing in shared memory when the block exits.
-      for (int s = 0; s < L::slots && s < J; ++s) {
-        const int last = s + ((J - 1 - s) / L::slots) * L::slots;
+      int row = __shfl_sync(0xffffffffu, w.now, (q0 + lane) % 32);
+      if (lane >= w.parts) row = outside;
+      if (row < 0) {  // a page outside the pool
+        record_status(a.status, ATTN_ERR_INVALID_ARG);
+        row = outside;
+      }
+      return row;
+    };
+    auto barrier_of = [&](uint64_t* full) { return PAIR ? in_leader(smem_u32(full)) : smem_u32(full); };
+    // No copy may still be landing in shared memory when the block exits (a pair's copies all complete on the first
+    // block's barriers, and the pair leaves together).
+    auto drain_copies = [&](uint64_t* full, int issued) {
+      for (int s = 0; rank == 0 && s < L::slots && s < issued; ++s) {
+        const int last = s + ((issued - 1 - s) / L::slots) * L::slots;
         mbar_wait_bounded(&full[s], (unsigned)((last / L::slots) & 1), a.status);
       }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issue
-      constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
-      constexpr uint32_t idesc_qk = tc::idesc_f32acc(fmt, false, kTcRows, kTcKeys);
-      constexpr uint32_t idesc_pv = tc::idesc_f32acc(fmt, true, kTcRows, D);
-      const uint64_t dq0 = tc::sdesc_sw128(smem_u32(sm.q[0]), 16, 1024);
-      const uint64_t dk0 = tc::sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
-      const uint64_t dv0 = tc::sdesc_sw128(smem_u32(sm.v[0]), L::chunk_bytes, 1024);
-      constexpr uint64_t tile16 = L::tile_bytes >> 4;
-      auto wait_all = [&](uint64_t* bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)); };
-      int jq = 0, xq = 0, iq = 0, nq = 0;  // the next Q K^T: tile jq, the iq-th of piece xq
-      bool more_q = true, ok = true;
-      auto issue_qk = [&]() {
-        if (!more_q || !ok) return;
-        if (iq == 0) {
-          const PieceDesc& d = piece(xq);
-          if (d.end || *(volatile int*)&sm.abort) {
-            more_q = false;
-            return;
-          }
-          nq = d.n;
-          ok = wait_all(&sm.q_ready[xq & 1], xq >> 1);
-        }
-        const int slot = jq % L::slots, b = jq & 1;
-        ok = ok && wait_all(&sm.k_full[slot], jq / L::slots) && (jq < 2 || wait_all(&sm.s_free[b], (jq - 2) >> 1));
-        if (!ok) return;
-        tc::fence_after_sync();
-        const uint64_t dq = dq0 + (xq & 1) * tile16, dk = dk0 + slot * tile16;
-#pragma unroll
-        for (int c4 = 0; c4 < L::chunks; ++c4) {
-          const uint64_t c = (uint64_t)((c4 * L::chunk_bytes) >> 4);
-          tc::mma4_f16_ss(tmem + kTcKeys * b, dq + c, dq + c + 2, dq + c + 4, dq + c + 6, dk + c, dk + c + 2, dk + c + 4,
-                          dk + c + 6, idesc_qk, c4 > 0 ? 1u : 0u);
-        }
-        tc::commit_elect(&sm.s_full[b]);
-        tc::commit_elect(&sm.k_empty[slot]);
-        ++jq;
-        if (++iq == nq) {
-          tc::commit_elect(&sm.q_free[xq & 1]);
-          iq = 0;
-          ++xq;
-        }
-      };
-      issue_qk();
-      issue_qk();
-      int J = 0;
-      for (int x = 0; ok; ++x) {
-        const PieceDesc& d = piece(x);
-        if (d.end || *(volatile int*)&sm.abort) break;
-        const int n = d.n, lo = d.lo_min, hi = d.hi_max, tile0 = d.tile0;
-        for (int i = 0; ok && i < n; ++i, ++J) {
-          // S_(J+2) first: its buffer is free before P_J is written.
-          issue_qk();
-          const int slot = J % L::slots, b = J & 1;
-          ok = ok && wait_all(&sm.v_full[slot], J / L::slots);
-          if (!ok) break;
-          const int key0 = (tile0 + i) * kTcKeys;
-          if (key0 < lo || key0 + kTcKeys > hi) {
-            // Rows of fetched page parts outside the windows of every row.
-            const int za = max(0, (lo - key0) / box_rows * box_rows), zb = max(0, lo - key0);
-            const int zc = min(kTcKeys, hi - key0), zd = min(kTcKeys, (zc + box_rows - 1) / box_rows * box_rows);
-            for (int r = za + (lane >> 3); r < zd; r += 4) {
-              if (r >= zb && r < zc) continue;
-#pragma unroll
-              for (int c = 0; c < L::chunks; ++c)
-                *reinterpret_cast<uint4*>(sm.v[slot] + c * L::chunk_bytes + r * 128 + 16 * (lane & 7)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_async_smem();
-            __syncwarp();
-          }
-          // The first product of a piece replaces O: both groups have read the last one.
-          if (i == 0 && x > 0) ok = wait_all(&sm.o_free, x - 1);
-          ok = ok && wait_all(&sm.p_ready[b], J >> 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          const uint64_t dv = dv0 + slot * tile16;
-          constexpr uint64_t st = (16 * 128) >> 4;  // one K step: 16 key rows of 128 bytes
-#pragma unroll
-          for (int c4 = 0; c4 < kTcKeys / 64; ++c4) {
-            const uint64_t c = 4 * st * c4;
-            const uint32_t pa = tmem + kPColumn + 64 * b + 32 * c4;  // P: 8 columns (16 keys) per K step
-            tc::mma4_f16_ts(tmem + kOColumn, pa, pa + 8, pa + 16, pa + 24, dv + c, dv + c + st, dv + c + 2 * st,
-                            dv + c + 3 * st, idesc_pv, (i > 0 || c4 > 0) ? 1u : 0u);
-          }
-          tc::commit_elect(&sm.pv_done[b]);
-          tc::commit_elect(&sm.v_empty[slot]);
-        }
-        if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+    };
+    if (warp == 0) {
+      // ---------------------------------------------------------- planner, Q and K producer
+      if (lane == 0) {
+        prefetch_tmap(&tm_k);
+        if (q_box) prefetch_tmap(&tm_q);
       }
-      tc::commit_elect(&sm.drain);
-      mbar_wait_bounded(&sm.drain, 0, a.status);
-    } else {
-      // ---------------------------------------------------------- planner, Q loads
-      if (lane == 0 && q_box) prefetch_tmap(&tm_q);
       BatchSplit split{};
-      plan::Walker<kTcRows, kTcKeys> walk(a, sm.start);
+      plan::Walker<L::rows, kTcKeys> walk(a, sm.start);
       plan::Piece p;
-      int x = 0;
-      bool more = true;
-      while (more) {
-        more = walk.next(p, &split) && !*(volatile int*)&sm.abort;
-        const int rows = more ? min(kTcRows, p.q.q_len * a.gs - p.b * kTcRows) : 0;
+      int x = 0, J = 0;
+      while (true) {
+        const bool more = walk.next(p, &split) && !*(volatile int*)&sm.abort;
+        // This block's rows: 128 flattened rows from first_row on.
+        const int first_row = p.b * L::rows + rank * kTcRows;
+        const int rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
         if (more && p.t1 == p.t0) {  // rows without keys
           for (int r = lane >> 2; r < rows; r += 8) {
-            const int f = p.b * kTcRows + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+            const int f = first_row + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
             T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * D;
             for (int u = lane & 3; u < D / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -358,52 +444,179 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             d.q_len = p.q.q_len;
             d.len = p.q.len;
             d.pfx = p.q.pfx;
-            d.blk = p.b;
+            d.first_row = first_row;
             d.rows = rows;
             d.lo_min = p.k.lo_min;
             d.lo_max = p.k.lo_max;
             d.hi_min = p.k.hi_min;
             d.hi_max = p.k.hi_max;
-            d.tile0 = p.k.kt0 + p.t0;
+            d.tile_last = p.k.kt0 + p.t1 - 1;
             d.n = p.t1 - p.t0;
+            d.pos_min = p.q.len - p.q.q_len + first_row / a.gs;
           }
           mbar_arrive(&sm.desc_full[x % kDescs]);
         }
         __syncwarp();
         if (!more) break;
+        // The piece's first page parts are looked up while its Q buffer falls free.
+        const int n = p.t1 - p.t0, col = p.g * D;
+        Parts w = open_parts(L::k_rows, n, p.k.lo_min, p.k.hi_max,
+                             (p.k.kt0 + p.t1 - 1) * kTcKeys + (PAIR ? rank * L::k_rows : 0), p.s);
         // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
         // only feeds itself, and those rows are not stored).
         if (x >= 2) wait(&sm.q_free[x & 1], (x >> 1) - 1);
-        if (q_box) {  // whole tokens a block: one box per column chunk
+        if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
           if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)L::tile_bytes);
+            uint64_t* full = &sm.q_ready[x & 1];
+            const uint32_t bar = barrier_of(full);
+            if (rank == 0) mbar_arrive_expect_tx(full, (unsigned)(PAIR ? 2 : 1) * L::q_bytes);
 #pragma unroll
             for (int c = 0; c < L::chunks; ++c)
-              tma_load_3d(sm.q[x & 1] + c * L::chunk_bytes, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + p.b * (kTcRows / a.gs),
-                          &sm.q_ready[x & 1]);
+              load_3d<PAIR>(sm.q[x & 1] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + first_row / a.gs, bar);
           }
           __syncwarp();
-          ++x;
-          continue;
+        } else {
+          constexpr int kUnits = D / 8, kRowsPer = 32 / kUnits;  // units of a row over the lanes
+          const int u = lane % kUnits;
+          unsigned char* qt = sm.q[x & 1] + (u >> 3) * L::q_chunk;
+          const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * D + 8 * u;
+          for (int r = lane / kUnits; r < rows; r += kRowsPer) {
+            const int f = first_row + r, t = f / a.gs;
+            cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)), src + (long long)t * a.q_stride + (f - t * a.gs) * D, 16u);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.q_ready[x & 1]);
         }
-        constexpr int units = D / 8, rows_per = 32 / units;  // units of a row over the lanes
-        const int u = lane % units;
-        unsigned char* qt = sm.q[x & 1] + (u >> 3) * L::chunk_bytes;
-        const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * D + 8 * u;
-        for (int r = lane / units; r < rows; r += rows_per) {
-          const int f = p.b * kTcRows + r, t = f / a.gs;
-          cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)), src + (long long)t * a.q_stride + (f - t * a.gs) * D, 16u);
+        for (int i = 0; i < n; ++i, ++J) {
+          const int row = part_row(w, i), slot = J % L::slots;
+          if (J >= L::slots) wait(&sm.k_empty[slot], J / L::slots - 1);
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
+          __syncwarp();
+          if (lane < w.parts) {
+            const uint32_t bar = barrier_of(&sm.k_full[slot]);
+#pragma unroll
+            for (int c = 0; c < L::chunks; ++c)
+              load_2d<PAIR>(sm.k[slot] + c * L::k_chunk + lane * box_rows * 128, &tm_k, col + 64 * c, row, bar);
+          }
         }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_ready[x & 1]);
         ++x;
       }
-      if (lane == 0) a.split[blockIdx.x] = split;
-      // The Q copies of the last pieces have landed before the block exits.
-      for (int y = max(0, x - 2); q_box && y < x; ++y) mbar_wait_bounded(&sm.q_ready[y & 1], (unsigned)((y >> 1) & 1), a.status);
+      if (rank == 0 && lane == 0) a.split[unit] = split;
+      drain_copies(sm.k_full, J);
+      for (int y = max(0, x - 2); rank == 0 && (PAIR || q_box) && y < x; ++y)
+        mbar_wait_bounded(&sm.q_ready[y & 1], (unsigned)((y >> 1) & 1), a.status);
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- V producer
+      if (lane == 0) {
+        prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_v1);
+      }
+      int J = 0;
+      for (int x = 0; !*(volatile int*)&sm.abort; ++x) {
+        const PieceDesc& d = piece(x);
+        if (d.end || *(volatile int*)&sm.abort) break;
+        const int n = d.n, col = d.g * D + (PAIR ? rank * 64 * L::v_chunks : 0);
+        Parts w = open_parts(kTcKeys, n, d.lo_min, d.hi_max, d.tile_last * kTcKeys, d.seq);
+        for (int i = 0; i < n; ++i, ++J) {
+          const int row = part_row(w, i), key = w.key0 - i * kTcKeys + lane * box_rows, slot = J % L::slots;
+          if (J >= L::slots) wait(&sm.v_empty[slot], J / L::slots - 1);
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.v_full[slot], (unsigned)(PAIR ? 2 : 1) * L::v_bytes);
+          __syncwarp();
+          const uint32_t bar = barrier_of(&sm.v_full[slot]);
+          // A part that reaches outside the block's windows goes row by row: what the page holds there (0 * NaN would
+          // reach every row) is replaced by zeros from outside the pool.
+          const bool edge = row != outside && (key < w.lo || key + box_rows > w.hi);
+          if (lane < w.parts && !edge) {
+#pragma unroll
+            for (int c = 0; c < L::v_chunks; ++c)
+              load_2d<PAIR>(sm.v[slot] + c * L::v_chunk + lane * box_rows * 128, &tm_v, col + 64 * c, row, bar);
+          }
+          unsigned edges = __ballot_sync(0xffffffffu, edge);
+          while (edges) {
+            const int p = __ffs(edges) - 1;
+            edges &= edges - 1;
+            const int row_p = __shfl_sync(0xffffffffu, row, p), key_p = __shfl_sync(0xffffffffu, key, p);
+            for (int r = lane; r < box_rows; r += 32) {
+              const int y = key_p + r >= w.lo && key_p + r < w.hi ? row_p + r : outside;
+#pragma unroll
+              for (int c = 0; c < L::v_chunks; ++c)
+                load_2d<PAIR>(sm.v[slot] + c * L::v_chunk + (p * box_rows + r) * 128, &tm_v1, col + 64 * c, y, bar);
+            }
+          }
+        }
+        if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+      }
+      drain_copies(sm.v_full, J);
+    } else {
+      // ---------------------------------------------------------- MMA issue (the first block's, in a pair)
+      // Two warps, one a product, so that neither holds up the other; warp-uniform loops, one elected lane issues.
+      constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
+      auto wait_all = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, wait_phase<PAIR>(bar, (unsigned)(phase & 1), a.status, &sm.abort));
+      };
+      if (rank != 0) {
+      } else if (warp == 1) {
+        constexpr uint32_t idesc_qk = tc::idesc_f32acc(fmt, false, L::rows, kTcKeys);
+        const uint64_t dq0 = tc::sdesc_sw128(smem_u32(sm.q[0]), 16, 1024);
+        const uint64_t dk0 = tc::sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
+        bool ok = true;
+        int j = 0;
+        for (int x = 0; ok; ++x) {
+          const PieceDesc& d = piece(x);
+          if (d.end || *(volatile int*)&sm.abort) break;
+          const int n = d.n;
+          const uint64_t dq = dq0 + (uint64_t)((x & 1) * (L::q_bytes >> 4));
+          ok = wait_all(&sm.q_ready[x & 1], x >> 1);
+          for (int i = 0; ok && i < n; ++i, ++j) {
+            const int slot = j % L::slots, b = j & 1;
+            ok = wait_all(&sm.k_full[slot], j / L::slots) && (j < 2 || wait_all(&sm.s_free[b], (j - 2) >> 1));
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t dk = dk0 + (uint64_t)(slot * (L::k_bytes >> 4));
+#pragma unroll
+            for (int c = 0; c < L::chunks; ++c)
+              mma4_ss<PAIR>(tmem + kTcKeys * b, dq + (uint64_t)((c * L::q_chunk) >> 4),
+                            dk + (uint64_t)((c * L::k_chunk) >> 4), idesc_qk, c > 0 ? 1u : 0u);
+            commit_all<PAIR>(&sm.s_full[b]);
+            commit_all<PAIR>(&sm.k_empty[slot]);
+          }
+          commit_all<PAIR>(&sm.q_free[x & 1]);
+        }
+      } else {
+        constexpr uint32_t idesc_pv = tc::idesc_f32acc(fmt, true, L::rows, D);
+        const uint64_t dv0 = tc::sdesc_sw128(smem_u32(sm.v[0]), L::v_chunk, 1024);
+        bool ok = true;
+        int j = 0;
+        for (int x = 0; ok; ++x) {
+          const PieceDesc& d = piece(x);
+          if (d.end || *(volatile int*)&sm.abort) break;
+          const int n = d.n;
+          // The first product of a piece replaces O: both groups have read the last one.
+          if (x > 0) ok = wait_all(&sm.o_free, x - 1);
+          for (int i = 0; ok && i < n; ++i, ++j) {
+            const int slot = j % L::slots, b = j & 1;
+            ok = wait_all(&sm.v_full[slot], j / L::slots) && wait_all(&sm.p_ready[b], j >> 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t dv = dv0 + (uint64_t)(slot * (L::v_bytes >> 4));
+            constexpr uint64_t st = (16 * 128) >> 4;  // one K step: 16 key rows of 128 bytes
+#pragma unroll
+            for (int c4 = 0; c4 < kTcKeys / 64; ++c4)  // P: 8 columns (16 keys) per K step
+              mma4_ts<PAIR>(tmem + kOColumn, tmem + kPColumn + 64 * b + 32 * c4, dv + 4 * st * c4, st, idesc_pv,
+                            (i > 0 || c4 > 0) ? 1u : 0u);
+            commit_all<PAIR>(&sm.pv_done[b]);
+            commit_all<PAIR>(&sm.v_empty[slot]);
+          }
+          if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+        }
+      }
+      if (rank == 0) {
+        commit_all<PAIR>(&sm.drain[warp - 1]);
+        mbar_wait_bounded(&sm.drain[warp - 1], 0, a.status);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax groups
@@ -434,12 +647,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (s1.y != 0.f) l_row += s1.y * ex2(s1.x - m_fin);
         inv = l_row == 0.f ? 0.f : 1.f / l_row;
         if (d.whole) {
-          const int f = d.blk * kTcRows + r, t = f / a.gs, h = d.g * a.gs + f % a.gs;
+          const int f = d.first_row + r, t = f / a.gs, h = d.g * a.gs + f % a.gs;
           dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D + grp * kHalfD;
         } else {
-          part = a.partial + (long long)(2 * blockIdx.x + d.slot) * kTcRows * (D + 2);
-          if (grp == 0 && r < d.rows) *reinterpret_cast<float2*>(part + kTcRows * D + 2 * r) = make_float2(m_fin, l_row);
-          part += r * D + grp * kHalfD;
+          const int pr = rank * kTcRows + r;  // row of the item
+          part = a.partial + (long long)(2 * unit + d.slot) * L::rows * (D + 2);
+          if (grp == 0 && r < d.rows) *reinterpret_cast<float2*>(part + L::rows * D + 2 * pr) = make_float2(m_fin, l_row);
+          part += pr * D + grp * kHalfD;
         }
       }
       const bool store = r < d.rows;
@@ -454,7 +668,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (c == kHalfD / 32 - 1) {
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.o_free);
+          if (lane == 0) arrive_leader<PAIR>(&sm.o_free);
         }
         if (store && dst != nullptr) {
 #pragma unroll
@@ -494,7 +708,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       lo_r = hi_r = pos_r = 0;
       slope = 0.f;
       if (!done && r < d.rows) {
-        const int f = d.blk * kTcRows + r, t = f / a.gs;
+        const int f = d.first_row + r, t = f / a.gs;
         const plan::SeqInfo q{d.row0, d.q_len, d.len, d.pfx};
         lo_r = plan::row_lo(a, q, t);
         hi_r = plan::row_hi(q, t);
@@ -513,12 +727,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // No valid row in this warp: only keep the barriers going (P_b of tile j - 2 must have been read
           // before this tile's arrival).
           if (lane == 0) {
-            mbar_arrive(&sm.s_free[b]);
+            arrive_leader<PAIR>(&sm.s_free[b]);
             mbar_arrive(&sm.chain_bar[qd][j % kChain]);
           }
           if (j >= 2) wait(&sm.pv_done[b], (j - 2) >> 1);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_ready[b]);
+          if (lane == 0) arrive_leader<PAIR>(&sm.p_ready[b]);
         } else {
           const uint32_t s_col = tmem + lane_base + kTcKeys * b;
           uint32_t s[4][32];
@@ -529,10 +743,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; c < 4; ++c) tc::reg_fence(s[c]);
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s_free[b]);
+          if (lane == 0) arrive_leader<PAIR>(&sm.s_free[b]);
 
-          const int key0 = (d.tile0 + i) * kTcKeys;
-          if (MODE == 1) {
+          const int key0 = (d.tile_last - i) * kTcKeys;
+          if (MODE == 1 && a.slopes == nullptr) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -578,12 +792,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (MODE != 0 && a.slopes != nullptr) {
-            const float dist = (float)(key0 - pos_r);
+            // slope = -slopes[h] log2 e.  Behind the row, |p - j| = p - j and the bias is linear in the column.
+            const float mul = MODE == 1 ? sc.scale2 : 1.f, dist = (float)(key0 - pos_r);
+            if (a.prefix_len == nullptr || key0 + kTcKeys - 1 <= d.pos_min) {
+              const float first = -slope * dist;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[c][e] = __float_as_uint(fmaf(slope, fabsf(dist + (float)(32 * c + e)), __uint_as_float(s[c][e])));
+                for (int e = 0; e < 32; e += 2) {
+                  float x0 = __uint_as_float(s[c][e]), x1 = __uint_as_float(s[c][e + 1]);
+                  float b0 = -slope, b1 = -slope;
+                  fma2(b0, b1, (float)(32 * c + e), (float)(32 * c + e + 1), first, first);
+                  fma2(x0, x1, mul, mul, b0, b1);
+                  s[c][e] = __float_as_uint(x0);
+                  s[c][e + 1] = __float_as_uint(x1);
+                }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  s[c][e] = __float_as_uint(
+                      fmaf(slope, fabsf(dist + (float)(32 * c + e)), __uint_as_float(s[c][e]) * mul));
+            }
           }
           if (key0 + kTcKeys > d.hi_min) {  // the tile crosses some row's window end
             const int lim = hi_r - key0;
@@ -649,8 +880,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           l = l * ((m_new != m_ref) ? ex2(m_ref - m_new) : 1.f) + tsum;
           m_ref = m_new;
           // O holds the piece's earlier tiles against m_prev.
-          if (i > 0 && __any_sync(0xffffffffu, m_new != m_prev)) {
-            const float corr = (m_new != m_prev) ? ex2(m_prev - m_new) : 1.f;  // m_prev = -inf gives 0
+          // (A row that had no keys yet holds zeros there, whatever the factor.)
+          const bool moved = m_new != m_prev && m_prev != -INFINITY;
+          if (i > 0 && __any_sync(0xffffffffu, moved)) {
+            const float corr = moved ? ex2(m_prev - m_new) : 1.f;
             wait(&sm.pv_done[b ^ 1], (j - 1) >> 1);
             tc::fence_after_sync();
 #pragma unroll
@@ -667,7 +900,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc::tmem_st_wait();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_ready[b]);
+          if (lane == 0) arrive_leader<PAIR>(&sm.p_ready[b]);
         }
         i += 2;
       }
@@ -691,22 +924,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 
   tc::fence_before_sync();
-  __syncthreads();
+  if (PAIR)
+    pair_sync();  // arrivals, commits and copies cross the pair: it leaves together
+  else
+    __syncthreads();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
-    tc::tmem_relinquish();
+    tmem_free_all<PAIR>(tmem);
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool PAIR>
 int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   const uint64_t dims[2] = {(uint64_t)a.kv_dim, (uint64_t)a.num_pages * a.page_rows};
   const uint64_t strides[1] = {(uint64_t)a.kv_dim * 2};
-  const uint32_t box[2] = {64, (uint32_t)box_rows};
-  CUtensorMap tm_k, tm_v;  // 16-bit elements are only moved: one element type serves both
+  if (PAIR && box_rows > 64) box_rows = 64;  // a block holds 64 keys of a K tile
+  const uint32_t box[2] = {64, (uint32_t)box_rows}, one_row[2] = {64, 1};
+  CUtensorMap tm_k, tm_v, tm_v1;  // 16-bit elements are only moved: one element type serves both
   if (!make_tmap(&tm_k, a.k_pages, 2, dims, strides, box, true, kSwizzle128) ||
-      !make_tmap(&tm_v, a.v_pages, 2, dims, strides, box, true, kSwizzle128))
+      !make_tmap(&tm_v, a.v_pages, 2, dims, strides, box, true, kSwizzle128) ||
+      !make_tmap(&tm_v1, a.v_pages, 2, dims, strides, one_row, true, kSwizzle128))
     return ATTN_ERR_CUDA;
   // Q: [rows][H][D]; a row block is one box of gs heads x 128/gs tokens when gs divides 128.
   int q_box = kTcRows % a.gs == 0 ? 1 : 0;
@@ -720,16 +957,29 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   ScoreMap sc = score_map(a);
   const void* kern;
   if (a.softcap > 0.f)
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR>);
   else if (a.slopes != nullptr || !(sc.scale2 >= FLT_MIN))
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR>);
   else
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0>);
-  const size_t smem = sizeof(TcSmem<D>) + 1024;
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR>);
+  const size_t smem = sizeof(TcSmem<D, PAIR>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;
-  void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_q, &box_rows, &q_box};
-  return launch_pdl(kern, dim3(blocks), dim3(kTcThreads), smem, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &tm_q, &box_rows, &q_box};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, kern, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace

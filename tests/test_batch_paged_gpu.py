@@ -248,3 +248,44 @@ def test_refused_workspace_and_types(cuda_lib):
         A.attend_paged(obj, b.q, b.k.cpu(), b.v.cpu(), out=out)
     torch.cuda.synchronize()
     assert (out == 9.0).all()
+
+
+LONG = dict(new=[700, 1, 513, 0, 256, 255, 40], kv=[700, 2000, 900, 77, 300, 4000, 131])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H,G,page_rows", [(4, 4, 64), (8, 2, 16), (32, 8, 128), (8, 1, 8), (16, 1, 24), (128, 1, 32),
+                                           (3, 1, 64), (10, 2, 64)])
+def test_many_rows(cuda_lib, H, G, page_rows, dtype):
+    """Batches of mostly long chunks, at head dimension 128 and 64."""
+    for D in (128, 64):
+        b = Batch(LONG["new"], LONG["kv"], H, G, D, page_rows, dtype, seed=H + page_rows, pad=2)
+        check(cuda_lib, b, "long chunks H%d G%d D%d" % (H, G, D))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(softcap=30.0), dict(window=1), dict(window=200), dict(window=1000, softcap=5.0), dict(prefix=True),
+    dict(slopes=True), dict(slopes=True, prefix=True, window=300, softcap=50.0), dict(scale=0.0), dict(scale=-0.1)])
+def test_many_rows_with_masks_and_maps(cuda_lib, kw):
+    b = Batch(LONG["new"], LONG["kv"], 16, 4, 128, 16, BF16, seed=21)
+    kw = dict(kw)
+    if kw.get("prefix"):
+        kw["prefix"] = [350, 2000, 1, 77, 44, 3900, 131]
+    if kw.get("slopes"):
+        kw["slopes"] = 2.0 ** (-0.5 * torch.arange(1, 17, device="cuda", dtype=torch.float32))
+    if kw.get("window") and "prefix" not in kw:
+        for i, (n, length) in enumerate(zip(b.new, b.kv)):
+            gone = max(0, length - n + 1 - kw["window"])
+            if gone:
+                sl = b.slots(i, 0, gone)
+                b.k[sl] = CUT
+                b.v[sl] = CUT
+    check(cuda_lib, b, str(kw), **kw)
+
+
+def test_many_rows_repeat_bits(cuda_lib):
+    b = Batch(LONG["new"], LONG["kv"], 32, 8, 128, 64, BF16, seed=22)
+    obj = b.object(cuda_lib)
+    first = cuda_lib.attend_paged(obj, b.q, b.k, b.v)
+    for _ in range(20):
+        assert torch.equal(first, cuda_lib.attend_paged(obj, b.q, b.k, b.v))
