@@ -114,6 +114,7 @@ struct __align__(1024) TcSmem {
   uint64_t drain[2];
   float chain[kChain][kTcRows];
   float2 stat[2][2][kTcRows];  // [piece & 1][group][row]: reference, sum
+  int4 row[256];               // each softmax thread's own row: window [x, y), position z, slope w (as float bits)
   PieceDesc desc[kDescs];
   plan::Start start;
   long long warp_sums[kTcThreads / 32];
@@ -695,8 +696,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // piece whose epilogue waits for this group's next tile (its last tile is J - 1).
     int x = -1, J = 0, n = 0, i = 0, pend = -1;
     bool busy = false, done = false;
-    int lo_r = 0, hi_r = 0, pos_r = 0;
-    float slope = 0.f, m_ref = -INFINITY, l = 0.f;
+    float m_ref = -INFINITY, l = 0.f;
     auto open_piece = [&]() {  // the next piece's row data
       const PieceDesc& d = piece(++x);
       done = d.end || *(volatile int*)&sm.abort;
@@ -705,16 +705,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       busy = !done && 32 * qd < d.rows;
       m_ref = -INFINITY;
       l = 0.f;
-      lo_r = hi_r = pos_r = 0;
-      slope = 0.f;
+      int4 info = make_int4(0, 0, 0, 0);
       if (!done && r < d.rows) {
         const int f = d.first_row + r, t = f / a.gs;
         const plan::SeqInfo q{d.row0, d.q_len, d.len, d.pfx};
-        lo_r = plan::row_lo(a, q, t);
-        hi_r = plan::row_hi(q, t);
-        pos_r = d.len - d.q_len + t;
-        if (MODE != 0 && a.slopes != nullptr) slope = -kLog2e * a.slopes[d.g * a.gs + f % a.gs];
+        info.x = plan::row_lo(a, q, t);
+        info.y = plan::row_hi(q, t);
+        info.z = d.len - d.q_len + t;
+        if (MODE != 0 && a.slopes != nullptr) info.w = __float_as_int(-kLog2e * a.slopes[d.g * a.gs + f % a.gs]);
       }
+      sm.row[128 * grp + r] = info;  // read on the tiles that need it: kept in registers it would spill scores
     };
     open_piece();
     while (!done || pend >= 0) {
@@ -793,7 +793,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (MODE != 0 && a.slopes != nullptr) {
             // slope = -slopes[h] log2 e.  Behind the row, |p - j| = p - j and the bias is linear in the column.
-            const float mul = MODE == 1 ? sc.scale2 : 1.f, dist = (float)(key0 - pos_r);
+            const int4 info = sm.row[128 * grp + r];
+            const float slope = __int_as_float(info.w);
+            const float mul = MODE == 1 ? sc.scale2 : 1.f, dist = (float)(key0 - info.z);
             if (a.prefix_len == nullptr || key0 + kTcKeys - 1 <= d.pos_min) {
               const float first = -slope * dist;
 #pragma unroll
@@ -817,7 +819,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (key0 + kTcKeys > d.hi_min) {  // the tile crosses some row's window end
-            const int lim = hi_r - key0;
+            const int lim = sm.row[128 * grp + r].y - key0;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -825,7 +827,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (32 * c + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
           }
           if (key0 < d.lo_max) {  // ... or some row's window start
-            const int lim = lo_r - key0;
+            const int lim = sm.row[128 * grp + r].x - key0;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -854,20 +856,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (lane == 0) mbar_arrive(&sm.chain_bar[qd][j % kChain]);
           const float neg_m = (m_new == -INFINITY) ? 0.f : -m_new;
 
-          float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          // Sixteen scores at a time: exponents, then exponentials, then sums and packing, so that the long-latency
+          // exponentials of a batch are in flight together.
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x0 = __uint_as_float(s[c][e]), x1 = __uint_as_float(s[c][e + 1]);
-              if (MODE == 0)
-                fma2(x0, x1, cf, cf, neg_m, neg_m);
-              else
-                add2(x0, x1, neg_m, neg_m);
-              const float p0 = ex2(x0), p1 = ex2(x1);
-              const int k = (e >> 1) & 3;
-              add2(sum[2 * k], sum[2 * k + 1], p0, p1);
-              s[c][e >> 1] = pack_pair<T>(p0, p1);
+            for (int h = 0; h < 2; ++h) {
+              float e[16];
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                e[k] = __uint_as_float(s[c][16 * h + k]);
+                e[k + 1] = __uint_as_float(s[c][16 * h + k + 1]);
+                if (MODE == 0)
+                  fma2(e[k], e[k + 1], cf, cf, neg_m, neg_m);
+                else
+                  add2(e[k], e[k + 1], neg_m, neg_m);
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) e[k] = ex2(e[k]);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                add2(sum[k & 2], sum[(k & 2) + 1], e[k], e[k + 1]);
+                s[c][8 * h + (k >> 1)] = pack_pair<T>(e[k], e[k + 1]);
+              }
             }
           // P_b was last read by P V of tile j - 2.
           if (j >= 2) {
@@ -876,7 +888,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::tmem_st16(tmem + lane_base + kPColumn + 64 * b + 16 * c, s[c]);
-          const float tsum = ((sum[0] + sum[1]) + (sum[2] + sum[3])) + ((sum[4] + sum[5]) + (sum[6] + sum[7]));
+          const float tsum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
           l = l * ((m_new != m_ref) ? ex2(m_ref - m_new) : 1.f) + tsum;
           m_ref = m_new;
           // O holds the piece's earlier tiles against m_prev.
