@@ -30,38 +30,107 @@ def rope_table(max_pos, head_dim, base=10000.0, device="cuda", stream=None, scal
 
 def _on(x, *others):
     """The device of x as the current one for a call; every tensor of the call must be on it."""
-    for o in others:
-        if o is not None and o.device != x.device:
-            raise ValueError("tensors of one call must be on one device, got %s and %s" % (x.device, o.device))
+    _same_device(x.get_device(), *others)
     return torch.cuda.device(x.device)
+
+
+# The calls below are made once a layer of a serving step, where a microsecond of Python counts as much as one on
+# the GPU: they check with the cheapest queries and hand addresses to the library directly.
+_CODES = {torch.float32: B.ATTN_DT_F32, torch.bfloat16: B.ATTN_DT_BF16, torch.float16: B.ATTN_DT_F16}
+_INT32 = (torch.int32, torch.uint32)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _same_device(index, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors of one call must be on one CUDA device, got cuda:%d and %s" % (index, t.device)
+                             if index >= 0 else "tensors must be in device memory, got %s" % t.device)
+
+
+def _code(x, name):
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise ValueError("%s must be float32, bfloat16 or float16, got %s" % (name, x.dtype))
+    return code
+
+
+def _like(dtype, name, x):
+    if x is not None and x.dtype != dtype:
+        raise ValueError("%s has type %s, unlike the tensors it goes with (%s)" % (name, x.dtype, dtype))
+
+
+def _int32(x, name):
+    """Address of a contiguous tensor of 32-bit integers, or None."""
+    if x is None:
+        return None
+    if x.dtype not in _INT32 or not x.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of 32-bit integers" % name)
+    return x.data_ptr()
+
+
+def _run(where, fn, index, stream, args):
+    """Calls library function `fn` with `args` and the stream, on device `index`."""
+    if index < 0:
+        raise ValueError("tensors must be in device memory")
+    if stream is None:
+        stream = _raw_stream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, stream)
+    if code:
+        raise B.AttnError(code, where)
 
 
 def _rows2d(x, name):
     """Row stride of a [rows, columns] tensor whose columns are contiguous."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    rows, columns = x.shape if x.dim() == 2 else (0, 0)
+    stride, one = x.stride() if x.dim() == 2 else (0, 0)
+    if x.dim() != 2 or (one != 1 and columns > 1):
         raise ValueError("%s must be [rows, columns] with contiguous columns" % name)
     # The stride of a single row is never used, and torch may leave anything there.
-    return max(x.stride(0), x.shape[1]) if x.shape[0] > 1 else x.shape[1]
+    return stride if rows > 1 else columns
+
+
+def _table(table, rot_dim):
+    """(address, rows) of a rotary table, or (None, 0)."""
+    if table is None:
+        return None, 0
+    if table.dim() != 2 or table.shape[1] != rot_dim or table.dtype != torch.float32 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous float32 [positions, %d] table of rope_table" % rot_dim)
+    return table.data_ptr(), table.shape[0]
 
 
 def _rope(x, table, heads, positions, rot_dim, interleaved, out, inverse, stream):
     xs = _rows2d(x, "x")
-    if heads < 1 or x.shape[1] % heads:
-        raise ValueError("x has %d columns, not a multiple of %d heads" % (x.shape[1], heads))
-    D = x.shape[1] // heads
-    rot_dim = D if rot_dim is None else rot_dim
-    if table.dim() != 2 or table.shape[1] != rot_dim or not table.is_contiguous():
-        raise ValueError("table must be a contiguous [positions, %d] table of rope_table" % rot_dim)
-    if positions is not None and positions.numel() != x.shape[0]:
+    rows, columns = x.shape
+    if heads < 1 or columns % heads:
+        raise ValueError("x has %d columns, not a multiple of %d heads" % (columns, heads))
+    D = columns // heads
+    if rot_dim is None:
+        rot_dim = D
+    code = _code(x, "x")
+    tab, tab_rows = _table(table, rot_dim)
+    pos = _int32(positions, "positions")
+    if pos is not None and positions.numel() != rows:
         raise ValueError("positions must hold one position a row")
+    index = x.get_device()
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape:
-        raise ValueError("out must have the shape of x")
-    with _on(x, table, positions, out):
-        B.attn_rope_apply(x, out, x.shape[0], heads, D, rot_dim, xs, _rows2d(out, "out"),
-                          B.ATTN_ROPE_INTERLEAVED if interleaved else B.ATTN_ROPE_HALF, positions, table, None, inverse,
-                          stream)
+        ys = columns
+    else:
+        if out.shape != x.shape:
+            raise ValueError("out must have the shape of x")
+        _like(x.dtype, "out", out)
+        ys = _rows2d(out, "out")
+    _same_device(index, table, positions, out)
+    _run("attn_rope_apply", B.load_library().attn_rope_apply, index, stream,
+         (x.data_ptr(), out.data_ptr(), code, rows, heads, D, rot_dim, xs, ys, 1 if interleaved else 0, pos, tab,
+          tab_rows, 1 if inverse else 0))
     return out
 
 
@@ -174,10 +243,11 @@ class PagedBatch:
 
     def pool(self, k_pages, v_pages):
         """(kv_dim, num_pages) of two pools [num_pages * page_rows, kv_dim]."""
-        if k_pages.shape != v_pages.shape or k_pages.dim() != 2 or k_pages.shape[0] % self.page_rows or \
+        shape = k_pages.shape
+        if shape != v_pages.shape or len(shape) != 2 or shape[0] % self.page_rows or \
                 not k_pages.is_contiguous() or not v_pages.is_contiguous():
             raise ValueError("k_pages and v_pages must be contiguous [num_pages * page_rows, kv_dim] pools")
-        return k_pages.shape[1], k_pages.shape[0] // self.page_rows
+        return shape[1], shape[0] // self.page_rows
 
 
 def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, table=None, rot_dim=None,
@@ -185,22 +255,43 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
     """Write the batch's new K (turned by `table`, when given) and V rows into the pages; with q, also
     return it turned, in the cache's type (q_out when given)."""
     kv_dim, num_pages = batch.pool(k_pages, v_pages)
-    rows, D, G = k_new.shape[0], batch.head_dim, batch.num_kv_heads
-    H = 0 if q is None else batch.num_heads
-    for name, x, heads in (("k_new", k_new, G), ("v_new", v_new, G), ("q", q, H), ("q_out", q_out, H)):
-        if x is not None and tuple(x.shape) != (rows, heads * D):
-            raise ValueError("%s must be [%d, %d]" % (name, rows, heads * D))
-    if q is not None and q_out is None:
-        q_out = torch.empty((rows, H * D), dtype=k_pages.dtype, device=q.device)
-    R = 0 if table is None else (D if rot_dim is None else rot_dim)
-    if table is not None and (table.dim() != 2 or table.shape[1] != R or not table.is_contiguous()):
-        raise ValueError("table must be a contiguous [positions, %d] table of rope_table" % R)
-    with _on(k_pages, v_pages, k_new, v_new, q, q_out, table, batch.block_table):
-        B.attn_append_paged(q, q_out, k_new, v_new, k_pages, v_pages, batch.block_table, batch.q_start, batch.kv_len,
-                            rows, batch.n_seqs, H, G, D, kv_dim, _rows2d(q, "q") if H else 0,
-                            _rows2d(q_out, "q_out") if H else 0, _rows2d(k_new, "k_new"), _rows2d(v_new, "v_new"),
-                            batch.page_rows, num_pages, batch.max_blocks, R,
-                            B.ATTN_ROPE_INTERLEAVED if interleaved else B.ATTN_ROPE_HALF, table, None, stream)
+    D, G = batch.head_dim, batch.num_kv_heads
+    ks, vs = _rows2d(k_new, "k_new"), _rows2d(v_new, "v_new")
+    rows = k_new.shape[0]
+    if k_new.shape[1] != G * D or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [rows, %d]" % (G * D))
+    dtype, cache = k_new.dtype, k_pages.dtype
+    code, cache_code = _code(k_new, "k_new"), _code(k_pages, "k_pages")
+    _like(dtype, "v_new", v_new)
+    _like(cache, "v_pages", v_pages)
+    if rot_dim is None:
+        rot_dim = D
+    tab, tab_rows = _table(table, rot_dim)
+    index = k_pages.get_device()
+    H = qs = qos = 0
+    q_ptr = qo_ptr = None
+    if q is not None:
+        H = batch.num_heads
+        qs = _rows2d(q, "q")
+        if q.shape[0] != rows or q.shape[1] != H * D:
+            raise ValueError("q must be [%d, %d]" % (rows, H * D))
+        _like(dtype, "q", q)
+        if q_out is None:
+            q_out = torch.empty((rows, H * D), dtype=cache, device=q.device)
+            qos = H * D
+        else:
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have the shape of q")
+            _like(cache, "q_out", q_out)
+            qos = _rows2d(q_out, "q_out")
+        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
+        _same_device(index, q, q_out)
+    _same_device(index, v_pages, k_new, v_new, table, batch.block_table, batch.q_start, batch.kv_len)
+    _run("attn_append_paged", B.load_library().attn_append_paged, index, stream,
+         (q_ptr, qo_ptr, k_new.data_ptr(), v_new.data_ptr(), code, k_pages.data_ptr(), v_pages.data_ptr(), cache_code,
+          _int32(batch.block_table, "block_table"), _int32(batch.q_start, "q_start"), _int32(batch.kv_len, "kv_len"),
+          rows, batch.n_seqs, H, G, D, kv_dim, qs, qos, ks, vs, batch.page_rows, num_pages, batch.max_blocks,
+          rot_dim if tab is not None else 0, 1 if interleaved else 0, tab, tab_rows))
     return q_out
 
 
@@ -212,21 +303,38 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
     left as they are in `out`."""
     kv_dim, num_pages = batch.pool(k_pages, v_pages)
     H, D = batch.num_heads, batch.head_dim
-    if q.dim() != 2 or q.shape[1] != H * D:
+    qs = _rows2d(q, "q")
+    rows = q.shape[0]
+    if q.shape[1] != H * D:
         raise ValueError("q must be [rows, %d]" % (H * D))
+    dtype = q.dtype
+    code = _code(q, "q")
+    _like(dtype, "k_pages", k_pages)
+    _like(dtype, "v_pages", v_pages)
     if out is None:
-        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    if alibi_slopes is not None and (alibi_slopes.numel() != H or not alibi_slopes.is_contiguous()):
-        raise ValueError("alibi_slopes must hold one slope a head")
+        out = torch.zeros((rows, H * D), dtype=dtype, device=q.device)
+        os = H * D
+    else:
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+        _like(dtype, "out", out)
+        os = _rows2d(out, "out")
+    slopes = None
+    if alibi_slopes is not None:
+        if alibi_slopes.numel() != H or alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_contiguous():
+            raise ValueError("alibi_slopes must hold one float32 slope a head")
+        slopes = alibi_slopes.data_ptr()
     if prefix_len is not None and prefix_len.numel() != batch.n_seqs:
         raise ValueError("prefix_len must hold one length a sequence")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    with _on(k_pages, v_pages, q, out, alibi_slopes, prefix_len, batch.block_table):
-        B.attn_batch_paged(q, k_pages, v_pages, out, batch.block_table, batch.q_start, batch.kv_len, q.shape[0],
-                           batch.n_seqs, H, batch.num_kv_heads, D, kv_dim, _rows2d(q, "q"), _rows2d(out, "out"),
-                           batch.page_rows, num_pages, batch.max_blocks, scale, window, softcap, alibi_slopes,
-                           prefix_len, batch.workspace, None, stream)
+    index = k_pages.get_device()
+    workspace = batch.workspace
+    _same_device(index, v_pages, q, out, alibi_slopes, prefix_len, batch.block_table, batch.q_start, batch.kv_len,
+                 workspace)
+    _run("attn_batch_paged", B.load_library().attn_batch_paged, index, stream,
+         (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), code,
+          _int32(batch.block_table, "block_table"), _int32(batch.q_start, "q_start"), _int32(batch.kv_len, "kv_len"),
+          rows, batch.n_seqs, H, batch.num_kv_heads, D, kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks,
+          scale, window, softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel()))
     return out
