@@ -239,7 +239,7 @@ class PagedBatch:
             nbytes = B.attn_batch_paged_workspace_bytes(num_heads, num_kv_heads, head_dim)
         if nbytes == 0:
             raise ValueError("unsupported head sizes")
-        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=block_table.device)
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=block_table.device)
 
     def pool(self, k_pages, v_pages):
         """(kv_dim, num_pages) of two pools [num_pages * page_rows, kv_dim]."""

@@ -77,6 +77,7 @@ struct BatchArgs {
   unsigned* status;
   float* partial;     // [2 * blocks][rows * (D + 2)]: unnormalised output, then (max, sum) of each row
   BatchSplit* split;  // [blocks]
+  unsigned* arrived;  // [blocks] pieces seen of the item that starts in the block; zero between calls
   long long q_stride, out_stride, kv_dim;  // elements
   uint32_t total_rows;
   int n_seqs, H, G, D, gs;
@@ -89,6 +90,7 @@ constexpr int kMaxBatchSeqs = 16384;
 size_t batch_workspace_bytes(int D, int sm_count);
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s);
 int launch_batch_mma(const BatchArgs& a, int dtype, int blocks, cudaStream_t s);
+int launch_batch_decode(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_d64(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_d128(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_pair(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);

@@ -1,0 +1,498 @@
+// batch_decode.cu -- single-token attention of a batch over its pages: the
+// operation of batch_mma.cu where each sequence has about one new token, so an
+// item has at most 16 rows (the query heads of one kv head) and its time is the
+// stream of K and V.
+//
+// One block per multiprocessor: a producer warp keeps 128 KB of 64-key K/V tiles
+// in flight (TMA boxes of page parts, 128-byte swizzle) and eight warps
+// consume them, tile J by warps 4 (J & 1) .. + 3, 16 keys a warp. The 16 rows
+// fill the M of m16n8k16, whose products cost a fraction of the tile's
+// transfer time, so the whole tile's softmax runs on all lanes (on the tcgen05
+// kernel the rows would be 4 to 16 of 128 lanes). Each warp keeps its own
+// running reference, sum and output in registers: no exchange per tile. The
+// reference moves only when a score exceeds it by more than kSlack (log2
+// units), so the row maximum is not reduced over lanes on every tile.
+//
+// At a piece's end the eight states are joined in shared memory, in two steps.
+// Pieces of a split item go to the workspace; the block that arrives last (a
+// counter per item, left at zero again) joins them in key order, so one launch
+// does everything and results do not depend on the order of arrival.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <type_traits>
+
+#include "batch.h"
+#include "batch_plan.cuh"
+#include "batch_score.cuh"
+#include "batch_wait.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "mma16.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kRows = 16, kKeys = 64;
+constexpr int kItemCost = 2;  // tiles
+constexpr int kConsumers = 256, kThreads = kConsumers + 32;
+constexpr int kDescs = 4;
+constexpr int kRingBytes = 128 * 1024;
+constexpr int kMaxStages = 8;
+
+struct DecodeDesc {
+  int end, whole, n, tile0;
+  int seq, g, row0, q_len, len, pfx, first_row, rows;
+  int lo_min, lo_max, hi_min, hi_max;
+  int slot, first, last, slot0;
+};
+
+template <int D>
+struct __align__(1024) DecodeSmem {
+  static constexpr int tile_bytes = kKeys * D * 2;  // K or V
+  static constexpr int stages = kRingBytes / (2 * tile_bytes);
+  // A group waits on every use of its own stages only (a parity wait that skips a phase is no wait).
+  static_assert(stages % 2 == 0 && stages <= kMaxStages, "tile J and tile J + stages belong to one group");
+  static constexpr int q_stride = D + 8;   // elements; 16 bytes off a multiple of 128: rows start in different banks
+  static constexpr int o_stride = D + 8;   // floats
+  unsigned char ring[stages][2][tile_bytes];
+  uint16_t q[2][kRows * q_stride];
+  float o[4][kRows * o_stride];
+  float2 ml[8][kRows];  // reference and sum of each warp's rows
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t q_ready[2], q_free[2];
+  uint64_t desc_full[kDescs], desc_free[kDescs];
+  DecodeDesc desc[kDescs];
+  plan::Start start;
+  long long warp_sums[kThreads / 32];
+  int abort;
+  int go;       // there is a piece
+  int is_last;  // this block joins the item
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    batch_decode_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1,
+                        const int box_rows) {
+  using S = DecodeSmem<D>;
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr float kSlack = kHalf ? 8.f : 24.f;  // P <= 2^8 or 2^24: inside the operand type's range
+  constexpr int kChunks = D / 64, kChunkBytes = kKeys * 128;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  allow_dependent_launch();
+  if (tid == 0) {
+    for (int i = 0; i < S::stages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_ready[i], 1);
+      mbar_init(&sm.q_free[i], 8);
+    }
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(&sm.desc_full[i], 1);
+      mbar_init(&sm.desc_free[i], 8);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid == kConsumers) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  grid_dependency_wait();  // lengths, tables and pages may be the previous kernel's output
+  plan::make_plan<kRows, kKeys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
+                                          &sm.start);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
+  __syncthreads();
+  auto wait = [&](uint64_t* bar, int phase) { return wait_phase<false>(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+
+  if (warp == kConsumers / 32) {
+    // ------------------------------------------------------------ planner and producer
+    const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
+    const int parts = kKeys / box_rows;             // page parts of a tile, at most 8
+    plan::Walker<kRows, kKeys, kItemCost> walk(a, sm.start);
+    plan::Piece p;
+    int x = 0, J = 0;
+    while (true) {
+      const bool more = walk.next(p) && !*(volatile int*)&sm.abort;
+      const int first_row = p.b * kRows;
+      const int rows = more ? min(kRows, p.q.q_len * a.gs - first_row) : 0;
+      if (more && p.t1 == p.t0) {  // rows without keys
+        for (int r = 0; r < rows; ++r) {
+          const int f = first_row + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+          T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * D;
+          if (lane < D / 8) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      if (x >= kDescs) wait(&sm.desc_free[x % kDescs], x / kDescs - 1);
+      if (lane == 0) {
+        DecodeDesc& d = sm.desc[x % kDescs];
+        d.end = !more;
+        if (more) {
+          d.whole = p.whole;
+          d.n = p.t1 - p.t0;
+          d.tile0 = p.k.kt0 + p.t0;
+          d.seq = p.s;
+          d.g = p.g;
+          d.row0 = p.q.row0;
+          d.q_len = p.q.q_len;
+          d.len = p.q.len;
+          d.pfx = p.q.pfx;
+          d.first_row = first_row;
+          d.rows = rows;
+          d.lo_min = p.k.lo_min;
+          d.lo_max = p.k.lo_max;
+          d.hi_min = p.k.hi_min;
+          d.hi_max = p.k.hi_max;
+          d.slot = p.slot;
+          d.first = p.first;
+          d.last = p.last;
+          d.slot0 = p.slot0;
+        }
+        mbar_arrive(&sm.desc_full[x % kDescs]);
+      }
+      __syncwarp();
+      if (!more) break;
+      // Pool rows of the piece's page parts, 32 at a time, read at least 32 parts ahead.
+      const int n = p.t1 - p.t0, lo = p.k.lo_min, hi = p.k.hi_max, key0 = (p.k.kt0 + p.t0) * kKeys;
+      const uint32_t* table = a.block_table + (long long)p.s * a.max_blocks;
+      auto rows_of = [&](int q0) {
+        const int q = q0 + lane, key = key0 + q * box_rows;
+        if (q >= n * parts || key >= hi || key + box_rows <= lo) return outside;
+        const uint32_t pg = table[key / a.page_rows];
+        return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key % a.page_rows : -1;
+      };
+      int now = rows_of(0), next = rows_of(32);
+      // Q rows, one copy each.
+      if (x >= 2) wait(&sm.q_free[x & 1], (x >> 1) - 1);
+      if (lane == 0) mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)(rows * D * 2));
+      __syncwarp();
+      if (lane < rows) {
+        const int f = first_row + lane, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+        bulk_g2s(&sm.q[x & 1][lane * S::q_stride],
+                 static_cast<const T*>(a.q) + (long long)(p.q.row0 + t) * a.q_stride + (long long)h * D, D * 2,
+                 &sm.q_ready[x & 1]);
+      }
+      const int col = p.g * D;
+      for (int i = 0; i < n; ++i, ++J) {
+        const int q0 = i * parts;
+        if (i > 0 && q0 % 32 == 0) {
+          now = next;
+          next = rows_of(q0 + 32);
+        }
+        // Lanes 0-15 fetch the K parts, lanes 16-31 the V parts.
+        const int part = lane & 15;
+        int row = __shfl_sync(0xffffffffu, now, (q0 + part) % 32);
+        if (part >= parts) row = outside;
+        if (row < 0) {  // a page outside the pool
+          record_status(a.status, ATTN_ERR_INVALID_ARG);
+          row = outside;
+        }
+        const int key = key0 + (q0 + part) * box_rows, st = J % S::stages;
+        if (J >= S::stages) wait(&sm.empty[st], J / S::stages - 1);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(2 * S::tile_bytes));
+        __syncwarp();
+        const bool is_v = lane >= 16;
+        // V rows of a fetched part that lie outside the windows are replaced by zeros, row by row (0 * NaN).
+        const bool edge = is_v && row != outside && (key < lo || key + box_rows > hi);
+        if (part < parts && !edge) {
+          unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + part * box_rows * 128;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_2d(dst + c * kChunkBytes, is_v ? &tm_v : &tm_k, col + 64 * c, row, &sm.full[st]);
+        }
+        unsigned edges = __ballot_sync(0xffffffffu, edge);
+        while (edges) {
+          const int e = __ffs(edges) - 1;
+          edges &= edges - 1;
+          const int row_e = __shfl_sync(0xffffffffu, row, e), key_e = __shfl_sync(0xffffffffu, key, e);
+          for (int r = lane; r < box_rows; r += 32) {
+            const int y = key_e + r >= lo && key_e + r < hi ? row_e + r : outside;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_2d(sm.ring[st][1] + c * kChunkBytes + ((e - 16) * box_rows + r) * 128, &tm_v1, col + 64 * c, y,
+                          &sm.full[st]);
+          }
+        }
+      }
+      ++x;
+    }
+    // No copy may still be landing in shared memory when the block exits.
+    for (int s = 0; s < S::stages && s < J; ++s) {
+      const int last = s + ((J - 1 - s) / S::stages) * S::stages;
+      mbar_wait_bounded(&sm.full[s], (unsigned)((last / S::stages) & 1), a.status);
+    }
+    for (int y = max(0, x - 2); y < x; ++y) mbar_wait_bounded(&sm.q_ready[y & 1], (unsigned)((y >> 1) & 1), a.status);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int grp = warp >> 2, kw = 16 * (warp & 3);  // group and first key of the tile's 16
+  const int lr = lane >> 2, lc = 2 * (lane & 3);
+  int J = 0;
+  for (int x = 0;; ++x) {
+    const DecodeDesc& d = sm.desc[x % kDescs];
+    // One thread decides for all whether there is a piece: the warps meet at barriers that none may miss.  (The
+    // joining buffers are free again after this barrier, too.)
+    if (tid == 0) sm.go = wait(&sm.desc_full[x % kDescs], x / kDescs) && *(volatile int*)&sm.abort == 0 && !d.end;
+    named_barrier(1, kConsumers);
+    if (!sm.go) break;
+    const int n = d.n, rows = d.rows;
+    // This thread's rows lr and lr + 8 (past the piece's: no keys).
+    int lo[2], hi[2], pos[2];
+    float slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = lr + 8 * e, f = d.first_row + min(r, rows - 1), t = f / a.gs;
+      const plan::SeqInfo q{d.row0, d.q_len, d.len, d.pfx};
+      lo[e] = plan::row_lo(a, q, t);
+      hi[e] = r < rows ? plan::row_hi(q, t) : 0;
+      pos[e] = d.len - d.q_len + t;
+      slope[e] = a.slopes != nullptr ? -kLog2e * a.slopes[d.g * a.gs + f % a.gs] : 0.f;
+    }
+    const int lo_max = d.lo_max, hi_min = rows < kRows ? 0 : d.hi_min;
+    wait(&sm.q_ready[x & 1], x >> 1);
+    uint32_t qa[D / 16][4];
+    {
+      const uint16_t* q = sm.q[x & 1];
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          qa[c][e] = *reinterpret_cast<const uint32_t*>(q + (lr + 8 * (e & 1)) * S::q_stride + 16 * c + lc + 8 * (e >> 1));
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_free[x & 1]);
+    float o[D / 8][4];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+
+    for (int i = (J & 1) ^ grp; i < n; i += 2) {
+      const int j = J + i, st = j % S::stages;
+      wait(&sm.full[st], j / S::stages);
+      const uint32_t k_base = smem_u32(sm.ring[st][0]), v_base = smem_u32(sm.ring[st][1]);
+      float s[2][4];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[y][e] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int r = kw + (lane & 7) + 8 * (lane >> 4), u = 2 * (c & 3) + ((lane >> 3) & 1);
+        uint32_t kb[4];
+        ldsm4(kb, k_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
+        mma16816<T>(s[0], qa[c], kb[0], kb[1]);
+        mma16816<T>(s[1], qa[c], kb[2], kb[3]);
+      }
+      const int key0 = (d.tile0 + i) * kKeys + kw + lc;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[y][e] = a.softcap > 0.f ? sc.out_mul * tanh_score(s[y][e] * sc.in_mul) : s[y][e] * sc.scale2;
+      if (a.slopes != nullptr) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s[y][e] = fmaf(slope[e >> 1], fabsf((float)(pos[e >> 1] - (key0 + 8 * y + (e & 1)))), s[y][e]);
+      }
+      const int tile_key = (d.tile0 + i) * kKeys;
+      if (tile_key + kKeys > hi_min || tile_key < lo_max) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + 8 * y + (e & 1);
+            if (key >= hi[e >> 1] || key < lo[e >> 1]) s[y][e] = -INFINITY;
+          }
+      }
+      bool over = false;
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) over = over || s[y][e] > m[e >> 1] + kSlack;
+      if (__any_sync(0xffffffffu, over)) {  // some reference moves: exact maxima of the tile's 16 keys
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float t = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+          const float mn = fmaxf(m[h], t), f = mn == m[h] ? 1.f : ex2(m[h] - mn);
+          m[h] = mn;
+          l[h] *= f;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            o[c][2 * h] *= f;
+            o[c][2 * h + 1] *= f;
+          }
+        }
+      }
+      const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[y][e] = ex2(s[y][e] - sub[e >> 1]);
+          l[e >> 1] += s[y][e];
+        }
+      const uint32_t pa[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]), pack2<T>(s[1][0], s[1][1]),
+                              pack2<T>(s[1][2], s[1][3])};
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const int r = kw + (lane & 15), u = 2 * (c & 3) + (lane >> 4);
+        uint32_t vb[4];
+        ldsm4_t(vb, v_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
+        mma16816<T>(o[2 * c], pa, vb[0], vb[1]);
+        mma16816<T>(o[2 * c + 1], pa, vb[2], vb[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
+    }
+    J += n;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    }
+
+    // Join of the eight warps: warps 4-7 hand over to 0-3, then four states are summed by all threads.
+    auto put = [&](int w) {
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(&sm.o[w][(lr + 8 * h) * S::o_stride + 8 * c + lc]) =
+              make_float2(o[c][2 * h], o[c][2 * h + 1]);
+      if ((lane & 3) == 0) {
+        sm.ml[w][lr] = make_float2(m[0], l[0]);
+        sm.ml[w][lr + 8] = make_float2(m[1], l[1]);
+      }
+    };
+    if (warp >= 4) put(warp - 4);
+    named_barrier(1, kConsumers);
+    if (warp < 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 other = sm.ml[warp][lr + 8 * h];
+        const float mn = fmaxf(m[h], other.x);
+        const float f0 = l[h] == 0.f ? 0.f : ex2(m[h] - mn), f1 = other.y == 0.f ? 0.f : ex2(other.x - mn);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const float2 v = *reinterpret_cast<const float2*>(&sm.o[warp][(lr + 8 * h) * S::o_stride + 8 * c + lc]);
+          o[c][2 * h] = o[c][2 * h] * f0 + v.x * f1;
+          o[c][2 * h + 1] = o[c][2 * h + 1] * f0 + v.y * f1;
+        }
+        l[h] = l[h] * f0 + other.y * f1;
+        m[h] = mn;
+      }
+      __syncwarp();
+      put(warp);
+    }
+    named_barrier(1, kConsumers);
+    constexpr int kPerRow = D / 8;  // threads of a row, eight columns each
+    const int r = tid / kPerRow, c0 = 8 * (tid % kPerRow);
+    const bool mine = tid < kRows * kPerRow && r < rows;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, m_all = -INFINITY, l_all = 0.f;
+    // Adds state (m, l, eight columns) to the thread's.
+    auto add = [&](float2 ml, float4 v0, float4 v1) {
+      if (ml.y == 0.f) return;  // none of the row's keys
+      const float mn = fmaxf(m_all, ml.x);
+      const float f0 = l_all == 0.f ? 0.f : ex2(m_all - mn), f1 = ex2(ml.x - mn);
+      const float w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = acc[k] * f0 + w[k] * f1;
+      l_all = l_all * f0 + ml.y * f1;
+      m_all = mn;
+    };
+    auto store = [&]() {
+      const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+      const int f = d.first_row + r, t = f / a.gs, h = d.g * a.gs + f % a.gs;
+      T* dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D + c0;
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = l_all == 0.f ? 0u : pack2<T>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    if (mine) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4* v = reinterpret_cast<const float4*>(&sm.o[w][r * S::o_stride + c0]);
+        add(sm.ml[w][r], v[0], v[1]);
+      }
+    }
+    if (d.whole) {
+      if (mine) store();
+    } else {
+      constexpr long long kSlotFloats = kRows * (D + 2);
+      float* part = a.partial + (2ll * blockIdx.x + d.slot) * kSlotFloats;
+      if (mine) {
+        *reinterpret_cast<float4*>(part + r * D + c0) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4*>(part + r * D + c0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (c0 == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m_all, l_all);
+      }
+      __threadfence();
+      named_barrier(1, kConsumers);
+      if (tid == 0) {
+        const unsigned seen = atomicAdd(&a.arrived[d.first], 1u);
+        sm.is_last = seen == (unsigned)(d.last - d.first);
+        if (sm.is_last) a.arrived[d.first] = 0u;  // for the next call
+        __threadfence();
+      }
+      named_barrier(1, kConsumers);
+      if (sm.is_last && mine) {
+        m_all = -INFINITY;
+        l_all = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+        for (int c = d.first; c <= d.last; ++c) {
+          const float* q = a.partial + (2ll * c + (c == d.first ? d.slot0 : 0)) * kSlotFloats;
+          const float4* v = reinterpret_cast<const float4*>(q + r * D + c0);
+          add(__ldcg(reinterpret_cast<const float2*>(q + kRows * D + 2 * r)), __ldcg(v), __ldcg(v + 1));
+        }
+        store();
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+  }
+}
+
+template <typename T, int D>
+int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
+  if (box_rows > kKeys) box_rows = kKeys;
+  const uint64_t dims[2] = {(uint64_t)a.kv_dim, (uint64_t)a.num_pages * a.page_rows};
+  const uint64_t strides[1] = {(uint64_t)a.kv_dim * 2};
+  const uint32_t box[2] = {64, (uint32_t)box_rows}, one_row[2] = {64, 1};
+  CUtensorMap tm_k, tm_v, tm_v1;  // 16-bit elements are only moved: one element type serves both
+  if (!make_tmap(&tm_k, a.k_pages, 2, dims, strides, box, true, kSwizzle128) ||
+      !make_tmap(&tm_v, a.v_pages, 2, dims, strides, box, true, kSwizzle128) ||
+      !make_tmap(&tm_v1, a.v_pages, 2, dims, strides, one_row, true, kSwizzle128))
+    return ATTN_ERR_CUDA;
+  const void* kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D>);
+  const size_t smem = sizeof(DecodeSmem<D>) + 1024;
+  if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
+  BatchArgs aa = a;
+  ScoreMap sc = score_map(a);
+  void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &box_rows};
+  return launch_pdl(kern, dim3(blocks), dim3(kThreads), smem, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_batch_decode(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s) {
+  if (dtype == ATTN_DT_BF16)
+    return a.D == 64 ? launch_decode_t<__nv_bfloat16, 64>(a, blocks, box_rows, s)
+                     : launch_decode_t<__nv_bfloat16, 128>(a, blocks, box_rows, s);
+  return a.D == 64 ? launch_decode_t<__half, 64>(a, blocks, box_rows, s)
+                   : launch_decode_t<__half, 128>(a, blocks, box_rows, s);
+}
+
+}  // namespace attn

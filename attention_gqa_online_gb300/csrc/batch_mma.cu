@@ -20,56 +20,13 @@
 #include "batch_score.cuh"
 #include "common.cuh"
 #include "internal.h"
-#include "rotary.cuh"
+#include "mma16.cuh"
 
 namespace attn {
 namespace {
 
 constexpr int kRows = 64, kKeys = 64, kThreads = 128, kStages = 2;
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-template <typename T>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
+constexpr int kItemCost = 2;  // tiles
 
 // A tile is rows of DP 16-bit elements; 16-byte unit u of row r sits at unit
 // u ^ (r & 7), so ldmatrix reads eight rows without bank conflicts.
@@ -92,9 +49,9 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
   __shared__ plan::Start start;
   __shared__ long long warp_sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  plan::make_plan<kRows, kKeys, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
+  plan::make_plan<kRows, kKeys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
   BatchSplit split{};
-  plan::Walker<kRows, kKeys> walk(a, start);
+  plan::Walker<kRows, kKeys, kItemCost> walk(a, start);
   plan::Piece p;
   const uint32_t q_base = smem_u32(sh.q);
   constexpr int kUnits = DP / 8;
@@ -334,26 +291,29 @@ int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, int rows, cu
                                : launch_combine_t<__half>(a, blocks, rows, s);
 }
 
-// Partial slots (two a thread block, 128 rows a multiprocessor either way) and
-// the split records.
+// Arrival counters, split records, and partial slots (two a thread block; at most 128 rows a multiprocessor).
 size_t batch_workspace_bytes(int D, int sm_count) {
-  return (size_t)2 * sm_count * 128 * (D + 2) * sizeof(float) + (size_t)2 * sm_count * sizeof(BatchSplit);
+  return (size_t)2 * sm_count * 128 * (D + 2) * sizeof(float) + (size_t)2 * sm_count * sizeof(BatchSplit) +
+         (size_t)(sm_count + 7) / 8 * 8 * sizeof(unsigned);
 }
 
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s) {
-  a.split = static_cast<BatchSplit*>(workspace);
+  a.arrived = static_cast<unsigned*>(workspace);
+  a.split = reinterpret_cast<BatchSplit*>(a.arrived + (sm_count + 7) / 8 * 8);
   a.partial = reinterpret_cast<float*>(a.split + 2 * sm_count);
   // The tensor-core kernel moves pages by TMA boxes of the largest power of
   // two of rows that divides a page, whole 8-row groups of the swizzle.
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
-  const bool pair = a.D == 128 && box >= 8 && 128 % a.gs == 0 && sm_count % 2 == 0 &&
+  const bool tma = (a.D == 64 || a.D == 128) && box >= 8;
+  if (tma && a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
+  const bool pair = tma && a.D == 128 && 128 % a.gs == 0 && sm_count % 2 == 0 &&
                     (long long)a.total_rows * a.gs >= 256ll * a.n_seqs;
   if (pair) {
     const int rc = launch_batch_tc_pair(a, dtype, sm_count, box, s);
     return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, sm_count / 2, 256, s);
   }
-  if ((a.D == 64 || a.D == 128) && box >= 8) {
+  if (tma) {
     const int rc = a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s)
                              : launch_batch_tc_d128(a, dtype, sm_count, box, s);
     return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, sm_count, 128, s);

@@ -4,8 +4,8 @@
 // The query rows of sequence s and kv head g are flattened as r = t * gs + j
 // (token t, head g * gs + j) and cut into blocks of ROWS; an item is one
 // (sequence, row block, kv head).  Its keys are the union of its rows'
-// windows, walked in tiles of KEYS.  Every item weighs its tiles plus kItemCost
-// (Q load, epilogue); the weights of all items, laid end to end in (sequence,
+// windows, walked in tiles of KEYS.  Every item weighs its tiles plus COST (what
+// its Q load, epilogue and masked tiles take, in tiles); the weights of all items, laid end to end in (sequence,
 // row block, kv head) order, are cut into equal ranges, one per thread block.  A
 // range boundary inside an item splits its keys: each part is a piece, whose
 // unnormalised output and (max, sum) go to a partial slot, and a second kernel
@@ -21,8 +21,6 @@
 
 namespace attn {
 namespace plan {
-
-constexpr int kItemCost = 3;  // tiles
 
 struct SeqInfo {
   int row0;   // first row of the token batch
@@ -82,6 +80,9 @@ struct Piece {
   int t0, t1;     // tiles [t0, t1) of the item's nt
   int slot;       // partial slot of a piece that is not the whole item
   bool whole;
+  // The item's pieces, when there are several: blocks first .. last, the first one's in slot slot0, the others in
+  // slot 0.
+  int first, last, slot0;
 };
 
 // What a block needs to walk its range; written by make_plan.
@@ -120,7 +121,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 // The range of thread block `c` of `blocks`.  Every thread of the block calls it;
 // first_block holds n_seqs + 1 ints and warp_sums THREADS/32 values in shared
 // memory.  On return (after its final barrier) *start is valid.
-template <int ROWS, int KEYS, int THREADS>
+template <int ROWS, int KEYS, int COST, int THREADS>
 __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_block, long long* warp_sums, Start* start) {
   const int tid = threadIdx.x;
   // Row blocks before each sequence.
@@ -165,19 +166,19 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
     for (int i = i0; i < i1; ++i) {
       while (first_block[ss + 1] <= i) ++ss;
       if (have != ss) q = load_seq(a, have = ss);
-      mine += (long long)(block_keys<ROWS, KEYS>(a, q, i - first_block[ss]).nt + kItemCost) * a.G;
+      mine += (long long)(block_keys<ROWS, KEYS>(a, q, i - first_block[ss]).nt + COST) * a.G;
     }
   }
   long long units;
   const long long upto = block_scan<THREADS>(mine, warp_sums, &units);
-  const long long per = max((units + blocks - 1) / blocks, (long long)(kItemCost + 1));
+  const long long per = max((units + blocks - 1) / blocks, (long long)(COST + 1));
   const long long u0 = per * c;
   long long at = upto - mine;
   if (u0 >= at && u0 < upto) {  // this thread's share holds the range's start
     int ss = s;
     for (int i = i0; i < i1; ++i) {
       while (first_block[ss + 1] <= i) ++ss;
-      const int w = block_keys<ROWS, KEYS>(a, load_seq(a, ss), i - first_block[ss]).nt + kItemCost;
+      const int w = block_keys<ROWS, KEYS>(a, load_seq(a, ss), i - first_block[ss]).nt + COST;
       if (u0 < at + (long long)w * a.G) {
         start->g = (int)((u0 - at) / w);
         start->x = (u0 - at) % w;
@@ -196,7 +197,7 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
 
 // Walks the pieces of a block's range, in order.  Warps of different roles
 // walk it independently and see the same pieces.
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int COST>
 struct Walker {
   const BatchArgs& a;
   SeqInfo q;
@@ -216,25 +217,30 @@ struct Walker {
   __device__ __forceinline__ bool next(Piece& p, BatchSplit* split = nullptr) {
     while (left > 0) {
       const BlockKeys k = block_keys<ROWS, KEYS>(a, q, b);
-      const long long w = k.nt + kItemCost;
+      const long long w = k.nt + COST;
       const long long take = min(left, w - x);
       p.q = q;
       p.k = k;
       p.s = s;
       p.b = b;
       p.g = g;
-      p.t0 = (int)max(0ll, x - kItemCost);
-      p.t1 = (int)max(0ll, x + take - kItemCost);
+      p.t0 = (int)max(0ll, x - COST);
+      p.t1 = (int)max(0ll, x + take - COST);
       p.slot = index == 0 ? 0 : 1;
       p.whole = p.t0 == 0 && p.t1 == k.nt;
       const bool have = p.t1 > p.t0 || (k.nt == 0 && x == 0);
+      if (!p.whole && have) {
+        p.first = (int)((u - x + COST) / per);  // the block that holds tile 0
+        p.last = (int)((u - x + w - 1) / per);
+        p.slot0 = p.first * per >= u - x ? 0 : 1;  // is the item the first of its first block's range?
+      }
       if (split != nullptr && p.t0 == 0 && p.t1 > 0 && p.t1 < k.nt) {
         split->valid = 1;
         split->seq = s;
         split->blk = b;
         split->g = g;
-        split->slot0 = p.slot;
-        split->last = (int)((u + w - x - 1) / per);
+        split->slot0 = p.slot0;
+        split->last = p.last;
       }
       ++index;
       x += take;

@@ -53,6 +53,7 @@
 #include "batch.h"
 #include "batch_plan.cuh"
 #include "batch_score.cuh"
+#include "batch_wait.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -61,6 +62,9 @@ namespace attn {
 namespace {
 
 constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384;
+// What a piece takes beyond its tiles, in tiles: prompt of 8192 (pieces of 1 to 64 tiles) 815, 690, 649, 657 us at 1,
+// 2, 3, 4.
+constexpr int kItemCost = 3;
 constexpr int kDescs = 4;        // piece descriptors in flight
 constexpr int kChain = 4;        // reference maxima in flight
 constexpr int kPColumn = 256, kOColumn = 384;
@@ -162,38 +166,6 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
                  : "memory");
   else
     mbar_arrive(bar);
-}
-// Waits for phase `parity` of `bar`, within kWaitLimitNs (as mbar_wait_bounded).
-// The thread suspends in try_wait itself: the form with a time hint becomes a
-// polling loop with sleeps, whose wake-ups come late (SYNCS and NANOSLEEP were
-// a tenth of all instructions).  REMOTE: the other block's threads arrive.
-template <bool REMOTE>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag) {
-  unsigned long long t0 = 0;
-  for (unsigned n = 0;; ++n) {
-    unsigned ok;
-    if (REMOTE)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity)
-          : "memory");
-    else
-      ok = mbar_try_wait(bar, parity);
-    if (ok) return true;
-    if (n % 16 == 15) {
-      if (*abort_flag != 0) return false;
-      const unsigned long long now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) {
-        record_status(status, ATTN_ERR_TIMEOUT);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-  }
 }
 // Tensor copies into this block's shared memory that complete on `bar` (a
 // barrier of the first block, by its cluster address, when PAIR).
@@ -345,7 +317,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) tmem_alloc_all<PAIR>(&sm.tmem_base);
   // Lengths, tables and pages may be the previous kernel's output.
   grid_dependency_wait();
-  plan::make_plan<L::rows, kTcKeys, kTcThreads>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
+  plan::make_plan<L::rows, kTcKeys, kItemCost, kTcThreads>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
   // The plan's scratch is where Q and the K/V tiles land.
   fence_async_smem();
   tc::fence_before_sync();
@@ -416,7 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (q_box) prefetch_tmap(&tm_q);
       }
       BatchSplit split{};
-      plan::Walker<L::rows, kTcKeys> walk(a, sm.start);
+      plan::Walker<L::rows, kTcKeys, kItemCost> walk(a, sm.start);
       plan::Piece p;
       int x = 0, J = 0;
       while (true) {

@@ -289,3 +289,51 @@ def test_many_rows_repeat_bits(cuda_lib):
     first = cuda_lib.attend_paged(obj, b.q, b.k, b.v)
     for _ in range(20):
         assert torch.equal(first, cuda_lib.attend_paged(obj, b.q, b.k, b.v))
+
+
+DECODE_KV = [1, 2, 63, 64, 65, 127, 128, 129, 300, 1000, 4097, 9000]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kw", [
+    dict(), dict(window=1), dict(window=65), dict(window=1000), dict(softcap=2.0), dict(softcap=50.0, window=3000),
+    dict(slopes=True), dict(slopes=True, softcap=20.0), dict(prefix=True, window=100), dict(scale=-0.05), dict(scale=0.0)])
+def test_single_tokens_with_masks_and_maps(cuda_lib, kw, D):
+    kw = dict(kw)
+    b = Batch([1] * len(DECODE_KV), DECODE_KV, 12, 2, D, 16, F16 if D == 64 else BF16, seed=31)
+    if kw.get("slopes"):
+        kw["slopes"] = 2.0 ** (-0.7 * torch.arange(1, 13, device="cuda", dtype=torch.float32))
+    if kw.get("prefix"):
+        kw["prefix"] = [1, 1, 63, 5, 65, 100, 0, 129, 150, 1000, 4000, 2]
+    elif kw.get("window"):
+        for i, n in enumerate(b.kv):
+            gone = max(0, n - kw["window"])
+            if gone:
+                sl = b.slots(i, 0, gone)
+                b.k[sl] = CUT
+                b.v[sl] = CUT
+    check(cuda_lib, b, str(kw), **kw)
+
+
+@pytest.mark.parametrize("page_rows", [8, 16, 24, 64, 100, 128, 256])
+@pytest.mark.parametrize("H,G,D", [(8, 8, 128), (32, 2, 64), (15, 3, 128)])
+def test_single_tokens_page_sizes(cuda_lib, H, G, D, page_rows):
+    check(cuda_lib, Batch([1, 0, 1, 1], [700, 5, 41, 2500], H, G, D, page_rows, BF16, seed=page_rows), "pages")
+
+
+@pytest.mark.parametrize("H,G,D,kv", [(32, 8, 128, [16384]), (8, 1, 128, [40000, 3, 700]), (16, 2, 64, [20000] * 5),
+                                      (32, 8, 128, [3000] * 40)])
+def test_single_tokens_repeat_bits_and_share_a_workspace(cuda_lib, H, G, D, kv):
+    """Fifty calls give the same bits, also between calls of other sizes on the same workspace."""
+    A = cuda_lib
+    b = Batch([1] * len(kv), kv, H, G, D, 64, BF16, seed=33)
+    other = Batch([300, 20], [5000, 20], H, G, D, 64, BF16, seed=34)
+    obj, obj2 = b.object(A), other.object(A)
+    obj2.workspace = obj.workspace
+    first = check(A, b, "first").clone()
+    second = A.attend_paged(obj2, other.q, other.k, other.v)
+    for i in range(50):
+        assert torch.equal(first, A.attend_paged(obj, b.q, b.k, b.v))
+        if i % 10 == 0:
+            assert torch.equal(second, A.attend_paged(obj2, other.q, other.k, other.v))
+    assert A.attn_get_status() == 0
