@@ -3,9 +3,9 @@
 // item has at most 16 rows (the query heads of one kv head) and its time is the
 // stream of K and V.
 //
-// One block per multiprocessor: a producer warp keeps 128 KB of 64-key K/V tiles
-// in flight (TMA boxes of page parts, 128-byte swizzle) and eight warps
-// consume them, tile J by warps 4 (J & 1) .. + 3, 16 keys a warp. The 16 rows
+// One block per multiprocessor: four producer warps keep 128 KB of 64-key K/V
+// tiles in flight (TMA boxes of page parts, 128-byte swizzle; a warp issues
+// one in about 100 cycles, so small pages need several) and eight warps consume them, tile J by warps 4 (J & 1) .. + 3, 16 keys a warp. The 16 rows
 // fill the M of m16n8k16, whose products cost a fraction of the tile's
 // transfer time, so the whole tile's softmax runs on all lanes (on the tcgen05
 // kernel the rows would be 4 to 16 of 128 lanes). Each warp keeps its own
@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kRows = 16, kKeys = 64;
 constexpr int kItemCost = 2;  // tiles
-constexpr int kConsumers = 256, kThreads = kConsumers + 32;
+constexpr int kConsumers = 256, kThreads = kConsumers + 128;
 constexpr int kDescs = 4;
 constexpr int kRingBytes = 128 * 1024;
 constexpr int kMaxStages = 8;
@@ -94,15 +94,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(&sm.desc_full[i], 1);
-      mbar_init(&sm.desc_free[i], 8);
+      mbar_init(&sm.desc_free[i], 11);  // eight consumers, three producers
     }
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (tid == kConsumers) {
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
-  }
+  if (tid == kConsumers) prefetch_tmap(&tm_k);
   grid_dependency_wait();  // lengths, tables and pages may be the previous kernel's output
   plan::make_plan<kRows, kKeys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
                                           &sm.start);
@@ -110,13 +107,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   auto wait = [&](uint64_t* bar, int phase) { return wait_phase<false>(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
 
-  if (warp == kConsumers / 32) {
-    // ------------------------------------------------------------ planner and producer
+  if (warp >= kConsumers / 32) {
+    // ------------------------------------------------------------ producers
+    // Warps 0, 1 fetch K and 2, 3 fetch V: at D = 128 a column chunk each, at D = 64 every other part.  Warp 0 is also
+    // the planner and loads Q.
+    const int pw = warp - kConsumers / 32, sub = pw & 1;
+    const bool is_v = pw >= 2;
+    const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
     const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
     const int parts = kKeys / box_rows;             // page parts of a tile, at most 8
+    const int chunk = D == 128 ? sub : 0;
+    const bool my_part = lane < parts && (D == 128 || (lane & 1) == sub);
+    // Tiles of one piece, from tile number J on.
+    auto load_tiles = [&](int n, int seq, int g, int lo, int hi, int tile0, int J) {
+      const int key0 = tile0 * kKeys, col = g * D + 64 * chunk;
+      const uint32_t* table = a.block_table + (long long)seq * a.max_blocks;
+      // Pool rows of the page parts, 32 at a time (one a lane), read at least 32 parts ahead.
+      auto rows_of = [&](int q0) {
+        const int q = q0 + lane, key = key0 + q * box_rows;
+        if (q >= n * parts || key >= hi || key + box_rows <= lo) return outside;
+        const uint32_t pg = table[key / a.page_rows];
+        return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key % a.page_rows : -1;
+      };
+      int now = rows_of(0), next = n * parts > 32 ? rows_of(32) : outside;
+      for (int i = 0; i < n; ++i, ++J) {
+        const int q0 = i * parts;
+        if (i > 0 && q0 % 32 == 0) {
+          now = next;
+          next = rows_of(q0 + 32);
+        }
+        int row = __shfl_sync(0xffffffffu, now, (q0 + lane) % 32);
+        if (!my_part) row = outside;
+        if (row < 0) {  // a page outside the pool
+          record_status(a.status, ATTN_ERR_INVALID_ARG);
+          row = outside;
+        }
+        const int key = key0 + (q0 + lane) * box_rows, st = J % S::stages;
+        if (J >= S::stages) wait(&sm.empty[st], J / S::stages - 1);
+        if (pw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(2 * S::tile_bytes));
+        __syncwarp();
+        unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + chunk * kChunkBytes;
+        // V rows of a fetched part that lie outside the windows are replaced by zeros, row by row (0 * NaN).
+        const bool edge = is_v && row != outside && (key < lo || key + box_rows > hi);
+        if (my_part && !edge) tma_load_2d(dst + lane * box_rows * 128, tm, col, row, &sm.full[st]);
+        unsigned edges = __ballot_sync(0xffffffffu, edge);
+        while (edges) {
+          const int e = __ffs(edges) - 1;
+          edges &= edges - 1;
+          const int row_e = __shfl_sync(0xffffffffu, row, e), key_e = __shfl_sync(0xffffffffu, key, e);
+          for (int r = lane; r < box_rows; r += 32) {
+            const int y = key_e + r >= lo && key_e + r < hi ? row_e + r : outside;
+            tma_load_2d(dst + (e * box_rows + r) * 128, &tm_v1, col, y, &sm.full[st]);
+          }
+        }
+      }
+      return J;
+    };
+    int x = 0, J = 0;
+    if (pw != 0) {
+      if (lane == 0) {
+        prefetch_tmap(tm);
+        if (is_v) prefetch_tmap(&tm_v1);
+      }
+      for (;; ++x) {
+        const bool ok = wait(&sm.desc_full[x % kDescs], x / kDescs);
+        const DecodeDesc& d = sm.desc[x % kDescs];
+        if (!__all_sync(0xffffffffu, ok && *(volatile int*)&sm.abort == 0) || d.end) return;
+        J = load_tiles(d.n, d.seq, d.g, d.lo_min, d.hi_max, d.tile0, J);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+      }
+    }
     plan::Walker<kRows, kKeys, kItemCost> walk(a, sm.start);
     plan::Piece p;
-    int x = 0, J = 0;
     while (true) {
       const bool more = walk.next(p) && !*(volatile int*)&sm.abort;
       const int first_row = p.b * kRows;
@@ -158,16 +221,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (!more) break;
-      // Pool rows of the piece's page parts, 32 at a time, read at least 32 parts ahead.
-      const int n = p.t1 - p.t0, lo = p.k.lo_min, hi = p.k.hi_max, key0 = (p.k.kt0 + p.t0) * kKeys;
-      const uint32_t* table = a.block_table + (long long)p.s * a.max_blocks;
-      auto rows_of = [&](int q0) {
-        const int q = q0 + lane, key = key0 + q * box_rows;
-        if (q >= n * parts || key >= hi || key + box_rows <= lo) return outside;
-        const uint32_t pg = table[key / a.page_rows];
-        return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key % a.page_rows : -1;
-      };
-      int now = rows_of(0), next = rows_of(32);
       // Q rows, one copy each.
       if (x >= 2) wait(&sm.q_free[x & 1], (x >> 1) - 1);
       if (lane == 0) mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)(rows * D * 2));
@@ -178,48 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  static_cast<const T*>(a.q) + (long long)(p.q.row0 + t) * a.q_stride + (long long)h * D, D * 2,
                  &sm.q_ready[x & 1]);
       }
-      const int col = p.g * D;
-      for (int i = 0; i < n; ++i, ++J) {
-        const int q0 = i * parts;
-        if (i > 0 && q0 % 32 == 0) {
-          now = next;
-          next = rows_of(q0 + 32);
-        }
-        // Lanes 0-15 fetch the K parts, lanes 16-31 the V parts.
-        const int part = lane & 15;
-        int row = __shfl_sync(0xffffffffu, now, (q0 + part) % 32);
-        if (part >= parts) row = outside;
-        if (row < 0) {  // a page outside the pool
-          record_status(a.status, ATTN_ERR_INVALID_ARG);
-          row = outside;
-        }
-        const int key = key0 + (q0 + part) * box_rows, st = J % S::stages;
-        if (J >= S::stages) wait(&sm.empty[st], J / S::stages - 1);
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(2 * S::tile_bytes));
-        __syncwarp();
-        const bool is_v = lane >= 16;
-        // V rows of a fetched part that lie outside the windows are replaced by zeros, row by row (0 * NaN).
-        const bool edge = is_v && row != outside && (key < lo || key + box_rows > hi);
-        if (part < parts && !edge) {
-          unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + part * box_rows * 128;
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_2d(dst + c * kChunkBytes, is_v ? &tm_v : &tm_k, col + 64 * c, row, &sm.full[st]);
-        }
-        unsigned edges = __ballot_sync(0xffffffffu, edge);
-        while (edges) {
-          const int e = __ffs(edges) - 1;
-          edges &= edges - 1;
-          const int row_e = __shfl_sync(0xffffffffu, row, e), key_e = __shfl_sync(0xffffffffu, key, e);
-          for (int r = lane; r < box_rows; r += 32) {
-            const int y = key_e + r >= lo && key_e + r < hi ? row_e + r : outside;
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_2d(sm.ring[st][1] + c * kChunkBytes + ((e - 16) * box_rows + r) * 128, &tm_v1, col + 64 * c, y,
-                          &sm.full[st]);
-          }
-        }
-      }
+      J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.lo_min, p.k.hi_max, p.k.kt0 + p.t0, J);
       ++x;
     }
     // No copy may still be landing in shared memory when the block exits.
@@ -278,19 +290,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = J + i, st = j % S::stages;
       wait(&sm.full[st], j / S::stages);
       const uint32_t k_base = smem_u32(sm.ring[st][0]), v_base = smem_u32(sm.ring[st][1]);
-      float s[2][4];
+      // Even and odd column steps accumulate apart: the chain of dependent products is half as long.
+      float s[2][4], s1[2][4];
 #pragma unroll
       for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[y][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[y][e] = s1[y][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
         const int r = kw + (lane & 7) + 8 * (lane >> 4), u = 2 * (c & 3) + ((lane >> 3) & 1);
         uint32_t kb[4];
         ldsm4(kb, k_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
-        mma16816<T>(s[0], qa[c], kb[0], kb[1]);
-        mma16816<T>(s[1], qa[c], kb[2], kb[3]);
+        mma16816<T>(c % 2 ? s1[0] : s[0], qa[c], kb[0], kb[1]);
+        mma16816<T>(c % 2 ? s1[1] : s[1], qa[c], kb[2], kb[3]);
       }
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[y][e] += s1[y][e];
       const int key0 = (d.tile0 + i) * kKeys + kw + lc;
 #pragma unroll
       for (int y = 0; y < 2; ++y)
@@ -438,13 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4*>(part + r * D + c0 + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
         if (c0 == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(m_all, l_all);
       }
-      __threadfence();
       named_barrier(1, kConsumers);
       if (tid == 0) {
-        const unsigned seen = atomicAdd(&a.arrived[d.first], 1u);
+        // Releases the block's part (its writes are ordered before by the barrier) and acquires the others'.
+        unsigned seen;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.arrived + d.first) : "memory");
         sm.is_last = seen == (unsigned)(d.last - d.first);
         if (sm.is_last) a.arrived[d.first] = 0u;  // for the next call
-        __threadfence();
       }
       named_barrier(1, kConsumers);
       if (sm.is_last && mine) {

@@ -73,6 +73,12 @@ __device__ __forceinline__ BlockKeys block_keys(const BatchArgs& a, const SeqInf
   return k;
 }
 
+// 64-bit quotient; unit counts nearly always fit in 32 bits, where a division takes a quarter of the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 struct Piece {
   SeqInfo q;
   BlockKeys k;
@@ -118,12 +124,83 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
   return v + before;
 }
 
+// Range of block c when the items weigh `units` in all.
+template <int COST>
+__device__ __forceinline__ long long units_per_block(long long units, int blocks) {
+  return max(quotient(units + blocks - 1, blocks), (long long)(COST + 1));
+}
+__device__ __forceinline__ void set_start(Start* start, int s, int b, long long offset, int w, long long u0, long long per,
+                                          long long units) {
+  start->g = (int)quotient(offset, w);
+  start->x = offset - (long long)start->g * w;
+  start->s = s;
+  start->b = b;
+  start->u0 = u0;
+  start->per = per;
+  start->left = min(per, units - u0);
+}
+
+// The plan by one warp, for batches of at most kWarpSeqs sequences with few
+// row blocks each (a lane takes consecutive sequences): no block barriers, so a
+// single-token step starts about a microsecond sooner.  Returns false (to every
+// lane) when the batch is too large for it.
+constexpr int kWarpSeqs = 512, kWarpBlocks = 32;
+template <int ROWS, int KEYS, int COST>
+__device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks, Start* start) {
+  const int lane = threadIdx.x & 31;
+  if (a.n_seqs > kWarpSeqs) return false;
+  const int share = (a.n_seqs + 31) / 32;
+  const int s0 = min(a.n_seqs, lane * share), s1 = min(a.n_seqs, s0 + share);
+  int nb = 0;
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    const SeqInfo q = load_seq(a, s);
+    const int n = row_blocks<ROWS>(a, q);
+    nb += n;
+    if (nb <= kWarpBlocks)
+      for (int b = 0; b < n; ++b) mine += block_keys<ROWS, KEYS>(a, q, b).nt + COST;
+  }
+  if (__any_sync(0xffffffffu, nb > kWarpBlocks)) return false;
+  mine *= a.G;
+  long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += o;
+  }
+  const long long units = __shfl_sync(0xffffffffu, upto, 31);
+  const long long per = units_per_block<COST>(units, blocks), u0 = per * c;
+  if (lane == 0 && u0 >= units) start->left = 0;
+  long long at = upto - mine;
+  if (u0 >= at && u0 < upto) {
+    bool found = false;
+    for (int s = s0; s < s1 && !found; ++s) {
+      const SeqInfo q = load_seq(a, s);
+      const int n = row_blocks<ROWS>(a, q);
+      for (int b = 0; b < n && !found; ++b) {
+        const int w = block_keys<ROWS, KEYS>(a, q, b).nt + COST;
+        found = u0 < at + (long long)w * a.G;
+        if (found) set_start(start, s, b, u0 - at, w, u0, per, units);
+        at += (long long)w * a.G;
+      }
+    }
+  }
+  return true;
+}
+
 // The range of thread block `c` of `blocks`.  Every thread of the block calls it;
 // first_block holds n_seqs + 1 ints and warp_sums THREADS/32 values in shared
 // memory.  On return (after its final barrier) *start is valid.
 template <int ROWS, int KEYS, int COST, int THREADS>
 __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_block, long long* warp_sums, Start* start) {
   const int tid = threadIdx.x;
+  if (tid < 32) {
+    const bool done = warp_plan<ROWS, KEYS, COST>(a, c, blocks, start);
+    if (tid == 0) first_block[0] = done ? 1 : 0;
+  }
+  __syncthreads();
+  if (first_block[0]) return;
+  __syncthreads();
   // Row blocks before each sequence.
   long long carry = 0;
   for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
@@ -138,9 +215,6 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
   if (tid == 0) {
     first_block[a.n_seqs] = n_blk;
     start->left = 0;
-    start->x = start->u0 = 0;
-    start->per = 1;
-    start->s = start->b = start->g = 0;
   }
   __syncthreads();
   // Weights of this thread's share of the row blocks (all kv heads of each).
@@ -171,8 +245,7 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
   }
   long long units;
   const long long upto = block_scan<THREADS>(mine, warp_sums, &units);
-  const long long per = max((units + blocks - 1) / blocks, (long long)(COST + 1));
-  const long long u0 = per * c;
+  const long long per = units_per_block<COST>(units, blocks), u0 = per * c;
   long long at = upto - mine;
   if (u0 >= at && u0 < upto) {  // this thread's share holds the range's start
     int ss = s;
@@ -180,13 +253,7 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
       while (first_block[ss + 1] <= i) ++ss;
       const int w = block_keys<ROWS, KEYS>(a, load_seq(a, ss), i - first_block[ss]).nt + COST;
       if (u0 < at + (long long)w * a.G) {
-        start->g = (int)((u0 - at) / w);
-        start->x = (u0 - at) % w;
-        start->s = ss;
-        start->b = i - first_block[ss];
-        start->u0 = u0;
-        start->per = per;
-        start->left = min(per, units - u0);
+        set_start(start, ss, i - first_block[ss], u0 - at, w, u0, per, units);
         break;
       }
       at += (long long)w * a.G;
@@ -230,9 +297,9 @@ struct Walker {
       p.whole = p.t0 == 0 && p.t1 == k.nt;
       const bool have = p.t1 > p.t0 || (k.nt == 0 && x == 0);
       if (!p.whole && have) {
-        p.first = (int)((u - x + COST) / per);  // the block that holds tile 0
-        p.last = (int)((u - x + w - 1) / per);
-        p.slot0 = p.first * per >= u - x ? 0 : 1;  // is the item the first of its first block's range?
+        p.first = (int)quotient(u - x + COST, per);  // the block that holds tile 0
+        p.last = (int)quotient(u - x + w - 1, per);
+        p.slot0 = (long long)p.first * per >= u - x ? 0 : 1;  // is the item the first of its first block's range?
       }
       if (split != nullptr && p.t0 == 0 && p.t1 > 0 && p.t1 < k.nt) {
         split->valid = 1;
