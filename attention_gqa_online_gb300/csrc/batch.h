@@ -77,7 +77,7 @@ struct BatchArgs {
   unsigned* status;
   float* partial;     // [2 * blocks][rows * (D + 2)]: unnormalised output, then (max, sum) of each row
   BatchSplit* split;  // [blocks]
-  unsigned* arrived;  // [blocks] pieces seen of the item that starts in the block; zero between calls
+  unsigned* arrived;  // pieces seen of the item that starts in a block (four a multiprocessor); zero between calls
   long long q_stride, out_stride, kv_dim;  // elements
   uint32_t total_rows;
   int n_seqs, H, G, D, gs;
@@ -94,6 +94,5 @@ int launch_batch_decode(const BatchArgs& a, int dtype, int blocks, int box_rows,
 int launch_batch_tc_d64(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_d128(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_pair(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
-int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, int rows, cudaStream_t s);
 
 }  // namespace attn

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           &sm.start);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
   __syncthreads();
-  auto wait = [&](uint64_t* bar, int phase) { return wait_phase<false>(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
 
   if (warp >= kConsumers / 32) {
     // ------------------------------------------------------------ producers
@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           row = outside;
         }
         const int key = key0 + (q0 + lane) * box_rows, st = J % S::stages;
-        if (J >= S::stages) wait(&sm.empty[st], J / S::stages - 1);
+        // A wait that ran out ends the role: a slot in use must not be written, nor a phase arrived at twice.
+        if (J >= S::stages && !__all_sync(0xffffffffu, wait(&sm.empty[st], J / S::stages - 1))) return J;
         if (pw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(2 * S::tile_bytes));
         __syncwarp();
         unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + chunk * kChunkBytes;
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (x >= kDescs) wait(&sm.desc_free[x % kDescs], x / kDescs - 1);
+      if (x >= kDescs && !__all_sync(0xffffffffu, wait(&sm.desc_free[x % kDescs], x / kDescs - 1))) break;
       if (lane == 0) {
         DecodeDesc& d = sm.desc[x % kDescs];
         d.end = !more;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (!more) break;
       // Q rows, one copy each.
-      if (x >= 2) wait(&sm.q_free[x & 1], (x >> 1) - 1);
+      if (x >= 2 && !__all_sync(0xffffffffu, wait(&sm.q_free[x & 1], (x >> 1) - 1))) break;
       if (lane == 0) mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)(rows * D * 2));
       __syncwarp();
       if (lane < rows) {
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.lo_min, p.k.hi_max, p.k.kt0 + p.t0, J);
       ++x;
+      if (*(volatile int*)&sm.abort) break;
     }
     // No copy may still be landing in shared memory when the block exits.
     for (int s = 0; s < S::stages && s < J; ++s) {

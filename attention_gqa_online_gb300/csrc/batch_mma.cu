@@ -223,15 +223,15 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
 // 2^(m_i - m) l_i, pieces in key order.  Grid (blocks of the attention grid,
 // row groups); a block without a split item leaves at once.
 constexpr int kJoinThreads = 128;
-template <typename T, int ROWS>
+template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) batch_combine_kernel(const BatchArgs a) {
   grid_dependency_wait();
   const BatchSplit sp = a.split[blockIdx.x];
   if (!sp.valid) return;
   const plan::SeqInfo q = plan::load_seq(a, sp.seq);
-  const int rows = min(ROWS, q.q_len * a.gs - sp.blk * ROWS);
+  const int rows = min(kRows, q.q_len * a.gs - sp.blk * kRows);
   const int tpr = a.D / 4;  // threads per row, four columns each
-  const long long slot_floats = (long long)ROWS * (a.D + 2);
+  const long long slot_floats = (long long)kRows * (a.D + 2);
   const int per = kJoinThreads / tpr;
   const int sub = threadIdx.x / tpr, col = 4 * (threadIdx.x % tpr);
   if (sub >= per) return;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kJoinThreads) batch_combine_kernel(const Batch
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = blockIdx.x; c <= sp.last; ++c) {
       const float* part = c == (int)blockIdx.x ? first : a.partial + 2ll * c * slot_floats;
-      const float2 ml = *reinterpret_cast<const float2*>(part + (long long)ROWS * a.D + 2 * r);
+      const float2 ml = *reinterpret_cast<const float2*>(part + (long long)kRows * a.D + 2 * r);
       const float4 v = *reinterpret_cast<const float4*>(part + (long long)r * a.D + col);
       if (ml.y == 0.f) continue;  // the piece holds none of the row's keys
       const float mn = fmaxf(m, ml.x);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kJoinThreads) batch_combine_kernel(const Batch
       m = mn;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int f = sp.blk * ROWS + r, t = f / a.gs, h = sp.g * a.gs + f % a.gs;
+    const int f = sp.blk * kRows + r, t = f / a.gs, h = sp.g * a.gs + f % a.gs;
     T* dst = static_cast<T*>(a.out) + (long long)(q.row0 + t) * a.out_stride + (long long)h * a.D + col;
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
   }
@@ -269,13 +269,13 @@ int launch_mma_t(const BatchArgs& a, int blocks, cudaStream_t s) {
 }
 
 template <typename T>
-int launch_combine_t(const BatchArgs& a, int blocks, int rows, cudaStream_t s) {
+int launch_combine_t(const BatchArgs& a, int blocks, cudaStream_t s) {
   BatchArgs b = a;
   void* args[] = {&b};
-  const void* kern = rows == 64    ? reinterpret_cast<const void*>(batch_combine_kernel<T, 64>)
-                     : rows == 128 ? reinterpret_cast<const void*>(batch_combine_kernel<T, 128>)
-                                   : reinterpret_cast<const void*>(batch_combine_kernel<T, 256>);
-  return launch_pdl(kern, dim3(blocks, rows / 16), dim3(kJoinThreads), 0, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_pdl(reinterpret_cast<const void*>(batch_combine_kernel<T>), dim3(blocks, 4), dim3(kJoinThreads), 0, s,
+                    args) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -286,20 +286,19 @@ int launch_batch_mma(const BatchArgs& a, int dtype, int blocks, cudaStream_t s) 
   return a.D <= 64 ? launch_mma_t<__half, 64>(a, blocks, s) : launch_mma_t<__half, 128>(a, blocks, s);
 }
 
-int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, int rows, cudaStream_t s) {
-  return dtype == ATTN_DT_BF16 ? launch_combine_t<__nv_bfloat16>(a, blocks, rows, s)
-                               : launch_combine_t<__half>(a, blocks, rows, s);
+static int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, cudaStream_t s) {
+  return dtype == ATTN_DT_BF16 ? launch_combine_t<__nv_bfloat16>(a, blocks, s) : launch_combine_t<__half>(a, blocks, s);
 }
 
 // Arrival counters, split records, and partial slots (two a thread block; at most 128 rows a multiprocessor).
 size_t batch_workspace_bytes(int D, int sm_count) {
   return (size_t)2 * sm_count * 128 * (D + 2) * sizeof(float) + (size_t)2 * sm_count * sizeof(BatchSplit) +
-         (size_t)(sm_count + 7) / 8 * 8 * sizeof(unsigned);
+         (size_t)4 * ((sm_count + 7) / 8 * 8) * sizeof(unsigned);
 }
 
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s) {
   a.arrived = static_cast<unsigned*>(workspace);
-  a.split = reinterpret_cast<BatchSplit*>(a.arrived + (sm_count + 7) / 8 * 8);
+  a.split = reinterpret_cast<BatchSplit*>(a.arrived + 4 * ((sm_count + 7) / 8 * 8));
   a.partial = reinterpret_cast<float*>(a.split + 2 * sm_count);
   // The tensor-core kernel moves pages by TMA boxes of the largest power of
   // two of rows that divides a page, whole 8-row groups of the swizzle.
@@ -309,17 +308,11 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   if (tma && a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
   const bool pair = tma && a.D == 128 && 128 % a.gs == 0 && sm_count % 2 == 0 &&
                     (long long)a.total_rows * a.gs >= 256ll * a.n_seqs;
-  if (pair) {
-    const int rc = launch_batch_tc_pair(a, dtype, sm_count, box, s);
-    return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, sm_count / 2, 256, s);
-  }
-  if (tma) {
-    const int rc = a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s)
-                             : launch_batch_tc_d128(a, dtype, sm_count, box, s);
-    return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, sm_count, 128, s);
-  }
+  if (pair) return launch_batch_tc_pair(a, dtype, sm_count, box, s);
+  if (tma)
+    return a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s) : launch_batch_tc_d128(a, dtype, sm_count, box, s);
   const int rc = launch_batch_mma(a, dtype, 2 * sm_count, s);
-  return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, 2 * sm_count, kRows, s);
+  return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, 2 * sm_count, s);
 }
 
 }  // namespace attn

@@ -8,7 +8,7 @@
 // one piece are in the softmax, the next piece's Q block, K tiles and first
 // scores are already being made.
 //
-// Warp roles (384 threads; three warpgroups, so registers can be split):
+// Warp roles (512 threads; four warpgroups, so registers can be split):
 //   warp 0      planner and K producer: walks the pieces, writes their descriptors
 //               into a four-deep ring, loads each piece's Q block (two buffers) and
 //               its K tiles, one TMA box per page part and 64-column chunk (lane l takes
@@ -20,6 +20,7 @@
 //   warps 4-7,
 //   warps 8-11  softmax groups 0 and 1: tile J (counted over all pieces of
 //               the block) belongs to group J & 1; a thread owns a whole row
+//   warps 12-15 output: O to memory at a piece's end, joins of split items
 // Tensor memory (512 columns): S_b [128 b, +128), P_b [256 + 64 b, +64), b = J & 1,
 // O [384, +D).
 //
@@ -30,11 +31,10 @@
 // type of V (bf16 <= 2^24, fp16 <= 2^8; both operands of an MMA share a type):
 // an error of half a step per weight, linear in the output.
 //
-// End of a piece.  The group that owns the last tile reads its half of O's
-// columns as soon as P V lands; the other group first does the next piece's first
-// tile, so the exponentials continue.  The next piece's first P V waits for
-// both reads.  A whole item is normalised and stored in the output's type, a split
-// one goes to its partial slot in fp32.
+// End of a piece.  The output warps read O as soon as the last P V lands, and
+// the next piece's first P V waits for that read only; the softmax groups go
+// straight on to the next piece.  (With the groups reading O themselves a piece
+// cost about five tiles' time more.)
 //
 // Rows of V that lie in a fetched page part but outside the block's windows
 // hold whatever the page holds (0 * NaN would reach every row): such parts are
@@ -61,16 +61,16 @@
 namespace attn {
 namespace {
 
-constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 384;
+constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 512;
 // What a piece takes beyond its tiles, in tiles: prompt of 8192 (pieces of 1 to 64 tiles) 815, 690, 649, 657 us at 1,
 // 2, 3, 4.
-constexpr int kItemCost = 3;
+constexpr int kItemCost = 2;
 constexpr int kDescs = 4;        // piece descriptors in flight
 constexpr int kChain = 4;        // reference maxima in flight
 constexpr int kPColumn = 256, kOColumn = 384;
 constexpr int kMaxSlots = 4;     // K (and V) tiles in flight, at most
-// Registers: 128 threads * 104 + 256 * 200 = 384 * 168, the block's allocation at launch.
-constexpr int kCtrlRegs = 104, kSoftmaxRegs = 200;
+// Registers: 128 threads * (72 + 72) + 256 * 184 = 512 * 128, the block's allocation at launch.
+constexpr int kCtrlRegs = 72, kOutRegs = 72, kSoftmaxRegs = 184;
 
 // A piece as the roles see it.
 struct PieceDesc {
@@ -81,6 +81,7 @@ struct PieceDesc {
   int first_row;   // first flattened row of this block
   int rows;        // valid rows from there on, at most 128
   int lo_min, lo_max, hi_min, hi_max;
+  int first, last, slot0;  // the item's pieces (plan::Piece)
   int tile_last, n;  // key tiles tile_last, tile_last - 1, ... (n of them) of the sequence
   int pos_min;       // position of the block's first row
 };
@@ -113,11 +114,12 @@ struct __align__(1024) TcSmem {
   uint64_t desc_full[kDescs], desc_free[kDescs];
   uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];
   uint64_t chain_bar[4][kChain];  // [row quarter][J & 3]
-  uint64_t stat_bar[4][2][2];     // [row quarter][piece & 1][group]
-  uint64_t o_free;                // both groups have read O
+  uint64_t stat_bar[4][kDescs][2];  // [row quarter][piece % kDescs][group]
+  uint64_t o_ready;               // the piece's last P V has completed
+  uint64_t o_free;                // O has been read
   uint64_t drain[2];
   float chain[kChain][kTcRows];
-  float2 stat[2][2][kTcRows];  // [piece & 1][group][row]: reference, sum
+  float2 stat[kDescs][2][kTcRows];  // [piece % kDescs][group][row]: reference, sum
   int4 row[256];               // each softmax thread's own row: window [x, y), position z, slope w (as float bits)
   PieceDesc desc[kDescs];
   plan::Start start;
@@ -157,8 +159,9 @@ __device__ __forceinline__ void pair_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // Arrives on a barrier of the first block.  These barriers hand over tensor
-// memory only, which tcgen05's own fences order, so the arrival needs no
-// cluster-scope release (which would wait for every store of the thread).
+// memory only, which tcgen05's own fences order, so neither the arrival needs a
+// cluster-scope release (it would wait for every store of the thread) nor the
+// wait a cluster-scope acquire (it would invalidate L1).
 template <bool PAIR>
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   if (PAIR)
@@ -300,14 +303,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (lane < kDescs) {
       mbar_init(&sm.desc_full[lane], 1);
-      mbar_init(&sm.desc_free[lane], rank == 0 ? 10 : 9);  // producer, (first block) P V and eight softmax warps
+      mbar_init(&sm.desc_free[lane], rank == 0 ? 14 : 13);  // V, (first block) P V, eight softmax and four output warps
     }
-    if (lane < 16) {
-      mbar_init(&sm.chain_bar[lane >> 2][lane & 3], 1);
-      mbar_init(&sm.stat_bar[lane >> 2][(lane >> 1) & 1][lane & 1], 1);
-    }
+    if (lane < 16) mbar_init(&sm.chain_bar[lane >> 2][lane & 3], 1);
+    mbar_init(&sm.stat_bar[lane >> 3][(lane >> 1) & 3][lane & 1], 1);
     if (lane == 31) {
-      mbar_init(&sm.o_free, PAIR ? 16 : 8);
+      mbar_init(&sm.o_ready, 1);
+      mbar_init(&sm.o_free, PAIR ? 8 : 4);
       mbar_init(&sm.drain[0], 1);
       mbar_init(&sm.drain[1], 1);
       sm.abort = 0;
@@ -327,8 +329,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
-  auto wait = [&](uint64_t* bar, int phase) { return wait_phase<false>(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  // The lanes of a warp may leave a wait at different times.  Before one lane arrives somewhere for the warp all must
+  // have left it (a warp-wide instruction or __syncwarp between): else the barrier could complete its next phase and
+  // leave the others waiting for a phase that is past.
+  auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
   // Descriptor of piece x (its slot stays valid until every role has released it).
+  // After a wait that ran out (sm.abort) its content means nothing: the roles leave.
   auto piece = [&](int x) -> const PieceDesc& {
     wait(&sm.desc_full[x % kDescs], x / kDescs);
     return sm.desc[x % kDescs];
@@ -372,6 +378,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return row;
     };
+    auto all_ok = [&](bool lane_ok) { return __all_sync(0xffffffffu, lane_ok) != 0; };
     auto barrier_of = [&](uint64_t* full) { return PAIR ? in_leader(smem_u32(full)) : smem_u32(full); };
     // No copy may still be landing in shared memory when the block exits (a pair's copies all complete on the first
     // block's barriers, and the pair leaves together).
@@ -387,12 +394,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tmap(&tm_k);
         if (q_box) prefetch_tmap(&tm_q);
       }
-      BatchSplit split{};
       plan::Walker<L::rows, kTcKeys, kItemCost> walk(a, sm.start);
       plan::Piece p;
       int x = 0, J = 0;
-      while (true) {
-        const bool more = walk.next(p, &split) && !*(volatile int*)&sm.abort;
+      // A wait that ran out ends the role at once: writing over a descriptor or a slot in use, or arriving twice in one
+      // phase, would turn a late block into a fault.
+      bool ok = true;
+      while (ok) {
+        const bool more = walk.next(p) && !*(volatile int*)&sm.abort;
         // This block's rows: 128 flattened rows from first_row on.
         const int first_row = p.b * L::rows + rank * kTcRows;
         const int rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
@@ -404,7 +413,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           continue;
         }
-        if (x >= kDescs) wait(&sm.desc_free[x % kDescs], x / kDescs - 1);
+        if (x >= kDescs) ok = all_ok(wait(&sm.desc_free[x % kDescs], x / kDescs - 1));
+        if (!ok) break;
         if (lane == 0) {
           PieceDesc& d = sm.desc[x % kDescs];
           d.end = !more;
@@ -413,6 +423,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             d.seq = p.s;
             d.g = p.g;
             d.slot = p.slot;
+            d.first = p.first;
+            d.last = p.last;
+            d.slot0 = p.slot0;
             d.row0 = p.q.row0;
             d.q_len = p.q.q_len;
             d.len = p.q.len;
@@ -437,7 +450,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                              (p.k.kt0 + p.t1 - 1) * kTcKeys + (PAIR ? rank * L::k_rows : 0), p.s);
         // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
         // only feeds itself, and those rows are not stored).
-        if (x >= 2) wait(&sm.q_free[x & 1], (x >> 1) - 1);
+        if (x >= 2) ok = all_ok(wait(&sm.q_free[x & 1], (x >> 1) - 1));
+        if (!ok) break;
         if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
           if (lane == 0) {
             uint64_t* full = &sm.q_ready[x & 1];
@@ -465,7 +479,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < n; ++i, ++J) {
           const int row = part_row(w, i), slot = J % L::slots;
-          if (J >= L::slots) wait(&sm.k_empty[slot], J / L::slots - 1);
+          if (J >= L::slots) ok = all_ok(wait(&sm.k_empty[slot], J / L::slots - 1));
+          if (!ok) break;
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
           __syncwarp();
           if (lane < w.parts) {
@@ -477,7 +492,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         ++x;
       }
-      if (rank == 0 && lane == 0) a.split[unit] = split;
       drain_copies(sm.k_full, J);
       for (int y = max(0, x - 2); rank == 0 && (PAIR || q_box) && y < x; ++y)
         mbar_wait_bounded(&sm.q_ready[y & 1], (unsigned)((y >> 1) & 1), a.status);
@@ -488,14 +502,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tmap(&tm_v1);
       }
       int J = 0;
-      for (int x = 0; !*(volatile int*)&sm.abort; ++x) {
+      bool ok = true;
+      for (int x = 0; ok; ++x) {
         const PieceDesc& d = piece(x);
         if (d.end || *(volatile int*)&sm.abort) break;
         const int n = d.n, col = d.g * D + (PAIR ? rank * 64 * L::v_chunks : 0);
         Parts w = open_parts(kTcKeys, n, d.lo_min, d.hi_max, d.tile_last * kTcKeys, d.seq);
         for (int i = 0; i < n; ++i, ++J) {
           const int row = part_row(w, i), key = w.key0 - i * kTcKeys + lane * box_rows, slot = J % L::slots;
-          if (J >= L::slots) wait(&sm.v_empty[slot], J / L::slots - 1);
+          if (J >= L::slots) ok = all_ok(wait(&sm.v_empty[slot], J / L::slots - 1));
+          if (!ok) break;
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.v_full[slot], (unsigned)(PAIR ? 2 : 1) * L::v_bytes);
           __syncwarp();
           const uint32_t bar = barrier_of(&sm.v_full[slot]);
@@ -528,7 +544,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // Two warps, one a product, so that neither holds up the other; warp-uniform loops, one elected lane issues.
       constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
       auto wait_all = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, wait_phase<PAIR>(bar, (unsigned)(phase & 1), a.status, &sm.abort));
+        return __all_sync(0xffffffffu, wait(bar, phase));
       };
       if (rank != 0) {
       } else if (warp == 1) {
@@ -567,7 +583,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const PieceDesc& d = piece(x);
           if (d.end || *(volatile int*)&sm.abort) break;
           const int n = d.n;
-          // The first product of a piece replaces O: both groups have read the last one.
+          // The first product of a piece replaces O.
           if (x > 0) ok = wait_all(&sm.o_free, x - 1);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
@@ -583,6 +599,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             commit_all<PAIR>(&sm.pv_done[b]);
             commit_all<PAIR>(&sm.v_empty[slot]);
           }
+          commit_all<PAIR>(&sm.o_ready);
           if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
         }
       }
@@ -591,94 +608,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_wait_bounded(&sm.drain[warp - 1], 0, a.status);
       }
     }
-  } else {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ softmax groups
     regs_inc<kSoftmaxRegs>();
     const int grp = (warp - 4) >> 2, qd = warp & 3;
     const int r = 32 * qd + lane;  // row == TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
     const uint32_t o_col = tmem + lane_base + kOColumn;
-    constexpr int kHalfD = D / 2;
-
-    // Reads this group's half of O of piece x, whose last tile is jl, and stores it.
-    auto epilogue = [&](int x, int jl) {
-      const PieceDesc& d = sm.desc[x % kDescs];
+    int J = 0;
+    for (int x = 0;; ++x) {
+      const PieceDesc& d = piece(x);
+      if (d.end || *(volatile int*)&sm.abort) break;
+      const int n = d.n;
       const bool busy = 32 * qd < d.rows;
-      float inv = 0.f, m_fin = -INFINITY, l_row = 0.f;
-      // A parity wait needs the phase before it to be over: for the other group's tile jl that follows from P V
-      // of this group's tile jl - 1 (products complete in order).
-      if (jl > 0 && (jl & 1) != grp) wait(&sm.pv_done[(jl - 1) & 1], (jl - 1) >> 1);
-      wait(&sm.pv_done[jl & 1], jl >> 1);
-      tc::fence_after_sync();
-      T* dst = nullptr;
-      float* part = nullptr;
-      if (busy) {
-        wait(&sm.stat_bar[qd][x & 1][grp ^ 1], x >> 1);
-        const float2 s0 = sm.stat[x & 1][0][r], s1 = sm.stat[x & 1][1][r];
-        m_fin = fmaxf(s0.x, s1.x);
-        if (s0.y != 0.f) l_row += s0.y * ex2(s0.x - m_fin);
-        if (s1.y != 0.f) l_row += s1.y * ex2(s1.x - m_fin);
-        inv = l_row == 0.f ? 0.f : 1.f / l_row;
-        if (d.whole) {
-          const int f = d.first_row + r, t = f / a.gs, h = d.g * a.gs + f % a.gs;
-          dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D + grp * kHalfD;
-        } else {
-          const int pr = rank * kTcRows + r;  // row of the item
-          part = a.partial + (long long)(2 * unit + d.slot) * L::rows * (D + 2);
-          if (grp == 0 && r < d.rows) *reinterpret_cast<float2*>(part + L::rows * D + 2 * pr) = make_float2(m_fin, l_row);
-          part += pr * D + grp * kHalfD;
-        }
-      }
-      const bool store = r < d.rows;
-#pragma unroll
-      for (int c = 0; c < kHalfD / 32; ++c) {  // 32 columns at a time; O is free after the last read
-        uint32_t o[32];
-        if (busy) {
-          tc::tmem_ld32(o_col + grp * kHalfD + 32 * c, o);
-          tc::tmem_ld_wait();
-          tc::reg_fence(o);
-        }
-        if (c == kHalfD / 32 - 1) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) arrive_leader<PAIR>(&sm.o_free);
-        }
-        if (store && dst != nullptr) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = l_row == 0.f
-                         ? 0u
-                         : pack_pair<T>(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-            *reinterpret_cast<uint4*>(dst + 32 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (store) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(part + 32 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
-    };
-
-    // One pass of this loop is at most one own tile and one epilogue.  pend: the
-    // piece whose epilogue waits for this group's next tile (its last tile is J - 1).
-    int x = -1, J = 0, n = 0, i = 0, pend = -1;
-    bool busy = false, done = false;
-    float m_ref = -INFINITY, l = 0.f;
-    auto open_piece = [&]() {  // the next piece's row data
-      const PieceDesc& d = piece(++x);
-      done = d.end || *(volatile int*)&sm.abort;
-      n = done ? 0 : d.n;
-      i = (J & 1) ^ grp;
-      busy = !done && 32 * qd < d.rows;
-      m_ref = -INFINITY;
-      l = 0.f;
+      float m_ref = -INFINITY, l = 0.f;
       int4 info = make_int4(0, 0, 0, 0);
-      if (!done && r < d.rows) {
+      if (r < d.rows) {
         const int f = d.first_row + r, t = f / a.gs;
         const plan::SeqInfo q{d.row0, d.q_len, d.len, d.pfx};
         info.x = plan::row_lo(a, q, t);
@@ -687,17 +632,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (MODE != 0 && a.slopes != nullptr) info.w = __float_as_int(-kLog2e * a.slopes[d.g * a.gs + f % a.gs]);
       }
       sm.row[128 * grp + r] = info;  // read on the tiles that need it: kept in registers it would spill scores
-    };
-    open_piece();
-    while (!done || pend >= 0) {
-      if (i < n) {
-        const PieceDesc& d = sm.desc[x % kDescs];
+      for (int i = (J & 1) ^ grp; i < n; i += 2) {
         const int j = J + i, b = j & 1;
+        const int key0 = (d.tile_last - i) * kTcKeys;
+        // Does the tile cross some row's window end, or start?
+        const bool cut_hi = key0 + kTcKeys > d.hi_min, cut_lo = key0 < d.lo_max;
         wait(&sm.s_full[b], j >> 1);
         tc::fence_after_sync();
         if (!busy) {
           // No valid row in this warp: only keep the barriers going (P_b of tile j - 2 must have been read
           // before this tile's arrival).
+          if (j > 0) wait(&sm.chain_bar[qd][(j - 1) % kChain], (j - 1) / kChain);
+          __syncwarp();
           if (lane == 0) {
             arrive_leader<PAIR>(&sm.s_free[b]);
             mbar_arrive(&sm.chain_bar[qd][j % kChain]);
@@ -717,7 +663,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_leader<PAIR>(&sm.s_free[b]);
 
-          const int key0 = (d.tile_last - i) * kTcKeys;
           if (MODE == 1 && a.slopes == nullptr) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -764,18 +709,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (MODE != 0 && a.slopes != nullptr) {
-            // slope = -slopes[h] log2 e.  Behind the row, |p - j| = p - j and the bias is linear in the column.
+            // slope = -slopes[h] log2 e.  In a tile wholly behind (or ahead of) the rows |p - j| is linear in the column;
+            // in one that crosses them, slope |d| is slope d with the sign of slope.
             const int4 info = sm.row[128 * grp + r];
-            const float slope = __int_as_float(info.w);
-            const float mul = MODE == 1 ? sc.scale2 : 1.f, dist = (float)(key0 - info.z);
-            if (a.prefix_len == nullptr || key0 + kTcKeys - 1 <= d.pos_min) {
-              const float first = -slope * dist;
+            const float slope = __int_as_float(info.w), mul = MODE == 1 ? sc.scale2 : 1.f;
+            const bool behind = a.prefix_len == nullptr || key0 + kTcKeys - 1 <= d.pos_min;
+            const float step = behind ? -slope : slope, first = step * (float)(key0 - info.z);
+            if (behind || key0 >= d.pos_min + (kTcRows - 1) / a.gs + 1) {
 #pragma unroll
               for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                   float x0 = __uint_as_float(s[c][e]), x1 = __uint_as_float(s[c][e + 1]);
-                  float b0 = -slope, b1 = -slope;
+                  float b0 = step, b1 = step;
                   fma2(b0, b1, (float)(32 * c + e), (float)(32 * c + e + 1), first, first);
                   fma2(x0, x1, mul, mul, b0, b1);
                   s[c][e] = __float_as_uint(x0);
@@ -785,12 +731,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  s[c][e] = __float_as_uint(
-                      fmaf(slope, fabsf(dist + (float)(32 * c + e)), __uint_as_float(s[c][e]) * mul));
+                for (int e = 0; e < 32; e += 2) {
+                  float x0 = __uint_as_float(s[c][e]), x1 = __uint_as_float(s[c][e + 1]);
+                  float b0 = step, b1 = step;
+                  fma2(b0, b1, (float)(32 * c + e), (float)(32 * c + e + 1), first, first);
+                  b0 = copysignf(b0, slope);
+                  b1 = copysignf(b1, slope);
+                  fma2(x0, x1, mul, mul, b0, b1);
+                  s[c][e] = __float_as_uint(x0);
+                  s[c][e + 1] = __float_as_uint(x1);
+                }
             }
           }
-          if (key0 + kTcKeys > d.hi_min) {  // the tile crosses some row's window end
+          if (cut_hi) {
             const int lim = sm.row[128 * grp + r].y - key0;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -798,7 +751,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int e = 0; e < 32; ++e)
                 if (32 * c + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
           }
-          if (key0 < d.lo_max) {  // ... or some row's window start
+          if (cut_lo) {
             const int lim = sm.row[128 * grp + r].x - key0;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -817,42 +770,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float tmax = cf * max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
 
           // The reference of the tile before (left by the other group), then this tile's.
+          // (The first tile of a piece, and warps without rows, wait too, for nothing but order: a group must not get
+          // two tiles ahead of the other one's wait on the same slot of the ring.)
           float m_prev = -INFINITY;
-          if (i > 0) {
-            wait(&sm.chain_bar[qd][(j - 1) % kChain], (j - 1) / kChain);
-            m_prev = sm.chain[(j - 1) % kChain][r];
-          }
+          if (j > 0) wait(&sm.chain_bar[qd][(j - 1) % kChain], (j - 1) / kChain);
+          if (i > 0) m_prev = sm.chain[(j - 1) % kChain][r];
           const float m_new = (tmax > m_prev + kRescale) ? tmax : m_prev;  // also for the first finite maximum
           sm.chain[j % kChain][r] = m_new;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.chain_bar[qd][j % kChain]);
           const float neg_m = (m_new == -INFINITY) ? 0.f : -m_new;
 
-          // Sixteen scores at a time: exponents, then exponentials, then sums and packing, so that the long-latency
-          // exponentials of a batch are in flight together.
+          // Exponentials run kLag scores ahead of their sum and packing (in place: packed pair k of a chunk replaces
+          // its score k, long done), so the special-function unit, 4 cycles an instruction, is never waited for.
+          constexpr int kLag = 16;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float e[16];
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                e[k] = __uint_as_float(s[c][16 * h + k]);
-                e[k + 1] = __uint_as_float(s[c][16 * h + k + 1]);
-                if (MODE == 0)
-                  fma2(e[k], e[k + 1], cf, cf, neg_m, neg_m);
-                else
-                  add2(e[k], e[k + 1], neg_m, neg_m);
-              }
-#pragma unroll
-              for (int k = 0; k < 16; ++k) e[k] = ex2(e[k]);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                add2(sum[k & 2], sum[(k & 2) + 1], e[k], e[k + 1]);
-                s[c][8 * h + (k >> 1)] = pack_pair<T>(e[k], e[k + 1]);
-              }
+          for (int e = 0; e < 128 + kLag; e += 2) {
+            if (e < 128) {
+              float x0 = __uint_as_float(s[e >> 5][e & 31]), x1 = __uint_as_float(s[e >> 5][(e & 31) + 1]);
+              if (MODE == 0)
+                fma2(x0, x1, cf, cf, neg_m, neg_m);
+              else
+                add2(x0, x1, neg_m, neg_m);
+              s[e >> 5][e & 31] = __float_as_uint(ex2(x0));
+              s[e >> 5][(e & 31) + 1] = __float_as_uint(ex2(x1));
             }
+            if (e >= kLag) {
+              const int k = e - kLag;
+              const float p0 = __uint_as_float(s[k >> 5][k & 31]), p1 = __uint_as_float(s[k >> 5][(k & 31) + 1]);
+              add2(sum[k & 2], sum[(k & 2) + 1], p0, p1);
+              s[k >> 5][(k & 31) >> 1] = pack_pair<T>(p0, p1);
+            }
+          }
           // P_b was last read by P V of tile j - 2.
           if (j >= 2) {
             wait(&sm.pv_done[b], (j - 2) >> 1);
@@ -886,24 +836,132 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
           if (lane == 0) arrive_leader<PAIR>(&sm.p_ready[b]);
         }
-        i += 2;
       }
-      int ep = -1;
-      if (pend >= 0) {  // the first tile of this piece is done; O still holds the last piece
-        ep = pend;
-        pend = -1;
-      } else if (i >= n) {
-        sm.stat[x & 1][grp][r] = make_float2(m_ref, l);
+      sm.stat[x % kDescs][grp][r] = make_float2(m_ref, l);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.stat_bar[qd][x % kDescs][grp]);
+        mbar_arrive(&sm.desc_free[x % kDescs]);
+      }
+      J += n;
+    }
+  } else {
+    // ------------------------------------------------------------ output warps
+    // O of each piece as soon as its last product lands: whole items leave normalised in the output's type, pieces of
+    // a split one in fp32 to the workspace, where the warp that arrives last joins its 32 rows in key order.
+    regs_dec<kOutRegs>();
+    const int qd = warp & 3, r = 32 * qd + lane;
+    const uint32_t o_col = tmem + ((uint32_t)(32 * qd) << 16) + kOColumn;
+    constexpr int kCols = 16, kChunks = D / kCols;  // columns at a time: few registers
+    for (int x = 0;; ++x) {
+      const PieceDesc& d = piece(x);
+      if (d.end || *(volatile int*)&sm.abort) break;
+      const bool busy = 32 * qd < d.rows, store = r < d.rows;
+      wait(&sm.stat_bar[qd][x % kDescs][0], x / kDescs);
+      wait(&sm.stat_bar[qd][x % kDescs][1], x / kDescs);
+      const float2 s0 = sm.stat[x % kDescs][0][r], s1 = sm.stat[x % kDescs][1][r];
+      const float m_fin = fmaxf(s0.x, s1.x);
+      float l_row = 0.f;
+      if (s0.y != 0.f) l_row += s0.y * ex2(s0.x - m_fin);
+      if (s1.y != 0.f) l_row += s1.y * ex2(s1.x - m_fin);
+      const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
+      T* dst = nullptr;
+      if (busy) {
+        const int f = d.first_row + min(r, d.rows - 1), t = f / a.gs, h = d.g * a.gs + (f - t * a.gs);
+        dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D;
+      }
+      const bool whole = d.whole;
+      const int pr = rank * kTcRows + r;  // row of the item
+      constexpr long long kSlotFloats = (long long)L::rows * (D + 2);
+      float* part = a.partial + (2ll * unit + d.slot) * kSlotFloats + pr * D;
+      auto put = [&](const float (&v)[kCols], int c, float mul, bool empty) {  // columns of the row, rounded
+#pragma unroll
+        for (int e = 0; e < kCols; e += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = empty ? 0u : pack_pair<T>(v[e + 2 * k] * mul, v[e + 2 * k + 1] * mul);
+          *reinterpret_cast<uint4*>(dst + kCols * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      };
+      wait(&sm.o_ready, x);
+      tc::fence_after_sync();
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t o[32];
+        if (busy) {
+          tc::tmem_ld16(o_col + kCols * c, o);
+          tc::tmem_ld_wait();
+          tc::reg_fence16(o);
+        }
+        if (c == kChunks - 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive_leader<PAIR>(&sm.o_free);
+        }
+        if (store) {
+          if (whole) {
+            float v[kCols];
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) v[e] = __uint_as_float(o[e]);
+            put(v, c, inv, l_row == 0.f);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kCols; e += 4)
+              *reinterpret_cast<uint4*>(part + kCols * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      }
+      if (!whole && busy) {
+        const int first = d.first, last = d.last, slot0 = d.slot0;
+        const long long ml_off = (long long)L::rows * D + 2 * pr - (long long)pr * D;
+        if (store) *reinterpret_cast<float2*>(part + ml_off) = make_float2(m_fin, l_row);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.stat_bar[qd][x & 1][grp]);
-        J += n;
-        if (((J - 1) & 1) == grp)
-          ep = x;
-        else
-          pend = x;
-        open_piece();
+        unsigned seen = 0;
+        unsigned* counter = a.arrived + ((PAIR ? 2 * first + rank : first) * 4 + qd);
+        if (lane == 0)  // releases this warp's rows, acquires the other pieces'
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(counter) : "memory");
+        seen = __shfl_sync(0xffffffffu, seen, 0);
+        if (seen == (unsigned)(last - first)) {
+          if (lane == 0) *counter = 0u;  // for the next call
+          if (store) {
+            const float* row0 = a.partial + (2ll * first + slot0) * kSlotFloats + pr * D;
+            const float* row1 = a.partial + 2ll * first * kSlotFloats + pr * D;  // block c > first: + 2 (c - first) slots
+            float m_all = -INFINITY, l_all = 0.f;
+            for (int c = first; c <= last; ++c) {
+              const float* q = c == first ? row0 : row1 + 2ll * (c - first) * kSlotFloats;
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
+              if (ml.y == 0.f) continue;  // none of the row's keys
+              const float mn = fmaxf(m_all, ml.x);
+              l_all = (l_all == 0.f ? 0.f : l_all * ex2(m_all - mn)) + ml.y * ex2(ml.x - mn);
+              m_all = mn;
+            }
+            const float inv_all = l_all == 0.f ? 0.f : 1.f / l_all;
+#pragma unroll 1
+            for (int k = 0; k < kChunks; ++k) {
+              float acc[kCols];
+#pragma unroll
+              for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+              for (int c = first; c <= last; ++c) {
+                const float* q = c == first ? row0 : row1 + 2ll * (c - first) * kSlotFloats;
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
+                if (ml.y == 0.f) continue;
+                const float f = ex2(ml.x - m_all);
+#pragma unroll
+                for (int e = 0; e < kCols; e += 4) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(q + kCols * k + e));
+                  acc[e] = fmaf(v.x, f, acc[e]);
+                  acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
+                  acc[e + 2] = fmaf(v.z, f, acc[e + 2]);
+                  acc[e + 3] = fmaf(v.w, f, acc[e + 3]);
+                }
+              }
+              put(acc, k, inv_all, l_all == 0.f);
+            }
+          }
+        }
       }
-      if (ep >= 0) epilogue(ep, J - 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
     }
   }
 
