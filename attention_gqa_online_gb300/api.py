@@ -232,14 +232,31 @@ class PagedBatch:
         if block_table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1 or \
                 q_start.numel() != block_table.shape[0] + 1 or kv_len.numel() != block_table.shape[0]:
             raise ValueError("block_table [n, max_blocks], q_start [n + 1] and kv_len [n] do not fit together")
-        self.block_table, self.q_start, self.kv_len = block_table, q_start, kv_len
+        self._index = block_table.get_device()
+        if self._index < 0:
+            raise ValueError("block_table, q_start and kv_len must be in device memory")
         self.n_seqs, self.max_blocks = block_table.shape
+        self.block_table, self.q_start, self.kv_len = block_table, q_start, kv_len
         self.num_heads, self.num_kv_heads, self.head_dim, self.page_rows = num_heads, num_kv_heads, head_dim, page_rows
         with _on(block_table, q_start, kv_len):
             nbytes = B.attn_batch_paged_workspace_bytes(num_heads, num_kv_heads, head_dim)
         if nbytes == 0:
             raise ValueError("unsupported head sizes")
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=block_table.device)
+
+    def __setattr__(self, name, value):
+        # The tensors are checked when they are set, so that a step need not check them again.
+        if name in ("block_table", "q_start", "kv_len"):
+            _int32(value, name)
+            _same_device(self._index, value)
+            n = {"block_table": self.n_seqs * self.max_blocks, "q_start": self.n_seqs + 1, "kv_len": self.n_seqs}[name]
+            if value.numel() != n:
+                raise ValueError("%s must hold %d values" % (name, n))
+        object.__setattr__(self, name, value)
+
+    def same_device(self, index):
+        if self._index != index:
+            raise ValueError("the batch is on cuda:%d, the pools on cuda:%d" % (self._index, index))
 
     def pool(self, k_pages, v_pages):
         """(kv_dim, num_pages) of two pools [num_pages * page_rows, kv_dim]."""
@@ -286,11 +303,12 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
             qos = _rows2d(q_out, "q_out")
         q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
         _same_device(index, q, q_out)
-    _same_device(index, v_pages, k_new, v_new, table, batch.block_table, batch.q_start, batch.kv_len)
+    _same_device(index, v_pages, k_new, v_new, table)
+    batch.same_device(index)
     _run("attn_append_paged", B.load_library().attn_append_paged, index, stream,
          (q_ptr, qo_ptr, k_new.data_ptr(), v_new.data_ptr(), code, k_pages.data_ptr(), v_pages.data_ptr(), cache_code,
-          _int32(batch.block_table, "block_table"), _int32(batch.q_start, "q_start"), _int32(batch.kv_len, "kv_len"),
-          rows, batch.n_seqs, H, G, D, kv_dim, qs, qos, ks, vs, batch.page_rows, num_pages, batch.max_blocks,
+          batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H, G, D,
+          kv_dim, qs, qos, ks, vs, batch.page_rows, num_pages, batch.max_blocks,
           rot_dim if tab is not None else 0, 1 if interleaved else 0, tab, tab_rows))
     return q_out
 
@@ -330,11 +348,10 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
         scale = 1.0 / math.sqrt(D)
     index = k_pages.get_device()
     workspace = batch.workspace
-    _same_device(index, v_pages, q, out, alibi_slopes, prefix_len, batch.block_table, batch.q_start, batch.kv_len,
-                 workspace)
+    _same_device(index, v_pages, q, out, alibi_slopes, prefix_len, workspace)
+    batch.same_device(index)
     _run("attn_batch_paged", B.load_library().attn_batch_paged, index, stream,
          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), code,
-          _int32(batch.block_table, "block_table"), _int32(batch.q_start, "q_start"), _int32(batch.kv_len, "kv_len"),
-          rows, batch.n_seqs, H, batch.num_kv_heads, D, kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks,
+          batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H, batch.num_kv_heads, D, kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks,
           scale, window, softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel()))
     return out

@@ -10,6 +10,19 @@
 
 namespace attn {
 
+// Division by a constant of the launch, for dividends below 2^31: n / d =
+// (n + umulhi(n, mul)) >> shift with shift = ceil(log2 d) and mul =
+// floor(2^32 (2^shift - d) / d) + 1 (Granlund and Montgomery's round-up form).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  while ((1ull << f.shift) < d) ++f.shift;
+  f.mul = (uint32_t)((((1ull << f.shift) - d) << 32) / d + 1);
+  return f;
+}
+
 struct RopeArgs {
   const void* x;
   void* y;
@@ -23,7 +36,8 @@ struct RopeArgs {
   float sgn;  // 1: turn, -1: turn back
   // Set by launch_rope_apply.
   int units;
-  bool total_fits32;
+  FastDiv per_head, per_row;  // by units, and by units * heads
+  bool total_fits31;
 };
 int launch_rope_apply(RopeArgs a, int dtype, cudaStream_t s);
 

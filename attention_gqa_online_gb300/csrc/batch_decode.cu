@@ -3,10 +3,13 @@
 // item has at most 16 rows (the query heads of one kv head) and its time is the
 // stream of K and V.
 //
-// One block per multiprocessor: four producer warps keep 128 KB of 64-key K/V
-// tiles in flight (TMA boxes of page parts, 128-byte swizzle; a warp issues
-// one in about 100 cycles, so small pages need several) and eight warps consume them, tile J by warps 4 (J & 1) .. + 3, 16 keys a warp. The 16 rows
-// fill the M of m16n8k16, whose products cost a fraction of the tile's
+// One block per multiprocessor: four producer warps keep 128 KB of K/V tiles in
+// flight (TMA boxes of page parts, 128-byte swizzle; a warp issues one in
+// about 100 cycles, so small pages need several) and eight warps consume them,
+// tile J by warps 4 (J & 1) .. + 3, 16 keys a warp, or 32 at D = 64, where the
+// fixed costs of a 64-key tile outweigh its products (33 sequences, 14 heads
+// over 2, window 4096, capped: 28 us with 16 keys a warp, 23 with 32). The 16
+// rows fill the M of m16n8k16, whose products cost a fraction of the tile's
 // transfer time, so the whole tile's softmax runs on all lanes (on the tcgen05
 // kernel the rows would be 4 to 16 of 128 lanes). Each warp keeps its own
 // running reference, sum and output in registers: no exchange per tile. The
@@ -32,12 +35,14 @@
 namespace attn {
 namespace {
 
-constexpr int kRows = 16, kKeys = 64;
-constexpr int kItemCost = 2;  // tiles
+constexpr int kRows = 16;
+// What a piece takes beyond its tiles, in tiles. One sequence of 1536 positions takes 14.8, 13.3, 12.0 us at 1, 2, 4;
+// 64 of up to 16384 take 259.6, 259.9, 260.6 us.
+constexpr int kItemCost = 4;
 constexpr int kConsumers = 256, kThreads = kConsumers + 128;
 constexpr int kDescs = 4;
 constexpr int kRingBytes = 128 * 1024;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 4;
 
 struct DecodeDesc {
   int end, whole, n, tile0;
@@ -48,7 +53,9 @@ struct DecodeDesc {
 
 template <int D>
 struct __align__(1024) DecodeSmem {
-  static constexpr int tile_bytes = kKeys * D * 2;  // K or V
+  // Keys of a warp and of a tile: a tile is 16 KB of K and 16 KB of V either way.
+  static constexpr int warp_keys = D == 64 ? 32 : 16, keys = 4 * warp_keys;
+  static constexpr int tile_bytes = keys * D * 2;  // K or V
   static constexpr int stages = kRingBytes / (2 * tile_bytes);
   // A group waits on every use of its own stages only (a parity wait that skips a phase is no wait).
   static_assert(stages % 2 == 0 && stages <= kMaxStages, "tile J and tile J + stages belong to one group");
@@ -77,7 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = DecodeSmem<D>;
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr float kSlack = kHalf ? 8.f : 24.f;  // P <= 2^8 or 2^24: inside the operand type's range
-  constexpr int kChunks = D / 64, kChunkBytes = kKeys * 128;
+  constexpr int kKeys = S::keys, kChunkBytes = kKeys * 128;
+  constexpr int kTiles = S::warp_keys / 8, kSteps = S::warp_keys / 16;  // n-tiles of a warp's scores, k-steps of P V
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -101,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == kConsumers) prefetch_tmap(&tm_k);
   grid_dependency_wait();  // lengths, tables and pages may be the previous kernel's output
-  plan::make_plan<kRows, kKeys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
+  plan::make_plan<kRows, S::keys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
                                           &sm.start);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
   __syncthreads();
@@ -115,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_v = pw >= 2;
     const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
     const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
-    const int parts = kKeys / box_rows;             // page parts of a tile, at most 8
+    const int parts = kKeys / box_rows;             // page parts of a tile, at most 16
     const int chunk = D == 128 ? sub : 0;
     const bool my_part = lane < parts && (D == 128 || (lane & 1) == sub);
     // Tiles of one piece, from tile number J on.
@@ -246,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // -------------------------------------------------------------- consumers
-  const int grp = warp >> 2, kw = 16 * (warp & 3);  // group and first key of the tile's 16
+  const int grp = warp >> 2, kw = S::warp_keys * (warp & 3);  // group, and the warp's first key of the tile
   const int lr = lane >> 2, lc = 2 * (lane & 3);
   int J = 0;
   for (int x = 0;; ++x) {
@@ -292,59 +300,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = J + i, st = j % S::stages;
       wait(&sm.full[st], j / S::stages);
       const uint32_t k_base = smem_u32(sm.ring[st][0]), v_base = smem_u32(sm.ring[st][1]);
-      // Even and odd column steps accumulate apart: the chain of dependent products is half as long.
-      float s[2][4], s1[2][4];
+      // With two n-tiles, even and odd column steps accumulate apart: the chain of dependent products is half as long.
+      constexpr int kSets = kTiles == 2 ? 2 : 1;
+      float s[kTiles][4], s1[kTiles][4];
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int y = 0; y < kTiles; ++y)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[y][e] = s1[y][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
-        const int r = kw + (lane & 7) + 8 * (lane >> 4), u = 2 * (c & 3) + ((lane >> 3) & 1);
-        uint32_t kb[4];
-        ldsm4(kb, k_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
-        mma16816<T>(c % 2 ? s1[0] : s[0], qa[c], kb[0], kb[1]);
-        mma16816<T>(c % 2 ? s1[1] : s[1], qa[c], kb[2], kb[3]);
+#pragma unroll
+        for (int g = 0; g < kSteps; ++g) {  // 16 keys
+          const int r = kw + 16 * g + (lane & 7) + 8 * (lane >> 4), u = 2 * (c & 3) + ((lane >> 3) & 1);
+          uint32_t kb[4];
+          ldsm4(kb, k_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
+          mma16816<T>(c % kSets ? s1[2 * g] : s[2 * g], qa[c], kb[0], kb[1]);
+          mma16816<T>(c % kSets ? s1[2 * g + 1] : s[2 * g + 1], qa[c], kb[2], kb[3]);
+        }
       }
+      if (kSets == 2) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < kTiles; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[y][e] += s1[y][e];
-      const int key0 = (d.tile0 + i) * kKeys + kw + lc;
+          for (int e = 0; e < 4; ++e) s[y][e] += s1[y][e];
+      }
+      const int tile_key = (d.tile0 + i) * kKeys, key0 = tile_key + kw + lc;
+      if (a.softcap > 0.f) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < kTiles; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[y][e] = a.softcap > 0.f ? sc.out_mul * tanh_score(s[y][e] * sc.in_mul) : s[y][e] * sc.scale2;
+          for (int e = 0; e < 4; ++e) s[y][e] = sc.out_mul * tanh_score(s[y][e] * sc.in_mul);
+      } else {
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[y][e] *= sc.scale2;
+      }
       if (a.slopes != nullptr) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < kTiles; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             s[y][e] = fmaf(slope[e >> 1], fabsf((float)(pos[e >> 1] - (key0 + 8 * y + (e & 1)))), s[y][e]);
       }
-      const int tile_key = (d.tile0 + i) * kKeys;
       if (tile_key + kKeys > hi_min || tile_key < lo_max) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < kTiles; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + 8 * y + (e & 1);
             if (key >= hi[e >> 1] || key < lo[e >> 1]) s[y][e] = -INFINITY;
           }
       }
-      bool over = false;
+      float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int y = 0; y < kTiles; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) over = over || s[y][e] > m[e >> 1] + kSlack;
-      if (__any_sync(0xffffffffu, over)) {  // some reference moves: exact maxima of the tile's 16 keys
+        for (int h = 0; h < 2; ++h) t[h] = max3(t[h], s[y][2 * h], s[y][2 * h + 1]);
+      if (__any_sync(0xffffffffu, t[0] > m[0] + kSlack || t[1] > m[1] + kSlack)) {  // some reference moves
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float t = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          const float mn = fmaxf(m[h], t), f = mn == m[h] ? 1.f : ex2(m[h] - mn);
+          t[h] = fmaxf(t[h], __shfl_xor_sync(0xffffffffu, t[h], 1));
+          t[h] = fmaxf(t[h], __shfl_xor_sync(0xffffffffu, t[h], 2));
+          const float mn = fmaxf(m[h], t[h]), f = mn == m[h] ? 1.f : ex2(m[h] - mn);
           m[h] = mn;
           l[h] *= f;
 #pragma unroll
@@ -356,21 +374,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int y = 0; y < kTiles; ++y)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[y][e] = ex2(s[y][e] - sub[e >> 1]);
           l[e >> 1] += s[y][e];
         }
-      const uint32_t pa[4] = {pack2<T>(s[0][0], s[0][1]), pack2<T>(s[0][2], s[0][3]), pack2<T>(s[1][0], s[1][1]),
-                              pack2<T>(s[1][2], s[1][3])};
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const int r = kw + (lane & 15), u = 2 * (c & 3) + (lane >> 4);
-        uint32_t vb[4];
-        ldsm4_t(vb, v_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
-        mma16816<T>(o[2 * c], pa, vb[0], vb[1]);
-        mma16816<T>(o[2 * c + 1], pa, vb[2], vb[3]);
+      for (int g = 0; g < kSteps; ++g) {
+        const uint32_t pa[4] = {pack2<T>(s[2 * g][0], s[2 * g][1]), pack2<T>(s[2 * g][2], s[2 * g][3]),
+                                pack2<T>(s[2 * g + 1][0], s[2 * g + 1][1]), pack2<T>(s[2 * g + 1][2], s[2 * g + 1][3])};
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const int r = kw + 16 * g + (lane & 15), u = 2 * (c & 3) + (lane >> 4);
+          uint32_t vb[4];
+          ldsm4_t(vb, v_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
+          mma16816<T>(o[2 * c], pa, vb[0], vb[1]);
+          mma16816<T>(o[2 * c + 1], pa, vb[2], vb[3]);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.empty[st]);
@@ -486,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <typename T, int D>
 int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
-  if (box_rows > kKeys) box_rows = kKeys;
+  if (box_rows > DecodeSmem<D>::keys) box_rows = DecodeSmem<D>::keys;
   const uint64_t dims[2] = {(uint64_t)a.kv_dim, (uint64_t)a.num_pages * a.page_rows};
   const uint64_t strides[1] = {(uint64_t)a.kv_dim * 2};
   const uint32_t box[2] = {64, (uint32_t)box_rows}, one_row[2] = {64, 1};
