@@ -28,8 +28,8 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) { return (n + __umulhi(n, f.mul)) >> f.shift; }
 
 // Bound by HBM (each element in and out once; the table's rows, shared by the
-// heads, come from L2): 8192 rows of 40 heads of 128, bf16, move 172 MB in 27 us,
-// 6.3 TB/s. A unit is 16 or 32 bytes, so a thread's index arithmetic counts: two
+// heads, come from L2): 8192 rows of 40 heads of 128, bf16, move 172 MB in 29 us,
+// 5.9 TB/s. A unit is 16 or 32 bytes, so a thread's index arithmetic counts: two
 // 32-bit multiplications in place of divisions.
 template <typename T, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const RopeArgs a) {
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const RopeArgs a) 
     const uint32_t pos = a.positions != nullptr ? a.positions[row] : row;
     const bool ok = pos < a.table_rows;
     if (!ok && rem == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
-    rot::move_unit<T, T, INTER, VEC>(x + (long long)row * a.x_stride + (long long)h * a.D,
+    rot::move_unit<T, T, INTER, VEC, true>(x + (long long)row * a.x_stride + (long long)h * a.D,
                                      y + (long long)row * a.y_stride + (long long)h * a.D, (int)u, a.D, a.R,
                                      a.table + (long long)(ok ? pos : 0) * a.R, a.sgn, ok);
   }
