@@ -101,6 +101,9 @@ struct BatchArgs {
 };
 // Sequences of a batch at most (the plan keeps one count each in shared memory).
 constexpr int kMaxBatchSeqs = 16384;
+// Positions of a sequence at most: a piece's warps wait for one another for at
+// most a second, and 2^24 keys of the slowest score map take about 0.7 s.
+constexpr uint64_t kMaxBatchCapacity = 1ull << 24;
 size_t batch_workspace_bytes(int D, int sm_count);
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s);
 int launch_batch_mma(const BatchArgs& a, int dtype, int blocks, cudaStream_t s);

@@ -167,7 +167,9 @@ extern "C" int attn_batch_paged(const void* q, const void* k_pages, const void* 
   if (dtype == ATTN_DT_F32 || head_dim % 8 != 0 || kv_dim % 8 != 0 || q_stride % 8 != 0 || out_stride % 8 != 0 ||
       !aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16))
     return ATTN_ERR_UNSUPPORTED;
-  if ((uint64_t)total_rows * n_heads > (1u << 30) || n_seqs > (uint32_t)kMaxBatchSeqs) return ATTN_ERR_UNSUPPORTED;
+  if ((uint64_t)total_rows * n_heads > (1u << 30) || n_seqs > (uint32_t)kMaxBatchSeqs ||
+      (uint64_t)page_rows * max_blocks > kMaxBatchCapacity)
+    return ATTN_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   if (workspace == nullptr || workspace_bytes < batch_workspace_bytes((int)head_dim, sms) || !aligned(workspace, 16))

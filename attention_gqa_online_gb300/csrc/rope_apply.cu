@@ -70,13 +70,15 @@ int launch_t(const RopeArgs& a, bool vec, cudaStream_t s) {
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// One thread per (position, pair); angles in fp64 (an fp32 angle p theta
-// would be off by up to p 2^-24 rad), rounded to fp32 once.
+// One thread per pair and eight positions, so that the pair's angle (a power)
+// is computed once for them; angles in fp64 (an fp32 angle p theta would be off
+// by up to p 2^-24 rad), rounded to fp32 once.
+constexpr int kTablePositions = 8;
 __global__ void __launch_bounds__(kThreads) rope_table_scaled_kernel(float* table, uint32_t max_pos, int R, RopeScale sc) {
   const int half = R / 2;
   const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (idx >= (long long)max_pos * half) return;
-  const uint32_t p = (uint32_t)(idx / half);
+  const long long p0 = idx / half * kTablePositions;
+  if (p0 >= max_pos) return;
   const int i = (int)(idx % half);
   double th = pow(sc.base, -2.0 * (double)i / (double)R);
   if (sc.kind == ATTN_ROPE_LINEAR) {
@@ -86,10 +88,12 @@ __global__ void __launch_bounds__(kThreads) rope_table_scaled_kernel(float* tabl
     const double g = fmin(1.0, fmax(0.0, (turns - sc.beta_slow) / (sc.beta_fast - sc.beta_slow)));
     th *= g + (1.0 - g) / sc.factor;
   }
-  double sn, cs;
-  sincos((double)p * th, &sn, &cs);
-  table[(long long)p * R + i] = (float)(sc.attn_factor * cs);
-  table[(long long)p * R + half + i] = (float)(sc.attn_factor * sn);
+  for (long long p = p0; p < p0 + kTablePositions && p < max_pos; ++p) {
+    double sn, cs;
+    sincos((double)p * th, &sn, &cs);
+    table[p * R + i] = (float)(sc.attn_factor * cs);
+    table[p * R + half + i] = (float)(sc.attn_factor * sn);
+  }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -114,7 +118,7 @@ int launch_rope_apply(RopeArgs a, int dtype, cudaStream_t s) {
 
 int launch_rope_table_scaled(float* table, uint32_t max_pos, int R, RopeScale sc, cudaStream_t s) {
   if (sc.kind == ATTN_ROPE_NTK) sc.base *= std::pow(sc.factor, (double)R / (R - 2.0));
-  const long long n = (long long)max_pos * (R / 2);
+  const long long n = ((long long)max_pos + kTablePositions - 1) / kTablePositions * (R / 2);
   rope_table_scaled_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(table, max_pos, R, sc);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

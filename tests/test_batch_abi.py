@@ -121,6 +121,7 @@ def test_batch_rejects(lib, kw):
 @pytest.mark.parametrize("kw", [
     dict(dt=0), dict(D=60, kv_dim=128), dict(kv_dim=132), dict(q_stride=260), dict(o_stride=260), dict(q=FAKE + 2),
     dict(kp=FAKE + 8), dict(vp=FAKE + 8), dict(out=FAKE + 8), dict(n=16385), dict(rows=2 ** 29),
+    dict(page_rows=2 ** 14, blocks=2 ** 11, pages=8),
 ])
 def test_batch_unsupported(lib, kw):
     assert batch_call(lib, **kw) == UNSUP

@@ -337,3 +337,62 @@ def test_single_tokens_repeat_bits_and_share_a_workspace(cuda_lib, H, G, D, kv):
         if i % 10 == 0:
             assert torch.equal(second, A.attend_paged(obj2, other.q, other.k, other.v))
     assert A.attn_get_status() == 0
+
+
+@pytest.mark.parametrize("H,G,D", [(8, 2, 128), (7, 1, 64), (16, 1, 128)])
+def test_rows_of_few_sequences_among_many_empty_ones(cuda_lib, H, G, D):
+    """No more rows than sequences, but several of one sequence (the single-token kernel's row blocks)."""
+    new = [0] * 12 + [7] + [0] * 5 + [1, 9] + [0] * 10
+    kv = [5] * 12 + [300] + [0] * 5 + [70, 9] + [3] * 10
+    check(cuda_lib, Batch(new, kv, H, G, D, 16, BF16, seed=41), "few of many")
+
+
+@pytest.mark.parametrize("D", [64, 128, 80])
+def test_the_most_sequences(cuda_lib, D):
+    n = 16384
+    kv = [1 + (i * 5) % 9 for i in range(n)]
+    b = Batch([1] * n, kv, 2, 1, D, 8, F16, seed=42)
+    got = cuda_lib.attend_paged(b.object(cuda_lib), b.q, b.k, b.v)
+    assert cuda_lib.attn_get_status() == 0
+    pick = list(range(0, n, 997)) + [n - 1]
+    for i in pick:
+        sl = b.slots(i, 0, kv[i])
+        k, v = b.k[sl].double(), b.v[sl].double()
+        w = torch.softmax(b.q[i].double().view(2, D) @ k.t() / D ** 0.5, -1)
+        ref, mag = (w @ v).view(-1), (w @ v.abs()).view(-1)
+        assert ((got[i].double() - ref).abs() <= attend_tolerance(ref, mag, F16, 9)).all(), i
+
+
+def test_infinite_scores_stay_in_their_row(cuda_lib):
+    """A NaN query makes its own row NaN and no other; a NaN key within reach makes its sequence's rows NaN."""
+    for new in ([1, 1, 1], [40, 40, 40], [400, 400, 400]):
+        b = Batch(new, [500, 450, 600], 8, 2, 128, 16, BF16, seed=43)
+        want = cuda_lib.attend_paged(b.object(cuda_lib), b.q, b.k, b.v).clone()
+        row = b.starts[1]
+        b.q[row] = float("nan")
+        b.k[b.slots(2, 0, 1)] = float("nan")
+        got = cuda_lib.attend_paged(b.object(cuda_lib), b.q, b.k, b.v)
+        torch.cuda.synchronize()
+        assert cuda_lib.attn_get_status() == 0
+        assert torch.isnan(got[row].float()).all() and torch.isnan(got[b.starts[2]:].float()).all()
+        keep = [i for i in range(b.starts[2]) if i != row]
+        assert torch.equal(got[keep], want[keep])
+
+
+def test_two_batches_on_two_streams(cuda_lib):
+    """Different batch objects (workspaces) may run at the same time."""
+    A = cuda_lib
+    bs = [Batch([1] * 9, [2000] * 9, 32, 8, 128, 16, BF16, seed=44), Batch([300, 2], [900, 4000], 8, 2, 128, 64, BF16, seed=45)]
+    want = [A.attend_paged(b.object(A), b.q, b.k, b.v) for b in bs]
+    objs, streams = [b.object(A) for b in bs], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[torch.zeros_like(b.q) for _ in range(20)] for b in bs]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for b, o, s, out in zip(bs, objs, streams, outs):
+            A.attend_paged(o, b.q, b.k, b.v, out=out[i], stream=s)
+    torch.cuda.synchronize()
+    assert A.attn_get_status() == 0
+    for w, out in zip(want, outs):
+        for o in out:
+            assert torch.equal(w, o)
