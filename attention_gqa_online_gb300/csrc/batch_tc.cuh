@@ -983,9 +983,10 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   if (PAIR && box_rows > 64) box_rows = 64;  // a block holds 64 keys of a K tile
   const uint32_t box[2] = {64, (uint32_t)box_rows}, one_row[2] = {64, 1};
   CUtensorMap tm_k, tm_v, tm_v1;  // 16-bit elements are only moved: one element type serves both
-  if (!make_tmap(&tm_k, a.k_pages, 2, dims, strides, box, true, kSwizzle128) ||
-      !make_tmap(&tm_v, a.v_pages, 2, dims, strides, box, true, kSwizzle128) ||
-      !make_tmap(&tm_v1, a.v_pages, 2, dims, strides, one_row, true, kSwizzle128))
+  // (L2 fetches no more than a head's row: its neighbour is another head's.)
+  if (!make_tmap(&tm_k, a.k_pages, 2, dims, strides, box, true, kSwizzle128, 2 * D) ||
+      !make_tmap(&tm_v, a.v_pages, 2, dims, strides, box, true, kSwizzle128, 2 * D) ||
+      !make_tmap(&tm_v1, a.v_pages, 2, dims, strides, one_row, true, kSwizzle128, 2 * D))
     return ATTN_ERR_CUDA;
   // Q: [rows][H][D]; a row block is one box of gs heads x 128/gs tokens when gs divides 128.
   int q_box = kTcRows % a.gs == 0 ? 1 : 0;

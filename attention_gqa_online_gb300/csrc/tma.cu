@@ -25,7 +25,7 @@ void resolve() {
 }  // namespace
 
 bool make_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-               const uint32_t* box, bool bf16, int swizzle) {
+               const uint32_t* box, bool bf16, int swizzle, int l2_bytes) {
   std::call_once(g_once, resolve);
   if (g_encode == nullptr || rank < 1 || rank > 5) return false;
   uint32_t estr[5] = {1, 1, 1, 1, 1};
@@ -35,7 +35,8 @@ bool make_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dim
                               swizzle == kSwizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B
                               : swizzle == kSwizzle128Atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B
                                                              : CU_TENSOR_MAP_SWIZZLE_NONE,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              l2_bytes == 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
