@@ -1,7 +1,8 @@
 // batch_decode.cu -- single-token attention of a batch over its pages: the
 // operation of batch_mma.cu where each sequence has about one new token, so an
 // item has at most 16 rows (the query heads of one kv head) and its time is the
-// stream of K and V.
+// stream of K and V. D is the head dimension rounded up to 64 or 128 (the
+// columns past the head are zeros and not stored).
 //
 // One block per multiprocessor: four producer warps keep 128 KB of K/V tiles in
 // flight (TMA boxes of page parts, 128-byte swizzle; a warp issues one in
@@ -108,6 +109,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (tid == kConsumers) prefetch_tmap(&tm_k);
+  // Columns of Q past the head stay zeros.
+  for (int i = tid; i < 2 * kRows * S::q_stride; i += kThreads) sm.q[0][i] = 0;
   grid_dependency_wait();  // lengths, tables and pages may be the previous kernel's output
   plan::make_plan<kRows, S::keys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
                                           &sm.start);
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool my_part = lane < parts && (D == 128 || (lane & 1) == sub);
     // Tiles of one piece, from tile number J on.
     auto load_tiles = [&](int n, int seq, int g, int lo, int hi, int tile0, int J) {
-      const int key0 = tile0 * kKeys, col = g * D + 64 * chunk;
+      const int key0 = tile0 * kKeys;
       const uint32_t* table = a.block_table + (long long)seq * a.max_blocks;
       // Pool rows of the page parts, 32 at a time (one a lane), read at least 32 parts ahead.
       auto rows_of = [&](int q0) {
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + chunk * kChunkBytes;
         // V rows of a fetched part that lie outside the windows are replaced by zeros, row by row (0 * NaN).
         const bool edge = is_v && row != outside && (key < lo || key + box_rows > hi);
-        if (my_part && !edge) tma_load_2d(dst + lane * box_rows * 128, tm, col, row, &sm.full[st]);
+        if (my_part && !edge) tma_load_3d(dst + lane * box_rows * 128, tm, 64 * chunk, g, row, &sm.full[st]);
         unsigned edges = __ballot_sync(0xffffffffu, edge);
         while (edges) {
           const int e = __ffs(edges) - 1;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row_e = __shfl_sync(0xffffffffu, row, e), key_e = __shfl_sync(0xffffffffu, key, e);
           for (int r = lane; r < box_rows; r += 32) {
             const int y = key_e + r >= lo && key_e + r < hi ? row_e + r : outside;
-            tma_load_2d(dst + (e * box_rows + r) * 128, &tm_v1, col, y, &sm.full[st]);
+            tma_load_3d(dst + (e * box_rows + r) * 128, &tm_v1, 64 * chunk, g, y, &sm.full[st]);
           }
         }
       }
@@ -196,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more && p.t1 == p.t0) {  // rows without keys
         for (int r = 0; r < rows; ++r) {
           const int f = first_row + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
-          T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * D;
-          if (lane < D / 8) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0u, 0u, 0u, 0u);
+          T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * a.D;
+          if (lane < a.D / 8) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0u, 0u, 0u, 0u);
         }
         continue;
       }
@@ -232,12 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!more) break;
       // Q rows, one copy each.
       if (x >= 2 && !__all_sync(0xffffffffu, wait(&sm.q_free[x & 1], (x >> 1) - 1))) break;
-      if (lane == 0) mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)(rows * D * 2));
+      if (lane == 0) mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)(rows * a.D * 2));
       __syncwarp();
       if (lane < rows) {
         const int f = first_row + lane, t = f / a.gs, h = p.g * a.gs + f % a.gs;
         bulk_g2s(&sm.q[x & 1][lane * S::q_stride],
-                 static_cast<const T*>(a.q) + (long long)(p.q.row0 + t) * a.q_stride + (long long)h * D, D * 2,
+                 static_cast<const T*>(a.q) + (long long)(p.q.row0 + t) * a.q_stride + (long long)h * a.D, a.D * 2,
                  &sm.q_ready[x & 1]);
       }
       J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.lo_min, p.k.hi_max, p.k.kt0 + p.t0, J);
@@ -440,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kPerRow = D / 8;  // threads of a row, eight columns each
     const int r = tid / kPerRow, c0 = 8 * (tid % kPerRow);
     const bool mine = tid < kRows * kPerRow && r < rows;
+    const bool inside = c0 < a.D;  // the others are columns past the head
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, m_all = -INFINITY, l_all = 0.f;
     // Adds state (m, l, eight columns) to the thread's.
     auto add = [&](float2 ml, float4 v0, float4 v1) {
@@ -455,11 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto store = [&]() {
       const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
       const int f = d.first_row + r, t = f / a.gs, h = d.g * a.gs + f % a.gs;
-      T* dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D + c0;
+      T* dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * a.D + c0;
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = l_all == 0.f ? 0u : pack2<T>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (inside) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     };
     if (mine) {
 #pragma unroll
@@ -508,15 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int D>
 int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   if (box_rows > DecodeSmem<D>::keys) box_rows = DecodeSmem<D>::keys;
-  const uint64_t dims[2] = {(uint64_t)a.kv_dim, (uint64_t)a.num_pages * a.page_rows};
-  const uint64_t strides[1] = {(uint64_t)a.kv_dim * 2};
-  const uint32_t box[2] = {64, (uint32_t)box_rows}, one_row[2] = {64, 1};
+  // K and V: [rows][G][head_dim]; columns past the head (head_dim < D) arrive as zeros.
+  const uint64_t dims[3] = {(uint64_t)a.D, (uint64_t)a.G, (uint64_t)a.num_pages * a.page_rows};
+  const uint64_t strides[2] = {(uint64_t)a.D * 2, (uint64_t)a.kv_dim * 2};
+  const uint32_t box[3] = {64, 1, (uint32_t)box_rows}, one_row[3] = {64, 1, 1};
   CUtensorMap tm_k, tm_v, tm_v1;  // 16-bit elements are only moved: one element type serves both
-  // A row of one head is 2 D bytes and its neighbour another head's, read much later by another block: at D = 64 L2
-  // must not fetch 256 bytes (64 sequences of 8192, 8 kv heads: 229 us so, 164 with 128, 6.5 TB/s).
-  if (!make_tmap(&tm_k, a.k_pages, 2, dims, strides, box, true, kSwizzle128, 2 * D) ||
-      !make_tmap(&tm_v, a.v_pages, 2, dims, strides, box, true, kSwizzle128, 2 * D) ||
-      !make_tmap(&tm_v1, a.v_pages, 2, dims, strides, one_row, true, kSwizzle128, 2 * D))
+  const int l2 = kv_l2_bytes(a.D);
+  if (!make_tmap(&tm_k, a.k_pages, 3, dims, strides, box, true, kSwizzle128, l2) ||
+      !make_tmap(&tm_v, a.v_pages, 3, dims, strides, box, true, kSwizzle128, l2) ||
+      !make_tmap(&tm_v1, a.v_pages, 3, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
   const void* kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D>);
   const size_t smem = sizeof(DecodeSmem<D>) + 1024;
@@ -531,9 +535,9 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
 
 int launch_batch_decode(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s) {
   if (dtype == ATTN_DT_BF16)
-    return a.D == 64 ? launch_decode_t<__nv_bfloat16, 64>(a, blocks, box_rows, s)
+    return a.D <= 64 ? launch_decode_t<__nv_bfloat16, 64>(a, blocks, box_rows, s)
                      : launch_decode_t<__nv_bfloat16, 128>(a, blocks, box_rows, s);
-  return a.D == 64 ? launch_decode_t<__half, 64>(a, blocks, box_rows, s)
+  return a.D <= 64 ? launch_decode_t<__half, 64>(a, blocks, box_rows, s)
                    : launch_decode_t<__half, 128>(a, blocks, box_rows, s);
 }
 

@@ -291,7 +291,8 @@ static int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, cudaS
 }
 
 // Arrival counters, split records, and partial slots (two a thread block; at most 128 rows a multiprocessor).
-size_t batch_workspace_bytes(int D, int sm_count) {
+size_t batch_workspace_bytes(int head_dim, int sm_count) {
+  const int D = head_dim <= 64 ? 64 : 128;  // as the kernels round it up
   return (size_t)2 * sm_count * 128 * (D + 2) * sizeof(float) + (size_t)2 * sm_count * sizeof(BatchSplit) +
          (size_t)4 * ((sm_count + 7) / 8 * 8) * sizeof(unsigned);
 }
@@ -300,17 +301,26 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   a.arrived = static_cast<unsigned*>(workspace);
   a.split = reinterpret_cast<BatchSplit*>(a.arrived + 4 * ((sm_count + 7) / 8 * 8));
   a.partial = reinterpret_cast<float*>(a.split + 2 * sm_count);
-  // The tensor-core kernel moves pages by TMA boxes of the largest power of
-  // two of rows that divides a page, whole 8-row groups of the swizzle.
+  // Pages move by TMA boxes of the largest power of two of rows that divides a
+  // page, whole 8-row groups of the swizzle; other pages take the mma kernel.
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
-  const bool tma = (a.D == 64 || a.D == 128) && box >= 8;
-  if (tma && a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
-  const bool pair = tma && a.D == 128 && 128 % a.gs == 0 && sm_count % 2 == 0 &&
-                    (long long)a.total_rows * a.gs >= 256ll * a.n_seqs;
-  if (pair) return launch_batch_tc_pair(a, dtype, sm_count, box, s);
-  if (tma)
-    return a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s) : launch_batch_tc_d128(a, dtype, sm_count, box, s);
+  if (box >= 8) {
+    // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 308
+    // us at 4 query heads a kv head, 313 at 16 (tcgen05 kernel: 326 and 332); 8 sequences of 2048: 16 us against 40.
+    // More heads a kv head would read K and V once for every 16 of them.
+    if (a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
+    // Pairs of multiprocessors share K and V tiles between 256 rows, where sequences have that many on average. 16
+    // sequences of 4096, 4 heads a kv head of 128, with 32, 128, 256, 512, 1024 rows a kv head: pairs 86, 97, 90, 140,
+    // 239 us, single blocks 84, 98, 113, 185, 327.
+    if (a.D > 64 && 128 % a.gs == 0 && sm_count % 2 == 0 && (long long)a.total_rows * a.gs >= 256ll * a.n_seqs)
+      return a.D == 128 ? launch_batch_tc_pair(a, dtype, sm_count, box, s)
+                        : launch_batch_tc_part_pair(a, dtype, sm_count, box, s);
+    if (a.D > 64)
+      return a.D == 128 ? launch_batch_tc_d128(a, dtype, sm_count, box, s)
+                        : launch_batch_tc_part128(a, dtype, sm_count, box, s);
+    return a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s) : launch_batch_tc_part64(a, dtype, sm_count, box, s);
+  }
   const int rc = launch_batch_mma(a, dtype, 2 * sm_count, s);
   return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, 2 * sm_count, s);
 }

@@ -1,5 +1,10 @@
 // batch_tc.cuh -- attention of each sequence's new tokens over its pages on
-// the tcgen05 tensor cores (D = 64 or 128, pages of whole 8-row groups).
+// the tcgen05 tensor cores (pages of whole 8-row groups). D is the head
+// dimension rounded up to 64 or 128. A smaller head (FULL false) takes TMA maps
+// that end at the head: the columns past it are zeros in Q, K and V, and are
+// not stored. 4 sequences of 512 new tokens at 8192, 32 heads over 8 of 96 and
+// of 40: 222 and 190 us (batch_mma.cu: 1425 and 917; heads of 128 and 64 in the
+// same form: 227 and 192, in their own 220 and 188).
 //
 // The operation and the division of work are those of batch_mma.cu and
 // batch_plan.cuh; here a row block is 128 flattened rows (the M of one MMA)
@@ -33,8 +38,7 @@
 //
 // End of a piece.  The output warps read O as soon as the last P V lands, and
 // the next piece's first P V waits for that read only; the softmax groups go
-// straight on to the next piece.  (With the groups reading O themselves a piece
-// cost about five tiles' time more.)
+// straight on to the next piece.
 //
 // Rows of V that lie in a fetched page part but outside the block's windows
 // hold whatever the page holds (0 * NaN would reach every row): such parts are
@@ -62,8 +66,8 @@ namespace attn {
 namespace {
 
 constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 512;
-// What a piece takes beyond its tiles, in tiles: prompt of 8192 (pieces of 1 to 64 tiles) 815, 690, 649, 657 us at 1,
-// 2, 3, 4.
+// What a piece takes beyond its tiles, in tiles, at 1, 2, 3: prompt of 8192 (pieces of 1 to 64 tiles) 574, 476, 500 us,
+// mixed batch of short and long chunks 283, 262, 262, long chunks alike 282, 282, 283.
 constexpr int kItemCost = 2;
 constexpr int kDescs = 4;        // piece descriptors in flight
 constexpr int kChain = 4;        // reference maxima in flight
@@ -202,6 +206,15 @@ __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int x
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
+// Rows of a kv head: column x of whole rows (FULL), or of head g in a map that
+// ends at the head.
+template <bool PAIR, bool FULL>
+__device__ __forceinline__ void load_rows(void* dst, const CUtensorMap* map, int x, int g, int row, uint32_t bar) {
+  if (FULL)
+    load_2d<PAIR>(dst, map, x, row, bar);
+  else
+    load_3d<PAIR>(dst, map, x, g, row, bar);
+}
 // Tensor-memory allocation and commits of a pair: both blocks allocate, the
 // first one issues, and a commit arrives in both.
 template <bool PAIR>
@@ -270,12 +283,13 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uin
 // MODE 0: scores are scale2 * S with scale2 > 0 (folded into the exponent's
 // fma); 1: scaled, with an optional distance bias; 2: capped, with an optional
 // distance bias.
-template <typename T, int D, int MODE, bool PAIR>
+template <typename T, int D, int MODE, bool PAIR, bool FULL>
 __global__ void __launch_bounds__(kTcThreads, 1)
     batch_tc_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1,
                     const __grid_constant__ CUtensorMap tm_q, const int box_rows, const int q_box) {
   using L = TcLayout<D, PAIR>;
+  const int hd = FULL ? D : a.D;  // columns of a head
   constexpr bool kHalf = std::is_same<T, __half>::value;
   constexpr float kRescale = kHalf ? 8.f : 24.f;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -408,8 +422,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (more && p.t1 == p.t0) {  // rows without keys
           for (int r = lane >> 2; r < rows; r += 8) {
             const int f = first_row + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
-            T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * D;
-            for (int u = lane & 3; u < D / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
+            T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * hd;
+            for (int u = lane & 3; u < hd / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
           }
           continue;
         }
@@ -445,7 +459,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (!more) break;
         // The piece's first page parts are looked up while its Q buffer falls free.
-        const int n = p.t1 - p.t0, col = p.g * D;
+        const int n = p.t1 - p.t0, col = FULL ? p.g * D : 0;
         Parts w = open_parts(L::k_rows, n, p.k.lo_min, p.k.hi_max,
                              (p.k.kt0 + p.t1 - 1) * kTcKeys + (PAIR ? rank * L::k_rows : 0), p.s);
         // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
@@ -466,10 +480,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           constexpr int kUnits = D / 8, kRowsPer = 32 / kUnits;  // units of a row over the lanes
           const int u = lane % kUnits;
           unsigned char* qt = sm.q[x & 1] + (u >> 3) * L::q_chunk;
-          const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * D + 8 * u;
+          const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * hd;
+          const bool inside = 8 * u < hd;  // columns past the head are zeros
           for (int r = lane / kUnits; r < rows; r += kRowsPer) {
             const int f = first_row + r, t = f / a.gs;
-            cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)), src + (long long)t * a.q_stride + (f - t * a.gs) * D, 16u);
+            cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)),
+                       src + (long long)t * a.q_stride + (f - t * a.gs) * hd + (inside ? 8 * u : 0), inside ? 16u : 0u);
           }
           cp_async_commit();
           cp_async_wait<0>();
@@ -487,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint32_t bar = barrier_of(&sm.k_full[slot]);
 #pragma unroll
             for (int c = 0; c < L::chunks; ++c)
-              load_2d<PAIR>(sm.k[slot] + c * L::k_chunk + lane * box_rows * 128, &tm_k, col + 64 * c, row, bar);
+              load_rows<PAIR, FULL>(sm.k[slot] + c * L::k_chunk + lane * box_rows * 128, &tm_k, col + 64 * c, p.g, row, bar);
           }
         }
         ++x;
@@ -506,7 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int x = 0; ok; ++x) {
         const PieceDesc& d = piece(x);
         if (d.end || *(volatile int*)&sm.abort) break;
-        const int n = d.n, col = d.g * D + (PAIR ? rank * 64 * L::v_chunks : 0);
+        const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
         Parts w = open_parts(kTcKeys, n, d.lo_min, d.hi_max, d.tile_last * kTcKeys, d.seq);
         for (int i = 0; i < n; ++i, ++J) {
           const int row = part_row(w, i), key = w.key0 - i * kTcKeys + lane * box_rows, slot = J % L::slots;
@@ -521,7 +537,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (lane < w.parts && !edge) {
 #pragma unroll
             for (int c = 0; c < L::v_chunks; ++c)
-              load_2d<PAIR>(sm.v[slot] + c * L::v_chunk + lane * box_rows * 128, &tm_v, col + 64 * c, row, bar);
+              load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + lane * box_rows * 128, &tm_v, col + 64 * c, g, row,
+                                       bar);
           }
           unsigned edges = __ballot_sync(0xffffffffu, edge);
           while (edges) {
@@ -532,7 +549,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int y = key_p + r >= w.lo && key_p + r < w.hi ? row_p + r : outside;
 #pragma unroll
               for (int c = 0; c < L::v_chunks; ++c)
-                load_2d<PAIR>(sm.v[slot] + c * L::v_chunk + (p * box_rows + r) * 128, &tm_v1, col + 64 * c, y, bar);
+                load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + (p * box_rows + r) * 128, &tm_v1, col + 64 * c, g, y,
+                                         bar);
             }
           }
         }
@@ -868,7 +886,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       T* dst = nullptr;
       if (busy) {
         const int f = d.first_row + min(r, d.rows - 1), t = f / a.gs, h = d.g * a.gs + (f - t * a.gs);
-        dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * D;
+        dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * hd;
       }
       const bool whole = d.whole;
       const int pr = rank * kTcRows + r;  // row of the item
@@ -880,7 +898,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) w[k] = empty ? 0u : pack_pair<T>(v[e + 2 * k] * mul, v[e + 2 * k + 1] * mul);
-          *reinterpret_cast<uint4*>(dst + kCols * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (kCols * c + e < hd) *reinterpret_cast<uint4*>(dst + kCols * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       };
       wait(&sm.o_ready, x);
@@ -976,35 +994,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <typename T, int D, bool PAIR>
+template <typename T, int D, bool PAIR, bool FULL>
 int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
-  const uint64_t dims[2] = {(uint64_t)a.kv_dim, (uint64_t)a.num_pages * a.page_rows};
-  const uint64_t strides[1] = {(uint64_t)a.kv_dim * 2};
+  // K and V: whole rows, or [rows][G][head_dim], where columns past the head arrive as zeros.
+  const int rank = FULL ? 2 : 3;
+  const uint64_t pool = (uint64_t)a.num_pages * a.page_rows;
+  const uint64_t dims[3] = {(uint64_t)(FULL ? a.kv_dim : a.D), FULL ? pool : (uint64_t)a.G, pool};
+  const uint64_t strides[2] = {(uint64_t)(FULL ? a.kv_dim : a.D) * 2, (uint64_t)a.kv_dim * 2};
   if (PAIR && box_rows > 64) box_rows = 64;  // a block holds 64 keys of a K tile
-  const uint32_t box[2] = {64, (uint32_t)box_rows}, one_row[2] = {64, 1};
+  const uint32_t box[3] = {64, FULL ? (uint32_t)box_rows : 1, (uint32_t)box_rows}, one_row[3] = {64, 1, 1};
   CUtensorMap tm_k, tm_v, tm_v1;  // 16-bit elements are only moved: one element type serves both
-  // (L2 fetches no more than a head's row: its neighbour is another head's.)
-  if (!make_tmap(&tm_k, a.k_pages, 2, dims, strides, box, true, kSwizzle128, 2 * D) ||
-      !make_tmap(&tm_v, a.v_pages, 2, dims, strides, box, true, kSwizzle128, 2 * D) ||
-      !make_tmap(&tm_v1, a.v_pages, 2, dims, strides, one_row, true, kSwizzle128, 2 * D))
+  const int l2 = kv_l2_bytes(a.D);
+  if (!make_tmap(&tm_k, a.k_pages, rank, dims, strides, box, true, kSwizzle128, l2) ||
+      !make_tmap(&tm_v, a.v_pages, rank, dims, strides, box, true, kSwizzle128, l2) ||
+      !make_tmap(&tm_v1, a.v_pages, rank, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
   // Q: [rows][H][D]; a row block is one box of gs heads x 128/gs tokens when gs divides 128.
   int q_box = kTcRows % a.gs == 0 ? 1 : 0;
   CUtensorMap tm_q = tm_k;
   if (q_box) {
-    const uint64_t qdims[3] = {(uint64_t)D, (uint64_t)a.H, (uint64_t)a.total_rows};
-    const uint64_t qstrides[2] = {(uint64_t)D * 2, (uint64_t)a.q_stride * 2};
+    const uint64_t qdims[3] = {(uint64_t)a.D, (uint64_t)a.H, (uint64_t)a.total_rows};
+    const uint64_t qstrides[2] = {(uint64_t)a.D * 2, (uint64_t)a.q_stride * 2};
     const uint32_t qbox[3] = {64, (uint32_t)a.gs, (uint32_t)(kTcRows / a.gs)};
     if (!make_tmap(&tm_q, a.q, 3, qdims, qstrides, qbox, true, kSwizzle128)) return ATTN_ERR_CUDA;
   }
   ScoreMap sc = score_map(a);
   const void* kern;
   if (a.softcap > 0.f)
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR, FULL>);
   else if (a.slopes != nullptr || !(sc.scale2 >= FLT_MIN))
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL>);
   else
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL>);
   const size_t smem = sizeof(TcSmem<D, PAIR>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;

@@ -92,8 +92,8 @@ bool set_smem_limit(const void* kernel, size_t bytes);
 // elements read as zero.  Swizzle: none, 128-byte rows with 16-byte chunks
 // permuted, or 128-byte rows with 32-byte chunks permuted.
 enum { kSwizzleNone = 0, kSwizzle128 = 1, kSwizzle128Atom32 = 2 };
-// l2_bytes: how much L2 fetches around a missed sector (256 or 128); 256 wants
-// neighbours that are read soon, too.
+// l2_bytes: how much L2 fetches around a missed sector (256, 128, 64, less:
+// the sector alone); more wants neighbours that are read soon, too.
 bool make_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                const uint32_t* box, bool bf16, int swizzle, int l2_bytes = 256);
 

@@ -35,7 +35,10 @@ bool make_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* dim
                               swizzle == kSwizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B
                               : swizzle == kSwizzle128Atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B
                                                              : CU_TENSOR_MAP_SWIZZLE_NONE,
-                              l2_bytes == 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              l2_bytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                              : l2_bytes >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                              : l2_bytes >= 64  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                : CU_TENSOR_MAP_L2_PROMOTION_NONE,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }

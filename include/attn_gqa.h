@@ -479,10 +479,10 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  * head_dim % 8 != 0, kv_dim or strides % 8 != 0, addresses of q, out or the
  * pools that are not 16-byte aligned, more than 16384 sequences, a capacity of
  * more than 2^24 positions, or total_rows * n_heads > 2^30.
- * Kernels: head_dim 64 and 128 with pages of whole 8-row groups run on the
- * tensor cores (tcgen05); calls of about one row a sequence (total_rows <=
- * n_seqs) with H/G <= 16 on a kernel that streams K and V; every other
- * layout on warp-level products. Results lie within the same bounds.
+ * Kernels: pages of whole 8-row groups (page_rows % 8 == 0) run on the tensor
+ * cores (tcgen05) or, for about one row a sequence (total_rows <= n_seqs) with
+ * H/G <= 16, on a kernel that streams K and V; other pages on warp-level
+ * products.  Results lie within the same bounds.
  */
 ATTN_API size_t attn_batch_paged_workspace_bytes(uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim);
 ATTN_API int attn_batch_paged(const void *q, const void *k_pages, const void *v_pages, void *out, attn_dtype_t dtype,

@@ -283,6 +283,20 @@ def test_many_rows_with_masks_and_maps(cuda_lib, kw):
     check(cuda_lib, b, str(kw), **kw)
 
 
+@pytest.mark.parametrize("H,G,D,page_rows,dtype", [(8, 2, 8, 16, F16), (6, 2, 40, 64, BF16), (8, 4, 56, 8, F16),
+                                                   (8, 2, 72, 64, BF16), (16, 4, 96, 16, F16), (5, 1, 96, 32, BF16),
+                                                   (128, 1, 120, 64, F16), (40, 8, 80, 128, BF16)])
+def test_many_rows_other_head_dims(cuda_lib, H, G, D, page_rows, dtype):
+    """Head dimensions between the tile widths, chunks and single tokens; NaN between the rows of the pools."""
+    for new, kv in ((LONG["new"], LONG["kv"]), ([1, 0, 1, 1, 1], [2500, 9, 1, 700, 65])):
+        b = Batch(new, kv, H, G, D, page_rows, dtype, seed=H + D, pad=2, kv_dim=G * D + 16)
+        b.k[:, G * D:] = float("nan")
+        b.v[:, G * D:] = float("nan")
+        check(cuda_lib, b, "H%d G%d D%d" % (H, G, D))
+        if D > 64:
+            check(cuda_lib, b, "capped", softcap=20.0, window=150)
+
+
 def test_many_rows_repeat_bits(cuda_lib):
     b = Batch(LONG["new"], LONG["kv"], 32, 8, 128, 64, BF16, seed=22)
     obj = b.object(cuda_lib)
