@@ -122,6 +122,7 @@ struct __align__(1024) TcSmem {
   uint64_t o_ready;               // the piece's last P V has completed
   uint64_t o_free;                // O has been read
   uint64_t drain[2];
+  unsigned char out[4][32 * 128];  // [row quarter]: 64 columns of its rows on their way out, 128-byte swizzle
   float chain[kChain][kTcRows];
   float2 stat[kDescs][2][kTcRows];  // [piece % kDescs][group][row]: reference, sum
   int4 row[256];               // each softmax thread's own row: window [x, y), position z, slope w (as float bits)
@@ -883,55 +884,99 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (s0.y != 0.f) l_row += s0.y * ex2(s0.x - m_fin);
       if (s1.y != 0.f) l_row += s1.y * ex2(s1.x - m_fin);
       const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
-      T* dst = nullptr;
+      long long dst = 0;  // the row's first element of the output
       if (busy) {
         const int f = d.first_row + min(r, d.rows - 1), t = f / a.gs, h = d.g * a.gs + (f - t * a.gs);
-        dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * hd;
+        dst = (long long)(d.row0 + t) * a.out_stride + (long long)h * hd;
       }
       const bool whole = d.whole;
-      const int pr = rank * kTcRows + r;  // row of the item
+      const int pr = rank * kTcRows + r, rows_here = d.rows - 32 * qd;  // row of the item; rows of this warp
       constexpr long long kSlotFloats = (long long)L::rows * (D + 2);
-      float* part = a.partial + (2ll * unit + d.slot) * kSlotFloats + pr * D;
-      auto put = [&](const float (&v)[kCols], int c, float mul, bool empty) {  // columns of the row, rounded
+      // Partial slots hold four columns of all rows, then the next four, so a warp's accesses are consecutive.
+      float* part = a.partial + (2ll * unit + d.slot) * kSlotFloats + 4 * pr;
+      unsigned char* stage = sm.out[qd];
+      // 16 columns of the row, rounded.
+      auto round16 = [&](const float* v, float mul, bool empty, uint32_t* w) {
 #pragma unroll
-        for (int e = 0; e < kCols; e += 8) {
-          uint32_t w[4];
+        for (int e = 0; e < kCols; e += 2) w[e >> 1] = empty ? 0u : pack_pair<T>(v[e] * mul, v[e + 1] * mul);
+      };
+      auto to_stage = [&](const uint32_t* w, int c) {  // columns [16 c, +16) of the 64
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = empty ? 0u : pack_pair<T>(v[e + 2 * k] * mul, v[e + 2 * k + 1] * mul);
-          if (kCols * c + e < hd) *reinterpret_cast<uint4*>(dst + kCols * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int u = 0; u < 2; ++u)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + 16 * ((2 * c + u) ^ (lane & 7))) =
+              make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+      };
+      // The 64 columns from col0 on, eight lanes a row: a lane a row would touch 32 lines a store (prompt of 8192: 469
+      // us so, 452 this way).
+      auto from_stage = [&](int col0) {
+        __syncwarp();
+        const int u = lane & 7;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = 4 * k + (lane >> 3);
+          const long long to = __shfl_sync(0xffffffffu, dst, row);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + 16 * (u ^ (row & 7)));
+          if (row < rows_here && col0 + 8 * u < hd)
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to + col0 + 8 * u) = v;
         }
+        __syncwarp();
+      };
+      auto read16 = [&](int c, float* v) {
+        uint32_t o[32];
+        tc::tmem_ld16(o_col + kCols * c, o);
+        tc::tmem_ld_wait();
+        tc::reg_fence16(o);
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) v[e] = __uint_as_float(o[e]);
+      };
+      auto free_o = [&] {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_leader<PAIR>(&sm.o_free);
       };
       wait(&sm.o_ready, x);
       tc::fence_after_sync();
+      if (!busy) {
+        free_o();
+      } else if (whole) {
+        float v[kCols];
+        uint32_t w[8], held[D == 128 ? 32 : 1];  // columns 64 on wait in registers, so O is free before any store
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        uint32_t o[32];
-        if (busy) {
-          tc::tmem_ld16(o_col + kCols * c, o);
-          tc::tmem_ld_wait();
-          tc::reg_fence16(o);
+        for (int c = 0; c < 4; ++c) {
+          read16(c, v);
+          round16(v, inv, l_row == 0.f, w);
+          to_stage(w, c);
         }
-        if (c == kChunks - 1) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) arrive_leader<PAIR>(&sm.o_free);
-        }
-        if (store) {
-          if (whole) {
-            float v[kCols];
+        if constexpr (D == 128) {
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) v[e] = __uint_as_float(o[e]);
-            put(v, c, inv, l_row == 0.f);
-          } else {
+          for (int c = 0; c < 4; ++c) {
+            read16(4 + c, v);
+            round16(v, inv, l_row == 0.f, held + 8 * c);
+          }
+        }
+        free_o();
+        from_stage(0);
+        if constexpr (D == 128) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) to_stage(held + 8 * c, c);
+          from_stage(64);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          float v[kCols];
+          read16(c, v);
+          if (c == kChunks - 1) free_o();
+          if (store) {
 #pragma unroll
             for (int e = 0; e < kCols; e += 4)
-              *reinterpret_cast<uint4*>(part + kCols * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<float4*>(part + (kCols * c + e) * L::rows) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
           }
         }
       }
       if (!whole && busy) {
         const int first = d.first, last = d.last, slot0 = d.slot0;
-        const long long ml_off = (long long)L::rows * D + 2 * pr - (long long)pr * D;
+        const long long ml_off = (long long)L::rows * D - 2 * pr;
         if (store) *reinterpret_cast<float2*>(part + ml_off) = make_float2(m_fin, l_row);
         __syncwarp();
         unsigned seen = 0;
@@ -941,40 +986,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         seen = __shfl_sync(0xffffffffu, seen, 0);
         if (seen == (unsigned)(last - first)) {
           if (lane == 0) *counter = 0u;  // for the next call
-          if (store) {
-            const float* row0 = a.partial + (2ll * first + slot0) * kSlotFloats + pr * D;
-            const float* row1 = a.partial + 2ll * first * kSlotFloats + pr * D;  // block c > first: + 2 (c - first) slots
-            float m_all = -INFINITY, l_all = 0.f;
-            for (int c = first; c <= last; ++c) {
+          const float* row0 = a.partial + (2ll * first + slot0) * kSlotFloats + 4 * pr;
+          const float* row1 = a.partial + 2ll * first * kSlotFloats + 4 * pr;  // block c > first: + 2 (c - first) slots
+          float m_all = -INFINITY, l_all = 0.f;
+          for (int c = first; store && c <= last; ++c) {
+            const float* q = c == first ? row0 : row1 + 2ll * (c - first) * kSlotFloats;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
+            if (ml.y == 0.f) continue;  // none of the row's keys
+            const float mn = fmaxf(m_all, ml.x);
+            l_all = (l_all == 0.f ? 0.f : l_all * ex2(m_all - mn)) + ml.y * ex2(ml.x - mn);
+            m_all = mn;
+          }
+          const float inv_all = l_all == 0.f ? 0.f : 1.f / l_all;
+#pragma unroll 1
+          for (int k = 0; k < kChunks; ++k) {
+            float acc[kCols];
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+            for (int c = first; store && c <= last; ++c) {
               const float* q = c == first ? row0 : row1 + 2ll * (c - first) * kSlotFloats;
               const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
-              if (ml.y == 0.f) continue;  // none of the row's keys
-              const float mn = fmaxf(m_all, ml.x);
-              l_all = (l_all == 0.f ? 0.f : l_all * ex2(m_all - mn)) + ml.y * ex2(ml.x - mn);
-              m_all = mn;
-            }
-            const float inv_all = l_all == 0.f ? 0.f : 1.f / l_all;
-#pragma unroll 1
-            for (int k = 0; k < kChunks; ++k) {
-              float acc[kCols];
+              if (ml.y == 0.f) continue;
+              const float f = ex2(ml.x - m_all);
 #pragma unroll
-              for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-              for (int c = first; c <= last; ++c) {
-                const float* q = c == first ? row0 : row1 + 2ll * (c - first) * kSlotFloats;
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
-                if (ml.y == 0.f) continue;
-                const float f = ex2(ml.x - m_all);
-#pragma unroll
-                for (int e = 0; e < kCols; e += 4) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(q + kCols * k + e));
-                  acc[e] = fmaf(v.x, f, acc[e]);
-                  acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
-                  acc[e + 2] = fmaf(v.z, f, acc[e + 2]);
-                  acc[e + 3] = fmaf(v.w, f, acc[e + 3]);
-                }
+              for (int e = 0; e < kCols; e += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(q + (kCols * k + e) * L::rows));
+                acc[e] = fmaf(v.x, f, acc[e]);
+                acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
+                acc[e + 2] = fmaf(v.z, f, acc[e + 2]);
+                acc[e + 3] = fmaf(v.w, f, acc[e + 3]);
               }
-              put(acc, k, inv_all, l_all == 0.f);
             }
+            uint32_t w[8];
+            round16(acc, inv_all, l_all == 0.f, w);
+            to_stage(w, k & 3);
+            if ((k & 3) == 3) from_stage(16 * (k - 3));
           }
         }
       }
