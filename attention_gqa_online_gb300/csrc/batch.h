@@ -16,6 +16,9 @@ namespace attn {
 struct FastDiv {
   uint32_t d, mul, shift;
 };
+#ifdef __CUDACC__
+__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) { return (n + __umulhi(n, f.mul)) >> f.shift; }
+#endif
 inline FastDiv fast_div(uint32_t d) {
   FastDiv f{d, 0, 0};
   while ((1ull << f.shift) < d) ++f.shift;
@@ -98,6 +101,7 @@ struct BatchArgs {
   int page_rows, num_pages, max_blocks, capacity;
   int window;  // 0 = none
   float scale, softcap;
+  FastDiv by_gs, by_page;  // by gs and page_rows; set by launch_batch_paged
 };
 // Sequences of a batch at most (the plan keeps one count each in shared memory).
 constexpr int kMaxBatchSeqs = 16384;

@@ -80,7 +80,7 @@ struct __align__(1024) DecodeSmem {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     batch_decode_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
                         const int box_rows) {
   using S = DecodeSmem<D>;
   constexpr bool kHalf = std::is_same<T, __half>::value;
@@ -136,9 +136,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Pool rows of the page parts, 32 at a time (one a lane), read at least 32 parts ahead.
       auto rows_of = [&](int q0) {
         const int q = q0 + lane, key = key0 + q * box_rows;
-        if (q >= n * parts || key >= hi || key + box_rows <= lo) return outside;
-        const uint32_t pg = table[key / a.page_rows];
-        return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key % a.page_rows : -1;
+        const bool seen = q < n * parts && key < hi && key + box_rows > lo;
+        const int col = seen ? plan::page_of(a, key) : 0;
+        const uint32_t pg = table[col];  // (no branch around it: two such reads overlap)
+        return !seen ? outside : pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
       };
       int now = rows_of(0), next = n * parts > 32 ? rows_of(32) : outside;
       for (int i = 0; i < n; ++i, ++J) {
@@ -159,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(2 * S::tile_bytes));
         __syncwarp();
         unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + chunk * kChunkBytes;
-        // V rows of a fetched part that lie outside the windows are replaced by zeros, row by row (0 * NaN).
+        // V rows of a fetched part that lie outside the windows are replaced by zeros (0 * NaN), by eights or single
+        // rows.
         const bool edge = is_v && row != outside && (key < lo || key + box_rows > hi);
         if (my_part && !edge) tma_load_3d(dst + lane * box_rows * 128, tm, 64 * chunk, g, row, &sm.full[st]);
         unsigned edges = __ballot_sync(0xffffffffu, edge);
@@ -167,9 +169,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int e = __ffs(edges) - 1;
           edges &= edges - 1;
           const int row_e = __shfl_sync(0xffffffffu, row, e), key_e = __shfl_sync(0xffffffffu, key, e);
-          for (int r = lane; r < box_rows; r += 32) {
-            const int y = key_e + r >= lo && key_e + r < hi ? row_e + r : outside;
-            tma_load_3d(dst + (e * box_rows + r) * 128, &tm_v1, 64 * chunk, g, y, &sm.full[st]);
+          const int key_8 = key_e + 8 * lane;  // eight rows a lane; those that are not all of one kind, row by row
+          const bool inside = key_8 >= lo && key_8 + 8 <= hi, outer = key_8 + 8 <= lo || key_8 >= hi;
+          if (8 * lane < box_rows && (inside || outer)) {
+            const int y = inside ? row_e + 8 * lane : outside;
+            tma_load_3d(dst + (e * box_rows + 8 * lane) * 128, &tm_v8, 64 * chunk, g, y, &sm.full[st]);
+          }
+          unsigned mixed = __ballot_sync(0xffffffffu, 8 * lane < box_rows && !inside && !outer);
+          while (mixed) {
+            const int r = 8 * (__ffs(mixed) - 1) + lane;
+            mixed &= mixed - 1;
+            if (lane < 8) {
+              const int y = key_e + r >= lo && key_e + r < hi ? row_e + r : outside;
+              tma_load_3d(dst + (e * box_rows + r) * 128, &tm_v1, 64 * chunk, g, y, &sm.full[st]);
+            }
           }
         }
       }
@@ -198,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = more ? min(kRows, p.q.q_len * a.gs - first_row) : 0;
       if (more && p.t1 == p.t0) {  // rows without keys
         for (int r = 0; r < rows; ++r) {
-          const int f = first_row + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+          const int f = first_row + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
           T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * a.D;
           if (lane < a.D / 8) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -238,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)(rows * a.D * 2));
       __syncwarp();
       if (lane < rows) {
-        const int f = first_row + lane, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+        const int f = first_row + lane, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
         bulk_g2s(&sm.q[x & 1][lane * S::q_stride],
                  static_cast<const T*>(a.q) + (long long)(p.q.row0 + t) * a.q_stride + (long long)h * a.D, a.D * 2,
                  &sm.q_ready[x & 1]);
@@ -273,12 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     float slope[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = lr + 8 * e, f = d.first_row + min(r, rows - 1), t = f / a.gs;
+      const int r = lr + 8 * e, f = d.first_row + min(r, rows - 1), t = plan::token_of(a, f);
       const plan::SeqInfo q{d.row0, d.q_len, d.len, d.pfx};
       lo[e] = plan::row_lo(a, q, t);
       hi[e] = r < rows ? plan::row_hi(q, t) : 0;
       pos[e] = d.len - d.q_len + t;
-      slope[e] = a.slopes != nullptr ? -kLog2e * a.slopes[d.g * a.gs + f % a.gs] : 0.f;
+      slope[e] = a.slopes != nullptr ? -kLog2e * a.slopes[d.g * a.gs + f - t * a.gs] : 0.f;
     }
     const int lo_max = d.lo_max, hi_min = rows < kRows ? 0 : d.hi_min;
     wait(&sm.q_ready[x & 1], x >> 1);
@@ -458,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto store = [&]() {
       const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
-      const int f = d.first_row + r, t = f / a.gs, h = d.g * a.gs + f % a.gs;
+      const int f = d.first_row + r, t = plan::token_of(a, f), h = d.g * a.gs + f - t * a.gs;
       T* dst = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * a.D + c0;
       uint32_t w[4];
 #pragma unroll
@@ -515,11 +528,12 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
   // K and V: [rows][G][head_dim]; columns past the head (head_dim < D) arrive as zeros.
   const uint64_t dims[3] = {(uint64_t)a.D, (uint64_t)a.G, (uint64_t)a.num_pages * a.page_rows};
   const uint64_t strides[2] = {(uint64_t)a.D * 2, (uint64_t)a.kv_dim * 2};
-  const uint32_t box[3] = {64, 1, (uint32_t)box_rows}, one_row[3] = {64, 1, 1};
-  CUtensorMap tm_k, tm_v, tm_v1;  // 16-bit elements are only moved: one element type serves both
+  const uint32_t box[3] = {64, 1, (uint32_t)box_rows}, one_row[3] = {64, 1, 1}, eight[3] = {64, 1, 8};
+  CUtensorMap tm_k, tm_v, tm_v1, tm_v8;  // 16-bit elements are only moved: one element type serves both
   const int l2 = kv_l2_bytes(a.D);
   if (!make_tmap(&tm_k, a.k_pages, 3, dims, strides, box, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v, a.v_pages, 3, dims, strides, box, true, kSwizzle128, l2) ||
+      !make_tmap(&tm_v8, a.v_pages, 3, dims, strides, eight, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v1, a.v_pages, 3, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
   const void* kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D>);
@@ -527,7 +541,7 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;
   ScoreMap sc = score_map(a);
-  void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &box_rows};
+  void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &tm_v8, &box_rows};
   return launch_pdl(kern, dim3(blocks), dim3(kThreads), smem, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

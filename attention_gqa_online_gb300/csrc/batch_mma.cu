@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
     // Q block; rows and columns past the data are zeros.
     for (int i = tid; i < kRows * kUnits; i += kThreads) {
       const int r = i / kUnits, u = i % kUnits;
-      const int f = p.b * kRows + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+      const int f = p.b * kRows + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
       const bool ok = r < rows && 8 * u < a.D;
       const T* src = static_cast<const T*>(a.q);
       if (ok) src += (long long)(p.q.row0 + t) * a.q_stride + (long long)h * a.D + 8 * u;
@@ -93,11 +93,11 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 16 * warp + (lane >> 2) + 8 * e;
-      const int f = p.b * kRows + min(r, rows - 1), t = f / a.gs;
+      const int f = p.b * kRows + min(r, rows - 1), t = plan::token_of(a, f);
       lo[e] = plan::row_lo(a, p.q, t);
       hi[e] = r < rows ? plan::row_hi(p.q, t) : 0;
       pos[e] = p.q.len - p.q.q_len + t;
-      slope[e] = a.slopes != nullptr ? a.slopes[p.g * a.gs + f % a.gs] * kLog2e : 0.f;
+      slope[e] = a.slopes != nullptr ? a.slopes[p.g * a.gs + f - t * a.gs] * kLog2e : 0.f;
     }
     float o[DP / 8][4];
 #pragma unroll
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
       if (r >= rows) continue;
       if (p.whole) {
         const float inv = l[x] == 0.f ? 0.f : 1.f / l[x];
-        const int f = p.b * kRows + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+        const int f = p.b * kRows + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
         T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * a.D;
 #pragma unroll
         for (int c = 0; c < DP / 8; ++c) {
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kJoinThreads) batch_combine_kernel(const Batch
       m = mn;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int f = sp.blk * kRows + r, t = f / a.gs, h = sp.g * a.gs + f % a.gs;
+    const int f = sp.blk * kRows + r, t = plan::token_of(a, f), h = sp.g * a.gs + f - t * a.gs;
     T* dst = static_cast<T*>(a.out) + (long long)(q.row0 + t) * a.out_stride + (long long)h * a.D + col;
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
   }
@@ -298,6 +298,8 @@ size_t batch_workspace_bytes(int head_dim, int sm_count) {
 }
 
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s) {
+  a.by_gs = fast_div((uint32_t)a.gs);
+  a.by_page = fast_div((uint32_t)a.page_rows);
   a.arrived = static_cast<unsigned*>(workspace);
   a.split = reinterpret_cast<BatchSplit*>(a.arrived + 4 * ((sm_count + 7) / 8 * 8));
   a.partial = reinterpret_cast<float*>(a.split + 2 * sm_count);

@@ -41,6 +41,10 @@ __device__ __forceinline__ SeqInfo load_seq(const BatchArgs& a, int s) {
   return q;
 }
 
+// Token of flattened row f, and the page of a position.
+__device__ __forceinline__ int token_of(const BatchArgs& a, int f) { return (int)divide((uint32_t)f, a.by_gs); }
+__device__ __forceinline__ int page_of(const BatchArgs& a, int key) { return (int)divide((uint32_t)key, a.by_page); }
+
 // Keys [lo, hi) of the row of token t (empty when hi <= lo).
 __device__ __forceinline__ int row_hi(const SeqInfo& q, int t) { return max(q.len - q.q_len + t + 1, q.pfx); }
 __device__ __forceinline__ int row_lo(const BatchArgs& a, const SeqInfo& q, int t) {
@@ -60,8 +64,8 @@ __device__ __forceinline__ int row_blocks(const BatchArgs& a, const SeqInfo& q) 
 
 template <int ROWS, int KEYS>
 __device__ __forceinline__ BlockKeys block_keys(const BatchArgs& a, const SeqInfo& q, int b) {
-  const int t0 = (b * ROWS) / a.gs;
-  const int t1 = (min(q.q_len * a.gs, (b + 1) * ROWS) - 1) / a.gs;
+  const int t0 = token_of(a, b * ROWS);
+  const int t1 = token_of(a, min(q.q_len * a.gs, (b + 1) * ROWS) - 1);
   BlockKeys k;
   k.lo_min = row_lo(a, q, t0);
   k.lo_max = row_lo(a, q, t1);

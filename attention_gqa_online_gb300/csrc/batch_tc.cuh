@@ -42,8 +42,8 @@
 //
 // Rows of V that lie in a fetched page part but outside the block's windows
 // hold whatever the page holds (0 * NaN would reach every row): such parts are
-// fetched row by row, those rows from outside the pool, as zeros. The same
-// rows of K only make scores that are masked.
+// fetched eight rows or one row at a time, those rows from outside the pool, as
+// zeros. The same rows of K only make scores that are masked.
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
 // MMAs, frees its tensor memory and leaves the status word set.
@@ -287,7 +287,7 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uin
 template <typename T, int D, int MODE, bool PAIR, bool FULL>
 __global__ void __launch_bounds__(kTcThreads, 1)
     batch_tc_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
                     const __grid_constant__ CUtensorMap tm_q, const int box_rows, const int q_box) {
   using L = TcLayout<D, PAIR>;
   const int hd = FULL ? D : a.D;  // columns of a head
@@ -361,32 +361,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // time (one a lane), at least 32 parts ahead: a table read is a trip to L2, longer than a tile's products.
     const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
     struct Parts {
-      int parts;             // page parts of a tile held here
+      int shift;             // log2 of the page parts of a tile held here
       int n, lo, hi, key0;   // tiles; the windows' ends; first key held here of tile 0
       const uint32_t* table;
       int now, next;         // pool rows of 32 parts, and of the 32 after
     };
     auto rows_of = [&](const Parts& w, int q0) {
-      const int q = q0 + lane, key = w.key0 - (q / w.parts) * kTcKeys + (q % w.parts) * box_rows;
-      if (q >= w.n * w.parts || key >= w.hi || key + box_rows <= w.lo) return outside;
-      const uint32_t pg = w.table[key / a.page_rows];
-      return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key % a.page_rows : -1;
+      const int q = q0 + lane, i = q >> w.shift, key = w.key0 - i * kTcKeys + (q - (i << w.shift)) * box_rows;
+      const bool seen = i < w.n && key < w.hi && key + box_rows > w.lo;
+      const int col = seen ? plan::page_of(a, key) : 0;
+      const uint32_t pg = w.table[col];  // (no branch around it: two such reads overlap)
+      return !seen ? outside : pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
     };
     auto open_parts = [&](int keys, int n, int lo, int hi, int key0, int seq) {
-      Parts w{keys / box_rows, n, lo, hi, key0, a.block_table + (long long)seq * a.max_blocks, 0, 0};
+      Parts w{__ffs(keys) - __ffs(box_rows), n, lo, hi, key0, a.block_table + (long long)seq * a.max_blocks, 0, 0};
       w.now = rows_of(w, 0);
       w.next = rows_of(w, 32);
       return w;
     };
     // Pool row of this lane's part of tile i (tiles in order).
     auto part_row = [&](Parts& w, int i) {
-      const int q0 = i * w.parts;
+      const int q0 = i << w.shift;
       if (i > 0 && q0 % 32 == 0) {
         w.now = w.next;
         w.next = rows_of(w, q0 + 32);
       }
       int row = __shfl_sync(0xffffffffu, w.now, (q0 + lane) % 32);
-      if (lane >= w.parts) row = outside;
+      if (lane >> w.shift) row = outside;
       if (row < 0) {  // a page outside the pool
         record_status(a.status, ATTN_ERR_INVALID_ARG);
         row = outside;
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
         if (more && p.t1 == p.t0) {  // rows without keys
           for (int r = lane >> 2; r < rows; r += 8) {
-            const int f = first_row + r, t = f / a.gs, h = p.g * a.gs + f % a.gs;
+            const int f = first_row + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
             T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * hd;
             for (int u = lane & 3; u < hd / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             d.hi_max = p.k.hi_max;
             d.tile_last = p.k.kt0 + p.t1 - 1;
             d.n = p.t1 - p.t0;
-            d.pos_min = p.q.len - p.q.q_len + first_row / a.gs;
+            d.pos_min = p.q.len - p.q.q_len + plan::token_of(a, first_row);
           }
           mbar_arrive(&sm.desc_full[x % kDescs]);
         }
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(full, (unsigned)(PAIR ? 2 : 1) * L::q_bytes);
 #pragma unroll
             for (int c = 0; c < L::chunks; ++c)
-              load_3d<PAIR>(sm.q[x & 1] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + first_row / a.gs, bar);
+              load_3d<PAIR>(sm.q[x & 1] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + plan::token_of(a, first_row), bar);
           }
           __syncwarp();
         } else {
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * hd;
           const bool inside = 8 * u < hd;  // columns past the head are zeros
           for (int r = lane / kUnits; r < rows; r += kRowsPer) {
-            const int f = first_row + r, t = f / a.gs;
+            const int f = first_row + r, t = plan::token_of(a, f);
             cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)),
                        src + (long long)t * a.q_stride + (f - t * a.gs) * hd + (inside ? 8 * u : 0), inside ? 16u : 0u);
           }
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!ok) break;
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
           __syncwarp();
-          if (lane < w.parts) {
+          if ((lane >> w.shift) == 0) {
             const uint32_t bar = barrier_of(&sm.k_full[slot]);
 #pragma unroll
             for (int c = 0; c < L::chunks; ++c)
@@ -532,10 +533,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.v_full[slot], (unsigned)(PAIR ? 2 : 1) * L::v_bytes);
           __syncwarp();
           const uint32_t bar = barrier_of(&sm.v_full[slot]);
-          // A part that reaches outside the block's windows goes row by row: what the page holds there (0 * NaN would
+          // A part that reaches outside the block's windows goes by eights or single rows: what the page holds there (0 * NaN would
           // reach every row) is replaced by zeros from outside the pool.
           const bool edge = row != outside && (key < w.lo || key + box_rows > w.hi);
-          if (lane < w.parts && !edge) {
+          if ((lane >> w.shift) == 0 && !edge) {
 #pragma unroll
             for (int c = 0; c < L::v_chunks; ++c)
               load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + lane * box_rows * 128, &tm_v, col + 64 * c, g, row,
@@ -546,12 +547,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int p = __ffs(edges) - 1;
             edges &= edges - 1;
             const int row_p = __shfl_sync(0xffffffffu, row, p), key_p = __shfl_sync(0xffffffffu, key, p);
-            for (int r = lane; r < box_rows; r += 32) {
-              const int y = key_p + r >= w.lo && key_p + r < w.hi ? row_p + r : outside;
+            const int key_8 = key_p + 8 * lane;  // eight rows a lane; those that are not all of one kind, row by row
+            const bool inside = key_8 >= w.lo && key_8 + 8 <= w.hi, outer = key_8 + 8 <= w.lo || key_8 >= w.hi;
+            if (8 * lane < box_rows && (inside || outer)) {
+              const int y = inside ? row_p + 8 * lane : outside;
 #pragma unroll
               for (int c = 0; c < L::v_chunks; ++c)
-                load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + (p * box_rows + r) * 128, &tm_v1, col + 64 * c, g, y,
-                                         bar);
+                load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + (p * box_rows + 8 * lane) * 128, &tm_v8, col + 64 * c, g,
+                                      y, bar);
+            }
+            unsigned mixed = __ballot_sync(0xffffffffu, 8 * lane < box_rows && !inside && !outer);
+            while (mixed) {
+              const int r = 8 * (__ffs(mixed) - 1) + lane;
+              mixed &= mixed - 1;
+              if (lane < 8) {
+                const int y = key_p + r >= w.lo && key_p + r < w.hi ? row_p + r : outside;
+#pragma unroll
+                for (int c = 0; c < L::v_chunks; ++c)
+                  load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + (p * box_rows + r) * 128, &tm_v1, col + 64 * c, g, y,
+                                        bar);
+              }
             }
           }
         }
@@ -643,12 +658,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       int4 info = make_int4(0, 0, 0, 0);
       if (r < d.rows) {
-        const int f = d.first_row + r, t = f / a.gs;
+        const int f = d.first_row + r, t = plan::token_of(a, f);
         const plan::SeqInfo q{d.row0, d.q_len, d.len, d.pfx};
         info.x = plan::row_lo(a, q, t);
         info.y = plan::row_hi(q, t);
         info.z = d.len - d.q_len + t;
-        if (MODE != 0 && a.slopes != nullptr) info.w = __float_as_int(-kLog2e * a.slopes[d.g * a.gs + f % a.gs]);
+        if (MODE != 0 && a.slopes != nullptr) info.w = __float_as_int(-kLog2e * a.slopes[d.g * a.gs + f - t * a.gs]);
       }
       sm.row[128 * grp + r] = info;  // read on the tiles that need it: kept in registers it would spill scores
       for (int i = (J & 1) ^ grp; i < n; i += 2) {
@@ -886,7 +901,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float inv = l_row == 0.f ? 0.f : 1.f / l_row;
       long long dst = 0;  // the row's first element of the output
       if (busy) {
-        const int f = d.first_row + min(r, d.rows - 1), t = f / a.gs, h = d.g * a.gs + (f - t * a.gs);
+        const int f = d.first_row + min(r, d.rows - 1), t = plan::token_of(a, f), h = d.g * a.gs + (f - t * a.gs);
         dst = (long long)(d.row0 + t) * a.out_stride + (long long)h * hd;
       }
       const bool whole = d.whole;
@@ -1049,10 +1064,12 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   const uint64_t strides[2] = {(uint64_t)(FULL ? a.kv_dim : a.D) * 2, (uint64_t)a.kv_dim * 2};
   if (PAIR && box_rows > 64) box_rows = 64;  // a block holds 64 keys of a K tile
   const uint32_t box[3] = {64, FULL ? (uint32_t)box_rows : 1, (uint32_t)box_rows}, one_row[3] = {64, 1, 1};
-  CUtensorMap tm_k, tm_v, tm_v1;  // 16-bit elements are only moved: one element type serves both
+  const uint32_t eight[3] = {64, FULL ? 8u : 1u, 8};
+  CUtensorMap tm_k, tm_v, tm_v1, tm_v8;  // 16-bit elements are only moved: one element type serves both
   const int l2 = kv_l2_bytes(a.D);
   if (!make_tmap(&tm_k, a.k_pages, rank, dims, strides, box, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v, a.v_pages, rank, dims, strides, box, true, kSwizzle128, l2) ||
+      !make_tmap(&tm_v8, a.v_pages, rank, dims, strides, eight, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v1, a.v_pages, rank, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
   // Q: [rows][H][D]; a row block is one box of gs heads x 128/gs tokens when gs divides 128.
@@ -1075,7 +1092,7 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   const size_t smem = sizeof(TcSmem<D, PAIR>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;
-  void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &tm_q, &box_rows, &q_box};
+  void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &tm_v8, &tm_q, &box_rows, &q_box};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kTcThreads);

@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) { return (n + __umulhi(n, f.mul)) >> f.shift; }
 
 // Bound by HBM (each element in and out once; the table's rows, shared by the
 // heads, come from L2): 8192 rows of 40 heads of 128, bf16, move 172 MB in 29 us,
