@@ -742,6 +742,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                   s[c][e] = __float_as_uint(sc.out_mul * tanh_score(__uint_as_float(s[c][e]) * sc.in_mul));
             }
           }
+          float fold = 0.f;  // to be added to every score of the row
           if (MODE != 0 && a.slopes != nullptr) {
             // slope = -slopes[h] log2 e.  In a tile wholly behind (or ahead of) the rows |p - j| is linear in the column;
             // in one that crosses them, slope |d| is slope d with the sign of slope.
@@ -750,17 +751,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool behind = a.prefix_len == nullptr || key0 + kTcKeys - 1 <= d.pos_min;
             const float step = behind ? -slope : slope, first = step * (float)(key0 - info.z);
             if (behind || key0 >= d.pos_min + (kTcRows - 1) / a.gs + 1) {
+              // What the whole tile shares joins the reference; the rest grows along the row by additions, from an
+              // exact value every 32 columns (at most 15 roundings of a bias within 128 keys).
+              fold = first;
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c) {
+                float b0 = step * (float)(32 * c), b1 = step * (float)(32 * c + 1);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                   float x0 = __uint_as_float(s[c][e]), x1 = __uint_as_float(s[c][e + 1]);
-                  float b0 = step, b1 = step;
-                  fma2(b0, b1, (float)(32 * c + e), (float)(32 * c + e + 1), first, first);
                   fma2(x0, x1, mul, mul, b0, b1);
+                  add2(b0, b1, 2.f * step, 2.f * step);
                   s[c][e] = __float_as_uint(x0);
                   s[c][e + 1] = __float_as_uint(x1);
                 }
+              }
             } else {
 #pragma unroll
               for (int c = 0; c < 4; ++c)
@@ -801,7 +806,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               mx[k] = max3(mx[k], __uint_as_float(s[e >> 5][(e & 31) + 2 * k]),
                            __uint_as_float(s[e >> 5][(e & 31) + 2 * k + 1]));
           const float cf = MODE == 0 ? sc.scale2 : 1.f;
-          const float tmax = cf * max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+          const float tmax = cf * max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) + fold;
 
           // The reference of the tile before (left by the other group), then this tile's.
           // (The first tile of a piece, and warps without rows, wait too, for nothing but order: a group must not get
@@ -813,7 +818,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           sm.chain[j % kChain][r] = m_new;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.chain_bar[qd][j % kChain]);
-          const float neg_m = (m_new == -INFINITY) ? 0.f : -m_new;
+          const float neg_m = (m_new == -INFINITY) ? 0.f : fold - m_new;
 
           // Exponentials run kLag scores ahead of their sum and packing (in place: packed pair k of a chunk replaces
           // its score k, long done), so the special-function unit, 4 cycles an instruction, is never waited for.
