@@ -102,6 +102,7 @@ struct BatchArgs {
   int window;  // 0 = none
   float scale, softcap;
   FastDiv by_gs, by_page;  // by gs and page_rows; set by launch_batch_paged
+  int item_cost;           // what an item takes beyond its tiles, in tiles; set by each kernel's launch
 };
 // Sequences of a batch at most (the plan keeps one count each in shared memory).
 constexpr int kMaxBatchSeqs = 16384;

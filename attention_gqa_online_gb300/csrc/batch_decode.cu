@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Columns of Q past the head stay zeros.
   for (int i = tid; i < 2 * kRows * S::q_stride; i += kThreads) sm.q[0][i] = 0;
   grid_dependency_wait();  // lengths, tables and pages may be the previous kernel's output
-  plan::make_plan<kRows, S::keys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
+  plan::make_plan<kRows, S::keys, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
                                           &sm.start);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
   __syncthreads();
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
       }
     }
-    plan::Walker<kRows, kKeys, kItemCost> walk(a, sm.start);
+    plan::Walker<kRows, kKeys> walk(a, sm.start);
     plan::Piece p;
     while (true) {
       const bool more = walk.next(p) && !*(volatile int*)&sm.abort;
@@ -540,6 +540,7 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
   const size_t smem = sizeof(DecodeSmem<D>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;
+  aa.item_cost = kItemCost;
   ScoreMap sc = score_map(a);
   void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &tm_v8, &box_rows};
   return launch_pdl(kern, dim3(blocks), dim3(kThreads), smem, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
   __shared__ plan::Start start;
   __shared__ long long warp_sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  plan::make_plan<kRows, kKeys, kItemCost, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
+  plan::make_plan<kRows, kKeys, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
   BatchSplit split{};
-  plan::Walker<kRows, kKeys, kItemCost> walk(a, start);
+  plan::Walker<kRows, kKeys> walk(a, start);
   plan::Piece p;
   const uint32_t q_base = smem_u32(sh.q);
   constexpr int kUnits = DP / 8;
@@ -264,7 +264,9 @@ int launch_mma_t(const BatchArgs& a, int blocks, cudaStream_t s) {
   const size_t smem = sizeof(MmaSmem<DP>) > plan_bytes ? sizeof(MmaSmem<DP>) : plan_bytes;
   auto kern = a.softcap > 0.f ? batch_mma_kernel<T, DP, true> : batch_mma_kernel<T, DP, false>;
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return ATTN_ERR_CUDA;
-  kern<<<blocks, kThreads, smem, s>>>(a, sm);
+  BatchArgs b = a;
+  b.item_cost = kItemCost;
+  kern<<<blocks, kThreads, smem, s>>>(b, sm);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

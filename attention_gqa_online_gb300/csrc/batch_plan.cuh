@@ -4,13 +4,14 @@
 // The query rows of sequence s and kv head g are flattened as r = t * gs + j
 // (token t, head g * gs + j) and cut into blocks of ROWS; an item is one
 // (sequence, row block, kv head).  Its keys are the union of its rows'
-// windows, walked in tiles of KEYS.  Every item weighs its tiles plus COST (what
+// windows, walked in tiles of KEYS.  Every item weighs its tiles plus item_cost (what
 // its Q load, epilogue and masked tiles take, in tiles); the weights of all items, laid end to end in (sequence,
 // row block, kv head) order, are cut into equal ranges, one per thread block.  A
 // range boundary inside an item splits its keys: each part is a piece, whose
 // unnormalised output and (max, sum) go to a partial slot, and a second kernel
 // joins the pieces of an item in key order (so results do not depend on the
-// order in which blocks run).
+// order in which blocks run).  An item of at most item_cost tiles is not split:
+// the block of its first unit takes it whole.
 #pragma once
 
 #include <cstdint>
@@ -129,9 +130,8 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 }
 
 // Range of block c when the items weigh `units` in all.
-template <int COST>
-__device__ __forceinline__ long long units_per_block(long long units, int blocks) {
-  return max(quotient(units + blocks - 1, blocks), (long long)(COST + 1));
+__device__ __forceinline__ long long units_per_block(long long units, int blocks, int cost) {
+  return max(quotient(units + blocks - 1, blocks), (long long)(cost + 1));
 }
 __device__ __forceinline__ void set_start(Start* start, int s, int b, long long offset, int w, long long u0, long long per,
                                           long long units) {
@@ -149,7 +149,7 @@ __device__ __forceinline__ void set_start(Start* start, int s, int b, long long 
 // single-token step starts about a microsecond sooner.  Returns false (to every
 // lane) when the batch is too large for it.
 constexpr int kWarpSeqs = 512, kWarpBlocks = 32;
-template <int ROWS, int KEYS, int COST>
+template <int ROWS, int KEYS>
 __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks, Start* start) {
   const int lane = threadIdx.x & 31;
   if (a.n_seqs > kWarpSeqs) return false;
@@ -162,7 +162,7 @@ __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks,
     const int n = row_blocks<ROWS>(a, q);
     nb += n;
     if (nb <= kWarpBlocks)
-      for (int b = 0; b < n; ++b) mine += block_keys<ROWS, KEYS>(a, q, b).nt + COST;
+      for (int b = 0; b < n; ++b) mine += block_keys<ROWS, KEYS>(a, q, b).nt + a.item_cost;
   }
   if (__any_sync(0xffffffffu, nb > kWarpBlocks)) return false;
   mine *= a.G;
@@ -173,7 +173,7 @@ __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks,
     if (lane >= d) upto += o;
   }
   const long long units = __shfl_sync(0xffffffffu, upto, 31);
-  const long long per = units_per_block<COST>(units, blocks), u0 = per * c;
+  const long long per = units_per_block(units, blocks, a.item_cost), u0 = per * c;
   if (lane == 0 && u0 >= units) start->left = 0;
   long long at = upto - mine;
   if (u0 >= at && u0 < upto) {
@@ -182,7 +182,7 @@ __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks,
       const SeqInfo q = load_seq(a, s);
       const int n = row_blocks<ROWS>(a, q);
       for (int b = 0; b < n && !found; ++b) {
-        const int w = block_keys<ROWS, KEYS>(a, q, b).nt + COST;
+        const int w = block_keys<ROWS, KEYS>(a, q, b).nt + a.item_cost;
         found = u0 < at + (long long)w * a.G;
         if (found) set_start(start, s, b, u0 - at, w, u0, per, units);
         at += (long long)w * a.G;
@@ -195,11 +195,11 @@ __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks,
 // The range of thread block `c` of `blocks`.  Every thread of the block calls it;
 // first_block holds n_seqs + 1 ints and warp_sums THREADS/32 values in shared
 // memory.  On return (after its final barrier) *start is valid.
-template <int ROWS, int KEYS, int COST, int THREADS>
+template <int ROWS, int KEYS, int THREADS>
 __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_block, long long* warp_sums, Start* start) {
   const int tid = threadIdx.x;
   if (tid < 32) {
-    const bool done = warp_plan<ROWS, KEYS, COST>(a, c, blocks, start);
+    const bool done = warp_plan<ROWS, KEYS>(a, c, blocks, start);
     if (tid == 0) first_block[0] = done ? 1 : 0;
   }
   __syncthreads();
@@ -244,18 +244,18 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
     for (int i = i0; i < i1; ++i) {
       while (first_block[ss + 1] <= i) ++ss;
       if (have != ss) q = load_seq(a, have = ss);
-      mine += (long long)(block_keys<ROWS, KEYS>(a, q, i - first_block[ss]).nt + COST) * a.G;
+      mine += (long long)(block_keys<ROWS, KEYS>(a, q, i - first_block[ss]).nt + a.item_cost) * a.G;
     }
   }
   long long units;
   const long long upto = block_scan<THREADS>(mine, warp_sums, &units);
-  const long long per = units_per_block<COST>(units, blocks), u0 = per * c;
+  const long long per = units_per_block(units, blocks, a.item_cost), u0 = per * c;
   long long at = upto - mine;
   if (u0 >= at && u0 < upto) {  // this thread's share holds the range's start
     int ss = s;
     for (int i = i0; i < i1; ++i) {
       while (first_block[ss + 1] <= i) ++ss;
-      const int w = block_keys<ROWS, KEYS>(a, load_seq(a, ss), i - first_block[ss]).nt + COST;
+      const int w = block_keys<ROWS, KEYS>(a, load_seq(a, ss), i - first_block[ss]).nt + a.item_cost;
       if (u0 < at + (long long)w * a.G) {
         set_start(start, ss, i - first_block[ss], u0 - at, w, u0, per, units);
         break;
@@ -268,7 +268,7 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
 
 // Walks the pieces of a block's range, in order.  Warps of different roles
 // walk it independently and see the same pieces.
-template <int ROWS, int KEYS, int COST>
+template <int ROWS, int KEYS>
 struct Walker {
   const BatchArgs& a;
   SeqInfo q;
@@ -288,20 +288,21 @@ struct Walker {
   __device__ __forceinline__ bool next(Piece& p, BatchSplit* split = nullptr) {
     while (left > 0) {
       const BlockKeys k = block_keys<ROWS, KEYS>(a, q, b);
-      const long long w = k.nt + COST;
+      const long long w = k.nt + a.item_cost;
       const long long take = min(left, w - x);
       p.q = q;
       p.k = k;
       p.s = s;
       p.b = b;
       p.g = g;
-      p.t0 = (int)max(0ll, x - COST);
-      p.t1 = (int)max(0ll, x + take - COST);
+      const bool one_piece = k.nt <= a.item_cost;
+      p.t0 = one_piece ? 0 : (int)max(0ll, x - a.item_cost);
+      p.t1 = one_piece ? (x == 0 ? k.nt : 0) : (int)max(0ll, x + take - a.item_cost);
       p.slot = index == 0 ? 0 : 1;
       p.whole = p.t0 == 0 && p.t1 == k.nt;
       const bool have = p.t1 > p.t0 || (k.nt == 0 && x == 0);
       if (!p.whole && have) {
-        p.first = (int)quotient(u - x + COST, per);  // the block that holds tile 0
+        p.first = (int)quotient(u - x + a.item_cost, per);  // the block that holds tile 0
         p.last = (int)quotient(u - x + w - 1, per);
         p.slot0 = (long long)p.first * per >= u - x ? 0 : 1;  // is the item the first of its first block's range?
       }

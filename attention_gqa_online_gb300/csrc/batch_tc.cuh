@@ -66,9 +66,10 @@ namespace attn {
 namespace {
 
 constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 512;
-// What a piece takes beyond its tiles, in tiles, at 1, 2, 3: prompt of 8192 (pieces of 1 to 64 tiles) 574, 476, 500 us,
-// mixed batch of short and long chunks 283, 262, 262, long chunks alike 282, 282, 283.
-constexpr int kItemCost = 2;
+// What an item takes beyond its tiles, in tiles; kItemCostRows where a block's rows are no whole tokens (gs does not
+// divide 128) and Q is copied by a warp. At 2, 3, 4, 5: 17 prompts of 512, 32 heads over 8, 123, 110, 99, 99 us; mixed
+// batch of chunks 218, 219, 214, 213; prompt of 8192 alike. At 2, 6, 8, 10 (20 heads over 4): 588, 360, 340, 321.
+constexpr int kItemCost = 4, kItemCostRows = 10;
 constexpr int kDescs = 4;        // piece descriptors in flight
 constexpr int kChain = 4;        // reference maxima in flight
 constexpr int kPColumn = 256, kOColumn = 384;
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) tmem_alloc_all<PAIR>(&sm.tmem_base);
   // Lengths, tables and pages may be the previous kernel's output.
   grid_dependency_wait();
-  plan::make_plan<L::rows, kTcKeys, kItemCost, kTcThreads>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
+  plan::make_plan<L::rows, kTcKeys, kTcThreads>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
   // The plan's scratch is where Q and the K/V tiles land.
   fence_async_smem();
   tc::fence_before_sync();
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tmap(&tm_k);
         if (q_box) prefetch_tmap(&tm_q);
       }
-      plan::Walker<L::rows, kTcKeys, kItemCost> walk(a, sm.start);
+      plan::Walker<L::rows, kTcKeys> walk(a, sm.start);
       plan::Piece p;
       int x = 0, J = 0;
       // A wait that ran out ends the role at once: writing over a descriptor or a slot in use, or arriving twice in one
@@ -1097,6 +1098,7 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   const size_t smem = sizeof(TcSmem<D, PAIR>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;
+  aa.item_cost = q_box ? kItemCost : kItemCostRows;
   void* args[] = {&aa, &sc, &tm_k, &tm_v, &tm_v1, &tm_v8, &tm_q, &box_rows, &q_box};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
