@@ -310,13 +310,14 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
   if (box >= 8) {
-    // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 308
-    // us at 4 query heads a kv head, 313 at 16 (tcgen05 kernel: 326 and 332); 8 sequences of 2048: 16 us against 40.
-    // More heads a kv head would read K and V once for every 16 of them.
+    // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 306
+    // us at 4 query heads a kv head, 312 at 16 (tcgen05 kernel: 323 and 328); heads of 64: 163 (192); 8 sequences of
+    // 2048: 16 us against 41. More heads a kv head would read K and V once for every 16 of them.
     if (a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
     // Pairs of multiprocessors share K and V tiles between 256 rows, where sequences have that many on average. 16
-    // sequences of 4096, 4 heads a kv head of 128, with 32, 128, 256, 512, 1024 rows a kv head: pairs 86, 97, 90, 140,
-    // 239 us, single blocks 84, 98, 113, 185, 327.
+    // sequences of 4096, 4 heads a kv head of 128, with 32, 128, 256, 512, 1024 rows a kv head: pairs 73, 77, 77, 121,
+    // 211 us, single blocks 78, 82, 98, 167, 299; but with 16 rows at 4096 69 against 67, at 300 (64 sequences) 66
+    // against 34.
     if (a.D > 64 && 128 % a.gs == 0 && sm_count % 2 == 0 && (long long)a.total_rows * a.gs >= 256ll * a.n_seqs)
       return a.D == 128 ? launch_batch_tc_pair(a, dtype, sm_count, box, s)
                         : launch_batch_tc_part_pair(a, dtype, sm_count, box, s);

@@ -122,12 +122,14 @@ struct __align__(1024) TcSmem {
   uint64_t stat_bar[4][kDescs][2];  // [row quarter][piece % kDescs][group]
   uint64_t o_ready;               // the piece's last P V has completed
   uint64_t o_free;                // O has been read
+  uint64_t join_bar[kDescs];      // [piece % kDescs] whether this block joins the piece's item is known
   uint64_t drain[2];
   unsigned char out[4][32 * 128];  // [row quarter]: 64 columns of its rows on their way out, 128-byte swizzle
   float chain[kChain][kTcRows];
   float2 stat[kDescs][2][kTcRows];  // [piece % kDescs][group][row]: reference, sum
   int4 row[256];               // each softmax thread's own row: window [x, y), position z, slope w (as float bits)
   PieceDesc desc[kDescs];
+  int joins[kDescs];
   plan::Start start;
   long long warp_sums[kTcThreads / 32];
   uint32_t tmem_base;
@@ -319,6 +321,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (lane < kDescs) {
       mbar_init(&sm.desc_full[lane], 1);
+      mbar_init(&sm.join_bar[lane], 1);
       mbar_init(&sm.desc_free[lane], rank == 0 ? 14 : 13);  // V, (first block) P V, eight softmax and four output warps
     }
     if (lane < 16) mbar_init(&sm.chain_bar[lane >> 2][lane & 3], 1);
@@ -995,51 +998,98 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
+      // Pieces of at most 32 rows are the first warp's, but all four warps join them, each some of the columns (4
+      // new tokens behind 16000, 4 heads a kv head, items of 19 pieces: 100 us with one warp, 32
+      // with four).
+      const bool shared_join = !whole && d.rows > 0 && d.rows <= 32;
+      const int first = d.first, last = d.last;
+      bool join = false;
       if (!whole && busy) {
-        const int first = d.first, last = d.last, slot0 = d.slot0;
-        const long long ml_off = (long long)L::rows * D - 2 * pr;
-        if (store) *reinterpret_cast<float2*>(part + ml_off) = make_float2(m_fin, l_row);
+        if (store) *reinterpret_cast<float2*>(part + (long long)L::rows * D - 2 * pr) = make_float2(m_fin, l_row);
         __syncwarp();
         unsigned seen = 0;
         unsigned* counter = a.arrived + ((PAIR ? 2 * first + rank : first) * 4 + qd);
         if (lane == 0)  // releases this warp's rows, acquires the other pieces'
           asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(counter) : "memory");
         seen = __shfl_sync(0xffffffffu, seen, 0);
-        if (seen == (unsigned)(last - first)) {
-          if (lane == 0) *counter = 0u;  // for the next call
-          const float* row0 = a.partial + (2ll * first + slot0) * kSlotFloats + 4 * pr;
-          const float* row1 = a.partial + 2ll * first * kSlotFloats + 4 * pr;  // block c > first: + 2 (c - first) slots
-          float m_all = -INFINITY, l_all = 0.f;
-          for (int c = first; store && c <= last; ++c) {
-            const float* q = c == first ? row0 : row1 + 2ll * (c - first) * kSlotFloats;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
-            if (ml.y == 0.f) continue;  // none of the row's keys
-            const float mn = fmaxf(m_all, ml.x);
-            l_all = (l_all == 0.f ? 0.f : l_all * ex2(m_all - mn)) + ml.y * ex2(ml.x - mn);
+        join = seen == (unsigned)(last - first);
+        if (join && lane == 0) *counter = 0u;  // for the next call
+      }
+      if (qd == 0) {
+        if (lane == 0) {
+          sm.joins[x % kDescs] = join ? 1 : 0;
+          mbar_arrive(&sm.join_bar[x % kDescs]);
+        }
+      } else if (shared_join) {
+        wait(&sm.join_bar[x % kDescs], x / kDescs);
+        __syncwarp();
+        join = *(volatile int*)&sm.joins[x % kDescs] != 0;
+      }
+      if (join) {
+        const int jr = shared_join ? lane : r, jpr = rank * kTcRows + jr;  // row of the block and of the item
+        const bool mine = jr < d.rows;
+        const long long ml_off = (long long)L::rows * D - 2 * jpr;
+        const int slot0 = d.slot0;
+        const float* row0 = a.partial + 4 * jpr;
+        auto piece_of = [&](int c) { return row0 + (2 * c + (c == first ? slot0 : 0)) * kSlotFloats; };
+        // Several pieces' loads go out together, a trip to L2 each.
+        float m_all = -INFINITY, l_all = 0.f;
+#pragma unroll 1
+        for (int c0 = first; c0 <= last; c0 += 4) {
+          float2 ml[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ml[i] = __ldcg(reinterpret_cast<const float2*>(piece_of(min(c0 + i, last)) + ml_off));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (!mine || c0 + i > last || ml[i].y == 0.f) continue;  // none of the row's keys
+            const float mn = fmaxf(m_all, ml[i].x);
+            l_all = (l_all == 0.f ? 0.f : l_all * ex2(m_all - mn)) + ml[i].y * ex2(ml[i].x - mn);
             m_all = mn;
           }
-          const float inv_all = l_all == 0.f ? 0.f : 1.f / l_all;
+        }
+        const float inv_all = l_all == 0.f ? 0.f : 1.f / l_all;
+        const int k0 = shared_join ? qd * (kChunks / 4) : 0, k1 = shared_join ? k0 + kChunks / 4 : kChunks;
 #pragma unroll 1
-          for (int k = 0; k < kChunks; ++k) {
-            float acc[kCols];
+        for (int k = k0; k < k1; ++k) {
+          float acc[kCols];
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
-            for (int c = first; store && c <= last; ++c) {
-              const float* q = c == first ? row0 : row1 + 2ll * (c - first) * kSlotFloats;
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
-              if (ml.y == 0.f) continue;
-              const float f = ex2(ml.x - m_all);
+          for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+#pragma unroll 1
+          for (int c0 = first; c0 <= last; c0 += 2) {
+            float2 ml[2];
+            float4 v[2][kCols / 4];
 #pragma unroll
-              for (int e = 0; e < kCols; e += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(q + (kCols * k + e) * L::rows));
-                acc[e] = fmaf(v.x, f, acc[e]);
-                acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
-                acc[e + 2] = fmaf(v.z, f, acc[e + 2]);
-                acc[e + 3] = fmaf(v.w, f, acc[e + 3]);
+            for (int i = 0; i < 2; ++i) {
+              const float* q = piece_of(min(c0 + i, last));
+              ml[i] = __ldcg(reinterpret_cast<const float2*>(q + ml_off));
+#pragma unroll
+              for (int e = 0; e < kCols / 4; ++e)
+                v[i][e] = __ldcg(reinterpret_cast<const float4*>(q + (kCols * k + 4 * e) * L::rows));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!mine || c0 + i > last || ml[i].y == 0.f) continue;
+              const float f = ex2(ml[i].x - m_all);
+#pragma unroll
+              for (int e = 0; e < kCols / 4; ++e) {
+                acc[4 * e] = fmaf(v[i][e].x, f, acc[4 * e]);
+                acc[4 * e + 1] = fmaf(v[i][e].y, f, acc[4 * e + 1]);
+                acc[4 * e + 2] = fmaf(v[i][e].z, f, acc[4 * e + 2]);
+                acc[4 * e + 3] = fmaf(v[i][e].w, f, acc[4 * e + 3]);
               }
             }
-            uint32_t w[8];
-            round16(acc, inv_all, l_all == 0.f, w);
+          }
+          uint32_t w[8];
+          round16(acc, inv_all, l_all == 0.f, w);
+          if (shared_join) {
+            const int f = d.first_row + min(jr, d.rows - 1), t = plan::token_of(a, f), h = d.g * a.gs + (f - t * a.gs);
+            T* to = static_cast<T*>(a.out) + (long long)(d.row0 + t) * a.out_stride + (long long)h * hd + kCols * k;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (mine && kCols * k + 8 * u < hd)
+                *reinterpret_cast<uint4*>(to + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+          } else {
             to_stage(w, k & 3);
             if ((k & 3) == 3) from_stage(16 * (k - 3));
           }

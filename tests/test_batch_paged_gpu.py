@@ -297,6 +297,19 @@ def test_many_rows_other_head_dims(cuda_lib, H, G, D, page_rows, dtype):
             check(cuda_lib, b, "capped", softcap=20.0, window=150)
 
 
+@pytest.mark.parametrize("H,G,D,dtype", [(32, 8, 128, BF16), (14, 2, 64, F16), (12, 4, 96, BF16)])
+@pytest.mark.parametrize("new,kv", [([4], [16000]), ([8], [9000]), ([9], [9000]), ([2, 0, 3, 1], [5000, 7, 6001, 130]),
+                                    ([33, 2], [700, 12000])])
+def test_few_rows_over_many_splits(cuda_lib, H, G, D, dtype, new, kv):
+    """A few tokens behind long caches: items of few rows cut into many pieces, joined by several warps."""
+    b = Batch(new, kv, H, G, D, 32, dtype, seed=51, pad=1)
+    check(cuda_lib, b, "few rows H%d G%d D%d" % (H, G, D))
+    obj = b.object(cuda_lib)
+    first = cuda_lib.attend_paged(obj, b.q, b.k, b.v)
+    for _ in range(5):
+        assert torch.equal(first, cuda_lib.attend_paged(obj, b.q, b.k, b.v))
+
+
 def test_many_rows_repeat_bits(cuda_lib):
     b = Batch(LONG["new"], LONG["kv"], 32, 8, 128, 64, BF16, seed=22)
     obj = b.object(cuda_lib)
