@@ -21,6 +21,12 @@
 // Pieces of a split item go to the workspace; the block that arrives last (a
 // counter per item, left at zero again) joins them in key order, so one launch
 // does everything and results do not depend on the order of arrival.
+//
+// Bound by HBM on large batches: 64 sequences of up to 16384 positions, 8 kv
+// heads of 128, read 1.69 GB in 259 us, 6.5 TB/s (96% of a copy's rate; pages of
+// 16 rows). A small call is bound by its latency: one sequence of 1536
+// positions takes 10.6 us, from launch and plan through the first tiles' trip
+// to HBM to the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <type_traits>

