@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
                 big = max3(big, fabsf(__uint_as_float(s[c][e])), fabsf(__uint_as_float(s[c][e + 1])));
-            if (!__any_sync(0xffffffffu, big * sc.in_mul > kTanhPolyMax)) {
+            if (!__any_sync(0xffffffffu, big * fabsf(sc.in_mul) > kTanhPolyMax)) {
               // tanh_poly on pairs: y = out_mul (x + x u q(u)).
               const float xo = sc.in_mul * sc.out_mul;
 #pragma unroll

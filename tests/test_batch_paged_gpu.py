@@ -423,3 +423,10 @@ def test_two_batches_on_two_streams(cuda_lib):
     for w, out in zip(want, outs):
         for o in out:
             assert torch.equal(w, o)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,kv", [([1, 1, 1], [700, 5, 90]), ([300, 70], [900, 70])])
+def test_negative_scale_with_a_cap(cuda_lib, D, new, kv):
+    """Scores far past the cap on both sides, turned around by the scale."""
+    check(cuda_lib, Batch(new, kv, 8, 2, D, 32, BF16, seed=61), "negative", scale=-0.5, softcap=2.0)
