@@ -43,6 +43,19 @@ __device__ __forceinline__ float tanh_poly(float x) {
 __device__ __forceinline__ float tanh_exp(float x) {
   return 1.f - __fdividef(2.f, ex2(x * (2.f * kLog2e)) + 1.f);
 }
+// The capped score in base-2 units, rounded as the tcgen05 kernel rounds it on
+// pairs of small scores: a tile takes that form or this one by what its largest
+// score is, masked ones included, and its results must not tell.
+__device__ __forceinline__ float capped_score(float s, const ScoreMap& sc) {
+  const float x = s * sc.in_mul;
+  if (!(fabsf(x) <= kTanhPolyMax)) return sc.out_mul * tanh_exp(x);
+  const float y = s * (sc.in_mul * sc.out_mul), u = x * x;
+  float q = fmaf(kTanhQ4, u, kTanhQ3);
+  q = fmaf(q, u, kTanhQ2);
+  q = fmaf(q, u, kTanhQ1);
+  q = fmaf(q, u, kTanhQ0) * u;
+  return fmaf(q, y, y);
+}
 __device__ __forceinline__ float tanh_score(float x) { return fabsf(x) <= kTanhPolyMax ? tanh_poly(x) : tanh_exp(x); }
 
 }  // namespace attn

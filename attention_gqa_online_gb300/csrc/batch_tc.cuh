@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                  s[c][e] = __float_as_uint(sc.out_mul * tanh_score(__uint_as_float(s[c][e]) * sc.in_mul));
+                  s[c][e] = __float_as_uint(capped_score(__uint_as_float(s[c][e]), sc));
             }
           }
           float fold = 0.f;  // to be added to every score of the row

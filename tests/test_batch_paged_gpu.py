@@ -430,3 +430,16 @@ def test_two_batches_on_two_streams(cuda_lib):
 def test_negative_scale_with_a_cap(cuda_lib, D, new, kv):
     """Scores far past the cap on both sides, turned around by the scale."""
     check(cuda_lib, Batch(new, kv, 8, 2, D, 32, BF16, seed=61), "negative", scale=-0.5, softcap=2.0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,kv", [([1, 1, 1], [700, 5, 90]), ([300, 70], [900, 70])])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=30.0), dict(softcap=5.0), dict(softcap=30.0, window=50)])
+def test_bits_do_not_depend_on_unattended_positions(cuda_lib, D, new, kv, kw, dtype):
+    """Past the end of each sequence the pages hold NaN, zeros or large values: the same bits come out."""
+    outs = []
+    for junk in (float("nan"), 0.0, 3e4):
+        b = Batch(new, kv, 8, 2, D, 32, dtype, seed=62, junk=junk)
+        outs.append(cuda_lib.attend_paged(b.object(cuda_lib), b.q, b.k, b.v, **kw))
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
