@@ -86,6 +86,16 @@ def _run(where, fn, index, stream, args):
         raise B.AttnError(code, where)
 
 
+def _new(make, shape, dtype, device, stream):
+    """A result made by torch on the call's stream: the memory and a fill belong to that stream's order."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _rows2d(x, name):
     """Row stride of a [rows, columns] tensor whose columns are contiguous."""
     rows, columns = x.shape if x.dim() == 2 else (0, 0)
@@ -120,7 +130,7 @@ def _rope(x, table, heads, positions, rot_dim, interleaved, out, inverse, stream
         raise ValueError("positions must hold one position a row")
     index = x.get_device()
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(torch.empty, x.shape, x.dtype, x.device, stream)
         ys = columns
     else:
         if out.shape != x.shape:
@@ -294,7 +304,7 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
             raise ValueError("q must be [%d, %d]" % (rows, H * D))
         _like(dtype, "q", q)
         if q_out is None:
-            q_out = torch.empty((rows, H * D), dtype=cache, device=q.device)
+            q_out = _new(torch.empty, (rows, H * D), cache, q.device, stream)
             qos = H * D
         else:
             if q_out.shape != q.shape:
@@ -330,7 +340,7 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
     _like(dtype, "k_pages", k_pages)
     _like(dtype, "v_pages", v_pages)
     if out is None:
-        out = torch.zeros((rows, H * D), dtype=dtype, device=q.device)
+        out = _new(torch.zeros, (rows, H * D), dtype, q.device, stream)
         os = H * D
     else:
         if out.shape != q.shape:
@@ -352,6 +362,7 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
     batch.same_device(index)
     _run("attn_batch_paged", B.load_library().attn_batch_paged, index, stream,
          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), code,
-          batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H, batch.num_kv_heads, D, kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks,
-          scale, window, softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel()))
+          batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H,
+          batch.num_kv_heads, D, kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks, scale, window,
+          softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel()))
     return out

@@ -443,3 +443,24 @@ def test_bits_do_not_depend_on_unattended_positions(cuda_lib, D, new, kv, kw, dt
         b = Batch(new, kv, 8, 2, D, 32, dtype, seed=62, junk=junk)
         outs.append(cuda_lib.attend_paged(b.object(cuda_lib), b.q, b.k, b.v, **kw))
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+
+def test_results_made_on_another_stream(cuda_lib):
+    """Tensors that a call makes for its results belong to the call's stream, whatever the current one still does."""
+    A = cuda_lib
+    b = Batch([1, 40], [400, 250], 8, 2, 64, 32, BF16, seed=63)
+    obj, table = b.object(A), A.rope_table(512, 64)
+    kn, vn = b.k[:41].clone(), b.v[:41].clone()
+    kn[:], vn[:] = 1.0, 2.0
+    want = A.attend_paged(obj, b.q, b.k, b.v), A.rope(b.q, table, 8)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda._sleep(20_000_000)
+        got = A.attend_paged(obj, b.q, b.k, b.v, stream=stream), A.rope(b.q, table, 8, stream=stream)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    assert A.append_paged(obj, kn, vn, b.k, b.v, q=b.q, table=table, stream=side).shape == b.q.shape
+    torch.cuda.synchronize()
