@@ -103,7 +103,11 @@ def _rows2d(x, name):
     if x.dim() != 2 or (one != 1 and columns > 1):
         raise ValueError("%s must be [rows, columns] with contiguous columns" % name)
     # The stride of a single row is never used, and torch may leave anything there.
-    return stride if rows > 1 else columns
+    if rows < 2:
+        stride = columns
+    if rows >> 32 or stride >> 32:
+        raise ValueError("%s has more rows, or rows farther apart, than 32 bits count" % name)
+    return stride
 
 
 def _table(table, rot_dim):

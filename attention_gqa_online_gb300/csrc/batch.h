@@ -114,6 +114,8 @@ constexpr uint64_t kMaxBatchCapacity = 1ull << 24;
 // later by another block).  64 sequences of 8192, 8 kv heads of 64: 229 us with
 // 256 bytes, 164 with 128 (6.5 TB/s).
 inline int kv_l2_bytes(int head_dim) { return (2 * head_dim) & -(2 * head_dim); }
+// Pool rows at most: a box of 256 rows from the first row past the pool still has 31-bit coordinates.
+constexpr uint64_t kMaxBatchPool = 0x7fffffffu - 256;
 size_t batch_workspace_bytes(int D, int sm_count);
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s);
 int launch_batch_mma(const BatchArgs& a, int dtype, int blocks, cudaStream_t s);

@@ -156,7 +156,8 @@ extern "C" int attn_batch_paged(const void* q, const void* k_pages, const void* 
   if (kv_dim < (uint64_t)n_kv_heads * head_dim || q_stride < (uint64_t)n_heads * head_dim ||
       out_stride < (uint64_t)n_heads * head_dim)
     return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap * 1.5f)) return ATTN_ERR_INVALID_ARG;
+  if (softcap > 0.f && !std::isfinite(scale / softcap)) return ATTN_ERR_INVALID_ARG;
   if (total_rows == 0 || n_seqs == 0) return ATTN_OK;
   if (q == nullptr || k_pages == nullptr || v_pages == nullptr || out == nullptr || block_table == nullptr ||
       q_start == nullptr || kv_len == nullptr)
@@ -168,7 +169,7 @@ extern "C" int attn_batch_paged(const void* q, const void* k_pages, const void* 
       !aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16))
     return ATTN_ERR_UNSUPPORTED;
   if ((uint64_t)total_rows * n_heads > (1u << 30) || n_seqs > (uint32_t)kMaxBatchSeqs ||
-      (uint64_t)page_rows * max_blocks > kMaxBatchCapacity)
+      (uint64_t)page_rows * max_blocks > kMaxBatchCapacity || (uint64_t)page_rows * num_pages > kMaxBatchPool)
     return ATTN_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;

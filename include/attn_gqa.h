@@ -473,12 +473,14 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  * descends or passes total_rows (the sequence is left out) record
  * ATTN_ERR_INVALID_ARG in the status word.  total_rows == 0 or n_seqs == 0 is
  * a no-op.  Errors: INVALID_ARG for NULL pointers, bad heads, sizes or
- * strides, a non-finite scale, a negative or non-finite softcap, or a
- * workspace that is too small or misaligned; UNSUPPORTED for
+ * strides, a non-finite scale, a softcap that is negative, above 2e38 or so
+ * small that scale / softcap is not finite, or a workspace that is too small or
+ * misaligned; UNSUPPORTED for
  * ATTN_DT_F32 (attn_decode_paged and attn_prefill_paged serve fp32 pools),
  * head_dim % 8 != 0, kv_dim or strides % 8 != 0, addresses of q, out or the
  * pools that are not 16-byte aligned, more than 16384 sequences, a capacity of
- * more than 2^24 positions, or total_rows * n_heads > 2^30.
+ * more than 2^24 positions, a pool of more than 2^31 - 257 rows, or total_rows
+ * * n_heads > 2^30.
  * Kernels: pages of whole 8-row groups (page_rows % 8 == 0) run on the tensor
  * cores (tcgen05) or, for about one row a sequence (total_rows <= n_seqs) with
  * H/G <= 16, on a kernel that streams K and V; other pages on warp-level

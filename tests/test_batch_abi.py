@@ -165,6 +165,30 @@ def test_python_layer_refuses_host_tensors_and_mismatched_types(lib):
                      torch.zeros(2, dtype=torch.int32), 4, 2, 64, 16)
 
 
+@hidden
+@pytest.mark.parametrize("kw", [dict(cap=1e-38, scale=10.0), dict(cap=1e-38, scale=-10.0), dict(cap=3e38)])
+def test_batch_rejects_caps_outside_the_range_of_its_arithmetic(lib, kw):
+    """scale / softcap and softcap log2 e have to be finite."""
+    assert batch_call(lib, **kw) == BAD
+
+
+@hidden
+def test_batch_refuses_pools_whose_last_boxes_pass_31_bits(lib):
+    assert batch_call(lib, page_rows=2 ** 8, pages=2 ** 23 - 1) == UNSUP
+
+
+@hidden
+def test_python_layer_refuses_sizes_that_do_not_fit_32_bits(lib):
+    """Tensors without memory behind them."""
+    import torch
+    import attention_gqa_online_gb300 as A
+    table = torch.zeros(4, 2)
+    for shape, strides in (((2 ** 32 + 1, 2), (2, 1)), ((2, 2), (2 ** 32 + 2, 1))):
+        x = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device="meta")
+        with pytest.raises(ValueError, match="32 bits"):
+            A.rope(x, table, 1)
+
+
 def test_refusals_run_with_the_device_hidden():
     if not gpu_visible():
         pytest.skip("no GPU visible: the tests above run in this process")
