@@ -101,6 +101,7 @@ extern "C" int attn_append_paged(const void* q, void* q_out, const void* k_new, 
       q_start == nullptr || kv_len == nullptr)
     return ATTN_ERR_INVALID_ARG;
   if (dtype != ATTN_DT_F32 && dtype != cache_dtype) return ATTN_ERR_UNSUPPORTED;
+  if (q != nullptr && q == q_out && (q_stride != q_out_stride || dtype != cache_dtype)) return ATTN_ERR_INVALID_ARG;
   const size_t ei = esize(dtype), ec = esize(cache_dtype);
   if (!aligned(q, ei) || !aligned(k_new, ei) || !aligned(v_new, ei) || !aligned(q_out, ec) || !aligned(k_pages, ec) ||
       !aligned(v_pages, ec) || !aligned(table, 4) || !aligned(block_table, 4) || !aligned(q_start, 4) ||

@@ -425,7 +425,8 @@ ATTN_API int attn_rope_apply(const void *x, void *y, attn_dtype_t dtype, uint32_
  * or past the table, or whose page is >= num_pages, is skipped (nothing of it
  * is written) and ATTN_ERR_INVALID_ARG recorded in the status word.  Two rows
  * that name the same pool row leave one of the two there.  total_rows == 0 or
- * n_seqs == 0 is a no-op.  q_out may be q when the types are the same.
+ * n_seqs == 0 is a no-op.  q_out may be q when types and strides are the
+ * same (else ATTN_ERR_INVALID_ARG); otherwise they must not overlap.
  * Errors: INVALID_ARG for NULL pointers, addresses not
  * aligned to their element, bad heads, sizes, types, layout or strides.
  */

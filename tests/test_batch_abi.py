@@ -93,6 +93,12 @@ def test_append_rejects_type_pairs(lib, dt, cdt):
 
 
 @hidden
+@pytest.mark.parametrize("kw", [dict(qo_stride=264), dict(dt=0, cdt=1)])
+def test_append_rejects_q_in_place_in_another_layout(lib, kw):
+    assert append_call(lib, rows=4, k=FAKE + 0x1000, **kw) == BAD
+
+
+@hidden
 def test_append_of_nothing_is_noop(lib):
     assert append_call(lib, rows=0, k=None, v=None, bt=None) == 0
     assert append_call(lib, n=0, qs=None, kl=None) == 0
