@@ -39,6 +39,7 @@ def _on(x, *others):
 _CODES = {torch.float32: B.ATTN_DT_F32, torch.bfloat16: B.ATTN_DT_BF16, torch.float16: B.ATTN_DT_F16}
 _INT32 = (torch.int32, torch.uint32)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _same_device(index, *tensors):
@@ -77,7 +78,7 @@ def _run(where, fn, index, stream, args):
         stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         code = fn(*args, stream)
     else:
         with torch.cuda.device(index):
@@ -97,31 +98,32 @@ def _new(make, shape, dtype, device, stream):
 
 
 def _rows2d(x, name):
-    """Row stride of a [rows, columns] tensor whose columns are contiguous."""
-    rows, columns = x.shape if x.dim() == 2 else (0, 0)
-    stride, one = x.stride() if x.dim() == 2 else (0, 0)
-    if x.dim() != 2 or (one != 1 and columns > 1):
-        raise ValueError("%s must be [rows, columns] with contiguous columns" % name)
-    # The stride of a single row is never used, and torch may leave anything there.
-    if rows < 2:
-        stride = columns
-    if rows >> 32 or stride >> 32:
-        raise ValueError("%s has more rows, or rows farther apart, than 32 bits count" % name)
-    return stride
+    """(rows, columns, row stride) of a [rows, columns] tensor whose columns are contiguous."""
+    shape = x.shape
+    if len(shape) == 2:
+        rows, columns = shape
+        stride, one = x.stride()
+        if one == 1 or columns < 2:
+            if rows < 2:  # the stride of a single row is never used, and torch may leave anything there
+                stride = columns
+            if rows >> 32 or stride >> 32:
+                raise ValueError("%s has more rows, or rows farther apart, than 32 bits count" % name)
+            return rows, columns, stride
+    raise ValueError("%s must be [rows, columns] with contiguous columns" % name)
 
 
 def _table(table, rot_dim):
     """(address, rows) of a rotary table, or (None, 0)."""
     if table is None:
         return None, 0
-    if table.dim() != 2 or table.shape[1] != rot_dim or table.dtype != torch.float32 or not table.is_contiguous():
+    shape = table.shape
+    if len(shape) != 2 or shape[1] != rot_dim or table.dtype != torch.float32 or not table.is_contiguous():
         raise ValueError("table must be a contiguous float32 [positions, %d] table of rope_table" % rot_dim)
-    return table.data_ptr(), table.shape[0]
+    return table.data_ptr(), shape[0]
 
 
 def _rope(x, table, heads, positions, rot_dim, interleaved, out, inverse, stream):
-    xs = _rows2d(x, "x")
-    rows, columns = x.shape
+    rows, columns, xs = _rows2d(x, "x")
     if heads < 1 or columns % heads:
         raise ValueError("x has %d columns, not a multiple of %d heads" % (columns, heads))
     D = columns // heads
@@ -134,14 +136,15 @@ def _rope(x, table, heads, positions, rot_dim, interleaved, out, inverse, stream
         raise ValueError("positions must hold one position a row")
     index = x.get_device()
     if out is None:
-        out = _new(torch.empty, x.shape, x.dtype, x.device, stream)
+        out = _new(torch.empty, (rows, columns), x.dtype, x.device, stream)
         ys = columns
     else:
-        if out.shape != x.shape:
+        out_rows, out_columns, ys = _rows2d(out, "out")
+        if out_rows != rows or out_columns != columns:
             raise ValueError("out must have the shape of x")
         _like(x.dtype, "out", out)
-        ys = _rows2d(out, "out")
-    _same_device(index, table, positions, out)
+        _same_device(index, out)
+    _same_device(index, table, positions)
     _run("attn_rope_apply", B.load_library().attn_rope_apply, index, stream,
          (x.data_ptr(), out.data_ptr(), code, rows, heads, D, rot_dim, xs, ys, 1 if interleaved else 0, pos, tab,
           tab_rows, 1 if inverse else 0))
@@ -287,9 +290,9 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
     return it turned, in the cache's type (q_out when given)."""
     kv_dim, num_pages = batch.pool(k_pages, v_pages)
     D, G = batch.head_dim, batch.num_kv_heads
-    ks, vs = _rows2d(k_new, "k_new"), _rows2d(v_new, "v_new")
-    rows = k_new.shape[0]
-    if k_new.shape[1] != G * D or v_new.shape != k_new.shape:
+    rows, columns, ks = _rows2d(k_new, "k_new")
+    v_rows, v_columns, vs = _rows2d(v_new, "v_new")
+    if columns != G * D or v_columns != columns or v_rows != rows:
         raise ValueError("k_new and v_new must be [rows, %d]" % (G * D))
     dtype, cache = k_new.dtype, k_pages.dtype
     code, cache_code = _code(k_new, "k_new"), _code(k_pages, "k_pages")
@@ -303,18 +306,18 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
     q_ptr = qo_ptr = None
     if q is not None:
         H = batch.num_heads
-        qs = _rows2d(q, "q")
-        if q.shape[0] != rows or q.shape[1] != H * D:
+        q_rows, q_columns, qs = _rows2d(q, "q")
+        if q_rows != rows or q_columns != H * D:
             raise ValueError("q must be [%d, %d]" % (rows, H * D))
         _like(dtype, "q", q)
         if q_out is None:
             q_out = _new(torch.empty, (rows, H * D), cache, q.device, stream)
             qos = H * D
         else:
-            if q_out.shape != q.shape:
+            o_rows, o_columns, qos = _rows2d(q_out, "q_out")
+            if o_rows != rows or o_columns != q_columns:
                 raise ValueError("q_out must have the shape of q")
             _like(cache, "q_out", q_out)
-            qos = _rows2d(q_out, "q_out")
         q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
         _same_device(index, q, q_out)
     _same_device(index, v_pages, k_new, v_new, table)
@@ -335,9 +338,8 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
     left as they are in `out`."""
     kv_dim, num_pages = batch.pool(k_pages, v_pages)
     H, D = batch.num_heads, batch.head_dim
-    qs = _rows2d(q, "q")
-    rows = q.shape[0]
-    if q.shape[1] != H * D:
+    rows, columns, qs = _rows2d(q, "q")
+    if columns != H * D:
         raise ValueError("q must be [rows, %d]" % (H * D))
     dtype = q.dtype
     code = _code(q, "q")
@@ -347,10 +349,10 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
         out = _new(torch.zeros, (rows, H * D), dtype, q.device, stream)
         os = H * D
     else:
-        if out.shape != q.shape:
+        out_rows, out_columns, os = _rows2d(out, "out")
+        if out_rows != rows or out_columns != columns:
             raise ValueError("out must have the shape of q")
         _like(dtype, "out", out)
-        os = _rows2d(out, "out")
     slopes = None
     if alibi_slopes is not None:
         if alibi_slopes.numel() != H or alibi_slopes.dtype != torch.float32 or not alibi_slopes.is_contiguous():
