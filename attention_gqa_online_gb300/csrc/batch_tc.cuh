@@ -47,9 +47,9 @@
 // zeros. The same rows of K only make scores that are masked.
 //
 // Bound by the softmax warps: a prompt of 8192, 32 heads over 8 of 128, bf16,
-// takes 394 us (1.40 PFLOP/s, 73% of the measured bf16 rate; tensor pipe 65%
+// takes 392 us (1.40 PFLOP/s, 73% of the measured bf16 rate; tensor pipe 65%
 // busy, special-function unit 33%, issue 47%), two chunks of 512 behind 16k to
-// 32k keys 251 us (71%). With the exponentials left out a chunk took seven
+// 32k keys 250 us (71%). With the exponentials left out a chunk took seven
 // eighths of its time, with tile loads and hand-overs alone two thirds.
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
