@@ -450,6 +450,14 @@ def attn_selftest_wait_timeout(timeout_us=10000, stream=None):
     _check(fn(timeout_us, _stream(stream)), "attn_selftest_wait_timeout")
 
 
+def attn_selftest_warp_wait(lanes, timeout_us=10000, stream=None):
+    """The failure path of the batched kernels' waits; lanes: 8 int32 on the device (see attn_gqa.h)."""
+    fn = load_library().attn_selftest_warp_wait
+    fn.restype = ctypes.c_int
+    fn.argtypes = [_u32, _vp, _vp]
+    _check(fn(timeout_us, _u32_addr(lanes, "lanes"), _stream(stream)), "attn_selftest_warp_wait")
+
+
 def attn_get_status(stream=None):
     """Synchronise `stream`, return and clear the device status word."""
     return int(load_library().attn_get_status(_stream(stream)))

@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           &sm.start);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
   __syncthreads();
-  auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  // Warps wait as a whole: lanes that left a wait at different times could arrive for, or part from, the others.
+  auto wait = [&](uint64_t* bar, int phase) { return warp_wait(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
 
   if (warp >= kConsumers / 32) {
     // ------------------------------------------------------------ producers
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int key = key0 + (q0 + lane) * box_rows, st = J % S::stages;
         // A wait that ran out ends the role: a slot in use must not be written, nor a phase arrived at twice.
-        if (J >= S::stages && !__all_sync(0xffffffffu, wait(&sm.empty[st], J / S::stages - 1))) return J;
+        if (J >= S::stages && !wait(&sm.empty[st], J / S::stages - 1)) return J;
         if (pw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(2 * S::tile_bytes));
         __syncwarp();
         unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + chunk * kChunkBytes;
@@ -201,9 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_v) prefetch_tmap(&tm_v1);
       }
       for (;; ++x) {
-        const bool ok = wait(&sm.desc_full[x % kDescs], x / kDescs);
         const DecodeDesc& d = sm.desc[x % kDescs];
-        if (!__all_sync(0xffffffffu, ok && *(volatile int*)&sm.abort == 0) || d.end) return;
+        if (!wait(&sm.desc_full[x % kDescs], x / kDescs) || !warp_whole(&sm.abort) || d.end) return;
         J = load_tiles(d.n, d.seq, d.g, d.lo_min, d.hi_max, d.tile0, J);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     plan::Walker<kRows, kKeys> walk(a, sm.start);
     plan::Piece p;
     while (true) {
-      const bool more = walk.next(p) && !*(volatile int*)&sm.abort;
+      const bool more = walk.next(p) && warp_whole(&sm.abort);
       const int first_row = p.b * kRows;
       const int rows = more ? min(kRows, p.q.q_len * a.gs - first_row) : 0;
       if (more && p.t1 == p.t0) {  // rows without keys
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      if (x >= kDescs && !__all_sync(0xffffffffu, wait(&sm.desc_free[x % kDescs], x / kDescs - 1))) break;
+      if (x >= kDescs && !wait(&sm.desc_free[x % kDescs], x / kDescs - 1)) break;
       if (lane == 0) {
         DecodeDesc& d = sm.desc[x % kDescs];
         d.end = !more;
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (!more) break;
       // Q rows, one copy each.
-      if (x >= 2 && !__all_sync(0xffffffffu, wait(&sm.q_free[x & 1], (x >> 1) - 1))) break;
+      if (x >= 2 && !wait(&sm.q_free[x & 1], (x >> 1) - 1)) break;
       if (lane == 0) mbar_arrive_expect_tx(&sm.q_ready[x & 1], (unsigned)(rows * a.D * 2));
       __syncwarp();
       if (lane < rows) {
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.lo_min, p.k.hi_max, p.k.kt0 + p.t0, J);
       ++x;
-      if (*(volatile int*)&sm.abort) break;
+      if (!warp_whole(&sm.abort)) break;
     }
     // No copy may still be landing in shared memory when the block exits.
     for (int s = 0; s < S::stages && s < J; ++s) {
@@ -283,7 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const DecodeDesc& d = sm.desc[x % kDescs];
     // One thread decides for all whether there is a piece: the warps meet at barriers that none may miss.  (The
     // joining buffers are free again after this barrier, too.)
-    if (tid == 0) sm.go = wait(&sm.desc_full[x % kDescs], x / kDescs) && *(volatile int*)&sm.abort == 0 && !d.end;
+    if (tid == 0)
+      sm.go = wait_phase(&sm.desc_full[x % kDescs], (unsigned)(x / kDescs & 1), a.status, &sm.abort) &&
+              *(volatile int*)&sm.abort == 0 && !d.end;
+    __syncwarp();
     named_barrier(1, kConsumers);
     if (!sm.go) break;
     const int n = d.n, rows = d.rows;

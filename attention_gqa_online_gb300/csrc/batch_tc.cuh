@@ -355,15 +355,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sm.tmem_base;
-  // The lanes of a warp may leave a wait at different times.  Before one lane arrives somewhere for the warp all must
-  // have left it (a warp-wide instruction or __syncwarp between): else the barrier could complete its next phase and
-  // leave the others waiting for a phase that is past.
-  auto wait = [&](uint64_t* bar, int phase) { return wait_phase(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
-  // Descriptor of piece x (its slot stays valid until every role has released it).
-  // After a wait that ran out (sm.abort) its content means nothing: the roles leave.
-  auto piece = [&](int x) -> const PieceDesc& {
-    wait(&sm.desc_full[x % kDescs], x / kDescs);
-    return sm.desc[x % kDescs];
+  // Warps wait as a whole.  Were lanes to leave a wait at different times, one could arrive somewhere for the warp, the
+  // barrier complete its next phase and the others wait for a phase that is past.
+  auto wait = [&](uint64_t* bar, int phase) { return warp_wait(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  // Without the vote, where no answer is asked for, nothing warp-wide follows at once and a __syncwarp comes before a lane
+  // arrives for the warp (17 ragged chunks with a bias, 16 heads: 223 us with votes there too, 219 this way).
+  auto lane_wait = [&](uint64_t* bar, int phase) { wait_phase(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  // Is there a piece x?  Its descriptor is then valid until every role has released it.  If not, there are no more or
+  // the pipeline broke: the role, all lanes of it, leaves.
+  auto next_piece = [&](int x) {
+    return wait(&sm.desc_full[x % kDescs], x / kDescs) && warp_whole(&sm.abort) && !sm.desc[x % kDescs].end;
   };
 
   if (warp < 4) {
@@ -405,7 +406,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return row;
     };
-    auto all_ok = [&](bool lane_ok) { return __all_sync(0xffffffffu, lane_ok) != 0; };
     auto barrier_of = [&](uint64_t* full) { return PAIR ? in_leader(smem_u32(full)) : smem_u32(full); };
     // No copy may still be landing in shared memory when the block exits (a pair's copies all complete on the first
     // block's barriers, and the pair leaves together).
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // phase, would turn a late block into a fault.
       bool ok = true;
       while (ok) {
-        const bool more = walk.next(p) && !*(volatile int*)&sm.abort;
+        const bool more = walk.next(p) && warp_whole(&sm.abort);
         // This block's rows: 128 flattened rows from first_row on.
         const int first_row = p.b * L::rows + rank * kTcRows;
         const int rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           continue;
         }
-        if (x >= kDescs) ok = all_ok(wait(&sm.desc_free[x % kDescs], x / kDescs - 1));
+        if (x >= kDescs) ok = wait(&sm.desc_free[x % kDescs], x / kDescs - 1);
         if (!ok) break;
         if (lane == 0) {
           PieceDesc& d = sm.desc[x % kDescs];
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                              (p.k.kt0 + p.t1 - 1) * kTcKeys + (PAIR ? rank * L::k_rows : 0), p.s);
         // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
         // only feeds itself, and those rows are not stored).
-        if (x >= 2) ok = all_ok(wait(&sm.q_free[x & 1], (x >> 1) - 1));
+        if (x >= 2) ok = wait(&sm.q_free[x & 1], (x >> 1) - 1);
         if (!ok) break;
         if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
           if (lane == 0) {
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < n; ++i, ++J) {
           const int row = part_row(w, i), slot = J % L::slots;
-          if (J >= L::slots) ok = all_ok(wait(&sm.k_empty[slot], J / L::slots - 1));
+          if (J >= L::slots) ok = wait(&sm.k_empty[slot], J / L::slots - 1);
           if (!ok) break;
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
           __syncwarp();
@@ -533,13 +533,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int J = 0;
       bool ok = true;
       for (int x = 0; ok; ++x) {
-        const PieceDesc& d = piece(x);
-        if (d.end || *(volatile int*)&sm.abort) break;
+        if (!next_piece(x)) break;
+        const PieceDesc& d = sm.desc[x % kDescs];
         const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
         Parts w = open_parts(kTcKeys, n, d.lo_min, d.hi_max, d.tile_last * kTcKeys, d.seq);
         for (int i = 0; i < n; ++i, ++J) {
           const int row = part_row(w, i), key = w.key0 - i * kTcKeys + lane * box_rows, slot = J % L::slots;
-          if (J >= L::slots) ok = all_ok(wait(&sm.v_empty[slot], J / L::slots - 1));
+          if (J >= L::slots) ok = wait(&sm.v_empty[slot], J / L::slots - 1);
           if (!ok) break;
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.v_full[slot], (unsigned)(PAIR ? 2 : 1) * L::v_bytes);
           __syncwarp();
@@ -588,9 +588,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ---------------------------------------------------------- MMA issue (the first block's, in a pair)
       // Two warps, one a product, so that neither holds up the other; warp-uniform loops, one elected lane issues.
       constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
-      auto wait_all = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, wait(bar, phase));
-      };
       if (rank != 0) {
       } else if (warp == 1) {
         constexpr uint32_t idesc_qk = tc::idesc_f32acc(fmt, false, L::rows, kTcKeys);
@@ -599,14 +596,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;
         int j = 0;
         for (int x = 0; ok; ++x) {
-          const PieceDesc& d = piece(x);
-          if (d.end || *(volatile int*)&sm.abort) break;
+          if (!next_piece(x)) break;
+          const PieceDesc& d = sm.desc[x % kDescs];
           const int n = d.n;
           const uint64_t dq = dq0 + (uint64_t)((x & 1) * (L::q_bytes >> 4));
-          ok = wait_all(&sm.q_ready[x & 1], x >> 1);
+          ok = wait(&sm.q_ready[x & 1], x >> 1);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = wait_all(&sm.k_full[slot], j / L::slots) && (j < 2 || wait_all(&sm.s_free[b], (j - 2) >> 1));
+            ok = wait(&sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t dk = dk0 + (uint64_t)(slot * (L::k_bytes >> 4));
@@ -625,14 +622,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;
         int j = 0;
         for (int x = 0; ok; ++x) {
-          const PieceDesc& d = piece(x);
-          if (d.end || *(volatile int*)&sm.abort) break;
+          if (!next_piece(x)) break;
+          const PieceDesc& d = sm.desc[x % kDescs];
           const int n = d.n;
           // The first product of a piece replaces O.
-          if (x > 0) ok = wait_all(&sm.o_free, x - 1);
+          if (x > 0) ok = wait(&sm.o_free, x - 1);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = wait_all(&sm.v_full[slot], j / L::slots) && wait_all(&sm.p_ready[b], j >> 1);
+            ok = wait(&sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t dv = dv0 + (uint64_t)(slot * (L::v_bytes >> 4));
@@ -662,8 +659,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t o_col = tmem + lane_base + kOColumn;
     int J = 0;
     for (int x = 0;; ++x) {
-      const PieceDesc& d = piece(x);
-      if (d.end || *(volatile int*)&sm.abort) break;
+      if (!next_piece(x)) break;
+      const PieceDesc& d = sm.desc[x % kDescs];
       const int n = d.n;
       const bool busy = 32 * qd < d.rows;
       float m_ref = -INFINITY, l = 0.f;
@@ -687,7 +684,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!busy) {
           // No valid row in this warp: only keep the barriers going (P_b of tile j - 2 must have been read
           // before this tile's arrival).
-          if (j > 0) wait(&sm.chain_bar[qd][(j - 1) % kChain], (j - 1) / kChain);
+          if (j > 0) lane_wait(&sm.chain_bar[qd][(j - 1) % kChain], (j - 1) / kChain);
           __syncwarp();
           if (lane == 0) {
             arrive_leader<PAIR>(&sm.s_free[b]);
@@ -823,7 +820,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // (The first tile of a piece, and warps without rows, wait too, for nothing but order: a group must not get
           // two tiles ahead of the other one's wait on the same slot of the ring.)
           float m_prev = -INFINITY;
-          if (j > 0) wait(&sm.chain_bar[qd][(j - 1) % kChain], (j - 1) / kChain);
+          if (j > 0) lane_wait(&sm.chain_bar[qd][(j - 1) % kChain], (j - 1) / kChain);
           if (i > 0) m_prev = sm.chain[(j - 1) % kChain][r];
           const float m_new = (tmax > m_prev + kRescale) ? tmax : m_prev;  // also for the first finite maximum
           sm.chain[j % kChain][r] = m_new;
@@ -904,11 +901,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t o_col = tmem + ((uint32_t)(32 * qd) << 16) + kOColumn;
     constexpr int kCols = 16, kChunks = D / kCols;  // columns at a time: few registers
     for (int x = 0;; ++x) {
-      const PieceDesc& d = piece(x);
-      if (d.end || *(volatile int*)&sm.abort) break;
+      if (!next_piece(x)) break;
+      const PieceDesc& d = sm.desc[x % kDescs];
       const bool busy = 32 * qd < d.rows, store = r < d.rows;
-      wait(&sm.stat_bar[qd][x % kDescs][0], x / kDescs);
-      wait(&sm.stat_bar[qd][x % kDescs][1], x / kDescs);
+      lane_wait(&sm.stat_bar[qd][x % kDescs][0], x / kDescs);
+      lane_wait(&sm.stat_bar[qd][x % kDescs][1], x / kDescs);
       const float2 s0 = sm.stat[x % kDescs][0][r], s1 = sm.stat[x % kDescs][1][r];
       const float m_fin = fmaxf(s0.x, s1.x);
       float l_row = 0.f;
@@ -1028,7 +1025,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mbar_arrive(&sm.join_bar[x % kDescs]);
         }
       } else if (shared_join) {
-        wait(&sm.join_bar[x % kDescs], x / kDescs);
+        lane_wait(&sm.join_bar[x % kDescs], x / kDescs);
         __syncwarp();
         join = *(volatile int*)&sm.joins[x % kDescs] != 0;
       }
@@ -1107,6 +1104,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   }
 
+  __syncwarp();
   tc::fence_before_sync();
   if (PAIR)
     pair_sync();  // arrivals, commits and copies cross the pair: it leaves together

@@ -650,6 +650,14 @@ ATTN_API int attn_get_status(attn_stream_t stream);
  */
 ATTN_API int attn_selftest_wait_timeout(uint32_t timeout_us, attn_stream_t stream);
 
+/*
+ * The same for the warp-wide wait of the batched kernels: one warp's wait gives
+ * up, seven others wait for a barrier that completes just then.  lanes
+ * [8] uint32 (device): the lanes of each warp whose wait succeeded, all or
+ * none.  Errors: INVALID_ARG for a timeout outside the range or NULL lanes.
+ */
+ATTN_API int attn_selftest_warp_wait(uint32_t timeout_us, uint32_t *lanes, attn_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 ATTN_API const char *attn_status_string(int status);
 
