@@ -458,6 +458,14 @@ def attn_selftest_warp_wait(lanes, timeout_us=10000, stream=None):
     _check(fn(timeout_us, _u32_addr(lanes, "lanes"), _stream(stream)), "attn_selftest_warp_wait")
 
 
+def attn_selftest_batch_wait(limit_ns=0):
+    """Limit of the waits inside later attn_batch_paged calls (0: the usual one; see attn_gqa.h)."""
+    fn = load_library().attn_selftest_batch_wait
+    fn.restype = ctypes.c_int
+    fn.argtypes = [_u32]
+    _check(fn(limit_ns), "attn_selftest_batch_wait")
+
+
 def attn_get_status(stream=None):
     """Synchronise `stream`, return and clear the device status word."""
     return int(load_library().attn_get_status(_stream(stream)))

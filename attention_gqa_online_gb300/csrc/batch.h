@@ -102,6 +102,7 @@ struct BatchArgs {
   int window;  // 0 = none
   float scale, softcap;
   FastDiv by_gs, by_page;  // by gs and page_rows; set by launch_batch_paged
+  unsigned wait_ns;        // limit of each wait inside the kernels, 0 = the usual one; set by launch_batch_paged
   int item_cost;           // what an item takes beyond its tiles, in tiles; set by each kernel's launch
 };
 // Sequences of a batch at most (the plan keeps one count each in shared memory).
@@ -117,6 +118,7 @@ inline int kv_l2_bytes(int head_dim) { return (2 * head_dim) & -(2 * head_dim); 
 // Pool rows at most: a box of 256 rows from the first row past the pool still has 31-bit coordinates.
 constexpr uint64_t kMaxBatchPool = 0x7fffffffu - 256;
 size_t batch_workspace_bytes(int D, int sm_count);
+void set_batch_wait_ns(unsigned ns);  // for later launches (the failure-path test)
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s);
 int launch_batch_mma(const BatchArgs& a, int dtype, int blocks, cudaStream_t s);
 int launch_batch_decode(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);

@@ -79,11 +79,13 @@ struct __align__(1024) DecodeSmem {
   plan::Start start;
   long long warp_sums[kThreads / 32];
   int abort;
+  int issued[4];  // tiles whose copies each producer warp issued
+  int share[4];   // bytes of a tile that are a producer warp's
   int go;       // there is a piece
   int is_last;  // this block joins the item
 };
 
-template <typename T, int D>
+template <typename T, int D, bool BRIEF = false>
 __global__ void __launch_bounds__(kThreads, 1)
     batch_decode_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
@@ -123,7 +125,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
   __syncthreads();
   // Warps wait as a whole: lanes that left a wait at different times could arrive for, or part from, the others.
-  auto wait = [&](uint64_t* bar, int phase) { return warp_wait(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  const unsigned long long limit = BRIEF ? a.wait_ns : kWaitLimitNs;
+  auto wait = [&](uint64_t* bar, int phase) {
+    return warp_wait<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
+  };
 
   if (warp >= kConsumers / 32) {
     // ------------------------------------------------------------ producers
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (;; ++x) {
         const DecodeDesc& d = sm.desc[x % kDescs];
-        if (!wait(&sm.desc_full[x % kDescs], x / kDescs) || !warp_whole(&sm.abort) || d.end) return;
+        if (!wait(&sm.desc_full[x % kDescs], x / kDescs) || !warp_whole(&sm.abort) || d.end) break;
         J = load_tiles(d.n, d.seq, d.g, d.lo_min, d.hi_max, d.tile0, J);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
@@ -211,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     plan::Walker<kRows, kKeys> walk(a, sm.start);
     plan::Piece p;
-    while (true) {
+    while (pw == 0) {
       const bool more = walk.next(p) && warp_whole(&sm.abort);
       const int first_row = p.b * kRows;
       const int rows = more ? min(kRows, p.q.q_len * a.gs - first_row) : 0;
@@ -266,12 +271,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++x;
       if (!warp_whole(&sm.abort)) break;
     }
-    // No copy may still be landing in shared memory when the block exits.
-    for (int s = 0; s < S::stages && s < J; ++s) {
-      const int last = s + ((J - 1 - s) / S::stages) * S::stages;
-      mbar_wait_bounded(&sm.full[s], (unsigned)((last / S::stages) & 1), a.status);
+    const int share = __popc(__ballot_sync(0xffffffffu, my_part)) * box_rows * 128;
+    if (lane == 0) {
+      sm.issued[pw] = J;
+      sm.share[pw] = share;
     }
-    for (int y = max(0, x - 2); y < x; ++y) mbar_wait_bounded(&sm.q_ready[y & 1], (unsigned)((y >> 1) & 1), a.status);
+    __syncwarp();
+    named_barrier(2, kThreads);
+    // No copy may still be landing in shared memory when the block exits.  The consumers have read every tile, unless
+    // the pipeline broke.  Then some producers may have issued a tile that others have not: its barrier was armed for
+    // all of them, or not at all.  (They are at most a ring apart, since a slot falls free when a whole tile is read.)
+    if (*(volatile int*)&sm.abort != 0 && tid == kConsumers) {
+      int lo = J, hi = J;
+      for (int w = 1; w < 4; ++w) {
+        lo = min(lo, sm.issued[w]);
+        hi = max(hi, sm.issued[w]);
+      }
+      for (int j = lo; j < hi; ++j) {
+        unsigned missing = 0;
+        for (int w = 0; w < 4; ++w) missing += sm.issued[w] <= j ? sm.share[w] : 0;
+        settle_tile(&sm.full[j % S::stages], J > j, 2 * S::tile_bytes, missing);
+      }
+      drain_ring(sm.full, S::stages, hi, a.status);
+      drain_ring(sm.q_ready, 2, x, a.status);
+    }
     return;
   }
 
@@ -284,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One thread decides for all whether there is a piece: the warps meet at barriers that none may miss.  (The
     // joining buffers are free again after this barrier, too.)
     if (tid == 0)
-      sm.go = wait_phase(&sm.desc_full[x % kDescs], (unsigned)(x / kDescs & 1), a.status, &sm.abort) &&
+      sm.go = wait_phase<BRIEF>(&sm.desc_full[x % kDescs], (unsigned)(x / kDescs & 1), a.status, &sm.abort, limit) &&
               *(volatile int*)&sm.abort == 0 && !d.end;
     __syncwarp();
     named_barrier(1, kConsumers);
@@ -303,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       slope[e] = a.slopes != nullptr ? -kLog2e * a.slopes[d.g * a.gs + f - t * a.gs] : 0.f;
     }
     const int lo_max = d.lo_max, hi_min = rows < kRows ? 0 : d.hi_min;
-    wait(&sm.q_ready[x & 1], x >> 1);
+    bool ok = wait(&sm.q_ready[x & 1], x >> 1);
     uint32_t qa[D / 16][4];
     {
       const uint16_t* q = sm.q[x & 1];
@@ -314,16 +337,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           qa[c][e] = *reinterpret_cast<const uint32_t*>(q + (lr + 8 * (e & 1)) * S::q_stride + 16 * c + lc + 8 * (e >> 1));
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.q_free[x & 1]);
+    // (After a wait that ran out a warp frees no slot any more, since copies may still be landing there, but keeps to
+    // the block's barriers until the next piece.)
+    if (ok && lane == 0) mbar_arrive(&sm.q_free[x & 1]);
     float o[D / 8][4];
 #pragma unroll
     for (int c = 0; c < D / 8; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
 
-    for (int i = (J & 1) ^ grp; i < n; i += 2) {
+    for (int i = (J & 1) ^ grp; ok && i < n; i += 2) {
       const int j = J + i, st = j % S::stages;
-      wait(&sm.full[st], j / S::stages);
+      ok = wait(&sm.full[st], j / S::stages);
+      if (!ok) break;
       const uint32_t k_base = smem_u32(sm.ring[st][0]), v_base = smem_u32(sm.ring[st][1]);
       // With two n-tiles, even and odd column steps accumulate apart: the chain of dependent products is half as long.
       constexpr int kSets = kTiles == 2 ? 2 : 1;
@@ -543,6 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
   }
+  __syncwarp();
+  named_barrier(2, kThreads);  // the producers wait for the last tiles' readers
 }
 
 template <typename T, int D>
@@ -560,6 +588,8 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
       !make_tmap(&tm_v1, a.v_pages, 3, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
   const void* kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D>);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)  // the failure-path test
+    if (a.wait_ns != 0) kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, true>);
   const size_t smem = sizeof(DecodeSmem<D>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;

@@ -16,6 +16,7 @@
 // fetched as boxes of the other kernels' shared-memory swizzle. Bound by its
 // products: 4 sequences of 512 new tokens at 8192, 32 heads over 8 of 96, in
 // 1425 us (as TMA boxes on tcgen05: 221).
+#include <atomic>
 #include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -304,9 +305,13 @@ size_t batch_workspace_bytes(int head_dim, int sm_count) {
          (size_t)4 * ((sm_count + 7) / 8 * 8) * sizeof(unsigned);
 }
 
+static std::atomic<unsigned> g_wait_ns{0};
+void set_batch_wait_ns(unsigned ns) { g_wait_ns = ns; }
+
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s) {
   a.by_gs = fast_div((uint32_t)a.gs);
   a.by_page = fast_div((uint32_t)a.page_rows);
+  a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   a.arrived = static_cast<unsigned*>(workspace);
   a.split = reinterpret_cast<BatchSplit*>(a.arrived + 4 * ((sm_count + 7) / 8 * 8));
   a.partial = reinterpret_cast<float*>(a.split + 2 * sm_count);

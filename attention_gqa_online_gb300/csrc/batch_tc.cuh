@@ -53,7 +53,8 @@
 // eighths of its time, with tile loads and hand-overs alone two thirds.
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
-// MMAs, frees its tensor memory and leaves the status word set.
+// MMAs, frees its tensor memory and leaves the status word set.  A role whose
+// wait ran out frees no slot that copies land in any more.
 #pragma once
 
 #include <cfloat>
@@ -141,6 +142,8 @@ struct __align__(1024) TcSmem {
   long long warp_sums[kTcThreads / 32];
   uint32_t tmem_base;
   int abort;
+  int broken;     // a wait of either block of the pair ran out
+  int issued[3];  // K tiles, V tiles and Q blocks whose copies this block issued
 };
 
 template <int N>
@@ -172,6 +175,20 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 }
 __device__ __forceinline__ void pair_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The same object in block `rank` of the pair: a store to it, a load from it.
+__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void store_in_block(int* p, uint32_t rank, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(in_block(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ int load_in_block(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(in_block(p, rank)) : "memory");
+  return v;
 }
 // Arrives on a barrier of the first block.  These barriers hand over tensor
 // memory only, which tcgen05's own fences order, so neither the arrival needs a
@@ -294,7 +311,7 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uin
 // MODE 0: scores are scale2 * S with scale2 > 0 (folded into the exponent's
 // fma); 1: scaled, with an optional distance bias; 2: capped, with an optional
 // distance bias.
-template <typename T, int D, int MODE, bool PAIR, bool FULL>
+template <typename T, int D, int MODE, bool PAIR, bool FULL, bool BRIEF = false>
 __global__ void __launch_bounds__(kTcThreads, 1)
     batch_tc_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&sm.o_free, PAIR ? 8 : 4);
       mbar_init(&sm.drain[0], 1);
       mbar_init(&sm.drain[1], 1);
-      sm.abort = 0;
+      sm.abort = sm.broken = 0;
     }
     fence_mbar_init();
   }
@@ -357,10 +374,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   // Warps wait as a whole.  Were lanes to leave a wait at different times, one could arrive somewhere for the warp, the
   // barrier complete its next phase and the others wait for a phase that is past.
-  auto wait = [&](uint64_t* bar, int phase) { return warp_wait(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  const unsigned long long limit = BRIEF ? a.wait_ns : kWaitLimitNs;
+  auto wait = [&](uint64_t* bar, int phase) {
+    return warp_wait<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
+  };
   // Without the vote, where no answer is asked for, nothing warp-wide follows at once and a __syncwarp comes before a lane
   // arrives for the warp (17 ragged chunks with a bias, 16 heads: 223 us with votes there too, 219 this way).
-  auto lane_wait = [&](uint64_t* bar, int phase) { wait_phase(bar, (unsigned)(phase & 1), a.status, &sm.abort); };
+  auto lane_wait = [&](uint64_t* bar, int phase) {
+    wait_phase<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
+  };
   // Is there a piece x?  Its descriptor is then valid until every role has released it.  If not, there are no more or
   // the pipeline broke: the role, all lanes of it, leaves.
   auto next_piece = [&](int x) {
@@ -407,14 +429,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       return row;
     };
     auto barrier_of = [&](uint64_t* full) { return PAIR ? in_leader(smem_u32(full)) : smem_u32(full); };
-    // No copy may still be landing in shared memory when the block exits (a pair's copies all complete on the first
-    // block's barriers, and the pair leaves together).
-    auto drain_copies = [&](uint64_t* full, int issued) {
-      for (int s = 0; rank == 0 && s < L::slots && s < issued; ++s) {
-        const int last = s + ((issued - 1 - s) / L::slots) * L::slots;
-        mbar_wait_bounded(&full[s], (unsigned)((last / L::slots) & 1), a.status);
-      }
-    };
     if (warp == 0) {
       // ---------------------------------------------------------- planner, Q and K producer
       if (lane == 0) {
@@ -521,9 +535,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         ++x;
       }
-      drain_copies(sm.k_full, J);
-      for (int y = max(0, x - 2); rank == 0 && (PAIR || q_box) && y < x; ++y)
-        mbar_wait_bounded(&sm.q_ready[y & 1], (unsigned)((y >> 1) & 1), a.status);
+      if (lane == 0) {
+        sm.issued[0] = J;
+        sm.issued[2] = PAIR || q_box ? x : 0;
+      }
     } else if (warp == 3) {
       // ---------------------------------------------------------- V producer
       if (lane == 0) {
@@ -581,9 +596,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+        if (ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
       }
-      drain_copies(sm.v_full, J);
+      if (lane == 0) sm.issued[1] = J;
     } else {
       // ---------------------------------------------------------- MMA issue (the first block's, in a pair)
       // Two warps, one a product, so that neither holds up the other; warp-uniform loops, one elected lane issues.
@@ -614,7 +629,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             commit_all<PAIR>(&sm.s_full[b]);
             commit_all<PAIR>(&sm.k_empty[slot]);
           }
-          commit_all<PAIR>(&sm.q_free[x & 1]);
+          if (ok) commit_all<PAIR>(&sm.q_free[x & 1]);  // (after a failed wait the block may still be landing)
         }
       } else {
         constexpr uint32_t idesc_pv = tc::idesc_f32acc(fmt, true, L::rows, D);
@@ -641,8 +656,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             commit_all<PAIR>(&sm.pv_done[b]);
             commit_all<PAIR>(&sm.v_empty[slot]);
           }
-          commit_all<PAIR>(&sm.o_ready);
-          if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+          if (ok) commit_all<PAIR>(&sm.o_ready);
+          if (ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
         }
       }
       if (rank == 0) {
@@ -1106,10 +1121,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   __syncwarp();
   tc::fence_before_sync();
-  if (PAIR)
-    pair_sync();  // arrivals, commits and copies cross the pair: it leaves together
-  else
+  // No copy may still be landing in shared memory when the block exits.  Products have read every tile, unless the
+  // pipeline broke.
+  if (PAIR) {
+    // Arrivals, commits and copies cross the pair: it leaves together.
+    if (lane == 0 && *(volatile int*)&sm.abort != 0)
+      for (int b = 0; b < 2; ++b) store_in_block(&sm.broken, b, 1);
+    pair_sync();
+    if (*(volatile int*)&sm.broken != 0) {
+      // A tile that only one block issued would never complete: its barrier was armed for both halves, or not at all.
+      // (One block is at most a ring ahead of the other, since a slot falls free by a product that read both halves.)
+      if (rank == 0 && tid == 0) {
+        auto settle = [&](uint64_t* full, int slots, int which, unsigned half) {
+          const int mine = sm.issued[which], other = load_in_block(&sm.issued[which], 1);
+          for (int j = min(mine, other); j < max(mine, other); ++j) settle_tile(&full[j % slots], mine > j, 2 * half, half);
+          drain_ring(full, slots, max(mine, other), a.status);
+        };
+        settle(sm.k_full, L::slots, 0, L::k_bytes);
+        settle(sm.v_full, L::slots, 1, L::v_bytes);
+        settle(sm.q_ready, 2, 2, L::q_bytes);
+      }
+      __syncwarp();
+      pair_sync();
+    }
+    // The first block's last commits arrive here, too.
+    if (rank != 0 && (warp == 1 || warp == 2)) mbar_wait_bounded(&sm.drain[warp - 1], 0, a.status);
+    __syncwarp();
+  } else {
     __syncthreads();
+    if (*(volatile int*)&sm.abort != 0 && tid == 0) {
+      drain_ring(sm.k_full, L::slots, sm.issued[0], a.status);
+      drain_ring(sm.v_full, L::slots, sm.issued[1], a.status);
+      drain_ring(sm.q_ready, 2, sm.issued[2], a.status);
+    }
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     tmem_free_all<PAIR>(tmem);
@@ -1150,6 +1195,9 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
     kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL>);
   else
     kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL>);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)  // the failure-path test
+    if (a.wait_ns != 0 && a.softcap == 0.f && a.slopes == nullptr && sc.scale2 >= FLT_MIN)
+      kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, true>);
   const size_t smem = sizeof(TcSmem<D, PAIR>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;

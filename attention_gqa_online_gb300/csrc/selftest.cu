@@ -5,6 +5,7 @@
 // no fault, no hang, and the CUDA context stays usable.  A second test runs
 // the warp-wide wait of the batched kernels into the same end.
 #include "../../include/attn_gqa.h"
+#include "batch.h"
 #include "batch_wait.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -62,6 +63,12 @@ extern "C" int attn_selftest_wait_timeout(uint32_t timeout_us, attn_stream_t str
   attn::wait_never_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       st, (unsigned long long)timeout_us * 1000ull);
   return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_selftest_batch_wait(uint32_t limit_ns) {
+  if (limit_ns > attn::kWaitLimitNs) return ATTN_ERR_INVALID_ARG;
+  attn::set_batch_wait_ns(limit_ns);
+  return ATTN_OK;
 }
 
 extern "C" int attn_selftest_warp_wait(uint32_t timeout_us, uint32_t* lanes, attn_stream_t stream) {

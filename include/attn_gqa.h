@@ -655,7 +655,15 @@ ATTN_API int attn_selftest_wait_timeout(uint32_t timeout_us, attn_stream_t strea
  * up, seven others wait for a barrier that completes just then.  lanes
  * [8] uint32 (device): the lanes of each warp whose wait succeeded, all or
  * none.  Errors: INVALID_ARG for a timeout outside the range or NULL lanes.
+ *
+ * attn_selftest_batch_wait sets the limit of the waits inside attn_batch_paged's
+ * kernels for this process's later calls in bf16 on pages of whole 8-row groups
+ * (tcgen05: without cap and bias, scale > 0): limit_ns nanoseconds, at most one
+ * second, 0 for the usual one.  With limits of a microsecond waits of an
+ * ordinary call run out: it records ATTN_ERR_TIMEOUT, drains what it has in
+ * flight and returns; its output is not valid.
  */
+ATTN_API int attn_selftest_batch_wait(uint32_t limit_ns);
 ATTN_API int attn_selftest_warp_wait(uint32_t timeout_us, uint32_t *lanes, attn_stream_t stream);
 
 /* Static, human-readable name of a status code. */

@@ -3,6 +3,8 @@ waits that give up within a limit, and the calls after them."""
 import pytest
 import torch
 
+from batch_ref import Batch
+
 pytestmark = pytest.mark.gpu
 
 
@@ -20,3 +22,50 @@ def test_the_lanes_of_a_warp_leave_a_broken_wait_together(cuda_lib):
         with pytest.raises(cuda_lib.AttnError):
             cuda_lib.attn_selftest_warp_wait(lanes, bad)
     assert cuda_lib.attn_get_status() == 0
+
+
+@pytest.fixture
+def brief_waits(cuda_lib):
+    """Sets the limit of the waits inside the batched kernels; the usual one is back at the end."""
+    yield cuda_lib.attn_selftest_batch_wait
+    cuda_lib.attn_selftest_batch_wait(0)
+
+
+# One batch per kernel and form: single tokens (whole and part heads, split and whole items), tcgen05 on single
+# multiprocessors and on pairs (Q as boxes and by a warp).
+BROKEN = [
+    dict(H=32, G=8, D=128, new=[1] * 40, kv=[3000] * 40),
+    dict(H=32, G=8, D=128, new=[1], kv=[9000]),
+    dict(H=14, G=2, D=64, new=[1, 1, 1], kv=[5000, 30, 800], softcap=30.0),
+    dict(H=8, G=8, D=96, new=[1] * 9, kv=[700] * 9),
+    dict(H=8, G=2, D=64, new=[300, 2], kv=[4000, 900]),
+    dict(H=10, G=2, D=64, new=[300, 2], kv=[4000, 900]),
+    dict(H=8, G=2, D=40, new=[300, 2], kv=[4000, 900]),
+    dict(H=32, G=8, D=128, new=[8, 1, 4], kv=[9000, 70, 300]),
+    dict(H=32, G=8, D=96, new=[8, 1, 4], kv=[9000, 70, 300]),
+    dict(H=32, G=8, D=128, new=[700, 256], kv=[4000, 256]),
+    dict(H=16, G=16, D=128, new=[700, 600], kv=[2000, 600]),
+    dict(H=32, G=8, D=96, new=[700, 256], kv=[4000, 256]),
+]
+
+
+@pytest.mark.parametrize("case", BROKEN, ids=lambda c: "H%d-G%d-D%d-%d" % (c["H"], c["G"], c["D"], sum(c["new"])))
+def test_calls_whose_waits_run_out_end_and_leave_later_calls_right(cuda_lib, brief_waits, case):
+    """Waits of ordinary calls run out within nanoseconds to tens of microseconds, wherever the pipeline is then: each
+    call ends, with ATTN_ERR_TIMEOUT or a result, and the next call on a fresh workspace has its usual bits."""
+    A, kw = cuda_lib, dict(case)
+    b = Batch(kw.pop("new"), kw.pop("kv"), kw.pop("H"), kw.pop("G"), kw.pop("D"), 32, torch.bfloat16, seed=71)
+    want = A.attend_paged(b.object(A), b.q, b.k, b.v, **kw)
+    assert A.attn_get_status() == 0
+    ran_out = 0
+    for ns in (1, 100, 300, 1000, 3000, 10000, 30000) * 4:
+        brief_waits(ns)
+        got = A.attend_paged(b.object(A), b.q, b.k, b.v, **kw)
+        status = A.attn_get_status()
+        brief_waits(0)
+        assert status in (0, A.ATTN_ERR_TIMEOUT)
+        assert status or torch.equal(got, want)
+        ran_out += status != 0
+        again = A.attend_paged(b.object(A), b.q, b.k, b.v, **kw)
+        assert A.attn_get_status() == 0 and torch.equal(again, want)
+    assert ran_out
