@@ -94,7 +94,10 @@ struct BatchArgs {
   unsigned* status;
   float* partial;     // [2 * blocks][rows * (D + 2)]: unnormalised output, then (max, sum) of each row
   BatchSplit* split;  // [blocks]
-  unsigned* arrived;  // pieces seen of the item that starts in a block (four a multiprocessor); zero between calls
+  // Pieces seen of the item that starts in a block (four counters a multiprocessor), under the call's tag: counts that a
+  // call left, because its waits ran out, are older than any later tag.
+  unsigned long long* arrived;
+  unsigned long long* calls;  // calls begun on this workspace, in units of 2^16 (batch_plan.cuh: begin_call)
   long long q_stride, out_stride, kv_dim;  // elements
   uint32_t total_rows;
   int n_seqs, H, G, D, gs;

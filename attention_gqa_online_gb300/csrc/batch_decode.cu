@@ -19,7 +19,7 @@
 //
 // At a piece's end the eight states are joined in shared memory, in two steps.
 // Pieces of a split item go to the workspace; the block that arrives last (a
-// counter per item, left at zero again) joins them in key order, so one launch
+// counter per item, which each call numbers anew) joins them in key order, so one launch
 // does everything and results do not depend on the order of arrival.
 //
 // Bound by HBM on large batches: 64 sequences of up to 16384 positions, 8 kv
@@ -78,6 +78,7 @@ struct __align__(1024) DecodeSmem {
   DecodeDesc desc[kDescs];
   plan::Start start;
   long long warp_sums[kThreads / 32];
+  unsigned long long tag;  // this call's (plan::begin_call)
   int abort;
   int issued[4];  // tiles whose copies each producer warp issued
   int share[4];   // bytes of a tile that are a producer warp's
@@ -120,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Columns of Q past the head stay zeros.
   for (int i = tid; i < 2 * kRows * S::q_stride; i += kThreads) sm.q[0][i] = 0;
   grid_dependency_wait();  // lengths, tables and pages may be the previous kernel's output
+  if (tid == 32) sm.tag = plan::begin_call(a);
   plan::make_plan<kRows, S::keys, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
                                           &sm.start);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
@@ -533,10 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_barrier(1, kConsumers);
       if (tid == 0) {
         // Releases the block's part (its writes are ordered before by the barrier) and acquires the others'.
-        unsigned seen;
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.arrived + d.first) : "memory");
-        sm.is_last = seen == (unsigned)(d.last - d.first);
-        if (sm.is_last) a.arrived[d.first] = 0u;  // for the next call
+        sm.is_last = plan::piece_arrives(a.arrived + d.first, sm.tag) == (unsigned)(d.last - d.first);
       }
       named_barrier(1, kConsumers);
       if (sm.is_last && mine) {

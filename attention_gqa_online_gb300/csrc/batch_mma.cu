@@ -298,11 +298,12 @@ static int launch_batch_combine(const BatchArgs& a, int dtype, int blocks, cudaS
   return dtype == ATTN_DT_BF16 ? launch_combine_t<__nv_bfloat16>(a, blocks, s) : launch_combine_t<__half>(a, blocks, s);
 }
 
-// Arrival counters, split records, and partial slots (two a thread block; at most 128 rows a multiprocessor).
+// Calls begun (a line of its own), arrival counters, split records, and partial slots (two a thread block; at most 128 rows a multiprocessor).
+constexpr size_t kCallsBytes = 128;
 size_t batch_workspace_bytes(int head_dim, int sm_count) {
   const int D = head_dim <= 64 ? 64 : 128;  // as the kernels round it up
   return (size_t)2 * sm_count * 128 * (D + 2) * sizeof(float) + (size_t)2 * sm_count * sizeof(BatchSplit) +
-         (size_t)4 * ((sm_count + 7) / 8 * 8) * sizeof(unsigned);
+         (size_t)4 * ((sm_count + 7) / 8 * 8) * sizeof(unsigned long long) + kCallsBytes;
 }
 
 static std::atomic<unsigned> g_wait_ns{0};
@@ -312,7 +313,8 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   a.by_gs = fast_div((uint32_t)a.gs);
   a.by_page = fast_div((uint32_t)a.page_rows);
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
-  a.arrived = static_cast<unsigned*>(workspace);
+  a.calls = static_cast<unsigned long long*>(workspace);
+  a.arrived = a.calls + kCallsBytes / sizeof(unsigned long long);
   a.split = reinterpret_cast<BatchSplit*>(a.arrived + 4 * ((sm_count + 7) / 8 * 8));
   a.partial = reinterpret_cast<float*>(a.split + 2 * sm_count);
   // Pages move by TMA boxes of the largest power of two of rows that divides a

@@ -266,6 +266,25 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
   __syncthreads();
 }
 
+// The call's tag, one larger (by 2^16) than any before on this workspace.  Each block adds its part of 2^16, once, so
+// until the last has all read the same multiple; nothing has to be put back, whatever becomes of the call.
+__device__ __forceinline__ unsigned long long begin_call(const BatchArgs& a) {
+  const unsigned long long mine = blockIdx.x == 0 ? 65536ull - (gridDim.x - 1) : 1ull;
+  return (atomicAdd(a.calls, mine) >> 16) << 16;
+}
+// One more piece of the item that begins in counter `c`'s block: how many were seen before.  Releases what the thread
+// (and those that it is ordered after) wrote, acquires what the earlier pieces' threads did.
+__device__ __forceinline__ unsigned piece_arrives(unsigned long long* c, unsigned long long tag) {
+  unsigned long long seen;
+  asm volatile(
+      "red.relaxed.gpu.global.max.u64 [%1], %2;\n\t"
+      "atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;"
+      : "=l"(seen)
+      : "l"(c), "l"(tag)
+      : "memory");
+  return (unsigned)(seen - tag);
+}
+
 // Walks the pieces of a block's range, in order.  Warps of different roles
 // walk it independently and see the same pieces.
 template <int ROWS, int KEYS>

@@ -140,6 +140,7 @@ struct __align__(1024) TcSmem {
   int joins[kDescs];
   plan::Start start;
   long long warp_sums[kTcThreads / 32];
+  unsigned long long tag;  // this call's (plan::begin_call)
   uint32_t tmem_base;
   int abort;
   int broken;     // a wait of either block of the pair ran out
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) tmem_alloc_all<PAIR>(&sm.tmem_base);
   // Lengths, tables and pages may be the previous kernel's output.
   grid_dependency_wait();
+  if (tid == 32) sm.tag = plan::begin_call(a);
   plan::make_plan<L::rows, kTcKeys, kTcThreads>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
   // The plan's scratch is where Q and the K/V tiles land.
   fence_async_smem();
@@ -1027,12 +1029,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (store) *reinterpret_cast<float2*>(part + (long long)L::rows * D - 2 * pr) = make_float2(m_fin, l_row);
         __syncwarp();
         unsigned seen = 0;
-        unsigned* counter = a.arrived + ((PAIR ? 2 * first + rank : first) * 4 + qd);
-        if (lane == 0)  // releases this warp's rows, acquires the other pieces'
-          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(seen) : "l"(counter) : "memory");
+        // Releases this warp's rows, acquires the other pieces'.
+        if (lane == 0) seen = plan::piece_arrives(a.arrived + ((PAIR ? 2 * first + rank : first) * 4 + qd), sm.tag);
         seen = __shfl_sync(0xffffffffu, seen, 0);
         join = seen == (unsigned)(last - first);
-        if (join && lane == 0) *counter = 0u;  // for the next call
       }
       if (qd == 0) {
         if (lane == 0) {

@@ -458,8 +458,8 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  *   alibi_slopes    [n_heads] fp32; prefix_len [n_seqs] uint32 (device), or NULL
  *   workspace       device buffer of attn_batch_paged_workspace_bytes(...)
  *                   bytes, 16-byte aligned.  Zero it once (cudaMemset) before
- *                   its first use; each completed call leaves it ready for the
- *                   next, of any sizes.  Calls that share it must not overlap on the GPU.
+ *                   its first use; each call leaves it ready for the next, of
+ *                   any sizes, also one that recorded ATTN_ERR_TIMEOUT.  Calls that share it must not overlap on the GPU.
  * Scores, softmax and sums are fp32; P is rounded to dtype for the second
  * product.  The work is divided over the GPU by each row block's number of key
  * tiles, splitting keys where rows are few; splits are joined in key order,

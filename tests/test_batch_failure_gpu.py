@@ -69,3 +69,34 @@ def test_calls_whose_waits_run_out_end_and_leave_later_calls_right(cuda_lib, bri
         again = A.attend_paged(b.object(A), b.q, b.k, b.v, **kw)
         assert A.attn_get_status() == 0 and torch.equal(again, want)
     assert ran_out
+
+
+@pytest.mark.parametrize("case", BROKEN, ids=lambda c: "H%d-G%d-D%d-%d" % (c["H"], c["G"], c["D"], sum(c["new"])))
+def test_a_workspace_serves_on_after_a_call_whose_waits_ran_out(cuda_lib, brief_waits, case):
+    """A broken call leaves pieces of split items uncounted; the next calls on its workspace must not count on them."""
+    A, kw = cuda_lib, dict(case)
+    b = Batch(kw.pop("new"), kw.pop("kv"), kw.pop("H"), kw.pop("G"), kw.pop("D"), 32, torch.bfloat16, seed=72)
+    obj = b.object(A)
+    want = A.attend_paged(obj, b.q, b.k, b.v, **kw)
+    for ns in (100, 1000, 2000, 4000, 8000, 16000) * 4:
+        brief_waits(ns)
+        A.attend_paged(obj, b.q, b.k, b.v, **kw)
+        assert A.attn_get_status() in (0, A.ATTN_ERR_TIMEOUT)
+        brief_waits(0)
+        for _ in range(2):
+            again = A.attend_paged(obj, b.q, b.k, b.v, **kw)
+            assert A.attn_get_status() == 0 and torch.equal(again, want)
+
+
+def test_counts_left_in_the_workspace_do_not_reach_a_later_call(cuda_lib):
+    """As above, with the counts of a broken call written by hand: one piece of every item seen."""
+    A = cuda_lib
+    for new, kv in (([1], [9000]), ([8], [9000]), ([300], [6000])):
+        b = Batch(new, kv, 32, 8, 128, 32, torch.bfloat16, seed=73)
+        obj = b.object(A)
+        want = A.attend_paged(obj, b.q, b.k, b.v)
+        for _ in range(3):
+            A.attend_paged(obj, -b.q, b.k, b.v)  # other pieces' results in the workspace
+            obj.workspace[128:128 + 4864].view(torch.int64).fill_(1)
+            assert torch.equal(A.attend_paged(obj, b.q, b.k, b.v), want)
+        assert A.attn_get_status() == 0
