@@ -70,14 +70,17 @@ def _int32(x, name):
     return x.data_ptr()
 
 
-def _run(where, fn, index, stream, args):
-    """Calls library function `fn` with `args` and the stream, on device `index`."""
+def _handle(stream, index):
+    """Raw stream of a call on device `index`."""
     if index < 0:
         raise ValueError("tensors must be in device memory")
     if stream is None:
-        stream = _raw_stream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
+        return _raw_stream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _run(where, fn, index, stream, args):
+    """Calls library function `fn` with `args` and the raw stream, on device `index`."""
     if _current_device() == index:
         code = fn(*args, stream)
     else:
@@ -91,10 +94,12 @@ def _new(make, shape, dtype, device, stream):
     """A result made by torch on the call's stream: the memory and a fill belong to that stream's order."""
     if stream is None:
         return make(shape, dtype=dtype, device=device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_object(stream, device) if isinstance(stream, int) else stream):
         return make(shape, dtype=dtype, device=device)
+
+
+def _stream_object(raw, device):
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
 
 
 def _rows2d(x, name):
@@ -145,7 +150,7 @@ def _rope(x, table, heads, positions, rot_dim, interleaved, out, inverse, stream
         _like(x.dtype, "out", out)
         _same_device(index, out)
     _same_device(index, table, positions)
-    _run("attn_rope_apply", B.load_library().attn_rope_apply, index, stream,
+    _run("attn_rope_apply", B.load_library().attn_rope_apply, index, _handle(stream, index),
          (x.data_ptr(), out.data_ptr(), code, rows, heads, D, rot_dim, xs, ys, 1 if interleaved else 0, pos, tab,
           tab_rows, 1 if inverse else 0))
     return out
@@ -243,7 +248,8 @@ class PagedBatch:
 
     block_table [n_seqs, max_blocks], q_start [n_seqs + 1] and kv_len [n_seqs] are int32 CUDA tensors, kept
     and read on the device at each call (write into them between steps; see attn_gqa.h).  Calls
-    that share a batch object must be ordered on one stream."""
+    that share a batch object, or a workspace (which may be set to another batch's), must be ordered on one
+    stream, which need not be the one that the object was made on."""
 
     def __init__(self, block_table, q_start, kv_len, num_heads, num_kv_heads, head_dim, page_rows):
         if block_table.dim() != 2 or q_start.dim() != 1 or kv_len.dim() != 1 or \
@@ -270,6 +276,24 @@ class PagedBatch:
             if value.numel() != n:
                 raise ValueError("%s must hold %d values" % (name, n))
         object.__setattr__(self, name, value)
+        if name == "workspace":
+            # It is ready, and may be freed, in the order of the stream that is current now; _use_on adds others.
+            made_on = torch.cuda.current_stream(value.device)
+            self._streams = {made_on.cuda_stream}
+            with torch.cuda.stream(made_on):
+                self._ready = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
+
+    def _use_on(self, raw):
+        """Orders the workspace's fill before, and its release after, the calls on another stream.  (A stream under
+        capture cannot wait for what was not captured with it; a graph is replayed after the work before its capture.)"""
+        stream = _stream_object(raw, self.workspace.device)
+        self.workspace.record_stream(stream)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        if self._ready is not None:
+            stream.wait_event(self._ready)
+        self._streams.add(raw)
 
     def same_device(self, index):
         if self._index != index:
@@ -322,7 +346,7 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
         _same_device(index, q, q_out)
     _same_device(index, v_pages, k_new, v_new, table)
     batch.same_device(index)
-    _run("attn_append_paged", B.load_library().attn_append_paged, index, stream,
+    _run("attn_append_paged", B.load_library().attn_append_paged, index, _handle(stream, index),
          (q_ptr, qo_ptr, k_new.data_ptr(), v_new.data_ptr(), code, k_pages.data_ptr(), v_pages.data_ptr(), cache_code,
           batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H, G, D,
           kv_dim, qs, qos, ks, vs, batch.page_rows, num_pages, batch.max_blocks,
@@ -366,6 +390,9 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
     workspace = batch.workspace
     _same_device(index, v_pages, q, out, alibi_slopes, prefix_len, workspace)
     batch.same_device(index)
+    stream = _handle(stream, index)
+    if stream not in batch._streams:
+        batch._use_on(stream)
     _run("attn_batch_paged", B.load_library().attn_batch_paged, index, stream,
          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), code,
           batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H,

@@ -464,3 +464,78 @@ def test_results_made_on_another_stream(cuda_lib):
             assert torch.equal(x, y)
     assert A.append_paged(obj, kn, vn, b.k, b.v, q=b.q, table=table, stream=side).shape == b.q.shape
     torch.cuda.synchronize()
+
+
+def same_memory(make, nbytes):
+    """Runs make() with `nbytes` of freed memory full of ones at hand, which it may be given."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+    return make()
+
+
+@pytest.mark.parametrize("new,kv", [([1], [9000]), ([8], [9000]), ([300, 2], [6000, 700])])
+def test_a_call_on_another_stream_waits_for_the_fresh_workspace(cuda_lib, new, kv):
+    """A batch object made while the current stream is busy, used at once on another stream: split items count their
+    pieces in the workspace, which must have been zeroed by then."""
+    A = cuda_lib
+    b = Batch(new, kv, 32, 8, 128, 32, BF16, seed=81)
+    want = A.attend_paged(b.object(A), b.q, b.k, b.v)
+    nbytes = b.object(A).workspace.numel()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        def make():
+            torch.cuda._sleep(20_000_000)
+            return b.object(A)
+        obj = same_memory(make, nbytes)
+        got = [A.attend_paged(obj, b.q, b.k, b.v, stream=stream) for _ in range(2)]
+        torch.cuda.synchronize()
+        assert A.attn_get_status() == 0
+        for x in got:
+            assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("new,kv", [([1], [9000]), ([8], [9000]), ([300, 2], [6000, 700])])
+def test_a_batch_object_may_go_while_its_call_runs_on_another_stream(cuda_lib, new, kv):
+    """The workspace of a batch object that is dropped after a launch is not given to the current stream's tensors
+    before the call has ended."""
+    A = cuda_lib
+    b = Batch(new, kv, 32, 8, 128, 32, BF16, seed=82)
+    want = A.attend_paged(b.object(A), b.q, b.k, b.v)
+    nbytes = b.object(A).workspace.numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        got = []
+        for _ in range(5):
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(2_000_000)
+            got.append(A.attend_paged(b.object(A), b.q, b.k, b.v, stream=stream))
+            for _ in range(20):
+                torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert A.attn_get_status() == 0
+        for x in got:
+            assert torch.equal(x, want)
+
+
+def test_a_shared_workspace_and_a_captured_call_on_another_stream(cuda_lib):
+    A = cuda_lib
+    b = Batch([8, 1], [9000, 30], 32, 8, 128, 32, BF16, seed=83)
+    obj, other = b.object(A), b.object(A)
+    want = A.attend_paged(obj, b.q, b.k, b.v)
+    other.workspace = obj.workspace
+    side = torch.cuda.Stream()
+    out = torch.zeros_like(b.q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        A.attend_paged(other, b.q, b.k, b.v, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    side.wait_stream(torch.cuda.current_stream())
+    got = A.attend_paged(other, b.q, b.k, b.v, stream=side)
+    torch.cuda.synchronize()
+    assert A.attn_get_status() == 0 and torch.equal(got, want)
