@@ -16,7 +16,7 @@ def rope_table(max_pos, head_dim, base=10000.0, device="cuda", stream=None, scal
     in part, head_dim is the turned part.  scaling ("none", "linear", "ntk", "by_parts") takes factor and,
     by parts, orig_max_pos, beta_fast, beta_slow; attn_factor multiplies every entry (see
     attn_rope_table_scaled in attn_gqa.h)."""
-    t = torch.empty((max_pos, head_dim), device=device, dtype=torch.float32)
+    t = _new(torch.empty, (max_pos, head_dim), torch.float32, device, stream)
     with _on(t):
         if scaling is None:
             B.attn_rope_table(t, max_pos, head_dim, base, stream)

@@ -140,3 +140,24 @@ def test_refusals(cuda_lib):
         A.rope(x, table, 2, out=torch.zeros(8, 64, device="cuda"))
     with pytest.raises(ValueError):
         A.rope_table(4, 64, scaling="cubic")
+
+
+@pytest.mark.parametrize("scaling", [None, "linear"])
+def test_a_table_made_on_another_stream(cuda_lib, scaling):
+    """Its memory belongs to that stream's order: what the current stream still does with memory that was freed there
+    cannot reach it."""
+    A = cuda_lib
+    kw = {} if scaling is None else dict(scaling=scaling, factor=2.0)
+    want = A.rope_table(4096, 128, **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.empty_cache()
+        for _ in range(4):
+            junk = torch.empty(4096, 128, device="cuda")
+            torch.cuda._sleep(2_000_000)
+            junk.fill_(7.0)
+            del junk
+            got = A.rope_table(4096, 128, stream=stream, **kw)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
