@@ -16,13 +16,17 @@ def rope_table(max_pos, head_dim, base=10000.0, device="cuda", stream=None, scal
     in part, head_dim is the turned part.  scaling ("none", "linear", "ntk", "by_parts") takes factor and,
     by parts, orig_max_pos, beta_fast, beta_slow; attn_factor multiplies every entry (see
     attn_rope_table_scaled in attn_gqa.h)."""
+    if scaling is None and (factor != 1.0 or orig_max_pos != 0 or beta_fast != 32.0 or beta_slow != 1.0):
+        raise ValueError("factor, orig_max_pos, beta_fast and beta_slow need a scaling")
+    if scaling is None and attn_factor != 1.0:
+        scaling = "none"
+    if scaling is not None and scaling not in _SCALINGS:
+        raise ValueError("scaling must be one of %s" % ", ".join(sorted(_SCALINGS)))
     t = _new(torch.empty, (max_pos, head_dim), torch.float32, device, stream)
     with _on(t):
         if scaling is None:
             B.attn_rope_table(t, max_pos, head_dim, base, stream)
         else:
-            if scaling not in _SCALINGS:
-                raise ValueError("scaling must be one of %s" % ", ".join(sorted(_SCALINGS)))
             B.attn_rope_table_scaled(t, max_pos, head_dim, base, _SCALINGS[scaling], factor, orig_max_pos, beta_fast,
                                      beta_slow, attn_factor, stream)
     return t

@@ -195,6 +195,16 @@ def test_python_layer_refuses_sizes_that_do_not_fit_32_bits(lib):
             A.rope(x, table, 1)
 
 
+@hidden
+@pytest.mark.parametrize("kw", [dict(factor=4.0), dict(orig_max_pos=4096), dict(beta_fast=16.0), dict(beta_slow=2.0),
+                                dict(factor=4.0, attn_factor=1.2), dict(scaling="yarn", factor=2.0)])
+def test_rope_table_refuses_what_it_would_not_use(lib, kw):
+    """Values that belong to a scaling, without one, and scalings that do not exist: before memory is asked for."""
+    import attention_gqa_online_gb300 as A
+    with pytest.raises(ValueError, match="scaling"):
+        A.rope_table(16, 64, **kw)
+
+
 def test_refusals_run_with_the_device_hidden():
     if not gpu_visible():
         pytest.skip("no GPU visible: the tests above run in this process")

@@ -161,3 +161,11 @@ def test_a_table_made_on_another_stream(cuda_lib, scaling):
             got = A.rope_table(4096, 128, stream=stream, **kw)
             torch.cuda.synchronize()
             assert torch.equal(got, want)
+
+
+def test_a_table_without_a_scaling_carries_its_factor(cuda_lib):
+    """attn_factor multiplies every entry, with or without a scaling: one rounding of a product with 1.5."""
+    A = cuda_lib
+    got, plain = A.rope_table(100, 64, attn_factor=1.5), A.rope_table(100, 64)
+    assert ((got.double() - 1.5 * plain.double()).abs() <= 3 * 2.0 ** -24).all()
+    assert torch.equal(got, A.rope_table(100, 64, scaling="none", attn_factor=1.5))
