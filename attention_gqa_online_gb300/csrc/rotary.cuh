@@ -119,14 +119,17 @@ __device__ __forceinline__ void move_unit_vec(const TI* x, TO* y, int u, int D, 
     store8<STREAM>(y + d, a);
     return;
   }
+  if (!ok) {  // (not 0 * x: x may hold NaN or infinities)
+    const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    store8<STREAM>(y + 8 * u, z);
+    if (!INTER) store8<STREAM>(y + R / 2 + 8 * u, z);
+    return;
+  }
   if (INTER) {
     float a[8], o[8];
     load8(x + 8 * u, a);
-    float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
-    if (ok) {
-      c = *reinterpret_cast<const float4*>(tab + 4 * u);
-      s = *reinterpret_cast<const float4*>(tab + R / 2 + 4 * u);
-    }
+    const float4 c = *reinterpret_cast<const float4*>(tab + 4 * u);
+    const float4 s = *reinterpret_cast<const float4*>(tab + R / 2 + 4 * u);
     const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -139,13 +142,8 @@ __device__ __forceinline__ void move_unit_vec(const TI* x, TO* y, int u, int D, 
     float a[8], b[8], c[8], s[8];
     load8(x + 8 * u, a);
     load8(x + R / 2 + 8 * u, b);
-    if (ok) {
-      load8_table(tab + 8 * u, c);
-      load8_table(tab + R / 2 + 8 * u, s);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = s[i] = 0.f;
-    }
+    load8_table(tab + 8 * u, c);
+    load8_table(tab + R / 2 + 8 * u, s);
     float o[8], p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -166,8 +164,11 @@ __device__ __forceinline__ void move_unit_scalar(const TI* x, TO* y, int u, int 
     return;
   }
   const int i0 = INTER ? 2 * u : u, i1 = INTER ? 2 * u + 1 : u + R / 2;
-  const float a = to_f32(x[i0]), b = to_f32(x[i1]);
-  const float c = ok ? tab[u] : 0.f, s = ok ? sgn * tab[R / 2 + u] : 0.f;
+  if (!ok) {
+    y[i0] = y[i1] = from_f32<TO>(0.f);
+    return;
+  }
+  const float a = to_f32(x[i0]), b = to_f32(x[i1]), c = tab[u], s = sgn * tab[R / 2 + u];
   y[i0] = from_f32<TO>(a * c - b * s);
   y[i1] = from_f32<TO>(b * c + a * s);
 }

@@ -169,3 +169,21 @@ def test_a_table_without_a_scaling_carries_its_factor(cuda_lib):
     got, plain = A.rope_table(100, 64, attn_factor=1.5), A.rope_table(100, 64)
     assert ((got.double() - 1.5 * plain.double()).abs() <= 3 * 2.0 ** -24).all()
     assert torch.equal(got, A.rope_table(100, 64, scaling="none", attn_factor=1.5))
+
+
+@pytest.mark.parametrize("D,R", [(64, 64), (80, 48), (33, 6)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_position_past_the_table_writes_zeros_whatever_the_row_holds(cuda_lib, dtype, interleaved, D, R):
+    """NaN and infinities among them; the columns behind the turned part pass."""
+    A = cuda_lib
+    table = A.rope_table(8, R)
+    x = torch.ones(3, 2 * D, device="cuda", dtype=dtype)
+    x[1, ::3], x[1, 1::3], x[1, 2::3] = float("nan"), float("inf"), float("-inf")
+    pos = torch.tensor([7, 8, 0], dtype=torch.int32, device="cuda")
+    for call in (A.rope, A.rope_backward):
+        y = call(x, table, 2, positions=pos, rot_dim=R, interleaved=interleaved)
+        assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG
+        assert (y.view(3, 2, D)[1, :, :R] == 0).all()
+        assert torch.equal(y.view(3, 2, D)[:, :, R:].isnan(), x.view(3, 2, D)[:, :, R:].isnan())
+        assert torch.isfinite(y[[0, 2]].float()).all() and (y.view(3, 2, D)[[0, 2]][..., :R] != 0).any()
