@@ -215,12 +215,17 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
     if (s < a.n_seqs) first_block[s] = (int)(carry + incl - nb);
     carry += sum;
   }
-  const int n_blk = (int)carry;  // at most total_rows * gs / ROWS + n_seqs
+  // Sequences that do not overlap have at most total_rows * gs / ROWS + n_seqs blocks. A q_start that goes up and down
+  // can give every second sequence all the rows: more blocks than 32 bits count, or than a call should take.
+  const bool fits = carry <= (long long)a.total_rows * a.gs / ROWS + a.n_seqs;
+  const int n_blk = fits ? (int)carry : 0;
   if (tid == 0) {
+    if (!fits) record_status(a.status, ATTN_ERR_INVALID_ARG);
     first_block[a.n_seqs] = n_blk;
     start->left = 0;
   }
   __syncthreads();
+  if (!fits) return;
   // Weights of this thread's share of the row blocks (all kv heads of each).
   const int share = (n_blk + THREADS - 1) / THREADS;
   const int i0 = min(n_blk, tid * share), i1 = min(n_blk, i0 + share);

@@ -471,7 +471,8 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  * A block-table entry >= num_pages reads as zeros; it, a kv_len[s] past the
  * capacity (the sequence is cut there) or below its number of new rows (rows
  * before position 0 attend no keys of their own), and a q_start that
- * descends or passes total_rows (the sequence is left out) record
+ * descends or passes total_rows (the sequence is left out, or all of them where
+ * they overlap so often that their blocks of rows are too many) record
  * ATTN_ERR_INVALID_ARG in the status word.  total_rows == 0 or n_seqs == 0 is
  * a no-op.  Errors: INVALID_ARG for NULL pointers, bad heads, sizes or
  * strides, a non-finite scale, a softcap that is negative, above 2e38 or so

@@ -539,3 +539,24 @@ def test_a_shared_workspace_and_a_captured_call_on_another_stream(cuda_lib):
     got = A.attend_paged(other, b.q, b.k, b.v, stream=side)
     torch.cuda.synchronize()
     assert A.attn_get_status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("rows,page_rows,D", [(64, 16, 128), (64, 16, 64), (2000, 32, 128), (2000, 16, 64), (2000, 4, 64)])
+def test_sequences_that_overlap_by_the_hundred_are_left_out(cuda_lib, rows, page_rows, D):
+    """A q_start that goes up and down again gives every second sequence all of the rows: more blocks of rows than the
+    batch can have, which are reported and not counted in 32 bits."""
+    A, n = cuda_lib, 600
+    table = torch.zeros(n, 2, dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, rows] * (n // 2) + [0], dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), 2 * page_rows, dtype=torch.int32, device="cuda")
+    obj = A.PagedBatch(table, starts, lens, 8, 2, D, page_rows)
+    q = torch.ones(rows, 8 * D, dtype=BF16, device="cuda")
+    pool = torch.ones(page_rows, 2 * D, dtype=BF16, device="cuda")
+    out = torch.full_like(q, 5.0)
+    A.attend_paged(obj, q, pool, pool, out=out)
+    assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG
+    assert (out == 5.0).all()
+    obj.q_start = torch.tensor([0] * n + [rows], dtype=torch.int32, device="cuda")
+    obj.kv_len = lens.clamp_min(rows)[:n].clone()  # past the capacity, which cuts it: reported, and computed
+    A.attend_paged(obj, q, pool, pool, out=out)
+    assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG and not (out == 5.0).any()
