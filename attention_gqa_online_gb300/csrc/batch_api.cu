@@ -95,7 +95,8 @@ extern "C" int attn_append_paged(const void* q, void* q_out, const void* k_new, 
   if (num_heads > 0 && (q_stride < wq || q_out_stride < wq || q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
   if (rot_dim % 2 != 0 || rot_dim > head_dim || (rot_dim > 0 && (table == nullptr || table_rows == 0)))
     return ATTN_ERR_INVALID_ARG;
-  if (total_rows > 0x7fffffffu || n_seqs > 0x7fffffffu) return ATTN_ERR_INVALID_ARG;
+  // (The search of a row's sequence adds to n_seqs in 32 bits.)
+  if (total_rows > 0x7fffffffu || n_seqs > (1u << 30)) return ATTN_ERR_INVALID_ARG;
   if (total_rows == 0 || n_seqs == 0) return ATTN_OK;
   if (k_new == nullptr || v_new == nullptr || k_pages == nullptr || v_pages == nullptr || block_table == nullptr ||
       q_start == nullptr || kv_len == nullptr)

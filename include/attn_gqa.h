@@ -428,7 +428,8 @@ ATTN_API int attn_rope_apply(const void *x, void *y, attn_dtype_t dtype, uint32_
  * n_seqs == 0 is a no-op.  q_out may be q when types and strides are the
  * same (else ATTN_ERR_INVALID_ARG); otherwise they must not overlap.
  * Errors: INVALID_ARG for NULL pointers, addresses not
- * aligned to their element, bad heads, sizes, types, layout or strides.
+ * aligned to their element, bad heads, sizes, types, layout or strides,
+ * total_rows >= 2^31 or n_seqs > 2^30.
  */
 ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, const void *v_new, attn_dtype_t dtype,
                                void *k_pages, void *v_pages, attn_dtype_t cache_dtype, const uint32_t *block_table,

@@ -196,6 +196,13 @@ def test_python_layer_refuses_sizes_that_do_not_fit_32_bits(lib):
 
 
 @hidden
+@pytest.mark.parametrize("n", [2 ** 30 + 1, 2 ** 31 - 32, 2 ** 31 - 1])
+def test_append_rejects_counts_that_its_search_cannot_add_to(lib, n):
+    """The search of a row's sequence rounds up n_seqs / 32 in 32-bit arithmetic."""
+    assert append_call(lib, n=n, k=FAKE + 0x1000) == BAD
+
+
+@hidden
 @pytest.mark.parametrize("kw", [dict(factor=4.0), dict(orig_max_pos=4096), dict(beta_fast=16.0), dict(beta_slow=2.0),
                                 dict(factor=4.0, attn_factor=1.2), dict(scaling="yarn", factor=2.0)])
 def test_rope_table_refuses_what_it_would_not_use(lib, kw):
