@@ -158,7 +158,7 @@ extern "C" int attn_batch_paged(const void* q, const void* k_pages, const void* 
   if (kv_dim < (uint64_t)n_kv_heads * head_dim || q_stride < (uint64_t)n_heads * head_dim ||
       out_stride < (uint64_t)n_heads * head_dim)
     return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap * 1.5f)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * 1.5f) || !(softcap >= 0.f) || !std::isfinite(softcap * 1.5f)) return ATTN_ERR_INVALID_ARG;
   if (softcap > 0.f && !std::isfinite(scale / softcap)) return ATTN_ERR_INVALID_ARG;
   if (total_rows == 0 || n_seqs == 0) return ATTN_OK;
   if (q == nullptr || k_pages == nullptr || v_pages == nullptr || out == nullptr || block_table == nullptr ||

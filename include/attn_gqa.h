@@ -476,7 +476,7 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  * they overlap so often that their blocks of rows are too many) record
  * ATTN_ERR_INVALID_ARG in the status word.  total_rows == 0 or n_seqs == 0 is
  * a no-op.  Errors: INVALID_ARG for NULL pointers, bad heads, sizes or
- * strides, a non-finite scale, a softcap that is negative, above 2e38 or so
+ * strides, a scale that is not finite or beyond 2e38, a softcap that is negative, above 2e38 or so
  * small that scale / softcap is not finite, or a workspace that is too small or
  * misaligned; UNSUPPORTED for
  * ATTN_DT_F32 (attn_decode_paged and attn_prefill_paged serve fp32 pools),

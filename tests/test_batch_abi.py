@@ -179,6 +179,13 @@ def test_batch_rejects_caps_outside_the_range_of_its_arithmetic(lib, kw):
 
 
 @hidden
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_batch_rejects_scales_outside_the_range_of_its_arithmetic(lib, scale):
+    """scale log2 e has to be finite: infinite, it would make NaN of zero scores."""
+    assert batch_call(lib, scale=scale) == BAD
+
+
+@hidden
 def test_batch_refuses_pools_whose_last_boxes_pass_31_bits(lib):
     assert batch_call(lib, page_rows=2 ** 8, pages=2 ** 23 - 1) == UNSUP
 
