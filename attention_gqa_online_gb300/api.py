@@ -276,9 +276,14 @@ class PagedBatch:
         if name in ("block_table", "q_start", "kv_len"):
             _int32(value, name)
             _same_device(self._index, value)
-            n = {"block_table": self.n_seqs * self.max_blocks, "q_start": self.n_seqs + 1, "kv_len": self.n_seqs}[name]
-            if value.numel() != n:
-                raise ValueError("%s must hold %d values" % (name, n))
+            shape = {"block_table": (self.n_seqs, self.max_blocks), "q_start": (self.n_seqs + 1,),
+                     "kv_len": (self.n_seqs,)}[name]
+            if value.shape != shape:
+                raise ValueError("%s must be %s, got %s" % (name, list(shape), list(value.shape)))
+        elif name in ("n_seqs", "max_blocks") and name in self.__dict__:
+            raise AttributeError("%s is the size of the batch's tensors" % name)
+        elif name == "workspace" and not value.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         object.__setattr__(self, name, value)
         if name == "workspace":
             # It is ready, and may be freed, in the order of the stream that is current now; _use_on adds others.

@@ -210,6 +210,27 @@ def test_append_rejects_counts_that_its_search_cannot_add_to(lib, n):
 
 
 @hidden
+def test_batch_objects_keep_sizes_and_tensors_together(lib):
+    """What the device reads follows from the tensors' shapes: sizes are not set apart from them.  (The object is
+    made without its tensors, which would have to be in device memory.)"""
+    import torch
+    import attention_gqa_online_gb300 as A
+    b = object.__new__(A.PagedBatch)
+    for name, value in dict(_index=-1, n_seqs=2, max_blocks=3, workspace=None).items():
+        object.__setattr__(b, name, value)
+    i32 = dict(dtype=torch.int32)
+    b.block_table, b.q_start, b.kv_len = torch.zeros(2, 3, **i32), torch.zeros(3, **i32), torch.zeros(2, **i32)
+    for name, value in (("n_seqs", 3), ("max_blocks", 4), ("block_table", torch.zeros(3, 2, **i32)),
+                        ("block_table", torch.zeros(6, **i32)), ("q_start", torch.zeros(4, **i32)),
+                        ("q_start", torch.zeros(3, 1, **i32)), ("kv_len", torch.zeros(2)),
+                        ("workspace", torch.zeros(1, dtype=torch.uint8).expand(1 << 20))):
+        before = getattr(b, name)
+        with pytest.raises((AttributeError, ValueError)):
+            setattr(b, name, value)
+        assert getattr(b, name) is before
+
+
+@hidden
 @pytest.mark.parametrize("kw", [dict(factor=4.0), dict(orig_max_pos=4096), dict(beta_fast=16.0), dict(beta_slow=2.0),
                                 dict(factor=4.0, attn_factor=1.2), dict(scaling="yarn", factor=2.0)])
 def test_rope_table_refuses_what_it_would_not_use(lib, kw):
