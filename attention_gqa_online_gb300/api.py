@@ -42,8 +42,9 @@ def _on(x, *others):
 # the GPU: they check with the cheapest queries and hand addresses to the library directly.
 _CODES = {torch.float32: B.ATTN_DT_F32, torch.bfloat16: B.ATTN_DT_BF16, torch.float16: B.ATTN_DT_F16}
 _INT32 = (torch.int32, torch.uint32)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _same_device(index, *tensors):

@@ -209,6 +209,14 @@ def test_append_rejects_counts_that_its_search_cannot_add_to(lib, n):
     assert append_call(lib, n=n, k=FAKE + 0x1000) == BAD
 
 
+def test_the_package_imports_under_a_torch_without_cuda():
+    """torch's private CUDA queries, which such a build lacks, are only a shorter way to the public ones."""
+    code = ("import torch\nfor n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n    delattr(torch._C, n)\n"
+            "import attention_gqa_online_gb300 as A\nprint('imported', A.api._current_device.__name__)")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.stdout.split() == ["imported", "current_device"], r.stderr[-2000:]
+
+
 @hidden
 def test_batch_objects_keep_sizes_and_tensors_together(lib):
     """What the device reads follows from the tensors' shapes: sizes are not set apart from them.  (The object is
