@@ -20,6 +20,7 @@ def rope_table(max_pos, head_dim, base=10000.0, device="cuda", stream=None, scal
         raise ValueError("factor, orig_max_pos, beta_fast and beta_slow need a scaling")
     if scaling is None and attn_factor != 1.0:
         scaling = "none"
+    _count32("orig_max_pos", orig_max_pos)
     if scaling is not None and scaling not in _SCALINGS:
         raise ValueError("scaling must be one of %s" % ", ".join(sorted(_SCALINGS)))
     t = _new(torch.empty, (max_pos, head_dim), torch.float32, device, stream)
@@ -52,6 +53,12 @@ def _same_device(index, *tensors):
         if t is not None and t.get_device() != index:
             raise ValueError("tensors of one call must be on one CUDA device, got cuda:%d and %s" % (index, t.device)
                              if index >= 0 else "tensors must be in device memory, got %s" % t.device)
+
+
+def _count32(name, value):
+    """Checks what ctypes would cut to 32 bits."""
+    if not 0 <= value < 1 << 32:
+        raise ValueError("%s must be from 0 to 2^32 - 1, got %d" % (name, value))
 
 
 def _code(x, name):
@@ -394,6 +401,8 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
         slopes = alibi_slopes.data_ptr()
     if prefix_len is not None and prefix_len.numel() != batch.n_seqs:
         raise ValueError("prefix_len must hold one length a sequence")
+    if window:
+        _count32("window", window)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     index = k_pages.get_device()

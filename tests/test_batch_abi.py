@@ -209,6 +209,22 @@ def test_append_rejects_counts_that_its_search_cannot_add_to(lib, n):
     assert append_call(lib, n=n, k=FAKE + 0x1000) == BAD
 
 
+@hidden
+@pytest.mark.parametrize("value", [2 ** 32, 2 ** 32 + 5, -1])
+def test_python_layer_refuses_counts_that_would_wrap_in_32_bits(lib, value):
+    """ctypes keeps the low 32 bits of what it is given: a window of 2^32 + 5 became one of 5."""
+    import torch
+    import attention_gqa_online_gb300 as A
+    b = object.__new__(A.PagedBatch)
+    for name, x in dict(_index=-1, n_seqs=1, max_blocks=1, num_heads=1, num_kv_heads=1, head_dim=8, page_rows=8).items():
+        object.__setattr__(b, name, x)
+    q, pool = torch.zeros(1, 8, dtype=torch.bfloat16), torch.zeros(8, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="window"):
+        A.attend_paged(b, q, pool, pool, out=q.clone(), window=value)
+    with pytest.raises(ValueError, match="orig_max_pos"):
+        A.rope_table(16, 64, scaling="by_parts", factor=2.0, orig_max_pos=value)
+
+
 def test_the_package_imports_under_a_torch_without_cuda():
     """torch's private CUDA queries, which such a build lacks, are only a shorter way to the public ones."""
     code = ("import torch\nfor n in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n    delattr(torch._C, n)\n"
