@@ -328,7 +328,7 @@ class PagedBatch:
 def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, table=None, rot_dim=None,
                  interleaved=False, stream=None):
     """Write the batch's new K (turned by `table`, when given) and V rows into the pages; with q, also
-    return it turned, in the cache's type (q_out when given)."""
+    return it turned, in the cache's type (in q_out when given; else rows that are not written are zeros)."""
     kv_dim, num_pages = batch.pool(k_pages, v_pages)
     D, G = batch.head_dim, batch.num_kv_heads
     rows, columns, ks = _rows2d(k_new, "k_new")
@@ -352,7 +352,7 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
             raise ValueError("q must be [%d, %d]" % (rows, H * D))
         _like(dtype, "q", q)
         if q_out is None:
-            q_out = _new(torch.empty, (rows, H * D), cache, q.device, stream)
+            q_out = _new(torch.zeros, (rows, H * D), cache, q.device, stream)
             qos = H * D
         else:
             o_rows, o_columns, qos = _rows2d(q_out, "q_out")

@@ -204,3 +204,22 @@ def test_refusals(cuda_lib):
             A.append_paged(obj, **args)
     with pytest.raises(A.AttnError):  # bf16 rows into an fp32 cache
         A.append_paged(obj, k, k, b.k.float(), b.v.float())
+
+
+@pytest.mark.parametrize("src,cache", [(BF16, BF16), (F32, F16)])
+def test_a_result_the_call_makes_holds_zeros_where_no_row_is_written(cuda_lib, src, cache):
+    """Rows behind the last sequence, and rows that are skipped, in a padded batch's q: zeros as attend_paged gives,
+    not what the memory held before."""
+    A = cuda_lib
+    b = Batch([2, 3], [10, 20], 4, 2, 64, 16, cache, seed=9, pad=6, junk=0.0)
+    k, v, q = (torch.ones(b.rows, w * 64, dtype=src, device="cuda") for w in (2, 2, 4))
+    for lens, skipped in (([10, 20], []), ([1, 20], [0])):
+        obj = b.object(A, kv_len=b.dev(lens))
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        torch.full((b.rows, 4 * 64), 7.0, dtype=cache, device="cuda")
+        got = A.append_paged(obj, k, v, b.k, b.v, q=q)
+        assert A.attn_get_status() == (A.ATTN_ERR_INVALID_ARG if skipped else 0)
+        want = torch.ones(b.rows, 4 * 64, dtype=cache, device="cuda")
+        want[skipped + list(range(5, b.rows))] = 0.0
+        assert torch.equal(got, want)
