@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int box_rows) {
   using S = DecodeSmem<D>;
   constexpr bool kHalf = std::is_same<T, __half>::value;
-  constexpr float kSlack = kHalf ? 8.f : 24.f;  // P <= 2^8 or 2^24: inside the operand type's range
+  constexpr float kSlack = kHalf ? 8.f : 24.f;  // P <= 2^8 (times 2^7) or 2^24: inside the operand type's range
   constexpr int kKeys = S::keys, kChunkBytes = kKeys * 128;
   constexpr int kTiles = S::warp_keys / 8, kSteps = S::warp_keys / 16;  // n-tiles of a warp's scores, k-steps of P V
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+      constexpr float kHead = kHalf ? kF16Head : 0.f;
+      const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0] - kHead, m[1] == -INFINITY ? 0.f : m[1] - kHead};
 #pragma unroll
       for (int y = 0; y < kTiles; ++y)
 #pragma unroll

@@ -20,6 +20,7 @@
 #include <cfloat>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "batch.h"
 #include "batch_plan.cuh"
@@ -163,7 +164,8 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
         m[x] = mn;
         l[x] *= corr[x];
       }
-      const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+      constexpr float kHead = std::is_same<T, __half>::value ? kF16Head : 0.f;
+      const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0] - kHead, m[1] == -INFINITY ? 0.f : m[1] - kHead};
 #pragma unroll
       for (int j = 0; j < DP / 8; ++j)
 #pragma unroll

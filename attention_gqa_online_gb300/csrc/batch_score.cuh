@@ -23,6 +23,12 @@ inline ScoreMap score_map(const BatchArgs& a) {
   return m;
 }
 
+// Powers of two on fp16 weights (in the sums, too, so they cancel): against a
+// reference that lags the maximum by up to 2^8 they reach 2^15, and weights
+// down to 2^-21 of the reference keep all their bits; below that each is off by
+// at most 2^-32.  Without it 65536 weights of e^-18 beside a large one vanish.
+constexpr float kF16Head = 7.f;
+
 // tanh with small relative error everywhere, because the cap multiplies it and
 // an exponential follows: for |x| <= 5/8 the odd polynomial x + x u q(u), u =
 // x^2, with q interpolating (tanh(x)/x - 1)/u at the five Chebyshev nodes of

@@ -34,8 +34,9 @@
 // when that exceeds it by more than kRescale (log2 units), so O is rarely
 // rescaled; the reference passes from tile to tile between the two groups,
 // and each group sums its own tiles' P in fp32.  P is rounded to the operand
-// type of V (bf16 <= 2^24, fp16 <= 2^8; both operands of an MMA share a type):
-// an error of half a step per weight, linear in the output.
+// type of V (bf16 <= 2^24, fp16 <= 2^15; both operands of an MMA share a type):
+// an error of half a step per weight, linear in the output (fp16 weights below
+// 2^-21 of the reference: 2^-32 each, kF16Head).
 //
 // End of a piece.  The output warps read O as soon as the last P V lands, and
 // the next piece's first P V waits for that read only; the softmax groups go
@@ -843,7 +844,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           sm.chain[j % kChain][r] = m_new;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.chain_bar[qd][j % kChain]);
-          const float neg_m = (m_new == -INFINITY) ? 0.f : fold - m_new;
+          const float neg_m = (m_new == -INFINITY) ? 0.f : kHalf ? fold - m_new + kF16Head : fold - m_new;
 
           // Exponentials run kLag scores ahead of their sum and packing (in place: packed pair k of a chunk replaces
           // its score k, long done), so the special-function unit, 4 cycles an instruction, is never waited for.

@@ -462,7 +462,8 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  *                   its first use; each call leaves it ready for the next, of
  *                   any sizes, also one that recorded ATTN_ERR_TIMEOUT.  Calls that share it must not overlap on the GPU.
  * Scores, softmax and sums are fp32; P is rounded to dtype for the second
- * product.  The work is divided over the GPU by each row block's number of key
+ * product: half a step of each weight, in fp16 at least 2^-32 of the largest
+ * so far.  The work is divided over the GPU by each row block's number of key
  * tiles, splitting keys where rows are few; splits are joined in key order,
  * so repeated calls give identical bits.
  * What the pages hold at positions that none of a sequence's rows attends, or

@@ -560,3 +560,29 @@ def test_sequences_that_overlap_by_the_hundred_are_left_out(cuda_lib, rows, page
     obj.kv_len = lens.clamp_min(rows)[:n].clone()  # past the capacity, which cuts it: reported, and computed
     A.attend_paged(obj, q, pool, pool, out=out)
     assert A.attn_get_status() == A.ATTN_ERR_INVALID_ARG and not (out == 5.0).any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("new,page_rows,D", [(1, 32, 128), (1, 32, 64), (2, 32, 128), (2, 32, 64), (300, 32, 128),
+                                             (1, 4, 64), (2, 4, 128)])
+def test_many_small_weights_beside_a_large_one(cuda_lib, new, page_rows, D, dtype):
+    """Two keys hold nearly all the weight and zeros in V; 65534 others, e^-18 of them each, hold ones.  Weights are
+    rounded once: to half a step, or in fp16, where they carry 2^7, below 2^-21 of the largest by 2^-32 of it each."""
+    A, n = cuda_lib, 65536
+    seqs = 160 if new < 100 else 60
+    table = torch.arange(n // page_rows, dtype=torch.int32, device="cuda").expand(seqs, -1).contiguous()
+    starts = torch.arange(0, new * seqs + 1, new, dtype=torch.int32, device="cuda")
+    obj = A.PagedBatch(table, starts, torch.full((seqs,), n, dtype=torch.int32, device="cuda"), 1, 1, D, page_rows)
+    q = torch.zeros(new * seqs, D, dtype=dtype, device="cuda")
+    q[:, 0] = 4.5
+    k, v = torch.zeros(n, D, dtype=dtype, device="cuda"), torch.ones(n, D, dtype=dtype, device="cuda")
+    heavy = [0, n - new]
+    k[heavy, 0], v[heavy] = 4.0, 0.0
+    got = A.attend_paged(obj, q, k, v, scale=1.0).view(seqs, new, D)
+    assert A.attn_get_status() == 0
+    light = torch.arange(n - new, n, dtype=torch.float64, device="cuda")[:, None] - 1  # light keys of each row
+    w = torch.exp(torch.tensor(-18.0, dtype=torch.float64, device="cuda"))
+    ref = light * w / (2 + light * w)
+    half = torch.finfo(dtype).eps / 2
+    tol = 1.01 * (2 * half + 2.0 ** -12) * ref + (n * 2.0 ** -32 if dtype == F16 else 0.0)
+    assert ((got.double() - ref).abs() <= tol).all(), float(((got.double() - ref).abs() / tol).max())
