@@ -12,10 +12,12 @@
 // the pages hold there), scores and the running max and sum stay in fp32
 // registers, and P is rounded to the cache's type for the second product.
 //
-// Only pages that are no whole 8-row groups come here: their rows cannot be
-// fetched as boxes of the other kernels' shared-memory swizzle. Bound by its
-// products: 4 sequences of 512 new tokens at 8192, 32 heads over 8 of 96, in
-// 1425 us (as TMA boxes on tcgen05: 221).
+// Only pages that are no whole 8-row groups come here: the other kernels fetch
+// boxes of 8 to 128 rows (they could fetch single rows, as they do at the ends
+// of windows, but have no form of it for whole tiles). Bound by its products and
+// row-wise copies: 2 chunks of 512 at 8192, 32 heads over 8 of 128, bf16, in 767
+// us with pages of 4 rows (tcgen05, pages of 16: 110), 64 single tokens of 8192
+// in 854 (310).
 #include <atomic>
 #include <cfloat>
 #include <cuda_bf16.h>
@@ -326,9 +328,12 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   if (box >= 8) {
     // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 308
     // us at 4 query heads a kv head, 313 at 16 (tcgen05 kernel: 317 and 322); heads of 64: 162 (187); 8 sequences of
-    // 2048: 16 us against 24. More heads a kv head would read K and V once for every 16 of them.
+    // 2048: 16 us against 24. More heads a kv head would read K and V once for every 16 of them. The lengths are on the
+    // device, so a call with as many sequences as rows comes here even if one sequence has them all, and its K and V
+    // are read once for every 16 rows: a chunk of 250 at 4096, 38 us by itself, takes 111 among 255 idle sequences.
     if (a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
-    // Pairs of multiprocessors share K and V tiles between 256 rows, where sequences have that many on average. 16
+    // Pairs of multiprocessors share K and V tiles between 256 rows, where sequences have that many on average (a long
+    // chunk beside many single tokens does not get them: 2048 tokens at 4096 and 63 single tokens 232 us, apart 91 and 158). 16
     // sequences of 4096, 4 heads a kv head of 128, with 32, 64, 128, 256, 512, 1024 rows a kv head: pairs 64, 74, 77,
     // 76, 120, 210 us, single blocks 57, 71, 74, 99, 164, 312.
     if (a.D > 64 && 128 % a.gs == 0 && sm_count % 2 == 0 && (long long)a.total_rows * a.gs >= 256ll * a.n_seqs)

@@ -10,7 +10,8 @@
 // range boundary inside an item splits its keys: each part is a piece, whose
 // unnormalised output and (max, sum) go to a partial slot, and the block that
 // arrives last (batch_mma.cu: a second kernel) joins the pieces of an item in key
-// order (so results do not depend on the order in which blocks run).  An item of at most item_cost tiles is not split:
+// order (so results do not depend on the order in which blocks run; the cuts, and
+// with them a sequence's last bits, depend on the whole batch).  An item of at most item_cost tiles is not split:
 // the block of its first unit takes it whole.
 #pragma once
 

@@ -48,9 +48,10 @@
 // zeros. The same rows of K only make scores that are masked.
 //
 // Bound by the softmax warps: a prompt of 8192, 32 heads over 8 of 128, bf16,
-// takes 392 us (1.40 PFLOP/s, 73% of the measured bf16 rate; tensor pipe 65%
-// busy, special-function unit 33%, issue 47%), two chunks of 512 behind 16k to
-// 32k keys 250 us (71%). With the exponentials left out a chunk took seven
+// takes 391 to 405 us (1.36 to 1.40 PFLOP/s, 71 to 73% of the measured bf16
+// rate; tensor pipe 65% busy, special-function unit 33%, issue 47%), two chunks
+// of 512 behind 16k to 32k keys 251 us (71%), at heads of 64 a prompt 449 us (32%:
+// the softmax takes as long a tile, the products half). With the exponentials left out a chunk took seven
 // eighths of its time, with tile loads and hand-overs alone two thirds.
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
@@ -77,7 +78,9 @@ namespace {
 constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 512;
 // What an item takes beyond its tiles, in tiles; kItemCostRows where a block's rows are no whole tokens (gs does not
 // divide 128) and Q is copied by a warp. At 2, 3, 4, 5: 17 prompts of 512, 32 heads over 8, 123, 110, 99, 99 us; mixed
-// batch of chunks 218, 219, 214, 213; prompt of 8192 alike. At 2, 6, 8, 10 (20 heads over 4): 588, 360, 340, 321.
+// batch of chunks 218, 219, 214, 213; prompt of 8192 alike. kItemCostRows at 2, 4, 7, 10, 16, prompt of 8192 with 20 heads
+// over 4: 588, 453, 344, 324, 321. At 4, 7, 10, 16: 12 heads over 4, the prompt 274, 214, 208, 204, 32 chunks of 100 at 1000
+// 69, 66, 54, 54, 8 x 4 tokens at 4000 24, 24, 25, 28; 14 over 2 of 64: 223, 198, 198, 199; 48, 47, 38, 38; 18, 20, 20, 24.
 constexpr int kItemCost = 4, kItemCostRows = 10;
 constexpr int kDescs = 4;        // piece descriptors in flight
 constexpr int kChain = 4;        // reference maxima in flight

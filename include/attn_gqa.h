@@ -378,7 +378,10 @@ ATTN_API int attn_prefill_paged(const float *q_batch, const float *k_pages, cons
  *                       theta_i / 2 pi - beta_slow) / (beta_fast - beta_slow),
  *                       0, 1): pairs that turn more than beta_fast times over
  *                       the original context keep their angle, those below
- *                       beta_slow are interpolated
+ *                       beta_slow are interpolated.  g is linear in the pair's
+ *                       turns; weights trained with a ramp over the pair's
+ *                       index between two rounded bounds want other angles (a
+ *                       table is only data: fill one accordingly)
  * and m = attn_factor on every entry.  Errors: INVALID_ARG for values outside
  * these rules or max_pos * rot_dim >= 2^31; max_pos == 0 is a no-op.
  */
@@ -424,7 +427,7 @@ ATTN_API int attn_rope_apply(const void *x, void *y, attn_dtype_t dtype, uint32_
  * A row whose position is negative, past the capacity page_rows * max_blocks
  * or past the table, or whose page is >= num_pages, is skipped (nothing of it
  * is written) and ATTN_ERR_INVALID_ARG recorded in the status word.  Two rows
- * that name the same pool row leave one of the two there.  total_rows == 0 or
+ * must not name the same pool row: its elements would come from either.  total_rows == 0 or
  * n_seqs == 0 is a no-op.  q_out may be q when types and strides are the
  * same (else ATTN_ERR_INVALID_ARG); otherwise they must not overlap.
  * Errors: INVALID_ARG for NULL pointers, addresses not
@@ -454,22 +457,27 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  * and writes sum_j softmax(s)_j v_j, rounded to dtype; a row without keys
  * writes zeros.
  *
- *   q, out          [total_rows, ...], rows q_stride / out_stride elements apart
+ *   q, out          [total_rows, ...], rows q_stride / out_stride elements
+ *                   apart; out must not overlap q or the pools
  *   dtype           of q, the pools and out
  *   alibi_slopes    [n_heads] fp32; prefix_len [n_seqs] uint32 (device), or NULL
  *   workspace       device buffer of attn_batch_paged_workspace_bytes(...)
  *                   bytes, 16-byte aligned.  Zero it once (cudaMemset) before
  *                   its first use; each call leaves it ready for the next, of
- *                   any sizes, also one that recorded ATTN_ERR_TIMEOUT.  Calls that share it must not overlap on the GPU.
+ *                   any sizes, also one that recorded ATTN_ERR_TIMEOUT.
+ *                   Calls that share it must not overlap on the GPU.
  * Scores, softmax and sums are fp32; P is rounded to dtype for the second
  * product: half a step of each weight, in fp16 at least 2^-32 of the largest
  * so far.  The work is divided over the GPU by each row block's number of key
  * tiles, splitting keys where rows are few; splits are joined in key order,
- * so repeated calls give identical bits.
+ * so repeated calls of the same batch give identical bits.  (In another batch a
+ * sequence may be cut elsewhere, or run on another of the kernels below, and
+ * its results differ in their last bits.)
  * What the pages hold at positions that none of a sequence's rows attends, or
  * past its end, never reaches a result.  K and V at positions that some row of
- * the sequence attends must be finite (a NaN or infinity there may also reach
- * rows of the same sequence that do not attend it).
+ * the sequence attends must be finite, |v| below 2^79 (sums are fp32, under
+ * weights of up to 2^24; a NaN or infinity may also reach rows of the same
+ * sequence that do not attend it).
  * A block-table entry >= num_pages reads as zeros; it, a kv_len[s] past the
  * capacity (the sequence is cut there) or below its number of new rows (rows
  * before position 0 attend no keys of their own), and a q_start that
@@ -477,10 +485,9 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  * they overlap so often that their blocks of rows are too many) record
  * ATTN_ERR_INVALID_ARG in the status word.  total_rows == 0 or n_seqs == 0 is
  * a no-op.  Errors: INVALID_ARG for NULL pointers, bad heads, sizes or
- * strides, a scale that is not finite or beyond 2e38, a softcap that is negative, above 2e38 or so
- * small that scale / softcap is not finite, or a workspace that is too small or
- * misaligned; UNSUPPORTED for
- * ATTN_DT_F32 (attn_decode_paged and attn_prefill_paged serve fp32 pools),
+ * strides, a scale that is not finite or beyond 2e38, a softcap that is
+ * negative, above 2e38 or so small that scale / softcap is not finite, or a
+ * workspace that is too small or misaligned; UNSUPPORTED for ATTN_DT_F32 (attn_decode_paged and attn_prefill_paged serve fp32 pools),
  * head_dim % 8 != 0, kv_dim or strides % 8 != 0, addresses of q, out or the
  * pools that are not 16-byte aligned, more than 16384 sequences, a capacity of
  * more than 2^24 positions, a pool of more than 2^31 - 257 rows, or total_rows
