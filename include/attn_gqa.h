@@ -427,9 +427,10 @@ ATTN_API int attn_rope_apply(const void *x, void *y, attn_dtype_t dtype, uint32_
  * A row whose position is negative, past the capacity page_rows * max_blocks
  * or past the table, or whose page is >= num_pages, is skipped (nothing of it
  * is written) and ATTN_ERR_INVALID_ARG recorded in the status word.  Two rows
- * must not name the same pool row: its elements would come from either.  total_rows == 0 or
- * n_seqs == 0 is a no-op.  q_out may be q when types and strides are the
- * same (else ATTN_ERR_INVALID_ARG); otherwise they must not overlap.
+ * must not name the same pool row: its elements would come from either.
+ * total_rows == 0 or n_seqs == 0 is a no-op.  q_out may be q when types and
+ * strides are the same (else ATTN_ERR_INVALID_ARG); otherwise they must not
+ * overlap.
  * Errors: INVALID_ARG for NULL pointers, addresses not
  * aligned to their element, bad heads, sizes, types, layout or strides,
  * total_rows >= 2^31 or n_seqs > 2^30.
@@ -487,11 +488,12 @@ ATTN_API int attn_append_paged(const void *q, void *q_out, const void *k_new, co
  * a no-op.  Errors: INVALID_ARG for NULL pointers, bad heads, sizes or
  * strides, a scale that is not finite or beyond 2e38, a softcap that is
  * negative, above 2e38 or so small that scale / softcap is not finite, or a
- * workspace that is too small or misaligned; UNSUPPORTED for ATTN_DT_F32 (attn_decode_paged and attn_prefill_paged serve fp32 pools),
- * head_dim % 8 != 0, kv_dim or strides % 8 != 0, addresses of q, out or the
- * pools that are not 16-byte aligned, more than 16384 sequences, a capacity of
- * more than 2^24 positions, a pool of more than 2^31 - 257 rows, or total_rows
- * * n_heads > 2^30.
+ * workspace that is too small or misaligned; UNSUPPORTED for ATTN_DT_F32
+ * (attn_decode_paged and attn_prefill_paged serve fp32 pools), head_dim % 8 !=
+ * 0, kv_dim or strides % 8 != 0, addresses of q, out or the pools that are not
+ * 16-byte aligned, more than 16384 sequences, a capacity of more than 2^24
+ * positions, a pool of more than 2^31 - 257 rows, or total_rows * n_heads >
+ * 2^30.
  * Kernels: pages of whole 8-row groups (page_rows % 8 == 0) run on the tensor
  * cores (tcgen05) or, for about one row a sequence (total_rows <= n_seqs) with
  * H/G <= 16, on a kernel that streams K and V; other pages on warp-level
