@@ -294,11 +294,16 @@ class PagedBatch:
             raise ValueError("workspace must be contiguous")
         object.__setattr__(self, name, value)
         if name == "workspace":
-            # It is ready, and may be freed, in the order of the stream that is current now; _use_on adds others.
-            made_on = torch.cuda.current_stream(value.device)
-            self._streams = {made_on.cuda_stream}
-            with torch.cuda.stream(made_on):
-                self._ready = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
+            # It is ready in the order of the stream that was current when a batch first took it; _use_on adds others.
+            # (Another batch's workspace comes with its mark.)
+            if not hasattr(value, "_ready_on"):
+                made_on = torch.cuda.current_stream(value.device)
+                value.record_stream(made_on)  # it may have been made elsewhere
+                with torch.cuda.stream(made_on):
+                    ready = None if torch.cuda.is_current_stream_capturing() else made_on.record_event()
+                value._ready_on = made_on.cuda_stream, ready
+            raw, self._ready = value._ready_on
+            self._streams = {raw}
 
     def _use_on(self, raw):
         """Orders the workspace's fill before, and its release after, the calls on another stream.  (A stream under

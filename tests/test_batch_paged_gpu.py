@@ -586,3 +586,38 @@ def test_many_small_weights_beside_a_large_one(cuda_lib, new, page_rows, D, dtyp
     half = torch.finfo(dtype).eps / 2
     tol = 1.01 * (2 * half + 2.0 ** -12) * ref + (n * 2.0 ** -32 if dtype == F16 else 0.0)
     assert ((got.double() - ref).abs() <= tol).all(), float(((got.double() - ref).abs() / tol).max())
+
+
+@pytest.mark.parametrize("new,kv", [([1], [9000]), ([300, 2], [6000, 700])])
+def test_a_workspace_made_on_another_stream_is_ready_and_held(cuda_lib, new, kv):
+    """A batch that takes the workspace of one made on a busy stream waits for its fill there, and holds its memory
+    against that stream's later tensors."""
+    A = cuda_lib
+    b = Batch(new, kv, 32, 8, 128, 32, BF16, seed=84)
+    want = A.attend_paged(b.object(A), b.q, b.k, b.v)
+    nbytes = b.object(A).workspace.numel()
+    side, got = torch.cuda.Stream(), []
+    torch.cuda.synchronize()
+    for kind in ["another batch's", "the caller's"] * 2:
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(side):
+            torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+            torch.cuda._sleep(5_000_000)
+            if kind == "another batch's":
+                workspace = b.object(A).workspace
+            else:
+                workspace = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+        obj = b.object(A)
+        if kind == "the caller's":
+            torch.cuda.current_stream().wait_stream(side)
+        obj.workspace = workspace
+        torch.cuda._sleep(5_000_000)
+        got.append(A.attend_paged(obj, b.q, b.k, b.v))
+        del obj, workspace
+        with torch.cuda.stream(side):
+            for _ in range(5):
+                torch.full((nbytes,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert A.attn_get_status() == 0
+    for x in got:
+        assert torch.equal(x, want)
