@@ -87,6 +87,19 @@ def load_library(path=None):
     lib.attn_batch_paged.restype = ctypes.c_int
     lib.attn_batch_paged.argtypes = [_vp] * 4 + [ctypes.c_int, _vp, _vp, _vp] + [_u32] * 11 + \
         [ctypes.c_float, _u32, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_qk_norm_rope.restype = ctypes.c_int
+    lib.attn_qk_norm_rope.argtypes = [_vp] * 6 + [ctypes.c_int] * 2 + [_u32] * 8 + \
+        [ctypes.c_float, _u32, ctypes.c_int, _vp, _vp, _u32, _vp]
+    lib.attn_qk_norm_rope_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.attn_qk_norm_rope_backward_workspace_bytes.argtypes = [_u32]
+    lib.attn_qk_norm_rope_backward.restype = ctypes.c_int
+    lib.attn_qk_norm_rope_backward.argtypes = [_vp] * 10 + [ctypes.c_int] * 2 + [_u32] * 10 + \
+        [ctypes.c_float, _u32, ctypes.c_int, _vp, _vp, _u32, _vp, ctypes.c_size_t, _vp]
+    lib.attn_append_paged8.restype = ctypes.c_int
+    lib.attn_append_paged8.argtypes = [_vp] * 4 + [ctypes.c_int] * 2 + [_vp] * 7 + [_u32] * 14 + \
+        [_vp, _vp, ctypes.c_int, ctypes.c_float, _u32, ctypes.c_int, _vp, _u32, _vp]
+    lib.attn_read_paged8.restype = ctypes.c_int
+    lib.attn_read_paged8.argtypes = [_vp] * 6 + [ctypes.c_int] + [_vp] * 4 + [_u32] * 11 + [_vp]
     lib.attn_get_status.restype = ctypes.c_int
     lib.attn_get_status.argtypes = [_vp]
     lib.attn_set_workspace.restype = ctypes.c_int
@@ -382,6 +395,90 @@ def attn_batch_paged(q, k_pages, v_pages, out, block_table, q_start, kv_len, tot
         float(scale), window, float(softcap), _addr(alibi_slopes, "alibi_slopes", _f32()),
         _u32_addr(prefix_len, "prefix_len"), _addr(workspace, "workspace"), workspace_bytes, _stream(stream)),
         "attn_batch_paged")
+
+
+def _weight_code(code, **weights):
+    """Type of the weights (the rows' own when there are none)."""
+    found = {_dtype_code(w, name) for name, w in weights.items() if w is not None}
+    if len(found) > 1:
+        raise ValueError("%s must have one type" % " and ".join(weights))
+    return found.pop() if found else code
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, q_weight, k_weight, rows, num_heads, num_kv_heads, head_dim, q_stride,
+                      k_stride, q_out_stride, k_out_stride, eps, rot_dim=0, layout=ATTN_ROPE_HALF, positions=None,
+                      table=None, table_rows=None, stream=None):
+    """Norm and turn the heads of Q and K; see attn_gqa.h."""
+    code = _dtype_code(q if q is not None else k, "q")
+    _same_dtype(code, q=q, k=k, q_out=q_out, k_out=k_out)
+    if table_rows is None:
+        table_rows = 0 if table is None else table.shape[0]
+    _check(load_library().attn_qk_norm_rope(
+        _addr(q, "q"), _addr(k, "k"), _addr(q_out, "q_out"), _addr(k_out, "k_out"), _addr(q_weight, "q_weight"),
+        _addr(k_weight, "k_weight"), code, _weight_code(code, q_weight=q_weight, k_weight=k_weight), rows, num_heads,
+        num_kv_heads, head_dim, q_stride, k_stride, q_out_stride, k_out_stride, float(eps), rot_dim, layout,
+        _u32_addr(positions, "positions"), _addr(table, "table", _f32()), table_rows, _stream(stream)),
+        "attn_qk_norm_rope")
+
+
+def attn_qk_norm_rope_backward_workspace_bytes(head_dim):
+    return int(load_library().attn_qk_norm_rope_backward_workspace_bytes(head_dim))
+
+
+def attn_qk_norm_rope_backward(dq, dk, q, k, dq_out, dk_out, q_weight, k_weight, dq_weight, dk_weight, rows, num_heads,
+                               num_kv_heads, head_dim, dq_stride, dk_stride, q_stride, k_stride, dq_out_stride,
+                               dk_out_stride, eps, rot_dim=0, layout=ATTN_ROPE_HALF, positions=None, table=None,
+                               table_rows=None, workspace=None, workspace_bytes=None, stream=None):
+    """Gradients of attn_qk_norm_rope; see attn_gqa.h."""
+    code = _dtype_code(q if q is not None else k, "q")
+    _same_dtype(code, dq=dq, dk=dk, q=q, k=k, dq_out=dq_out, dk_out=dk_out)
+    if table_rows is None:
+        table_rows = 0 if table is None else table.shape[0]
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().attn_qk_norm_rope_backward(
+        _addr(dq, "dq"), _addr(dk, "dk"), _addr(q, "q"), _addr(k, "k"), _addr(dq_out, "dq_out"),
+        _addr(dk_out, "dk_out"), _addr(q_weight, "q_weight"), _addr(k_weight, "k_weight"),
+        _addr(dq_weight, "dq_weight"), _addr(dk_weight, "dk_weight"), code,
+        _weight_code(code, q_weight=q_weight, k_weight=k_weight, dq_weight=dq_weight, dk_weight=dk_weight), rows,
+        num_heads, num_kv_heads, head_dim, dq_stride, dk_stride, q_stride, k_stride, dq_out_stride, dk_out_stride,
+        float(eps), rot_dim, layout, _u32_addr(positions, "positions"), _addr(table, "table", _f32()), table_rows,
+        _addr(workspace, "workspace"), workspace_bytes, _stream(stream)), "attn_qk_norm_rope_backward")
+
+
+def attn_append_paged8(q, q_out, k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, q_start, kv_len,
+                       total_rows, n_seqs, num_heads, num_kv_heads, head_dim, kv_dim, q_stride, q_out_stride, k_stride,
+                       v_stride, page_rows, num_pages, max_blocks, scale_rows, q_weight=None, k_weight=None, eps=1e-6,
+                       rot_dim=0, layout=ATTN_ROPE_HALF, table=None, table_rows=None, stream=None):
+    """Write a ragged batch's new K (normed, turned) and V rows into an 8-bit cache, and norm and turn Q; see
+    attn_gqa.h."""
+    code = _dtype_code(k_new, "k_new")
+    _same_dtype(code, v_new=v_new, q=q)
+    if table_rows is None:
+        table_rows = 0 if table is None else table.shape[0]
+    _check(load_library().attn_append_paged8(
+        _addr(q, "q"), _addr(q_out, "q_out"), _addr(k_new, "k_new"), _addr(v_new, "v_new"), code,
+        code if q_out is None else _dtype_code(q_out, "q_out"), _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"),
+        _addr(k_scales, "k_scales"), _addr(v_scales, "v_scales"), _u32_addr(block_table, "block_table"),
+        _u32_addr(q_start, "q_start"), _u32_addr(kv_len, "kv_len"), total_rows, n_seqs, num_heads, num_kv_heads,
+        head_dim, kv_dim, q_stride, q_out_stride, k_stride, v_stride, page_rows, num_pages, max_blocks, scale_rows,
+        _addr(q_weight, "q_weight"), _addr(k_weight, "k_weight"),
+        _weight_code(code, q_weight=q_weight, k_weight=k_weight), float(eps), rot_dim, layout,
+        _addr(table, "table", _f32()), table_rows, _stream(stream)), "attn_append_paged8")
+
+
+def attn_read_paged8(k_pages, v_pages, k_scales, v_scales, k_out, v_out, block_table, starts, first, kv_len, total_rows,
+                     n_seqs, num_kv_heads, head_dim, kv_dim, k_stride, v_stride, page_rows, num_pages, max_blocks,
+                     scale_rows, stream=None):
+    """Ranges of the sequences' positions back from an 8-bit cache; see attn_gqa.h."""
+    code = _dtype_code(k_out, "k_out")
+    _same_dtype(code, v_out=v_out)
+    _check(load_library().attn_read_paged8(
+        _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"), _addr(k_scales, "k_scales"),
+        _addr(v_scales, "v_scales"), _addr(k_out, "k_out"), _addr(v_out, "v_out"), code,
+        _u32_addr(block_table, "block_table"), _u32_addr(starts, "starts"), _u32_addr(first, "first"),
+        _u32_addr(kv_len, "kv_len"), total_rows, n_seqs, num_kv_heads, head_dim, kv_dim, k_stride, v_stride, page_rows,
+        num_pages, max_blocks, scale_rows, _stream(stream)), "attn_read_paged8")
 
 
 def attn_decode_cached_noalloc(q, k_cache, v_cache, kv_pos_dev, out, num_heads, num_kv_heads, head_dim, max_seq,

@@ -179,6 +179,113 @@ def rope_backward(dy, table, heads, positions=None, rot_dim=None, interleaved=Fa
     return _rope(dy, table, heads, positions, rot_dim, interleaved, out, True, stream)
 
 
+def _rows_out(out, like, shape, name, stream, make=torch.empty):
+    """(tensor, row stride) of a result like `like`, allocated when out is None."""
+    if out is None:
+        return _new(make, shape, like.dtype, like.device, stream), shape[1]
+    rows, columns, stride = _rows2d(out, name)
+    if (rows, columns) != shape:
+        raise ValueError("%s must be [%d, %d]" % ((name,) + shape))
+    _like(like.dtype, name, out)
+    return out, stride
+
+
+def _heads2d(x, heads, name):
+    rows, columns, stride = _rows2d(x, name)
+    if heads < 1 or columns % heads:
+        raise ValueError("%s has %d columns, not a multiple of %d heads" % (name, columns, heads))
+    return rows, columns // heads, stride
+
+
+def _weights(D, **weights):
+    """Type code of the weight vectors (0 when there are none)."""
+    code = None
+    for name, w in weights.items():
+        if w is None:
+            continue
+        if w.shape != (D,) or not w.is_contiguous():
+            raise ValueError("%s must be a contiguous vector of %d" % (name, D))
+        if code is not None and code != _code(w, name):
+            raise ValueError("%s must have one type" % " and ".join(weights))
+        code = _code(w, name)
+    return B.ATTN_DT_F32 if code is None else code
+
+
+def _ptr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _norm_sizes(q, k, num_heads, num_kv_heads, q_weight, k_weight, table, positions, rot_dim):
+    rows, D, qs = _heads2d(q, num_heads, "q")
+    k_rows, k_D, ks = _heads2d(k, num_kv_heads, "k")
+    if k_rows != rows or k_D != D:
+        raise ValueError("q and k must have the same rows and the same head dimension")
+    _like(q.dtype, "k", k)
+    w_code = _weights(D, q_weight=q_weight, k_weight=k_weight)
+    if table is None:
+        if rot_dim:
+            raise ValueError("a turn needs a table")
+        rot_dim = 0
+    elif rot_dim is None:
+        rot_dim = D
+    tab, tab_rows = _table(table, rot_dim)
+    pos = _int32(positions, "positions")
+    if pos is not None and positions.numel() != rows:
+        raise ValueError("positions must hold one position a row")
+    return rows, D, qs, ks, w_code, rot_dim, tab, tab_rows, pos
+
+
+def qk_norm_rope(q, k, num_heads, num_kv_heads, q_weight=None, k_weight=None, table=None, positions=None, rot_dim=None,
+                 interleaved=False, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """q [rows, H*D] and k [rows, G*D] (fp32, bf16 or fp16; rows may be strided) with each head normed by its
+    root mean square, multiplied by its weight vector [D] (None: ones) and turned by its row's position (row t
+    at t without `positions`; no table: not turned).  Returns (q_out, k_out), which may be the inputs."""
+    rows, D, qs, ks, w_code, rot_dim, tab, tab_rows, pos = _norm_sizes(q, k, num_heads, num_kv_heads, q_weight, k_weight,
+                                                                      table, positions, rot_dim)
+    code, index = _code(q, "q"), q.get_device()
+    q_out, qos = _rows_out(q_out, q, (rows, num_heads * D), "q_out", stream)
+    k_out, kos = _rows_out(k_out, k, (rows, num_kv_heads * D), "k_out", stream)
+    _same_device(index, k, q_out, k_out, q_weight, k_weight, table, positions)
+    _run("attn_qk_norm_rope", B.load_library().attn_qk_norm_rope, index, _handle(stream, index),
+         (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight), _ptr(k_weight), code, w_code,
+          rows, num_heads, num_kv_heads, D, qs, ks, qos, kos, eps, rot_dim, 1 if interleaved else 0, pos, tab,
+          tab_rows))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq, dk, q, k, num_heads, num_kv_heads, q_weight=None, k_weight=None, table=None,
+                          positions=None, rot_dim=None, interleaved=False, eps=1e-6, dq_out=None, dk_out=None,
+                          stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope's q, k and weights (None for a weight that is None)
+    for upstream dq, dk of its results.  dq_out and dk_out take the first two; they may be dq and dk, or q and k."""
+    rows, D, qs, ks, w_code, rot_dim, tab, tab_rows, pos = _norm_sizes(q, k, num_heads, num_kv_heads, q_weight, k_weight,
+                                                                      table, positions, rot_dim)
+    code, index = _code(q, "q"), q.get_device()
+    strides = []
+    for name, x, heads in (("dq", dq, num_heads), ("dk", dk, num_kv_heads)):
+        x_rows, x_D, stride = _heads2d(x, heads, name)
+        if x_rows != rows or x_D != D:
+            raise ValueError("%s must have the shape of %s" % (name, name[1]))
+        _like(q.dtype, name, x)
+        strides.append(stride)
+    dq_out, dqos = _rows_out(dq_out, q, (rows, num_heads * D), "dq_out", stream)
+    dk_out, dkos = _rows_out(dk_out, k, (rows, num_kv_heads * D), "dk_out", stream)
+    _same_device(index, dq, dk, k, dq_out, dk_out, q_weight, k_weight, table, positions)
+    raw = _handle(stream, index)
+    dw = [None if w is None else _new(torch.empty, (D,), w.dtype, w.device, stream) for w in (q_weight, k_weight)]
+    workspace, nbytes = None, 0
+    if dw[0] is not None or dw[1] is not None:
+        with torch.cuda.device(index):
+            nbytes = B.attn_qk_norm_rope_backward_workspace_bytes(D)
+        workspace = _new(torch.empty, (nbytes,), torch.uint8, q.device, stream)
+    _run("attn_qk_norm_rope_backward", B.load_library().attn_qk_norm_rope_backward, index, raw,
+         (dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
+          _ptr(q_weight), _ptr(k_weight), _ptr(dw[0]), _ptr(dw[1]), code, w_code, rows, num_heads, num_kv_heads, D,
+          strides[0], strides[1], qs, ks, dqos, dkos, eps, rot_dim, 1 if interleaved else 0, pos, tab, tab_rows,
+          _ptr(workspace), nbytes))
+    return dq_out, dk_out, dw[0], dw[1]
+
+
 def forward(q, k, v, num_heads, num_kv_heads, mask=B.ATTN_CAUSAL, prec=B.ATTN_FP32, want_lse=True,
             stream=None, window=0, rope=None):
     """q [q_seq, H*D], k/v [kv_seq, G*D] (CUDA fp32) -> (out [q_seq, H*D], lse [q_seq, H, 2] or None).
@@ -374,6 +481,134 @@ def append_paged(batch, k_new, v_new, k_pages, v_pages, q=None, q_out=None, tabl
           kv_dim, qs, qos, ks, vs, batch.page_rows, num_pages, batch.max_blocks,
           rot_dim if tab is not None else 0, 1 if interleaved else 0, tab, tab_rows))
     return q_out
+
+
+_CODE8 = tuple(t for t in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if t is not None)
+_SCALE8 = tuple(t for t in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if t is not None)
+
+
+class PagedCache8:
+    """A paged cache in 8 bits: pools of e4m3 codes and their scales (see attn_append_paged8 in attn_gqa.h).
+
+    k_pages, v_pages [num_pages * page_rows, kv_dim] (uint8 or float8_e4m3fn) and k_scales, v_scales
+    [num_pages * page_rows / scale_rows, num_kv_heads] (uint8 or float8_e8m0fnu), contiguous CUDA tensors, kept;
+    PagedCache8.empty makes them."""
+
+    __slots__ = ("k_pages", "v_pages", "k_scales", "v_scales", "rows", "kv_dim", "num_kv_heads", "scale_rows", "index")
+
+    def __init__(self, k_pages, v_pages, k_scales, v_scales):
+        for name, x, types in (("k_pages", k_pages, _CODE8), ("v_pages", v_pages, _CODE8),
+                               ("k_scales", k_scales, _SCALE8), ("v_scales", v_scales, _SCALE8)):
+            if x.dim() != 2 or x.dtype not in types or not x.is_contiguous():
+                raise ValueError("%s must be a contiguous matrix of %s" % (name, " or ".join(map(str, types))))
+        if k_pages.shape != v_pages.shape or k_scales.shape != v_scales.shape:
+            raise ValueError("the pools, and the scales, of K and V must have one shape")
+        (rows, kv_dim), (blocks, heads) = k_pages.shape, k_scales.shape
+        if rows == 0 or blocks == 0 or heads == 0 or rows % blocks:
+            raise ValueError("%d pool rows cannot be divided into %d blocks of scales" % (rows, blocks))
+        index = k_pages.get_device()
+        if index < 0:
+            raise ValueError("the cache must be in device memory")
+        _same_device(index, v_pages, k_scales, v_scales)
+        for name, x in (("k_pages", k_pages), ("v_pages", v_pages), ("k_scales", k_scales), ("v_scales", v_scales),
+                        ("rows", rows), ("kv_dim", kv_dim), ("num_kv_heads", heads), ("scale_rows", rows // blocks),
+                        ("index", index)):
+            object.__setattr__(self, name, x)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a cache keeps the tensors that it was made of")
+
+    @classmethod
+    def empty(cls, num_pages, page_rows, num_kv_heads, head_dim, scale_rows=16, device="cuda"):
+        """A cache of zeros.  scale_rows positions of a head share a scale; it divides page_rows."""
+        if scale_rows < 1 or page_rows % scale_rows:
+            raise ValueError("scale_rows must divide page_rows")
+        rows = num_pages * page_rows
+        pools = [torch.zeros(rows, num_kv_heads * head_dim, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.full((rows // scale_rows, num_kv_heads), 127 - 14, dtype=torch.uint8, device=device)
+                  for _ in range(2)]
+        return cls(*pools, *scales)
+
+    def pages(self, batch):
+        """Pages of the pools, as the batch counts them."""
+        page_rows = batch.page_rows
+        if self.rows % page_rows or page_rows % self.scale_rows or self.num_kv_heads != batch.num_kv_heads:
+            raise ValueError("the cache (%d rows, %d a scale, %d heads) does not fit the batch (%d rows a page, %d heads)"
+                             % (self.rows, self.scale_rows, self.num_kv_heads, page_rows, batch.num_kv_heads))
+        batch.same_device(self.index)
+        return self.rows // page_rows
+
+
+def append_paged8(batch, k_new, v_new, cache, q=None, q_out=None, table=None, rot_dim=None, interleaved=False,
+                  q_weight=None, k_weight=None, eps=1e-6, stream=None):
+    """Write the batch's new K (normed by k_weight and turned by `table`, when given) and V rows into a PagedCache8;
+    with q, also return it normed (q_weight) and turned, in q_out or in a new tensor (of q's type, bf16 for fp32;
+    rows that are not written are zeros)."""
+    num_pages = cache.pages(batch)
+    D, G = batch.head_dim, batch.num_kv_heads
+    rows, columns, ks = _rows2d(k_new, "k_new")
+    v_rows, v_columns, vs = _rows2d(v_new, "v_new")
+    if columns != G * D or v_columns != columns or v_rows != rows:
+        raise ValueError("k_new and v_new must be [rows, %d]" % (G * D))
+    dtype = k_new.dtype
+    code = q_code = _code(k_new, "k_new")
+    _like(dtype, "v_new", v_new)
+    if rot_dim is None:
+        rot_dim = D
+    tab, tab_rows = _table(table, rot_dim)
+    w_code = _weights(D, q_weight=q_weight, k_weight=k_weight) if q_weight is not None or k_weight is not None else 0
+    index = cache.index
+    H = qs = qos = 0
+    if q is not None:
+        H = batch.num_heads
+        q_rows, q_columns, qs = _rows2d(q, "q")
+        if q_rows != rows or q_columns != H * D:
+            raise ValueError("q must be [%d, %d]" % (rows, H * D))
+        _like(dtype, "q", q)
+        if q_out is None:
+            q_out = _new(torch.zeros, (rows, H * D), torch.bfloat16 if dtype == torch.float32 else dtype, q.device,
+                         stream)
+            qos = H * D
+        else:
+            o_rows, o_columns, qos = _rows2d(q_out, "q_out")
+            if o_rows != rows or o_columns != q_columns:
+                raise ValueError("q_out must have the shape of q")
+        q_code = _code(q_out, "q_out")
+        _same_device(index, q, q_out)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    _same_device(index, k_new, v_new, table, q_weight, k_weight)
+    _run("attn_append_paged8", B.load_library().attn_append_paged8, index, _handle(stream, index),
+         (_ptr(q), _ptr(q_out), k_new.data_ptr(), v_new.data_ptr(), code, q_code, cache.k_pages.data_ptr(),
+          cache.v_pages.data_ptr(), cache.k_scales.data_ptr(), cache.v_scales.data_ptr(), batch.block_table.data_ptr(),
+          batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H, G, D, cache.kv_dim, qs, qos, ks, vs,
+          batch.page_rows, num_pages, batch.max_blocks, cache.scale_rows, _ptr(q_weight), _ptr(k_weight), w_code, eps,
+          rot_dim if tab is not None else 0, 1 if interleaved else 0, tab, tab_rows))
+    return q_out
+
+
+def read_paged8(batch, cache, starts, k_out, v_out, first=None, stream=None):
+    """Positions of the batch's sequences back from a PagedCache8: rows [starts[s], starts[s+1]) of k_out and v_out
+    (fp32, bf16 or fp16, [rows, G*D]) become positions first[s] (None: 0), first[s] + 1, ...  starts [n + 1] and
+    first [n] are int32 CUDA tensors.  Rows of no sequence are left as they are.  Returns (k_out, v_out)."""
+    num_pages = cache.pages(batch)
+    G, D = batch.num_kv_heads, batch.head_dim
+    rows, columns, ks = _rows2d(k_out, "k_out")
+    v_rows, v_columns, vs = _rows2d(v_out, "v_out")
+    if columns != G * D or v_columns != columns or v_rows != rows:
+        raise ValueError("k_out and v_out must be [rows, %d]" % (G * D))
+    code = _code(k_out, "k_out")
+    _like(k_out.dtype, "v_out", v_out)
+    if starts.shape != (batch.n_seqs + 1,) or (first is not None and first.shape != (batch.n_seqs,)):
+        raise ValueError("starts must hold %d entries and first %d" % (batch.n_seqs + 1, batch.n_seqs))
+    index = cache.index
+    _same_device(index, k_out, v_out, starts, first)
+    _run("attn_read_paged8", B.load_library().attn_read_paged8, index, _handle(stream, index),
+         (cache.k_pages.data_ptr(), cache.v_pages.data_ptr(), cache.k_scales.data_ptr(), cache.v_scales.data_ptr(),
+          k_out.data_ptr(), v_out.data_ptr(), code, batch.block_table.data_ptr(), _int32(starts, "starts"),
+          _int32(first, "first"), batch.kv_len.data_ptr(), rows, batch.n_seqs, G, D, cache.kv_dim, ks, vs,
+          batch.page_rows, num_pages, batch.max_blocks, cache.scale_rows))
+    return k_out, v_out
 
 
 def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, softcap=0.0, alibi_slopes=None,

@@ -44,6 +44,32 @@ struct RopeArgs {
 };
 int launch_rope_apply(RopeArgs a, int dtype, cudaStream_t s);
 
+// Norm and turn of the heads of Q and K.
+struct NormTensor {
+  const void* x;
+  const void* dy;  // backward: upstream gradient
+  void* y;         // forward: result; backward: gradient of x
+  const void* weight;  // [D] or nullptr (ones)
+  void* dw;            // backward: [D] or nullptr
+  long long x_stride, dy_stride, y_stride;  // elements
+  int heads;                                // 0: no such tensor
+  int splits;                               // warps that share a row; set by launch_qk_norm
+};
+struct NormArgs {
+  NormTensor q, k;
+  const uint32_t* positions;  // nullptr: row t is at position t
+  const float* table;         // nullptr with R == 0
+  float* partial;             // backward: [blocks][D] sums of dw
+  unsigned* status;
+  uint32_t rows, table_rows;
+  int D, R, w_dtype;
+  bool interleaved;
+  float eps;
+  int lanes, q_blocks;  // set by launch_qk_norm
+};
+size_t qk_norm_workspace_bytes(int D, int sm_count);
+int launch_qk_norm(NormArgs a, int dtype, bool backward, int sm_count, cudaStream_t s);
+
 struct RopeScale {
   int kind;
   double base, factor, orig_max_pos, beta_fast, beta_slow, attn_factor;
@@ -70,6 +96,57 @@ struct AppendArgs {
   int units;  // set by launch_append_paged
 };
 int launch_append_paged(AppendArgs a, int in_dtype, int cache_dtype, cudaStream_t s);
+
+// The 8-bit cache (cache8.cuh): append and read.
+struct Append8Args {
+  const void* q;  // nullptr with H == 0
+  void* q_out;
+  const void* k;
+  const void* v;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  uint8_t* k_scales;  // [num_pages * page_rows / scale_rows][G]
+  uint8_t* v_scales;
+  const void* q_weight;  // [D], or nullptr: not normed
+  const void* k_weight;
+  const uint32_t* block_table;  // [n_seqs][max_blocks]
+  const uint32_t* q_start;      // [n_seqs + 1]
+  const uint32_t* kv_len;       // [n_seqs]
+  const float* table;
+  unsigned* status;
+  long long q_stride, q_out_stride, k_stride, v_stride, kv_dim;
+  uint32_t total_rows, table_rows;
+  int n_seqs, H, G, D, R;
+  int page_rows, num_pages, max_blocks, scale_rows, w_dtype;
+  bool interleaved;
+  float eps;
+  // Set by launch_append8.
+  FastDiv by_page, by_scale;
+  int lanes, team, chunk, kv_blocks, q_splits;
+};
+int launch_append8(Append8Args a, int dtype, int q_dtype, int sm_count, cudaStream_t s);
+struct Read8Args {
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  void* k_out;
+  void* v_out;
+  const uint32_t* block_table;
+  const uint32_t* starts;  // [n_seqs + 1]: rows of each sequence
+  const uint32_t* first;   // [n_seqs] first position, or nullptr: 0
+  const uint32_t* kv_len;
+  unsigned* status;
+  long long k_stride, v_stride, kv_dim;
+  uint32_t total_rows;
+  int n_seqs, G, D;
+  int page_rows, num_pages, max_blocks, scale_rows;
+  // Set by launch_read8.
+  FastDiv by_page, by_scale;
+  int rows_per_block;
+  bool vec;
+};
+int launch_read8(Read8Args a, int dtype, cudaStream_t s);
 
 // One record per thread block of the attention grid: the item whose first
 // keys the block computed and whose last keys a later block did.

@@ -1,0 +1,461 @@
+// cache8.cu -- the 8-bit paged cache: the new tokens of a ragged batch written
+// into it (K normed and turned on the way, Q too), and ranges of positions read
+// back.  The numbers are those of cache8.cuh.
+//
+// Append.  A scale belongs to scale_rows positions of a kv head, so whoever
+// rounds one of them needs the largest magnitude of all.  A team of threads takes
+// one block of positions and one kv head of K or V: it reads the block's new rows
+// (up to two a thread stay in registers as fp32, more are read again), finds the
+// largest magnitude and with it the scale, and stores the codes.  The first
+// block of a sequence may hold older rows; they count by the scale that they have,
+// and where the new scale is larger their codes are multiplied and rounded again.
+// A block belongs to the team whose chunk of token rows holds the block's first
+// new row, so nothing is left to atomics and results do not depend on order.
+//
+// Read.  Sixteen codes a thread; bound by the 16- or 32-bit rows it writes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <type_traits>
+
+#include "batch.h"
+#include "cache8.cuh"
+#include "common.cuh"
+#include "find_seq.cuh"
+#include "internal.h"
+#include "norm_rope.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kKeep = 2;  // rows of a thread that stay in registers between the maximum and the codes
+
+// A row of a head in a lane's registers: 16 columns of a unit, or (scalar) four.
+template <bool VEC>
+struct Held {
+  float v[VEC ? 16 : 4];
+};
+
+// The row x of a head (its first column), normed and turned.  `mask`: the lanes
+// of the head.
+template <typename TI, bool INTER, bool VEC>
+__device__ __forceinline__ void load_row(const Append8Args& a, const TI* x, uint32_t pos, const norm::Unit<INTER>& u,
+                                         const void* weight, bool turn, int lane, unsigned mask, Held<VEC>& out) {
+  const float* tab = a.table + (long long)pos * a.R;
+  const float inv_d = 1.f / (float)a.D;
+  if constexpr (VEC) {
+    norm::load_unit(x, u, out.v);
+    if (weight != nullptr) {
+      float sum = 0.f, w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum = fmaf(out.v[i], out.v[i], sum);
+      norm::load_weight(weight, a.w_dtype, u, w);
+      const float rms = rsqrtf(fmaf(norm::head_sum(sum, a.lanes, mask), inv_d, a.eps));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out.v[i] *= rms * w[i];
+    }
+    if (turn) {
+      float cs[16];
+      norm::load_turn(tab, a.R, u, true, cs);
+      norm::turn_unit<INTER, 1>(out.v, cs, u, false);
+    }
+  } else {
+    float rms = 1.f;
+    if (weight != nullptr) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = lane + 32 * j < a.D ? rot::to_f32(x[lane + 32 * j]) : 0.f;
+        sum = fmaf(v, v, sum);
+      }
+      rms = rsqrtf(fmaf(norm::head_sum(sum, 32, mask), inv_d, a.eps));
+    }
+    auto z = [&](int d) {
+      const float v = rot::to_f32(x[d]);
+      return weight != nullptr ? v * (rms * norm::weight_at(weight, a.w_dtype, d)) : v;
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int d = lane + 32 * j;
+      out.v[j] = 0.f;
+      if (d < a.D)
+        out.v[j] = turn ? norm::turned_column<1>(norm::column_of<INTER>(d, a.R), tab, a.R, true, z) : z(d);
+    }
+  }
+}
+
+template <bool INTER, bool VEC>
+__device__ __forceinline__ float held_max(const Held<VEC>& h) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < (VEC ? 16 : 4); ++i) m = fmaxf(m, fabsf(h.v[i]));  // (a NaN leaves m)
+  return m;
+}
+template <bool INTER, bool VEC>
+__device__ __forceinline__ void store_codes(const Held<VEC>& h, float mul, uint8_t* dst, const norm::Unit<INTER>& u,
+                                            int lane, int D) {
+  if constexpr (VEC) {
+    auto eight = [&](int i, int c) {
+      *reinterpret_cast<uint2*>(dst + c) =
+          make_uint2(c8::from_float4(h.v[i] * mul, h.v[i + 1] * mul, h.v[i + 2] * mul, h.v[i + 3] * mul),
+                     c8::from_float4(h.v[i + 4] * mul, h.v[i + 5] * mul, h.v[i + 6] * mul, h.v[i + 7] * mul));
+    };
+    if (u.any) eight(0, u.c0);
+    if (u.pair) eight(8, u.c1);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + 32 * j < D) dst[lane + 32 * j] = (uint8_t)c8::from_float2(h.v[j] * mul, 0.f);
+  }
+}
+
+struct Team {
+  int size, id, thread;  // threads of a team, this team of the block, this thread of the team
+  int row, rows;         // the thread's first row of a block, and rows at once
+  float* red;            // [warps of the block], shared memory
+  // Largest of m over the team.
+  __device__ __forceinline__ float max(float m) const {
+    const int w = size < 32 ? size : 32, lane = threadIdx.x & 31;
+    const unsigned mask = w == 32 ? 0xffffffffu : ((1u << w) - 1u) << (lane & ~(w - 1));
+    for (int d = w >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, d));
+    if (size > 32) {
+      const int warp = threadIdx.x >> 5, w0 = id * (size >> 5);
+      if (lane == 0) red[warp] = m;
+      named_barrier(1 + id, size);
+      m = 0.f;
+      for (int k = 0; k < (size >> 5); ++k) m = fmaxf(m, red[w0 + k]);
+      named_barrier(1 + id, size);  // red may be written again
+    }
+    return m;
+  }
+};
+
+// One block of positions of one kv head: token rows [row0, row0 + m) at
+// positions pos0 ..., pool rows slot0 ...; `held` older rows stand before them.
+template <typename TI, bool INTER, bool VEC>
+__device__ __forceinline__ void write_block(const Append8Args& a, const Team& t, const TI* src, long long stride,
+                                            uint8_t* pages, uint8_t* scales, int h, long long row0, int m,
+                                            uint32_t pos0, long long slot0, int held, const void* weight, int R_geo,
+                                            bool turn) {
+  const int lane = threadIdx.x & (a.lanes - 1);
+  const unsigned mask = a.lanes == 32 ? 0xffffffffu : ((1u << a.lanes) - 1u) << (threadIdx.x & 31 & ~(a.lanes - 1));
+  const norm::Unit<INTER> u(lane, a.D, R_geo);
+  uint8_t* scale = scales + (long long)divide((uint32_t)slot0, a.by_scale) * a.G + h;
+  const int e0 = held > 0 ? c8::exp_of(*scale) : c8::kMinExp;
+  const TI* x = src + row0 * stride + (long long)h * a.D;
+  uint8_t* dst = pages + slot0 * a.kv_dim + (long long)h * a.D;
+  Held<VEC> kept[kKeep];
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int r = t.row + k * t.rows;
+    if (r < m) {
+      load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, u, weight, turn, lane, mask, kept[k]);
+      amax = fmaxf(amax, held_max<INTER, VEC>(kept[k]));
+    }
+  }
+  for (int r = t.row + kKeep * t.rows; r < m; r += t.rows) {
+    Held<VEC> v;
+    load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, u, weight, turn, lane, mask, v);
+    amax = fmaxf(amax, held_max<INTER, VEC>(v));
+  }
+  const int e = ::max(e0, c8::exp_for(t.max(amax)));
+  if (held > 0 && e > e0) {  // the older rows move to the new scale
+    const float mul = pow2f(e0 - e);
+    const int words = a.D / 4;
+    for (int i = t.thread; i < held * words; i += t.size) {
+      const int r = i / words;
+      uint32_t* p = reinterpret_cast<uint32_t*>(dst - (long long)(held - r) * a.kv_dim) + (i - r * words);
+      float v[4];
+      c8::to_float4(*p, v);
+      *p = c8::from_float4(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul);
+    }
+  }
+  if (t.thread == 0) *scale = (uint8_t)(127 + e);
+  const float mul = pow2f(-e);
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int r = t.row + k * t.rows;
+    if (r < m) store_codes<INTER, VEC>(kept[k], mul, dst + (long long)r * a.kv_dim, u, lane, a.D);
+  }
+  for (int r = t.row + kKeep * t.rows; r < m; r += t.rows) {
+    Held<VEC> v;
+    load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, u, weight, turn, lane, mask, v);
+    store_codes<INTER, VEC>(v, mul, dst + (long long)r * a.kv_dim, u, lane, a.D);
+  }
+}
+
+// First sequence from s on that ends after row i (q_start ascends).
+__device__ __forceinline__ int seq_after(const uint32_t* q_start, int n, int s, uint32_t i) {
+  for (int k = 0; k < 4; ++k, ++s)
+    if (s >= n || q_start[s + 1] > i) return s;
+  int hi = n;
+  while (s < hi) {
+    const int mid = (s + hi) >> 1;
+    if (q_start[mid + 1] > i)
+      hi = mid;
+    else
+      s = mid + 1;
+  }
+  return s;
+}
+
+template <typename TI, typename TQ, bool INTER, bool VEC>
+__device__ __forceinline__ void append_q(const Append8Args& a, int block) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long task = (long long)block * kWarps + warp;
+  const long long row = task / a.q_splits;
+  if (row >= a.total_rows) return;
+  const int split = (int)(task - row * a.q_splits);
+  const int s = find_seq(a.q_start, a.n_seqs, (uint32_t)row);
+  if (s < 0) return;
+  const uint32_t end = a.q_start[s + 1];
+  if (row >= end) return;
+  const long long pos = (long long)a.kv_len[s] - (long long)end + row;
+  if (pos < 0 || pos >= (long long)a.page_rows * a.max_blocks || (a.R > 0 && pos >= (long long)a.table_rows) ||
+      a.block_table[(long long)s * a.max_blocks + divide((uint32_t)pos, a.by_page)] >= (uint32_t)a.num_pages)
+    return;  // (recorded by the row's keys)
+  const int at_once = 32 / a.lanes, sub = lane / a.lanes, in = lane & (a.lanes - 1);
+  const unsigned mask = a.lanes == 32 ? 0xffffffffu : ((1u << a.lanes) - 1u) << (lane & ~(a.lanes - 1));
+  const norm::Unit<INTER> u(in, a.D, a.R > 0 ? a.R : a.D);
+  const TI* x = static_cast<const TI*>(a.q) + row * a.q_stride;
+  TQ* y = static_cast<TQ*>(a.q_out) + row * a.q_out_stride;
+  for (int h = split * at_once + sub; h < a.H; h += at_once * a.q_splits) {
+    Held<VEC> v;
+    load_row<TI, INTER, VEC>(a, x + (long long)h * a.D, (uint32_t)pos, u, a.q_weight, a.R > 0, in, mask, v);
+    __syncwarp(mask);  // (scalar form: the head's lanes have read it; y may be x)
+    if constexpr (VEC) {
+      norm::store_unit(y + (long long)h * a.D, u, v.v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (in + 32 * j < a.D) y[(long long)h * a.D + in + 32 * j] = rot::from_f32<TQ>(v.v[j]);
+    }
+  }
+}
+
+template <typename TI, typename TQ, bool INTER, bool VEC>
+__global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) {
+  __shared__ float red[kWarps];
+  if (blockIdx.x >= (unsigned)a.kv_blocks) {
+    append_q<TI, TQ, INTER, VEC>(a, blockIdx.x - a.kv_blocks);
+    return;
+  }
+  Team t;
+  t.size = a.team;
+  t.id = threadIdx.x / a.team;
+  t.thread = threadIdx.x - t.id * a.team;
+  t.row = t.thread / a.lanes;
+  t.rows = a.team / a.lanes;
+  t.red = red;
+  const int teams = kThreads / a.team;
+  const long long first = (long long)blockIdx.x * teams, item = first + t.id;
+  // All lanes of a warp look for the sequence of the warp's first row.
+  const long long row_w = (first + (threadIdx.x & ~31) / a.team) / (2 * a.G) * a.chunk;
+  if (row_w >= a.total_rows) return;
+  int s = ::max(0, find_seq(a.q_start, a.n_seqs, (uint32_t)row_w));
+  const long long chunk = item / (2 * a.G);
+  if (chunk * a.chunk >= a.total_rows) return;
+  const int which = (int)(item - chunk * 2 * a.G);
+  const bool is_v = which >= a.G;
+  const int h = is_v ? which - a.G : which;
+  uint32_t i = (uint32_t)(chunk * a.chunk);
+  const uint32_t i_end = (uint32_t)min((long long)a.total_rows, (long long)i + a.chunk);
+  const int sr = a.scale_rows;
+  while (i < i_end) {
+    s = seq_after(a.q_start, a.n_seqs, s, i);
+    if (s >= a.n_seqs) break;
+    const uint32_t start = a.q_start[s], full_end = a.q_start[s + 1], end = min(full_end, a.total_rows);
+    if (i < start) {  // rows of no sequence
+      i = start;
+      continue;
+    }
+    const long long pos = (long long)a.kv_len[s] - (long long)full_end + (long long)i;
+    if (pos < 0) {  // rows before position 0
+      if (t.thread == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
+      i = (uint32_t)min((long long)end, (long long)i - pos);
+      continue;
+    }
+    const int in_block = (int)(pos % sr);
+    const int m = (int)min((long long)(sr - in_block), (long long)end - (long long)i);
+    if (in_block != 0 && i != start) {  // the block's first new row is in another chunk
+      i += m;
+      continue;
+    }
+    bool ok = pos < (long long)a.page_rows * a.max_blocks;
+    long long slot = 0;
+    if (ok) {
+      const uint32_t col = divide((uint32_t)pos, a.by_page);
+      const uint32_t page = a.block_table[(long long)s * a.max_blocks + col];
+      ok = page < (uint32_t)a.num_pages;
+      slot = (long long)page * a.page_rows + ((uint32_t)pos - col * (uint32_t)a.page_rows);
+    }
+    int take = m;
+    if (a.R > 0) take = (int)min((long long)m, ::max(0ll, (long long)a.table_rows - pos));
+    if ((!ok || take < m) && t.thread == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
+    if (ok && take > 0) {
+      const int held = in_block;
+      if (is_v)
+        write_block<TI, false, VEC>(a, t, static_cast<const TI*>(a.v), a.v_stride, a.v_pages, a.v_scales, h, i, take,
+                                    (uint32_t)pos, slot, held, nullptr, a.D, false);
+      else
+        write_block<TI, INTER, VEC>(a, t, static_cast<const TI*>(a.k), a.k_stride, a.k_pages, a.k_scales, h, i, take,
+                                    (uint32_t)pos, slot, held, a.k_weight, a.R > 0 ? a.R : a.D, a.R > 0);
+    }
+    i += m;
+  }
+}
+
+// ---------------------------------------------------------------- read
+template <typename T>
+__device__ __forceinline__ void store16(T* y, const float (&v)[16], bool vec) {
+  if (vec) {
+    float a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = v[i];
+      b[i] = v[8 + i];
+    }
+    rot::store8<true>(y, a);
+    rot::store8<true>(y + 8, b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = rot::from_f32<T>(v[i]);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) read8_kernel(const Read8Args a) {
+  __shared__ long long slot_s[kWarps];  // cache row, -1: zeros, -2: a row of no sequence
+  const uint32_t row0 = blockIdx.x * (uint32_t)a.rows_per_block;
+  const int nrows = (int)min((uint32_t)a.rows_per_block, a.total_rows - row0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < nrows) {
+    const uint32_t row = row0 + warp;
+    const int s = find_seq(a.starts, a.n_seqs, row);
+    if (lane == 0) {
+      long long slot = -2;
+      if (s >= 0 && row < a.starts[s + 1]) {
+        slot = -1;
+        const long long pos = (long long)(a.first != nullptr ? a.first[s] : 0u) + (row - a.starts[s]);
+        if (pos < (long long)a.kv_len[s] && pos < (long long)a.page_rows * a.max_blocks) {
+          const uint32_t col = divide((uint32_t)pos, a.by_page);
+          const uint32_t page = a.block_table[(long long)s * a.max_blocks + col];
+          if (page < (uint32_t)a.num_pages)
+            slot = (long long)page * a.page_rows + ((uint32_t)pos - col * (uint32_t)a.page_rows);
+        }
+        if (slot == -1) record_status(a.status, ATTN_ERR_INVALID_ARG);
+      }
+      slot_s[warp] = slot;
+    }
+  }
+  __syncthreads();
+  const int per = a.D / 16, half = a.G * per, upr = 2 * half;  // units of a head, of K, of a row
+  T* const k_out = static_cast<T*>(a.k_out);
+  T* const v_out = static_cast<T*>(a.v_out);
+  for (int i = threadIdx.x; i < nrows * upr; i += kThreads) {
+    const int r = i / upr;
+    int u = i - r * upr;
+    const long long slot = slot_s[r];
+    if (slot == -2) continue;
+    const bool is_v = u >= half;
+    if (is_v) u -= half;
+    const int h = u / per;
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = 0.f;
+    if (slot >= 0) {
+      const uint4 c = __ldcs(reinterpret_cast<const uint4*>((is_v ? a.v_pages : a.k_pages) + slot * a.kv_dim + 16 * u));
+      const uint8_t b = (is_v ? a.v_scales : a.k_scales)[(long long)divide((uint32_t)slot, a.by_scale) * a.G + h];
+      const float mul = pow2f(c8::exp_of(b));
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f[4];
+        c8::to_float4(w[k], f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * k + e] = f[e] * mul;
+      }
+    }
+    const long long row = (long long)row0 + r;
+    if (is_v)
+      store16(v_out + row * a.v_stride + 16 * u, v, a.vec);
+    else
+      store16(k_out + row * a.k_stride + 16 * u, v, a.vec);
+  }
+}
+
+template <typename TI, typename TQ>
+const void* append_kernel_of(bool vec, bool interleaved) {
+  if (vec)
+    return interleaved ? reinterpret_cast<const void*>(append8_kernel<TI, TQ, true, true>)
+                       : reinterpret_cast<const void*>(append8_kernel<TI, TQ, false, true>);
+  return interleaved ? reinterpret_cast<const void*>(append8_kernel<TI, TQ, true, false>)
+                     : reinterpret_cast<const void*>(append8_kernel<TI, TQ, false, false>);
+}
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int pow2_from(long long n) {
+  int p = 1;
+  while (p < n) p <<= 1;
+  return p;
+}
+
+}  // namespace
+
+int launch_append8(Append8Args a, int dtype, int q_dtype, int sm_count, cudaStream_t s) {
+  a.by_page = fast_div((uint32_t)a.page_rows);
+  a.by_scale = fast_div((uint32_t)a.scale_rows);
+  if (a.R == 0) a.interleaved = false;
+  const int R_geo = a.R > 0 ? a.R : a.D;
+  const bool vec = rot::vec_sizes(a.D, R_geo, a.interleaved) && aligned(a.q, 16) && aligned(a.q_out, 16) &&
+                   aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.table, 16) && a.q_stride % 8 == 0 &&
+                   a.q_out_stride % 8 == 0 && a.k_stride % 8 == 0 && a.v_stride % 8 == 0;
+  a.lanes = vec ? norm::head_lanes(a.D, R_geo, a.interleaved) : 32;
+  // A team's rows at once: as many as its block has, by the batch's average; the rest of a block follows in turns.
+  const long long avg = a.total_rows / (uint32_t)a.n_seqs;
+  const int at_once = pow2_from(avg < 1 ? 1 : avg < a.scale_rows ? avg : a.scale_rows);
+  a.team = at_once * a.lanes < kThreads ? at_once * a.lanes : kThreads;
+  a.chunk = avg >= 2 ? a.scale_rows : 1;
+  const int teams = kThreads / a.team;
+  const long long chunks = ((long long)a.total_rows + a.chunk - 1) / a.chunk;
+  const long long kv_blocks = (chunks * 2 * a.G + teams - 1) / teams;
+  long long q_blocks = 0;
+  if (a.H > 0) {
+    const int steps = (a.H * a.lanes + 31) / 32;
+    a.q_splits = 1;
+    while (2 * a.q_splits <= steps && (long long)a.total_rows * a.q_splits < 16ll * kWarps * sm_count) a.q_splits *= 2;
+    q_blocks = ((long long)a.total_rows * a.q_splits + kWarps - 1) / kWarps;
+  }
+  if (kv_blocks + q_blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+  a.kv_blocks = (int)kv_blocks;
+  const void* kern;
+  if (dtype == ATTN_DT_BF16)
+    kern = append_kernel_of<__nv_bfloat16, __nv_bfloat16>(vec, a.interleaved);
+  else if (dtype == ATTN_DT_F16)
+    kern = append_kernel_of<__half, __half>(vec, a.interleaved);
+  else if (q_dtype == ATTN_DT_F16)
+    kern = append_kernel_of<float, __half>(vec, a.interleaved);
+  else
+    kern = append_kernel_of<float, __nv_bfloat16>(vec, a.interleaved);
+  void* args[] = {&a};
+  return cudaLaunchKernel(kern, dim3((unsigned)(kv_blocks + q_blocks)), dim3(kThreads), args, 0, s) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+int launch_read8(Read8Args a, int dtype, cudaStream_t s) {
+  a.by_page = fast_div((uint32_t)a.page_rows);
+  a.by_scale = fast_div((uint32_t)a.scale_rows);
+  a.vec = aligned(a.k_out, 16) && aligned(a.v_out, 16) && a.k_stride % 8 == 0 && a.v_stride % 8 == 0;
+  a.rows_per_block = a.total_rows >= 4096 ? 8 : 1;
+  const dim3 grid((a.total_rows + a.rows_per_block - 1) / a.rows_per_block);
+  if (dtype == ATTN_DT_BF16)
+    read8_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a);
+  else if (dtype == ATTN_DT_F16)
+    read8_kernel<__half><<<grid, kThreads, 0, s>>>(a);
+  else
+    read8_kernel<float><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace attn

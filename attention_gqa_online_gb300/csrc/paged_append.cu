@@ -15,28 +15,13 @@
 // 51.4 us, 6.0 TB/s; one token of 64 sequences takes 3.2 us in a graph.
 #include "common.cuh"
 #include "batch.h"
+#include "find_seq.cuh"
 #include "rotary.cuh"
 
 namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Last s in [0, n) with starts[s] <= row, or -1; every lane gets the result.
-__device__ __forceinline__ int find_seq(const uint32_t* starts, int n, uint32_t row) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;  // the answer, if any, is in [lo, hi)
-  while (true) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + lane * step;
-    const bool le = at < hi && starts[at] <= row;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
-    if (cnt == 0) return -1;
-    lo += (cnt - 1) * step;
-    if (step == 1) return lo;
-    hi = min(hi, lo + step);
-  }
-}
 
 template <typename TI, typename TO, bool INTER, bool VEC>
 __global__ void __launch_bounds__(kThreads) append_paged_kernel(const AppendArgs a, int rows_per_block) {

@@ -1,0 +1,312 @@
+// qk_norm.cu -- root-mean-square norm of every query and key head with the
+// rotary turn in the same pass, and its backward.
+//
+//   forward   z = w xh, xh = r x, r = 1 / sqrt(mean(x^2) + eps);  y = R(p) z
+//   backward  dz = R(p)^T dy;  dw = sum over rows and heads of dz xh;
+//             dx = r (w dz - xh mean(w dz xh))
+//
+// The backward reads x and makes r anew: one more value a head to keep between
+// the passes would save it nothing, as x is read for xh in any case.
+//
+// A warp takes a row of Q or of K (blocks are divided between the two by their
+// heads) and walks its heads, 32 / lanes at a time, two steps' loads in flight,
+// with the row's cosines and sines and the weights in registers.  Where rows are
+// few, several warps share a row's heads.  dw: each lane sums its columns over all
+// its rows and heads in fp32; a block's lanes join in shared memory, blocks in a
+// second kernel, always in the same order, so repeated calls give the same bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "batch.h"
+#include "common.cuh"
+#include "internal.h"
+#include "norm_rope.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+template <typename T>
+struct Rows {
+  const T* x;
+  const T* dy;
+  T* y;
+  long long xs, ds, ys;
+};
+template <typename T>
+__device__ __forceinline__ Rows<T> rows_of(const NormTensor& t) {
+  return {static_cast<const T*>(t.x), static_cast<const T*>(t.dy), static_cast<T*>(t.y), t.x_stride, t.dy_stride,
+          t.y_stride};
+}
+
+// Position of a row, and whether the table holds it.
+__device__ __forceinline__ bool position_of(const NormArgs& a, uint32_t row, uint32_t* p) {
+  *p = a.positions != nullptr ? a.positions[row] : row;
+  const bool ok = a.R == 0 || *p < a.table_rows;
+  if (!ok && (threadIdx.x & 31) == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
+  return ok;
+}
+
+template <typename T, bool INTER, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads) qk_norm_vec_kernel(const NormArgs a) {
+  const bool is_k = blockIdx.x >= (unsigned)a.q_blocks;
+  const NormTensor& t = is_k ? a.k : a.q;
+  const int block = is_k ? blockIdx.x - a.q_blocks : blockIdx.x, blocks = is_k ? gridDim.x - a.q_blocks : a.q_blocks;
+  const Rows<T> r = rows_of<T>(t);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lanes = a.lanes;
+  const int sub = lane / lanes, at_once = 32 / lanes;  // heads of a warp at once
+  const norm::Unit<INTER> u(lane & (lanes - 1), a.D, a.R);
+  float w[16], dw[16];
+  norm::load_weight(t.weight, a.w_dtype, u, w);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+  const long long tasks = (long long)a.rows * t.splits;
+  const float inv_d = 1.f / (float)a.D;
+  for (long long task = (long long)block * kWarps + warp; task < tasks; task += (long long)blocks * kWarps) {
+    const uint32_t row = t.splits == 1 ? (uint32_t)task : (uint32_t)(task / t.splits);
+    const int split = t.splits == 1 ? 0 : (int)(task - (long long)row * t.splits);
+    uint32_t p;
+    const bool ok = position_of(a, row, &p);
+    float cs[16];
+    norm::load_turn(a.table + (long long)p * a.R, a.R, u, ok, cs);
+    const T* x = r.x + (long long)row * r.xs;
+    T* y = r.y + (long long)row * r.ys;
+    const T* dy = BACKWARD ? r.dy + (long long)row * r.ds : nullptr;
+    constexpr int kAhead = 2;  // heads of a lane whose loads are in flight
+    const int step = at_once * t.splits;
+    for (int h0 = split * at_once; h0 < t.heads; h0 += kAhead * step) {
+      float v[kAhead][16], g[BACKWARD ? kAhead : 1][16];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int h = min(h0 + k * step + sub, t.heads - 1);
+        norm::load_unit(x + (long long)h * a.D, u, v[k]);
+        if constexpr (BACKWARD) norm::load_unit(dy + (long long)h * a.D, u, g[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (h0 + k * step >= t.heads) break;  // (the same for all lanes)
+        const int h = h0 + k * step + sub;
+        const bool mine = h < t.heads;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum = fmaf(v[k][i], v[k][i], sum);
+        sum = norm::head_sum(sum, lanes, 0xffffffffu);
+        const float rms = rsqrtf(fmaf(sum, inv_d, a.eps));
+        if constexpr (BACKWARD) {
+          norm::turn_unit<INTER, -1>(g[k], cs, u, !ok);
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[k][i] *= rms;  // xh
+            if (mine) dw[i] = fmaf(g[k][i], v[k][i], dw[i]);
+            g[k][i] *= w[i];
+            dot = fmaf(g[k][i], v[k][i], dot);
+          }
+          dot = norm::head_sum(dot, lanes, 0xffffffffu) * inv_d;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[k][i] = rms * (g[k][i] - v[k][i] * dot);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[k][i] *= rms * w[i];
+          norm::turn_unit<INTER, 1>(v[k], cs, u, !ok);
+        }
+        if (mine) norm::store_unit(y + (long long)h * a.D, u, v[k]);
+      }
+    }
+  }
+  if constexpr (BACKWARD) {
+    if (t.dw == nullptr) return;  // (all threads of the block)
+    // The block's sum of each column, in the order of its head groups.
+    __shared__ float part[kThreads * 16];
+    const int groups = kThreads / lanes, group = threadIdx.x / lanes;
+    if (u.any)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[group * a.D + u.c0 + i] = dw[i];
+    if (u.pair)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[group * a.D + u.c1 + i] = dw[8 + i];
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.D; d += kThreads) {
+      float sum = 0.f;
+      for (int k = 0; k < groups; ++k) sum += part[k * a.D + d];
+      a.partial[(long long)blockIdx.x * a.D + d] = sum;
+    }
+  }
+}
+
+// One warp a head, columns lane, lane + 32, ...
+template <typename T, bool INTER, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads) qk_norm_scalar_kernel(const NormArgs a) {
+  const bool is_k = blockIdx.x >= (unsigned)a.q_blocks;
+  const NormTensor& t = is_k ? a.k : a.q;
+  const int block = is_k ? blockIdx.x - a.q_blocks : blockIdx.x, blocks = is_k ? gridDim.x - a.q_blocks : a.q_blocks;
+  const Rows<T> r = rows_of<T>(t);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float w[norm::kMaxScalar], dw[norm::kMaxScalar];
+  norm::Column col[norm::kMaxScalar];
+#pragma unroll
+  for (int j = 0; j < norm::kMaxScalar; ++j) {
+    const int d = lane + 32 * j;
+    dw[j] = 0.f;
+    w[j] = t.weight != nullptr && d < a.D ? norm::weight_at(t.weight, a.w_dtype, d) : 1.f;
+    col[j] = norm::column_of<INTER>(d, a.R);
+  }
+  const float inv_d = 1.f / (float)a.D;
+  const long long tasks = (long long)a.rows * t.heads;
+  for (long long task = (long long)block * kWarps + warp; task < tasks; task += (long long)blocks * kWarps) {
+    const uint32_t row = (uint32_t)(task / t.heads);
+    const int h = (int)(task - (long long)row * t.heads);
+    uint32_t p;
+    const bool ok = position_of(a, row, &p);
+    const float* tab = a.table + (long long)p * a.R;
+    const T* x = r.x + (long long)row * r.xs + (long long)h * a.D;
+    T* y = r.y + (long long)row * r.ys + (long long)h * a.D;
+    float v[norm::kMaxScalar], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < norm::kMaxScalar; ++j) {
+      v[j] = lane + 32 * j < a.D ? rot::to_f32(x[lane + 32 * j]) : 0.f;
+      sum = fmaf(v[j], v[j], sum);
+    }
+    const float rms = rsqrtf(fmaf(norm::head_sum(sum, 32, 0xffffffffu), inv_d, a.eps));
+    if constexpr (BACKWARD) {
+      const T* dy = r.dy + (long long)row * r.ds + (long long)h * a.D;
+      float g[norm::kMaxScalar], dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < norm::kMaxScalar; ++j) {
+        g[j] = 0.f;
+        if (lane + 32 * j < a.D)
+          g[j] = norm::turned_column<-1>(col[j], tab, a.R, ok, [&](int d) { return rot::to_f32(dy[d]); });
+        v[j] *= rms;
+        dw[j] = fmaf(g[j], v[j], dw[j]);
+        g[j] *= w[j];
+        dot = fmaf(g[j], v[j], dot);
+      }
+      dot = norm::head_sum(dot, 32, 0xffffffffu) * inv_d;  // (all lanes have read dy: y may be dy)
+#pragma unroll
+      for (int j = 0; j < norm::kMaxScalar; ++j) v[j] = rms * (g[j] - v[j] * dot);
+    } else {
+      float z[norm::kMaxScalar];
+#pragma unroll
+      for (int j = 0; j < norm::kMaxScalar; ++j) {
+        z[j] = 0.f;
+        if (lane + 32 * j < a.D)
+          z[j] = norm::turned_column<1>(col[j], tab, a.R, ok, [&](int d) {
+            return rot::to_f32(x[d]) * (rms * (t.weight != nullptr ? norm::weight_at(t.weight, a.w_dtype, d) : 1.f));
+          });
+      }
+#pragma unroll
+      for (int j = 0; j < norm::kMaxScalar; ++j) v[j] = z[j];
+    }
+    __syncwarp();  // every lane has read the row: y may be x
+#pragma unroll
+    for (int j = 0; j < norm::kMaxScalar; ++j)
+      if (lane + 32 * j < a.D) y[lane + 32 * j] = rot::from_f32<T>(v[j]);
+  }
+  if constexpr (BACKWARD) {
+    if (t.dw == nullptr) return;
+    __shared__ float part[kWarps][32 * norm::kMaxScalar];
+#pragma unroll
+    for (int j = 0; j < norm::kMaxScalar; ++j) part[warp][lane + 32 * j] = dw[j];
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.D; d += kThreads) {
+      float sum = 0.f;
+      for (int k = 0; k < kWarps; ++k) sum += part[k][d];
+      a.partial[(long long)blockIdx.x * a.D + d] = sum;
+    }
+  }
+}
+
+// dw: the blocks' sums, 32 columns a thread block, each of 32 warps every 32nd block, then the warps in order.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const NormArgs a, const int blocks) {
+  grid_dependency_wait();
+  const NormTensor& t = blockIdx.y ? a.k : a.q;
+  if (t.dw == nullptr) return;
+  const int b0 = blockIdx.y ? a.q_blocks : 0, b1 = blockIdx.y ? blocks : a.q_blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = blockIdx.x * 32 + lane;
+  __shared__ float part[32][33];
+  float sum = 0.f;
+  if (d < a.D)
+#pragma unroll 8
+    for (int b = b0 + warp; b < b1; b += 32) sum += a.partial[(long long)b * a.D + d];
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || d >= a.D) return;
+  sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) sum += part[k][lane];
+  if (a.w_dtype == ATTN_DT_F32)
+    static_cast<float*>(t.dw)[d] = sum;
+  else if (a.w_dtype == ATTN_DT_BF16)
+    static_cast<__nv_bfloat16*>(t.dw)[d] = __float2bfloat16_rn(sum);
+  else
+    static_cast<__half*>(t.dw)[d] = __float2half_rn(sum);
+}
+
+template <typename T, bool BACKWARD>
+const void* kernel_of(bool vec, bool interleaved) {
+  if (vec)
+    return interleaved ? reinterpret_cast<const void*>(qk_norm_vec_kernel<T, true, BACKWARD>)
+                       : reinterpret_cast<const void*>(qk_norm_vec_kernel<T, false, BACKWARD>);
+  return interleaved ? reinterpret_cast<const void*>(qk_norm_scalar_kernel<T, true, BACKWARD>)
+                     : reinterpret_cast<const void*>(qk_norm_scalar_kernel<T, false, BACKWARD>);
+}
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool vec_rows(const NormTensor& t) {
+  return aligned16(t.x) && aligned16(t.y) && aligned16(t.dy) && t.x_stride % 8 == 0 && t.y_stride % 8 == 0 &&
+         t.dy_stride % 8 == 0;
+}
+// Thread blocks of the backward at most, of both tensors together: each leaves a row of partial sums.
+int most_blocks(int sms) { return sms * 4; }
+
+}  // namespace
+
+size_t qk_norm_workspace_bytes(int D, int sm_count) { return (size_t)most_blocks(sm_count) * D * sizeof(float); }
+
+int launch_qk_norm(NormArgs a, int dtype, bool backward, int sm_count, cudaStream_t s) {
+  const bool vec = rot::vec_sizes(a.D, a.R, a.interleaved) && vec_rows(a.q) && vec_rows(a.k) &&
+                   (a.R == 0 || aligned16(a.table));
+  a.lanes = vec ? norm::head_lanes(a.D, a.R, a.interleaved) : 32;
+  // A row's heads are split over warps where rows alone would leave multiprocessors idle, and in the backward, whose
+  // blocks are limited, until warps have rounds enough to end together.
+  const int most = most_blocks(sm_count);
+  long long want[2] = {0, 0};
+  NormTensor* t[2] = {&a.q, &a.k};
+  for (int i = 0; i < 2; ++i) {
+    if (t[i]->heads == 0) continue;
+    const int steps = vec ? (t[i]->heads * a.lanes + 31) / 32 : t[i]->heads;
+    int splits = vec ? 1 : steps;
+    while (2 * splits <= steps && (long long)a.rows * splits < (backward ? 64ll : 16ll) * kWarps * sm_count) splits *= 2;
+    t[i]->splits = splits;
+    want[i] = ((long long)a.rows * splits + kWarps - 1) / kWarps;
+    const long long limit = backward ? most : 0x3fffffffll;
+    if (want[i] > limit) want[i] = limit;
+  }
+  if (backward && want[0] + want[1] > most) {  // in proportion to the heads, at least one each
+    int q = (int)((long long)most * a.q.heads / (a.q.heads + a.k.heads));
+    if (a.q.heads > 0 && q == 0) q = 1;
+    if (a.k.heads > 0 && q == most) q = most - 1;
+    if (want[0] > q) want[0] = q;
+    if (want[1] > most - want[0]) want[1] = most - want[0];
+  }
+  a.q_blocks = (int)want[0];
+  const int blocks = (int)(want[0] + want[1]);
+  const void* kern;
+  if (dtype == ATTN_DT_BF16)
+    kern = backward ? kernel_of<__nv_bfloat16, true>(vec, a.interleaved) : kernel_of<__nv_bfloat16, false>(vec, a.interleaved);
+  else if (dtype == ATTN_DT_F16)
+    kern = backward ? kernel_of<__half, true>(vec, a.interleaved) : kernel_of<__half, false>(vec, a.interleaved);
+  else
+    kern = backward ? kernel_of<float, true>(vec, a.interleaved) : kernel_of<float, false>(vec, a.interleaved);
+  void* args[] = {&a};
+  if (cudaLaunchKernel(kern, dim3(blocks), dim3(kThreads), args, 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (!backward || (a.q.dw == nullptr && a.k.dw == nullptr)) return ATTN_OK;
+  int n = blocks;
+  void* args2[] = {&a, &n};
+  return launch_pdl(reinterpret_cast<const void*>(qk_norm_dw_kernel), dim3((a.D + 31) / 32, 2), dim3(1024), 0, s,
+                    args2) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+}  // namespace attn

@@ -509,6 +509,128 @@ ATTN_API int attn_batch_paged(const void *q, const void *k_pages, const void *v_
                               void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /*
+ * Norms of query and key heads with their rotary turn in the same pass, and
+ * the gradients, for fp32, bf16 or fp16 rows.  Of every head x of Q and of K
+ *   z = w x r,  r = 1 / sqrt(mean(x^2) + eps)      (over its head_dim columns)
+ *   y = m R(p) z                                   (as attn_rope_apply)
+ * with one weight vector for the heads of Q and one for those of K.
+ *
+ *   q, k            [rows, heads*D], rows *_stride elements apart, so both are
+ *                   read where a packed projection left them; num_heads or
+ *                   num_kv_heads 0 leaves one of them out
+ *   q_out, k_out    as q and k; each may be its input (same stride), otherwise
+ *                   they must not overlap any input
+ *   q_weight,
+ *   k_weight        [D] of type weight_dtype, or NULL: ones
+ *   dtype           of the rows; the arithmetic is fp32, rounded once
+ *   rot_dim, layout, positions, table, table_rows
+ *                   as attn_rope_apply; rot_dim == 0 (table NULL): no turn
+ * A position >= table_rows writes zeros to the row's turned columns (the
+ * backward takes their upstream gradient as zero) and records
+ * ATTN_ERR_INVALID_ARG in the status word.  The sum of squares is fp32: |x|
+ * below 1e18.  rows == 0 is a no-op.  Errors: INVALID_ARG for NULL or
+ * misaligned pointers, unknown types or layouts, both head counts 0, D == 0 or
+ * D > 256, an odd or too large rot_dim, strides < heads*D, an output in place
+ * with another stride, an eps that is not finite or below 1e-30, or (with
+ * positions NULL) table_rows < rows.
+ *
+ * The backward takes the forward's inputs and the upstream gradients dq, dk
+ * of q_out and k_out:
+ *   dz = m R(p)^T dy,  dw = sum over rows and heads of dz x r,
+ *   dx = r (w dz - x r mean(w dz x r))
+ * dq_out and dk_out are written as q_out and k_out are (each may be dq or q,
+ * dk or k); dq_weight and dk_weight ([D] of weight_dtype, either may be NULL:
+ * not wanted) are written in full, also for rows == 0.  Sums are fp32, in a
+ * fixed order: repeated calls give identical bits.  workspace (16-byte
+ * aligned; not needed when both are NULL) holds
+ * attn_qk_norm_rope_backward_workspace_bytes bytes and keeps nothing between
+ * calls; calls that share it must not overlap on the GPU.
+ */
+ATTN_API int attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const void *q_weight,
+                               const void *k_weight, attn_dtype_t dtype, attn_dtype_t weight_dtype, uint32_t rows,
+                               uint32_t num_heads, uint32_t num_kv_heads, uint32_t head_dim, uint32_t q_stride,
+                               uint32_t k_stride, uint32_t q_out_stride, uint32_t k_out_stride, float eps,
+                               uint32_t rot_dim, attn_rope_layout_t layout, const uint32_t *positions,
+                               const float *table, uint32_t table_rows, attn_stream_t stream);
+ATTN_API size_t attn_qk_norm_rope_backward_workspace_bytes(uint32_t head_dim);
+ATTN_API int attn_qk_norm_rope_backward(const void *dq, const void *dk, const void *q, const void *k, void *dq_out,
+                                        void *dk_out, const void *q_weight, const void *k_weight, void *dq_weight,
+                                        void *dk_weight, attn_dtype_t dtype, attn_dtype_t weight_dtype, uint32_t rows,
+                                        uint32_t num_heads, uint32_t num_kv_heads, uint32_t head_dim,
+                                        uint32_t dq_stride, uint32_t dk_stride, uint32_t q_stride, uint32_t k_stride,
+                                        uint32_t dq_out_stride, uint32_t dk_out_stride, float eps, uint32_t rot_dim,
+                                        attn_rope_layout_t layout, const uint32_t *positions, const float *table,
+                                        uint32_t table_rows, void *workspace, size_t workspace_bytes,
+                                        attn_stream_t stream);
+
+/*
+ * The paged cache in 8 bits.  The batch is described as for attn_append_paged;
+ * the pools hold e4m3 codes and two arrays their scales:
+ *   k_pages, v_pages    [num_pages * page_rows, kv_dim] bytes; kv head g at
+ *                       column g*D
+ *   k_scales, v_scales  [num_pages * page_rows / scale_rows, num_kv_heads]
+ *                       bytes: pool rows [b * scale_rows, (b + 1) * scale_rows)
+ *                       of head g share the scale 2^(k_scales[b][g] - 127)
+ *   scale_rows          divides page_rows (1: a scale for every position and
+ *                       head; page_rows: one a page)
+ * A value is code times scale.  Scales run from 2^-14 to 2^7 (bytes outside
+ * read as the nearest of these), so every value is exactly a bf16 and an fp16
+ * number, from steps of 2^-23 up to 57344.
+ *
+ * attn_append_paged8 writes the new rows' K and V: K normed (k_weight, [D] of
+ * weight_dtype, not NULL; as attn_qk_norm_rope) and turned by its position
+ * (rot_dim > 0), both then rounded to codes of the smallest scale 2^e with
+ * max|x| <= 448 * 2^e over all rows of the scale's block written so far; and
+ * Q, normed (q_weight) and turned, into q_out.
+ *   - A block whose first position is among the new rows starts anew,
+ *     whatever its page held.  In a block that held earlier positions of the
+ *     sequence, these keep their codes, or, where the scale grows, are
+ *     multiplied by the scales' quotient and rounded again (exact but for
+ *     codes that become subnormal).
+ *   - Magnitudes above 57344, and infinities, become 57344; a NaN stays one
+ *     and counts for no scale.  The arithmetic is fp32 up to the rounding.
+ *   - q_out_dtype is ATTN_DT_BF16 or ATTN_DT_F16: dtype itself unless that is
+ *     ATTN_DT_F32 (else ATTN_ERR_UNSUPPORTED).  q, q_out NULL with num_heads == 0
+ *     leave Q out.
+ * Rows that attn_append_paged skips are skipped here (their q_out, too), with
+ * the same status.  No two rows may belong to the same scale of the pools
+ * unless they are of one sequence.  total_rows == 0 or n_seqs == 0 is a no-op.
+ * Errors: INVALID_ARG as attn_append_paged, and for a scale_rows that does not
+ * divide page_rows, NULL scales, a weight for Q without Q, or (with a weight)
+ * an eps as attn_qk_norm_rope; UNSUPPORTED for head_dim % 16 != 0, kv_dim %
+ * 16 != 0 or pools that are not 16-byte aligned.
+ *
+ * attn_read_paged8 writes the values of a range of each sequence's positions,
+ * rounded to dtype (bf16 and fp16 hold them exactly):
+ *   starts       [n_seqs + 1]: rows [starts[s], starts[s+1]) of k_out and
+ *                v_out are sequence s's positions first[s], first[s] + 1, ...
+ *                Rows of no sequence are left untouched.
+ *   first        [n_seqs], or NULL: from position 0
+ *   kv_len       [n_seqs]: a position past it (or past the capacity, or in a
+ *                page outside the pool) reads as zeros and records
+ *                ATTN_ERR_INVALID_ARG in the status word
+ *   k_out, v_out [total_rows, ...] of type dtype, rows k_stride / v_stride
+ *                elements apart
+ * Errors as attn_append_paged8's.
+ */
+ATTN_API int attn_append_paged8(const void *q, void *q_out, const void *k_new, const void *v_new, attn_dtype_t dtype,
+                                attn_dtype_t q_out_dtype, void *k_pages, void *v_pages, uint8_t *k_scales,
+                                uint8_t *v_scales, const uint32_t *block_table, const uint32_t *q_start,
+                                const uint32_t *kv_len, uint32_t total_rows, uint32_t n_seqs, uint32_t num_heads,
+                                uint32_t num_kv_heads, uint32_t head_dim, uint32_t kv_dim, uint32_t q_stride,
+                                uint32_t q_out_stride, uint32_t k_stride, uint32_t v_stride, uint32_t page_rows,
+                                uint32_t num_pages, uint32_t max_blocks, uint32_t scale_rows, const void *q_weight,
+                                const void *k_weight, attn_dtype_t weight_dtype, float eps, uint32_t rot_dim,
+                                attn_rope_layout_t layout, const float *table, uint32_t table_rows,
+                                attn_stream_t stream);
+ATTN_API int attn_read_paged8(const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+                              const uint8_t *v_scales, void *k_out, void *v_out, attn_dtype_t dtype,
+                              const uint32_t *block_table, const uint32_t *starts, const uint32_t *first,
+                              const uint32_t *kv_len, uint32_t total_rows, uint32_t n_seqs, uint32_t num_kv_heads,
+                              uint32_t head_dim, uint32_t kv_dim, uint32_t k_stride, uint32_t v_stride,
+                              uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks, uint32_t scale_rows,
+                              attn_stream_t stream);
+/*
  * Backward of attn_forward / attn_forward_window: the gradients of `out` with
  * respect to q, k and v for an upstream gradient dout.  The pages emit the
  * per-row (max, log-sum) pair for a backward pass (meganeura attention.wgsl:
