@@ -87,6 +87,8 @@ def load_library(path=None):
     lib.attn_batch_paged.restype = ctypes.c_int
     lib.attn_batch_paged.argtypes = [_vp] * 4 + [ctypes.c_int, _vp, _vp, _vp] + [_u32] * 11 + \
         [ctypes.c_float, _u32, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_batch_paged_sinks.restype = ctypes.c_int
+    lib.attn_batch_paged_sinks.argtypes = lib.attn_batch_paged.argtypes[:-1] + [_u32, _vp]
     lib.attn_qk_norm_rope.restype = ctypes.c_int
     lib.attn_qk_norm_rope.argtypes = [_vp] * 6 + [ctypes.c_int] * 2 + [_u32] * 8 + \
         [ctypes.c_float, _u32, ctypes.c_int, _vp, _vp, _u32, _vp]
@@ -395,6 +397,24 @@ def attn_batch_paged(q, k_pages, v_pages, out, block_table, q_start, kv_len, tot
         float(scale), window, float(softcap), _addr(alibi_slopes, "alibi_slopes", _f32()),
         _u32_addr(prefix_len, "prefix_len"), _addr(workspace, "workspace"), workspace_bytes, _stream(stream)),
         "attn_batch_paged")
+
+
+def attn_batch_paged_sinks(q, k_pages, v_pages, out, block_table, q_start, kv_len, total_rows, n_seqs, n_heads,
+                           n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks, scale,
+                           window, softcap, alibi_slopes, prefix_len, workspace, workspace_bytes=None, sinks=0,
+                           stream=None):
+    """attn_batch_paged with the first `sinks` positions visible behind the window; see attn_gqa.h."""
+    code = _dtype_code(q, "q")
+    _same_dtype(code, k_pages=k_pages, v_pages=v_pages, out=out)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(load_library().attn_batch_paged_sinks(
+        _addr(q, "q"), _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"), _addr(out, "out"), code,
+        _u32_addr(block_table, "block_table"), _u32_addr(q_start, "q_start"), _u32_addr(kv_len, "kv_len"), total_rows,
+        n_seqs, n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks,
+        float(scale), window, float(softcap), _addr(alibi_slopes, "alibi_slopes", _f32()),
+        _u32_addr(prefix_len, "prefix_len"), _addr(workspace, "workspace"), workspace_bytes, sinks, _stream(stream)),
+        "attn_batch_paged_sinks")
 
 
 def _weight_code(code, **weights):

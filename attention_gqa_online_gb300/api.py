@@ -612,9 +612,9 @@ def read_paged8(batch, cache, starts, k_out, v_out, first=None, stream=None):
 
 
 def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, softcap=0.0, alibi_slopes=None,
-                 prefix_len=None, stream=None):
+                 prefix_len=None, stream=None, sinks=0):
     """Attention of the batch's new tokens, q [rows, H*D] (bf16 or fp16), over its pages: the last `window`
-    keys of each row (0 = all), scores capped by softcap * tanh(s / softcap) (0 = uncapped) and biased by
+    keys of each row (0 = all) and its sequence's first `sinks`, scores capped by softcap * tanh(s / softcap) (0 = uncapped) and biased by
     -alibi_slopes[h] * distance, keys below prefix_len[s] visible to every row.  Rows of no sequence are
     left as they are in `out`."""
     kv_dim, num_pages = batch.pool(k_pages, v_pages)
@@ -641,8 +641,9 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
         slopes = alibi_slopes.data_ptr()
     if prefix_len is not None and prefix_len.numel() != batch.n_seqs:
         raise ValueError("prefix_len must hold one length a sequence")
-    if window:
+    if window or sinks:
         _count32("window", window)
+        _count32("sinks", sinks)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     index = k_pages.get_device()
@@ -652,9 +653,9 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
     stream = _handle(stream, index)
     if stream not in batch._streams:
         batch._use_on(stream)
-    _run("attn_batch_paged", B.load_library().attn_batch_paged, index, stream,
+    _run("attn_batch_paged_sinks" if sinks else "attn_batch_paged", B.load_library().attn_batch_paged_sinks, index, stream,
          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), code,
           batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H,
           batch.num_kv_heads, D, kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks, scale, window,
-          softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel()))
+          softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel(), sinks))
     return out

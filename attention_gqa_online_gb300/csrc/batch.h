@@ -180,6 +180,7 @@ struct BatchArgs {
   int n_seqs, H, G, D, gs;
   int page_rows, num_pages, max_blocks, capacity;
   int window;  // 0 = none
+  int sinks;   // first positions that stay visible behind the window (0 without a window)
   float scale, softcap;
   FastDiv by_gs, by_page;  // by gs and page_rows; set by launch_batch_paged
   unsigned wait_ns;        // limit of each wait inside the kernels, 0 = the usual one; set by launch_batch_paged

@@ -153,6 +153,20 @@ extern "C" int attn_batch_paged(const void* q, const void* k_pages, const void* 
                                 uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks, float scale,
                                 uint32_t window, float softcap, const float* alibi_slopes, const uint32_t* prefix_len,
                                 void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  return attn_batch_paged_sinks(q, k_pages, v_pages, out, dtype, block_table, q_start, kv_len, total_rows, n_seqs,
+                                n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages,
+                                max_blocks, scale, window, softcap, alibi_slopes, prefix_len, workspace,
+                                workspace_bytes, 0, stream);
+}
+
+extern "C" int attn_batch_paged_sinks(const void* q, const void* k_pages, const void* v_pages, void* out,
+                                      attn_dtype_t dtype, const uint32_t* block_table, const uint32_t* q_start,
+                                      const uint32_t* kv_len, uint32_t total_rows, uint32_t n_seqs, uint32_t n_heads,
+                                      uint32_t n_kv_heads, uint32_t head_dim, uint32_t kv_dim, uint32_t q_stride,
+                                      uint32_t out_stride, uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks,
+                                      float scale, uint32_t window, float softcap, const float* alibi_slopes,
+                                      const uint32_t* prefix_len, void* workspace, size_t workspace_bytes,
+                                      uint32_t sinks, attn_stream_t stream) {
   if (!heads_ok(n_heads, n_kv_heads, head_dim) || !dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
   if (!paged_ok(page_rows, num_pages, max_blocks)) return ATTN_ERR_INVALID_ARG;
   if (kv_dim < (uint64_t)n_kv_heads * head_dim || q_stride < (uint64_t)n_heads * head_dim ||
@@ -203,6 +217,7 @@ extern "C" int attn_batch_paged(const void* q, const void* k_pages, const void* 
   a.max_blocks = (int)max_blocks;
   a.capacity = (int)(page_rows * max_blocks);
   a.window = window > 0x7fffffffu ? 0x7fffffff : (int)window;
+  a.sinks = window == 0 ? 0 : sinks > 0x3fffffffu ? 0x3fffffff : (int)sinks;
   a.scale = scale;
   a.softcap = softcap;
   return launch_batch_paged(a, dtype, workspace, sms, reinterpret_cast<cudaStream_t>(stream));

@@ -52,9 +52,9 @@ constexpr int kRingBytes = 128 * 1024;
 constexpr int kMaxStages = 4;
 
 struct DecodeDesc {
-  int end, whole, n, tile0;
+  int end, whole, n, tile0, ns, skip;  // tiles tile0 .. tile0 + n - 1 of the item's (plan::tile_at)
   int seq, g, row0, q_len, len, pfx, first_row, rows;
-  int lo_min, lo_max, hi_min, hi_max;
+  int lo_min, lo_max, hi_min, hi_max, se;
   int slot, first, last, slot0;
 };
 
@@ -141,16 +141,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
     const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
     const int parts = kKeys / box_rows;             // page parts of a tile, at most 16
+    const int parts_log2 = __ffs(parts) - 1;
     const int chunk = D == 128 ? sub : 0;
     const bool my_part = lane < parts && (D == 128 || (lane & 1) == sub);
     // Tiles of one piece, from tile number J on.
-    auto load_tiles = [&](int n, int seq, int g, int lo, int hi, int tile0, int J) {
-      const int key0 = tile0 * kKeys;
+    auto load_tiles = [&](int n, int seq, int g, int se, int lo, int hi, int tile0, int ns, int skip, int J) {
+      // First key of part q.
+      auto key_of = [&](int q) {
+        return plan::tile_at(tile0 + (q >> parts_log2), ns, skip) * kKeys + (q & (parts - 1)) * box_rows;
+      };
       const uint32_t* table = a.block_table + (long long)seq * a.max_blocks;
       // Pool rows of the page parts, 32 at a time (one a lane), read at least 32 parts ahead.
       auto rows_of = [&](int q0) {
-        const int q = q0 + lane, key = key0 + q * box_rows;
-        const bool seen = q < n * parts && key < hi && key + box_rows > lo;
+        const int q = q0 + lane, key = key_of(q);
+        const bool seen = q < n * parts && !plan::keys_hidden(key, box_rows, se, lo, hi);
         const int col = seen ? plan::page_of(a, key) : 0;
         const uint32_t pg = table[col];  // (no branch around it: two such reads overlap)
         return !seen ? outside : pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           record_status(a.status, ATTN_ERR_INVALID_ARG);
           row = outside;
         }
-        const int key = key0 + (q0 + lane) * box_rows, st = J % S::stages;
+        const int key = key_of(q0) + lane * box_rows, st = J % S::stages;
         // A wait that ran out ends the role: a slot in use must not be written, nor a phase arrived at twice.
         if (J >= S::stages && !wait(&sm.empty[st], J / S::stages - 1)) return J;
         if (pw == 0 && lane == 0) mbar_arrive_expect_tx(&sm.full[st], (unsigned)(2 * S::tile_bytes));
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + chunk * kChunkBytes;
         // V rows of a fetched part that lie outside the windows are replaced by zeros (0 * NaN), by eights or single
         // rows.
-        const bool edge = is_v && row != outside && (key < lo || key + box_rows > hi);
+        const bool edge = is_v && row != outside && !plan::keys_inside(key, box_rows, se, lo, hi);
         if (my_part && !edge) tma_load_3d(dst + lane * box_rows * 128, tm, 64 * chunk, g, row, &sm.full[st]);
         unsigned edges = __ballot_sync(0xffffffffu, edge);
         while (edges) {
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           edges &= edges - 1;
           const int row_e = __shfl_sync(0xffffffffu, row, e), key_e = __shfl_sync(0xffffffffu, key, e);
           const int key_8 = key_e + 8 * lane;  // eight rows a lane; those that are not all of one kind, row by row
-          const bool inside = key_8 >= lo && key_8 + 8 <= hi, outer = key_8 + 8 <= lo || key_8 >= hi;
+          const bool inside = plan::keys_inside(key_8, 8, se, lo, hi), outer = plan::keys_hidden(key_8, 8, se, lo, hi);
           if (8 * lane < box_rows && (inside || outer)) {
             const int y = inside ? row_e + 8 * lane : outside;
             tma_load_3d(dst + (e * box_rows + 8 * lane) * 128, &tm_v8, 64 * chunk, g, y, &sm.full[st]);
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 8 * (__ffs(mixed) - 1) + lane;
             mixed &= mixed - 1;
             if (lane < 8) {
-              const int y = key_e + r >= lo && key_e + r < hi ? row_e + r : outside;
+              const int y = plan::keys_inside(key_e + r, 1, se, lo, hi) ? row_e + r : outside;
               tma_load_3d(dst + (e * box_rows + r) * 128, &tm_v1, 64 * chunk, g, y, &sm.full[st]);
             }
           }
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (;; ++x) {
         const DecodeDesc& d = sm.desc[x % kDescs];
         if (!wait(&sm.desc_full[x % kDescs], x / kDescs) || !warp_whole(&sm.abort) || d.end) break;
-        J = load_tiles(d.n, d.seq, d.g, d.lo_min, d.hi_max, d.tile0, J);
+        J = load_tiles(d.n, d.seq, d.g, d.se, d.lo_min, d.hi_max, d.tile0, d.ns, d.skip, J);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
       }
@@ -237,7 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) {
           d.whole = p.whole;
           d.n = p.t1 - p.t0;
-          d.tile0 = p.k.kt0 + p.t0;
+          d.tile0 = p.t0;
+          d.ns = p.k.ns;
+          d.skip = p.k.skip;
+          d.se = p.k.se;
           d.seq = p.s;
           d.g = p.g;
           d.row0 = p.q.row0;
@@ -269,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  static_cast<const T*>(a.q) + (long long)(p.q.row0 + t) * a.q_stride + (long long)h * a.D, a.D * 2,
                  &sm.q_ready[x & 1]);
       }
-      J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.lo_min, p.k.hi_max, p.k.kt0 + p.t0, J);
+      J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.se, p.k.lo_min, p.k.hi_max, p.t0, p.k.ns, p.k.skip, J);
       ++x;
       if (!warp_whole(&sm.abort)) break;
     }
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[y][e] += s1[y][e];
       }
-      const int tile_key = (d.tile0 + i) * kKeys, key0 = tile_key + kw + lc;
+      const int tile_key = plan::tile_at(d.tile0 + i, d.ns, d.skip) * kKeys, key0 = tile_key + kw + lc;
       if (a.softcap > 0.f) {
 #pragma unroll
         for (int y = 0; y < kTiles; ++y)
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + 8 * y + (e & 1);
-            if (key >= hi[e >> 1] || key < lo[e >> 1]) s[y][e] = -INFINITY;
+            if (key >= hi[e >> 1] || (key < lo[e >> 1] && key >= a.sinks)) s[y][e] = -INFINITY;
           }
       }
       float t[2] = {-INFINITY, -INFINITY};

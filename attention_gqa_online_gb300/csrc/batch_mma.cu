@@ -78,12 +78,12 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
     }
     const uint32_t* table = a.block_table + (long long)p.s * a.max_blocks;
     auto load_tile = [&](int i, int st) {
-      const int key0 = (p.k.kt0 + i) * kKeys;
+      const int key0 = plan::tile_at(i, p.k.ns, p.k.skip) * kKeys;
       for (int c = tid; c < kKeys * kUnits; c += kThreads) {
         const int r = c / kUnits, u = c % kUnits;
         const int key = key0 + r;
         long long row = -1;
-        if (key >= p.k.lo_min && key < p.k.hi_max)
+        if ((key >= p.k.lo_min && key < p.k.hi_max) || key < p.k.se)
           row = paged_row(table, a.page_rows, a.num_pages, key, a.status);
         const bool ok = row >= 0 && 8 * u < a.D;
         const long long off = ok ? row * a.kv_dim + (long long)p.g * a.D + 8 * u : 0;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
           mma16816<T>(s[2 * j + 1], qa, kb[2], kb[3]);
         }
       }
-      const int key0 = (p.k.kt0 + p.t0 + i) * kKeys;
+      const int key0 = plan::tile_at(p.t0 + i, p.k.ns, p.k.skip) * kKeys;
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int j = 0; j < kKeys / 8; ++j)
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
             v *= sm.scale2;
           }
           v -= slope[x] * fabsf((float)(pos[x] - key));
-          v = (key >= lo[x] && key < hi[x]) ? v : -INFINITY;
+          v = ((key >= lo[x] || key < a.sinks) && key < hi[x]) ? v : -INFINITY;
           s[j][e] = v;
           mx[x] = fmaxf(mx[x], v);
         }

@@ -4,7 +4,7 @@
 // The query rows of sequence s and kv head g are flattened as r = t * gs + j
 // (token t, head g * gs + j) and cut into blocks of ROWS; an item is one
 // (sequence, row block, kv head).  Its keys are the union of its rows'
-// windows, walked in tiles of KEYS.  Every item weighs its tiles plus item_cost (what
+// windows, and of the first positions that stay visible behind them, walked in tiles of KEYS.  Every item weighs its tiles plus item_cost (what
 // its Q load, epilogue and masked tiles take, in tiles); the weights of all items, laid end to end in (sequence,
 // row block, kv head) order, are cut into equal ranges, one per thread block.  A
 // range boundary inside an item splits its keys: each part is a piece, whose
@@ -54,10 +54,21 @@ __device__ __forceinline__ int row_lo(const BatchArgs& a, const SeqInfo& q, int 
   return (a.window > 0 && n > a.window) ? n - a.window : 0;
 }
 
+// Keys of a block's rows: [0, se) and [lo_min, hi_max), se < lo_min or se == 0.
 struct BlockKeys {
-  int lo_min, lo_max, hi_min, hi_max;  // extremes over the block's rows
-  int kt0, nt;                         // key tiles kt0 .. kt0 + nt - 1
+  int lo_min, lo_max, hi_min, hi_max;  // extremes over the rows' windows (lo_min 0 where the first positions reach them)
+  int se;                              // end of the first positions in sight of a row
+  int ns, skip, nt;                    // tiles: nt in all, the first ns from tile 0 on, the others `skip` later
 };
+// Key tile of tile t of the nt.
+__device__ __forceinline__ int tile_at(int t, int ns, int skip) { return t < ns ? t : t + skip; }
+// Can no row see, or can some row see all of, keys [key, key + n)?  (Of one of the two ranges.)
+__device__ __forceinline__ bool keys_hidden(int key, int n, int se, int lo, int hi) {
+  return (key + n <= lo || key >= hi) && key >= se;
+}
+__device__ __forceinline__ bool keys_inside(int key, int n, int se, int lo, int hi) {
+  return (key >= lo && key + n <= hi) || key + n <= se;
+}
 
 template <int ROWS>
 __device__ __forceinline__ int row_blocks(const BatchArgs& a, const SeqInfo& q) {
@@ -74,8 +85,12 @@ __device__ __forceinline__ BlockKeys block_keys(const BatchArgs& a, const SeqInf
   k.hi_min = row_hi(q, t0);
   k.hi_max = row_hi(q, t1);
   const bool any = k.hi_max > k.lo_min;
-  k.kt0 = k.lo_min / KEYS;
-  k.nt = any ? (k.hi_max + KEYS - 1) / KEYS - k.kt0 : 0;
+  k.se = min(a.sinks, k.lo_max);
+  if (k.se >= k.lo_min) k.lo_min = k.se = 0;
+  const int kt0 = k.lo_min / KEYS;
+  k.ns = min((k.se + KEYS - 1) / KEYS, kt0);
+  k.skip = kt0 - k.ns;
+  k.nt = any ? (k.hi_max + KEYS - 1) / KEYS - k.skip : 0;
   return k;
 }
 

@@ -97,9 +97,9 @@ struct PieceDesc {
   int row0, q_len, len, pfx;
   int first_row;   // first flattened row of this block
   int rows;        // valid rows from there on, at most 128
-  int lo_min, lo_max, hi_min, hi_max;
+  int lo_min, lo_max, hi_min, hi_max, se;
   int first, last, slot0;  // the item's pieces (plan::Piece)
-  int tile_last, n;  // key tiles tile_last, tile_last - 1, ... (n of them) of the sequence
+  int tile_last, n, ns, skip;  // tiles tile_last, tile_last - 1, ... (n of them) of the item's (plan::tile_at)
   int pos_min;       // position of the block's first row
 };
 
@@ -402,19 +402,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
     struct Parts {
       int shift;             // log2 of the page parts of a tile held here
-      int n, lo, hi, key0;   // tiles; the windows' ends; first key held here of tile 0
+      int n, se, lo, hi;     // tiles; what the rows see: keys [0, se) and [lo, hi)
+      int last, ns, skip;    // the item's tile that is tile 0 here, and plan::tile_at's
+      int off;               // first key held here of a tile
       const uint32_t* table;
       int now, next;         // pool rows of 32 parts, and of the 32 after
     };
+    auto first_key_of = [&](const Parts& w, int i) { return plan::tile_at(w.last - i, w.ns, w.skip) * kTcKeys + w.off; };
     auto rows_of = [&](const Parts& w, int q0) {
-      const int q = q0 + lane, i = q >> w.shift, key = w.key0 - i * kTcKeys + (q - (i << w.shift)) * box_rows;
-      const bool seen = i < w.n && key < w.hi && key + box_rows > w.lo;
+      const int q = q0 + lane, i = q >> w.shift, key = first_key_of(w, i) + (q - (i << w.shift)) * box_rows;
+      const bool seen = i < w.n && !plan::keys_hidden(key, box_rows, w.se, w.lo, w.hi);
       const int col = seen ? plan::page_of(a, key) : 0;
       const uint32_t pg = w.table[col];  // (no branch around it: two such reads overlap)
       return !seen ? outside : pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
     };
-    auto open_parts = [&](int keys, int n, int lo, int hi, int key0, int seq) {
-      Parts w{__ffs(keys) - __ffs(box_rows), n, lo, hi, key0, a.block_table + (long long)seq * a.max_blocks, 0, 0};
+    auto open_parts = [&](int keys, int off, const PieceDesc& d) {
+      Parts w{__ffs(keys) - __ffs(box_rows), d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip, off,
+              a.block_table + (long long)d.seq * a.max_blocks, 0, 0};
       w.now = rows_of(w, 0);
       w.next = rows_of(w, 32);
       return w;
@@ -483,7 +487,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             d.lo_max = p.k.lo_max;
             d.hi_min = p.k.hi_min;
             d.hi_max = p.k.hi_max;
-            d.tile_last = p.k.kt0 + p.t1 - 1;
+            d.se = p.k.se;
+            d.tile_last = p.t1 - 1;
+            d.ns = p.k.ns;
+            d.skip = p.k.skip;
             d.n = p.t1 - p.t0;
             d.pos_min = p.q.len - p.q.q_len + plan::token_of(a, first_row);
           }
@@ -493,8 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!more) break;
         // The piece's first page parts are looked up while its Q buffer falls free.
         const int n = p.t1 - p.t0, col = FULL ? p.g * D : 0;
-        Parts w = open_parts(L::k_rows, n, p.k.lo_min, p.k.hi_max,
-                             (p.k.kt0 + p.t1 - 1) * kTcKeys + (PAIR ? rank * L::k_rows : 0), p.s);
+        Parts w = open_parts(L::k_rows, PAIR ? rank * L::k_rows : 0, sm.desc[x % kDescs]);
         // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
         // only feeds itself, and those rows are not stored).
         if (x >= 2) ok = wait(&sm.q_free[x & 1], (x >> 1) - 1);
@@ -557,9 +563,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!next_piece(x)) break;
         const PieceDesc& d = sm.desc[x % kDescs];
         const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
-        Parts w = open_parts(kTcKeys, n, d.lo_min, d.hi_max, d.tile_last * kTcKeys, d.seq);
+        Parts w = open_parts(kTcKeys, 0, d);
         for (int i = 0; i < n; ++i, ++J) {
-          const int row = part_row(w, i), key = w.key0 - i * kTcKeys + lane * box_rows, slot = J % L::slots;
+          const int row = part_row(w, i), key = first_key_of(w, i) + lane * box_rows, slot = J % L::slots;
           if (J >= L::slots) ok = wait(&sm.v_empty[slot], J / L::slots - 1);
           if (!ok) break;
           if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.v_full[slot], (unsigned)(PAIR ? 2 : 1) * L::v_bytes);
@@ -567,7 +573,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint32_t bar = barrier_of(&sm.v_full[slot]);
           // A part that reaches outside the block's windows goes by eights or single rows: what the page holds there (0 * NaN would
           // reach every row) is replaced by zeros from outside the pool.
-          const bool edge = row != outside && (key < w.lo || key + box_rows > w.hi);
+          const bool edge = row != outside && !plan::keys_inside(key, box_rows, w.se, w.lo, w.hi);
           if ((lane >> w.shift) == 0 && !edge) {
 #pragma unroll
             for (int c = 0; c < L::v_chunks; ++c)
@@ -580,7 +586,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             edges &= edges - 1;
             const int row_p = __shfl_sync(0xffffffffu, row, p), key_p = __shfl_sync(0xffffffffu, key, p);
             const int key_8 = key_p + 8 * lane;  // eight rows a lane; those that are not all of one kind, row by row
-            const bool inside = key_8 >= w.lo && key_8 + 8 <= w.hi, outer = key_8 + 8 <= w.lo || key_8 >= w.hi;
+            const bool inside = plan::keys_inside(key_8, 8, w.se, w.lo, w.hi);
+            const bool outer = plan::keys_hidden(key_8, 8, w.se, w.lo, w.hi);
             if (8 * lane < box_rows && (inside || outer)) {
               const int y = inside ? row_p + 8 * lane : outside;
 #pragma unroll
@@ -593,7 +600,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int r = 8 * (__ffs(mixed) - 1) + lane;
               mixed &= mixed - 1;
               if (lane < 8) {
-                const int y = key_p + r >= w.lo && key_p + r < w.hi ? row_p + r : outside;
+                const int y = plan::keys_inside(key_p + r, 1, w.se, w.lo, w.hi) ? row_p + r : outside;
 #pragma unroll
                 for (int c = 0; c < L::v_chunks; ++c)
                   load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + (p * box_rows + r) * 128, &tm_v1, col + 64 * c, g, y,
@@ -697,7 +704,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm.row[128 * grp + r] = info;  // read on the tiles that need it: kept in registers it would spill scores
       for (int i = (J & 1) ^ grp; i < n; i += 2) {
         const int j = J + i, b = j & 1;
-        const int key0 = (d.tile_last - i) * kTcKeys;
+        const int key0 = plan::tile_at(d.tile_last - i, d.ns, d.skip) * kTcKeys;
         // Does the tile cross some row's window end, or start?
         const bool cut_hi = key0 + kTcKeys > d.hi_min, cut_lo = key0 < d.lo_max;
         wait(&sm.s_full[b], j >> 1);
@@ -820,12 +827,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (32 * c + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
           }
           if (cut_lo) {
-            const int lim = sm.row[128 * grp + r].x - key0;
+            // Keys [sinks, lo) of the sequence: columns [from, from + count) of the tile.
+            const int from = a.sinks - key0;
+            const unsigned count = (unsigned)max(0, sm.row[128 * grp + r].x - a.sinks);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (32 * c + e < lim) s[c][e] = __float_as_uint(-INFINITY);
+                if ((unsigned)(32 * c + e - from) < count) s[c][e] = __float_as_uint(-INFINITY);
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll

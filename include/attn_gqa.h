@@ -509,6 +509,25 @@ ATTN_API int attn_batch_paged(const void *q, const void *k_pages, const void *v_
                               void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /*
+ * attn_batch_paged_sinks: attn_batch_paged with one more argument, `sinks`,
+ * placed just before `stream`: the sequence's first positions stay visible
+ * behind the window.  The row at position p attends the keys
+ *   [0, min(sinks, lo)) and [lo, hi)
+ * with lo and hi as above (sinks == 0, or a window that reaches the first
+ * positions: attn_batch_paged; bias and cap are those of each key's own
+ * position).  Key tiles between the two ranges are neither read nor computed.
+ * No further errors.
+ */
+ATTN_API int attn_batch_paged_sinks(const void *q, const void *k_pages, const void *v_pages, void *out,
+                                    attn_dtype_t dtype, const uint32_t *block_table, const uint32_t *q_start,
+                                    const uint32_t *kv_len, uint32_t total_rows, uint32_t n_seqs, uint32_t n_heads,
+                                    uint32_t n_kv_heads, uint32_t head_dim, uint32_t kv_dim, uint32_t q_stride,
+                                    uint32_t out_stride, uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks,
+                                    float scale, uint32_t window, float softcap, const float *alibi_slopes,
+                                    const uint32_t *prefix_len, void *workspace, size_t workspace_bytes,
+                                    uint32_t sinks, attn_stream_t stream);
+
+/*
  * Norms of query and key heads with their rotary turn in the same pass, and
  * the gradients, for fp32, bf16 or fp16 rows.  Of every head x of Q and of K
  *   z = w x r,  r = 1 / sqrt(mean(x^2) + eps)      (over its head_dim columns)

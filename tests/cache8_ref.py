@@ -62,3 +62,50 @@ class Batch8(Batch):
             for first in range((n - m) // self.sr * self.sr, n if m else 0, self.sr):
                 out.append((i, first, max(0, n - m - first), min(self.sr, n - first)))
         return out
+
+
+def attend64(b, q=None, window=0, sinks=0, softcap=0.0, slopes=None, prefix=None, scale=None):
+    """(out, sum_j p_j |v_j|, largest |v| attended) in 64 bits from b.k and b.v; rows of no sequence are zeros."""
+    q = b.q if q is None else q
+    H, G, D = b.H, b.G, b.D
+    gs = H // G
+    scale = D ** -0.5 if scale is None else scale
+    out = torch.zeros(q.shape[0], H * D, dtype=torch.float64, device="cuda")
+    mag, vmax = torch.zeros_like(out), 0.0
+    for i, (n, length) in enumerate(zip(b.new, b.kv)):
+        if n == 0 or length == 0:
+            continue
+        sl = b.slots(i, 0, length)
+        k, v = (x[sl, :G * D].double().view(length, G, D) for x in (b.k, b.v))
+        j = torch.arange(length, device="cuda")
+        for r0 in range(0, n, 512):
+            r1 = min(n, r0 + 512)
+            p = torch.arange(length - n + r0, length - n + r1, device="cuda")[:, None]
+            ok = j <= p
+            if prefix is not None:
+                ok = ok | (j < prefix[i])
+            if window:
+                ok = ok & ((j > p - window) | (j < sinks))
+            used = ok.any(0).view(length, 1, 1)
+            kk, vv = (torch.where(used, x, torch.zeros((), dtype=x.dtype, device="cuda")) for x in (k, v))
+            x = q[b.starts[i] + r0:b.starts[i] + r1].double().view(r1 - r0, G, gs, D)
+            s = scale * torch.einsum("nghd,jgd->ghnj", x, kk)
+            if softcap:
+                s = softcap * torch.tanh(s / softcap)
+            if slopes is not None:
+                s = s - slopes.double().view(G, gs, 1, 1) * (p - j).abs()
+            s = s.masked_fill(~ok, float("-inf"))
+            w = torch.exp(s - s.amax(-1, keepdim=True).clamp_min(-1e300)).masked_fill(~ok, 0.0)
+            w = w / w.sum(-1, keepdim=True).clamp_min(1e-300)
+            rows = slice(b.starts[i] + r0, b.starts[i] + r1)
+            out[rows] = torch.einsum("ghnj,jgd->nghd", w, vv).reshape(r1 - r0, H * D)
+            mag[rows] = torch.einsum("ghnj,jgd->nghd", w, vv.abs()).reshape(r1 - r0, H * D)
+            vmax = max(vmax, float(vv.abs().max()))
+    return out, mag, vmax
+
+
+def tolerance(ref, mag, vmax, dtype, p_dtype, keys):
+    """Bound on |kernel - ref|, as attend_tolerance of batch_ref.py, for weights rounded to p_dtype and results to dtype."""
+    sub = vmax * keys * 2.0 ** -25 if p_dtype == torch.float16 else 0.0
+    half, half_p = torch.finfo(dtype).eps / 2, torch.finfo(p_dtype).eps / 2
+    return 1.01 * (half_p * mag + half * ref.abs() + 2.0 ** -12 * mag) + sub + 1e-9
