@@ -86,7 +86,7 @@ struct __align__(1024) DecodeSmem {
   int is_last;  // this block joins the item
 };
 
-template <typename T, int D, bool BRIEF = false>
+template <typename T, int D, bool SINKS, bool BRIEF = false>
 __global__ void __launch_bounds__(kThreads, 1)
     batch_decode_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = tid; i < 2 * kRows * S::q_stride; i += kThreads) sm.q[0][i] = 0;
   grid_dependency_wait();  // lengths, tables and pages may be the previous kernel's output
   if (tid == 32) sm.tag = plan::begin_call(a);
-  plan::make_plan<kRows, S::keys, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
+  plan::make_plan<kRows, S::keys, kThreads, SINKS>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(sm.ring[0][0]), sm.warp_sums,
                                           &sm.start);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the plan's scratch is where the tiles land
   __syncthreads();
@@ -148,13 +148,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load_tiles = [&](int n, int seq, int g, int se, int lo, int hi, int tile0, int ns, int skip, int J) {
       // First key of part q.
       auto key_of = [&](int q) {
-        return plan::tile_at(tile0 + (q >> parts_log2), ns, skip) * kKeys + (q & (parts - 1)) * box_rows;
+        if (!SINKS) return tile0 * kKeys + q * box_rows;
+        return plan::tile_at<SINKS>(tile0 + (q >> parts_log2), ns, skip) * kKeys + (q & (parts - 1)) * box_rows;
       };
       const uint32_t* table = a.block_table + (long long)seq * a.max_blocks;
       // Pool rows of the page parts, 32 at a time (one a lane), read at least 32 parts ahead.
       auto rows_of = [&](int q0) {
         const int q = q0 + lane, key = key_of(q);
-        const bool seen = q < n * parts && !plan::keys_hidden(key, box_rows, se, lo, hi);
+        const bool seen = q < n * parts && !plan::keys_hidden<SINKS>(key, box_rows, se, lo, hi);
         const int col = seen ? plan::page_of(a, key) : 0;
         const uint32_t pg = table[col];  // (no branch around it: two such reads overlap)
         return !seen ? outside : pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* dst = sm.ring[st][is_v ? 1 : 0] + chunk * kChunkBytes;
         // V rows of a fetched part that lie outside the windows are replaced by zeros (0 * NaN), by eights or single
         // rows.
-        const bool edge = is_v && row != outside && !plan::keys_inside(key, box_rows, se, lo, hi);
+        const bool edge = is_v && row != outside && !plan::keys_inside<SINKS>(key, box_rows, se, lo, hi);
         if (my_part && !edge) tma_load_3d(dst + lane * box_rows * 128, tm, 64 * chunk, g, row, &sm.full[st]);
         unsigned edges = __ballot_sync(0xffffffffu, edge);
         while (edges) {
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           edges &= edges - 1;
           const int row_e = __shfl_sync(0xffffffffu, row, e), key_e = __shfl_sync(0xffffffffu, key, e);
           const int key_8 = key_e + 8 * lane;  // eight rows a lane; those that are not all of one kind, row by row
-          const bool inside = plan::keys_inside(key_8, 8, se, lo, hi), outer = plan::keys_hidden(key_8, 8, se, lo, hi);
+          const bool inside = plan::keys_inside<SINKS>(key_8, 8, se, lo, hi), outer = plan::keys_hidden<SINKS>(key_8, 8, se, lo, hi);
           if (8 * lane < box_rows && (inside || outer)) {
             const int y = inside ? row_e + 8 * lane : outside;
             tma_load_3d(dst + (e * box_rows + 8 * lane) * 128, &tm_v8, 64 * chunk, g, y, &sm.full[st]);
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 8 * (__ffs(mixed) - 1) + lane;
             mixed &= mixed - 1;
             if (lane < 8) {
-              const int y = plan::keys_inside(key_e + r, 1, se, lo, hi) ? row_e + r : outside;
+              const int y = plan::keys_inside<SINKS>(key_e + r, 1, se, lo, hi) ? row_e + r : outside;
               tma_load_3d(dst + (e * box_rows + r) * 128, &tm_v1, 64 * chunk, g, y, &sm.full[st]);
             }
           }
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
       }
     }
-    plan::Walker<kRows, kKeys> walk(a, sm.start);
+    plan::Walker<kRows, kKeys, SINKS> walk(a, sm.start);
     plan::Piece p;
     while (pw == 0) {
       const bool more = walk.next(p) && warp_whole(&sm.abort);
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) {
           d.whole = p.whole;
           d.n = p.t1 - p.t0;
-          d.tile0 = p.t0;
+          d.tile0 = plan::first_tile<SINKS>(p.k) + p.t0;
           d.ns = p.k.ns;
           d.skip = p.k.skip;
           d.se = p.k.se;
@@ -276,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  static_cast<const T*>(a.q) + (long long)(p.q.row0 + t) * a.q_stride + (long long)h * a.D, a.D * 2,
                  &sm.q_ready[x & 1]);
       }
-      J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.se, p.k.lo_min, p.k.hi_max, p.t0, p.k.ns, p.k.skip, J);
+      J = load_tiles(p.t1 - p.t0, p.s, p.g, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t0,
+                     p.k.ns, p.k.skip, J);
       ++x;
       if (!warp_whole(&sm.abort)) break;
     }
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[y][e] += s1[y][e];
       }
-      const int tile_key = plan::tile_at(d.tile0 + i, d.ns, d.skip) * kKeys, key0 = tile_key + kw + lc;
+      const int tile_key = plan::tile_at<SINKS>(d.tile0 + i, d.ns, d.skip) * kKeys, key0 = tile_key + kw + lc;
       if (a.softcap > 0.f) {
 #pragma unroll
         for (int y = 0; y < kTiles; ++y)
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + 8 * y + (e & 1);
-            if (key >= hi[e >> 1] || (key < lo[e >> 1] && key >= a.sinks)) s[y][e] = -INFINITY;
+            if (key >= hi[e >> 1] || (key < lo[e >> 1] && (!SINKS || key >= a.sinks))) s[y][e] = -INFINITY;
           }
       }
       float t[2] = {-INFINITY, -INFINITY};
@@ -594,9 +596,10 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
       !make_tmap(&tm_v8, a.v_pages, 3, dims, strides, eight, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v1, a.v_pages, 3, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
-  const void* kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D>);
+  const void* kern = a.sinks > 0 ? reinterpret_cast<const void*>(batch_decode_kernel<T, D, true>)
+                                 : reinterpret_cast<const void*>(batch_decode_kernel<T, D, false>);
   if constexpr (std::is_same<T, __nv_bfloat16>::value)  // the failure-path test
-    if (a.wait_ns != 0) kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, true>);
+    if (a.wait_ns != 0 && a.sinks == 0) kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, false, true>);
   const size_t smem = sizeof(DecodeSmem<D>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;

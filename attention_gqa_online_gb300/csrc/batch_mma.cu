@@ -58,9 +58,9 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
   __shared__ plan::Start start;
   __shared__ long long warp_sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  plan::make_plan<kRows, kKeys, kThreads>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
+  plan::make_plan<kRows, kKeys, kThreads, true>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
   BatchSplit split{};
-  plan::Walker<kRows, kKeys> walk(a, start);
+  plan::Walker<kRows, kKeys, true> walk(a, start);
   plan::Piece p;
   const uint32_t q_base = smem_u32(sh.q);
   constexpr int kUnits = DP / 8;
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
     }
     const uint32_t* table = a.block_table + (long long)p.s * a.max_blocks;
     auto load_tile = [&](int i, int st) {
-      const int key0 = plan::tile_at(i, p.k.ns, p.k.skip) * kKeys;
+      const int key0 = plan::tile_at<true>(i, p.k.ns, p.k.skip) * kKeys;
       for (int c = tid; c < kKeys * kUnits; c += kThreads) {
         const int r = c / kUnits, u = c % kUnits;
         const int key = key0 + r;
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
           mma16816<T>(s[2 * j + 1], qa, kb[2], kb[3]);
         }
       }
-      const int key0 = plan::tile_at(p.t0 + i, p.k.ns, p.k.skip) * kKeys;
+      const int key0 = plan::tile_at<true>(p.t0 + i, p.k.ns, p.k.skip) * kKeys;
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int j = 0; j < kKeys / 8; ++j)
@@ -337,12 +337,16 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
     // sequences of 4096, 4 heads a kv head of 128, with 32, 64, 128, 256, 512, 1024 rows a kv head: pairs 64, 74, 77,
     // 76, 120, 210 us, single blocks 57, 71, 74, 99, 164, 312.
     if (a.D > 64 && 128 % a.gs == 0 && sm_count % 2 == 0 && (long long)a.total_rows * a.gs >= 256ll * a.n_seqs)
-      return a.D == 128 ? launch_batch_tc_pair(a, dtype, sm_count, box, s)
-                        : launch_batch_tc_part_pair(a, dtype, sm_count, box, s);
+      return a.sinks > 0  ? launch_batch_tc_sinks_pair(a, dtype, sm_count, box, s)
+             : a.D == 128 ? launch_batch_tc_pair(a, dtype, sm_count, box, s)
+                          : launch_batch_tc_part_pair(a, dtype, sm_count, box, s);
     if (a.D > 64)
-      return a.D == 128 ? launch_batch_tc_d128(a, dtype, sm_count, box, s)
-                        : launch_batch_tc_part128(a, dtype, sm_count, box, s);
-    return a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s) : launch_batch_tc_part64(a, dtype, sm_count, box, s);
+      return a.sinks > 0  ? launch_batch_tc_sinks128(a, dtype, sm_count, box, s)
+             : a.D == 128 ? launch_batch_tc_d128(a, dtype, sm_count, box, s)
+                          : launch_batch_tc_part128(a, dtype, sm_count, box, s);
+    return a.sinks > 0 ? launch_batch_tc_sinks64(a, dtype, sm_count, box, s)
+           : a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s)
+                       : launch_batch_tc_part64(a, dtype, sm_count, box, s);
   }
   const int rc = launch_batch_mma(a, dtype, 2 * sm_count, s);
   return rc != ATTN_OK ? rc : launch_batch_combine(a, dtype, 2 * sm_count, s);

@@ -54,20 +54,26 @@ __device__ __forceinline__ int row_lo(const BatchArgs& a, const SeqInfo& q, int 
   return (a.window > 0 && n > a.window) ? n - a.window : 0;
 }
 
-// Keys of a block's rows: [0, se) and [lo_min, hi_max), se < lo_min or se == 0.
+// Keys of a block's rows: [0, se) and [lo_min, hi_max), se < lo_min or se == 0.  (SINKS false, here and below: a call
+// without first positions, se == 0 everywhere; that in the lookups cost a mixed batch of short pieces 3% of its time.)
 struct BlockKeys {
   int lo_min, lo_max, hi_min, hi_max;  // extremes over the rows' windows (lo_min 0 where the first positions reach them)
   int se;                              // end of the first positions in sight of a row
   int ns, skip, nt;                    // tiles: nt in all, the first ns from tile 0 on, the others `skip` later
 };
-// Key tile of tile t of the nt.
-__device__ __forceinline__ int tile_at(int t, int ns, int skip) { return t < ns ? t : t + skip; }
+// Key tile of tile t, which the item's tiles are counted from: of the nt (SINKS), or key tiles as they are.
+template <bool SINKS>
+__device__ __forceinline__ int first_tile(const BlockKeys& k) { return SINKS ? 0 : k.skip; }
+template <bool SINKS>
+__device__ __forceinline__ int tile_at(int t, int ns, int skip) { return SINKS && t >= ns ? t + skip : t; }
 // Can no row see, or can some row see all of, keys [key, key + n)?  (Of one of the two ranges.)
+template <bool SINKS>
 __device__ __forceinline__ bool keys_hidden(int key, int n, int se, int lo, int hi) {
-  return (key + n <= lo || key >= hi) && key >= se;
+  return (key + n <= lo || key >= hi) && (!SINKS || key >= se);
 }
+template <bool SINKS>
 __device__ __forceinline__ bool keys_inside(int key, int n, int se, int lo, int hi) {
-  return (key >= lo && key + n <= hi) || key + n <= se;
+  return (key >= lo && key + n <= hi) || (SINKS && key + n <= se);
 }
 
 template <int ROWS>
@@ -75,7 +81,7 @@ __device__ __forceinline__ int row_blocks(const BatchArgs& a, const SeqInfo& q) 
   return (q.q_len * a.gs + ROWS - 1) / ROWS;
 }
 
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, bool SINKS>
 __device__ __forceinline__ BlockKeys block_keys(const BatchArgs& a, const SeqInfo& q, int b) {
   const int t0 = token_of(a, b * ROWS);
   const int t1 = token_of(a, min(q.q_len * a.gs, (b + 1) * ROWS) - 1);
@@ -85,10 +91,13 @@ __device__ __forceinline__ BlockKeys block_keys(const BatchArgs& a, const SeqInf
   k.hi_min = row_hi(q, t0);
   k.hi_max = row_hi(q, t1);
   const bool any = k.hi_max > k.lo_min;
-  k.se = min(a.sinks, k.lo_max);
-  if (k.se >= k.lo_min) k.lo_min = k.se = 0;
+  k.se = k.ns = 0;
+  if (SINKS) {
+    k.se = min(a.sinks, k.lo_max);
+    if (k.se >= k.lo_min) k.lo_min = k.se = 0;
+  }
   const int kt0 = k.lo_min / KEYS;
-  k.ns = min((k.se + KEYS - 1) / KEYS, kt0);
+  if (SINKS) k.ns = min((k.se + KEYS - 1) / KEYS, kt0);
   k.skip = kt0 - k.ns;
   k.nt = any ? (k.hi_max + KEYS - 1) / KEYS - k.skip : 0;
   return k;
@@ -165,7 +174,7 @@ __device__ __forceinline__ void set_start(Start* start, int s, int b, long long 
 // single-token step starts about a microsecond sooner.  Returns false (to every
 // lane) when the batch is too large for it.
 constexpr int kWarpSeqs = 512, kWarpBlocks = 32;
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, bool SINKS>
 __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks, Start* start) {
   const int lane = threadIdx.x & 31;
   if (a.n_seqs > kWarpSeqs) return false;
@@ -178,7 +187,7 @@ __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks,
     const int n = row_blocks<ROWS>(a, q);
     nb += n;
     if (nb <= kWarpBlocks)
-      for (int b = 0; b < n; ++b) mine += block_keys<ROWS, KEYS>(a, q, b).nt + a.item_cost;
+      for (int b = 0; b < n; ++b) mine += block_keys<ROWS, KEYS, SINKS>(a, q, b).nt + a.item_cost;
   }
   if (__any_sync(0xffffffffu, nb > kWarpBlocks)) return false;
   mine *= a.G;
@@ -198,7 +207,7 @@ __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks,
       const SeqInfo q = load_seq(a, s);
       const int n = row_blocks<ROWS>(a, q);
       for (int b = 0; b < n && !found; ++b) {
-        const int w = block_keys<ROWS, KEYS>(a, q, b).nt + a.item_cost;
+        const int w = block_keys<ROWS, KEYS, SINKS>(a, q, b).nt + a.item_cost;
         found = u0 < at + (long long)w * a.G;
         if (found) set_start(start, s, b, u0 - at, w, u0, per, units);
         at += (long long)w * a.G;
@@ -211,11 +220,11 @@ __device__ __forceinline__ bool warp_plan(const BatchArgs& a, int c, int blocks,
 // The range of thread block `c` of `blocks`.  Every thread of the block calls it;
 // first_block holds n_seqs + 1 ints and warp_sums THREADS/32 values in shared
 // memory.  On return (after its final barrier) *start is valid.
-template <int ROWS, int KEYS, int THREADS>
+template <int ROWS, int KEYS, int THREADS, bool SINKS>
 __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_block, long long* warp_sums, Start* start) {
   const int tid = threadIdx.x;
   if (tid < 32) {
-    const bool done = warp_plan<ROWS, KEYS>(a, c, blocks, start);
+    const bool done = warp_plan<ROWS, KEYS, SINKS>(a, c, blocks, start);
     if (tid == 0) first_block[0] = done ? 1 : 0;
   }
   __syncthreads();
@@ -265,7 +274,7 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
     for (int i = i0; i < i1; ++i) {
       while (first_block[ss + 1] <= i) ++ss;
       if (have != ss) q = load_seq(a, have = ss);
-      mine += (long long)(block_keys<ROWS, KEYS>(a, q, i - first_block[ss]).nt + a.item_cost) * a.G;
+      mine += (long long)(block_keys<ROWS, KEYS, SINKS>(a, q, i - first_block[ss]).nt + a.item_cost) * a.G;
     }
   }
   long long units;
@@ -276,7 +285,7 @@ __device__ void make_plan(const BatchArgs& a, int c, int blocks, int* first_bloc
     int ss = s;
     for (int i = i0; i < i1; ++i) {
       while (first_block[ss + 1] <= i) ++ss;
-      const int w = block_keys<ROWS, KEYS>(a, load_seq(a, ss), i - first_block[ss]).nt + a.item_cost;
+      const int w = block_keys<ROWS, KEYS, SINKS>(a, load_seq(a, ss), i - first_block[ss]).nt + a.item_cost;
       if (u0 < at + (long long)w * a.G) {
         set_start(start, ss, i - first_block[ss], u0 - at, w, u0, per, units);
         break;
@@ -308,7 +317,7 @@ __device__ __forceinline__ unsigned piece_arrives(unsigned long long* c, unsigne
 
 // Walks the pieces of a block's range, in order.  Warps of different roles
 // walk it independently and see the same pieces.
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, bool SINKS>
 struct Walker {
   const BatchArgs& a;
   SeqInfo q;
@@ -327,7 +336,7 @@ struct Walker {
   // an item that starts here and ends in a later block.
   __device__ __forceinline__ bool next(Piece& p, BatchSplit* split = nullptr) {
     while (left > 0) {
-      const BlockKeys k = block_keys<ROWS, KEYS>(a, q, b);
+      const BlockKeys k = block_keys<ROWS, KEYS, SINKS>(a, q, b);
       const long long w = k.nt + a.item_cost;
       const long long take = min(left, w - x);
       p.q = q;

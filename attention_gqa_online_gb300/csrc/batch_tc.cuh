@@ -5,7 +5,8 @@
 // not stored. 4 sequences of 512 new tokens at 8192, 32 heads over 8: 222 us at
 // 96 columns and 190 at 40 (batch_mma.cu: 1425 and 917). Heads of 128 and 64
 // keep a form with widths known at compile time: 220 and 188 us, against 227
-// and 192 in this one.
+// and 192 in this one.  Calls with first positions (SINKS) take the smaller
+// heads' form at every width.
 //
 // The operation and the division of work are those of batch_mma.cu and
 // batch_plan.cuh; here a row block is 128 flattened rows (the M of one MMA)
@@ -316,7 +317,7 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uin
 // MODE 0: scores are scale2 * S with scale2 > 0 (folded into the exponent's
 // fma); 1: scaled, with an optional distance bias; 2: capped, with an optional
 // distance bias.
-template <typename T, int D, int MODE, bool PAIR, bool FULL, bool BRIEF = false>
+template <typename T, int D, int MODE, bool PAIR, bool FULL, bool SINKS, bool BRIEF = false>
 __global__ void __launch_bounds__(kTcThreads, 1)
     batch_tc_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Lengths, tables and pages may be the previous kernel's output.
   grid_dependency_wait();
   if (tid == 32) sm.tag = plan::begin_call(a);
-  plan::make_plan<L::rows, kTcKeys, kTcThreads>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
+  plan::make_plan<L::rows, kTcKeys, kTcThreads, SINKS>(a, unit, units, reinterpret_cast<int*>(sm.q[0]), sm.warp_sums, &sm.start);
   // The plan's scratch is where Q and the K/V tiles land.
   fence_async_smem();
   tc::fence_before_sync();
@@ -408,17 +409,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t* table;
       int now, next;         // pool rows of 32 parts, and of the 32 after
     };
-    auto first_key_of = [&](const Parts& w, int i) { return plan::tile_at(w.last - i, w.ns, w.skip) * kTcKeys + w.off; };
+    auto first_key_of = [&](const Parts& w, int i) {
+      return plan::tile_at<SINKS>(w.last - i, w.ns, w.skip) * kTcKeys + w.off;
+    };
     auto rows_of = [&](const Parts& w, int q0) {
       const int q = q0 + lane, i = q >> w.shift, key = first_key_of(w, i) + (q - (i << w.shift)) * box_rows;
-      const bool seen = i < w.n && !plan::keys_hidden(key, box_rows, w.se, w.lo, w.hi);
+      const bool seen = i < w.n && !plan::keys_hidden<SINKS>(key, box_rows, w.se, w.lo, w.hi);
       const int col = seen ? plan::page_of(a, key) : 0;
       const uint32_t pg = w.table[col];  // (no branch around it: two such reads overlap)
       return !seen ? outside : pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
     };
-    auto open_parts = [&](int keys, int off, const PieceDesc& d) {
-      Parts w{__ffs(keys) - __ffs(box_rows), d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip, off,
-              a.block_table + (long long)d.seq * a.max_blocks, 0, 0};
+    auto open_parts = [&](int keys, int n, int se, int lo, int hi, int last, int ns, int skip, int off, int seq) {
+      Parts w{__ffs(keys) - __ffs(box_rows), n, se, lo, hi, last, ns, skip, off,
+              a.block_table + (long long)seq * a.max_blocks, 0, 0};
       w.now = rows_of(w, 0);
       w.next = rows_of(w, 32);
       return w;
@@ -445,7 +448,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         prefetch_tmap(&tm_k);
         if (q_box) prefetch_tmap(&tm_q);
       }
-      plan::Walker<L::rows, kTcKeys> walk(a, sm.start);
+      plan::Walker<L::rows, kTcKeys, SINKS> walk(a, sm.start);
       plan::Piece p;
       int x = 0, J = 0;
       // A wait that ran out ends the role at once: writing over a descriptor or a slot in use, or arriving twice in one
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             d.hi_min = p.k.hi_min;
             d.hi_max = p.k.hi_max;
             d.se = p.k.se;
-            d.tile_last = p.t1 - 1;
+            d.tile_last = plan::first_tile<SINKS>(p.k) + p.t1 - 1;
             d.ns = p.k.ns;
             d.skip = p.k.skip;
             d.n = p.t1 - p.t0;
@@ -500,7 +503,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!more) break;
         // The piece's first page parts are looked up while its Q buffer falls free.
         const int n = p.t1 - p.t0, col = FULL ? p.g * D : 0;
-        Parts w = open_parts(L::k_rows, PAIR ? rank * L::k_rows : 0, sm.desc[x % kDescs]);
+        Parts w = open_parts(L::k_rows, n, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t1 - 1, p.k.ns,
+                             p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
         // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
         // only feeds itself, and those rows are not stored).
         if (x >= 2) ok = wait(&sm.q_free[x & 1], (x >> 1) - 1);
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!next_piece(x)) break;
         const PieceDesc& d = sm.desc[x % kDescs];
         const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
-        Parts w = open_parts(kTcKeys, 0, d);
+        Parts w = open_parts(kTcKeys, n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip, 0, d.seq);
         for (int i = 0; i < n; ++i, ++J) {
           const int row = part_row(w, i), key = first_key_of(w, i) + lane * box_rows, slot = J % L::slots;
           if (J >= L::slots) ok = wait(&sm.v_empty[slot], J / L::slots - 1);
@@ -573,7 +577,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint32_t bar = barrier_of(&sm.v_full[slot]);
           // A part that reaches outside the block's windows goes by eights or single rows: what the page holds there (0 * NaN would
           // reach every row) is replaced by zeros from outside the pool.
-          const bool edge = row != outside && !plan::keys_inside(key, box_rows, w.se, w.lo, w.hi);
+          const bool edge = row != outside && !plan::keys_inside<SINKS>(key, box_rows, w.se, w.lo, w.hi);
           if ((lane >> w.shift) == 0 && !edge) {
 #pragma unroll
             for (int c = 0; c < L::v_chunks; ++c)
@@ -586,8 +590,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             edges &= edges - 1;
             const int row_p = __shfl_sync(0xffffffffu, row, p), key_p = __shfl_sync(0xffffffffu, key, p);
             const int key_8 = key_p + 8 * lane;  // eight rows a lane; those that are not all of one kind, row by row
-            const bool inside = plan::keys_inside(key_8, 8, w.se, w.lo, w.hi);
-            const bool outer = plan::keys_hidden(key_8, 8, w.se, w.lo, w.hi);
+            const bool inside = plan::keys_inside<SINKS>(key_8, 8, w.se, w.lo, w.hi);
+            const bool outer = plan::keys_hidden<SINKS>(key_8, 8, w.se, w.lo, w.hi);
             if (8 * lane < box_rows && (inside || outer)) {
               const int y = inside ? row_p + 8 * lane : outside;
 #pragma unroll
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int r = 8 * (__ffs(mixed) - 1) + lane;
               mixed &= mixed - 1;
               if (lane < 8) {
-                const int y = plan::keys_inside(key_p + r, 1, w.se, w.lo, w.hi) ? row_p + r : outside;
+                const int y = plan::keys_inside<SINKS>(key_p + r, 1, w.se, w.lo, w.hi) ? row_p + r : outside;
 #pragma unroll
                 for (int c = 0; c < L::v_chunks; ++c)
                   load_rows<PAIR, FULL>(sm.v[slot] + c * L::v_chunk + (p * box_rows + r) * 128, &tm_v1, col + 64 * c, g, y,
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sm.row[128 * grp + r] = info;  // read on the tiles that need it: kept in registers it would spill scores
       for (int i = (J & 1) ^ grp; i < n; i += 2) {
         const int j = J + i, b = j & 1;
-        const int key0 = plan::tile_at(d.tile_last - i, d.ns, d.skip) * kTcKeys;
+        const int key0 = plan::tile_at<SINKS>(d.tile_last - i, d.ns, d.skip) * kTcKeys;
         // Does the tile cross some row's window end, or start?
         const bool cut_hi = key0 + kTcKeys > d.hi_min, cut_lo = key0 < d.lo_max;
         wait(&sm.s_full[b], j >> 1);
@@ -827,14 +831,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (32 * c + e >= lim) s[c][e] = __float_as_uint(-INFINITY);
           }
           if (cut_lo) {
-            // Keys [sinks, lo) of the sequence: columns [from, from + count) of the tile.
-            const int from = a.sinks - key0;
-            const unsigned count = (unsigned)max(0, sm.row[128 * grp + r].x - a.sinks);
+            // Keys [sinks, lo) of the sequence: columns [from, lim) of the tile.
+            const int lim = sm.row[128 * grp + r].x - key0, from = SINKS ? a.sinks - key0 : 0;
+            const unsigned count = (unsigned)max(0, lim - from);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if ((unsigned)(32 * c + e - from) < count) s[c][e] = __float_as_uint(-INFINITY);
+                if (SINKS ? (unsigned)(32 * c + e - from) < count : 32 * c + e < lim) s[c][e] = __float_as_uint(-INFINITY);
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1174,7 +1178,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <typename T, int D, bool PAIR, bool FULL>
+template <typename T, int D, bool PAIR, bool FULL, bool SINKS>
 int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   // K and V: whole rows, or [rows][G][head_dim], where columns past the head arrive as zeros.
   const int rank = FULL ? 2 : 3;
@@ -1203,14 +1207,14 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   ScoreMap sc = score_map(a);
   const void* kern;
   if (a.softcap > 0.f)
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR, FULL>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR, FULL, SINKS>);
   else if (a.slopes != nullptr || !(sc.scale2 >= FLT_MIN))
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL, SINKS>);
   else
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL>);
-  if constexpr (std::is_same<T, __nv_bfloat16>::value)  // the failure-path test
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS>);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && !SINKS)  // the failure-path test
     if (a.wait_ns != 0 && a.softcap == 0.f && a.slopes == nullptr && sc.scale2 >= FLT_MIN)
-      kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, true>);
+      kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS, true>);
   const size_t smem = sizeof(TcSmem<D, PAIR>) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;

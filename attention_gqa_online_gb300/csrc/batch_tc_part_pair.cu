@@ -5,8 +5,8 @@
 namespace attn {
 
 int launch_batch_tc_part_pair(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s) {
-  return dtype == ATTN_DT_BF16 ? launch_tc_t<__nv_bfloat16, 128, true, false>(a, blocks, box_rows, s)
-                               : launch_tc_t<__half, 128, true, false>(a, blocks, box_rows, s);
+  return dtype == ATTN_DT_BF16 ? launch_tc_t<__nv_bfloat16, 128, true, false, false>(a, blocks, box_rows, s)
+                               : launch_tc_t<__half, 128, true, false, false>(a, blocks, box_rows, s);
 }
 
 }  // namespace attn
