@@ -15,9 +15,9 @@ from ._binding import (ATTN_BF16, ATTN_CAUSAL, ATTN_CROSS, ATTN_ERR_CUDA, ATTN_E
                        attn_scratch_peak_bytes, attn_release_scratch, ATTN_DT_BF16, ATTN_DT_F16, ATTN_DT_F32,
                        ATTN_ROPE_BY_PARTS, ATTN_ROPE_HALF, ATTN_ROPE_INTERLEAVED, ATTN_ROPE_LINEAR, ATTN_ROPE_NONE,
                        ATTN_ROPE_NTK, attn_append_paged, attn_batch_paged, attn_batch_paged_workspace_bytes,
-                       attn_rope_apply, attn_rope_table_scaled, attn_append_paged8, attn_batch_paged_sinks,
+                       attn_rope_apply, attn_rope_table_scaled, attn_append_paged8, attn_batch_paged8, attn_batch_paged_sinks,
                        attn_qk_norm_rope, attn_qk_norm_rope_backward, attn_qk_norm_rope_backward_workspace_bytes,
                        attn_read_paged8)
-from .api import (append_paged, append_paged8, attend_paged, backward, decode, forward, prefill,  # noqa: F401
+from .api import (append_paged, append_paged8, attend_paged, attend_paged8, backward, decode, forward, prefill,  # noqa: F401
                   qk_norm_rope, qk_norm_rope_backward, read_paged8, rope, rope_backward, rope_table, DecodeState,
                   PagedBatch, PagedCache8)

@@ -102,6 +102,9 @@ def load_library(path=None):
         [_vp, _vp, ctypes.c_int, ctypes.c_float, _u32, ctypes.c_int, _vp, _u32, _vp]
     lib.attn_read_paged8.restype = ctypes.c_int
     lib.attn_read_paged8.argtypes = [_vp] * 6 + [ctypes.c_int] + [_vp] * 4 + [_u32] * 11 + [_vp]
+    lib.attn_batch_paged8.restype = ctypes.c_int
+    lib.attn_batch_paged8.argtypes = [_vp] * 6 + [ctypes.c_int, _vp, _vp, _vp] + [_u32] * 12 + \
+        [ctypes.c_float, _u32, _u32, ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.attn_get_status.restype = ctypes.c_int
     lib.attn_get_status.argtypes = [_vp]
     lib.attn_set_workspace.restype = ctypes.c_int
@@ -499,6 +502,24 @@ def attn_read_paged8(k_pages, v_pages, k_scales, v_scales, k_out, v_out, block_t
         _u32_addr(block_table, "block_table"), _u32_addr(starts, "starts"), _u32_addr(first, "first"),
         _u32_addr(kv_len, "kv_len"), total_rows, n_seqs, num_kv_heads, head_dim, kv_dim, k_stride, v_stride, page_rows,
         num_pages, max_blocks, scale_rows, _stream(stream)), "attn_read_paged8")
+
+
+def attn_batch_paged8(q, k_pages, v_pages, k_scales, v_scales, out, block_table, q_start, kv_len, total_rows, n_seqs,
+                      n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks,
+                      scale_rows, scale, window, sinks, softcap, alibi_slopes, prefix_len, workspace,
+                      workspace_bytes=None, stream=None):
+    """Attention of a ragged batch's new tokens over an 8-bit paged cache; see attn_gqa.h."""
+    code = _dtype_code(q, "q")
+    _same_dtype(code, out=out)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(load_library().attn_batch_paged8(
+        _addr(q, "q"), _addr(k_pages, "k_pages"), _addr(v_pages, "v_pages"), _addr(k_scales, "k_scales"),
+        _addr(v_scales, "v_scales"), _addr(out, "out"), code, _u32_addr(block_table, "block_table"),
+        _u32_addr(q_start, "q_start"), _u32_addr(kv_len, "kv_len"), total_rows, n_seqs, n_heads, n_kv_heads, head_dim,
+        kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks, scale_rows, float(scale), window, sinks,
+        float(softcap), _addr(alibi_slopes, "alibi_slopes", _f32()), _u32_addr(prefix_len, "prefix_len"),
+        _addr(workspace, "workspace"), workspace_bytes, _stream(stream)), "attn_batch_paged8")
 
 
 def attn_decode_cached_noalloc(q, k_cache, v_cache, kv_pos_dev, out, num_heads, num_kv_heads, head_dim, max_seq,

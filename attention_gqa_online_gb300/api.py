@@ -611,21 +611,16 @@ def read_paged8(batch, cache, starts, k_out, v_out, first=None, stream=None):
     return k_out, v_out
 
 
-def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, softcap=0.0, alibi_slopes=None,
-                 prefix_len=None, stream=None, sinks=0):
-    """Attention of the batch's new tokens, q [rows, H*D] (bf16 or fp16), over its pages: the last `window`
-    keys of each row (0 = all) and its sequence's first `sinks`, scores capped by softcap * tanh(s / softcap) (0 = uncapped) and biased by
-    -alibi_slopes[h] * distance, keys below prefix_len[s] visible to every row.  Rows of no sequence are
-    left as they are in `out`."""
-    kv_dim, num_pages = batch.pool(k_pages, v_pages)
+def _attend_args(batch, q, out, cache_type, scale, window, sinks, alibi_slopes, prefix_len, stream):
+    """What attend_paged and attend_paged8 check alike: (type code, rows, q stride, out, out stride, scale, slopes)."""
     H, D = batch.num_heads, batch.head_dim
     rows, columns, qs = _rows2d(q, "q")
     if columns != H * D:
         raise ValueError("q must be [rows, %d]" % (H * D))
     dtype = q.dtype
     code = _code(q, "q")
-    _like(dtype, "k_pages", k_pages)
-    _like(dtype, "v_pages", v_pages)
+    if cache_type is not None and cache_type != dtype:
+        raise ValueError("k_pages has type %s, unlike the tensors it goes with (%s)" % (cache_type, dtype))
     if out is None:
         out = _new(torch.zeros, (rows, H * D), dtype, q.device, stream)
         os = H * D
@@ -646,16 +641,53 @@ def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, sof
         _count32("sinks", sinks)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    index = k_pages.get_device()
-    workspace = batch.workspace
-    _same_device(index, v_pages, q, out, alibi_slopes, prefix_len, workspace)
+    return code, rows, qs, out, os, scale, slopes
+
+
+def _attend_stream(batch, index, stream):
     batch.same_device(index)
     stream = _handle(stream, index)
     if stream not in batch._streams:
         batch._use_on(stream)
-    _run("attn_batch_paged_sinks" if sinks else "attn_batch_paged", B.load_library().attn_batch_paged_sinks, index, stream,
+    return stream
+
+
+def attend_paged(batch, q, k_pages, v_pages, out=None, scale=None, window=0, softcap=0.0, alibi_slopes=None,
+                 prefix_len=None, stream=None, sinks=0):
+    """Attention of the batch's new tokens, q [rows, H*D] (bf16 or fp16), over its pages: the last `window`
+    keys of each row (0 = all) and its sequence's first `sinks`, scores capped by softcap * tanh(s / softcap) (0 =
+    uncapped) and biased by -alibi_slopes[h] * distance, keys below prefix_len[s] visible to every row.  Rows of no
+    sequence are left as they are in `out`."""
+    kv_dim, num_pages = batch.pool(k_pages, v_pages)
+    code, rows, qs, out, os, scale, slopes = _attend_args(batch, q, out, k_pages.dtype, scale, window, sinks,
+                                                          alibi_slopes, prefix_len, stream)
+    _like(q.dtype, "v_pages", v_pages)
+    index = k_pages.get_device()
+    workspace = batch.workspace
+    _same_device(index, v_pages, q, out, alibi_slopes, prefix_len, workspace)
+    _run("attn_batch_paged_sinks" if sinks else "attn_batch_paged", B.load_library().attn_batch_paged_sinks, index,
+         _attend_stream(batch, index, stream),
          (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), code,
-          batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H,
-          batch.num_kv_heads, D, kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks, scale, window,
-          softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel(), sinks))
+          batch.block_table.data_ptr(), batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs,
+          batch.num_heads, batch.num_kv_heads, batch.head_dim, kv_dim, qs, os, batch.page_rows, num_pages,
+          batch.max_blocks, scale, window, softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(),
+          workspace.numel(), sinks))
+    return out
+
+
+def attend_paged8(batch, q, cache, out=None, scale=None, window=0, sinks=0, softcap=0.0, alibi_slopes=None,
+                  prefix_len=None, stream=None):
+    """attend_paged over a PagedCache8; q and out are bf16 or fp16."""
+    num_pages = cache.pages(batch)
+    code, rows, qs, out, os, scale, slopes = _attend_args(batch, q, out, None, scale, window, sinks, alibi_slopes,
+                                                          prefix_len, stream)
+    index = cache.index
+    workspace = batch.workspace
+    _same_device(index, q, out, alibi_slopes, prefix_len, workspace)
+    _run("attn_batch_paged8", B.load_library().attn_batch_paged8, index, _attend_stream(batch, index, stream),
+         (q.data_ptr(), cache.k_pages.data_ptr(), cache.v_pages.data_ptr(), cache.k_scales.data_ptr(),
+          cache.v_scales.data_ptr(), out.data_ptr(), code, batch.block_table.data_ptr(), batch.q_start.data_ptr(),
+          batch.kv_len.data_ptr(), rows, batch.n_seqs, batch.num_heads, batch.num_kv_heads, batch.head_dim,
+          cache.kv_dim, qs, os, batch.page_rows, num_pages, batch.max_blocks, cache.scale_rows, scale, window, sinks,
+          softcap, slopes, _int32(prefix_len, "prefix_len"), workspace.data_ptr(), workspace.numel()))
     return out

@@ -168,6 +168,8 @@ struct BatchArgs {
   const uint32_t* kv_len;       // [n_seqs]
   const float* slopes;          // [H] or nullptr
   const uint32_t* prefix_len;   // [n_seqs] or nullptr
+  const uint8_t* k_scales;      // 8-bit pools (cache8.cuh): [pool rows / scale_rows][G]; nullptr: pools of dtype
+  const uint8_t* v_scales;
   unsigned* status;
   float* partial;     // [2 * blocks][rows * (D + 2)]: unnormalised output, then (max, sum) of each row
   BatchSplit* split;  // [blocks]
@@ -181,8 +183,9 @@ struct BatchArgs {
   int page_rows, num_pages, max_blocks, capacity;
   int window;  // 0 = none
   int sinks;   // first positions that stay visible behind the window (0 without a window)
+  int scale_rows;
   float scale, softcap;
-  FastDiv by_gs, by_page;  // by gs and page_rows; set by launch_batch_paged
+  FastDiv by_gs, by_page, by_scale;  // by gs, page_rows and scale_rows; set by launch_batch_paged
   unsigned wait_ns;        // limit of each wait inside the kernels, 0 = the usual one; set by launch_batch_paged
   int item_cost;           // what an item takes beyond its tiles, in tiles; set by each kernel's launch
 };

@@ -24,6 +24,74 @@ bool paged_ok(uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks) {
 }
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// The batched attention over pools of dtype (k_scales nullptr) or of 8-bit codes.
+int batch_paged(const void* q, const void* k_pages, const void* v_pages, const uint8_t* k_scales, const uint8_t* v_scales, void* out,
+                int dtype, const uint32_t* block_table, const uint32_t* q_start, const uint32_t* kv_len,
+                uint32_t total_rows, uint32_t n_seqs, uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim,
+                uint32_t kv_dim, uint32_t q_stride, uint32_t out_stride, uint32_t page_rows, uint32_t num_pages,
+                uint32_t max_blocks, uint32_t scale_rows, float scale, uint32_t window, uint32_t sinks, float softcap,
+                const float* alibi_slopes, const uint32_t* prefix_len, void* workspace, size_t workspace_bytes,
+                attn_stream_t stream) {
+  if (!heads_ok(n_heads, n_kv_heads, head_dim) || !dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
+  if (!paged_ok(page_rows, num_pages, max_blocks)) return ATTN_ERR_INVALID_ARG;
+  if (kv_dim < (uint64_t)n_kv_heads * head_dim || q_stride < (uint64_t)n_heads * head_dim ||
+      out_stride < (uint64_t)n_heads * head_dim)
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale * 1.5f) || !(softcap >= 0.f) || !std::isfinite(softcap * 1.5f)) return ATTN_ERR_INVALID_ARG;
+  if (softcap > 0.f && !std::isfinite(scale / softcap)) return ATTN_ERR_INVALID_ARG;
+  if (total_rows == 0 || n_seqs == 0) return ATTN_OK;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || out == nullptr || block_table == nullptr ||
+      q_start == nullptr || kv_len == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(alibi_slopes, 4) ||
+      !aligned(prefix_len, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (k_scales != nullptr && (head_dim % 16 != 0 || kv_dim % 16 != 0)) return ATTN_ERR_UNSUPPORTED;
+  if (dtype == ATTN_DT_F32 || head_dim % 8 != 0 || kv_dim % 8 != 0 || q_stride % 8 != 0 || out_stride % 8 != 0 ||
+      !aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16))
+    return ATTN_ERR_UNSUPPORTED;
+  if ((uint64_t)total_rows * n_heads > (1u << 30) || n_seqs > (uint32_t)kMaxBatchSeqs ||
+      (uint64_t)page_rows * max_blocks > kMaxBatchCapacity || (uint64_t)page_rows * num_pages > kMaxBatchPool)
+    return ATTN_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  if (workspace == nullptr || workspace_bytes < batch_workspace_bytes((int)head_dim, sms) || !aligned(workspace, 16))
+    return ATTN_ERR_INVALID_ARG;
+  BatchArgs a{};
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.out = out;
+  a.block_table = block_table;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.slopes = alibi_slopes;
+  a.prefix_len = prefix_len;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.scale_rows = scale_rows > 0 ? (int)scale_rows : 1;
+  a.status = device_status_word();
+  if (a.status == nullptr) return ATTN_ERR_CUDA;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.kv_dim = kv_dim;
+  a.total_rows = total_rows;
+  a.n_seqs = (int)n_seqs;
+  a.H = (int)n_heads;
+  a.G = (int)n_kv_heads;
+  a.D = (int)head_dim;
+  a.gs = a.H / a.G;
+  a.page_rows = (int)page_rows;
+  a.num_pages = (int)num_pages;
+  a.max_blocks = (int)max_blocks;
+  a.capacity = (int)(page_rows * max_blocks);
+  a.window = window > 0x7fffffffu ? 0x7fffffff : (int)window;
+  a.sinks = window == 0 ? 0 : sinks > 0x3fffffffu ? 0x3fffffff : (int)sinks;
+  a.scale = scale;
+  a.softcap = softcap;
+  return launch_batch_paged(a, dtype, workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" int attn_rope_table_scaled(float* table, uint32_t max_pos, uint32_t rot_dim, double base,
@@ -153,10 +221,9 @@ extern "C" int attn_batch_paged(const void* q, const void* k_pages, const void* 
                                 uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks, float scale,
                                 uint32_t window, float softcap, const float* alibi_slopes, const uint32_t* prefix_len,
                                 void* workspace, size_t workspace_bytes, attn_stream_t stream) {
-  return attn_batch_paged_sinks(q, k_pages, v_pages, out, dtype, block_table, q_start, kv_len, total_rows, n_seqs,
-                                n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages,
-                                max_blocks, scale, window, softcap, alibi_slopes, prefix_len, workspace,
-                                workspace_bytes, 0, stream);
+  return batch_paged(q, k_pages, v_pages, nullptr, nullptr, out, dtype, block_table, q_start, kv_len, total_rows, n_seqs,
+                     n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks, 0,
+                     scale, window, 0, softcap, alibi_slopes, prefix_len, workspace, workspace_bytes, stream);
 }
 
 extern "C" int attn_batch_paged_sinks(const void* q, const void* k_pages, const void* v_pages, void* out,
@@ -167,58 +234,23 @@ extern "C" int attn_batch_paged_sinks(const void* q, const void* k_pages, const 
                                       float scale, uint32_t window, float softcap, const float* alibi_slopes,
                                       const uint32_t* prefix_len, void* workspace, size_t workspace_bytes,
                                       uint32_t sinks, attn_stream_t stream) {
-  if (!heads_ok(n_heads, n_kv_heads, head_dim) || !dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
-  if (!paged_ok(page_rows, num_pages, max_blocks)) return ATTN_ERR_INVALID_ARG;
-  if (kv_dim < (uint64_t)n_kv_heads * head_dim || q_stride < (uint64_t)n_heads * head_dim ||
-      out_stride < (uint64_t)n_heads * head_dim)
-    return ATTN_ERR_INVALID_ARG;
-  if (!std::isfinite(scale * 1.5f) || !(softcap >= 0.f) || !std::isfinite(softcap * 1.5f)) return ATTN_ERR_INVALID_ARG;
-  if (softcap > 0.f && !std::isfinite(scale / softcap)) return ATTN_ERR_INVALID_ARG;
-  if (total_rows == 0 || n_seqs == 0) return ATTN_OK;
-  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || out == nullptr || block_table == nullptr ||
-      q_start == nullptr || kv_len == nullptr)
-    return ATTN_ERR_INVALID_ARG;
-  if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(alibi_slopes, 4) ||
-      !aligned(prefix_len, 4))
-    return ATTN_ERR_INVALID_ARG;
-  if (dtype == ATTN_DT_F32 || head_dim % 8 != 0 || kv_dim % 8 != 0 || q_stride % 8 != 0 || out_stride % 8 != 0 ||
-      !aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16))
-    return ATTN_ERR_UNSUPPORTED;
-  if ((uint64_t)total_rows * n_heads > (1u << 30) || n_seqs > (uint32_t)kMaxBatchSeqs ||
-      (uint64_t)page_rows * max_blocks > kMaxBatchCapacity || (uint64_t)page_rows * num_pages > kMaxBatchPool)
-    return ATTN_ERR_UNSUPPORTED;
-  const int sms = device_sm_count();
-  if (sms <= 0) return ATTN_ERR_CUDA;
-  if (workspace == nullptr || workspace_bytes < batch_workspace_bytes((int)head_dim, sms) || !aligned(workspace, 16))
-    return ATTN_ERR_INVALID_ARG;
-  BatchArgs a{};
-  a.q = q;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.out = out;
-  a.block_table = block_table;
-  a.q_start = q_start;
-  a.kv_len = kv_len;
-  a.slopes = alibi_slopes;
-  a.prefix_len = prefix_len;
-  a.status = device_status_word();
-  if (a.status == nullptr) return ATTN_ERR_CUDA;
-  a.q_stride = q_stride;
-  a.out_stride = out_stride;
-  a.kv_dim = kv_dim;
-  a.total_rows = total_rows;
-  a.n_seqs = (int)n_seqs;
-  a.H = (int)n_heads;
-  a.G = (int)n_kv_heads;
-  a.D = (int)head_dim;
-  a.gs = a.H / a.G;
-  a.page_rows = (int)page_rows;
-  a.num_pages = (int)num_pages;
-  a.max_blocks = (int)max_blocks;
-  a.capacity = (int)(page_rows * max_blocks);
-  a.window = window > 0x7fffffffu ? 0x7fffffff : (int)window;
-  a.sinks = window == 0 ? 0 : sinks > 0x3fffffffu ? 0x3fffffff : (int)sinks;
-  a.scale = scale;
-  a.softcap = softcap;
-  return launch_batch_paged(a, dtype, workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+  return batch_paged(q, k_pages, v_pages, nullptr, nullptr, out, dtype, block_table, q_start, kv_len, total_rows, n_seqs,
+                     n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages, max_blocks, 0,
+                     scale, window, sinks, softcap, alibi_slopes, prefix_len, workspace, workspace_bytes, stream);
+}
+
+extern "C" int attn_batch_paged8(const void* q, const void* k_pages, const void* v_pages, const uint8_t* k_scales,
+                                 const uint8_t* v_scales, void* out, attn_dtype_t dtype, const uint32_t* block_table,
+                                 const uint32_t* q_start, const uint32_t* kv_len, uint32_t total_rows, uint32_t n_seqs,
+                                 uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim, uint32_t kv_dim,
+                                 uint32_t q_stride, uint32_t out_stride, uint32_t page_rows, uint32_t num_pages,
+                                 uint32_t max_blocks, uint32_t scale_rows, float scale, uint32_t window, uint32_t sinks,
+                                 float softcap, const float* alibi_slopes, const uint32_t* prefix_len, void* workspace,
+                                 size_t workspace_bytes, attn_stream_t stream) {
+  if (scale_rows == 0 || page_rows % scale_rows != 0) return ATTN_ERR_INVALID_ARG;
+  if (total_rows > 0 && n_seqs > 0 && (k_scales == nullptr || v_scales == nullptr)) return ATTN_ERR_INVALID_ARG;
+  return batch_paged(q, k_pages, v_pages, k_scales, v_scales, out, dtype, block_table, q_start, kv_len, total_rows,
+                     n_seqs, n_heads, n_kv_heads, head_dim, kv_dim, q_stride, out_stride, page_rows, num_pages,
+                     max_blocks, scale_rows, scale, window, sinks, softcap, alibi_slopes, prefix_len, workspace,
+                     workspace_bytes, stream);
 }

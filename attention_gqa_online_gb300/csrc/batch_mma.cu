@@ -27,6 +27,7 @@
 #include "batch.h"
 #include "batch_plan.cuh"
 #include "batch_score.cuh"
+#include "cache8.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "mma16.cuh"
@@ -51,8 +52,10 @@ struct MmaSmem {
   unsigned char v[kStages][kKeys * DP * 2];
 };
 
-template <typename T, int DP, bool CAP>
+// T: of Q and the result.  C8: K and V are codes of cache8.cuh, and operands fp16.
+template <typename T, int DP, bool CAP, bool C8>
 __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, const ScoreMap sm) {
+  using TO = typename std::conditional<C8, __half, T>::type;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   MmaSmem<DP>& sh = *reinterpret_cast<MmaSmem<DP>*>(smem_raw);
   __shared__ plan::Start start;
@@ -86,6 +89,25 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
         if ((key >= p.k.lo_min && key < p.k.hi_max) || key < p.k.se)
           row = paged_row(table, a.page_rows, a.num_pages, key, a.status);
         const bool ok = row >= 0 && 8 * u < a.D;
+        if constexpr (C8) {
+          const long long block = ok ? (long long)divide((uint32_t)row, a.by_scale) * a.G + p.g : 0;
+          auto eight = [&](const void* pages, const uint8_t* scales, unsigned char* dst) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (ok) {
+              const uint2 c8 = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages) + row * a.kv_dim +
+                                                               (long long)p.g * a.D + 8 * u);
+              const uint32_t mul = c8::pow2_half2(c8::exp_of(scales[block]));
+              c8::to_half4(c8.x, w.x, w.y);
+              c8::to_half4(c8.y, w.z, w.w);
+              w = make_uint4(c8::mul_half2(w.x, mul), c8::mul_half2(w.y, mul), c8::mul_half2(w.z, mul),
+                             c8::mul_half2(w.w, mul));
+            }
+            *reinterpret_cast<uint4*>(dst + r * DP * 2 + 16 * (u ^ (r & 7))) = w;
+          };
+          eight(a.k_pages, a.k_scales, sh.k[st]);
+          eight(a.v_pages, a.v_scales, sh.v[st]);
+          continue;
+        }
         const long long off = ok ? row * a.kv_dim + (long long)p.g * a.D + 8 * u : 0;
         const int dst = r * DP * 2 + 16 * (u ^ (r & 7));
         cp_async16(sh.k[st] + dst, static_cast<const T*>(a.k_pages) + off, ok ? 16u : 0u);
@@ -114,6 +136,23 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 
+    float qf[2] = {1.f, 1.f};  // powers of two that came off the rows of Q (rows r0 and r0 + 8)
+    if constexpr (C8 && !std::is_same<T, __half>::value) {
+      cp_async_wait<0>();
+      __syncthreads();
+      // Two lanes a row, every other unit.
+      const int r = 16 * warp + (lane >> 1);
+      unsigned char* row = sh.q + r * DP * 2;
+      float m = 0.f;
+      for (int u = lane & 1; u < kUnits; u += 2) m = fmaxf(m, q16::largest(row + 16 * (u ^ (r & 7))));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      const int E = pow2_scale_exp(m);
+      for (int u = lane & 1; u < kUnits; u += 2) q16::to_half(row + 16 * (u ^ (r & 7)), pow2f(14 - E));
+      const float f = pow2f(E - 14);
+      qf[0] = __shfl_sync(0xffffffffu, f, 2 * (lane >> 2));
+      qf[1] = __shfl_sync(0xffffffffu, f, 2 * (lane >> 2) + 16);
+      __syncwarp();  // the warp's own rows: it alone reads them
+    }
     for (int i = 0; i < n; ++i) {
       const int st = i % kStages;
       if (i + 1 < n) load_tile(p.t0 + i + 1, (i + 1) % kStages);
@@ -134,8 +173,8 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
         for (int j = 0; j < kKeys / 16; ++j) {  // 16 keys: units 2c, 2c+1 of two 8-row groups
           uint32_t kb[4];
           ldsm4(kb, unit_addr<DP>(k_base, 16 * j + (lane & 7) + 8 * (lane >> 4), 2 * c + ((lane >> 3) & 1)));
-          mma16816<T>(s[2 * j], qa, kb[0], kb[1]);
-          mma16816<T>(s[2 * j + 1], qa, kb[2], kb[3]);
+          mma16816<TO>(s[2 * j], qa, kb[0], kb[1]);
+          mma16816<TO>(s[2 * j + 1], qa, kb[2], kb[3]);
         }
       }
       const int key0 = plan::tile_at<true>(p.t0 + i, p.k.ns, p.k.skip) * kKeys;
@@ -146,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
         for (int e = 0; e < 4; ++e) {
           const int key = key0 + 8 * j + 2 * (lane & 3) + (e & 1), x = e >> 1;
           float v = s[j][e];
+          if (C8) v *= qf[x];
           if (CAP) {
             v = sm.out_mul * tanh_score(v * sm.in_mul);
           } else {
@@ -166,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
         m[x] = mn;
         l[x] *= corr[x];
       }
-      constexpr float kHead = std::is_same<T, __half>::value ? kF16Head : 0.f;
+      constexpr float kHead = std::is_same<TO, __half>::value ? kF16Head : 0.f;
       const float sub[2] = {m[0] == -INFINITY ? 0.f : m[0] - kHead, m[1] == -INFINITY ? 0.f : m[1] - kHead};
 #pragma unroll
       for (int j = 0; j < DP / 8; ++j)
@@ -183,14 +223,14 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
             pr[y][e] = ex2(s[2 * j + y][e] - sub[e >> 1]);
             l[e >> 1] += pr[y][e];
           }
-        const uint32_t pa[4] = {pack2<T>(pr[0][0], pr[0][1]), pack2<T>(pr[0][2], pr[0][3]), pack2<T>(pr[1][0], pr[1][1]),
-                                pack2<T>(pr[1][2], pr[1][3])};
+        const uint32_t pa[4] = {pack2<TO>(pr[0][0], pr[0][1]), pack2<TO>(pr[0][2], pr[0][3]),
+                                pack2<TO>(pr[1][0], pr[1][1]), pack2<TO>(pr[1][2], pr[1][3])};
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c) {
           uint32_t vb[4];
           ldsm4_t(vb, unit_addr<DP>(v_base, 16 * j + (lane & 15), 2 * c + (lane >> 4)));
-          mma16816<T>(o[2 * c], pa, vb[0], vb[1]);
-          mma16816<T>(o[2 * c + 1], pa, vb[2], vb[3]);
+          mma16816<TO>(o[2 * c], pa, vb[0], vb[1]);
+          mma16816<TO>(o[2 * c + 1], pa, vb[2], vb[3]);
         }
       }
       __syncthreads();  // the stage may be refilled
@@ -272,7 +312,9 @@ int launch_mma_t(const BatchArgs& a, int blocks, cudaStream_t s) {
   const ScoreMap sm = score_map(a);
   const size_t plan_bytes = ((size_t)a.n_seqs + 1) * sizeof(int);
   const size_t smem = sizeof(MmaSmem<DP>) > plan_bytes ? sizeof(MmaSmem<DP>) : plan_bytes;
-  auto kern = a.softcap > 0.f ? batch_mma_kernel<T, DP, true> : batch_mma_kernel<T, DP, false>;
+  auto kern = a.k_scales != nullptr
+                  ? (a.softcap > 0.f ? batch_mma_kernel<T, DP, true, true> : batch_mma_kernel<T, DP, false, true>)
+                  : (a.softcap > 0.f ? batch_mma_kernel<T, DP, true, false> : batch_mma_kernel<T, DP, false, false>);
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return ATTN_ERR_CUDA;
   BatchArgs b = a;
   b.item_cost = kItemCost;
@@ -316,6 +358,7 @@ void set_batch_wait_ns(unsigned ns) { g_wait_ns = ns; }
 int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cudaStream_t s) {
   a.by_gs = fast_div((uint32_t)a.gs);
   a.by_page = fast_div((uint32_t)a.page_rows);
+  a.by_scale = fast_div((uint32_t)a.scale_rows);
   a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
   a.calls = static_cast<unsigned long long*>(workspace);
   a.arrived = a.calls + kCallsBytes / sizeof(unsigned long long);
@@ -325,7 +368,7 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   // page, whole 8-row groups of the swizzle; other pages take the mma kernel.
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
-  if (box >= 8) {
+  if (box >= 8 && a.k_scales == nullptr) {
     // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 308
     // us at 4 query heads a kv head, 313 at 16 (tcgen05 kernel: 317 and 322); heads of 64: 162 (187); 8 sequences of
     // 2048: 16 us against 24. More heads a kv head would read K and V once for every 16 of them. The lengths are on the

@@ -73,4 +73,34 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 }
 
 }  // namespace c8
+
+// Q of bf16 as an fp16 operand: a row is multiplied by the power of two that
+// brings its largest magnitude to [2^14, 2^15) (pow2_scale_exp), which every
+// score of the row is divided by again.  Entries down to 2^-28 of the largest
+// keep all their bits, smaller ones are off by at most 2^-39 of it.
+namespace q16 {
+
+// Largest magnitude of eight bf16 numbers in shared memory (16 bytes).
+__device__ __forceinline__ float largest(const unsigned char* p) {
+  const uint4 x = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+  return m;
+}
+// Eight bf16 numbers in shared memory become fp16, times mul.
+__device__ __forceinline__ void to_half(unsigned char* p, float mul) {
+  uint4 x = *reinterpret_cast<uint4*>(p);
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+        : "=r"(w[i])
+        : "f"(__uint_as_float(w[i] & 0xffff0000u) * mul), "f"(__uint_as_float(w[i] << 16) * mul));
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace q16
 }  // namespace attn

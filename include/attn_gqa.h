@@ -631,6 +631,16 @@ ATTN_API int attn_qk_norm_rope_backward(const void *dq, const void *dk, const vo
  *   k_out, v_out [total_rows, ...] of type dtype, rows k_stride / v_stride
  *                elements apart
  * Errors as attn_append_paged8's.
+ *
+ * attn_batch_paged8 is attn_batch_paged_sinks over such a cache: dtype
+ * (ATTN_DT_BF16 or ATTN_DT_F16) is that of q and out.  The products run on
+ * fp16 operands: K and V exactly, Q of bf16 times a power of two of its row
+ * (entries below 2^-28 of the row's largest lose bits), P with half a step of fp16 of each weight
+ * and at least 2^-32 of the largest so far.  V must hold no NaN code at
+ * positions that some row of the sequence attends, K neither.  The workspace
+ * is attn_batch_paged's.  Errors as attn_batch_paged; INVALID_ARG for a
+ * scale_rows that does not divide page_rows or NULL scales, UNSUPPORTED for
+ * head_dim % 16 != 0 and kv_dim % 16 != 0.
  */
 ATTN_API int attn_append_paged8(const void *q, void *q_out, const void *k_new, const void *v_new, attn_dtype_t dtype,
                                 attn_dtype_t q_out_dtype, void *k_pages, void *v_pages, uint8_t *k_scales,
@@ -649,6 +659,15 @@ ATTN_API int attn_read_paged8(const void *k_pages, const void *v_pages, const ui
                               uint32_t head_dim, uint32_t kv_dim, uint32_t k_stride, uint32_t v_stride,
                               uint32_t page_rows, uint32_t num_pages, uint32_t max_blocks, uint32_t scale_rows,
                               attn_stream_t stream);
+ATTN_API int attn_batch_paged8(const void *q, const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+                               const uint8_t *v_scales, void *out, attn_dtype_t dtype, const uint32_t *block_table,
+                               const uint32_t *q_start, const uint32_t *kv_len, uint32_t total_rows, uint32_t n_seqs,
+                               uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim, uint32_t kv_dim,
+                               uint32_t q_stride, uint32_t out_stride, uint32_t page_rows, uint32_t num_pages,
+                               uint32_t max_blocks, uint32_t scale_rows, float scale, uint32_t window, uint32_t sinks,
+                               float softcap, const float *alibi_slopes, const uint32_t *prefix_len, void *workspace,
+                               size_t workspace_bytes, attn_stream_t stream);
+
 /*
  * Backward of attn_forward / attn_forward_window: the gradients of `out` with
  * respect to q, k and v for an upstream gradient dout.  The pages emit the

@@ -167,3 +167,35 @@ def test_refusals_run_with_the_device_hidden():
     r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", os.path.abspath(__file__)], env=env, cwd=ROOT,
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def attend_call(lib, q=P[0], kp=P[1], vp=P[2], ks=P[3], vs=P[4], out=P[5], dt=1, bt=P[6], st=P[7], kvl=P[8], rows=4, n=2,
+                H=4, G=2, D=64, kvd=128, qs=256, os=256, pr=16, np=8, mb=4, sr=8, scale=0.1, window=0, sinks=0, cap=0.0,
+                slopes=P[9], prefix=P[10], ws=P[11], wsb=1 << 40):
+    return lib.attn_batch_paged8(q, kp, vp, ks, vs, out, dt, bt, st, kvl, rows, n, H, G, D, kvd, qs, os, pr, np, mb, sr,
+                                 scale, window, sinks, cap, slopes, prefix, ws, wsb, None)
+
+
+@hidden
+@pytest.mark.parametrize("kw", [
+    dict(q=None), dict(kp=None), dict(vp=None), dict(ks=None), dict(vs=None), dict(out=None), dict(bt=None),
+    dict(st=None), dict(kvl=None), dict(dt=3), dict(H=0), dict(G=0), dict(H=5), dict(D=0),
+    dict(D=144, kvd=1024, qs=1024, os=1024), dict(kvd=127), dict(qs=255), dict(os=255), dict(pr=0), dict(np=0),
+    dict(mb=0), dict(sr=0), dict(sr=3), dict(sr=32), dict(scale=float("nan")), dict(scale=3e38), dict(cap=-1.0),
+    dict(cap=float("inf")), dict(bt=P[6] + 2), dict(slopes=P[9] + 1), dict(prefix=P[10] + 2)])
+def test_attend_rejects(lib, kw):
+    assert attend_call(lib, **kw) == BAD
+
+
+@hidden
+@pytest.mark.parametrize("kw", [
+    dict(dt=0), dict(D=24, kvd=128), dict(kvd=136), dict(qs=260), dict(os=260), dict(q=P[0] + 8), dict(kp=P[1] + 8),
+    dict(vp=P[2] + 8), dict(out=P[5] + 8), dict(n=16385), dict(mb=2 ** 21), dict(rows=2 ** 29)])
+def test_attend_unsupported(lib, kw):
+    assert attend_call(lib, **kw) == UNSUP
+
+
+@hidden
+def test_attend_of_nothing_is_noop(lib):
+    for kw in (dict(rows=0), dict(n=0)):
+        assert attend_call(lib, q=None, ks=None, **kw) == 0
