@@ -35,6 +35,7 @@
 #include "batch_plan.cuh"
 #include "batch_score.cuh"
 #include "batch_wait.cuh"
+#include "cache8.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "mma16.cuh"
@@ -58,11 +59,13 @@ struct DecodeDesc {
   int slot, first, last, slot0;
 };
 
-template <int D>
+template <int D, bool C8>
 struct __align__(1024) DecodeSmem {
-  // Keys of a warp and of a tile: a tile is 16 KB of K and 16 KB of V either way.
-  static constexpr int warp_keys = D == 64 ? 32 : 16, keys = 4 * warp_keys;
-  static constexpr int tile_bytes = keys * D * 2;  // K or V
+  // Keys of a warp and of a tile: a tile is 16 KB of K and 16 KB of V either way.  Rows are 128 bytes a chunk (codes: one
+  // chunk, at D = 64 half of it zeros).
+  static constexpr int chunks = C8 || D == 64 ? 1 : 2;
+  static constexpr int warp_keys = chunks == 1 ? 32 : 16, keys = 4 * warp_keys;
+  static constexpr int tile_bytes = keys * chunks * 128;  // K or V
   static constexpr int stages = kRingBytes / (2 * tile_bytes);
   // A group waits on every use of its own stages only (a parity wait that skips a phase is no wait).
   static_assert(stages % 2 == 0 && stages <= kMaxStages, "tile J and tile J + stages belong to one group");
@@ -86,13 +89,15 @@ struct __align__(1024) DecodeSmem {
   int is_last;  // this block joins the item
 };
 
-template <typename T, int D, bool SINKS, bool BRIEF = false>
+// T: of Q and the result.  C8: K and V are codes of cache8.cuh (see "Codes" below).
+template <typename T, int D, bool C8, bool SINKS, bool BRIEF = false>
 __global__ void __launch_bounds__(kThreads, 1)
     batch_decode_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
                         const int box_rows) {
-  using S = DecodeSmem<D>;
-  constexpr bool kHalf = std::is_same<T, __half>::value;
+  using S = DecodeSmem<D, C8>;
+  using TO = typename std::conditional<C8, __half, T>::type;  // operands
+  constexpr bool kHalf = std::is_same<TO, __half>::value;
   constexpr float kSlack = kHalf ? 8.f : 24.f;  // P <= 2^8 (times 2^7) or 2^24: inside the operand type's range
   constexpr int kKeys = S::keys, kChunkBytes = kKeys * 128;
   constexpr int kTiles = S::warp_keys / 8, kSteps = S::warp_keys / 16;  // n-tiles of a warp's scores, k-steps of P V
@@ -142,8 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int outside = a.num_pages * a.page_rows;  // a row past the pool: arrives as zeros
     const int parts = kKeys / box_rows;             // page parts of a tile, at most 16
     const int parts_log2 = __ffs(parts) - 1;
-    const int chunk = D == 128 ? sub : 0;
-    const bool my_part = lane < parts && (D == 128 || (lane & 1) == sub);
+    const int chunk = S::chunks == 2 ? sub : 0;
+    const bool my_part = lane < parts && (S::chunks == 2 || (lane & 1) == sub);
     // Tiles of one piece, from tile number J on.
     auto load_tiles = [&](int n, int seq, int g, int se, int lo, int hi, int tile0, int ns, int skip, int J) {
       // First key of part q.
@@ -338,16 +343,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int lo_max = d.lo_max, hi_min = rows < kRows ? 0 : d.hi_min;
     bool ok = wait(&sm.q_ready[x & 1], x >> 1);
+    // Codes: a lane's word of a row of K is four columns, so its columns of a step are 4 (lane % 4) + 0 .. 3.
     uint32_t qa[D / 16][4];
     {
-      const uint16_t* q = sm.q[x & 1];
+      const uint16_t* q = sm.q[x & 1] + (C8 ? 2 * lc : lc);
 #pragma unroll
       for (int c = 0; c < D / 16; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          qa[c][e] = *reinterpret_cast<const uint32_t*>(q + (lr + 8 * (e & 1)) * S::q_stride + 16 * c + lc + 8 * (e >> 1));
+          qa[c][e] = *reinterpret_cast<const uint32_t*>(q + (lr + 8 * (e & 1)) * S::q_stride + 16 * c +
+                                                        (C8 ? 2 : 8) * (e >> 1));
     }
     __syncwarp();
+    float qf[2] = {1.f, 1.f};  // powers of two that came off the rows
+    if constexpr (C8 && !std::is_same<T, __half>::value) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float big = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) big = max3(big, q16::largest2(qa[c][h]), q16::largest2(qa[c][2 + h]));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int E = pow2_scale_exp(big);
+        const float mul = pow2f(14 - E);
+        qf[h] = pow2f(E - 14);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          qa[c][h] = q16::to_half2(qa[c][h], mul);
+          qa[c][2 + h] = q16::to_half2(qa[c][2 + h], mul);
+        }
+      }
+    }
+    // Codes: lane l looks up the scales of the warp's key l, the page of a tile two of the group's tiles ahead and the
+    // scales one ahead, so their trips to L2 are over when the tile is.
+    const uint32_t* table = C8 ? a.block_table + (long long)d.seq * a.max_blocks : nullptr;
+    auto page_ahead = [&](int i) {  // pool row of the lane's key of tile i, or -1
+      const int key = plan::tile_at<SINKS>(d.tile0 + i, d.ns, d.skip) * kKeys + kw + lane;
+      if (i >= n || plan::keys_hidden<SINKS>(key, 1, d.se, d.lo_min, d.hi_max)) return -1;
+      const int col = plan::page_of(a, key);
+      const uint32_t pg = table[col];
+      return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
+    };
+    auto scales_at = [&](int row) {  // bytes: K in bits 0 to 7, V in 8 to 15
+      if (row < 0) return 0x7f7fu;
+      const long long b = (long long)divide((uint32_t)row, a.by_scale) * a.G + d.g;
+      return (uint32_t)a.k_scales[b] | (uint32_t)a.v_scales[b] << 8;
+    };
+    int row_ahead = -1;
+    uint32_t scales_ahead = 0;
+    if constexpr (C8) {
+      const int i0 = (J & 1) ^ grp;
+      const int row0 = page_ahead(i0);
+      row_ahead = page_ahead(i0 + 2);
+      scales_ahead = scales_at(row0);
+    }
     // (After a wait that ran out a warp frees no slot any more, since copies may still be landing there, but keeps to
     // the block's barriers until the next piece.)
     if (ok && lane == 0) mbar_arrive(&sm.q_free[x & 1]);
@@ -359,6 +408,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     for (int i = (J & 1) ^ grp; ok && i < n; i += 2) {
       const int j = J + i, st = j % S::stages;
+      // Scales of this lane's keys 8 y + lc + {0, 1}: K's as a float, V's as a pair of fp16 numbers.
+      float kf[C8 ? kTiles : 1][2];
+      uint32_t vf[C8 ? kTiles : 1];
+      if constexpr (C8) {
+        const uint32_t mine = (uint32_t)(127 + c8::exp_of(scales_ahead & 0xffu)) << 16 |
+                              (uint32_t)(15 + c8::exp_of(scales_ahead >> 8)) << 10;
+        scales_ahead = scales_at(row_ahead);
+        row_ahead = page_ahead(i + 4);
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y) {
+          const uint32_t p0 = __shfl_sync(0xffffffffu, mine, 8 * y + lc), p1 = __shfl_sync(0xffffffffu, mine, 8 * y + lc + 1);
+          kf[y][0] = __uint_as_float(p0 >> 16 << 23);
+          kf[y][1] = __uint_as_float(p1 >> 16 << 23);
+          vf[y] = __byte_perm(p0, p1, 0x5410);
+        }
+      }
       ok = wait(&sm.full[st], j / S::stages);
       if (!ok) break;
       const uint32_t k_base = smem_u32(sm.ring[st][0]), v_base = smem_u32(sm.ring[st][1]);
@@ -369,6 +434,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int y = 0; y < kTiles; ++y)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[y][e] = s1[y][e] = 0.f;
+      if constexpr (C8) {
+        // Eight keys, four steps of 16 columns: a lane's four words are its columns of each.
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y)
+#pragma unroll
+          for (int c4 = 0; c4 < D / 64; ++c4) {
+            const int r = kw + 8 * y + (lane & 7), u = 4 * c4 + (lane >> 3);
+            uint32_t kb[4];
+            ldsm4(kb, k_base + r * 128 + 16 * (u ^ (r & 7)));
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t b0, b1;
+              c8::to_half4(kb[c], b0, b1);
+              mma16816<TO>(s[y], qa[4 * c4 + c], b0, b1);
+            }
+          }
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[y][e] *= kf[y][e & 1] * qf[e >> 1];
+      } else
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
 #pragma unroll
@@ -376,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = kw + 16 * g + (lane & 7) + 8 * (lane >> 4), u = 2 * (c & 3) + ((lane >> 3) & 1);
           uint32_t kb[4];
           ldsm4(kb, k_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
-          mma16816<T>(c % kSets ? s1[2 * g] : s[2 * g], qa[c], kb[0], kb[1]);
-          mma16816<T>(c % kSets ? s1[2 * g + 1] : s[2 * g + 1], qa[c], kb[2], kb[3]);
+          mma16816<TO>(c % kSets ? s1[2 * g] : s[2 * g], qa[c], kb[0], kb[1]);
+          mma16816<TO>(c % kSets ? s1[2 * g + 1] : s[2 * g + 1], qa[c], kb[2], kb[3]);
         }
       }
       if (kSets == 2) {
@@ -445,15 +531,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
       for (int g = 0; g < kSteps; ++g) {
-        const uint32_t pa[4] = {pack2<T>(s[2 * g][0], s[2 * g][1]), pack2<T>(s[2 * g][2], s[2 * g][3]),
-                                pack2<T>(s[2 * g + 1][0], s[2 * g + 1][1]), pack2<T>(s[2 * g + 1][2], s[2 * g + 1][3])};
+        const uint32_t pa[4] = {pack2<TO>(s[2 * g][0], s[2 * g][1]), pack2<TO>(s[2 * g][2], s[2 * g][3]),
+                                pack2<TO>(s[2 * g + 1][0], s[2 * g + 1][1]), pack2<TO>(s[2 * g + 1][2], s[2 * g + 1][3])};
+        if constexpr (C8) {
+          // A transposed word is two neighbouring columns of two keys; their even columns make one product, the odd ones
+          // another: o[2 u] and o[2 u + 1] hold columns 16 u + 2 n and 16 u + 2 n + 1.
+#pragma unroll
+          for (int u2 = 0; u2 < D / 32; ++u2) {
+            const int r = kw + 16 * g + (lane & 15), u = 2 * u2 + (lane >> 4);
+            uint32_t vb[4];
+            ldsm4_t(vb, v_base + r * 128 + 16 * (u ^ (r & 7)));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t even0, odd0, even1, odd1;
+              c8::to_half4(__byte_perm(vb[2 * e], 0, 0x3120), even0, odd0);
+              c8::to_half4(__byte_perm(vb[2 * e + 1], 0, 0x3120), even1, odd1);
+              mma16816<TO>(o[4 * u2 + 2 * e], pa, c8::mul_half2(even0, vf[2 * g]), c8::mul_half2(even1, vf[2 * g + 1]));
+              mma16816<TO>(o[4 * u2 + 2 * e + 1], pa, c8::mul_half2(odd0, vf[2 * g]), c8::mul_half2(odd1, vf[2 * g + 1]));
+            }
+          }
+        } else
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           const int r = kw + 16 * g + (lane & 15), u = 2 * (c & 3) + (lane >> 4);
           uint32_t vb[4];
           ldsm4_t(vb, v_base + (c >> 2) * kChunkBytes + r * 128 + 16 * (u ^ (r & 7)));
-          mma16816<T>(o[2 * c], pa, vb[0], vb[1]);
-          mma16816<T>(o[2 * c + 1], pa, vb[2], vb[3]);
+          mma16816<TO>(o[2 * c], pa, vb[0], vb[1]);
+          mma16816<TO>(o[2 * c + 1], pa, vb[2], vb[3]);
         }
       }
       __syncwarp();
@@ -471,9 +575,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < D / 8; ++c)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<float2*>(&sm.o[w][(lr + 8 * h) * S::o_stride + 8 * c + lc]) =
-              make_float2(o[c][2 * h], o[c][2 * h + 1]);
+        for (int h = 0; h < 2; ++h) {
+          float* row = &sm.o[w][(lr + 8 * h) * S::o_stride];
+          if constexpr (!C8)
+            *reinterpret_cast<float2*>(row + 8 * c + lc) = make_float2(o[c][2 * h], o[c][2 * h + 1]);
+          else if (c % 2 == 0)
+            *reinterpret_cast<float4*>(row + 8 * c + 2 * lc) =
+                make_float4(o[c][2 * h], o[c + 1][2 * h], o[c][2 * h + 1], o[c + 1][2 * h + 1]);
+        }
       if ((lane & 3) == 0) {
         sm.ml[w][lr] = make_float2(m[0], l[0]);
         sm.ml[w][lr + 8] = make_float2(m[1], l[1]);
@@ -489,9 +598,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f0 = l[h] == 0.f ? 0.f : ex2(m[h] - mn), f1 = other.y == 0.f ? 0.f : ex2(other.x - mn);
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const float2 v = *reinterpret_cast<const float2*>(&sm.o[warp][(lr + 8 * h) * S::o_stride + 8 * c + lc]);
-          o[c][2 * h] = o[c][2 * h] * f0 + v.x * f1;
-          o[c][2 * h + 1] = o[c][2 * h + 1] * f0 + v.y * f1;
+          const float* row = &sm.o[warp][(lr + 8 * h) * S::o_stride];
+          if constexpr (!C8) {
+            const float2 v = *reinterpret_cast<const float2*>(row + 8 * c + lc);
+            o[c][2 * h] = o[c][2 * h] * f0 + v.x * f1;
+            o[c][2 * h + 1] = o[c][2 * h + 1] * f0 + v.y * f1;
+          } else if (c % 2 == 0) {
+            const float4 v = *reinterpret_cast<const float4*>(row + 8 * c + 2 * lc);
+            o[c][2 * h] = o[c][2 * h] * f0 + v.x * f1;
+            o[c + 1][2 * h] = o[c + 1][2 * h] * f0 + v.y * f1;
+            o[c][2 * h + 1] = o[c][2 * h + 1] * f0 + v.z * f1;
+            o[c + 1][2 * h + 1] = o[c + 1][2 * h + 1] * f0 + v.w * f1;
+          }
         }
         l[h] = l[h] * f0 + other.y * f1;
         m[h] = mn;
@@ -582,25 +700,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   named_barrier(2, kThreads);  // the producers wait for the last tiles' readers
 }
 
-template <typename T, int D>
+template <typename T, int D, bool C8>
 int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
-  if (box_rows > DecodeSmem<D>::keys) box_rows = DecodeSmem<D>::keys;
-  // K and V: [rows][G][head_dim]; columns past the head (head_dim < D) arrive as zeros.
-  const uint64_t dims[3] = {(uint64_t)a.D, (uint64_t)a.G, (uint64_t)a.num_pages * a.page_rows};
-  const uint64_t strides[2] = {(uint64_t)a.D * 2, (uint64_t)a.kv_dim * 2};
+  using S = DecodeSmem<D, C8>;
+  if (box_rows > S::keys) box_rows = S::keys;
+  // K and V: [rows][G][head_dim]; columns past the head (head_dim < D) arrive as zeros.  16-bit elements are only moved:
+  // one element type serves both, and pairs of codes.
+  constexpr int kBytes = C8 ? 1 : 2;
+  const uint64_t dims[3] = {(uint64_t)a.D * kBytes / 2, (uint64_t)a.G, (uint64_t)a.num_pages * a.page_rows};
+  const uint64_t strides[2] = {(uint64_t)a.D * kBytes, (uint64_t)a.kv_dim * kBytes};
   const uint32_t box[3] = {64, 1, (uint32_t)box_rows}, one_row[3] = {64, 1, 1}, eight[3] = {64, 1, 8};
-  CUtensorMap tm_k, tm_v, tm_v1, tm_v8;  // 16-bit elements are only moved: one element type serves both
-  const int l2 = kv_l2_bytes(a.D);
+  CUtensorMap tm_k, tm_v, tm_v1, tm_v8;
+  const int l2 = kv_l2_bytes(a.D * kBytes / 2);
   if (!make_tmap(&tm_k, a.k_pages, 3, dims, strides, box, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v, a.v_pages, 3, dims, strides, box, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v8, a.v_pages, 3, dims, strides, eight, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v1, a.v_pages, 3, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
-  const void* kern = a.sinks > 0 ? reinterpret_cast<const void*>(batch_decode_kernel<T, D, true>)
-                                 : reinterpret_cast<const void*>(batch_decode_kernel<T, D, false>);
+  const void* kern;
+  if constexpr (C8)
+    kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, true, true>);
+  else
+    kern = a.sinks > 0 ? reinterpret_cast<const void*>(batch_decode_kernel<T, D, false, true>)
+                       : reinterpret_cast<const void*>(batch_decode_kernel<T, D, false, false>);
   if constexpr (std::is_same<T, __nv_bfloat16>::value)  // the failure-path test
-    if (a.wait_ns != 0 && a.sinks == 0) kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, false, true>);
-  const size_t smem = sizeof(DecodeSmem<D>) + 1024;
+    if (a.wait_ns != 0 && a.sinks == 0) kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, C8, C8, true>);
+  const size_t smem = sizeof(S) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;
   aa.item_cost = kItemCost;
@@ -609,14 +734,20 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
   return launch_pdl(kern, dim3(blocks), dim3(kThreads), smem, s, args) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+template <bool C8>
+int launch_decode(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s) {
+  if (dtype == ATTN_DT_BF16)
+    return a.D <= 64 ? launch_decode_t<__nv_bfloat16, 64, C8>(a, blocks, box_rows, s)
+                     : launch_decode_t<__nv_bfloat16, 128, C8>(a, blocks, box_rows, s);
+  return a.D <= 64 ? launch_decode_t<__half, 64, C8>(a, blocks, box_rows, s)
+                   : launch_decode_t<__half, 128, C8>(a, blocks, box_rows, s);
+}
+
 }  // namespace
 
 int launch_batch_decode(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s) {
-  if (dtype == ATTN_DT_BF16)
-    return a.D <= 64 ? launch_decode_t<__nv_bfloat16, 64>(a, blocks, box_rows, s)
-                     : launch_decode_t<__nv_bfloat16, 128>(a, blocks, box_rows, s);
-  return a.D <= 64 ? launch_decode_t<__half, 64>(a, blocks, box_rows, s)
-                   : launch_decode_t<__half, 128>(a, blocks, box_rows, s);
+  return a.k_scales != nullptr ? launch_decode<true>(a, dtype, blocks, box_rows, s)
+                               : launch_decode<false>(a, dtype, blocks, box_rows, s);
 }
 
 }  // namespace attn

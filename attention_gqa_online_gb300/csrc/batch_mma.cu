@@ -368,7 +368,7 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   // page, whole 8-row groups of the swizzle; other pages take the mma kernel.
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
-  if (box >= 8 && a.k_scales == nullptr) {
+  if (box >= 8 && (a.k_scales == nullptr || (a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16))) {
     // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 308
     // us at 4 query heads a kv head, 313 at 16 (tcgen05 kernel: 317 and 322); heads of 64: 162 (187); 8 sequences of
     // 2048: 16 us against 24. More heads a kv head would read K and V once for every 16 of them. The lengths are on the

@@ -80,14 +80,24 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 // keep all their bits, smaller ones are off by at most 2^-39 of it.
 namespace q16 {
 
-// Largest magnitude of eight bf16 numbers in shared memory (16 bytes).
+// Largest magnitude of two bf16 numbers, and the two as fp16, times mul.
+__device__ __forceinline__ float largest2(uint32_t w) {
+  return fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u)));
+}
+__device__ __forceinline__ uint32_t to_half2(uint32_t w, float mul) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+      : "=r"(r)
+      : "f"(__uint_as_float(w & 0xffff0000u) * mul), "f"(__uint_as_float(w << 16) * mul));
+  return r;
+}
+// Largest magnitude of eight, in shared memory (16 bytes).
 __device__ __forceinline__ float largest(const unsigned char* p) {
   const uint4 x = *reinterpret_cast<const uint4*>(p);
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, largest2(w[i]));
   return m;
 }
 // Eight bf16 numbers in shared memory become fp16, times mul.
@@ -95,10 +105,7 @@ __device__ __forceinline__ void to_half(unsigned char* p, float mul) {
   uint4 x = *reinterpret_cast<uint4*>(p);
   uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-        : "=r"(w[i])
-        : "f"(__uint_as_float(w[i] & 0xffff0000u) * mul), "f"(__uint_as_float(w[i] << 16) * mul));
+  for (int i = 0; i < 4; ++i) w[i] = to_half2(w[i], mul);
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
