@@ -215,5 +215,8 @@ int launch_batch_tc_part_pair(const BatchArgs& a, int dtype, int blocks, int box
 int launch_batch_tc_sinks64(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_sinks128(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 int launch_batch_tc_sinks_pair(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
+int launch_batch_tc_codes64(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
+int launch_batch_tc_codes128(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
+int launch_batch_tc_codes_pair(const BatchArgs& a, int dtype, int blocks, int box_rows, cudaStream_t s);
 
 }  // namespace attn

@@ -368,7 +368,8 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
   // page, whole 8-row groups of the swizzle; other pages take the mma kernel.
   int box = a.page_rows & -a.page_rows;
   if (box > 128) box = 128;
-  if (box >= 8 && (a.k_scales == nullptr || (a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16))) {
+  const bool codes = a.k_scales != nullptr;
+  if (box >= 8) {
     // About one row a sequence: the kernel of 16-row blocks. 64 sequences of 8192 positions, 8 kv heads of 128: 308
     // us at 4 query heads a kv head, 313 at 16 (tcgen05 kernel: 317 and 322); heads of 64: 162 (187); 8 sequences of
     // 2048: 16 us against 24. More heads a kv head would read K and V once for every 16 of them. The lengths are on the
@@ -380,14 +381,17 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
     // sequences of 4096, 4 heads a kv head of 128, with 32, 64, 128, 256, 512, 1024 rows a kv head: pairs 64, 74, 77,
     // 76, 120, 210 us, single blocks 57, 71, 74, 99, 164, 312.
     if (a.D > 64 && 128 % a.gs == 0 && sm_count % 2 == 0 && (long long)a.total_rows * a.gs >= 256ll * a.n_seqs)
-      return a.sinks > 0  ? launch_batch_tc_sinks_pair(a, dtype, sm_count, box, s)
+      return codes        ? launch_batch_tc_codes_pair(a, dtype, sm_count, box, s)
+             : a.sinks > 0 ? launch_batch_tc_sinks_pair(a, dtype, sm_count, box, s)
              : a.D == 128 ? launch_batch_tc_pair(a, dtype, sm_count, box, s)
                           : launch_batch_tc_part_pair(a, dtype, sm_count, box, s);
     if (a.D > 64)
-      return a.sinks > 0  ? launch_batch_tc_sinks128(a, dtype, sm_count, box, s)
+      return codes         ? launch_batch_tc_codes128(a, dtype, sm_count, box, s)
+             : a.sinks > 0 ? launch_batch_tc_sinks128(a, dtype, sm_count, box, s)
              : a.D == 128 ? launch_batch_tc_d128(a, dtype, sm_count, box, s)
                           : launch_batch_tc_part128(a, dtype, sm_count, box, s);
-    return a.sinks > 0 ? launch_batch_tc_sinks64(a, dtype, sm_count, box, s)
+    return codes         ? launch_batch_tc_codes64(a, dtype, sm_count, box, s)
+           : a.sinks > 0 ? launch_batch_tc_sinks64(a, dtype, sm_count, box, s)
            : a.D == 64 ? launch_batch_tc_d64(a, dtype, sm_count, box, s)
                        : launch_batch_tc_part64(a, dtype, sm_count, box, s);
   }

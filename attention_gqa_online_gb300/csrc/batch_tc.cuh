@@ -55,6 +55,15 @@
 // the softmax takes as long a tile, the products half). With the exponentials left out a chunk took seven
 // eighths of its time, with tile loads and hand-overs alone two thirds.
 //
+// Codes (C8: pools of cache8.cuh).  K and V arrive as bytes in a ring of their
+// own and warps 12-15 make fp16 operand tiles of them (every value is an fp16
+// number), and fp16 of a bf16 Q block, whose rows' powers of two the softmax
+// multiplies scores by (q16).  They convert a piece's first tiles before they
+// store the last piece's O: as many as there are operand slots, since those wait for
+// products of earlier pieces only.  Rows of V out of sight become zeros there.
+// In a pair each block fetches and converts its own halves, and its warps arrive
+// on the first block's barriers.
+//
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
 // MMAs, frees its tensor memory and leaves the status word set.  A role whose
 // wait ran out frees no slot that copies land in any more.
@@ -69,6 +78,7 @@
 #include "batch_plan.cuh"
 #include "batch_score.cuh"
 #include "batch_wait.cuh"
+#include "cache8.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -106,7 +116,7 @@ struct PieceDesc {
 
 // Shared memory of one block.  A pair splits the keys of a K tile and the
 // columns of a V tile, so each block holds half of both.
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool C8>
 struct TcLayout {
   static constexpr int rows = PAIR ? 256 : 128;       // flattened rows of an item
   static constexpr int chunks = D / 64;               // 128-byte column chunks of a row
@@ -118,15 +128,25 @@ struct TcLayout {
   static constexpr int v_chunks = PAIR ? chunks / 2 : chunks;
   static constexpr int v_chunk = kTcKeys * 128;
   static constexpr int v_bytes = v_chunks * v_chunk;
-  static constexpr int slots = k_bytes == 32768 ? 2 : 4;  // K tiles (and V tiles) in flight: 128 KB or 64 KB in all
+  // K tiles (and V tiles) in flight: 128 KB or 64 KB in all; codes: as operands, 96 KB or 128 KB.
+  static constexpr int slots = k_bytes == 32768 ? 2 : C8 ? 3 : 4;
+  static constexpr int q_bufs = C8 && k_bytes == 32768 ? 1 : 2;
+  // Codes as they come, in units of 8 KB of K or V: row bytes, rows and units of a tile, units in flight.
+  static constexpr int kr_bytes = D, vr_bytes = 64 * v_chunks;
+  static constexpr int kr_rows = C8 ? 8192 / kr_bytes : 1, vr_rows = C8 ? 8192 / vr_bytes : 1;
+  static constexpr int kr_units = C8 ? k_rows / kr_rows : 1, vr_units = C8 ? kTcKeys / vr_rows : 1;
+  static constexpr int raw_slots = !C8 ? 1 : D == 64 ? 4 : 2;
 };
+constexpr int kMaxRaw = 4;
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool C8>
 struct __align__(1024) TcSmem {
-  using L = TcLayout<D, PAIR>;
-  unsigned char q[2][L::q_bytes];
+  using L = TcLayout<D, PAIR, C8>;
+  unsigned char q[L::q_bufs][L::q_bytes];
   unsigned char k[L::slots][L::k_bytes];
   unsigned char v[L::slots][L::v_bytes];
+  unsigned char raw[2][L::raw_slots][C8 ? 8192 : 128];  // [K, V]
+  uint64_t raw_full[2][kMaxRaw], raw_empty[2][kMaxRaw], q_raw[2], qf_bar[kDescs];  // codes
   uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
   uint64_t q_ready[2], q_free[2];
   uint64_t desc_full[kDescs], desc_free[kDescs];
@@ -140,6 +160,7 @@ struct __align__(1024) TcSmem {
   unsigned char out[4][32 * 128];  // [row quarter]: 64 columns of its rows on their way out, 128-byte swizzle
   float chain[kChain][kTcRows];
   float2 stat[kDescs][2][kTcRows];  // [piece % kDescs][group][row]: reference, sum
+  float qf[C8 ? kDescs : 1][C8 ? kTcRows : 1];  // [piece % kDescs] powers of two that came off the rows of Q
   int4 row[256];               // each softmax thread's own row: window [x, y), position z, slope w (as float bits)
   PieceDesc desc[kDescs];
   int joins[kDescs];
@@ -149,7 +170,7 @@ struct __align__(1024) TcSmem {
   uint32_t tmem_base;
   int abort;
   int broken;     // a wait of either block of the pair ran out
-  int issued[3];  // K tiles, V tiles and Q blocks whose copies this block issued
+  int issued[3];  // K tiles, V tiles (codes: units) and Q blocks whose copies this block issued
 };
 
 template <int N>
@@ -207,6 +228,20 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
                  : "memory");
   else
     mbar_arrive(bar);
+}
+// As arrive_leader, for tiles that this thread's warp wrote.
+template <bool PAIR>
+__device__ __forceinline__ void arrive_leader_release(uint64_t* bar) {
+  if (PAIR)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_leader(smem_u32(bar)))
+                 : "memory");
+  else
+    mbar_arrive(bar);
+}
+// After a wait on a barrier that such arrivals complete: acquires what they released.
+template <bool PAIR>
+__device__ __forceinline__ void acquire_pair() {
+  if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
 // Tensor copies into this block's shared memory that complete on `bar` (a
 // barrier of the first block, by its cluster address, when PAIR).
@@ -314,20 +349,146 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uin
 #undef ATTN_A_DESC
 #undef ATTN_PAIR_MMA4
 
+// ---------------------------------------------------------------- codes
+// Row r of Q buffer qb, bf16, becomes fp16; what came off it.
+template <int D, bool PAIR, typename S>
+__device__ __forceinline__ float q_to_half(S& sm, int qb, int r) {
+  using L = TcLayout<D, PAIR, true>;
+  unsigned char* row = sm.q[qb] + r * 128;
+  float m = 0.f;
+#pragma unroll 8
+  for (int u = 0; u < D / 8; ++u) m = fmaxf(m, q16::largest(row + (u >> 3) * L::q_chunk + 16 * ((u & 7) ^ (r & 7))));
+  const int E = pow2_scale_exp(m);
+  const float mul = pow2f(14 - E);
+#pragma unroll 4
+  for (int u = 0; u < D / 8; ++u) q16::to_half(row + (u >> 3) * L::q_chunk + 16 * ((u & 7) ^ (r & 7)), mul);
+  return pow2f(E - 14);
+}
+
+// One of the four warps that make operand tiles of codes (`w`): a quarter of each unit's rows.  A lane looks up the
+// scales of one of the warp's rows, pool rows two tiles ahead and scales one ahead.
+template <int D, bool PAIR>
+struct Codes {
+  using L = TcLayout<D, PAIR, true>;
+  int J, Jk, Jv;          // tiles, units of K and of V so far
+  int k_row, v_row;       // pool row of the lane's key of the next tile, or -1
+  uint32_t k_mul, v_mul;  // scales of the lane's keys, both halves; V: 0 where no row sees the key
+  const uint32_t* table;
+
+  // The lane's key, within a tile, of the rows that the warp converts.
+  static __device__ __forceinline__ int key_of(int rows, int w) {
+    const int lane = threadIdx.x & 31;
+    return rows == 128 ? 32 * w + lane : 64 * (lane >> 4) + 16 * w + (lane & 15);
+  }
+  static __device__ __forceinline__ int pool_row(const BatchArgs& a, const PieceDesc& d, const uint32_t* table, int key) {
+    if (plan::keys_hidden<true>(key, 1, d.se, d.lo_min, d.hi_max)) return -1;
+    const int col = plan::page_of(a, key);
+    const uint32_t pg = table[col];
+    return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
+  }
+  __device__ __forceinline__ void look_rows(const BatchArgs& a, const PieceDesc& d, int i, int w, int rank) {
+    k_row = v_row = -1;
+    if (i >= d.n) return;
+    const int key0 = plan::tile_at<true>(d.tile_last - i, d.ns, d.skip) * kTcKeys;
+    v_row = pool_row(a, d, table, key0 + key_of(L::vr_rows, w));
+    // (A pair's block holds 64 rows of K: 16 of a warp.)
+    k_row = PAIR ? pool_row(a, d, table, key0 + 64 * rank + 16 * w + (threadIdx.x & 15)) : v_row;
+  }
+  __device__ __forceinline__ uint32_t scale_of(const BatchArgs& a, const uint8_t* scales, int row, int g) const {
+    return row < 0 ? 0u : scales[(long long)divide((uint32_t)row, a.by_scale) * a.G + g];
+  }
+  __device__ __forceinline__ void look_scales(const BatchArgs& a, const PieceDesc& d) {
+    // (The bytes stay as they are until the tile needs them.)
+    k_mul = scale_of(a, a.k_scales, k_row, d.g);
+    v_mul = v_row < 0 ? 0xffffffffu : scale_of(a, a.v_scales, v_row, d.g);
+  }
+  __device__ __forceinline__ void open(const BatchArgs& a, const PieceDesc& d, int w, int rank) {
+    table = a.block_table + (long long)d.seq * a.max_blocks;
+    look_rows(a, d, 0, w, rank);
+    look_scales(a, d);
+    look_rows(a, d, 1, w, rank);
+  }
+
+  // Units of one operand tile.  `row_bytes` of a row, `rows` of a unit, dst chunks `chunk` bytes apart.
+  template <int ROW_BYTES, int ROWS, int UNITS, typename S, typename W>
+  __device__ __forceinline__ bool make(S& sm, int is_v, int& Ju, unsigned char* dst, int chunk, uint32_t mul, int w,
+                                       W& wait) {
+    constexpr int kLanes = ROW_BYTES / 16, kAtOnce = 32 / kLanes, kWarpRows = ROWS / 4;
+    const int lane = threadIdx.x & 31, u = lane % kLanes;
+    for (int h = 0; h < UNITS; ++h, ++Ju) {
+      const int st = Ju % L::raw_slots;
+      if (!wait(&sm.raw_full[is_v][st], Ju / L::raw_slots)) return false;
+      const unsigned char* src = sm.raw[is_v][st];
+      uint4 c[kWarpRows / kAtOnce];
+#pragma unroll
+      for (int it = 0; it < kWarpRows / kAtOnce; ++it)
+        c[it] = *reinterpret_cast<const uint4*>(src + (kWarpRows * w + kAtOnce * it) * ROW_BYTES + 16 * lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.raw_empty[is_v][st]);
+#pragma unroll
+      for (int it = 0; it < kWarpRows / kAtOnce; ++it) {
+        const int in_warp = kAtOnce * it + lane / kLanes, row = ROWS * h + kWarpRows * w + in_warp;
+        const uint32_t m = __shfl_sync(0xffffffffu, mul, kWarpRows == 32 ? in_warp : 16 * (h & 1) + in_warp);
+        uint32_t x[8];
+        c8::to_half4(c[it].x, x[0], x[1]);
+        c8::to_half4(c[it].y, x[2], x[3]);
+        c8::to_half4(c[it].z, x[4], x[5]);
+        c8::to_half4(c[it].w, x[6], x[7]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = m == 0u ? 0u : c8::mul_half2(x[e], m);
+        // Lanes of the second chunk store their halves the other way round: eight lanes, eight bank groups.
+        unsigned char* to = dst + (u >> 2) * chunk + row * 128;
+        const int u0 = 2 * (u & 3) + (u >> 2), u1 = u0 ^ 1;
+        const bool swap = (u >> 2) != 0;
+        *reinterpret_cast<uint4*>(to + 16 * (u0 ^ (row & 7))) =
+            swap ? make_uint4(x[4], x[5], x[6], x[7]) : make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(to + 16 * (u1 ^ (row & 7))) =
+            swap ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(x[4], x[5], x[6], x[7]);
+      }
+    }
+    return true;
+  }
+  template <typename S, typename W>
+  __device__ __forceinline__ bool convert(const BatchArgs& a, S& sm, const PieceDesc& d, int i, int w, int rank, W& wait) {
+    const int slot = J % L::slots, lane = threadIdx.x & 31;
+    const uint32_t km = c8::pow2_half2(c8::exp_of(k_mul));
+    const uint32_t vm = v_mul == 0xffffffffu ? 0u : c8::pow2_half2(c8::exp_of(v_mul));
+    look_scales(a, d);
+    look_rows(a, d, i + 2, w, rank);
+    if (J >= L::slots && !wait(&sm.k_empty[slot], J / L::slots - 1)) return false;
+    if (!make<L::kr_bytes, L::kr_rows, L::kr_units>(sm, 0, Jk, sm.k[slot], L::k_chunk, km, w, wait)) return false;
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) arrive_leader_release<PAIR>(&sm.k_full[slot]);
+    if (J >= L::slots && !wait(&sm.v_empty[slot], J / L::slots - 1)) return false;
+    if (!make<L::vr_bytes, L::vr_rows, L::vr_units>(sm, 1, Jv, sm.v[slot], L::v_chunk, vm, w, wait)) return false;
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) arrive_leader_release<PAIR>(&sm.v_full[slot]);
+    ++J;
+    return true;
+  }
+};
+
 // MODE 0: scores are scale2 * S with scale2 > 0 (folded into the exponent's
 // fma); 1: scaled, with an optional distance bias; 2: capped, with an optional
 // distance bias.
-template <typename T, int D, int MODE, bool PAIR, bool FULL, bool SINKS, bool BRIEF = false>
+// T: of Q and the result.
+template <typename T, int D, int MODE, bool PAIR, bool FULL, bool SINKS, bool C8, bool BRIEF = false>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    batch_tc_kernel(const BatchArgs a, const ScoreMap sc, const __grid_constant__ CUtensorMap tm_k,
+    batch_tc_kernel(const BatchArgs a, const ScoreMap score, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_v1, const __grid_constant__ CUtensorMap tm_v8,
                     const __grid_constant__ CUtensorMap tm_q, const int box_rows, const int q_box) {
-  using L = TcLayout<D, PAIR>;
+  static_assert(!C8 || (!FULL && SINKS), "codes have one form");
+  using L = TcLayout<D, PAIR, C8>;
+  using TO = typename std::conditional<C8, __half, T>::type;  // operands
   const int hd = FULL ? D : a.D;  // columns of a head
-  constexpr bool kHalf = std::is_same<T, __half>::value;
+  constexpr bool kHalf = std::is_same<TO, __half>::value;
+  constexpr int kQBufs = L::q_bufs;
   constexpr float kRescale = kHalf ? 8.f : 24.f;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  TcSmem<D, PAIR>& sm = *reinterpret_cast<TcSmem<D, PAIR>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  using S = TcSmem<D, PAIR, C8>;
+  S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The block (or pair) of the plan, and this block's place in its pair.
   const int unit = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, units = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
@@ -335,14 +496,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   allow_dependent_launch();
   if (warp == 0) {
+    constexpr int kMakers = C8 ? (PAIR ? 8 : 4) : 1;  // arrivals that make an operand tile ready
     for (int i = lane; i < kMaxSlots; i += 32) {
-      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_full[i], kMakers);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_full[i], kMakers);
       mbar_init(&sm.v_empty[i], 1);
     }
+    if (C8 && lane < 2 * kMaxRaw) {
+      mbar_init(&sm.raw_full[lane & 1][lane >> 1], 1);
+      mbar_init(&sm.raw_empty[lane & 1][lane >> 1], 4);
+    }
+    if (C8 && lane < kDescs) mbar_init(&sm.qf_bar[lane], 4);
     if (lane < 2) {
-      mbar_init(&sm.q_ready[lane], 1);
+      mbar_init(&sm.q_ready[lane], kMakers);
+      if (C8) mbar_init(&sm.q_raw[lane], 1);
       mbar_init(&sm.q_free[lane], 1);
       mbar_init(&sm.s_full[lane], 1);
       mbar_init(&sm.s_free[lane], PAIR ? 8 : 4);  // the group's warps, of both blocks
@@ -441,6 +609,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return row;
     };
+    // Codes of tile i of K (is_v 0) or V (1), unit by unit; J counts units.
+    auto load_codes = [&](Parts& w, int i, int is_v, int g, int& J) {
+      const int rows = is_v ? L::vr_rows : L::kr_rows, units = is_v ? L::vr_units : L::kr_units;
+      const int bytes = is_v ? L::vr_bytes : L::kr_bytes;
+      const int row = part_row(w, i), parts_log2 = __ffs(rows) - __ffs(box_rows);
+      for (int h = 0; h < units; ++h, ++J) {
+        const int st = J % L::raw_slots;
+        if (J >= L::raw_slots && !wait(&sm.raw_empty[is_v][st], J / L::raw_slots - 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[is_v][st], 8192u);
+        __syncwarp();
+        if (lane >> parts_log2 == h && (lane >> w.shift) == 0)
+          load_3d<false>(sm.raw[is_v][st] + (lane - (h << parts_log2)) * box_rows * bytes, is_v ? &tm_v : &tm_k,
+                         is_v && PAIR ? 32 * rank : 0, g, row, smem_u32(&sm.raw_full[is_v][st]));
+      }
+      return true;
+    };
     auto barrier_of = [&](uint64_t* full) { return PAIR ? in_leader(smem_u32(full)) : smem_u32(full); };
     if (warp == 0) {
       // ---------------------------------------------------------- planner, Q and K producer
@@ -507,22 +691,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                              p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
         // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
         // only feeds itself, and those rows are not stored).
-        if (x >= 2) ok = wait(&sm.q_free[x & 1], (x >> 1) - 1);
+        const int qb = x % kQBufs;
+        if (x >= kQBufs) ok = wait(&sm.q_free[qb], x / kQBufs - 1);
         if (!ok) break;
         if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
           if (lane == 0) {
-            uint64_t* full = &sm.q_ready[x & 1];
-            const uint32_t bar = barrier_of(full);
-            if (rank == 0) mbar_arrive_expect_tx(full, (unsigned)(PAIR ? 2 : 1) * L::q_bytes);
+            constexpr bool kShared = PAIR && !C8;  // both blocks' halves complete on the first one's barrier
+            uint64_t* full = C8 ? &sm.q_raw[qb] : &sm.q_ready[qb];
+            const uint32_t bar = kShared ? barrier_of(full) : smem_u32(full);
+            if (C8 || rank == 0) mbar_arrive_expect_tx(full, (unsigned)(kShared ? 2 : 1) * L::q_bytes);
 #pragma unroll
             for (int c = 0; c < L::chunks; ++c)
-              load_3d<PAIR>(sm.q[x & 1] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + plan::token_of(a, first_row), bar);
+              load_3d<kShared>(sm.q[qb] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + plan::token_of(a, first_row), bar);
           }
           __syncwarp();
         } else {
           constexpr int kUnits = D / 8, kRowsPer = 32 / kUnits;  // units of a row over the lanes
           const int u = lane % kUnits;
-          unsigned char* qt = sm.q[x & 1] + (u >> 3) * L::q_chunk;
+          unsigned char* qt = sm.q[qb] + (u >> 3) * L::q_chunk;
           const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * hd;
           const bool inside = 8 * u < hd;  // columns past the head are zeros
           for (int r = lane / kUnits; r < rows; r += kRowsPer) {
@@ -534,9 +720,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           cp_async_wait<0>();
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.q_ready[x & 1]);
+          if (lane == 0) mbar_arrive(C8 ? &sm.q_raw[qb] : &sm.q_ready[qb]);
         }
-        for (int i = 0; i < n; ++i, ++J) {
+        if constexpr (C8) {
+          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, 0, p.g, J);
+        }
+        for (int i = 0; !C8 && i < n; ++i, ++J) {
           const int row = part_row(w, i), slot = J % L::slots;
           if (J >= L::slots) ok = wait(&sm.k_empty[slot], J / L::slots - 1);
           if (!ok) break;
@@ -559,7 +748,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ---------------------------------------------------------- V producer
       if (lane == 0) {
         prefetch_tmap(&tm_v);
-        prefetch_tmap(&tm_v1);
+        if (!C8) prefetch_tmap(&tm_v1);
       }
       int J = 0;
       bool ok = true;
@@ -568,7 +757,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const PieceDesc& d = sm.desc[x % kDescs];
         const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
         Parts w = open_parts(kTcKeys, n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip, 0, d.seq);
-        for (int i = 0; i < n; ++i, ++J) {
+        if constexpr (C8) {
+          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, 1, d.g, J);
+        }
+        for (int i = 0; !C8 && i < n; ++i, ++J) {
           const int row = part_row(w, i), key = first_key_of(w, i) + lane * box_rows, slot = J % L::slots;
           if (J >= L::slots) ok = wait(&sm.v_empty[slot], J / L::slots - 1);
           if (!ok) break;
@@ -631,12 +823,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (!next_piece(x)) break;
           const PieceDesc& d = sm.desc[x % kDescs];
           const int n = d.n;
-          const uint64_t dq = dq0 + (uint64_t)((x & 1) * (L::q_bytes >> 4));
-          ok = wait(&sm.q_ready[x & 1], x >> 1);
+          const int qb = x % kQBufs;
+          const uint64_t dq = dq0 + (uint64_t)(qb * (L::q_bytes >> 4));
+          ok = wait(&sm.q_ready[qb], x / kQBufs);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
             ok = wait(&sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
             if (!ok) break;
+            acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
             const uint64_t dk = dk0 + (uint64_t)(slot * (L::k_bytes >> 4));
 #pragma unroll
@@ -646,7 +840,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             commit_all<PAIR>(&sm.s_full[b]);
             commit_all<PAIR>(&sm.k_empty[slot]);
           }
-          if (ok) commit_all<PAIR>(&sm.q_free[x & 1]);  // (after a failed wait the block may still be landing)
+          if (ok) commit_all<PAIR>(&sm.q_free[qb]);  // (after a failed wait the block may still be landing)
         }
       } else {
         constexpr uint32_t idesc_pv = tc::idesc_f32acc(fmt, true, L::rows, D);
@@ -663,6 +857,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int slot = j % L::slots, b = j & 1;
             ok = wait(&sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
             if (!ok) break;
+            acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
             const uint64_t dv = dv0 + (uint64_t)(slot * (L::v_bytes >> 4));
             constexpr uint64_t st = (16 * 128) >> 4;  // one K step: 16 key rows of 128 bytes
@@ -704,6 +899,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         info.y = plan::row_hi(q, t);
         info.z = d.len - d.q_len + t;
         if (MODE != 0 && a.slopes != nullptr) info.w = __float_as_int(-kLog2e * a.slopes[d.g * a.gs + f - t * a.gs]);
+      }
+      ScoreMap sc = score;  // codes: with what came off the row
+      if constexpr (C8) {
+        lane_wait(&sm.qf_bar[x % kDescs], x / kDescs);
+        const float f = sm.qf[x % kDescs][r];
+        // (Masked scores are -inf before they are multiplied: not by zero, and a row this small has scores of zero.)
+        sc.scale2 = MODE == 0 ? fmaxf(sc.scale2 * f, FLT_MIN) : sc.scale2 * f;
+        sc.in_mul *= f;
       }
       sm.row[128 * grp + r] = info;  // read on the tiles that need it: kept in registers it would spill scores
       for (int i = (J & 1) ^ grp; i < n; i += 2) {
@@ -881,7 +1084,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               const int k = e - kLag;
               const float p0 = __uint_as_float(s[k >> 5][k & 31]), p1 = __uint_as_float(s[k >> 5][(k & 31) + 1]);
               add2(sum[k & 2], sum[(k & 2) + 1], p0, p1);
-              s[k >> 5][(k & 31) >> 1] = pack_pair<T>(p0, p1);
+              s[k >> 5][(k & 31) >> 1] = pack_pair<TO>(p0, p1);
             }
           }
           // P_b was last read by P V of tile j - 2.
@@ -934,8 +1137,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int qd = warp & 3, r = 32 * qd + lane;
     const uint32_t o_col = tmem + ((uint32_t)(32 * qd) << 16) + kOColumn;
     constexpr int kCols = 16, kChunks = D / kCols;  // columns at a time: few registers
-    for (int x = 0;; ++x) {
-      if (!next_piece(x)) break;
+    auto output = [&](int x) {
       const PieceDesc& d = sm.desc[x % kDescs];
       const bool busy = 32 * qd < d.rows, store = r < d.rows;
       lane_wait(&sm.stat_bar[qd][x % kDescs][0], x / kDescs);
@@ -1133,6 +1335,42 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+    };
+    if constexpr (!C8) {
+      for (int x = 0;; ++x) {
+        if (!next_piece(x)) break;
+        output(x);
+      }
+    } else {
+      Codes<D, PAIR> codes{0, 0, 0};
+      for (int x = 0;; ++x) {
+        const bool more = next_piece(x);
+        bool ok = more;
+        if (more) {
+          const PieceDesc& d = sm.desc[x % kDescs];
+          const int qb = x % kQBufs;
+          ok = wait(&sm.q_raw[qb], x / kQBufs);
+          if (ok) {
+            float f = 1.f;
+            if constexpr (!std::is_same<T, __half>::value) f = q_to_half<D, PAIR, S>(sm, qb, r);
+            sm.qf[x % kDescs][r] = f;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sm.qf_bar[x % kDescs]);
+              arrive_leader_release<PAIR>(&sm.q_ready[qb]);
+            }
+            codes.open(a, d, qd, rank);
+            for (int i = 0; ok && i < d.n && i < L::slots; ++i) ok = codes.convert(a, sm, d, i, qd, rank, wait);
+          }
+        }
+        if (more ? !ok : !warp_whole(&sm.abort)) break;  // the pipeline broke
+        if (x > 0) output(x - 1);
+        if (!more) break;
+        const PieceDesc& d = sm.desc[x % kDescs];
+        for (int i = L::slots; ok && i < d.n; ++i) ok = codes.convert(a, sm, d, i, qd, rank, wait);
+        if (!ok) break;
+      }
     }
   }
 
@@ -1140,12 +1378,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_before_sync();
   // No copy may still be landing in shared memory when the block exits.  Products have read every tile, unless the
   // pipeline broke.
+  auto drain_codes = [&] {
+    drain_ring(sm.raw_full[0], L::raw_slots, sm.issued[0], a.status);
+    drain_ring(sm.raw_full[1], L::raw_slots, sm.issued[1], a.status);
+    drain_ring(sm.q_raw, kQBufs, sm.issued[2], a.status);
+  };
   if (PAIR) {
     // Arrivals, commits and copies cross the pair: it leaves together.
     if (lane == 0 && *(volatile int*)&sm.abort != 0)
       for (int b = 0; b < 2; ++b) store_in_block(&sm.broken, b, 1);
     pair_sync();
-    if (*(volatile int*)&sm.broken != 0) {
+    if constexpr (C8) {  // (each block's copies are its own)
+      if (*(volatile int*)&sm.broken != 0) {
+        if (tid == 0) drain_codes();
+        __syncwarp();
+        pair_sync();
+      }
+    } else if (*(volatile int*)&sm.broken != 0) {
       // A tile that only one block issued would never complete: its barrier was armed for both halves, or not at all.
       // (One block is at most a ring ahead of the other, since a slot falls free by a product that read both halves.)
       if (rank == 0 && tid == 0) {
@@ -1166,7 +1415,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else {
     __syncthreads();
-    if (*(volatile int*)&sm.abort != 0 && tid == 0) {
+    if (C8 && *(volatile int*)&sm.abort != 0 && tid == 0) {
+      drain_codes();
+    } else if (*(volatile int*)&sm.abort != 0 && tid == 0) {
       drain_ring(sm.k_full, L::slots, sm.issued[0], a.status);
       drain_ring(sm.v_full, L::slots, sm.issued[1], a.status);
       drain_ring(sm.q_ready, 2, sm.issued[2], a.status);
@@ -1178,19 +1429,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <typename T, int D, bool PAIR, bool FULL, bool SINKS>
+template <typename T, int D, bool PAIR, bool FULL, bool SINKS, bool C8 = false>
 int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   // K and V: whole rows, or [rows][G][head_dim], where columns past the head arrive as zeros.
   const int rank = FULL ? 2 : 3;
+  using L = TcLayout<D, PAIR, C8>;
   const uint64_t pool = (uint64_t)a.num_pages * a.page_rows;
-  const uint64_t dims[3] = {(uint64_t)(FULL ? a.kv_dim : a.D), FULL ? pool : (uint64_t)a.G, pool};
-  const uint64_t strides[2] = {(uint64_t)(FULL ? a.kv_dim : a.D) * 2, (uint64_t)a.kv_dim * 2};
+  constexpr int kBytes = C8 ? 1 : 2;
+  const uint64_t dims[3] = {(uint64_t)(FULL ? a.kv_dim : a.D) * kBytes / 2, FULL ? pool : (uint64_t)a.G, pool};
+  const uint64_t strides[2] = {(uint64_t)(FULL ? a.kv_dim : a.D) * kBytes, (uint64_t)a.kv_dim * kBytes};
   if (PAIR && box_rows > 64) box_rows = 64;  // a block holds 64 keys of a K tile
+  if (C8 && box_rows > L::kr_rows) box_rows = L::kr_rows;
+  if (C8 && box_rows > L::vr_rows) box_rows = L::vr_rows;
   const uint32_t box[3] = {64, FULL ? (uint32_t)box_rows : 1, (uint32_t)box_rows}, one_row[3] = {64, 1, 1};
   const uint32_t eight[3] = {64, FULL ? 8u : 1u, 8};
-  CUtensorMap tm_k, tm_v, tm_v1, tm_v8;  // 16-bit elements are only moved: one element type serves both
-  const int l2 = kv_l2_bytes(a.D);
-  if (!make_tmap(&tm_k, a.k_pages, rank, dims, strides, box, true, kSwizzle128, l2) ||
+  CUtensorMap tm_k, tm_v, tm_v1, tm_v8;  // 16-bit elements are only moved: one element type serves both, and pairs of codes
+  const int l2 = kv_l2_bytes(a.D * kBytes / 2);
+  if constexpr (C8) {
+    const uint32_t kbox[3] = {L::kr_bytes / 2, 1, (uint32_t)box_rows}, vbox[3] = {L::vr_bytes / 2, 1, (uint32_t)box_rows};
+    if (!make_tmap(&tm_k, a.k_pages, 3, dims, strides, kbox, true, kSwizzleNone, l2) ||
+        !make_tmap(&tm_v, a.v_pages, 3, dims, strides, vbox, true, kSwizzleNone, l2))
+      return ATTN_ERR_CUDA;
+    tm_v1 = tm_v8 = tm_v;
+  } else if (!make_tmap(&tm_k, a.k_pages, rank, dims, strides, box, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v, a.v_pages, rank, dims, strides, box, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v8, a.v_pages, rank, dims, strides, eight, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v1, a.v_pages, rank, dims, strides, one_row, true, kSwizzle128, l2))
@@ -1207,15 +1468,16 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
   ScoreMap sc = score_map(a);
   const void* kern;
   if (a.softcap > 0.f)
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR, FULL, SINKS>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR, FULL, SINKS, C8>);
   else if (a.slopes != nullptr || !(sc.scale2 >= FLT_MIN))
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL, SINKS>);
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL, SINKS, C8>);
   else
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS>);
-  if constexpr (std::is_same<T, __nv_bfloat16>::value && !SINKS)  // the failure-path test
-    if (a.wait_ns != 0 && a.softcap == 0.f && a.slopes == nullptr && sc.scale2 >= FLT_MIN)
-      kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS, true>);
-  const size_t smem = sizeof(TcSmem<D, PAIR>) + 1024;
+    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS, C8>);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value && (C8 || !SINKS))  // the failure-path test
+    if (a.wait_ns != 0 && a.sinks == 0 && a.softcap == 0.f && a.slopes == nullptr && sc.scale2 >= FLT_MIN)
+      kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS, C8, true>);
+  const size_t smem = sizeof(TcSmem<D, PAIR, C8>) + 1024;
+  static_assert(sizeof(TcSmem<D, PAIR, C8>) + 1024 <= 227 * 1024, "shared memory of a block");
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;
   aa.item_cost = q_box ? kItemCost : kItemCostRows;
