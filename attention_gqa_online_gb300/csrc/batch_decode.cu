@@ -377,25 +377,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Codes: lane l looks up the scales of the warp's key l, the page of a tile two of the group's tiles ahead and the
     // scales one ahead, so their trips to L2 are over when the tile is.
     const uint32_t* table = C8 ? a.block_table + (long long)d.seq * a.max_blocks : nullptr;
-    auto page_ahead = [&](int i) {  // pool row of the lane's key of tile i, or -1
-      const int key = plan::tile_at<SINKS>(d.tile0 + i, d.ns, d.skip) * kKeys + kw + lane;
-      if (i >= n || plan::keys_hidden<SINKS>(key, 1, d.se, d.lo_min, d.hi_max)) return -1;
-      const int col = plan::page_of(a, key);
-      const uint32_t pg = table[col];
-      return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
+    // (What a load brings is first used a tile later.)
+    auto key_at = [&](int i) { return plan::tile_at<SINKS>(d.tile0 + i, d.ns, d.skip) * kKeys + kw + lane; };
+    auto page_at = [&](int i) {  // page of the lane's key of tile i; none where no row sees it
+      const int key = key_at(i);
+      if (i >= n || plan::keys_hidden<SINKS>(key, 1, d.se, d.lo_min, d.hi_max)) return 0xffffffffu;
+      return table[plan::page_of(a, key)];
     };
-    auto scales_at = [&](int row) {  // bytes: K in bits 0 to 7, V in 8 to 15
-      if (row < 0) return 0x7f7fu;
-      const long long b = (long long)divide((uint32_t)row, a.by_scale) * a.G + d.g;
-      return (uint32_t)a.k_scales[b] | (uint32_t)a.v_scales[b] << 8;
+    uint32_t page_ahead = 0, k_ahead = 0, v_ahead = 0;
+    auto scales_at = [&](int i) {  // of the key whose page is in page_ahead
+      if (page_ahead >= (uint32_t)a.num_pages) return;
+      const int key = key_at(i);
+      const uint32_t row = page_ahead * (uint32_t)a.page_rows + (uint32_t)(key - plan::page_of(a, key) * a.page_rows);
+      const long long b = (long long)divide(row, a.by_scale) * a.G + d.g;
+      k_ahead = a.k_scales[b];
+      v_ahead = a.v_scales[b];
     };
-    int row_ahead = -1;
-    uint32_t scales_ahead = 0;
     if constexpr (C8) {
       const int i0 = (J & 1) ^ grp;
-      const int row0 = page_ahead(i0);
-      row_ahead = page_ahead(i0 + 2);
-      scales_ahead = scales_at(row0);
+      page_ahead = page_at(i0);
+      scales_at(i0);
+      page_ahead = page_at(i0 + 2);
     }
     // (After a wait that ran out a warp frees no slot any more, since copies may still be landing there, but keeps to
     // the block's barriers until the next piece.)
@@ -412,10 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float kf[C8 ? kTiles : 1][2];
       uint32_t vf[C8 ? kTiles : 1];
       if constexpr (C8) {
-        const uint32_t mine = (uint32_t)(127 + c8::exp_of(scales_ahead & 0xffu)) << 16 |
-                              (uint32_t)(15 + c8::exp_of(scales_ahead >> 8)) << 10;
-        scales_ahead = scales_at(row_ahead);
-        row_ahead = page_ahead(i + 4);
+        const uint32_t mine = (uint32_t)(127 + c8::exp_of(k_ahead)) << 16 | (uint32_t)(15 + c8::exp_of(v_ahead)) << 10;
+        scales_at(i + 2);
+        page_ahead = page_at(i + 4);
 #pragma unroll
         for (int y = 0; y < kTiles; ++y) {
           const uint32_t p0 = __shfl_sync(0xffffffffu, mine, 8 * y + lc), p1 = __shfl_sync(0xffffffffu, mine, 8 * y + lc + 1);

@@ -61,8 +61,7 @@
 // multiplies scores by (q16).  They convert a piece's first tiles before they
 // store the last piece's O: as many as there are operand slots, since those wait for
 // products of earlier pieces only.  Rows of V out of sight become zeros there.
-// In a pair each block fetches and converts its own halves, and its warps arrive
-// on the first block's barriers.
+// In a pair each block fetches and converts its own halves.
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
 // MMAs, frees its tensor memory and leaves the status word set.  A role whose
@@ -98,7 +97,10 @@ constexpr int kChain = 4;        // reference maxima in flight
 constexpr int kPColumn = 256, kOColumn = 384;
 constexpr int kMaxSlots = 4;     // K (and V) tiles in flight, at most
 // Registers: 128 threads * (72 + 72) + 256 * 184 = 512 * 128, the block's allocation at launch.
-constexpr int kCtrlRegs = 72, kOutRegs = 72, kSoftmaxRegs = 184;
+// Codes: 128 * (72 + 104) + 256 * 168, for the warps that make operand tiles.
+constexpr int kCtrlRegs = 72, kOutRegs = 72, kSoftmaxRegs = 184, kOutRegsC8 = 104, kSoftmaxRegsC8 = 168;
+static_assert(128 * (kCtrlRegs + kOutRegs) + 256 * kSoftmaxRegs == 65536 &&
+                  128 * (kCtrlRegs + kOutRegsC8) + 256 * kSoftmaxRegsC8 == 65536, "the block's registers at launch");
 
 // A piece as the roles see it.
 struct PieceDesc {
@@ -135,7 +137,7 @@ struct TcLayout {
   static constexpr int kr_bytes = D, vr_bytes = 64 * v_chunks;
   static constexpr int kr_rows = C8 ? 8192 / kr_bytes : 1, vr_rows = C8 ? 8192 / vr_bytes : 1;
   static constexpr int kr_units = C8 ? k_rows / kr_rows : 1, vr_units = C8 ? kTcKeys / vr_rows : 1;
-  static constexpr int raw_slots = !C8 ? 1 : D == 64 ? 4 : 2;
+  static constexpr int raw_slots = !C8 ? 1 : D == 64 ? 3 : 2;
 };
 constexpr int kMaxRaw = 4;
 
@@ -145,8 +147,10 @@ struct __align__(1024) TcSmem {
   unsigned char q[L::q_bufs][L::q_bytes];
   unsigned char k[L::slots][L::k_bytes];
   unsigned char v[L::slots][L::v_bytes];
-  unsigned char raw[2][L::raw_slots][C8 ? 8192 : 128];  // [K, V]
+  alignas(128) unsigned char raw[2][L::raw_slots][C8 ? 8192 : 128];  // [K, V]
+  uint16_t scale[2][L::raw_slots][C8 ? (D == 64 || PAIR ? 128 : 64) : 1];  // of each row of a unit, fp16; 0: out of sight
   uint64_t raw_full[2][kMaxRaw], raw_empty[2][kMaxRaw], q_raw[2], qf_bar[kDescs];  // codes
+  uint64_t k_made[kMaxSlots], v_made[kMaxSlots], q_made[2];                        // codes: operands written by this block
   uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
   uint64_t q_ready[2], q_free[2];
   uint64_t desc_full[kDescs], desc_free[kDescs];
@@ -157,10 +161,10 @@ struct __align__(1024) TcSmem {
   uint64_t o_free;                // O has been read
   uint64_t join_bar[kDescs];      // [piece % kDescs] whether this block joins the piece's item is known
   uint64_t drain[2];
-  unsigned char out[4][32 * 128];  // [row quarter]: 64 columns of its rows on their way out, 128-byte swizzle
+  alignas(128) unsigned char out[4][32 * 128];  // [row quarter]: 64 columns of its rows on their way out, 128-byte swizzle
   float chain[kChain][kTcRows];
   float2 stat[kDescs][2][kTcRows];  // [piece % kDescs][group][row]: reference, sum
-  float qf[C8 ? kDescs : 1][C8 ? kTcRows : 1];  // [piece % kDescs] powers of two that came off the rows of Q
+  int8_t qf[C8 ? kDescs : 1][C8 ? kTcRows : 1];  // [piece % kDescs] powers of two that came off the rows of Q: 2^(qf - 14)
   int4 row[256];               // each softmax thread's own row: window [x, y), position z, slope w (as float bits)
   PieceDesc desc[kDescs];
   int joins[kDescs];
@@ -350,9 +354,9 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b0, uin
 #undef ATTN_PAIR_MMA4
 
 // ---------------------------------------------------------------- codes
-// Row r of Q buffer qb, bf16, becomes fp16; what came off it.
+// Row r of Q buffer qb, bf16, becomes fp16, times 2^(14 - the result).
 template <int D, bool PAIR, typename S>
-__device__ __forceinline__ float q_to_half(S& sm, int qb, int r) {
+__device__ __forceinline__ int q_to_half(S& sm, int qb, int r) {
   using L = TcLayout<D, PAIR, true>;
   unsigned char* row = sm.q[qb] + r * 128;
   float m = 0.f;
@@ -362,113 +366,63 @@ __device__ __forceinline__ float q_to_half(S& sm, int qb, int r) {
   const float mul = pow2f(14 - E);
 #pragma unroll 4
   for (int u = 0; u < D / 8; ++u) q16::to_half(row + (u >> 3) * L::q_chunk + 16 * ((u & 7) ^ (r & 7)), mul);
-  return pow2f(E - 14);
+  return E;
 }
 
-// One of the four warps that make operand tiles of codes (`w`): a quarter of each unit's rows.  A lane looks up the
-// scales of one of the warp's rows, pool rows two tiles ahead and scales one ahead.
-template <int D, bool PAIR>
-struct Codes {
+// Operand tiles of tile J (K, then V), this warp's quarter of each unit's rows.  One piece of code for both, and short:
+// a warp alone runs at three or four clocks an instruction, and all roles of the block share the instruction cache (both
+// unrolled apart, and scales looked up here: 2 chunks of 512 behind 16k to 32k 706 us).
+template <int D, bool PAIR, typename S, typename W>
+__device__ __forceinline__ bool make_operands(S& sm, int J, int w, W& wait) {
   using L = TcLayout<D, PAIR, true>;
-  int J, Jk, Jv;          // tiles, units of K and of V so far
-  int k_row, v_row;       // pool row of the lane's key of the next tile, or -1
-  uint32_t k_mul, v_mul;  // scales of the lane's keys, both halves; V: 0 where no row sees the key
-  const uint32_t* table;
-
-  // The lane's key, within a tile, of the rows that the warp converts.
-  static __device__ __forceinline__ int key_of(int rows, int w) {
-    const int lane = threadIdx.x & 31;
-    return rows == 128 ? 32 * w + lane : 64 * (lane >> 4) + 16 * w + (lane & 15);
-  }
-  static __device__ __forceinline__ int pool_row(const BatchArgs& a, const PieceDesc& d, const uint32_t* table, int key) {
-    if (plan::keys_hidden<true>(key, 1, d.se, d.lo_min, d.hi_max)) return -1;
-    const int col = plan::page_of(a, key);
-    const uint32_t pg = table[col];
-    return pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
-  }
-  __device__ __forceinline__ void look_rows(const BatchArgs& a, const PieceDesc& d, int i, int w, int rank) {
-    k_row = v_row = -1;
-    if (i >= d.n) return;
-    const int key0 = plan::tile_at<true>(d.tile_last - i, d.ns, d.skip) * kTcKeys;
-    v_row = pool_row(a, d, table, key0 + key_of(L::vr_rows, w));
-    // (A pair's block holds 64 rows of K: 16 of a warp.)
-    k_row = PAIR ? pool_row(a, d, table, key0 + 64 * rank + 16 * w + (threadIdx.x & 15)) : v_row;
-  }
-  __device__ __forceinline__ uint32_t scale_of(const BatchArgs& a, const uint8_t* scales, int row, int g) const {
-    return row < 0 ? 0u : scales[(long long)divide((uint32_t)row, a.by_scale) * a.G + g];
-  }
-  __device__ __forceinline__ void look_scales(const BatchArgs& a, const PieceDesc& d) {
-    // (The bytes stay as they are until the tile needs them.)
-    k_mul = scale_of(a, a.k_scales, k_row, d.g);
-    v_mul = v_row < 0 ? 0xffffffffu : scale_of(a, a.v_scales, v_row, d.g);
-  }
-  __device__ __forceinline__ void open(const BatchArgs& a, const PieceDesc& d, int w, int rank) {
-    table = a.block_table + (long long)d.seq * a.max_blocks;
-    look_rows(a, d, 0, w, rank);
-    look_scales(a, d);
-    look_rows(a, d, 1, w, rank);
-  }
-
-  // Units of one operand tile.  `row_bytes` of a row, `rows` of a unit, dst chunks `chunk` bytes apart.
-  template <int ROW_BYTES, int ROWS, int UNITS, typename S, typename W>
-  __device__ __forceinline__ bool make(S& sm, int is_v, int& Ju, unsigned char* dst, int chunk, uint32_t mul, int w,
-                                       W& wait) {
-    constexpr int kLanes = ROW_BYTES / 16, kAtOnce = 32 / kLanes, kWarpRows = ROWS / 4;
-    const int lane = threadIdx.x & 31, u = lane % kLanes;
-    for (int h = 0; h < UNITS; ++h, ++Ju) {
-      const int st = Ju % L::raw_slots;
-      if (!wait(&sm.raw_full[is_v][st], Ju / L::raw_slots)) return false;
-      const unsigned char* src = sm.raw[is_v][st];
-      uint4 c[kWarpRows / kAtOnce];
+  const int slot = J % L::slots, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int t = 0; t < 2; ++t) {
+    // Lanes of a row, 16 columns each: 8, or 4 where rows are 64 bytes.  A warp makes 2 KB of a unit.
+    const int lanes_log2 = (t ? L::vr_bytes : L::kr_bytes) == 128 ? 3 : 2;
+    const int u = lane & ((1 << lanes_log2) - 1), at_once = 32 >> lanes_log2;
+    const int in_unit = 4 * at_once * w + (lane >> lanes_log2);  // the lane's first row
+    // Lanes of the second chunk (columns from 64 on) store their halves the other way round: eight lanes, eight bank
+    // groups.  Every row of a lane has the same place among eight, or that four further, by turns.
+    const bool swap = (u >> 2) != 0;
+    const int at = 16 * ((2 * (u & 3) + (u >> 2)) ^ (in_unit & 7)), flip = at_once == 4 ? 64 : 0;
+    unsigned char* dst = (t ? sm.v[slot] + (u >> 2) * L::v_chunk : sm.k[slot] + (u >> 2) * L::k_chunk) + 128 * in_unit;
+    if (J >= L::slots && !wait(t ? &sm.v_empty[slot] : &sm.k_empty[slot], J / L::slots - 1)) return false;
+#pragma unroll 1
+    for (int h = 0; h < (t ? L::vr_units : L::kr_units); ++h) {
+      const int Ju = (t ? L::vr_units : L::kr_units) * J + h, st = Ju % L::raw_slots;
+      if (!wait(&sm.raw_full[t][st], Ju / L::raw_slots)) return false;
+      const unsigned char* src = sm.raw[t][st] + 2048 * w + 16 * lane;
+      const uint16_t* scale = sm.scale[t][st] + in_unit;
 #pragma unroll
-      for (int it = 0; it < kWarpRows / kAtOnce; ++it)
-        c[it] = *reinterpret_cast<const uint4*>(src + (kWarpRows * w + kAtOnce * it) * ROW_BYTES + 16 * lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.raw_empty[is_v][st]);
-#pragma unroll
-      for (int it = 0; it < kWarpRows / kAtOnce; ++it) {
-        const int in_warp = kAtOnce * it + lane / kLanes, row = ROWS * h + kWarpRows * w + in_warp;
-        const uint32_t m = __shfl_sync(0xffffffffu, mul, kWarpRows == 32 ? in_warp : 16 * (h & 1) + in_warp);
+      for (int it = 0; it < 4; ++it) {
+        uint4 c = *reinterpret_cast<const uint4*>(src + 512 * it);
+        const uint32_t m = scale[at_once * it] * 0x10001u;
+        if (__any_sync(0xffffffffu, m == 0u))
+          if (m == 0u) c = make_uint4(0u, 0u, 0u, 0u);  // (not 0 * code: that may be NaN)
+        if (swap) c = make_uint4(c.z, c.w, c.x, c.y);
         uint32_t x[8];
-        c8::to_half4(c[it].x, x[0], x[1]);
-        c8::to_half4(c[it].y, x[2], x[3]);
-        c8::to_half4(c[it].z, x[4], x[5]);
-        c8::to_half4(c[it].w, x[6], x[7]);
+        c8::to_half4(c.x, x[0], x[1]);
+        c8::to_half4(c.y, x[2], x[3]);
+        c8::to_half4(c.z, x[4], x[5]);
+        c8::to_half4(c.w, x[6], x[7]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = m == 0u ? 0u : c8::mul_half2(x[e], m);
-        // Lanes of the second chunk store their halves the other way round: eight lanes, eight bank groups.
-        unsigned char* to = dst + (u >> 2) * chunk + row * 128;
-        const int u0 = 2 * (u & 3) + (u >> 2), u1 = u0 ^ 1;
-        const bool swap = (u >> 2) != 0;
-        *reinterpret_cast<uint4*>(to + 16 * (u0 ^ (row & 7))) =
-            swap ? make_uint4(x[4], x[5], x[6], x[7]) : make_uint4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<uint4*>(to + 16 * (u1 ^ (row & 7))) =
-            swap ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(x[4], x[5], x[6], x[7]);
+        for (int e = 0; e < 8; ++e) x[e] = c8::mul_half2(x[e], m);
+        unsigned char* to = dst + 128 * at_once * it;
+        const int a0 = it & 1 ? at ^ flip : at;
+        *reinterpret_cast<uint4*>(to + a0) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(to + (a0 ^ 16)) = make_uint4(x[4], x[5], x[6], x[7]);
       }
+      dst += 128 * 16 * at_once;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.raw_empty[t][st]);
     }
-    return true;
-  }
-  template <typename S, typename W>
-  __device__ __forceinline__ bool convert(const BatchArgs& a, S& sm, const PieceDesc& d, int i, int w, int rank, W& wait) {
-    const int slot = J % L::slots, lane = threadIdx.x & 31;
-    const uint32_t km = c8::pow2_half2(c8::exp_of(k_mul));
-    const uint32_t vm = v_mul == 0xffffffffu ? 0u : c8::pow2_half2(c8::exp_of(v_mul));
-    look_scales(a, d);
-    look_rows(a, d, i + 2, w, rank);
-    if (J >= L::slots && !wait(&sm.k_empty[slot], J / L::slots - 1)) return false;
-    if (!make<L::kr_bytes, L::kr_rows, L::kr_units>(sm, 0, Jk, sm.k[slot], L::k_chunk, km, w, wait)) return false;
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) arrive_leader_release<PAIR>(&sm.k_full[slot]);
-    if (J >= L::slots && !wait(&sm.v_empty[slot], J / L::slots - 1)) return false;
-    if (!make<L::vr_bytes, L::vr_rows, L::vr_units>(sm, 1, Jv, sm.v[slot], L::v_chunk, vm, w, wait)) return false;
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) arrive_leader_release<PAIR>(&sm.v_full[slot]);
-    ++J;
-    return true;
+    if (lane == 0) mbar_arrive(t ? &sm.v_made[slot] : &sm.k_made[slot]);
   }
-};
+  return true;
+}
 
 // MODE 0: scores are scale2 * S with scale2 > 0 (folded into the exponent's
 // fma); 1: scaled, with an optional distance bias; 2: capped, with an optional
@@ -496,21 +450,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   allow_dependent_launch();
   if (warp == 0) {
-    constexpr int kMakers = C8 ? (PAIR ? 8 : 4) : 1;  // arrivals that make an operand tile ready
     for (int i = lane; i < kMaxSlots; i += 32) {
-      mbar_init(&sm.k_full[i], kMakers);
+      mbar_init(&sm.k_full[i], 1);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], kMakers);
+      mbar_init(&sm.v_full[i], 1);
       mbar_init(&sm.v_empty[i], 1);
+      if (C8) {
+        mbar_init(&sm.k_made[i], 4);
+        mbar_init(&sm.v_made[i], 4);
+      }
     }
     if (C8 && lane < 2 * kMaxRaw) {
-      mbar_init(&sm.raw_full[lane & 1][lane >> 1], 1);
+      mbar_init(&sm.raw_full[lane & 1][lane >> 1], 2);  // the copy, and the scales
       mbar_init(&sm.raw_empty[lane & 1][lane >> 1], 4);
     }
     if (C8 && lane < kDescs) mbar_init(&sm.qf_bar[lane], 4);
     if (lane < 2) {
-      mbar_init(&sm.q_ready[lane], kMakers);
+      mbar_init(&sm.q_ready[lane], 1);
       if (C8) mbar_init(&sm.q_raw[lane], 1);
+      if (C8) mbar_init(&sm.q_made[lane], 4);
       mbar_init(&sm.q_free[lane], 1);
       mbar_init(&sm.s_full[lane], 1);
       mbar_init(&sm.s_free[lane], PAIR ? 8 : 4);  // the group's warps, of both blocks
@@ -520,7 +478,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane < kDescs) {
       mbar_init(&sm.desc_full[lane], 1);
       mbar_init(&sm.join_bar[lane], 1);
-      mbar_init(&sm.desc_free[lane], rank == 0 ? 14 : 13);  // V, (first block) P V, eight softmax and four output warps
+      // V, (first block) P V, eight softmax and four output warps; codes: the second block's idle issue warps, too
+      mbar_init(&sm.desc_free[lane], rank == 0 ? 14 : C8 ? 15 : 13);
     }
     if (lane < 16) mbar_init(&sm.chain_bar[lane >> 2][lane & 3], 1);
     mbar_init(&sm.stat_bar[lane >> 3][(lane >> 1) & 3][lane & 1], 1);
@@ -609,19 +568,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return row;
     };
-    // Codes of tile i of K (is_v 0) or V (1), unit by unit; J counts units.
-    auto load_codes = [&](Parts& w, int i, int is_v, int g, int& J) {
-      const int rows = is_v ? L::vr_rows : L::kr_rows, units = is_v ? L::vr_units : L::kr_units;
-      const int bytes = is_v ? L::vr_bytes : L::kr_bytes;
-      const int row = part_row(w, i), parts_log2 = __ffs(rows) - __ffs(box_rows);
+    // Codes of tile i of K (is_v 0) or V (1) and their rows' scales, unit by unit; J counts units.
+    auto load_codes = [&](Parts& w, int i, auto is_v, int g, int& J) {
+      constexpr bool V = decltype(is_v)::value;
+      constexpr int rows = V ? L::vr_rows : L::kr_rows, units = V ? L::vr_units : L::kr_units;
+      constexpr int bytes = V ? L::vr_bytes : L::kr_bytes, kPer = rows < 32 ? 1 : rows / 32;
+      const uint8_t* scales = (V ? a.v_scales : a.k_scales) + g;
+      const int row = part_row(w, i), box_log2 = __ffs(box_rows) - 1, parts_log2 = __ffs(rows) - 1 - box_log2;
       for (int h = 0; h < units; ++h, ++J) {
         const int st = J % L::raw_slots;
-        if (J >= L::raw_slots && !wait(&sm.raw_empty[is_v][st], J / L::raw_slots - 1)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[is_v][st], 8192u);
+        if (J >= L::raw_slots && !wait(&sm.raw_empty[V][st], J / L::raw_slots - 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[V][st], 8192u);
         __syncwarp();
         if (lane >> parts_log2 == h && (lane >> w.shift) == 0)
-          load_3d<false>(sm.raw[is_v][st] + (lane - (h << parts_log2)) * box_rows * bytes, is_v ? &tm_v : &tm_k,
-                         is_v && PAIR ? 32 * rank : 0, g, row, smem_u32(&sm.raw_full[is_v][st]));
+          load_3d<false>(sm.raw[V][st] + (lane - (h << parts_log2)) * box_rows * bytes, V ? &tm_v : &tm_k,
+                         V && PAIR ? 32 * rank : 0, g, row, smem_u32(&sm.raw_full[V][st]));
+        uint32_t byte[kPer];
+        int key = first_key_of(w, i) + rows * h + lane;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int r = 32 * k + lane;
+          const int part = __shfl_sync(0xffffffffu, row, (h << parts_log2) + (r >> box_log2));
+          const bool seen = part != outside && !(V && plan::keys_hidden<SINKS>(key + 32 * k, 1, w.se, w.lo, w.hi));
+          byte[k] = 0u;
+          if (seen) byte[k] = 256u + scales[(long long)divide((uint32_t)(part + (r & (box_rows - 1))), a.by_scale) * a.G];
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          sm.scale[V][st][32 * k + lane] = byte[k] == 0u ? 0 : (uint16_t)c8::pow2_half2(c8::exp_of(byte[k] - 256u));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.raw_full[V][st]);
       }
       return true;
     };
@@ -723,7 +699,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (lane == 0) mbar_arrive(C8 ? &sm.q_raw[qb] : &sm.q_ready[qb]);
         }
         if constexpr (C8) {
-          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, 0, p.g, J);
+          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, std::false_type{}, p.g, J);
         }
         for (int i = 0; !C8 && i < n; ++i, ++J) {
           const int row = part_row(w, i), slot = J % L::slots;
@@ -758,7 +734,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
         Parts w = open_parts(kTcKeys, n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip, 0, d.seq);
         if constexpr (C8) {
-          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, 1, d.g, J);
+          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, std::true_type{}, d.g, J);
         }
         for (int i = 0; !C8 && i < n; ++i, ++J) {
           const int row = part_row(w, i), key = first_key_of(w, i) + lane * box_rows, slot = J % L::slots;
@@ -812,7 +788,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ---------------------------------------------------------- MMA issue (the first block's, in a pair)
       // Two warps, one a product, so that neither holds up the other; warp-uniform loops, one elected lane issues.
       constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
+      // Codes: operands are whole when the block's own four warps have written their parts (*_made) and, in a pair, the
+      // second block's (*_full, where that block's idle issue warps pass its *_made on: released to the cluster by a
+      // thread that has no loads in flight, which a release would wait for).
+      auto operands = [&](uint64_t* made, uint64_t* full, int phase) {
+        return C8 ? wait(made, phase) && (!PAIR || wait(full, phase)) : wait(full, phase);
+      };
       if (rank != 0) {
+        if constexpr (C8) {
+          bool ok = true;
+          int j = 0;
+          for (int x = 0; ok; ++x) {
+            if (!next_piece(x)) break;
+            const int n = sm.desc[x % kDescs].n, qb = x % kQBufs;
+            if (warp == 1) {
+              ok = wait(&sm.q_made[qb], x / kQBufs);
+              if (ok && lane == 0) arrive_leader_release<PAIR>(&sm.q_ready[qb]);
+            }
+            for (int i = 0; ok && i < n; ++i, ++j) {
+              const int slot = j % L::slots;
+              ok = wait(warp == 1 ? &sm.k_made[slot] : &sm.v_made[slot], j / L::slots);
+              if (ok && lane == 0) arrive_leader_release<PAIR>(warp == 1 ? &sm.k_full[slot] : &sm.v_full[slot]);
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+          }
+        }
       } else if (warp == 1) {
         constexpr uint32_t idesc_qk = tc::idesc_f32acc(fmt, false, L::rows, kTcKeys);
         const uint64_t dq0 = tc::sdesc_sw128(smem_u32(sm.q[0]), 16, 1024);
@@ -825,10 +826,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int n = d.n;
           const int qb = x % kQBufs;
           const uint64_t dq = dq0 + (uint64_t)(qb * (L::q_bytes >> 4));
-          ok = wait(&sm.q_ready[qb], x / kQBufs);
+          ok = operands(&sm.q_made[qb], &sm.q_ready[qb], x / kQBufs);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = wait(&sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
+            ok = operands(&sm.k_made[slot], &sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
             if (!ok) break;
             acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
@@ -855,7 +856,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (x > 0) ok = wait(&sm.o_free, x - 1);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = wait(&sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
+            ok = operands(&sm.v_made[slot], &sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
             if (!ok) break;
             acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp < 12) {
     // ------------------------------------------------------------ softmax groups
-    regs_inc<kSoftmaxRegs>();
+    regs_inc<C8 ? kSoftmaxRegsC8 : kSoftmaxRegs>();
     const int grp = (warp - 4) >> 2, qd = warp & 3;
     const int r = 32 * qd + lane;  // row == TMEM lane
     const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
@@ -903,7 +904,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ScoreMap sc = score;  // codes: with what came off the row
       if constexpr (C8) {
         lane_wait(&sm.qf_bar[x % kDescs], x / kDescs);
-        const float f = sm.qf[x % kDescs][r];
+        const float f = pow2f(sm.qf[x % kDescs][r] - 14);
         // (Masked scores are -inf before they are multiplied: not by zero, and a row this small has scores of zero.)
         sc.scale2 = MODE == 0 ? fmaxf(sc.scale2 * f, FLT_MIN) : sc.scale2 * f;
         sc.in_mul *= f;
@@ -1133,7 +1134,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------------------ output warps
     // O of each piece as soon as its last product lands: whole items leave normalised in the output's type, pieces of
     // a split one in fp32 to the workspace, where the warp that arrives last joins its 32 rows in key order.
-    regs_dec<kOutRegs>();
+    regs_dec<C8 ? kOutRegsC8 : kOutRegs>();
     const int qd = warp & 3, r = 32 * qd + lane;
     const uint32_t o_col = tmem + ((uint32_t)(32 * qd) << 16) + kOColumn;
     constexpr int kCols = 16, kChunks = D / kCols;  // columns at a time: few registers
@@ -1342,34 +1343,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         output(x);
       }
     } else {
-      Codes<D, PAIR> codes{0, 0, 0};
+      int J = 0;
       for (int x = 0;; ++x) {
         const bool more = next_piece(x);
         bool ok = more;
         if (more) {
-          const PieceDesc& d = sm.desc[x % kDescs];
           const int qb = x % kQBufs;
           ok = wait(&sm.q_raw[qb], x / kQBufs);
           if (ok) {
-            float f = 1.f;
-            if constexpr (!std::is_same<T, __half>::value) f = q_to_half<D, PAIR, S>(sm, qb, r);
-            sm.qf[x % kDescs][r] = f;
+            int E = 14;
+            if constexpr (!std::is_same<T, __half>::value) E = q_to_half<D, PAIR, S>(sm, qb, r);
+            sm.qf[x % kDescs][r] = (int8_t)E;
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&sm.qf_bar[x % kDescs]);
-              arrive_leader_release<PAIR>(&sm.q_ready[qb]);
+              mbar_arrive(&sm.q_made[qb]);
             }
-            codes.open(a, d, qd, rank);
-            for (int i = 0; ok && i < d.n && i < L::slots; ++i) ok = codes.convert(a, sm, d, i, qd, rank, wait);
           }
         }
-        if (more ? !ok : !warp_whole(&sm.abort)) break;  // the pipeline broke
-        if (x > 0) output(x - 1);
-        if (!more) break;
-        const PieceDesc& d = sm.desc[x % kDescs];
-        for (int i = L::slots; ok && i < d.n; ++i) ok = codes.convert(a, sm, d, i, qd, rank, wait);
-        if (!ok) break;
+        // The piece's first tiles (no more than there are slots), the last piece's output, the other tiles.
+        const int n = more ? sm.desc[x % kDescs].n : 0, ahead = min(n, L::slots);
+#pragma unroll 1
+        for (int i = 0; more ? ok : warp_whole(&sm.abort); ++i) {
+          if (i == ahead && x > 0) output(x - 1);
+          if (i >= n) break;
+          ok = make_operands<D, PAIR>(sm, J++, qd, wait);
+        }
+        if (!more || !ok) break;
       }
     }
   }
