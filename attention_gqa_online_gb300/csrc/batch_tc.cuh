@@ -510,12 +510,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // barrier complete its next phase and the others wait for a phase that is past.
   const unsigned long long limit = BRIEF ? a.wait_ns : kWaitLimitNs;
   auto wait = [&](uint64_t* bar, int phase) {
-    return warp_wait<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
+    if constexpr (C8 && !BRIEF)
+      return __all_sync(0xffffffffu, wait_phase_short(bar, (unsigned)(phase & 1), a.status, &sm.abort)) != 0;
+    else
+      return warp_wait<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
   };
   // Without the vote, where no answer is asked for, nothing warp-wide follows at once and a __syncwarp comes before a lane
   // arrives for the warp (17 ragged chunks with a bias, 16 heads: 223 us with votes there too, 219 this way).
   auto lane_wait = [&](uint64_t* bar, int phase) {
-    wait_phase<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
+    if constexpr (C8 && !BRIEF)
+      wait_phase_short(bar, (unsigned)(phase & 1), a.status, &sm.abort);
+    else
+      wait_phase<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
   };
   // Is there a piece x?  Its descriptor is then valid until every role has released it.  If not, there are no more or
   // the pipeline broke: the role, all lanes of it, leaves.
@@ -568,42 +574,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return row;
     };
-    // Codes of tile i of K (is_v 0) or V (1) and their rows' scales, unit by unit; J counts units.
-    auto load_codes = [&](Parts& w, int i, auto is_v, int g, int& J) {
-      constexpr bool V = decltype(is_v)::value;
-      constexpr int rows = V ? L::vr_rows : L::kr_rows, units = V ? L::vr_units : L::kr_units;
-      constexpr int bytes = V ? L::vr_bytes : L::kr_bytes, kPer = rows < 32 ? 1 : rows / 32;
-      const uint8_t* scales = (V ? a.v_scales : a.k_scales) + g;
+    // Codes of tile i of K (v 0) or V (1) and their rows' scales, unit by unit; J counts units.
+    auto load_codes = [&](Parts& w, int i, int v, int g, int& J) {
+      const int rows = v ? L::vr_rows : L::kr_rows, units = v ? L::vr_units : L::kr_units;
+      const uint8_t* scales = (v ? a.v_scales : a.k_scales) + g;
       const int row = part_row(w, i), box_log2 = __ffs(box_rows) - 1, parts_log2 = __ffs(rows) - 1 - box_log2;
+#pragma unroll 1
       for (int h = 0; h < units; ++h, ++J) {
         const int st = J % L::raw_slots;
-        if (J >= L::raw_slots && !wait(&sm.raw_empty[V][st], J / L::raw_slots - 1)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[V][st], 8192u);
+        if (J >= L::raw_slots && !wait(&sm.raw_empty[v][st], J / L::raw_slots - 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[v][st], 8192u);
         __syncwarp();
         if (lane >> parts_log2 == h && (lane >> w.shift) == 0)
-          load_3d<false>(sm.raw[V][st] + (lane - (h << parts_log2)) * box_rows * bytes, V ? &tm_v : &tm_k,
-                         V && PAIR ? 32 * rank : 0, g, row, smem_u32(&sm.raw_full[V][st]));
+          load_3d<false>(sm.raw[v][st] + (lane - (h << parts_log2)) * box_rows * (8192 / rows), v ? &tm_v : &tm_k,
+                         PAIR ? 32 * rank * v : 0, g, row, smem_u32(&sm.raw_full[v][st]));
+        constexpr int kPer = 4;  // rows of a lane, at most
         uint32_t byte[kPer];
-        int key = first_key_of(w, i) + rows * h + lane;
+        const int key = first_key_of(w, i) + rows * h + lane;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
           const int r = 32 * k + lane;
-          const int part = __shfl_sync(0xffffffffu, row, (h << parts_log2) + (r >> box_log2));
-          const bool seen = part != outside && !(V && plan::keys_hidden<SINKS>(key + 32 * k, 1, w.se, w.lo, w.hi));
+          const int part = __shfl_sync(0xffffffffu, row, ((h << parts_log2) + (r >> box_log2)) & 31);
+          const bool seen = 32 * k < rows && part != outside && !(v && plan::keys_hidden<SINKS>(key + 32 * k, 1, w.se, w.lo, w.hi));
           byte[k] = 0u;
           if (seen) byte[k] = 256u + scales[(long long)divide((uint32_t)(part + (r & (box_rows - 1))), a.by_scale) * a.G];
         }
 #pragma unroll
         for (int k = 0; k < kPer; ++k)
-          sm.scale[V][st][32 * k + lane] = byte[k] == 0u ? 0 : (uint16_t)c8::pow2_half2(c8::exp_of(byte[k] - 256u));
+          if (32 * k < rows)
+            sm.scale[v][st][32 * k + lane] = byte[k] == 0u ? 0 : (uint16_t)c8::pow2_half2(c8::exp_of(byte[k] - 256u));
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.raw_full[V][st]);
+        if (lane == 0) mbar_arrive(&sm.raw_full[v][st]);
       }
       return true;
     };
     auto barrier_of = [&](uint64_t* full) { return PAIR ? in_leader(smem_u32(full)) : smem_u32(full); };
-    if (warp == 0) {
-      // ---------------------------------------------------------- planner, Q and K producer
+    if (warp == 0 || (C8 && warp == 3)) {
+      // ---------------------------------------------------------- planner, Q and K producer (codes: V producer, too)
       if (lane == 0) {
         prefetch_tmap(&tm_k);
         if (q_box) prefetch_tmap(&tm_q);
@@ -615,91 +622,104 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // phase, would turn a late block into a fault.
       bool ok = true;
       while (ok) {
-        const bool more = walk.next(p) && warp_whole(&sm.abort);
-        // This block's rows: 128 flattened rows from first_row on.
-        const int first_row = p.b * L::rows + rank * kTcRows;
-        const int rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
-        if (more && p.t1 == p.t0) {  // rows without keys
-          for (int r = lane >> 2; r < rows; r += 8) {
-            const int f = first_row + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
-            T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * hd;
-            for (int u = lane & 3; u < hd / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          continue;
-        }
-        if (x >= kDescs) ok = wait(&sm.desc_free[x % kDescs], x / kDescs - 1);
-        if (!ok) break;
-        if (lane == 0) {
-          PieceDesc& d = sm.desc[x % kDescs];
-          d.end = !more;
-          if (more) {
-            d.whole = p.whole;
-            d.seq = p.s;
-            d.g = p.g;
-            d.slot = p.slot;
-            d.first = p.first;
-            d.last = p.last;
-            d.slot0 = p.slot0;
-            d.row0 = p.q.row0;
-            d.q_len = p.q.q_len;
-            d.len = p.q.len;
-            d.pfx = p.q.pfx;
-            d.first_row = first_row;
-            d.rows = rows;
-            d.lo_min = p.k.lo_min;
-            d.lo_max = p.k.lo_max;
-            d.hi_min = p.k.hi_min;
-            d.hi_max = p.k.hi_max;
-            d.se = p.k.se;
-            d.tile_last = plan::first_tile<SINKS>(p.k) + p.t1 - 1;
-            d.ns = p.k.ns;
-            d.skip = p.k.skip;
-            d.n = p.t1 - p.t0;
-            d.pos_min = p.q.len - p.q.q_len + plan::token_of(a, first_row);
-          }
-          mbar_arrive(&sm.desc_full[x % kDescs]);
-        }
-        __syncwarp();
-        if (!more) break;
-        // The piece's first page parts are looked up while its Q buffer falls free.
-        const int n = p.t1 - p.t0, col = FULL ? p.g * D : 0;
-        Parts w = open_parts(L::k_rows, n, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t1 - 1, p.k.ns,
-                             p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
-        // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
-        // only feeds itself, and those rows are not stored).
-        const int qb = x % kQBufs;
-        if (x >= kQBufs) ok = wait(&sm.q_free[qb], x / kQBufs - 1);
-        if (!ok) break;
-        if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
-          if (lane == 0) {
-            constexpr bool kShared = PAIR && !C8;  // both blocks' halves complete on the first one's barrier
-            uint64_t* full = C8 ? &sm.q_raw[qb] : &sm.q_ready[qb];
-            const uint32_t bar = kShared ? barrier_of(full) : smem_u32(full);
-            if (C8 || rank == 0) mbar_arrive_expect_tx(full, (unsigned)(kShared ? 2 : 1) * L::q_bytes);
-#pragma unroll
-            for (int c = 0; c < L::chunks; ++c)
-              load_3d<kShared>(sm.q[qb] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + plan::token_of(a, first_row), bar);
-          }
-          __syncwarp();
+        int n = 0, col = 0;
+        Parts w{};
+        if (C8 && warp == 3) {
+          if (!next_piece(x)) break;
         } else {
-          constexpr int kUnits = D / 8, kRowsPer = 32 / kUnits;  // units of a row over the lanes
-          const int u = lane % kUnits;
-          unsigned char* qt = sm.q[qb] + (u >> 3) * L::q_chunk;
-          const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * hd;
-          const bool inside = 8 * u < hd;  // columns past the head are zeros
-          for (int r = lane / kUnits; r < rows; r += kRowsPer) {
-            const int f = first_row + r, t = plan::token_of(a, f);
-            cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)),
-                       src + (long long)t * a.q_stride + (f - t * a.gs) * hd + (inside ? 8 * u : 0), inside ? 16u : 0u);
+          const bool more = walk.next(p) && warp_whole(&sm.abort);
+          // This block's rows: 128 flattened rows from first_row on.
+          const int first_row = p.b * L::rows + rank * kTcRows;
+          const int rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
+          if (more && p.t1 == p.t0) {  // rows without keys
+            for (int r = lane >> 2; r < rows; r += 8) {
+              const int f = first_row + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
+              T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * hd;
+              for (int u = lane & 3; u < hd / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            continue;
           }
-          cp_async_commit();
-          cp_async_wait<0>();
-          fence_async_smem();
+          if (x >= kDescs) ok = wait(&sm.desc_free[x % kDescs], x / kDescs - 1);
+          if (!ok) break;
+          if (lane == 0) {
+            PieceDesc& d = sm.desc[x % kDescs];
+            d.end = !more;
+            if (more) {
+              d.whole = p.whole;
+              d.seq = p.s;
+              d.g = p.g;
+              d.slot = p.slot;
+              d.first = p.first;
+              d.last = p.last;
+              d.slot0 = p.slot0;
+              d.row0 = p.q.row0;
+              d.q_len = p.q.q_len;
+              d.len = p.q.len;
+              d.pfx = p.q.pfx;
+              d.first_row = first_row;
+              d.rows = rows;
+              d.lo_min = p.k.lo_min;
+              d.lo_max = p.k.lo_max;
+              d.hi_min = p.k.hi_min;
+              d.hi_max = p.k.hi_max;
+              d.se = p.k.se;
+              d.tile_last = plan::first_tile<SINKS>(p.k) + p.t1 - 1;
+              d.ns = p.k.ns;
+              d.skip = p.k.skip;
+              d.n = p.t1 - p.t0;
+              d.pos_min = p.q.len - p.q.q_len + plan::token_of(a, first_row);
+            }
+            mbar_arrive(&sm.desc_full[x % kDescs]);
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(C8 ? &sm.q_raw[qb] : &sm.q_ready[qb]);
+          if (!more) break;
+          // The piece's first page parts are looked up while its Q buffer falls free.
+          n = p.t1 - p.t0;
+          col = FULL ? p.g * D : 0;
+          if constexpr (!C8) w = open_parts(L::k_rows, n, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t1 - 1, p.k.ns,
+                               p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
+          // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
+          // only feeds itself, and those rows are not stored).
+          const int qb = x % kQBufs;
+          if (x >= kQBufs) ok = wait(&sm.q_free[qb], x / kQBufs - 1);
+          if (!ok) break;
+          if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
+            if (lane == 0) {
+              constexpr bool kShared = PAIR && !C8;  // both blocks' halves complete on the first one's barrier
+              uint64_t* full = C8 ? &sm.q_raw[qb] : &sm.q_ready[qb];
+              const uint32_t bar = kShared ? barrier_of(full) : smem_u32(full);
+              if (C8 || rank == 0) mbar_arrive_expect_tx(full, (unsigned)(kShared ? 2 : 1) * L::q_bytes);
+#pragma unroll
+              for (int c = 0; c < L::chunks; ++c)
+                load_3d<kShared>(sm.q[qb] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + plan::token_of(a, first_row), bar);
+            }
+            __syncwarp();
+          } else {
+            constexpr int kUnits = D / 8, kRowsPer = 32 / kUnits;  // units of a row over the lanes
+            const int u = lane % kUnits;
+            unsigned char* qt = sm.q[qb] + (u >> 3) * L::q_chunk;
+            const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * hd;
+            const bool inside = 8 * u < hd;  // columns past the head are zeros
+            for (int r = lane / kUnits; r < rows; r += kRowsPer) {
+              const int f = first_row + r, t = plan::token_of(a, f);
+              cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)),
+                         src + (long long)t * a.q_stride + (f - t * a.gs) * hd + (inside ? 8 * u : 0), inside ? 16u : 0u);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(C8 ? &sm.q_raw[qb] : &sm.q_ready[qb]);
+          }
         }
-        if constexpr (C8) {
-          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, std::false_type{}, p.g, J);
+        if constexpr (C8) {  // one piece of code for K and V
+          const PieceDesc& d = sm.desc[x % kDescs];
+          const int v = warp == 3 ? 1 : 0;
+          w = open_parts(v ? kTcKeys : L::k_rows, d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip,
+                         PAIR && !v ? rank * L::k_rows : 0, d.seq);
+#pragma unroll 1
+          for (int i = 0; ok && i < d.n; ++i) ok = load_codes(w, i, v, d.g, J);
+          if (v && ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
         }
         for (int i = 0; !C8 && i < n; ++i, ++J) {
           const int row = part_row(w, i), slot = J % L::slots;
@@ -716,7 +736,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         ++x;
       }
-      if (lane == 0) {
+      if (C8 && warp == 3) {
+        if (lane == 0) sm.issued[1] = J;
+      } else if (lane == 0) {
         sm.issued[0] = J;
         sm.issued[2] = PAIR || q_box ? x : 0;
       }
@@ -733,9 +755,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const PieceDesc& d = sm.desc[x % kDescs];
         const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
         Parts w = open_parts(kTcKeys, n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip, 0, d.seq);
-        if constexpr (C8) {
-          for (int i = 0; ok && i < n; ++i) ok = load_codes(w, i, std::true_type{}, d.g, J);
-        }
         for (int i = 0; !C8 && i < n; ++i, ++J) {
           const int row = part_row(w, i), key = first_key_of(w, i) + lane * box_rows, slot = J % L::slots;
           if (J >= L::slots) ok = wait(&sm.v_empty[slot], J / L::slots - 1);

@@ -30,6 +30,24 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, unsig
   }
 }
 
+// As wait_phase, in half the code: for kernels whose roles together outgrow the instruction cache.
+__device__ __forceinline__ bool wait_phase_short(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag) {
+  unsigned t0 = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag != 0) return false;
+    unsigned now;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));  // (wraps after four seconds)
+    if (t0 == 0) t0 = now | 1u;
+    if (now - t0 > (unsigned)kWaitLimitNs && now != t0 - 1u) {
+      record_status(status, ATTN_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // The same for a warp, all of whose lanes call it together.  The lanes see a
 // phase complete, or the block's abort flag set, at different times, so they
 // meet again here, with one answer for all, before any of them arrives
