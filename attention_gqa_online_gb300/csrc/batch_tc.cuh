@@ -148,9 +148,9 @@ struct __align__(1024) TcSmem {
   unsigned char k[L::slots][L::k_bytes];
   unsigned char v[L::slots][L::v_bytes];
   alignas(128) unsigned char raw[2][L::raw_slots][C8 ? 8192 : 128];  // [K, V]
-  uint16_t scale[2][L::raw_slots][C8 ? (D == 64 || PAIR ? 128 : 64) : 1];  // of each row of a unit, fp16; 0: out of sight
+  alignas(8) uint16_t scale[2][L::raw_slots][C8 ? (D == 64 || PAIR ? 128 : 64) : 1];  // of each row of a unit, fp16; 0: out of sight
   uint64_t raw_full[2][kMaxRaw], raw_empty[2][kMaxRaw], q_raw[2], qf_bar[kDescs];  // codes
-  uint64_t k_made[kMaxSlots], v_made[kMaxSlots], q_made[2];                        // codes: operands written by this block
+  uint64_t k_made[kMaxSlots], v_made[kMaxSlots], q_made[2];  // codes: operands written by the pair's second block
   uint64_t k_full[kMaxSlots], k_empty[kMaxSlots], v_full[kMaxSlots], v_empty[kMaxSlots];
   uint64_t q_ready[2], q_free[2];
   uint64_t desc_full[kDescs], desc_free[kDescs];
@@ -373,7 +373,8 @@ __device__ __forceinline__ int q_to_half(S& sm, int qb, int r) {
 // a warp alone runs at three or four clocks an instruction, and all roles of the block share the instruction cache (both
 // unrolled apart, and scales looked up here: 2 chunks of 512 behind 16k to 32k 706 us).
 template <int D, bool PAIR, typename S, typename W>
-__device__ __forceinline__ bool make_operands(S& sm, int J, int w, W& wait) {
+__device__ __forceinline__ bool make_operands(S& sm, uint64_t* k_made, uint64_t* v_made, int J, int w,
+                                              W& wait) {
   using L = TcLayout<D, PAIR, true>;
   const int slot = J % L::slots, lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -419,7 +420,7 @@ __device__ __forceinline__ bool make_operands(S& sm, int J, int w, W& wait) {
     }
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(t ? &sm.v_made[slot] : &sm.k_made[slot]);
+    if (lane == 0) mbar_arrive(t ? &v_made[slot] : &k_made[slot]);
   }
   return true;
 }
@@ -450,10 +451,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   allow_dependent_launch();
   if (warp == 0) {
+    constexpr int kMakers = !C8 ? 1 : PAIR ? 5 : 4;  // arrivals that make an operand whole: four warps, the second block
     for (int i = lane; i < kMaxSlots; i += 32) {
-      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_full[i], kMakers);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_full[i], kMakers);
       mbar_init(&sm.v_empty[i], 1);
       if (C8) {
         mbar_init(&sm.k_made[i], 4);
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (C8 && lane < kDescs) mbar_init(&sm.qf_bar[lane], 4);
     if (lane < 2) {
-      mbar_init(&sm.q_ready[lane], 1);
+      mbar_init(&sm.q_ready[lane], kMakers);
       if (C8) mbar_init(&sm.q_raw[lane], 1);
       if (C8) mbar_init(&sm.q_made[lane], 4);
       mbar_init(&sm.q_free[lane], 1);
@@ -574,37 +576,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return row;
     };
-    // Codes of tile i of K (v 0) or V (1) and their rows' scales, unit by unit; J counts units.
-    auto load_codes = [&](Parts& w, int i, int v, int g, int& J) {
-      const int rows = v ? L::vr_rows : L::kr_rows, units = v ? L::vr_units : L::kr_units;
+    // Codes of a piece's tiles of K (v 0) or V (1) and their rows' scales, unit by unit; J counts units.  A lane looks up
+    // the scales of four rows of a unit, one tile ahead (a trip to L2); four rows of one page share one where the blocks of
+    // the scales are whole fours.
+    auto load_codes = [&](Parts& w, int v, int g, int& J) {
+      const int rows = v ? L::vr_rows : L::kr_rows, r = 4 * lane;
+      constexpr int kUnits = L::vr_units;  // (of K, too, but for a pair's)
+      const int units = v ? L::vr_units : L::kr_units;
       const uint8_t* scales = (v ? a.v_scales : a.k_scales) + g;
-      const int row = part_row(w, i), box_log2 = __ffs(box_rows) - 1, parts_log2 = __ffs(rows) - 1 - box_log2;
+      const int box_log2 = __ffs(box_rows) - 1, parts_log2 = __ffs(rows) - 1 - box_log2;
+      const bool quad = (a.scale_rows & 3) == 0;
+      auto look = [&](int row, int h) {  // bytes of the lane's four rows
+        const int part = __shfl_sync(0xffffffffu, row, ((h << parts_log2) + (r >> box_log2)) & 31);
+        if (r >= rows || part == outside) return 0u;
+        const uint32_t at = (uint32_t)(part + (r & (box_rows - 1)));
+        if (quad) return 0x01010101u * scales[(long long)divide(at, a.by_scale) * a.G];
+        uint32_t b = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b |= (uint32_t)scales[(long long)divide(at + k, a.by_scale) * a.G] << (8 * k);
+        return b;
+      };
+      int row = part_row(w, 0);
+      uint32_t bytes[kUnits];
+#pragma unroll
+      for (int h = 0; h < kUnits; ++h) bytes[h] = look(row, h);
 #pragma unroll 1
-      for (int h = 0; h < units; ++h, ++J) {
-        const int st = J % L::raw_slots;
-        if (J >= L::raw_slots && !wait(&sm.raw_empty[v][st], J / L::raw_slots - 1)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[v][st], 8192u);
-        __syncwarp();
-        if (lane >> parts_log2 == h && (lane >> w.shift) == 0)
-          load_3d<false>(sm.raw[v][st] + (lane - (h << parts_log2)) * box_rows * (8192 / rows), v ? &tm_v : &tm_k,
-                         PAIR ? 32 * rank * v : 0, g, row, smem_u32(&sm.raw_full[v][st]));
-        constexpr int kPer = 4;  // rows of a lane, at most
-        uint32_t byte[kPer];
-        const int key = first_key_of(w, i) + rows * h + lane;
+      for (int i = 0; i < w.n; ++i) {
+        const int key0 = first_key_of(w, i);
+        const bool cut = v && !plan::keys_inside<SINKS>(key0, kTcKeys, w.se, w.lo, w.hi);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int r = 32 * k + lane;
-          const int part = __shfl_sync(0xffffffffu, row, ((h << parts_log2) + (r >> box_log2)) & 31);
-          const bool seen = 32 * k < rows && part != outside && !(v && plan::keys_hidden<SINKS>(key + 32 * k, 1, w.se, w.lo, w.hi));
-          byte[k] = 0u;
-          if (seen) byte[k] = 256u + scales[(long long)divide((uint32_t)(part + (r & (box_rows - 1))), a.by_scale) * a.G];
+        for (int h = 0; h < kUnits; ++h) {
+          if (h >= units) break;
+          const int st = J % L::raw_slots;
+          if (J >= L::raw_slots && !wait(&sm.raw_empty[v][st], J / L::raw_slots - 1)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.raw_full[v][st], 8192u);
+          __syncwarp();
+          if (lane >> parts_log2 == h && (lane >> w.shift) == 0)
+            load_3d<false>(sm.raw[v][st] + (lane - (h << parts_log2)) * box_rows * (8192 / rows), v ? &tm_v : &tm_k,
+                           PAIR ? 32 * rank * v : 0, g, row, smem_u32(&sm.raw_full[v][st]));
+          if (r < rows) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[k] = (uint32_t)(c8::exp_of((bytes[h] >> (8 * k)) & 0xffu) + 15) << 10;
+              if (cut && plan::keys_hidden<SINKS>(key0 + rows * h + r + k, 1, w.se, w.lo, w.hi)) x[k] = 0u;
+            }
+            *reinterpret_cast<uint2*>(&sm.scale[v][st][r]) = make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.raw_full[v][st]);
+          ++J;
         }
+        if (i + 1 < w.n) {
+          row = part_row(w, i + 1);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (32 * k < rows)
-            sm.scale[v][st][32 * k + lane] = byte[k] == 0u ? 0 : (uint16_t)c8::pow2_half2(c8::exp_of(byte[k] - 256u));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.raw_full[v][st]);
+          for (int h = 0; h < kUnits; ++h) bytes[h] = look(row, h);
+        }
       }
       return true;
     };
@@ -717,8 +744,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int v = warp == 3 ? 1 : 0;
           w = open_parts(v ? kTcKeys : L::k_rows, d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip,
                          PAIR && !v ? rank * L::k_rows : 0, d.seq);
-#pragma unroll 1
-          for (int i = 0; ok && i < d.n; ++i) ok = load_codes(w, i, v, d.g, J);
+          ok = load_codes(w, v, d.g, J);
           if (v && ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
         }
         for (int i = 0; !C8 && i < n; ++i, ++J) {
@@ -807,12 +833,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // ---------------------------------------------------------- MMA issue (the first block's, in a pair)
       // Two warps, one a product, so that neither holds up the other; warp-uniform loops, one elected lane issues.
       constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
-      // Codes: operands are whole when the block's own four warps have written their parts (*_made) and, in a pair, the
-      // second block's (*_full, where that block's idle issue warps pass its *_made on: released to the cluster by a
-      // thread that has no loads in flight, which a release would wait for).
-      auto operands = [&](uint64_t* made, uint64_t* full, int phase) {
-        return C8 ? wait(made, phase) && (!PAIR || wait(full, phase)) : wait(full, phase);
-      };
+      // Codes: operands are whole when the first block's four warps have written their parts and, in a pair, the second
+      // block's, whose idle issue warps pass that on (*_made): released to the cluster by a thread that has no loads in
+      // flight, which a release would wait for.
       if (rank != 0) {
         if constexpr (C8) {
           bool ok = true;
@@ -845,10 +868,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int n = d.n;
           const int qb = x % kQBufs;
           const uint64_t dq = dq0 + (uint64_t)(qb * (L::q_bytes >> 4));
-          ok = operands(&sm.q_made[qb], &sm.q_ready[qb], x / kQBufs);
+          ok = wait(&sm.q_ready[qb], x / kQBufs);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = operands(&sm.k_made[slot], &sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
+            ok = wait(&sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
             if (!ok) break;
             acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
@@ -875,7 +898,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (x > 0) ok = wait(&sm.o_free, x - 1);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = operands(&sm.v_made[slot], &sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
+            ok = wait(&sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
             if (!ok) break;
             acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
@@ -1377,7 +1400,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&sm.qf_bar[x % kDescs]);
-              mbar_arrive(&sm.q_made[qb]);
+              mbar_arrive(rank == 0 ? &sm.q_ready[qb] : &sm.q_made[qb]);
             }
           }
         }
@@ -1387,7 +1410,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; more ? ok : warp_whole(&sm.abort); ++i) {
           if (i == ahead && x > 0) output(x - 1);
           if (i >= n) break;
-          ok = make_operands<D, PAIR>(sm, J++, qd, wait);
+          ok = make_operands<D, PAIR>(sm, rank == 0 ? sm.k_full : sm.k_made, rank == 0 ? sm.v_full : sm.v_made, J++, qd,
+                                       wait);
         }
         if (!more || !ok) break;
       }
