@@ -242,11 +242,6 @@ __device__ __forceinline__ void arrive_leader_release(uint64_t* bar) {
   else
     mbar_arrive(bar);
 }
-// After a wait on a barrier that such arrivals complete: acquires what they released.
-template <bool PAIR>
-__device__ __forceinline__ void acquire_pair() {
-  if (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
-}
 // Tensor copies into this block's shared memory that complete on `bar` (a
 // barrier of the first block, by its cluster address, when PAIR).
 template <bool PAIR>
@@ -835,7 +830,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
       // Codes: operands are whole when the first block's four warps have written their parts and, in a pair, the second
       // block's, whose idle issue warps pass that on (*_made): released to the cluster by a thread that has no loads in
-      // flight, which a release would wait for.
+      // flight, which a release would wait for.  (The issuing thread reads none of it: the tensor cores do, past L1, after
+      // tcgen05's own fence; an acquire for the cluster would only invalidate L1: 470 us for 444.)
       if (rank != 0) {
         if constexpr (C8) {
           bool ok = true;
@@ -873,7 +869,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int slot = j % L::slots, b = j & 1;
             ok = wait(&sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
             if (!ok) break;
-            acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
             const uint64_t dk = dk0 + (uint64_t)(slot * (L::k_bytes >> 4));
 #pragma unroll
@@ -900,7 +895,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int slot = j % L::slots, b = j & 1;
             ok = wait(&sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
             if (!ok) break;
-            acquire_pair<PAIR && C8>();
             tc::fence_after_sync();
             const uint64_t dv = dv0 + (uint64_t)(slot * (L::v_bytes >> 4));
             constexpr uint64_t st = (16 * 128) >> 4;  // one K step: 16 key rows of 128 bytes
