@@ -5,7 +5,7 @@
 // Append.  A scale belongs to scale_rows positions of a kv head, so whoever
 // rounds one of them needs the largest magnitude of all.  A team of threads takes
 // one block of positions and one kv head of K or V: it reads the block's new rows
-// (up to two a thread stay in registers as fp32, more are read again), finds the
+// (one a thread stays in registers as fp32, more are read again), finds the
 // largest magnitude and with it the scale, and stores the codes.  The first
 // block of a sequence may hold older rows; they count by the scale that they have,
 // and where the new scale is larger their codes are multiplied and rounded again.
@@ -28,84 +28,123 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kKeep = 2;  // rows of a thread that stay in registers between the maximum and the codes
+constexpr int kKeep = 1;  // rows of a thread that stay in registers between the maximum and the codes
 
-// A row of a head in a lane's registers: 16 columns of a unit, or (scalar) four.
-template <bool VEC>
+// A row of a head in a lane's registers: the pairs of a unit, or (scalar) four columns in a.
+template <bool INTER, bool VEC>
 struct Held {
-  float v[VEC ? 16 : 4];
+  static constexpr int P = VEC ? norm::Unit<INTER>::P : 4;
+  float a[P], b[VEC ? P : 1];
 };
 
-// The row x of a head (its first column), normed and turned.  `mask`: the lanes
-// of the head.
+// What a lane needs of a tensor's rows whatever the row.
+template <bool INTER, bool VEC>
+struct Head {
+  norm::Unit<INTER> u;
+  const void* weight;  // nullptr: not normed
+  bool turn;
+  int lane;       // of the head
+  unsigned mask;  // the head's lanes
+  __device__ __forceinline__ Head(const Append8Args& a, const void* w, int R_geo, bool t)
+      : u(threadIdx.x & (a.lanes - 1), a.D, R_geo), weight(w), turn(t), lane(threadIdx.x & (a.lanes - 1)),
+        mask(a.lanes == 32 ? 0xffffffffu : ((1u << a.lanes) - 1u) << (threadIdx.x & 31 & ~(a.lanes - 1))) {}
+};
+
+// The row x of a head (its first column), normed and turned.
 template <typename TI, bool INTER, bool VEC>
-__device__ __forceinline__ void load_row(const Append8Args& a, const TI* x, uint32_t pos, const norm::Unit<INTER>& u,
-                                         const void* weight, bool turn, int lane, unsigned mask, Held<VEC>& out) {
+__device__ __forceinline__ void load_row(const Append8Args& a, const TI* x, uint32_t pos, const Head<INTER, VEC>& hd,
+                                         Held<INTER, VEC>& out) {
   const float* tab = a.table + (long long)pos * a.R;
   const float inv_d = 1.f / (float)a.D;
   if constexpr (VEC) {
-    norm::load_unit(x, u, out.v);
-    if (weight != nullptr) {
-      float sum = 0.f, w[16];
+    constexpr int P = Held<INTER, VEC>::P;
+    norm::Raw<TI, INTER> raw;
+    norm::load_raw(x, hd.u, raw);
+    norm::unpack(raw, out.a, out.b);
+    if (hd.weight != nullptr) {
+      float wa[P], wb[P];
+      norm::load_weight(hd.weight, a.w_dtype, hd.u, wa, wb);
+      const float rms = rsqrtf(fmaf(norm::head_sum(norm::squares(hd.u, out.a, out.b), a.lanes, hd.mask), inv_d, a.eps));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum = fmaf(out.v[i], out.v[i], sum);
-      norm::load_weight(weight, a.w_dtype, u, w);
-      const float rms = rsqrtf(fmaf(norm::head_sum(sum, a.lanes, mask), inv_d, a.eps));
-#pragma unroll
-      for (int i = 0; i < 16; ++i) out.v[i] *= rms * w[i];
+      for (int i = 0; i < P; ++i) {
+        out.a[i] *= rms * wa[i];
+        out.b[i] *= rms * wb[i];
+      }
     }
-    if (turn) {
-      float cs[16];
-      norm::load_turn(tab, a.R, u, true, cs);
-      norm::turn_unit<INTER, 1>(out.v, cs, u, false);
+    if (hd.turn) {
+      float c[P], s[P];
+      norm::load_turn(tab, a.R, hd.u, true, c, s);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const float va = out.a[i], vb = out.b[i];
+        out.a[i] = va * c[i] - vb * s[i];
+        out.b[i] = vb * c[i] + va * s[i];
+      }
+    }
+    if (!hd.u.any) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) out.a[i] = 0.f;
+    }
+    if (!hd.u.both) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) out.b[i] = 0.f;
     }
   } else {
     float rms = 1.f;
-    if (weight != nullptr) {
+    if (hd.weight != nullptr) {
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float v = lane + 32 * j < a.D ? rot::to_f32(x[lane + 32 * j]) : 0.f;
+        const float v = hd.lane + 32 * j < a.D ? rot::to_f32(x[hd.lane + 32 * j]) : 0.f;
         sum = fmaf(v, v, sum);
       }
-      rms = rsqrtf(fmaf(norm::head_sum(sum, 32, mask), inv_d, a.eps));
+      rms = rsqrtf(fmaf(norm::head_sum(sum, 32, hd.mask), inv_d, a.eps));
     }
     auto z = [&](int d) {
       const float v = rot::to_f32(x[d]);
-      return weight != nullptr ? v * (rms * norm::weight_at(weight, a.w_dtype, d)) : v;
+      return hd.weight != nullptr ? v * (rms * norm::weight_at(hd.weight, a.w_dtype, d)) : v;
     };
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int d = lane + 32 * j;
-      out.v[j] = 0.f;
+      const int d = hd.lane + 32 * j;
+      out.a[j] = 0.f;
       if (d < a.D)
-        out.v[j] = turn ? norm::turned_column<1>(norm::column_of<INTER>(d, a.R), tab, a.R, true, z) : z(d);
+        out.a[j] = hd.turn ? norm::turned_column<1>(norm::column_of<INTER>(d, a.R), tab, a.R, true, z) : z(d);
     }
   }
 }
 
 template <bool INTER, bool VEC>
-__device__ __forceinline__ float held_max(const Held<VEC>& h) {
-  float m = 0.f;
+__device__ __forceinline__ float held_max(const Held<INTER, VEC>& h) {
+  float m = 0.f;  // (a NaN leaves it)
 #pragma unroll
-  for (int i = 0; i < (VEC ? 16 : 4); ++i) m = fmaxf(m, fabsf(h.v[i]));  // (a NaN leaves m)
+  for (int i = 0; i < Held<INTER, VEC>::P; ++i) {
+    m = fmaxf(m, fabsf(h.a[i]));
+    if constexpr (VEC) m = fmaxf(m, fabsf(h.b[i]));
+  }
   return m;
 }
 template <bool INTER, bool VEC>
-__device__ __forceinline__ void store_codes(const Held<VEC>& h, float mul, uint8_t* dst, const norm::Unit<INTER>& u,
-                                            int lane, int D) {
+__device__ __forceinline__ void store_codes(const Held<INTER, VEC>& h, float mul, uint8_t* dst, const Head<INTER, VEC>& hd,
+                                            int D) {
   if constexpr (VEC) {
-    auto eight = [&](int i, int c) {
-      *reinterpret_cast<uint2*>(dst + c) =
-          make_uint2(c8::from_float4(h.v[i] * mul, h.v[i + 1] * mul, h.v[i + 2] * mul, h.v[i + 3] * mul),
-                     c8::from_float4(h.v[i + 4] * mul, h.v[i + 5] * mul, h.v[i + 6] * mul, h.v[i + 7] * mul));
+    float v[8];
+    auto eight = [&](int c) {
+      *reinterpret_cast<uint2*>(dst + c) = make_uint2(c8::from_float4(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul),
+                                                      c8::from_float4(v[4] * mul, v[5] * mul, v[6] * mul, v[7] * mul));
     };
-    if (u.any) eight(0, u.c0);
-    if (u.pair) eight(8, u.c1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = INTER ? (i & 1 ? h.b[i / 2] : h.a[i / 2]) : h.a[i % Held<INTER, VEC>::P];
+    if (hd.u.any) eight(hd.u.c0);
+    if constexpr (!INTER) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = h.b[i];
+      if (hd.u.both) eight(hd.u.c1);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < D) dst[lane + 32 * j] = (uint8_t)c8::from_float2(h.v[j] * mul, 0.f);
+      if (hd.lane + 32 * j < D) dst[hd.lane + 32 * j] = (uint8_t)c8::from_float2(h.a[j] * mul, 0.f);
   }
 }
 
@@ -135,28 +174,24 @@ struct Team {
 template <typename TI, bool INTER, bool VEC>
 __device__ __forceinline__ void write_block(const Append8Args& a, const Team& t, const TI* src, long long stride,
                                             uint8_t* pages, uint8_t* scales, int h, long long row0, int m,
-                                            uint32_t pos0, long long slot0, int held, const void* weight, int R_geo,
-                                            bool turn) {
-  const int lane = threadIdx.x & (a.lanes - 1);
-  const unsigned mask = a.lanes == 32 ? 0xffffffffu : ((1u << a.lanes) - 1u) << (threadIdx.x & 31 & ~(a.lanes - 1));
-  const norm::Unit<INTER> u(lane, a.D, R_geo);
+                                            uint32_t pos0, long long slot0, int held, const Head<INTER, VEC>& hd) {
   uint8_t* scale = scales + (long long)divide((uint32_t)slot0, a.by_scale) * a.G + h;
   const int e0 = held > 0 ? c8::exp_of(*scale) : c8::kMinExp;
   const TI* x = src + row0 * stride + (long long)h * a.D;
   uint8_t* dst = pages + slot0 * a.kv_dim + (long long)h * a.D;
-  Held<VEC> kept[kKeep];
+  Held<INTER, VEC> kept[kKeep];
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) {
     const int r = t.row + k * t.rows;
     if (r < m) {
-      load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, u, weight, turn, lane, mask, kept[k]);
+      load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, hd, kept[k]);
       amax = fmaxf(amax, held_max<INTER, VEC>(kept[k]));
     }
   }
   for (int r = t.row + kKeep * t.rows; r < m; r += t.rows) {
-    Held<VEC> v;
-    load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, u, weight, turn, lane, mask, v);
+    Held<INTER, VEC> v;
+    load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, hd, v);
     amax = fmaxf(amax, held_max<INTER, VEC>(v));
   }
   const int e = ::max(e0, c8::exp_for(t.max(amax)));
@@ -176,12 +211,12 @@ __device__ __forceinline__ void write_block(const Append8Args& a, const Team& t,
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) {
     const int r = t.row + k * t.rows;
-    if (r < m) store_codes<INTER, VEC>(kept[k], mul, dst + (long long)r * a.kv_dim, u, lane, a.D);
+    if (r < m) store_codes<INTER, VEC>(kept[k], mul, dst + (long long)r * a.kv_dim, hd, a.D);
   }
   for (int r = t.row + kKeep * t.rows; r < m; r += t.rows) {
-    Held<VEC> v;
-    load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, u, weight, turn, lane, mask, v);
-    store_codes<INTER, VEC>(v, mul, dst + (long long)r * a.kv_dim, u, lane, a.D);
+    Held<INTER, VEC> v;
+    load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, hd, v);
+    store_codes<INTER, VEC>(v, mul, dst + (long long)r * a.kv_dim, hd, a.D);
   }
 }
 
@@ -215,27 +250,26 @@ __device__ __forceinline__ void append_q(const Append8Args& a, int block) {
   if (pos < 0 || pos >= (long long)a.page_rows * a.max_blocks || (a.R > 0 && pos >= (long long)a.table_rows) ||
       a.block_table[(long long)s * a.max_blocks + divide((uint32_t)pos, a.by_page)] >= (uint32_t)a.num_pages)
     return;  // (recorded by the row's keys)
-  const int at_once = 32 / a.lanes, sub = lane / a.lanes, in = lane & (a.lanes - 1);
-  const unsigned mask = a.lanes == 32 ? 0xffffffffu : ((1u << a.lanes) - 1u) << (lane & ~(a.lanes - 1));
-  const norm::Unit<INTER> u(in, a.D, a.R > 0 ? a.R : a.D);
+  const int at_once = 32 / a.lanes, sub = lane / a.lanes;
+  const Head<INTER, VEC> hd(a, a.q_weight, a.R > 0 ? a.R : a.D, a.R > 0);
   const TI* x = static_cast<const TI*>(a.q) + row * a.q_stride;
   TQ* y = static_cast<TQ*>(a.q_out) + row * a.q_out_stride;
   for (int h = split * at_once + sub; h < a.H; h += at_once * a.q_splits) {
-    Held<VEC> v;
-    load_row<TI, INTER, VEC>(a, x + (long long)h * a.D, (uint32_t)pos, u, a.q_weight, a.R > 0, in, mask, v);
-    __syncwarp(mask);  // (scalar form: the head's lanes have read it; y may be x)
+    Held<INTER, VEC> v;
+    load_row<TI, INTER, VEC>(a, x + (long long)h * a.D, (uint32_t)pos, hd, v);
+    __syncwarp(hd.mask);  // (scalar form: the head's lanes have read it; y may be x)
     if constexpr (VEC) {
-      norm::store_unit(y + (long long)h * a.D, u, v.v);
+      norm::store_unit(y + (long long)h * a.D, hd.u, v.a, v.b);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (in + 32 * j < a.D) y[(long long)h * a.D + in + 32 * j] = rot::from_f32<TQ>(v.v[j]);
+        if (hd.lane + 32 * j < a.D) y[(long long)h * a.D + hd.lane + 32 * j] = rot::from_f32<TQ>(v.a[j]);
     }
   }
 }
 
 template <typename TI, typename TQ, bool INTER, bool VEC>
-__global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) {
+__global__ void __launch_bounds__(kThreads, 3) append8_kernel(const Append8Args a) {
   __shared__ float red[kWarps];
   if (blockIdx.x >= (unsigned)a.kv_blocks) {
     append_q<TI, TQ, INTER, VEC>(a, blockIdx.x - a.kv_blocks);
@@ -297,10 +331,11 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) 
       const int held = in_block;
       if (is_v)
         write_block<TI, false, VEC>(a, t, static_cast<const TI*>(a.v), a.v_stride, a.v_pages, a.v_scales, h, i, take,
-                                    (uint32_t)pos, slot, held, nullptr, a.D, false);
+                                    (uint32_t)pos, slot, held, Head<false, VEC>(a, nullptr, a.D, false));
       else
         write_block<TI, INTER, VEC>(a, t, static_cast<const TI*>(a.k), a.k_stride, a.k_pages, a.k_scales, h, i, take,
-                                    (uint32_t)pos, slot, held, a.k_weight, a.R > 0 ? a.R : a.D, a.R > 0);
+                                    (uint32_t)pos, slot, held,
+                                    Head<INTER, VEC>(a, a.k_weight, a.R > 0 ? a.R : a.D, a.R > 0));
     }
     i += m;
   }
@@ -408,7 +443,8 @@ int launch_append8(Append8Args a, int dtype, int q_dtype, int sm_count, cudaStre
   if (a.R == 0) a.interleaved = false;
   const int R_geo = a.R > 0 ? a.R : a.D;
   const bool vec = rot::vec_sizes(a.D, R_geo, a.interleaved) && aligned(a.q, 16) && aligned(a.q_out, 16) &&
-                   aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.table, 16) && a.q_stride % 8 == 0 &&
+                   aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.table, 16) && aligned(a.q_weight, 16) &&
+                   aligned(a.k_weight, 16) && a.q_stride % 8 == 0 &&
                    a.q_out_stride % 8 == 0 && a.k_stride % 8 == 0 && a.v_stride % 8 == 0;
   a.lanes = vec ? norm::head_lanes(a.D, R_geo, a.interleaved) : 32;
   // A team's rows at once: as many as its block has, by the batch's average; the rest of a block follows in turns.

@@ -9,7 +9,7 @@
 // the passes would save it nothing, as x is read for xh in any case.
 //
 // A warp takes a row of Q or of K (blocks are divided between the two by their
-// heads) and walks its heads, 32 / lanes at a time, two steps' loads in flight,
+// heads) and walks its heads, 32 / lanes at a time, the next step's loads in flight,
 // with the row's cosines and sines and the weights in registers.  Where rows are
 // few, several warps share a row's heads.  dw: each lane sums its columns over all
 // its rows and heads in fp32; a block's lanes join in shared memory, blocks in a
@@ -49,83 +49,133 @@ __device__ __forceinline__ bool position_of(const NormArgs& a, uint32_t row, uin
 }
 
 template <typename T, bool INTER, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads) qk_norm_vec_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs a) {
+  using U = norm::Unit<INTER>;
+  constexpr int P = U::P;
   const bool is_k = blockIdx.x >= (unsigned)a.q_blocks;
   const NormTensor& t = is_k ? a.k : a.q;
   const int block = is_k ? blockIdx.x - a.q_blocks : blockIdx.x, blocks = is_k ? gridDim.x - a.q_blocks : a.q_blocks;
   const Rows<T> r = rows_of<T>(t);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lanes = a.lanes;
   const int sub = lane / lanes, at_once = 32 / lanes;  // heads of a warp at once
-  const norm::Unit<INTER> u(lane & (lanes - 1), a.D, a.R);
-  float w[16], dw[16];
-  norm::load_weight(t.weight, a.w_dtype, u, w);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+  const U u(lane & (lanes - 1), a.D, a.R);
   const long long tasks = (long long)a.rows * t.splits;
   const float inv_d = 1.f / (float)a.D;
+  const int step = at_once * t.splits, last = t.heads - 1;
+  float wa[P], wb[P], dwa[P], dwb[P];
+  norm::load_weight(t.weight, a.w_dtype, u, wa, wb);
+  if constexpr (BACKWARD) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) dwa[i] = dwb[i] = 0.f;
+  }
   for (long long task = (long long)block * kWarps + warp; task < tasks; task += (long long)blocks * kWarps) {
     const uint32_t row = t.splits == 1 ? (uint32_t)task : (uint32_t)(task / t.splits);
-    const int split = t.splits == 1 ? 0 : (int)(task - (long long)row * t.splits);
+    const int h0 = (t.splits == 1 ? 0 : (int)(task - (long long)row * t.splits)) * at_once;
+    const T* x = r.x + (long long)row * r.xs;
+    const T* dy = BACKWARD ? r.dy + (long long)row * r.ds : nullptr;
+    T* y = r.y + (long long)row * r.ys;
+    // The next head's loads are in flight while one is computed.
+    norm::Raw<T, INTER> x_ahead, d_ahead;
+    auto look = [&](int h) {
+      const int at = min(h + sub, last) * a.D;
+      norm::load_raw(x + at, u, x_ahead);
+      if constexpr (BACKWARD) norm::load_raw(dy + at, u, d_ahead);
+    };
+    look(h0);
     uint32_t p;
     const bool ok = position_of(a, row, &p);
-    float cs[16];
-    norm::load_turn(a.table + (long long)p * a.R, a.R, u, ok, cs);
-    const T* x = r.x + (long long)row * r.xs;
-    T* y = r.y + (long long)row * r.ys;
-    const T* dy = BACKWARD ? r.dy + (long long)row * r.ds : nullptr;
-    constexpr int kAhead = 2;  // heads of a lane whose loads are in flight
-    const int step = at_once * t.splits;
-    for (int h0 = split * at_once; h0 < t.heads; h0 += kAhead * step) {
-      float v[kAhead][16], g[BACKWARD ? kAhead : 1][16];
+    float c[P], s[P];
+    norm::load_turn(a.table + (long long)p * a.R, a.R, u, ok, c, s);
+    const bool zero = u.turned && !ok;
+    // Forward: y_a = r (a w_a c - b w_b s), y_b = r (b w_b c + a w_a s).
+    float ac[P], bs[P], bc[P], as[P];
+    if constexpr (!BACKWARD) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int h = min(h0 + k * step + sub, t.heads - 1);
-        norm::load_unit(x + (long long)h * a.D, u, v[k]);
-        if constexpr (BACKWARD) norm::load_unit(dy + (long long)h * a.D, u, g[k]);
+      for (int i = 0; i < P; ++i) {
+        ac[i] = wa[i] * c[i];
+        bs[i] = -wb[i] * s[i];
+        bc[i] = wb[i] * c[i];
+        as[i] = wa[i] * s[i];
       }
+    }
+    for (int h = h0; h <= last; h += step) {
+      float va[P], vb[P];
+      norm::unpack(x_ahead, va, vb);
+      norm::Raw<T, INTER> d_now;
+      if constexpr (BACKWARD) d_now = d_ahead;
+      if (h + step <= last) look(h + step);
+      const bool mine = h + sub <= last;
+      T* to = y + (h + sub) * a.D;
+      const float rms = rsqrtf(fmaf(norm::head_sum(norm::squares(u, va, vb), lanes, 0xffffffffu), inv_d, a.eps));
+      if constexpr (!BACKWARD) {
+        float ya[P], yb[P];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (h0 + k * step >= t.heads) break;  // (the same for all lanes)
-        const int h = h0 + k * step + sub;
-        const bool mine = h < t.heads;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum = fmaf(v[k][i], v[k][i], sum);
-        sum = norm::head_sum(sum, lanes, 0xffffffffu);
-        const float rms = rsqrtf(fmaf(sum, inv_d, a.eps));
-        if constexpr (BACKWARD) {
-          norm::turn_unit<INTER, -1>(g[k], cs, u, !ok);
-          float dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[k][i] *= rms;  // xh
-            if (mine) dw[i] = fmaf(g[k][i], v[k][i], dw[i]);
-            g[k][i] *= w[i];
-            dot = fmaf(g[k][i], v[k][i], dot);
-          }
-          dot = norm::head_sum(dot, lanes, 0xffffffffu) * inv_d;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[k][i] = rms * (g[k][i] - v[k][i] * dot);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[k][i] *= rms * w[i];
-          norm::turn_unit<INTER, 1>(v[k], cs, u, !ok);
+        for (int i = 0; i < P; i += 2) {
+          mul2(va[i], va[i + 1], rms, rms);
+          mul2(vb[i], vb[i + 1], rms, rms);
+          ya[i] = va[i], ya[i + 1] = va[i + 1];
+          yb[i] = vb[i], yb[i + 1] = vb[i + 1];
+          mul2(ya[i], ya[i + 1], ac[i], ac[i + 1]);
+          fma2_acc(ya[i], ya[i + 1], vb[i], vb[i + 1], bs[i], bs[i + 1]);
+          mul2(yb[i], yb[i + 1], bc[i], bc[i + 1]);
+          fma2_acc(yb[i], yb[i + 1], va[i], va[i + 1], as[i], as[i + 1]);
         }
-        if (mine) norm::store_unit(y + (long long)h * a.D, u, v[k]);
+        if (zero) {  // (not 0 * x: that may be NaN)
+#pragma unroll
+          for (int i = 0; i < P; ++i) ya[i] = yb[i] = 0.f;
+        }
+        if (mine) norm::store_unit(to, u, ya, yb);
+      } else {
+        float ga[P], gb[P], da[P], db[P];
+        norm::unpack(d_now, da, db);
+        if (zero) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) da[i] = db[i] = 0.f;
+        }
+        float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
+        const float counts = mine ? 1.f : 0.f;
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+          mul2(va[i], va[i + 1], rms, rms);  // x r
+          mul2(vb[i], vb[i + 1], rms, rms);
+          // dz_a = dy_a c + dy_b s, dz_b = dy_b c - dy_a s
+          ga[i] = da[i] * c[i], ga[i + 1] = da[i + 1] * c[i + 1];
+          gb[i] = db[i] * c[i], gb[i + 1] = db[i + 1] * c[i + 1];
+          fma2_acc(ga[i], ga[i + 1], db[i], db[i + 1], s[i], s[i + 1]);
+          fma2_acc(gb[i], gb[i + 1], da[i], da[i + 1], -s[i], -s[i + 1]);
+          // dz x r: into dw, and times w into the mean
+          float p0 = ga[i], p1 = ga[i + 1], q0 = gb[i], q1 = gb[i + 1];
+          mul2(p0, p1, va[i], va[i + 1]);
+          mul2(q0, q1, vb[i], vb[i + 1]);
+          fma2_acc(x0, x1, p0, p1, wa[i], wa[i + 1]);
+          fma2_acc(y0, y1, q0, q1, wb[i], wb[i + 1]);
+          fma2_acc(dwa[i], dwa[i + 1], p0, p1, counts, counts);
+          fma2_acc(dwb[i], dwb[i + 1], q0, q1, counts, counts);
+          mul2(ga[i], ga[i + 1], wa[i], wa[i + 1]);
+          mul2(gb[i], gb[i + 1], wb[i], wb[i + 1]);
+        }
+        const float dot = -norm::head_sum((u.any ? x0 + x1 : 0.f) + (u.both ? y0 + y1 : 0.f), lanes, 0xffffffffu) * inv_d;
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+          fma2_acc(ga[i], ga[i + 1], va[i], va[i + 1], dot, dot);
+          fma2_acc(gb[i], gb[i + 1], vb[i], vb[i + 1], dot, dot);
+          mul2(ga[i], ga[i + 1], rms, rms);
+          mul2(gb[i], gb[i + 1], rms, rms);
+        }
+        if (mine) norm::store_unit(to, u, ga, gb);
       }
     }
   }
   if constexpr (BACKWARD) {
     if (t.dw == nullptr) return;  // (all threads of the block)
     // The block's sum of each column, in the order of its head groups.
-    __shared__ float part[kThreads * 16];
+    __shared__ float part[kThreads * 2 * P];
     const int groups = kThreads / lanes, group = threadIdx.x / lanes;
-    if (u.any)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) part[group * a.D + u.c0 + i] = dw[i];
-    if (u.pair)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) part[group * a.D + u.c1 + i] = dw[8 + i];
+    for (int i = 0; i < P; ++i) {
+      if (u.any) part[group * a.D + u.c0 + (INTER ? 2 * i : i)] = dwa[i];
+      if (u.both) part[group * a.D + (INTER ? u.c0 + 2 * i + 1 : u.c1 + i)] = dwb[i];
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < a.D; d += kThreads) {
       float sum = 0.f;
@@ -265,7 +315,7 @@ size_t qk_norm_workspace_bytes(int D, int sm_count) { return (size_t)most_blocks
 
 int launch_qk_norm(NormArgs a, int dtype, bool backward, int sm_count, cudaStream_t s) {
   const bool vec = rot::vec_sizes(a.D, a.R, a.interleaved) && vec_rows(a.q) && vec_rows(a.k) &&
-                   (a.R == 0 || aligned16(a.table));
+                   (a.R == 0 || aligned16(a.table)) && aligned16(a.q.weight) && aligned16(a.k.weight);
   a.lanes = vec ? norm::head_lanes(a.D, a.R, a.interleaved) : 32;
   // A row's heads are split over warps where rows alone would leave multiprocessors idle, and in the backward, whose
   // blocks are limited, until warps have rounds enough to end together.
