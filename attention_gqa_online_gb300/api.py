@@ -197,18 +197,21 @@ def _heads2d(x, heads, name):
     return rows, columns // heads, stride
 
 
-def _weights(D, **weights):
-    """Type code of the weight vectors (0 when there are none)."""
-    code = None
-    for name, w in weights.items():
+def _weights(D, q_weight, k_weight):
+    """(type code, addresses) of two weight vectors, either of them None (code 0 without any)."""
+    code, ptr = None, [None, None]
+    for i, w in enumerate((q_weight, k_weight)):
         if w is None:
             continue
+        name = "k_weight" if i else "q_weight"
         if w.shape != (D,) or not w.is_contiguous():
             raise ValueError("%s must be a contiguous vector of %d" % (name, D))
-        if code is not None and code != _code(w, name):
-            raise ValueError("%s must have one type" % " and ".join(weights))
-        code = _code(w, name)
-    return B.ATTN_DT_F32 if code is None else code
+        if code is None:
+            code = _code(w, name)
+        elif _CODES.get(w.dtype) != code:
+            raise ValueError("q_weight and k_weight must have one type")
+        ptr[i] = w.data_ptr()
+    return code or 0, ptr[0], ptr[1]
 
 
 def _ptr(x):
@@ -221,7 +224,7 @@ def _norm_sizes(q, k, num_heads, num_kv_heads, q_weight, k_weight, table, positi
     if k_rows != rows or k_D != D:
         raise ValueError("q and k must have the same rows and the same head dimension")
     _like(q.dtype, "k", k)
-    w_code = _weights(D, q_weight=q_weight, k_weight=k_weight)
+    w_code, wq, wk = _weights(D, q_weight, k_weight)
     if table is None:
         if rot_dim:
             raise ValueError("a turn needs a table")
@@ -232,7 +235,7 @@ def _norm_sizes(q, k, num_heads, num_kv_heads, q_weight, k_weight, table, positi
     pos = _int32(positions, "positions")
     if pos is not None and positions.numel() != rows:
         raise ValueError("positions must hold one position a row")
-    return rows, D, qs, ks, w_code, rot_dim, tab, tab_rows, pos
+    return rows, D, qs, ks, w_code, wq, wk, rot_dim, tab, tab_rows, pos
 
 
 def qk_norm_rope(q, k, num_heads, num_kv_heads, q_weight=None, k_weight=None, table=None, positions=None, rot_dim=None,
@@ -240,17 +243,20 @@ def qk_norm_rope(q, k, num_heads, num_kv_heads, q_weight=None, k_weight=None, ta
     """q [rows, H*D] and k [rows, G*D] (fp32, bf16 or fp16; rows may be strided) with each head normed by its
     root mean square, multiplied by its weight vector [D] (None: ones) and turned by its row's position (row t
     at t without `positions`; no table: not turned).  Returns (q_out, k_out), which may be the inputs."""
-    rows, D, qs, ks, w_code, rot_dim, tab, tab_rows, pos = _norm_sizes(q, k, num_heads, num_kv_heads, q_weight, k_weight,
-                                                                      table, positions, rot_dim)
+    rows, D, qs, ks, w_code, wq, wk, rot_dim, tab, tab_rows, pos = _norm_sizes(
+        q, k, num_heads, num_kv_heads, q_weight, k_weight, table, positions, rot_dim)
     code, index = _code(q, "q"), q.get_device()
     q_out, qos = _rows_out(q_out, q, (rows, num_heads * D), "q_out", stream)
     k_out, kos = _rows_out(k_out, k, (rows, num_kv_heads * D), "k_out", stream)
     _same_device(index, k, q_out, k_out, q_weight, k_weight, table, positions)
     _run("attn_qk_norm_rope", B.load_library().attn_qk_norm_rope, index, _handle(stream, index),
-         (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight), _ptr(k_weight), code, w_code,
+         (q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), wq, wk, code, w_code,
           rows, num_heads, num_kv_heads, D, qs, ks, qos, kos, eps, rot_dim, 1 if interleaved else 0, pos, tab,
           tab_rows))
     return q_out, k_out
+
+
+_norm_workspace = {}  # bytes by (device, head dimension)
 
 
 def qk_norm_rope_backward(dq, dk, q, k, num_heads, num_kv_heads, q_weight=None, k_weight=None, table=None,
@@ -258,8 +264,8 @@ def qk_norm_rope_backward(dq, dk, q, k, num_heads, num_kv_heads, q_weight=None, 
                           stream=None):
     """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope's q, k and weights (None for a weight that is None)
     for upstream dq, dk of its results.  dq_out and dk_out take the first two; they may be dq and dk, or q and k."""
-    rows, D, qs, ks, w_code, rot_dim, tab, tab_rows, pos = _norm_sizes(q, k, num_heads, num_kv_heads, q_weight, k_weight,
-                                                                      table, positions, rot_dim)
+    rows, D, qs, ks, w_code, wq, wk, rot_dim, tab, tab_rows, pos = _norm_sizes(
+        q, k, num_heads, num_kv_heads, q_weight, k_weight, table, positions, rot_dim)
     code, index = _code(q, "q"), q.get_device()
     strides = []
     for name, x, heads in (("dq", dq, num_heads), ("dk", dk, num_kv_heads)):
@@ -275,12 +281,14 @@ def qk_norm_rope_backward(dq, dk, q, k, num_heads, num_kv_heads, q_weight=None, 
     dw = [None if w is None else _new(torch.empty, (D,), w.dtype, w.device, stream) for w in (q_weight, k_weight)]
     workspace, nbytes = None, 0
     if dw[0] is not None or dw[1] is not None:
-        with torch.cuda.device(index):
-            nbytes = B.attn_qk_norm_rope_backward_workspace_bytes(D)
+        nbytes = _norm_workspace.get((index, D))
+        if nbytes is None:
+            with torch.cuda.device(index):
+                nbytes = _norm_workspace[index, D] = B.attn_qk_norm_rope_backward_workspace_bytes(D)
         workspace = _new(torch.empty, (nbytes,), torch.uint8, q.device, stream)
     _run("attn_qk_norm_rope_backward", B.load_library().attn_qk_norm_rope_backward, index, raw,
          (dq.data_ptr(), dk.data_ptr(), q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(),
-          _ptr(q_weight), _ptr(k_weight), _ptr(dw[0]), _ptr(dw[1]), code, w_code, rows, num_heads, num_kv_heads, D,
+          wq, wk, _ptr(dw[0]), _ptr(dw[1]), code, w_code, rows, num_heads, num_kv_heads, D,
           strides[0], strides[1], qs, ks, dqos, dkos, eps, rot_dim, 1 if interleaved else 0, pos, tab, tab_rows,
           _ptr(workspace), nbytes))
     return dq_out, dk_out, dw[0], dw[1]
@@ -556,7 +564,7 @@ def append_paged8(batch, k_new, v_new, cache, q=None, q_out=None, table=None, ro
     if rot_dim is None:
         rot_dim = D
     tab, tab_rows = _table(table, rot_dim)
-    w_code = _weights(D, q_weight=q_weight, k_weight=k_weight) if q_weight is not None or k_weight is not None else 0
+    w_code, wq, wk = _weights(D, q_weight, k_weight)
     index = cache.index
     H = qs = qos = 0
     if q is not None:
@@ -582,7 +590,7 @@ def append_paged8(batch, k_new, v_new, cache, q=None, q_out=None, table=None, ro
          (_ptr(q), _ptr(q_out), k_new.data_ptr(), v_new.data_ptr(), code, q_code, cache.k_pages.data_ptr(),
           cache.v_pages.data_ptr(), cache.k_scales.data_ptr(), cache.v_scales.data_ptr(), batch.block_table.data_ptr(),
           batch.q_start.data_ptr(), batch.kv_len.data_ptr(), rows, batch.n_seqs, H, G, D, cache.kv_dim, qs, qos, ks, vs,
-          batch.page_rows, num_pages, batch.max_blocks, cache.scale_rows, _ptr(q_weight), _ptr(k_weight), w_code, eps,
+          batch.page_rows, num_pages, batch.max_blocks, cache.scale_rows, wq, wk, w_code, eps,
           rot_dim if tab is not None else 0, 1 if interleaved else 0, tab, tab_rows))
     return q_out
 

@@ -53,7 +53,7 @@ struct NormTensor {
   void* dw;            // backward: [D] or nullptr
   long long x_stride, dy_stride, y_stride;  // elements
   int heads;                                // 0: no such tensor
-  int splits;                               // warps that share a row; set by launch_qk_norm
+  int splits, splits_log2;                  // warps that share a row; set by launch_qk_norm
 };
 struct NormArgs {
   NormTensor q, k;

@@ -50,16 +50,14 @@ struct Head {
         mask(a.lanes == 32 ? 0xffffffffu : ((1u << a.lanes) - 1u) << (threadIdx.x & 31 & ~(a.lanes - 1))) {}
 };
 
-// The row x of a head (its first column), normed and turned.
+// The row x of a head (its first column), normed and turned; (vector form) as it lies in memory in `raw`.
 template <typename TI, bool INTER, bool VEC>
-__device__ __forceinline__ void load_row(const Append8Args& a, const TI* x, uint32_t pos, const Head<INTER, VEC>& hd,
-                                         Held<INTER, VEC>& out) {
+__device__ __forceinline__ void make_row(const Append8Args& a, const TI* x, const norm::Raw<TI, INTER>& raw, uint32_t pos,
+                                         const Head<INTER, VEC>& hd, Held<INTER, VEC>& out) {
   const float* tab = a.table + (long long)pos * a.R;
   const float inv_d = 1.f / (float)a.D;
   if constexpr (VEC) {
     constexpr int P = Held<INTER, VEC>::P;
-    norm::Raw<TI, INTER> raw;
-    norm::load_raw(x, hd.u, raw);
     norm::unpack(raw, out.a, out.b);
     if (hd.weight != nullptr) {
       float wa[P], wb[P];
@@ -114,6 +112,14 @@ __device__ __forceinline__ void load_row(const Append8Args& a, const TI* x, uint
   }
 }
 
+template <typename TI, bool INTER, bool VEC>
+__device__ __forceinline__ void load_row(const Append8Args& a, const TI* x, uint32_t pos, const Head<INTER, VEC>& hd,
+                                         Held<INTER, VEC>& out) {
+  norm::Raw<TI, INTER> raw{};
+  if constexpr (VEC) norm::load_raw(x, hd.u, raw);
+  make_row<TI, INTER, VEC>(a, x, raw, pos, hd, out);
+}
+
 template <bool INTER, bool VEC>
 __device__ __forceinline__ float held_max(const Held<INTER, VEC>& h) {
   float m = 0.f;  // (a NaN leaves it)
@@ -152,11 +158,19 @@ struct Team {
   int size, id, thread;  // threads of a team, this team of the block, this thread of the team
   int row, rows;         // the thread's first row of a block, and rows at once
   float* red;            // [warps of the block], shared memory
+  __device__ __forceinline__ unsigned mask() const {
+    return size >= 32 ? 0xffffffffu : ((1u << size) - 1u) << (threadIdx.x & 31 & ~(size - 1));
+  }
+  __device__ __forceinline__ void sync() const {
+    if (size > 32)
+      named_barrier(1 + id, size);
+    else
+      __syncwarp(mask());
+  }
   // Largest of m over the team.
   __device__ __forceinline__ float max(float m) const {
     const int w = size < 32 ? size : 32, lane = threadIdx.x & 31;
-    const unsigned mask = w == 32 ? 0xffffffffu : ((1u << w) - 1u) << (lane & ~(w - 1));
-    for (int d = w >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, d));
+    for (int d = w >> 1; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(mask(), m, d));
     if (size > 32) {
       const int warp = threadIdx.x >> 5, w0 = id * (size >> 5);
       if (lane == 0) red[warp] = m;
@@ -170,15 +184,12 @@ struct Team {
 };
 
 // One block of positions of one kv head: token rows [row0, row0 + m) at
-// positions pos0 ..., pool rows slot0 ...; `held` older rows stand before them.
+// positions pos0 ... of pool page `page`; `held` older rows stand before them.
 template <typename TI, bool INTER, bool VEC>
 __device__ __forceinline__ void write_block(const Append8Args& a, const Team& t, const TI* src, long long stride,
                                             uint8_t* pages, uint8_t* scales, int h, long long row0, int m,
-                                            uint32_t pos0, long long slot0, int held, const Head<INTER, VEC>& hd) {
-  uint8_t* scale = scales + (long long)divide((uint32_t)slot0, a.by_scale) * a.G + h;
-  const int e0 = held > 0 ? c8::exp_of(*scale) : c8::kMinExp;
+                                            uint32_t pos0, uint32_t page, int held, const Head<INTER, VEC>& hd) {
   const TI* x = src + row0 * stride + (long long)h * a.D;
-  uint8_t* dst = pages + slot0 * a.kv_dim + (long long)h * a.D;
   Held<INTER, VEC> kept[kKeep];
   float amax = 0.f;
 #pragma unroll
@@ -194,7 +205,21 @@ __device__ __forceinline__ void write_block(const Append8Args& a, const Team& t,
     load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, hd, v);
     amax = fmaxf(amax, held_max<INTER, VEC>(v));
   }
-  const int e = ::max(e0, c8::exp_for(t.max(amax)));
+  const int e_new = c8::exp_for(t.max(amax));
+  // (The page is looked at here, so that its lookup and the rows' loads are in flight together.)
+  if (page >= (uint32_t)a.num_pages) {
+    if (t.thread == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
+    return;
+  }
+  const long long slot0 = (long long)page * a.page_rows + (pos0 - divide(pos0, a.by_page) * (uint32_t)a.page_rows);
+  uint8_t* scale = scales + (long long)divide((uint32_t)slot0, a.by_scale) * a.G + h;
+  uint8_t* dst = pages + slot0 * a.kv_dim + (long long)h * a.D;
+  int e0 = c8::kMinExp;
+  if (held > 0) {
+    e0 = c8::exp_of(*scale);
+    t.sync();  // all have read it
+  }
+  const int e = ::max(e0, e_new);
   if (held > 0 && e > e0) {  // the older rows move to the new scale
     const float mul = pow2f(e0 - e);
     const int words = a.D / 4;
@@ -254,9 +279,16 @@ __device__ __forceinline__ void append_q(const Append8Args& a, int block) {
   const Head<INTER, VEC> hd(a, a.q_weight, a.R > 0 ? a.R : a.D, a.R > 0);
   const TI* x = static_cast<const TI*>(a.q) + row * a.q_stride;
   TQ* y = static_cast<TQ*>(a.q_out) + row * a.q_out_stride;
-  for (int h = split * at_once + sub; h < a.H; h += at_once * a.q_splits) {
+  // The next head's loads are in flight while one is computed.
+  norm::Raw<TI, INTER> ahead{};
+  int h = split * at_once + sub;
+  if (VEC && h < a.H) norm::load_raw(x + (long long)h * a.D, hd.u, ahead);
+  while (h < a.H) {
+    const norm::Raw<TI, INTER> raw = ahead;
+    const int next = h + at_once * a.q_splits;
+    if (VEC && next < a.H) norm::load_raw(x + (long long)next * a.D, hd.u, ahead);
     Held<INTER, VEC> v;
-    load_row<TI, INTER, VEC>(a, x + (long long)h * a.D, (uint32_t)pos, hd, v);
+    make_row<TI, INTER, VEC>(a, x + (long long)h * a.D, raw, (uint32_t)pos, hd, v);
     __syncwarp(hd.mask);  // (scalar form: the head's lanes have read it; y may be x)
     if constexpr (VEC) {
       norm::store_unit(y + (long long)h * a.D, hd.u, v.a, v.b);
@@ -265,6 +297,7 @@ __device__ __forceinline__ void append_q(const Append8Args& a, int block) {
       for (int j = 0; j < 4; ++j)
         if (hd.lane + 32 * j < a.D) y[(long long)h * a.D + hd.lane + 32 * j] = rot::from_f32<TQ>(v.a[j]);
     }
+    h = next;
   }
 }
 
@@ -316,25 +349,18 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const Append8Args 
       i += m;
       continue;
     }
-    bool ok = pos < (long long)a.page_rows * a.max_blocks;
-    long long slot = 0;
-    if (ok) {
-      const uint32_t col = divide((uint32_t)pos, a.by_page);
-      const uint32_t page = a.block_table[(long long)s * a.max_blocks + col];
-      ok = page < (uint32_t)a.num_pages;
-      slot = (long long)page * a.page_rows + ((uint32_t)pos - col * (uint32_t)a.page_rows);
-    }
     int take = m;
-    if (a.R > 0) take = (int)min((long long)m, ::max(0ll, (long long)a.table_rows - pos));
-    if ((!ok || take < m) && t.thread == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
-    if (ok && take > 0) {
-      const int held = in_block;
+    if (pos >= (long long)a.page_rows * a.max_blocks) take = 0;
+    if (a.R > 0) take = (int)min((long long)take, ::max(0ll, (long long)a.table_rows - pos));
+    if (take < m && t.thread == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
+    if (take > 0) {
+      const uint32_t page = a.block_table[(long long)s * a.max_blocks + divide((uint32_t)pos, a.by_page)];
       if (is_v)
         write_block<TI, false, VEC>(a, t, static_cast<const TI*>(a.v), a.v_stride, a.v_pages, a.v_scales, h, i, take,
-                                    (uint32_t)pos, slot, held, Head<false, VEC>(a, nullptr, a.D, false));
+                                    (uint32_t)pos, page, in_block, Head<false, VEC>(a, nullptr, a.D, false));
       else
         write_block<TI, INTER, VEC>(a, t, static_cast<const TI*>(a.k), a.k_stride, a.k_pages, a.k_scales, h, i, take,
-                                    (uint32_t)pos, slot, held,
+                                    (uint32_t)pos, page, in_block,
                                     Head<INTER, VEC>(a, a.k_weight, a.R > 0 ? a.R : a.D, a.R > 0));
     }
     i += m;

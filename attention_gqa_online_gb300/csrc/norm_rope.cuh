@@ -49,8 +49,14 @@ struct Unit {
 
 // Sum over the `lanes` lanes of a head (aligned groups of a warp).  `mask`
 // names lanes that call it together, whole groups.
+template <int LANES = 0>  // known when it is not 0
 __device__ __forceinline__ float head_sum(float v, int lanes, unsigned mask) {
-  for (int d = lanes >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(mask, v, d);
+  if constexpr (LANES != 0) {
+#pragma unroll
+    for (int d = LANES >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(mask, v, d);
+  } else {
+    for (int d = lanes >> 1; d > 0; d >>= 1) v += __shfl_xor_sync(mask, v, d);
+  }
   return v;
 }
 

@@ -48,7 +48,8 @@ __device__ __forceinline__ bool position_of(const NormArgs& a, uint32_t row, uin
   return ok;
 }
 
-template <typename T, bool INTER, bool BACKWARD>
+// LANES: of a head, when it is not 0; the case that every lane of them has a unit of 16 columns which turn.
+template <typename T, bool INTER, bool BACKWARD, int LANES>
 __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs a) {
   using U = norm::Unit<INTER>;
   constexpr int P = U::P;
@@ -56,9 +57,10 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
   const NormTensor& t = is_k ? a.k : a.q;
   const int block = is_k ? blockIdx.x - a.q_blocks : blockIdx.x, blocks = is_k ? gridDim.x - a.q_blocks : a.q_blocks;
   const Rows<T> r = rows_of<T>(t);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lanes = a.lanes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lanes = LANES != 0 ? LANES : a.lanes;
   const int sub = lane / lanes, at_once = 32 / lanes;  // heads of a warp at once
-  const U u(lane & (lanes - 1), a.D, a.R);
+  U u(lane & (lanes - 1), a.D, a.R);
+  if constexpr (LANES != 0) u.any = u.both = u.turned = true;
   const long long tasks = (long long)a.rows * t.splits;
   const float inv_d = 1.f / (float)a.D;
   const int step = at_once * t.splits, last = t.heads - 1;
@@ -68,9 +70,15 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
 #pragma unroll
     for (int i = 0; i < P; ++i) dwa[i] = dwb[i] = 0.f;
   }
-  for (long long task = (long long)block * kWarps + warp; task < tasks; task += (long long)blocks * kWarps) {
-    const uint32_t row = t.splits == 1 ? (uint32_t)task : (uint32_t)(task / t.splits);
-    const int h0 = (t.splits == 1 ? 0 : (int)(task - (long long)row * t.splits)) * at_once;
+  const long long first = (long long)block * kWarps + warp, stride = (long long)blocks * kWarps;
+  auto position_at = [&](long long task) {
+    const uint32_t row = (uint32_t)(task >> t.splits_log2);  // (splits is a power of two)
+    return a.positions != nullptr && task < tasks ? a.positions[row] : row;
+  };
+  uint32_t p_ahead = position_at(first);
+  for (long long task = first; task < tasks; task += stride) {
+    const uint32_t row = (uint32_t)(task >> t.splits_log2);
+    const int h0 = ((int)task & (t.splits - 1)) * at_once;
     const T* x = r.x + (long long)row * r.xs;
     const T* dy = BACKWARD ? r.dy + (long long)row * r.ds : nullptr;
     T* y = r.y + (long long)row * r.ys;
@@ -82,13 +90,19 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
       if constexpr (BACKWARD) norm::load_raw(dy + at, u, d_ahead);
     };
     look(h0);
-    uint32_t p;
-    const bool ok = position_of(a, row, &p);
+    const uint32_t p = p_ahead;
+    p_ahead = position_at(task + stride);
+    const bool ok = a.R == 0 || p < a.table_rows;
+    if (!ok && lane == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
     float c[P], s[P];
     norm::load_turn(a.table + (long long)p * a.R, a.R, u, ok, c, s);
     const bool zero = u.turned && !ok;
     // Forward: y_a = r (a w_a c - b w_b s), y_b = r (b w_b c + a w_a s).
-    float ac[P], bs[P], bc[P], as[P];
+    float ac[P], bs[P], bc[P], as[P], ns[P];
+    if constexpr (BACKWARD) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) ns[i] = -s[i];
+    }
     if constexpr (!BACKWARD) {
 #pragma unroll
       for (int i = 0; i < P; ++i) {
@@ -106,19 +120,16 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
       if (h + step <= last) look(h + step);
       const bool mine = h + sub <= last;
       T* to = y + (h + sub) * a.D;
-      const float rms = rsqrtf(fmaf(norm::head_sum(norm::squares(u, va, vb), lanes, 0xffffffffu), inv_d, a.eps));
+      const float rms = rsqrtf(fmaf(norm::head_sum<LANES>(norm::squares(u, va, vb), lanes, 0xffffffffu), inv_d, a.eps));
       if constexpr (!BACKWARD) {
         float ya[P], yb[P];
 #pragma unroll
         for (int i = 0; i < P; i += 2) {
-          mul2(va[i], va[i + 1], rms, rms);
-          mul2(vb[i], vb[i + 1], rms, rms);
-          ya[i] = va[i], ya[i + 1] = va[i + 1];
-          yb[i] = vb[i], yb[i + 1] = vb[i + 1];
-          mul2(ya[i], ya[i + 1], ac[i], ac[i + 1]);
-          fma2_acc(ya[i], ya[i + 1], vb[i], vb[i + 1], bs[i], bs[i + 1]);
-          mul2(yb[i], yb[i + 1], bc[i], bc[i + 1]);
-          fma2_acc(yb[i], yb[i + 1], va[i], va[i + 1], as[i], as[i + 1]);
+          const float2 ra = mul2_of(va[i], va[i + 1], rms, rms), rb = mul2_of(vb[i], vb[i + 1], rms, rms);
+          const float2 oa = fma2_of(rb.x, rb.y, bs[i], bs[i + 1], mul2_of(ra.x, ra.y, ac[i], ac[i + 1]));
+          const float2 ob = fma2_of(ra.x, ra.y, as[i], as[i + 1], mul2_of(rb.x, rb.y, bc[i], bc[i + 1]));
+          ya[i] = oa.x, ya[i + 1] = oa.y;
+          yb[i] = ob.x, yb[i + 1] = ob.y;
         }
         if (zero) {  // (not 0 * x: that may be NaN)
 #pragma unroll
@@ -139,22 +150,19 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
           mul2(va[i], va[i + 1], rms, rms);  // x r
           mul2(vb[i], vb[i + 1], rms, rms);
           // dz_a = dy_a c + dy_b s, dz_b = dy_b c - dy_a s
-          ga[i] = da[i] * c[i], ga[i + 1] = da[i + 1] * c[i + 1];
-          gb[i] = db[i] * c[i], gb[i + 1] = db[i + 1] * c[i + 1];
-          fma2_acc(ga[i], ga[i + 1], db[i], db[i + 1], s[i], s[i + 1]);
-          fma2_acc(gb[i], gb[i + 1], da[i], da[i + 1], -s[i], -s[i + 1]);
+          const float2 za = fma2_of(db[i], db[i + 1], s[i], s[i + 1], mul2_of(da[i], da[i + 1], c[i], c[i + 1]));
+          const float2 zb = fma2_of(da[i], da[i + 1], ns[i], ns[i + 1], mul2_of(db[i], db[i + 1], c[i], c[i + 1]));
           // dz x r: into dw, and times w into the mean
-          float p0 = ga[i], p1 = ga[i + 1], q0 = gb[i], q1 = gb[i + 1];
-          mul2(p0, p1, va[i], va[i + 1]);
-          mul2(q0, q1, vb[i], vb[i + 1]);
-          fma2_acc(x0, x1, p0, p1, wa[i], wa[i + 1]);
-          fma2_acc(y0, y1, q0, q1, wb[i], wb[i + 1]);
-          fma2_acc(dwa[i], dwa[i + 1], p0, p1, counts, counts);
-          fma2_acc(dwb[i], dwb[i + 1], q0, q1, counts, counts);
-          mul2(ga[i], ga[i + 1], wa[i], wa[i + 1]);
-          mul2(gb[i], gb[i + 1], wb[i], wb[i + 1]);
+          const float2 pa = mul2_of(za.x, za.y, va[i], va[i + 1]), pb = mul2_of(zb.x, zb.y, vb[i], vb[i + 1]);
+          fma2_acc(x0, x1, pa.x, pa.y, wa[i], wa[i + 1]);
+          fma2_acc(y0, y1, pb.x, pb.y, wb[i], wb[i + 1]);
+          fma2_acc(dwa[i], dwa[i + 1], pa.x, pa.y, counts, counts);
+          fma2_acc(dwb[i], dwb[i + 1], pb.x, pb.y, counts, counts);
+          const float2 ta = mul2_of(za.x, za.y, wa[i], wa[i + 1]), tb = mul2_of(zb.x, zb.y, wb[i], wb[i + 1]);
+          ga[i] = ta.x, ga[i + 1] = ta.y;
+          gb[i] = tb.x, gb[i + 1] = tb.y;
         }
-        const float dot = -norm::head_sum((u.any ? x0 + x1 : 0.f) + (u.both ? y0 + y1 : 0.f), lanes, 0xffffffffu) * inv_d;
+        const float dot = -norm::head_sum<LANES>((u.any ? x0 + x1 : 0.f) + (u.both ? y0 + y1 : 0.f), lanes, 0xffffffffu) * inv_d;
 #pragma unroll
         for (int i = 0; i < P; i += 2) {
           fma2_acc(ga[i], ga[i + 1], va[i], va[i + 1], dot, dot);
@@ -294,10 +302,12 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const NormArgs a, cons
 }
 
 template <typename T, bool BACKWARD>
-const void* kernel_of(bool vec, bool interleaved) {
+const void* kernel_of(bool vec, bool interleaved, int whole) {
+  if (vec && !interleaved && whole == 8) return reinterpret_cast<const void*>(qk_norm_vec_kernel<T, false, BACKWARD, 8>);
+  if (vec && !interleaved && whole == 4) return reinterpret_cast<const void*>(qk_norm_vec_kernel<T, false, BACKWARD, 4>);
   if (vec)
-    return interleaved ? reinterpret_cast<const void*>(qk_norm_vec_kernel<T, true, BACKWARD>)
-                       : reinterpret_cast<const void*>(qk_norm_vec_kernel<T, false, BACKWARD>);
+    return interleaved ? reinterpret_cast<const void*>(qk_norm_vec_kernel<T, true, BACKWARD, 0>)
+                       : reinterpret_cast<const void*>(qk_norm_vec_kernel<T, false, BACKWARD, 0>);
   return interleaved ? reinterpret_cast<const void*>(qk_norm_scalar_kernel<T, true, BACKWARD>)
                      : reinterpret_cast<const void*>(qk_norm_scalar_kernel<T, false, BACKWARD>);
 }
@@ -306,8 +316,9 @@ bool vec_rows(const NormTensor& t) {
   return aligned16(t.x) && aligned16(t.y) && aligned16(t.dy) && t.x_stride % 8 == 0 && t.y_stride % 8 == 0 &&
          t.dy_stride % 8 == 0;
 }
-// Thread blocks of the backward at most, of both tensors together: each leaves a row of partial sums.
-int most_blocks(int sms) { return sms * 4; }
+// Thread blocks at most, of both tensors together: two resident on a multiprocessor (in the backward each leaves a row
+// of partial sums).
+int most_blocks(int sms) { return sms * 2; }
 
 }  // namespace
 
@@ -317,22 +328,27 @@ int launch_qk_norm(NormArgs a, int dtype, bool backward, int sm_count, cudaStrea
   const bool vec = rot::vec_sizes(a.D, a.R, a.interleaved) && vec_rows(a.q) && vec_rows(a.k) &&
                    (a.R == 0 || aligned16(a.table)) && aligned16(a.q.weight) && aligned16(a.k.weight);
   a.lanes = vec ? norm::head_lanes(a.D, a.R, a.interleaved) : 32;
-  // A row's heads are split over warps where rows alone would leave multiprocessors idle, and in the backward, whose
-  // blocks are limited, until warps have rounds enough to end together.
+  // Heads of 128 and 64 that turn as a whole (every lane has a whole unit) run on kernels that know it.
+  const int whole = a.R == a.D && a.D == 16 * a.lanes ? a.lanes : 0;
+  // Blocks stay and take rows in turns, so weights are read once.  A row's heads are split over warps until there are
+  // rounds enough for all to end together, and in small calls until no multiprocessor is idle.
   const int most = most_blocks(sm_count);
+  const long long rounds = 2ll * most * kWarps;
   long long want[2] = {0, 0};
   NormTensor* t[2] = {&a.q, &a.k};
   for (int i = 0; i < 2; ++i) {
     if (t[i]->heads == 0) continue;
     const int steps = vec ? (t[i]->heads * a.lanes + 31) / 32 : t[i]->heads;
-    int splits = vec ? 1 : steps;
-    while (2 * splits <= steps && (long long)a.rows * splits < (backward ? 64ll : 16ll) * kWarps * sm_count) splits *= 2;
-    t[i]->splits = splits;
-    want[i] = ((long long)a.rows * splits + kWarps - 1) / kWarps;
-    const long long limit = backward ? most : 0x3fffffffll;
-    if (want[i] > limit) want[i] = limit;
+    t[i]->splits = 1;
+    t[i]->splits_log2 = 0;
+    while (vec && 2 * t[i]->splits <= steps && (long long)a.rows * t[i]->splits < rounds) {
+      t[i]->splits *= 2;
+      ++t[i]->splits_log2;
+    }
+    want[i] = ((long long)a.rows * (vec ? t[i]->splits : steps) + kWarps - 1) / kWarps;
+    if (want[i] > most) want[i] = most;
   }
-  if (backward && want[0] + want[1] > most) {  // in proportion to the heads, at least one each
+  if (want[0] + want[1] > most) {  // in proportion to the heads, at least one each
     int q = (int)((long long)most * a.q.heads / (a.q.heads + a.k.heads));
     if (a.q.heads > 0 && q == 0) q = 1;
     if (a.k.heads > 0 && q == most) q = most - 1;
@@ -343,11 +359,11 @@ int launch_qk_norm(NormArgs a, int dtype, bool backward, int sm_count, cudaStrea
   const int blocks = (int)(want[0] + want[1]);
   const void* kern;
   if (dtype == ATTN_DT_BF16)
-    kern = backward ? kernel_of<__nv_bfloat16, true>(vec, a.interleaved) : kernel_of<__nv_bfloat16, false>(vec, a.interleaved);
+    kern = backward ? kernel_of<__nv_bfloat16, true>(vec, a.interleaved, whole) : kernel_of<__nv_bfloat16, false>(vec, a.interleaved, whole);
   else if (dtype == ATTN_DT_F16)
-    kern = backward ? kernel_of<__half, true>(vec, a.interleaved) : kernel_of<__half, false>(vec, a.interleaved);
+    kern = backward ? kernel_of<__half, true>(vec, a.interleaved, whole) : kernel_of<__half, false>(vec, a.interleaved, whole);
   else
-    kern = backward ? kernel_of<float, true>(vec, a.interleaved) : kernel_of<float, false>(vec, a.interleaved);
+    kern = backward ? kernel_of<float, true>(vec, a.interleaved, whole) : kernel_of<float, false>(vec, a.interleaved, whole);
   void* args[] = {&a};
   if (cudaLaunchKernel(kern, dim3(blocks), dim3(kThreads), args, 0, s) != cudaSuccess) return ATTN_ERR_CUDA;
   if (!backward || (a.q.dw == nullptr && a.k.dw == nullptr)) return ATTN_OK;
