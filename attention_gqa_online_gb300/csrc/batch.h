@@ -121,7 +121,7 @@ struct Append8Args {
   bool interleaved;
   float eps;
   // Set by launch_append8.
-  FastDiv by_page, by_scale;
+  FastDiv by_page, by_scale, by_heads;  // by_heads: by 2 G
   int lanes, team, chunk, kv_blocks, q_splits;
 };
 int launch_append8(Append8Args a, int dtype, int q_dtype, int sm_count, cudaStream_t s);

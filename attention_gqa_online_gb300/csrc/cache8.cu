@@ -79,14 +79,6 @@ __device__ __forceinline__ void make_row(const Append8Args& a, const TI* x, cons
         out.b[i] = vb * c[i] + va * s[i];
       }
     }
-    if (!hd.u.any) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) out.a[i] = 0.f;
-    }
-    if (!hd.u.both) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) out.b[i] = 0.f;
-    }
   } else {
     float rms = 1.f;
     if (hd.weight != nullptr) {
@@ -120,14 +112,16 @@ __device__ __forceinline__ void load_row(const Append8Args& a, const TI* x, uint
   make_row<TI, INTER, VEC>(a, x, raw, pos, hd, out);
 }
 
+// Largest magnitude of a lane's own columns (a NaN leaves it).
 template <bool INTER, bool VEC>
-__device__ __forceinline__ float held_max(const Held<INTER, VEC>& h) {
-  float m = 0.f;  // (a NaN leaves it)
+__device__ __forceinline__ float held_max(const Held<INTER, VEC>& h, const Head<INTER, VEC>& hd) {
+  float m = 0.f, mb = 0.f;
 #pragma unroll
   for (int i = 0; i < Held<INTER, VEC>::P; ++i) {
     m = fmaxf(m, fabsf(h.a[i]));
-    if constexpr (VEC) m = fmaxf(m, fabsf(h.b[i]));
+    if constexpr (VEC) mb = fmaxf(mb, fabsf(h.b[i]));
   }
+  if constexpr (VEC) m = fmaxf(hd.u.any ? m : 0.f, hd.u.both ? mb : 0.f);
   return m;
 }
 template <bool INTER, bool VEC>
@@ -197,13 +191,13 @@ __device__ __forceinline__ void write_block(const Append8Args& a, const Team& t,
     const int r = t.row + k * t.rows;
     if (r < m) {
       load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, hd, kept[k]);
-      amax = fmaxf(amax, held_max<INTER, VEC>(kept[k]));
+      amax = fmaxf(amax, held_max<INTER, VEC>(kept[k], hd));
     }
   }
   for (int r = t.row + kKeep * t.rows; r < m; r += t.rows) {
     Held<INTER, VEC> v;
     load_row<TI, INTER, VEC>(a, x + r * stride, pos0 + r, hd, v);
-    amax = fmaxf(amax, held_max<INTER, VEC>(v));
+    amax = fmaxf(amax, held_max<INTER, VEC>(v, hd));
   }
   const int e_new = c8::exp_for(t.max(amax));
   // (The page is looked at here, so that its lookup and the rows' loads are in flight together.)
@@ -279,25 +273,58 @@ __device__ __forceinline__ void append_q(const Append8Args& a, int block) {
   const Head<INTER, VEC> hd(a, a.q_weight, a.R > 0 ? a.R : a.D, a.R > 0);
   const TI* x = static_cast<const TI*>(a.q) + row * a.q_stride;
   TQ* y = static_cast<TQ*>(a.q_out) + row * a.q_out_stride;
-  // The next head's loads are in flight while one is computed.
-  norm::Raw<TI, INTER> ahead{};
-  int h = split * at_once + sub;
-  if (VEC && h < a.H) norm::load_raw(x + (long long)h * a.D, hd.u, ahead);
-  while (h < a.H) {
-    const norm::Raw<TI, INTER> raw = ahead;
-    const int next = h + at_once * a.q_splits;
-    if (VEC && next < a.H) norm::load_raw(x + (long long)next * a.D, hd.u, ahead);
-    Held<INTER, VEC> v;
-    make_row<TI, INTER, VEC>(a, x + (long long)h * a.D, raw, (uint32_t)pos, hd, v);
-    __syncwarp(hd.mask);  // (scalar form: the head's lanes have read it; y may be x)
-    if constexpr (VEC) {
-      norm::store_unit(y + (long long)h * a.D, hd.u, v.a, v.b);
-    } else {
+  const int step = at_once * a.q_splits;
+  if constexpr (VEC) {
+    // y_a = r (a w_a c - b w_b s), y_b = r (b w_b c + a w_a s): what does not depend on the head is made once.  The next
+    // head's loads are in flight while one is computed.
+    constexpr int P = Held<INTER, VEC>::P;
+    const norm::Unit<INTER>& u = hd.u;
+    norm::Raw<TI, INTER> ahead;
+    int h = split * at_once + sub;
+    if (h < a.H) norm::load_raw(x + h * a.D, u, ahead);
+    float wa[P], wb[P], ac[P], bs[P], bc[P], as[P];
+    norm::load_weight(a.q_weight, a.w_dtype, u, wa, wb);
+    if (a.R > 0) {
+      norm::load_turn(a.table + pos * a.R, a.R, u, true, ac, as);
+    } else {  // (u is then that of a head turned as a whole, and there is no table)
+#pragma unroll
+      for (int i = 0; i < P; ++i) ac[i] = 1.f, as[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      bc[i] = ac[i] * wb[i];
+      bs[i] = -as[i] * wb[i];
+      ac[i] *= wa[i];
+      as[i] *= wa[i];
+    }
+    const float inv_d = 1.f / (float)a.D;
+    for (; h < a.H; h += step) {
+      float va[P], vb[P], ya[P], yb[P];
+      norm::unpack(ahead, va, vb);
+      if (h + step < a.H) norm::load_raw(x + (h + step) * a.D, u, ahead);
+      float r = 1.f;
+      if (a.q_weight != nullptr)
+        r = rsqrtf(fmaf(norm::head_sum(norm::squares(u, va, vb), a.lanes, hd.mask), inv_d, a.eps));
+#pragma unroll
+      for (int i = 0; i < P; i += 2) {
+        const float2 ra = mul2_of(va[i], va[i + 1], r, r), rb = mul2_of(vb[i], vb[i + 1], r, r);
+        const float2 oa = fma2_of(rb.x, rb.y, bs[i], bs[i + 1], mul2_of(ra.x, ra.y, ac[i], ac[i + 1]));
+        const float2 ob = fma2_of(ra.x, ra.y, as[i], as[i + 1], mul2_of(rb.x, rb.y, bc[i], bc[i + 1]));
+        ya[i] = oa.x, ya[i + 1] = oa.y;
+        yb[i] = ob.x, yb[i + 1] = ob.y;
+      }
+      norm::store_unit(y + h * a.D, u, ya, yb);
+    }
+  } else {
+    const norm::Raw<TI, INTER> none{};
+    for (int h = split * at_once + sub; h < a.H; h += step) {
+      Held<INTER, VEC> v;
+      make_row<TI, INTER, VEC>(a, x + (long long)h * a.D, none, (uint32_t)pos, hd, v);
+      __syncwarp(hd.mask);  // the head's lanes have read it: y may be x
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (hd.lane + 32 * j < a.D) y[(long long)h * a.D + hd.lane + 32 * j] = rot::from_f32<TQ>(v.a[j]);
     }
-    h = next;
   }
 }
 
@@ -316,17 +343,17 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const Append8Args 
   t.rows = a.team / a.lanes;
   t.red = red;
   const int teams = kThreads / a.team;
-  const long long first = (long long)blockIdx.x * teams, item = first + t.id;
+  const uint32_t first = blockIdx.x * (uint32_t)teams, item = first + t.id;  // (below 2^31)
   // All lanes of a warp look for the sequence of the warp's first row.
-  const long long row_w = (first + (threadIdx.x & ~31) / a.team) / (2 * a.G) * a.chunk;
+  const long long row_w = (long long)divide(first + (threadIdx.x & ~31) / a.team, a.by_heads) * a.chunk;
   if (row_w >= a.total_rows) return;
   int s = ::max(0, find_seq(a.q_start, a.n_seqs, (uint32_t)row_w));
-  const long long chunk = item / (2 * a.G);
-  if (chunk * a.chunk >= a.total_rows) return;
+  const uint32_t chunk = divide(item, a.by_heads);
+  if ((long long)chunk * a.chunk >= a.total_rows) return;
   const int which = (int)(item - chunk * 2 * a.G);
   const bool is_v = which >= a.G;
   const int h = is_v ? which - a.G : which;
-  uint32_t i = (uint32_t)(chunk * a.chunk);
+  uint32_t i = chunk * (uint32_t)a.chunk;
   const uint32_t i_end = (uint32_t)min((long long)a.total_rows, (long long)i + a.chunk);
   const int sr = a.scale_rows;
   while (i < i_end) {
@@ -343,24 +370,29 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const Append8Args 
       i = (uint32_t)min((long long)end, (long long)i - pos);
       continue;
     }
-    const int in_block = (int)(pos % sr);
-    const int m = (int)min((long long)(sr - in_block), (long long)end - (long long)i);
+    if (pos >= (long long)a.page_rows * a.max_blocks) {  // and all that follow
+      if (t.thread == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
+      i = end;
+      continue;
+    }
+    const uint32_t p = (uint32_t)pos;
+    const int in_block = (int)(p - divide(p, a.by_scale) * (uint32_t)sr);
+    const int m = (int)min((uint32_t)(sr - in_block), end - i);
     if (in_block != 0 && i != start) {  // the block's first new row is in another chunk
       i += m;
       continue;
     }
     int take = m;
-    if (pos >= (long long)a.page_rows * a.max_blocks) take = 0;
-    if (a.R > 0) take = (int)min((long long)take, ::max(0ll, (long long)a.table_rows - pos));
+    if (a.R > 0) take = p < a.table_rows ? (int)min((uint32_t)m, a.table_rows - p) : 0;
     if (take < m && t.thread == 0) record_status(a.status, ATTN_ERR_INVALID_ARG);
     if (take > 0) {
-      const uint32_t page = a.block_table[(long long)s * a.max_blocks + divide((uint32_t)pos, a.by_page)];
+      const uint32_t page = a.block_table[(long long)s * a.max_blocks + divide(p, a.by_page)];
       if (is_v)
         write_block<TI, false, VEC>(a, t, static_cast<const TI*>(a.v), a.v_stride, a.v_pages, a.v_scales, h, i, take,
-                                    (uint32_t)pos, page, in_block, Head<false, VEC>(a, nullptr, a.D, false));
+                                    p, page, in_block, Head<false, VEC>(a, nullptr, a.D, false));
       else
         write_block<TI, INTER, VEC>(a, t, static_cast<const TI*>(a.k), a.k_stride, a.k_pages, a.k_scales, h, i, take,
-                                    (uint32_t)pos, page, in_block,
+                                    p, page, in_block,
                                     Head<INTER, VEC>(a, a.k_weight, a.R > 0 ? a.R : a.D, a.R > 0));
     }
     i += m;
@@ -485,10 +517,11 @@ int launch_append8(Append8Args a, int dtype, int q_dtype, int sm_count, cudaStre
   if (a.H > 0) {
     const int steps = (a.H * a.lanes + 31) / 32;
     a.q_splits = 1;
-    while (2 * a.q_splits <= steps && (long long)a.total_rows * a.q_splits < 16ll * kWarps * sm_count) a.q_splits *= 2;
+    while (2 * a.q_splits <= steps && (long long)a.total_rows * a.q_splits < 2ll * kWarps * sm_count) a.q_splits *= 2;
     q_blocks = ((long long)a.total_rows * a.q_splits + kWarps - 1) / kWarps;
   }
-  if (kv_blocks + q_blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+  if (chunks * 2 * a.G > 0x7fffff00ll || kv_blocks + q_blocks > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+  a.by_heads = fast_div((uint32_t)(2 * a.G));
   a.kv_blocks = (int)kv_blocks;
   const void* kern;
   if (dtype == ATTN_DT_BF16)

@@ -617,7 +617,8 @@ ATTN_API int attn_qk_norm_rope_backward(const void *dq, const void *dk, const vo
  * Errors: INVALID_ARG as attn_append_paged, and for a scale_rows that does not
  * divide page_rows, NULL scales, a weight for Q without Q, or (with a weight)
  * an eps as attn_qk_norm_rope; UNSUPPORTED for head_dim % 16 != 0, kv_dim %
- * 16 != 0 or pools that are not 16-byte aligned.
+ * 16 != 0, pools that are not 16-byte aligned, or total_rows * 2 *
+ * num_kv_heads beyond 2^31 - 256.
  *
  * attn_read_paged8 writes the values of a range of each sequence's positions,
  * rounded to dtype (bf16 and fp16 hold them exactly):
