@@ -72,6 +72,7 @@ struct __align__(1024) DecodeSmem {
   static constexpr int q_stride = D + 8;   // elements; 16 bytes off a multiple of 128: rows start in different banks
   static constexpr int o_stride = D + 8;   // floats
   unsigned char ring[stages][2][tile_bytes];
+  float4 scale[kMaxStages][C8 ? keys : 1];  // of a tile's keys: K's scale, log2 of V's, one over V's
   uint16_t q[2][kRows * q_stride];
   float o[4][kRows * o_stride];
   float2 ml[8][kRows];  // reference and sum of each warp's rows
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   allow_dependent_launch();
   if (tid == 0) {
     for (int i = 0; i < S::stages; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.full[i], C8 ? 5 : 1);  // the copies; codes: four warps' scales, too
       mbar_init(&sm.empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
@@ -166,6 +167,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         return !seen ? outside : pg < (uint32_t)a.num_pages ? (int)pg * a.page_rows + key - col * a.page_rows : -1;
       };
       int now = rows_of(0), next = n * parts > 32 ? rows_of(32) : outside;
+      // Codes: the lane's key of each tile, 32 pw + lane; its scales are looked up a tile ahead (a trip to L2).
+      const int box_log2 = __ffs(box_rows) - 1, mine = 32 * pw + lane;
+      uint32_t k_byte = 0, v_byte = 0;
+      auto look = [&](int rows, int i) {  // rows: of the 32 parts that hold tile i's
+        const int row = __shfl_sync(0xffffffffu, rows, (i * parts + (mine >> box_log2)) & 31);
+        if (row < 0 || row == outside) return;  // (the codes arrive as zeros)
+        const long long b = (long long)divide((uint32_t)(row + (mine & (box_rows - 1))), a.by_scale) * a.G + g;
+        k_byte = a.k_scales[b];
+        v_byte = a.v_scales[b];
+      };
+      if constexpr (C8) look(now, 0);
       for (int i = 0; i < n; ++i, ++J) {
         const int q0 = i * parts;
         if (i > 0 && q0 % 32 == 0) {
@@ -208,6 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(dst + (e * box_rows + r) * 128, &tm_v1, 64 * chunk, g, y, &sm.full[st]);
             }
           }
+        }
+        if constexpr (C8) {
+          const int ev = c8::exp_of(v_byte);
+          sm.scale[st][mine] = make_float4(pow2f(c8::exp_of(k_byte)), (float)ev, pow2f(-ev), 0.f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.full[st]);
+          if (i + 1 < n) look(((i + 1) * parts) % 32 == 0 ? next : now, i + 1);
         }
       }
       return J;
@@ -307,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned missing = 0;
         for (int w = 0; w < 4; ++w) missing += sm.issued[w] <= j ? sm.share[w] : 0;
         settle_tile(&sm.full[j % S::stages], J > j, 2 * S::tile_bytes, missing);
+        for (int w = 0; C8 && w < 4; ++w)
+          if (sm.issued[w] <= j) mbar_arrive(&sm.full[j % S::stages]);
       }
       drain_ring(sm.full, S::stages, hi, a.status);
       drain_ring(sm.q_ready, 2, x, a.status);
@@ -355,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                         (C8 ? 2 : 8) * (e >> 1));
     }
     __syncwarp();
-    float qf[2] = {1.f, 1.f};  // powers of two that came off the rows
+    float qf[2] = {1.f, 1.f};  // powers of two that came off the rows; without a cap, with the scores' scale
     if constexpr (C8 && !std::is_same<T, __half>::value) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -374,30 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    // Codes: lane l looks up the scales of the warp's key l, the page of a tile two of the group's tiles ahead and the
-    // scales one ahead, so their trips to L2 are over when the tile is.
-    const uint32_t* table = C8 ? a.block_table + (long long)d.seq * a.max_blocks : nullptr;
-    // (What a load brings is first used a tile later.)
-    auto key_at = [&](int i) { return plan::tile_at<SINKS>(d.tile0 + i, d.ns, d.skip) * kKeys + kw + lane; };
-    auto page_at = [&](int i) {  // page of the lane's key of tile i; none where no row sees it
-      const int key = key_at(i);
-      if (i >= n || plan::keys_hidden<SINKS>(key, 1, d.se, d.lo_min, d.hi_max)) return 0xffffffffu;
-      return table[plan::page_of(a, key)];
-    };
-    uint32_t page_ahead = 0, k_ahead = 0, v_ahead = 0;
-    auto scales_at = [&](int i) {  // of the key whose page is in page_ahead
-      if (page_ahead >= (uint32_t)a.num_pages) return;
-      const int key = key_at(i);
-      const uint32_t row = page_ahead * (uint32_t)a.page_rows + (uint32_t)(key - plan::page_of(a, key) * a.page_rows);
-      const long long b = (long long)divide(row, a.by_scale) * a.G + d.g;
-      k_ahead = a.k_scales[b];
-      v_ahead = a.v_scales[b];
-    };
-    if constexpr (C8) {
-      const int i0 = (J & 1) ^ grp;
-      page_ahead = page_at(i0);
-      scales_at(i0);
-      page_ahead = page_at(i0 + 2);
+    if (C8 && !(a.softcap > 0.f)) {
+      qf[0] *= sc.scale2;
+      qf[1] *= sc.scale2;
     }
     // (After a wait that ran out a warp frees no slot any more, since copies may still be landing there, but keeps to
     // the block's barriers until the next piece.)
@@ -410,24 +410,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     for (int i = (J & 1) ^ grp; ok && i < n; i += 2) {
       const int j = J + i, st = j % S::stages;
-      // Scales of this lane's keys 8 y + lc + {0, 1}: K's as a float, V's as a pair of fp16 numbers.
-      float kf[C8 ? kTiles : 1][2];
-      uint32_t vf[C8 ? kTiles : 1];
-      if constexpr (C8) {
-        const uint32_t mine = (uint32_t)(127 + c8::exp_of(k_ahead)) << 16 | (uint32_t)(15 + c8::exp_of(v_ahead)) << 10;
-        scales_at(i + 2);
-        page_ahead = page_at(i + 4);
-#pragma unroll
-        for (int y = 0; y < kTiles; ++y) {
-          const uint32_t p0 = __shfl_sync(0xffffffffu, mine, 8 * y + lc), p1 = __shfl_sync(0xffffffffu, mine, 8 * y + lc + 1);
-          kf[y][0] = __uint_as_float(p0 >> 16 << 23);
-          kf[y][1] = __uint_as_float(p1 >> 16 << 23);
-          vf[y] = __byte_perm(p0, p1, 0x5410);
-        }
-      }
       ok = wait(&sm.full[st], j / S::stages);
       if (!ok) break;
       const uint32_t k_base = smem_u32(sm.ring[st][0]), v_base = smem_u32(sm.ring[st][1]);
+      // Codes: V's scale 2^v of a key joins its score, so weights are p 2^v against the largest of these and V stays as it
+      // is; sums of p take 2^-v off again.
+      float4 ks[C8 ? kTiles : 1][2];  // of the keys 8 y + lc + {0, 1}
       // With two n-tiles, even and odd column steps accumulate apart: the chain of dependent products is half as long.
       constexpr int kSets = kTiles == 2 ? 2 : 1;
       float s[kTiles][4], s1[kTiles][4];
@@ -451,10 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma16816<TO>(s[y], qa[4 * c4 + c], b0, b1);
             }
           }
-#pragma unroll
-        for (int y = 0; y < kTiles; ++y)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[y][e] *= kf[y][e & 1] * qf[e >> 1];
       } else
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {
@@ -473,13 +457,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[y][e] += s1[y][e];
       }
+      if constexpr (C8) {
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y) {
+          ks[y][0] = sm.scale[st][kw + 8 * y + lc];
+          ks[y][1] = sm.scale[st][kw + 8 * y + lc + 1];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[y][e] *= ks[y][e & 1].x * qf[e >> 1];
+        }
+      }
       const int tile_key = plan::tile_at<SINKS>(d.tile0 + i, d.ns, d.skip) * kKeys, key0 = tile_key + kw + lc;
       if (a.softcap > 0.f) {
 #pragma unroll
         for (int y = 0; y < kTiles; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[y][e] = sc.out_mul * tanh_score(s[y][e] * sc.in_mul);
-      } else {
+      } else if (!C8) {
 #pragma unroll
         for (int y = 0; y < kTiles; ++y)
 #pragma unroll
@@ -491,6 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             s[y][e] = fmaf(slope[e >> 1], fabsf((float)(pos[e >> 1] - (key0 + 8 * y + (e & 1)))), s[y][e]);
+      }
+      if constexpr (C8) {
+#pragma unroll
+        for (int y = 0; y < kTiles; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[y][e] += ks[y][e & 1].y;
       }
       if (tile_key + kKeys > hi_min || tile_key < lo_max) {
 #pragma unroll
@@ -528,7 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[y][e] = ex2(s[y][e] - sub[e >> 1]);
-          l[e >> 1] += s[y][e];
+          if constexpr (C8)
+            l[e >> 1] = fmaf(s[y][e], ks[y][e & 1].z, l[e >> 1]);
+          else
+            l[e >> 1] += s[y][e];
         }
 #pragma unroll
       for (int g = 0; g < kSteps; ++g) {
@@ -547,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t even0, odd0, even1, odd1;
               c8::to_half4(__byte_perm(vb[2 * e], 0, 0x3120), even0, odd0);
               c8::to_half4(__byte_perm(vb[2 * e + 1], 0, 0x3120), even1, odd1);
-              mma16816<TO>(o[4 * u2 + 2 * e], pa, c8::mul_half2(even0, vf[2 * g]), c8::mul_half2(even1, vf[2 * g + 1]));
-              mma16816<TO>(o[4 * u2 + 2 * e + 1], pa, c8::mul_half2(odd0, vf[2 * g]), c8::mul_half2(odd1, vf[2 * g + 1]));
+              mma16816<TO>(o[4 * u2 + 2 * e], pa, even0, even1);
+              mma16816<TO>(o[4 * u2 + 2 * e + 1], pa, odd0, odd1);
             }
           }
         } else
