@@ -506,8 +506,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Warps wait as a whole.  Were lanes to leave a wait at different times, one could arrive somewhere for the warp, the
   // barrier complete its next phase and the others wait for a phase that is past.
   const unsigned long long limit = BRIEF ? a.wait_ns : kWaitLimitNs;
+  // The forms with more code wait in less of it (17 ragged chunks with a bias 218 us, 202 so; a prompt of 8192 with a window
+  // and first positions 237 and 226); the plainest one does not gain (prompt of 8192 395 and 405).
+  constexpr bool kShortWaits = !BRIEF && (C8 || SINKS || MODE != 0);
   auto wait = [&](uint64_t* bar, int phase) {
-    if constexpr (C8 && !BRIEF)
+    if constexpr (kShortWaits)
       return __all_sync(0xffffffffu, wait_phase_short(bar, (unsigned)(phase & 1), a.status, &sm.abort)) != 0;
     else
       return warp_wait<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Without the vote, where no answer is asked for, nothing warp-wide follows at once and a __syncwarp comes before a lane
   // arrives for the warp (17 ragged chunks with a bias, 16 heads: 223 us with votes there too, 219 this way).
   auto lane_wait = [&](uint64_t* bar, int phase) {
-    if constexpr (C8 && !BRIEF)
+    if constexpr (kShortWaits)
       wait_phase_short(bar, (unsigned)(phase & 1), a.status, &sm.abort);
     else
       wait_phase<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
@@ -644,8 +647,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // phase, would turn a late block into a fault.
       bool ok = true;
       while (ok) {
-        int n = 0, col = 0;
-        Parts w{};
         if (C8 && warp == 3) {
           if (!next_piece(x)) break;
         } else {
@@ -696,10 +697,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           __syncwarp();
           if (!more) break;
           // The piece's first page parts are looked up while its Q buffer falls free.
-          n = p.t1 - p.t0;
-          col = FULL ? p.g * D : 0;
-          if constexpr (!C8) w = open_parts(L::k_rows, n, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t1 - 1, p.k.ns,
-                               p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
+          const int n = p.t1 - p.t0, col = FULL ? p.g * D : 0;
+          Parts w;
+          if constexpr (!C8)
+            w = open_parts(L::k_rows, n, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t1 - 1, p.k.ns,
+                           p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
           // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
           // only feeds itself, and those rows are not stored).
           const int qb = x % kQBufs;
@@ -733,27 +735,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(C8 ? &sm.q_raw[qb] : &sm.q_ready[qb]);
           }
+          for (int i = 0; !C8 && i < n; ++i, ++J) {
+            const int row = part_row(w, i), slot = J % L::slots;
+            if (J >= L::slots) ok = wait(&sm.k_empty[slot], J / L::slots - 1);
+            if (!ok) break;
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
+            __syncwarp();
+            if ((lane >> w.shift) == 0) {
+              const uint32_t bar = barrier_of(&sm.k_full[slot]);
+#pragma unroll
+              for (int c = 0; c < L::chunks; ++c)
+                load_rows<PAIR, FULL>(sm.k[slot] + c * L::k_chunk + lane * box_rows * 128, &tm_k, col + 64 * c, p.g, row, bar);
+            }
+          }
         }
         if constexpr (C8) {  // one piece of code for K and V
           const PieceDesc& d = sm.desc[x % kDescs];
           const int v = warp == 3 ? 1 : 0;
-          w = open_parts(v ? kTcKeys : L::k_rows, d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip,
+          Parts w = open_parts(v ? kTcKeys : L::k_rows, d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip,
                          PAIR && !v ? rank * L::k_rows : 0, d.seq);
           ok = load_codes(w, v, d.g, J);
           if (v && ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
-        }
-        for (int i = 0; !C8 && i < n; ++i, ++J) {
-          const int row = part_row(w, i), slot = J % L::slots;
-          if (J >= L::slots) ok = wait(&sm.k_empty[slot], J / L::slots - 1);
-          if (!ok) break;
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
-          __syncwarp();
-          if ((lane >> w.shift) == 0) {
-            const uint32_t bar = barrier_of(&sm.k_full[slot]);
-#pragma unroll
-            for (int c = 0; c < L::chunks; ++c)
-              load_rows<PAIR, FULL>(sm.k[slot] + c * L::k_chunk + lane * box_rows * 128, &tm_k, col + 64 * c, p.g, row, bar);
-          }
         }
         ++x;
       }

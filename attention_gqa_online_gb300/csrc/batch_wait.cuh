@@ -30,7 +30,8 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, unsig
   }
 }
 
-// As wait_phase, in half the code: for kernels whose roles together outgrow the instruction cache.
+// As wait_phase, in half the code: for kernels whose roles together outgrow the instruction cache.  (The limit is
+// looked at every time the wait's own suspension ends.)
 __device__ __forceinline__ bool wait_phase_short(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag) {
   unsigned t0 = 0;
 #pragma unroll 1
