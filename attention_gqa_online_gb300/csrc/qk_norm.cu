@@ -82,10 +82,15 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
     const T* x = r.x + (long long)row * r.xs;
     const T* dy = BACKWARD ? r.dy + (long long)row * r.ds : nullptr;
     T* y = r.y + (long long)row * r.ys;
-    // The next head's loads are in flight while one is computed.
+    // The next head's loads are in flight while one is computed.  Lanes without a head compute one of zeros
+    // (another's infinities, times zero, would make dw NaN).
     norm::Raw<T, INTER> x_ahead, d_ahead;
     auto look = [&](int h) {
-      const int at = min(h + sub, last) * a.D;
+      const int at = (h + sub) * a.D;
+      if (h + sub > last) {
+        x_ahead = d_ahead = norm::Raw<T, INTER>{};
+        return;
+      }
       norm::load_raw(x + at, u, x_ahead);
       if constexpr (BACKWARD) norm::load_raw(dy + at, u, d_ahead);
     };
@@ -144,7 +149,6 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
           for (int i = 0; i < P; ++i) da[i] = db[i] = 0.f;
         }
         float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
-        const float counts = mine ? 1.f : 0.f;
 #pragma unroll
         for (int i = 0; i < P; i += 2) {
           mul2(va[i], va[i + 1], rms, rms);  // x r
@@ -156,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
           const float2 pa = mul2_of(za.x, za.y, va[i], va[i + 1]), pb = mul2_of(zb.x, zb.y, vb[i], vb[i + 1]);
           fma2_acc(x0, x1, pa.x, pa.y, wa[i], wa[i + 1]);
           fma2_acc(y0, y1, pb.x, pb.y, wb[i], wb[i + 1]);
-          fma2_acc(dwa[i], dwa[i + 1], pa.x, pa.y, counts, counts);
-          fma2_acc(dwb[i], dwb[i + 1], pb.x, pb.y, counts, counts);
+          add2(dwa[i], dwa[i + 1], pa.x, pa.y);
+          add2(dwb[i], dwb[i + 1], pb.x, pb.y);
           const float2 ta = mul2_of(za.x, za.y, wa[i], wa[i + 1]), tb = mul2_of(zb.x, zb.y, wb[i], wb[i + 1]);
           ga[i] = ta.x, ga[i + 1] = ta.y;
           gb[i] = tb.x, gb[i + 1] = tb.y;

@@ -114,7 +114,7 @@ typedef enum {
 typedef enum { ATTN_FP32 = 0, ATTN_TF32 = 1, ATTN_BF16 = 2 } attn_prec_t;
 
 /* Element types of the calls that take more than fp32 (attn_rope_apply,
- * attn_append_paged, attn_batch_paged). */
+ * attn_qk_norm_rope, the paged appends, the batched attention). */
 typedef enum { ATTN_DT_F32 = 0, ATTN_DT_BF16 = 1, ATTN_DT_F16 = 2 } attn_dtype_t;
 
 /* Which columns of a head make a rotary pair, and how its angles are scaled
@@ -613,7 +613,9 @@ ATTN_API int attn_qk_norm_rope_backward(const void *dq, const void *dk, const vo
  *     leave Q out.
  * Rows that attn_append_paged skips are skipped here (their q_out, too), with
  * the same status.  No two rows may belong to the same scale of the pools
- * unless they are of one sequence.  total_rows == 0 or n_seqs == 0 is a no-op.
+ * unless they are of one sequence; a page that sequences share is written by
+ * none of them, so they share whole blocks of scale_rows positions (what is
+ * written into a block may move all of its codes).  total_rows == 0 or n_seqs == 0 is a no-op.
  * Errors: INVALID_ARG as attn_append_paged, and for a scale_rows that does not
  * divide page_rows, NULL scales, a weight for Q without Q, or (with a weight)
  * an eps as attn_qk_norm_rope; UNSUPPORTED for head_dim % 16 != 0, kv_dim %
@@ -636,12 +638,15 @@ ATTN_API int attn_qk_norm_rope_backward(const void *dq, const void *dk, const vo
  * attn_batch_paged8 is attn_batch_paged_sinks over such a cache: dtype
  * (ATTN_DT_BF16 or ATTN_DT_F16) is that of q and out.  The products run on
  * fp16 operands: K and V exactly, Q of bf16 times a power of two of its row
- * (entries below 2^-28 of the row's largest lose bits), P with half a step of fp16 of each weight
- * and at least 2^-32 of the largest so far.  V must hold no NaN code at
- * positions that some row of the sequence attends, K neither.  The workspace
- * is attn_batch_paged's.  Errors as attn_batch_paged; INVALID_ARG for a
- * scale_rows that does not divide page_rows or NULL scales, UNSUPPORTED for
- * head_dim % 16 != 0 and kv_dim % 16 != 0.
+ * (entries below 2^-28 of the row's largest lose bits), P with half a step of
+ * fp16 of each weight and at least 2^-32 of the largest so far (single tokens:
+ * of each weight times its key's V scale, and of the largest of these).
+ * Neither K nor V may hold a NaN code at positions that some row of the
+ * sequence attends; at others, and in pages of other sequences, codes and
+ * scales are free.  The workspace is attn_batch_paged's, also the same one by
+ * turns, and the kernels are chosen as there.  Errors as attn_batch_paged;
+ * INVALID_ARG for a scale_rows that does not divide page_rows or NULL scales,
+ * UNSUPPORTED for head_dim % 16 != 0 and kv_dim % 16 != 0.
  */
 ATTN_API int attn_append_paged8(const void *q, void *q_out, const void *k_new, const void *v_new, attn_dtype_t dtype,
                                 attn_dtype_t q_out_dtype, void *k_pages, void *v_pages, uint8_t *k_scales,

@@ -229,3 +229,16 @@ def test_streams_and_graphs(cuda_lib):
     want = A.qk_norm_rope(q, k, H, G, w, w, table=table)
     grads = A.qk_norm_rope_backward(dq, dk, q, k, H, G, w, w, table=table)
     assert all(torch.equal(a, b) for a, b in zip(want + grads, got + back))
+
+
+@pytest.mark.parametrize("H,G,D,interleaved", [(5, 3, 128, False), (7, 1, 64, False), (3, 5, 80, True), (5, 2, 36, False)])
+def test_an_infinite_gradient_reaches_its_own_column_of_the_weights(cuda_lib, H, G, D, interleaved):
+    """Heads that do not fill a warp: the lanes that are left add nothing, not a product of zero and infinity."""
+    A = cuda_lib
+    w = torch.ones(D, device="cuda")
+    q, k, dq, dk = (make(3, n, D, F32, seed) for n, seed in ((H, 1), (G, 2), (H, 3), (G, 4)))
+    dq[2, (H - 1) * D + 9] = dk[1, (G - 1) * D + 3] = float("inf")
+    _, _, dwq, dwk = A.qk_norm_rope_backward(dq, dk, q, k, H, G, w, w, interleaved=interleaved)
+    for dw, at, x in ((dwq, 9, q[2, (H - 1) * D + 9]), (dwk, 3, k[1, (G - 1) * D + 3])):
+        assert dw[at] == float("inf") * torch.sign(x)
+        assert dw.isfinite().sum() >= D - 2  # (and the column that it would turn with)
