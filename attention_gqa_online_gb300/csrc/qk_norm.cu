@@ -131,8 +131,11 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
 #pragma unroll
         for (int i = 0; i < P; i += 2) {
           const float2 ra = mul2_of(va[i], va[i + 1], rms, rms), rb = mul2_of(vb[i], vb[i + 1], rms, rms);
-          const float2 oa = fma2_of(rb.x, rb.y, bs[i], bs[i + 1], mul2_of(ra.x, ra.y, ac[i], ac[i + 1]));
-          const float2 ob = fma2_of(ra.x, ra.y, as[i], as[i + 1], mul2_of(rb.x, rb.y, bc[i], bc[i + 1]));
+          float2 oa = mul2_of(ra.x, ra.y, ac[i], ac[i + 1]), ob = mul2_of(rb.x, rb.y, bc[i], bc[i + 1]);
+          if (u.turned) {  // (not + 0 * the other column: that may be an infinity)
+            oa = fma2_of(rb.x, rb.y, bs[i], bs[i + 1], oa);
+            ob = fma2_of(ra.x, ra.y, as[i], as[i + 1], ob);
+          }
           ya[i] = oa.x, ya[i + 1] = oa.y;
           yb[i] = ob.x, yb[i + 1] = ob.y;
         }
@@ -153,9 +156,12 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_vec_kernel(const NormArgs
         for (int i = 0; i < P; i += 2) {
           mul2(va[i], va[i + 1], rms, rms);  // x r
           mul2(vb[i], vb[i + 1], rms, rms);
-          // dz_a = dy_a c + dy_b s, dz_b = dy_b c - dy_a s
-          const float2 za = fma2_of(db[i], db[i + 1], s[i], s[i + 1], mul2_of(da[i], da[i + 1], c[i], c[i + 1]));
-          const float2 zb = fma2_of(da[i], da[i + 1], ns[i], ns[i + 1], mul2_of(db[i], db[i + 1], c[i], c[i + 1]));
+          // dz_a = dy_a c + dy_b s, dz_b = dy_b c - dy_a s; not turned: dy (not + 0 * the other column, as above)
+          float2 za = mul2_of(da[i], da[i + 1], c[i], c[i + 1]), zb = mul2_of(db[i], db[i + 1], c[i], c[i + 1]);
+          if (u.turned) {
+            za = fma2_of(db[i], db[i + 1], s[i], s[i + 1], za);
+            zb = fma2_of(da[i], da[i + 1], ns[i], ns[i + 1], zb);
+          }
           // dz x r: into dw, and times w into the mean
           const float2 pa = mul2_of(za.x, za.y, va[i], va[i + 1]), pb = mul2_of(zb.x, zb.y, vb[i], vb[i + 1]);
           fma2_acc(x0, x1, pa.x, pa.y, wa[i], wa[i + 1]);

@@ -242,3 +242,43 @@ def test_an_infinite_gradient_reaches_its_own_column_of_the_weights(cuda_lib, H,
     for dw, at, x in ((dwq, 9, q[2, (H - 1) * D + 9]), (dwk, 3, k[1, (G - 1) * D + 3])):
         assert dw[at] == float("inf") * torch.sign(x)
         assert dw.isfinite().sum() >= D - 2  # (and the column that it would turn with)
+
+
+def same_values(got, ref, tol):
+    """NaN where ref is, the same infinities, and finite values within tol."""
+    assert torch.equal(got.isnan(), ref.isnan()) and torch.equal(got.isinf(), ref.isinf())
+    assert torch.equal(got[ref.isinf()].double(), ref[ref.isinf()])
+    fine = ref.isfinite()
+    assert ((got.double() - ref).abs() <= tol)[fine].all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("D,R,interleaved", [(128, 0, False), (128, 0, True), (64, 32, False), (64, 32, True),
+                                             (80, 32, True), (96, 48, False), (36, 10, True)])
+def test_infinities_stay_in_columns_that_do_not_turn(cuda_lib, D, R, interleaved, dtype):
+    """A column behind rot_dim (or any, without a turn) meets no other one, but through its head's sums."""
+    A = cuda_lib
+    rows, H, G = 4, 3, 2
+    table = A.rope_table(rows, R) if R else None
+    th, pos = theta(R), torch.arange(rows).cuda()
+    how = dict(table=table, rot_dim=R or None, interleaved=interleaved)
+    w = 1 + 0.3 * make(1, 1, D, F32, 5)[0]
+    q, k, dq, dk = (make(rows, n, D, dtype, seed) for n, seed in ((H, 1), (G, 2), (H, 3), (G, 4)))
+    half = torch.finfo(dtype).eps / 2
+    for at in (R, R + 9, D - 2):
+        y, u = dq.clone(), dk.clone()
+        y[1, D + at], u[2, D + at] = float("inf"), -float("inf")
+        got = A.qk_norm_rope_backward(y, u, q, k, H, G, w, w, **how)
+        for i, (x, dy) in enumerate(((q, y), (k, u))):
+            dx, dw, _, _ = backward64(x, dy, w, D, pos, th, interleaved)
+            assert dw.isinf().sum() == 1 and dw.isnan().sum() == 0
+            # (Finite values: those of test_both_directions.  Here a coarse bound will do.)
+            same_values(got[i].view(dx.shape), dx, 2 * half * dx.abs() + 1e-4)
+            same_values(got[2 + i], dw, 1e-4)
+        x = q.clone()
+        x[1, D + at] = float("inf")
+        got = A.qk_norm_rope(x, k, H, G, w, w, **how)[0]
+        ref = forward64(x, w, D, pos, th, interleaved)[0]
+        assert ref.isnan().sum() == 1
+        same_values(got.view(ref.shape), ref, 2 * half * ref.abs() + 1e-4)
+    assert A.attn_get_status() == 0
