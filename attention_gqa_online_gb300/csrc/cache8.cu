@@ -69,7 +69,7 @@ __device__ __forceinline__ void make_row(const Append8Args& a, const TI* x, cons
         out.b[i] *= rms * wb[i];
       }
     }
-    if (hd.turn) {
+    if (hd.turn && hd.u.turned) {  // (others as they are, not + 0 * a column that may hold an infinity)
       float c[P], s[P];
       norm::load_turn(tab, a.R, hd.u, true, c, s);
 #pragma unroll
@@ -298,6 +298,7 @@ __device__ __forceinline__ void append_q(const Append8Args& a, int block) {
       as[i] *= wa[i];
     }
     const float inv_d = 1.f / (float)a.D;
+    const bool turned = a.R > 0 && u.turned;
     for (; h < a.H; h += step) {
       float va[P], vb[P], ya[P], yb[P];
       norm::unpack(ahead, va, vb);
@@ -308,8 +309,11 @@ __device__ __forceinline__ void append_q(const Append8Args& a, int block) {
 #pragma unroll
       for (int i = 0; i < P; i += 2) {
         const float2 ra = mul2_of(va[i], va[i + 1], r, r), rb = mul2_of(vb[i], vb[i + 1], r, r);
-        const float2 oa = fma2_of(rb.x, rb.y, bs[i], bs[i + 1], mul2_of(ra.x, ra.y, ac[i], ac[i + 1]));
-        const float2 ob = fma2_of(ra.x, ra.y, as[i], as[i + 1], mul2_of(rb.x, rb.y, bc[i], bc[i + 1]));
+        float2 oa = mul2_of(ra.x, ra.y, ac[i], ac[i + 1]), ob = mul2_of(rb.x, rb.y, bc[i], bc[i + 1]);
+        if (turned) {  // (not + 0 * the other column: that may be an infinity)
+          oa = fma2_of(rb.x, rb.y, bs[i], bs[i + 1], oa);
+          ob = fma2_of(ra.x, ra.y, as[i], as[i + 1], ob);
+        }
         ya[i] = oa.x, ya[i + 1] = oa.y;
         yb[i] = ob.x, yb[i + 1] = ob.y;
       }

@@ -280,3 +280,47 @@ def test_streams_and_graphs(cuda_lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(q1, q2) and torch.equal(k1, k2) and torch.equal(v1, v2)
+
+
+@pytest.mark.parametrize("src,pad", [(F32, 0), (BF16, 8), (F16, 0), (BF16, 3)])  # (3: rows that do not begin on 16 bytes)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,R", [(128, 64), (64, 16), (96, 48), (128, 0), (64, 0)])
+def test_infinities_stay_in_columns_that_do_not_turn(cuda_lib, D, R, interleaved, src, pad):
+    """They become 57344 in the cache and stay infinities in Q; the columns beside them are as without them, but for the
+    scale of their block."""
+    A = cuda_lib
+    n, H, G, sr = 24, 4, 2, 4
+    b = Batch8([n], [n], H, G, D, 8, sr, seed=D)
+    k, v, q = rows_of(b, G, src, 1, pad), rows_of(b, G, src, 2, pad), rows_of(b, H, src, 3, pad)
+    inf = float("inf")
+    where = [(4 * i + 1, D + c, inf if i % 2 else -inf) for i, c in enumerate((R, R + 3, R + 9, D - 1))]
+    for row, col, x in where:
+        k[row, col] = v[row, col] = x
+        q[row, D + col] = x
+    table = A.rope_table(n, R) if R else None
+    out = A.append_paged8(b.object(A), k, v, b.cache(A), q=q, table=table, rot_dim=R or None, interleaved=interleaved)
+    assert A.attn_get_status() == 0
+    pos, th = positions(b), theta(R)
+    sl = b.slots(0, 0, n)
+    hit = torch.zeros(n, G * D, dtype=torch.bool, device="cuda")
+    for row, col, x in where:
+        hit[row, col] = True
+    for name, x in (("k", turn(k.reshape(n, G, D), pos, th, interleaved)), ("v", v.double().reshape(n, G, D))):
+        got = b.values(name)[sl]
+        assert got.isfinite().all()
+        x = x.reshape(n, -1)
+        assert torch.equal(got[hit], torch.sign(x[hit]) * 57344)
+        scales = b.scales[name][sl[::sr] // sr].double() - 127
+        infinite = hit.view(-1, sr, G, D).any(1).any(-1)
+        amax = torch.where(hit, torch.zeros_like(x), x).abs().view(-1, sr, G, D).amax((1, 3))
+        low, high = exp_for(amax * (1 - 2.0 ** -20)), exp_for(amax * (1 + 2.0 ** -20))  # (eight roundings of fp32)
+        assert (scales[infinite] == 7).all() and ((scales == low) | (scales == high) | infinite).all()
+        size = torch.exp2(scales).repeat_interleave(sr, 0).repeat_interleave(D, 1)
+        tol = 2.0 ** -20 + torch.maximum(x.abs() * 1.001 * 2.0 ** -4, size * 2.0 ** -10)
+        assert ((got - x).abs() <= tol)[~hit].all()
+    ref = turn(q.reshape(n, H, D), pos, th, interleaved).reshape(n, -1)
+    assert torch.equal(out.isinf(), ref.isinf()) and not out.isnan().any()
+    fine = ref.isfinite()
+    # (A result is made of two values, of up to 6 here.)
+    assert torch.equal(out[~fine].double(), ref[~fine])
+    assert ((out.double() - ref).abs() <= torch.finfo(out.dtype).eps / 2 * ref.abs() + 2.0 ** -18)[fine].all()
