@@ -832,8 +832,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       constexpr uint32_t fmt = kHalf ? tc::kFmtF16 : tc::kFmtBF16;
       // Codes: operands are whole when the first block's four warps have written their parts and, in a pair, the second
       // block's, whose idle issue warps pass that on (*_made): released to the cluster by a thread that has no loads in
-      // flight, which a release would wait for.  (The issuing thread reads none of it: the tensor cores do, past L1, after
-      // tcgen05's own fence; an acquire for the cluster would only invalidate L1: 470 us for 444.)
+      // flight, which a release would wait for, and acquired for the cluster by the warp that issues the products (the
+      // test after the wait, whose phase cannot end before that warp goes on; as a fence it took 2 chunks of 512 from
+      // 444 to 470 us, this way nothing).
+      auto wait_operand = [&](uint64_t* bar, int phase) {
+        const bool ok = wait(bar, phase);
+        if constexpr (C8 && PAIR) return ok && __all_sync(0xffffffffu, mbar_test_wait_cluster(bar, (unsigned)(phase & 1))) != 0;
+        return ok;
+      };
       if (rank != 0) {
         if constexpr (C8) {
           bool ok = true;
@@ -866,10 +872,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int n = d.n;
           const int qb = x % kQBufs;
           const uint64_t dq = dq0 + (uint64_t)(qb * (L::q_bytes >> 4));
-          ok = wait(&sm.q_ready[qb], x / kQBufs);
+          ok = wait_operand(&sm.q_ready[qb], x / kQBufs);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = wait(&sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
+            ok = wait_operand(&sm.k_full[slot], j / L::slots) && (j < 2 || wait(&sm.s_free[b], (j - 2) >> 1));
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t dk = dk0 + (uint64_t)(slot * (L::k_bytes >> 4));
@@ -895,7 +901,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (x > 0) ok = wait(&sm.o_free, x - 1);
           for (int i = 0; ok && i < n; ++i, ++j) {
             const int slot = j % L::slots, b = j & 1;
-            ok = wait(&sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
+            ok = wait_operand(&sm.v_full[slot], j / L::slots) && wait(&sm.p_ready[b], j >> 1);
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t dv = dv0 + (uint64_t)(slot * (L::v_bytes >> 4));

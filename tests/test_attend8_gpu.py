@@ -238,3 +238,29 @@ def test_refusals(cuda_lib):
         A.append_paged8(batch, b.q[:, :64], b.q[:, :64], other.cache(A))
     with pytest.raises(AttributeError):
         cache.scale_rows = 4
+
+
+def test_blocks_of_a_pair_read_each_others_latest_operands(cuda_lib):
+    """Each block of a pair makes half of every operand tile and the first one multiplies all of them: with other codes in
+    the same pages at every replay, results are those of the codes of that replay."""
+    A = cuda_lib
+    b = Batch8([512, 300], [3000, 2100], 8, 2, 128, 64, 16, dtype=BF16, seed=12)
+    batch, cache = b.object(A), b.cache(A)
+    out = torch.empty_like(b.q)
+    graph = torch.cuda.CUDAGraph()
+    A.attend_paged8(batch, b.q, cache, out=out)
+    with torch.cuda.graph(graph):
+        A.attend_paged8(batch, b.q, cache, out=out)
+    g = torch.Generator(device="cuda").manual_seed(13)
+    codes = {x: b.codes[x].clone() for x in "kv"}
+    for step in range(40):
+        flip = torch.randint(0, 2, (2, b.codes["k"].shape[0], 1), generator=g, device="cuda", dtype=torch.uint8) * 0x80
+        for x, f in zip("kv", flip):  # other signs of whole rows
+            b.codes[x].copy_(codes[x] ^ f)
+        graph.replay()
+        got = out.clone()
+        assert torch.equal(got, A.attend_paged8(batch, b.q, cache)) and A.attn_get_status() == 0
+        if step % 10 == 0:
+            own = ~b.k.isnan()
+            b.k, b.v = (torch.where(own, b.values(x).to(BF16), float("nan")) for x in "kv")
+            check(b, got, attend64(b))
