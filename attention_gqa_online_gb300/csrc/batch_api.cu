@@ -156,16 +156,16 @@ extern "C" int attn_append_paged(const void* q, void* q_out, const void* k_new, 
                                  attn_stream_t stream) {
   if (!dtype_ok(dtype) || !dtype_ok(cache_dtype) || !layout_ok(layout)) return ATTN_ERR_INVALID_ARG;
   if (!heads_ok(num_heads > 0 ? num_heads : num_kv_heads, num_kv_heads, head_dim)) return ATTN_ERR_INVALID_ARG;
-  if ((num_heads == 0) != (q == nullptr)) return ATTN_ERR_INVALID_ARG;
   if (!paged_ok(page_rows, num_pages, max_blocks)) return ATTN_ERR_INVALID_ARG;
   const uint64_t w = (uint64_t)num_kv_heads * head_dim, wq = (uint64_t)num_heads * head_dim;
   if (kv_dim < w || k_stride < w || v_stride < w) return ATTN_ERR_INVALID_ARG;
-  if (num_heads > 0 && (q_stride < wq || q_out_stride < wq || q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (num_heads > 0 && (q_stride < wq || q_out_stride < wq)) return ATTN_ERR_INVALID_ARG;
   if (rot_dim % 2 != 0 || rot_dim > head_dim || (rot_dim > 0 && (table == nullptr || table_rows == 0)))
     return ATTN_ERR_INVALID_ARG;
   // (The search of a row's sequence adds to n_seqs in 32 bits.)
   if (total_rows > 0x7fffffffu || n_seqs > (1u << 30)) return ATTN_ERR_INVALID_ARG;
-  if (total_rows == 0 || n_seqs == 0) return ATTN_OK;
+  if (total_rows == 0 || n_seqs == 0) return ATTN_OK;  // (tensors of no rows have no address)
+  if ((num_heads == 0) != (q == nullptr) || (num_heads > 0 && q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
   if (k_new == nullptr || v_new == nullptr || k_pages == nullptr || v_pages == nullptr || block_table == nullptr ||
       q_start == nullptr || kv_len == nullptr)
     return ATTN_ERR_INVALID_ARG;

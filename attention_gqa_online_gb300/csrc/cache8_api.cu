@@ -159,17 +159,17 @@ extern "C" int attn_append_paged8(const void* q, void* q_out, const void* k_new,
   if (!dtype_ok(dtype) || !dtype_ok(weight_dtype) || !layout_ok(layout)) return ATTN_ERR_INVALID_ARG;
   if (!cache_ok(num_kv_heads, head_dim, kv_dim, page_rows, num_pages, max_blocks, scale_rows))
     return ATTN_ERR_INVALID_ARG;
-  if (num_heads > (1u << 20) || (num_heads == 0) != (q == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (num_heads > (1u << 20)) return ATTN_ERR_INVALID_ARG;
   if (num_heads == 0 && q_weight != nullptr) return ATTN_ERR_INVALID_ARG;
   if (num_heads > 0 && q_out_dtype != ATTN_DT_BF16 && q_out_dtype != ATTN_DT_F16) return ATTN_ERR_INVALID_ARG;
   const uint64_t w = (uint64_t)num_kv_heads * head_dim, wq = (uint64_t)num_heads * head_dim;
-  if (k_stride < w || v_stride < w || (num_heads > 0 && (q_stride < wq || q_out_stride < wq || q_out == nullptr)))
-    return ATTN_ERR_INVALID_ARG;
+  if (k_stride < w || v_stride < w || (num_heads > 0 && (q_stride < wq || q_out_stride < wq))) return ATTN_ERR_INVALID_ARG;
   if (!turn_ok(rot_dim, head_dim, table) || (rot_dim > 0 && table_rows == 0)) return ATTN_ERR_INVALID_ARG;
   if ((q_weight != nullptr || k_weight != nullptr) && !eps_ok(eps)) return ATTN_ERR_INVALID_ARG;
   // (The search of a row's sequence adds to n_seqs in 32 bits.)
   if (total_rows > 0x7fffffffu || n_seqs > (1u << 30)) return ATTN_ERR_INVALID_ARG;
-  if (total_rows == 0 || n_seqs == 0) return ATTN_OK;
+  if (total_rows == 0 || n_seqs == 0) return ATTN_OK;  // (tensors of no rows have no address)
+  if ((num_heads == 0) != (q == nullptr) || (num_heads > 0 && q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
   if (k_new == nullptr || v_new == nullptr || k_pages == nullptr || v_pages == nullptr || k_scales == nullptr ||
       v_scales == nullptr || block_table == nullptr || q_start == nullptr || kv_len == nullptr)
     return ATTN_ERR_INVALID_ARG;

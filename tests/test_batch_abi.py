@@ -273,3 +273,10 @@ def test_refusals_run_with_the_device_hidden():
                        text=True, timeout=900)
     assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-4000:]
     assert " passed" in r.stdout
+
+
+@hidden
+def test_append_of_no_rows_with_queries_is_noop(lib):
+    """Tensors of no rows have no address."""
+    assert append_call(lib, rows=0, q=None, q_out=None, k=None, v=None) == 0
+    assert append_call(lib, n=0, q=None, q_out=None, qs=None, kl=None) == 0

@@ -199,3 +199,10 @@ def test_attend_unsupported(lib, kw):
 def test_attend_of_nothing_is_noop(lib):
     for kw in (dict(rows=0), dict(n=0)):
         assert attend_call(lib, q=None, ks=None, **kw) == 0
+
+
+@hidden
+def test_append_of_no_rows_with_queries_is_noop(lib):
+    """Tensors of no rows have no address."""
+    for kw in (dict(rows=0), dict(n=0)):
+        assert append_call(lib, q=None, qo=None, k=None, v=None, **kw) == 0

@@ -324,3 +324,23 @@ def test_infinities_stay_in_columns_that_do_not_turn(cuda_lib, D, R, interleaved
     # (A result is made of two values, of up to 6 here.)
     assert torch.equal(out[~fine].double(), ref[~fine])
     assert ((out.double() - ref).abs() <= torch.finfo(out.dtype).eps / 2 * ref.abs() + 2.0 ** -18)[fine].all()
+
+
+def test_calls_without_rows(cuda_lib):
+    """Q, K and V of no rows, through the package: results of no rows, and an unchanged cache; nor any rows read."""
+    A = cuda_lib
+    b = Batch8([0, 0], [5, 9], 4, 2, 64, 8, 8, dtype=BF16, seed=3)
+    w, table = torch.ones(64, dtype=BF16, device="cuda"), A.rope_table(16, 64)
+    q, k, v = (torch.empty(0, n * 64, dtype=BF16, device="cuda") for n in (4, 2, 2))
+    before = [x.clone() for d in (b.codes, b.scales) for x in d.values()]
+    batch, cache = b.object(A), b.cache(A)
+    out = A.append_paged8(batch, k, v, cache, q=q, table=table, q_weight=w, k_weight=w)
+    assert out.shape == (0, 256)
+    assert A.append_paged8(batch, k, v, cache, q=q, q_out=out, table=table) is out
+    assert A.attend_paged8(batch, out, cache, window=4, sinks=1).shape == (0, 256)
+    A.read_paged8(batch, cache, b.dev([0, 0, 0]), k, v)
+    assert all(torch.equal(x, y) for x, y in zip(before, [x for d in (b.codes, b.scales) for x in d.values()]))
+    pools = torch.zeros_like(b.k), torch.zeros_like(b.v)
+    out = A.append_paged(batch, k, v, *pools, q=q, table=table)
+    assert out.shape == (0, 256) and A.attend_paged(batch, out, *pools).shape == (0, 256)
+    assert A.attn_get_status() == 0
