@@ -596,8 +596,16 @@ def attn_selftest_warp_wait(lanes, timeout_us=10000, stream=None):
     _check(fn(timeout_us, _u32_addr(lanes, "lanes"), _stream(stream)), "attn_selftest_warp_wait")
 
 
+def attn_selftest_short_wait(lanes, timeout_us=10000, stream=None):
+    """As attn_selftest_warp_wait, for the batched kernels' other wait (see attn_gqa.h)."""
+    fn = load_library().attn_selftest_short_wait
+    fn.restype = ctypes.c_int
+    fn.argtypes = [_u32, _vp, _vp]
+    _check(fn(timeout_us, _u32_addr(lanes, "lanes"), _stream(stream)), "attn_selftest_short_wait")
+
+
 def attn_selftest_batch_wait(limit_ns=0):
-    """Limit of the waits inside later attn_batch_paged calls (0: the usual one; see attn_gqa.h)."""
+    """Limit of the waits inside later batched paged attention calls (0: the usual one; see attn_gqa.h)."""
     fn = load_library().attn_selftest_batch_wait
     fn.restype = ctypes.c_int
     fn.argtypes = [_u32]

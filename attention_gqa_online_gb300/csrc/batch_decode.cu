@@ -720,14 +720,14 @@ int launch_decode_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s
       !make_tmap(&tm_v8, a.v_pages, 3, dims, strides, eight, true, kSwizzle128, l2) ||
       !make_tmap(&tm_v1, a.v_pages, 3, dims, strides, one_row, true, kSwizzle128, l2))
     return ATTN_ERR_CUDA;
-  const void* kern;
-  if constexpr (C8)
-    kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, true, true>);
-  else
-    kern = a.sinks > 0 ? reinterpret_cast<const void*>(batch_decode_kernel<T, D, false, true>)
-                       : reinterpret_cast<const void*>(batch_decode_kernel<T, D, false, false>);
+  auto of_form = [&](auto brief) {
+    constexpr bool B = decltype(brief)::value;
+    if (C8 || a.sinks > 0) return reinterpret_cast<const void*>(batch_decode_kernel<T, D, C8, true, B>);
+    return reinterpret_cast<const void*>(batch_decode_kernel<T, D, C8, C8, B>);  // (codes have one form)
+  };
+  const void* kern = of_form(std::false_type{});
   if constexpr (std::is_same<T, __nv_bfloat16>::value)  // the failure-path test
-    if (a.wait_ns != 0 && a.sinks == 0) kern = reinterpret_cast<const void*>(batch_decode_kernel<T, D, C8, C8, true>);
+    if (a.wait_ns != 0) kern = of_form(std::true_type{});
   const size_t smem = sizeof(S) + 1024;
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;
   BatchArgs aa = a;

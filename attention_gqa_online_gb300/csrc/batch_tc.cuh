@@ -508,18 +508,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const unsigned long long limit = BRIEF ? a.wait_ns : kWaitLimitNs;
   // The forms with more code wait in less of it (17 ragged chunks with a bias 218 us, 202 so; a prompt of 8192 with a window
   // and first positions 237 and 226); the plainest one does not gain (prompt of 8192 395 and 405).
-  constexpr bool kShortWaits = !BRIEF && (C8 || SINKS || MODE != 0);
+  constexpr bool kShortWaits = C8 || SINKS || MODE != 0;
   auto wait = [&](uint64_t* bar, int phase) {
-    if constexpr (kShortWaits)
-      return __all_sync(0xffffffffu, wait_phase_short(bar, (unsigned)(phase & 1), a.status, &sm.abort)) != 0;
-    else
-      return warp_wait<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
+    return warp_wait<BRIEF, kShortWaits>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
   };
   // Without the vote, where no answer is asked for, nothing warp-wide follows at once and a __syncwarp comes before a lane
   // arrives for the warp (17 ragged chunks with a bias, 16 heads: 223 us with votes there too, 219 this way).
   auto lane_wait = [&](uint64_t* bar, int phase) {
     if constexpr (kShortWaits)
-      wait_phase_short(bar, (unsigned)(phase & 1), a.status, &sm.abort);
+      wait_phase_short<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, (unsigned)limit);
     else
       wait_phase<BRIEF>(bar, (unsigned)(phase & 1), a.status, &sm.abort, limit);
   };
@@ -1512,16 +1509,16 @@ int launch_tc_t(const BatchArgs& a, int blocks, int box_rows, cudaStream_t s) {
     if (!make_tmap(&tm_q, a.q, 3, qdims, qstrides, qbox, true, kSwizzle128)) return ATTN_ERR_CUDA;
   }
   ScoreMap sc = score_map(a);
-  const void* kern;
-  if (a.softcap > 0.f)
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR, FULL, SINKS, C8>);
-  else if (a.slopes != nullptr || !(sc.scale2 >= FLT_MIN))
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL, SINKS, C8>);
-  else
-    kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS, C8>);
-  if constexpr (std::is_same<T, __nv_bfloat16>::value && (C8 || !SINKS))  // the failure-path test
-    if (a.wait_ns != 0 && a.sinks == 0 && a.softcap == 0.f && a.slopes == nullptr && sc.scale2 >= FLT_MIN)
-      kern = reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS, C8, true>);
+  auto of_mode = [&](auto brief) {
+    constexpr bool B = decltype(brief)::value;
+    if (a.softcap > 0.f) return reinterpret_cast<const void*>(batch_tc_kernel<T, D, 2, PAIR, FULL, SINKS, C8, B>);
+    if (a.slopes != nullptr || !(sc.scale2 >= FLT_MIN))
+      return reinterpret_cast<const void*>(batch_tc_kernel<T, D, 1, PAIR, FULL, SINKS, C8, B>);
+    return reinterpret_cast<const void*>(batch_tc_kernel<T, D, 0, PAIR, FULL, SINKS, C8, B>);
+  };
+  const void* kern = of_mode(std::false_type{});
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)  // the failure-path test
+    if (a.wait_ns != 0) kern = of_mode(std::true_type{});
   const size_t smem = sizeof(TcSmem<D, PAIR, C8>) + 1024;
   static_assert(sizeof(TcSmem<D, PAIR, C8>) + 1024 <= 227 * 1024, "shared memory of a block");
   if (!set_smem_limit(kern, smem)) return ATTN_ERR_CUDA;

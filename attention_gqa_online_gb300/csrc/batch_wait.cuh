@@ -32,15 +32,17 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, unsigned parity, unsig
 
 // As wait_phase, in half the code: for kernels whose roles together outgrow the instruction cache.  (The limit is
 // looked at every time the wait's own suspension ends.)
-__device__ __forceinline__ bool wait_phase_short(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag) {
+template <bool BRIEF = false>
+__device__ __forceinline__ bool wait_phase_short(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag,
+                                                 unsigned limit_ns = (unsigned)kWaitLimitNs) {
   unsigned t0 = 0;
 #pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
+  while (!(BRIEF ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
     if (*abort_flag != 0) return false;
     unsigned now;
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));  // (wraps after four seconds)
     if (t0 == 0) t0 = now | 1u;
-    if (now - t0 > (unsigned)kWaitLimitNs && now != t0 - 1u) {
+    if (now - t0 > limit_ns && now != t0 - 1u) {
       record_status(status, ATTN_ERR_TIMEOUT);
       *abort_flag = 1;
       return false;
@@ -53,10 +55,15 @@ __device__ __forceinline__ bool wait_phase_short(uint64_t* bar, unsigned parity,
 // phase complete, or the block's abort flag set, at different times, so they
 // meet again here, with one answer for all, before any of them arrives
 // somewhere for the warp, takes part in a warp-wide instruction or leaves.
-template <bool BRIEF = false>
+template <bool BRIEF = false, bool SHORT = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned* status, volatile int* abort_flag,
                                           unsigned long long limit_ns = kWaitLimitNs) {
-  return __all_sync(0xffffffffu, wait_phase<BRIEF>(bar, parity, status, abort_flag, limit_ns));
+  bool ok;
+  if constexpr (SHORT)
+    ok = wait_phase_short<BRIEF>(bar, parity, status, abort_flag, (unsigned)limit_ns);
+  else
+    ok = wait_phase<BRIEF>(bar, parity, status, abort_flag, limit_ns);
+  return __all_sync(0xffffffffu, ok) != 0;
 }
 // Is the block's pipeline whole?  One answer for the warp, too.
 __device__ __forceinline__ bool warp_whole(volatile int* abort_flag) {

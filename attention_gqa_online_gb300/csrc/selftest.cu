@@ -3,7 +3,7 @@
 // that nothing will ever complete.  The wait gives up after the requested
 // limit, the kernel records ATTN_ERR_TIMEOUT in the status word and returns;
 // no fault, no hang, and the CUDA context stays usable.  A second test runs
-// the warp-wide wait of the batched kernels into the same end.
+// both forms of the warp-wide wait of the batched kernels into the same end.
 #include "../../include/attn_gqa.h"
 #include "batch.h"
 #include "batch_wait.cuh"
@@ -30,6 +30,7 @@ __global__ void wait_never_kernel(unsigned* status, unsigned long long limit_ns)
 // after the other, see either first.  lanes[w] = the lanes of warp w whose wait
 // succeeded.
 constexpr int kWaitWarps = 8;
+template <bool SHORT>
 __global__ void warp_wait_kernel(unsigned* status, unsigned* lanes, unsigned long long limit_ns) {
   __shared__ uint64_t never, late;
   __shared__ int abort_flag;
@@ -43,11 +44,11 @@ __global__ void warp_wait_kernel(unsigned* status, unsigned* lanes, unsigned lon
   __syncthreads();
   bool ok;
   if (warp == 0) {
-    ok = warp_wait(&never, 0, status, &abort_flag, limit_ns);
+    ok = warp_wait<false, SHORT>(&never, 0, status, &abort_flag, limit_ns);
     if (lane == 0) mbar_arrive(&late);
   } else {
     __nanosleep(lane * 100);
-    ok = warp_wait(&late, 0, status, &abort_flag);
+    ok = warp_wait<false, SHORT>(&late, 0, status, &abort_flag);
   }
   const unsigned mask = __ballot_sync(0xffffffffu, ok);
   if (lane == 0) lanes[warp] = mask;
@@ -71,11 +72,20 @@ extern "C" int attn_selftest_batch_wait(uint32_t limit_ns) {
   return ATTN_OK;
 }
 
-extern "C" int attn_selftest_warp_wait(uint32_t timeout_us, uint32_t* lanes, attn_stream_t stream) {
+template <bool SHORT>
+static int selftest_warp_wait(uint32_t timeout_us, uint32_t* lanes, attn_stream_t stream) {
   if (timeout_us == 0 || timeout_us > 1000000u || lanes == nullptr) return ATTN_ERR_INVALID_ARG;
   unsigned* st = attn::device_status_word();
   if (st == nullptr) return ATTN_ERR_CUDA;
-  attn::warp_wait_kernel<<<1, 32 * attn::kWaitWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  attn::warp_wait_kernel<SHORT><<<1, 32 * attn::kWaitWarps, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       st, lanes, (unsigned long long)timeout_us * 1000ull);
   return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_selftest_warp_wait(uint32_t timeout_us, uint32_t* lanes, attn_stream_t stream) {
+  return selftest_warp_wait<false>(timeout_us, lanes, stream);
+}
+
+extern "C" int attn_selftest_short_wait(uint32_t timeout_us, uint32_t* lanes, attn_stream_t stream) {
+  return selftest_warp_wait<true>(timeout_us, lanes, stream);
 }
