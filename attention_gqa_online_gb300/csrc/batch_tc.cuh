@@ -110,10 +110,11 @@ struct PieceDesc {
   int row0, q_len, len, pfx;
   int first_row;   // first flattened row of this block
   int rows;        // valid rows from there on, at most 128
-  int lo_min, lo_max, hi_min, hi_max, se;
+  int lo_min, lo_max, hi_min, hi_max;
   int first, last, slot0;  // the item's pieces (plan::Piece)
-  int tile_last, n, ns, skip;  // tiles tile_last, tile_last - 1, ... (n of them) of the item's (plan::tile_at)
+  int tile_last, n;  // tiles tile_last, tile_last - 1, ... (n of them) of the item's (plan::tile_at)
   int pos_min;       // position of the block's first row
+  int se, ns, skip;  // with first positions (plan::BlockKeys); other calls leave them as they are
 };
 
 // Shared memory of one block.  A pair splits the keys of a K tile and the
@@ -631,142 +632,167 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       return true;
     };
     auto barrier_of = [&](uint64_t* full) { return PAIR ? in_leader(smem_u32(full)) : smem_u32(full); };
-    if (warp == 0 || (C8 && warp == 3)) {
-      // ---------------------------------------------------------- planner, Q and K producer (codes: V producer, too)
+    struct Planned {
+      plan::Piece p;
+      int first_row, rows;  // this block's of p: 128 flattened rows from first_row on
+    };
+    using Walk = plan::Walker<L::rows, kTcKeys, SINKS>;
+    // Planner: descriptor x, of the next piece.  False: the role ends.  (A wait that ran out ends it at once: writing over a
+    // descriptor or a slot in use, or arriving twice in one phase, would turn a late block into a fault.)
+    auto plan_piece = [&](Walk& walk, Planned& at, int x) {
+      plan::Piece& p = at.p;
+      int &first_row = at.first_row, &rows = at.rows;
+      bool more;
+      while (true) {
+        more = walk.next(p) && warp_whole(&sm.abort);
+        first_row = p.b * L::rows + rank * kTcRows;
+        rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
+        if (!more || p.t1 != p.t0) break;
+        for (int r = lane >> 2; r < rows; r += 8) {  // rows without keys
+          const int f = first_row + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
+          T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * hd;
+          for (int u = lane & 3; u < hd / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      if (x >= kDescs && !wait(&sm.desc_free[x % kDescs], x / kDescs - 1)) return false;
+      if (lane == 0) {
+        PieceDesc& d = sm.desc[x % kDescs];
+        d.end = !more;
+        if (more) {
+          d.whole = p.whole;
+          d.seq = p.s;
+          d.g = p.g;
+          d.slot = p.slot;
+          d.first = p.first;
+          d.last = p.last;
+          d.slot0 = p.slot0;
+          d.row0 = p.q.row0;
+          d.q_len = p.q.q_len;
+          d.len = p.q.len;
+          d.pfx = p.q.pfx;
+          d.first_row = first_row;
+          d.rows = rows;
+          d.lo_min = p.k.lo_min;
+          d.lo_max = p.k.lo_max;
+          d.hi_min = p.k.hi_min;
+          d.hi_max = p.k.hi_max;
+          d.tile_last = plan::first_tile<SINKS>(p.k) + p.t1 - 1;
+          d.n = p.t1 - p.t0;
+          d.pos_min = p.q.len - p.q.q_len + plan::token_of(a, first_row);
+          if (SINKS) {
+            d.se = p.k.se;
+            d.ns = p.k.ns;
+            d.skip = p.k.skip;
+          }
+        }
+        mbar_arrive(&sm.desc_full[x % kDescs]);
+      }
+      __syncwarp();
+      return more;
+    };
+    // Q block of piece x, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row only
+    // feeds itself, and those rows are not stored).  False: its buffer did not fall free.
+    auto load_q = [&](const Planned& at, int x) {
+      const plan::Piece& p = at.p;
+      const int first_row = at.first_row, rows = at.rows;
+      const int qb = x % kQBufs;
+      if (x >= kQBufs && !wait(&sm.q_free[qb], x / kQBufs - 1)) return false;
+      if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
+        if (lane == 0) {
+          constexpr bool kShared = PAIR && !C8;  // both blocks' halves complete on the first one's barrier
+          uint64_t* full = C8 ? &sm.q_raw[qb] : &sm.q_ready[qb];
+          const uint32_t bar = kShared ? barrier_of(full) : smem_u32(full);
+          if (C8 || rank == 0) mbar_arrive_expect_tx(full, (unsigned)(kShared ? 2 : 1) * L::q_bytes);
+#pragma unroll
+          for (int c = 0; c < L::chunks; ++c)
+            load_3d<kShared>(sm.q[qb] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + plan::token_of(a, first_row), bar);
+        }
+        __syncwarp();
+      } else {
+        constexpr int kUnits = D / 8, kRowsPer = 32 / kUnits;  // units of a row over the lanes
+        const int u = lane % kUnits;
+        unsigned char* qt = sm.q[qb] + (u >> 3) * L::q_chunk;
+        const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * hd;
+        const bool inside = 8 * u < hd;  // columns past the head are zeros
+        for (int r = lane / kUnits; r < rows; r += kRowsPer) {
+          const int f = first_row + r, t = plan::token_of(a, f);
+          cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)),
+                     src + (long long)t * a.q_stride + (f - t * a.gs) * hd + (inside ? 8 * u : 0), inside ? 16u : 0u);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(C8 ? &sm.q_raw[qb] : &sm.q_ready[qb]);
+      }
+      return true;
+    };
+    if (C8 && (warp == 0 || warp == 3)) {
+      // ---------------------------------------------------------- codes: planner, Q and K producer; V producer
+      if constexpr (C8) {
+        const int v = warp == 3 ? 1 : 0;
+        if (lane == 0) prefetch_tmap(v ? &tm_v : &tm_k);
+        Walk walk(a, sm.start);
+        Planned at;
+        int x = 0, J = 0;
+        for (bool ok = true; ok; ++x) {
+          if (v) {
+            if (!next_piece(x)) break;
+          } else {
+            if (!plan_piece(walk, at, x)) break;
+            if (!load_q(at, x)) break;
+          }
+          // (One piece of code for K and V.)
+          const PieceDesc& d = sm.desc[x % kDescs];
+          Parts w = open_parts(v ? kTcKeys : L::k_rows, d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip,
+                               PAIR && !v ? rank * L::k_rows : 0, d.seq);
+          ok = load_codes(w, v, d.g, J);
+          if (v && ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
+        }
+        if (lane == 0) {
+          sm.issued[v] = J;
+          if (!v) sm.issued[2] = PAIR || q_box ? x : 0;
+        }
+      }
+    } else if (!C8 && warp == 0) {
+      // ---------------------------------------------------------- planner, Q and K producer
       if (lane == 0) {
         prefetch_tmap(&tm_k);
         if (q_box) prefetch_tmap(&tm_q);
       }
-      plan::Walker<L::rows, kTcKeys, SINKS> walk(a, sm.start);
-      plan::Piece p;
+      Walk walk(a, sm.start);
+      Planned at;
+      const plan::Piece& p = at.p;
       int x = 0, J = 0;
-      // A wait that ran out ends the role at once: writing over a descriptor or a slot in use, or arriving twice in one
-      // phase, would turn a late block into a fault.
-      bool ok = true;
-      while (ok) {
-        if (C8 && warp == 3) {
-          if (!next_piece(x)) break;
-        } else {
-          const bool more = walk.next(p) && warp_whole(&sm.abort);
-          // This block's rows: 128 flattened rows from first_row on.
-          const int first_row = p.b * L::rows + rank * kTcRows;
-          const int rows = more ? max(0, min(kTcRows, p.q.q_len * a.gs - first_row)) : 0;
-          if (more && p.t1 == p.t0) {  // rows without keys
-            for (int r = lane >> 2; r < rows; r += 8) {
-              const int f = first_row + r, t = plan::token_of(a, f), h = p.g * a.gs + f - t * a.gs;
-              T* dst = static_cast<T*>(a.out) + (long long)(p.q.row0 + t) * a.out_stride + (long long)h * hd;
-              for (int u = lane & 3; u < hd / 8; u += 4) *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            continue;
-          }
-          if (x >= kDescs) ok = wait(&sm.desc_free[x % kDescs], x / kDescs - 1);
+      for (bool ok = true; ok && plan_piece(walk, at, x); ++x) {
+        // The piece's first page parts are looked up while its Q buffer falls free.
+        const int n = p.t1 - p.t0, col = FULL ? p.g * D : 0;
+        Parts w = open_parts(L::k_rows, n, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t1 - 1, p.k.ns,
+                             p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
+        if (!load_q(at, x)) break;
+        for (int i = 0; i < n; ++i, ++J) {
+          const int row = part_row(w, i), slot = J % L::slots;
+          if (J >= L::slots) ok = wait(&sm.k_empty[slot], J / L::slots - 1);
           if (!ok) break;
-          if (lane == 0) {
-            PieceDesc& d = sm.desc[x % kDescs];
-            d.end = !more;
-            if (more) {
-              d.whole = p.whole;
-              d.seq = p.s;
-              d.g = p.g;
-              d.slot = p.slot;
-              d.first = p.first;
-              d.last = p.last;
-              d.slot0 = p.slot0;
-              d.row0 = p.q.row0;
-              d.q_len = p.q.q_len;
-              d.len = p.q.len;
-              d.pfx = p.q.pfx;
-              d.first_row = first_row;
-              d.rows = rows;
-              d.lo_min = p.k.lo_min;
-              d.lo_max = p.k.lo_max;
-              d.hi_min = p.k.hi_min;
-              d.hi_max = p.k.hi_max;
-              d.se = p.k.se;
-              d.tile_last = plan::first_tile<SINKS>(p.k) + p.t1 - 1;
-              d.ns = p.k.ns;
-              d.skip = p.k.skip;
-              d.n = p.t1 - p.t0;
-              d.pos_min = p.q.len - p.q.q_len + plan::token_of(a, first_row);
-            }
-            mbar_arrive(&sm.desc_full[x % kDescs]);
-          }
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
           __syncwarp();
-          if (!more) break;
-          // The piece's first page parts are looked up while its Q buffer falls free.
-          const int n = p.t1 - p.t0, col = FULL ? p.g * D : 0;
-          Parts w;
-          if constexpr (!C8)
-            w = open_parts(L::k_rows, n, p.k.se, p.k.lo_min, p.k.hi_max, plan::first_tile<SINKS>(p.k) + p.t1 - 1, p.k.ns,
-                           p.k.skip, PAIR ? rank * L::k_rows : 0, p.s);
-          // Q block, 128-byte swizzle.  Rows past the piece's are left as they are or hold other rows (an MMA row
-          // only feeds itself, and those rows are not stored).
-          const int qb = x % kQBufs;
-          if (x >= kQBufs) ok = wait(&sm.q_free[qb], x / kQBufs - 1);
-          if (!ok) break;
-          if (PAIR || q_box) {  // whole tokens a block: one box per column chunk
-            if (lane == 0) {
-              constexpr bool kShared = PAIR && !C8;  // both blocks' halves complete on the first one's barrier
-              uint64_t* full = C8 ? &sm.q_raw[qb] : &sm.q_ready[qb];
-              const uint32_t bar = kShared ? barrier_of(full) : smem_u32(full);
-              if (C8 || rank == 0) mbar_arrive_expect_tx(full, (unsigned)(kShared ? 2 : 1) * L::q_bytes);
+          if ((lane >> w.shift) == 0) {
+            const uint32_t bar = barrier_of(&sm.k_full[slot]);
 #pragma unroll
-              for (int c = 0; c < L::chunks; ++c)
-                load_3d<kShared>(sm.q[qb] + c * L::q_chunk, &tm_q, 64 * c, p.g * a.gs, p.q.row0 + plan::token_of(a, first_row), bar);
-            }
-            __syncwarp();
-          } else {
-            constexpr int kUnits = D / 8, kRowsPer = 32 / kUnits;  // units of a row over the lanes
-            const int u = lane % kUnits;
-            unsigned char* qt = sm.q[qb] + (u >> 3) * L::q_chunk;
-            const T* src = static_cast<const T*>(a.q) + (long long)p.q.row0 * a.q_stride + (long long)p.g * a.gs * hd;
-            const bool inside = 8 * u < hd;  // columns past the head are zeros
-            for (int r = lane / kUnits; r < rows; r += kRowsPer) {
-              const int f = first_row + r, t = plan::token_of(a, f);
-              cp_async16(qt + r * 128 + 16 * ((u & 7) ^ (r & 7)),
-                         src + (long long)t * a.q_stride + (f - t * a.gs) * hd + (inside ? 8 * u : 0), inside ? 16u : 0u);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(C8 ? &sm.q_raw[qb] : &sm.q_ready[qb]);
-          }
-          for (int i = 0; !C8 && i < n; ++i, ++J) {
-            const int row = part_row(w, i), slot = J % L::slots;
-            if (J >= L::slots) ok = wait(&sm.k_empty[slot], J / L::slots - 1);
-            if (!ok) break;
-            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&sm.k_full[slot], (unsigned)(PAIR ? 2 : 1) * L::k_bytes);
-            __syncwarp();
-            if ((lane >> w.shift) == 0) {
-              const uint32_t bar = barrier_of(&sm.k_full[slot]);
-#pragma unroll
-              for (int c = 0; c < L::chunks; ++c)
-                load_rows<PAIR, FULL>(sm.k[slot] + c * L::k_chunk + lane * box_rows * 128, &tm_k, col + 64 * c, p.g, row, bar);
-            }
+            for (int c = 0; c < L::chunks; ++c)
+              load_rows<PAIR, FULL>(sm.k[slot] + c * L::k_chunk + lane * box_rows * 128, &tm_k, col + 64 * c, p.g, row, bar);
           }
         }
-        if constexpr (C8) {  // one piece of code for K and V
-          const PieceDesc& d = sm.desc[x % kDescs];
-          const int v = warp == 3 ? 1 : 0;
-          Parts w = open_parts(v ? kTcKeys : L::k_rows, d.n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip,
-                         PAIR && !v ? rank * L::k_rows : 0, d.seq);
-          ok = load_codes(w, v, d.g, J);
-          if (v && ok && lane == 0) mbar_arrive(&sm.desc_free[x % kDescs]);
-        }
-        ++x;
       }
-      if (C8 && warp == 3) {
-        if (lane == 0) sm.issued[1] = J;
-      } else if (lane == 0) {
+      if (lane == 0) {
         sm.issued[0] = J;
         sm.issued[2] = PAIR || q_box ? x : 0;
       }
-    } else if (warp == 3) {
+    } else if (!C8 && warp == 3) {
       // ---------------------------------------------------------- V producer
       if (lane == 0) {
         prefetch_tmap(&tm_v);
-        if (!C8) prefetch_tmap(&tm_v1);
+        prefetch_tmap(&tm_v1);
       }
       int J = 0;
       bool ok = true;
@@ -775,7 +801,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const PieceDesc& d = sm.desc[x % kDescs];
         const int n = d.n, g = FULL ? 0 : d.g, col = (FULL ? d.g * D : 0) + (PAIR ? rank * 64 * L::v_chunks : 0);
         Parts w = open_parts(kTcKeys, n, d.se, d.lo_min, d.hi_max, d.tile_last, d.ns, d.skip, 0, d.seq);
-        for (int i = 0; !C8 && i < n; ++i, ++J) {
+        for (int i = 0; i < n; ++i, ++J) {
           const int row = part_row(w, i), key = first_key_of(w, i) + lane * box_rows, slot = J % L::slots;
           if (J >= L::slots) ok = wait(&sm.v_empty[slot], J / L::slots - 1);
           if (!ok) break;
