@@ -53,7 +53,7 @@ struct MmaSmem {
 };
 
 // T: of Q and the result.  C8: K and V are codes of cache8.cuh, and operands fp16.
-template <typename T, int DP, bool CAP, bool C8>
+template <typename T, int DP, bool CAP, bool SINKS, bool C8>
 __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, const ScoreMap sm) {
   using TO = typename std::conditional<C8, __half, T>::type;
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
   __shared__ plan::Start start;
   __shared__ long long warp_sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  plan::make_plan<kRows, kKeys, kThreads, true>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
+  plan::make_plan<kRows, kKeys, kThreads, SINKS>(a, blockIdx.x, gridDim.x, reinterpret_cast<int*>(smem_raw), warp_sums, &start);
   BatchSplit split{};
-  plan::Walker<kRows, kKeys, true> walk(a, start);
+  plan::Walker<kRows, kKeys, SINKS> walk(a, start);
   plan::Piece p;
   const uint32_t q_base = smem_u32(sh.q);
   constexpr int kUnits = DP / 8;
@@ -80,13 +80,14 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
       cp_async16(sh.q + r * DP * 2 + 16 * (u ^ (r & 7)), src, ok ? 16u : 0u);
     }
     const uint32_t* table = a.block_table + (long long)p.s * a.max_blocks;
+    const int tile0 = plan::first_tile<SINKS>(p.k) + p.t0;  // the piece's first tile, as plan::tile_at counts
     auto load_tile = [&](int i, int st) {
-      const int key0 = plan::tile_at<true>(i, p.k.ns, p.k.skip) * kKeys;
+      const int key0 = plan::tile_at<SINKS>(i, p.k.ns, p.k.skip) * kKeys;
       for (int c = tid; c < kKeys * kUnits; c += kThreads) {
         const int r = c / kUnits, u = c % kUnits;
         const int key = key0 + r;
         long long row = -1;
-        if ((key >= p.k.lo_min && key < p.k.hi_max) || key < p.k.se)
+        if ((key >= p.k.lo_min && key < p.k.hi_max) || (SINKS && key < p.k.se))
           row = paged_row(table, a.page_rows, a.num_pages, key, a.status);
         const bool ok = row >= 0 && 8 * u < a.D;
         if constexpr (C8) {
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
       }
     };
     const int n = p.t1 - p.t0;
-    if (n > 0) load_tile(p.t0, 0);
+    if (n > 0) load_tile(tile0, 0);
     cp_async_commit();
 
     // This thread's rows: r0 = 16 warp + lane/4 and r0 + 8.
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
     }
     for (int i = 0; i < n; ++i) {
       const int st = i % kStages;
-      if (i + 1 < n) load_tile(p.t0 + i + 1, (i + 1) % kStages);
+      if (i + 1 < n) load_tile(tile0 + i + 1, (i + 1) % kStages);
       cp_async_commit();
       cp_async_wait<1>();
       __syncthreads();
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
           mma16816<TO>(s[2 * j + 1], qa, kb[2], kb[3]);
         }
       }
-      const int key0 = plan::tile_at<true>(p.t0 + i, p.k.ns, p.k.skip) * kKeys;
+      const int key0 = plan::tile_at<SINKS>(tile0 + i, p.k.ns, p.k.skip) * kKeys;
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int j = 0; j < kKeys / 8; ++j)
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) batch_mma_kernel(const BatchArgs a, 
             v *= sm.scale2;
           }
           v -= slope[x] * fabsf((float)(pos[x] - key));
-          v = ((key >= lo[x] || key < a.sinks) && key < hi[x]) ? v : -INFINITY;
+          v = ((key >= lo[x] || (SINKS && key < a.sinks)) && key < hi[x]) ? v : -INFINITY;
           s[j][e] = v;
           mx[x] = fmaxf(mx[x], v);
         }
@@ -312,9 +313,14 @@ int launch_mma_t(const BatchArgs& a, int blocks, cudaStream_t s) {
   const ScoreMap sm = score_map(a);
   const size_t plan_bytes = ((size_t)a.n_seqs + 1) * sizeof(int);
   const size_t smem = sizeof(MmaSmem<DP>) > plan_bytes ? sizeof(MmaSmem<DP>) : plan_bytes;
-  auto kern = a.k_scales != nullptr
-                  ? (a.softcap > 0.f ? batch_mma_kernel<T, DP, true, true> : batch_mma_kernel<T, DP, false, true>)
-                  : (a.softcap > 0.f ? batch_mma_kernel<T, DP, true, false> : batch_mma_kernel<T, DP, false, false>);
+  // (Codes have one form.)
+  auto of_cap = [&](auto cap) {
+    constexpr bool CAP = decltype(cap)::value;
+    return a.k_scales != nullptr ? batch_mma_kernel<T, DP, CAP, true, true>
+           : a.sinks > 0         ? batch_mma_kernel<T, DP, CAP, true, false>
+                                 : batch_mma_kernel<T, DP, CAP, false, false>;
+  };
+  auto kern = a.softcap > 0.f ? of_cap(std::true_type{}) : of_cap(std::false_type{});
   if (!set_smem_limit(reinterpret_cast<const void*>(kern), smem)) return ATTN_ERR_CUDA;
   BatchArgs b = a;
   b.item_cost = kItemCost;
