@@ -131,11 +131,12 @@ extern "C" int attn_qk_norm_rope_backward(const void* dq, const void* dk, const 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (num_heads > 0) a.q.dy = dq, a.q.dy_stride = dq_stride, a.q.dw = dq_weight;
   if (num_kv_heads > 0) a.k.dy = dk, a.k.dy_stride = dk_stride, a.k.dw = dk_weight;
-  if (rows == 0) {
-    if (a.q.dw != nullptr && cudaMemsetAsync(a.q.dw, 0, head_dim * ew, s) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (a.k.dw != nullptr && cudaMemsetAsync(a.k.dw, 0, head_dim * ew, s) != cudaSuccess) return ATTN_ERR_CUDA;
-    return ATTN_OK;
-  }
+  // A sum over no rows or no heads.
+  if ((rows == 0 || num_heads == 0) && dq_weight != nullptr && cudaMemsetAsync(dq_weight, 0, head_dim * ew, s) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if ((rows == 0 || num_kv_heads == 0) && dk_weight != nullptr && cudaMemsetAsync(dk_weight, 0, head_dim * ew, s) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  if (rows == 0) return ATTN_OK;
   const int sms = device_sm_count();
   a.status = device_status_word();
   if (sms <= 0 || a.status == nullptr) return ATTN_ERR_CUDA;

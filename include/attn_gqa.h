@@ -559,11 +559,11 @@ ATTN_API int attn_batch_paged_sinks(const void *q, const void *k_pages, const vo
  *   dx = r (w dz - x r mean(w dz x r))
  * dq_out and dk_out are written as q_out and k_out are (each may be dq or q,
  * dk or k); dq_weight and dk_weight ([D] of weight_dtype, either may be NULL:
- * not wanted) are written in full, also for rows == 0.  Sums are fp32, in a
- * fixed order: repeated calls give identical bits.  workspace (16-byte
- * aligned; not needed when both are NULL) holds
- * attn_qk_norm_rope_backward_workspace_bytes bytes and keeps nothing between
- * calls; calls that share it must not overlap on the GPU.
+ * not wanted) are written in full, also for rows == 0 and for a tensor that is
+ * left out (zeros).  Sums are fp32, in a fixed order: repeated calls give
+ * identical bits.  workspace (16-byte aligned; not needed when both are NULL)
+ * holds attn_qk_norm_rope_backward_workspace_bytes bytes and keeps nothing
+ * between calls; calls that share it must not overlap on the GPU.
  */
 ATTN_API int attn_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const void *q_weight,
                                const void *k_weight, attn_dtype_t dtype, attn_dtype_t weight_dtype, uint32_t rows,

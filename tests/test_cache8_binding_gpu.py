@@ -34,6 +34,23 @@ def test_norms(cuda_lib):
         A.attn_qk_norm_rope(q, k, got[0], got[1], w, w.float(), rows, H, G, D, H * D, G * D, H * D, G * D, 1e-6)
 
 
+def test_the_weights_gradient_of_a_tensor_that_is_left_out_is_zero(cuda_lib):
+    A = cuda_lib
+    rows, G, D = 9, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, dk = (torch.randn(rows, G * D, generator=g, device="cuda") for _ in range(2))
+    w, out = torch.ones(D, device="cuda"), torch.empty_like(k)
+    workspace = torch.empty(A.attn_qk_norm_rope_backward_workspace_bytes(D), dtype=torch.uint8, device="cuda")
+    one, other = (torch.full((D,), 7.0, device="cuda") for _ in range(2))
+    A.attn_qk_norm_rope_backward(None, dk, None, k, None, out, None, w, other, one, rows, 0, G, D, 0, G * D, 0, G * D, 0,
+                                 G * D, 1e-6, workspace=workspace)
+    assert (other == 0).all() and one.isfinite().all() and (one != 0).any()
+    other.fill_(7.0)
+    A.attn_qk_norm_rope_backward(dk, None, k, None, out, None, w, None, one, other, rows, G, 0, D, G * D, 0, G * D, 0,
+                                 G * D, 0, 1e-6, workspace=workspace)
+    assert A.attn_get_status() == 0 and (other == 0).all() and (one != 0).any()
+
+
 def test_a_serving_step(cuda_lib):
     A = cuda_lib
     H, G, D, pr, sr = 8, 2, 64, 16, 8
