@@ -344,3 +344,35 @@ def test_calls_without_rows(cuda_lib):
     out = A.append_paged(batch, k, v, *pools, q=q, table=table)
     assert out.shape == (0, 256) and A.attend_paged(batch, out, *pools).shape == (0, 256)
     assert A.attn_get_status() == 0
+
+
+@pytest.mark.parametrize("page_rows,scale_rows", [(64, 16), (7, 1)])
+def test_pools_whose_offsets_pass_32_bits(cuda_lib, page_rows, scale_rows):
+    """Pages behind byte 2^31 of a pool, and behind scale 2^24: the bits of the same step over a small pool."""
+    A = cuda_lib
+    G, D, H = 8, 128, 16
+    new, kv = [1, 200, 3], [40, 210, 90]
+    b = Batch8(new, kv, H, G, D, page_rows, scale_rows, dtype=BF16, seed=4)
+    pages = 2 ** 31 // (page_rows * G * D) + 1 + b.num_pages
+    far = pages - b.num_pages
+    x, q = rows_of(b, G, BF16, 1, pad=0), rows_of(b, H, BF16, 2, pad=0)
+    w, rope = torch.ones(D, device="cuda", dtype=BF16), A.rope_table(256, D)
+    starts = b.dev([0, 40, 250, 340])
+    results = []
+    for shift, total in ((0, b.num_pages), (far, pages)):
+        cache = A.PagedCache8(*(torch.empty(total * page_rows, G * D, dtype=torch.uint8, device="cuda") for _ in "kv"),
+                              *(torch.empty(total * page_rows // scale_rows, G, dtype=torch.uint8, device="cuda") for _ in "kv"))
+        for pool, n in ((cache.k_pages, "k"), (cache.v_pages, "v")):
+            pool[shift * page_rows:] = b.codes[n]
+        for pool, n in ((cache.k_scales, "k"), (cache.v_scales, "v")):
+            pool[shift * page_rows // scale_rows:] = b.scales[n]
+        batch = b.object(A, block_table=torch.where(b.block_table >= 0, b.block_table + shift, b.block_table))
+        one = A.PagedBatch(batch.block_table[:1].contiguous(), b.dev([0, 1]), b.kv_len[:1].contiguous(), H, G, D, page_rows)
+        qt = A.append_paged8(batch, x, x, cache, q=q, table=rope, q_weight=w, k_weight=w)
+        k, v = (torch.empty(340, G * D, device="cuda") for _ in "kv")
+        A.read_paged8(batch, cache, starts, k, v)
+        results.append((qt, k, v, A.attend_paged8(batch, qt, cache), A.attend_paged8(one, qt[:1], cache),
+                        cache.k_pages[shift * page_rows:].clone(), cache.v_scales[shift * page_rows // scale_rows:].clone()))
+        assert A.attn_get_status() == 0
+        del cache
+    assert all(torch.equal(a, c) for a, c in zip(*results))
